@@ -76,6 +76,8 @@ typedef enum { PKV_F32 = 0, PKV_BF16 = 1 } pkv_dtype;
 #define PKV_DEVERR_SEQLEN_RANGE 3 /* sequence length < 1 or beyond its bound (sequence skipped) */
 #define PKV_DEVERR_TIMEOUT 4      /* an internal wait ran out of time (results unspecified) */
 #define PKV_DEVERR_SMEM_LAYOUT 5  /* shared memory not laid out as a kernel needs (call skipped) */
+#define PKV_DEVERR_POSITION_RANGE 6 /* rotating append: position outside the table (token skipped) */
+#define PKV_DEVERR_SLOT_ORDER 7   /* block-scaled append: a block's new rows not in order (entry skipped) */
 
 /* Largest num_seqs accepted by paged_decode_attention. */
 #define PKV_MAX_SEQS 8192
@@ -92,6 +94,64 @@ pkv_status pkv_kv_append(const void *k_new, const void *v_new, void *k_cache, vo
                          const int64_t *slot_mapping, int64_t num_tokens, int64_t num_blocks,
                          int num_kv_heads, int head_dim, int block_size, pkv_dtype dtype,
                          pkv_stream_t stream);
+
+/*
+ * Rotating appends: the position rotation of queries and keys applied on the
+ * way into the cache.  Of each head's head_dim elements the first rot_dim form
+ * pairs (a, b): elements i and i + rot_dim/2, or 2i and 2i + 1 (interleaved),
+ * i < rot_dim/2.  Pair i of token t turns by its table entry,
+ *   a' = a cos - b sin,  b' = b cos + a sin,
+ *   cos = cos_sin[p][i], sin = cos_sin[p][rot_dim/2 + i],
+ *   p = positions[axis(i)][t],
+ * in fp32, rounded once to the stored type; elements rot_dim.. are copied.
+ * With one axis p is the token's position; with several (time, height and
+ * width of an image patch) pair_axis names each pair's axis.
+ */
+#define PKV_MAX_ROPE_AXES 4
+#define PKV_MAX_ROT_DIM 256
+#define PKV_MAX_APPEND_HEAD_DIM 512
+
+typedef struct pkv_rope_append_args {
+  void *q_out;                 /* [num_tokens][num_q_heads][head_dim], device, written */
+  const void *q;               /* as q_out, read; q_out == q rotates in place (one stride); */
+                               /* both NULL (num_q_heads then unused): no queries */
+  const void *k_new;           /* [num_tokens][num_kv_heads][head_dim], device, read */
+  const void *v_new;
+  void *k_cache;               /* pools, written in place at the given slots only */
+  void *v_cache;
+  uint8_t *k_scale;            /* pkv_kv_append_fp8_block only: [num_blocks][num_kv_heads] */
+  uint8_t *v_scale;
+  const int64_t *slot_mapping; /* int64 [num_tokens]; < 0: padding, nothing of the token is */
+                               /* written, its q_out row included */
+  int64_t num_tokens;
+  int64_t num_blocks;
+  int64_t q_out_stride;        /* elements from one token's heads to the next's (at least */
+  int64_t q_stride;            /* heads * head_dim, a multiple of 16 bytes); 0: heads * */
+  int64_t k_stride;            /* head_dim, the contiguous layout.  The heads of one token */
+  int64_t v_stride;            /* are contiguous. */
+  int num_q_heads;
+  int num_kv_heads;
+  int head_dim;
+  int block_size;
+  pkv_dtype dtype;             /* of q, k_new, v_new (and, pkv_kv_append_rope, the pools) */
+  const float *cos_sin;        /* device [num_positions][rot_dim]; NULL: no rotation */
+  int64_t num_positions;       /* (pkv_kv_append_fp8_block without queries only) */
+  const int32_t *positions;    /* device [num_axes][num_tokens] */
+  int num_axes;                /* 1 .. PKV_MAX_ROPE_AXES */
+  int rot_dim;                 /* even, 2 .. min(head_dim, PKV_MAX_ROT_DIM) */
+  int interleaved;
+  const uint8_t *pair_axis;    /* HOST [rot_dim/2], each < num_axes; NULL with one axis */
+} pkv_rope_append_args;
+
+/*
+ * kv_append_rope -- pkv_kv_append with the rotation: q_out receives the
+ * rotated queries, k_cache the rotated keys, v_cache the values as they are.
+ * bf16 or fp32; head_dim up to PKV_MAX_APPEND_HEAD_DIM whose rows are a
+ * multiple of 16 bytes (PKV_EUNSUPPORTED otherwise).  A token with a slot
+ * beyond the pool or a position outside the table is skipped as a whole and
+ * reported in the device error word.  Slots must be distinct.
+ */
+pkv_status pkv_kv_append_rope(const pkv_rope_append_args *args, pkv_stream_t stream);
 
 /*
  * Bytes of device workspace paged_decode_attention needs for these sizes
@@ -314,6 +374,41 @@ pkv_status pkv_paged_decode_attention_fp8(void *out, const void *q, const void *
                                           int head_dim, int block_size, float scale,
                                           void *workspace, size_t workspace_bytes,
                                           pkv_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Block-scaled fp8 KV cache: E4M3 codes with one power-of-two scale per block
+ * of 16 tokens and KV head, which follows the data.  Pools are bytes
+ * [num_blocks][num_kv_heads][block_size][head_dim]; k_scale and v_scale are
+ * device bytes [num_blocks][num_kv_heads], byte b standing for 2^(b - 127)
+ * (b <= 254); an element reads as decode(code) * 2^(b - 127).  An append
+ * writes b in 1 .. 246.
+ * A power of two loses nothing to a tighter scale while codes are normal
+ * E4M3 numbers; x / scale and code * scale are exact, so an element is
+ * rounded once, and re-expressing it under a larger scale changes it only
+ * where it becomes an E4M3 subnormal.
+ * ------------------------------------------------------------------------- */
+
+/* Quantise and scatter new keys and values, optionally rotated (cos_sin not
+ * NULL; keys turn in fp32 and are rounded once, to E4M3), and rotate the
+ * queries.  bf16 input; head_dim a multiple of 16 up to 128, rot_dim a
+ * multiple of 4, of 16 with queries, as is head_dim - rot_dim then
+ * (PKV_EUNSUPPORTED otherwise).
+ *   Slots: the new rows of one block must be consecutive entries of
+ * slot_mapping with consecutive slots (a run), as the tokens of a sequence in
+ * order are.  A run that starts at row 0 starts its block anew; one that
+ * starts at row r > 0 continues it: rows 0 .. r - 1 are kept.  Per head,
+ *   e = the smallest integer in [-126, 119] with |x| <= 448 * 2^e for every
+ *       finite new element x of the run, but at least a continued block's e;
+ *   new rows: code = E4M3(x / 2^e), to nearest even; beyond 448, and infinite
+ *       x, becomes +-448; NaN stays NaN;
+ *   kept rows, where e grew by d: code = E4M3(decode(code) / 2^d); if a
+ *       continued block's scale byte is 0 or above 253, they become 0;
+ *   the scale byte is e + 127.
+ * Entries of a block that follow another run of the same block among the 32
+ * entries before them are skipped and reported (PKV_DEVERR_SLOT_ORDER); such
+ * runs further apart race.  A position outside the table skips its token and
+ * the rest of its run. */
+pkv_status pkv_kv_append_fp8_block(const pkv_rope_append_args *args, pkv_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * Latent (MLA-style) cache.  "The KV cache and prefix caching", section "What

@@ -22,12 +22,14 @@ _lock = threading.Lock()
 PKV_F32, PKV_BF16 = 0, 1
 DEVERR = {0: "none", 1: "slot out of range", 2: "block id out of range",
           3: "sequence length out of range", 4: "internal wait timed out",
-          5: "shared-memory layout check failed"}
+          5: "shared-memory layout check failed", 6: "position out of range",
+          7: "new rows of a block out of order"}
 EXPORTS = ("pkv_kv_append", "pkv_decode_workspace_bytes", "pkv_paged_decode_attention",
            "pkv_paged_decode_attention_append", "pkv_paged_decode_attention_noalloc", "pkv_chunked_prefill_attention",
            "pkv_decode_prefill_attention",
            "pkv_get_device_error", "pkv_status_str", "pkv_abi_version",
            "pkv_kv_append_fp8", "pkv_paged_decode_attention_fp8",
+           "pkv_kv_append_rope", "pkv_kv_append_fp8_block",
            "pkv_latent_append", "pkv_mla_workspace_bytes", "pkv_mla_decode_attention",
            "pkv_mla_decode_attention_append",
            "pkv_fnv1a64", "pkv_prefix_hash_blocks", "pkv_prefix_cache_create",
@@ -54,6 +56,24 @@ class DecodePrefillArgs(ctypes.Structure):
                 ("scale", ctypes.c_float), ("dtype", ctypes.c_int), ("prefill_sms", ctypes.c_int),
                 ("chunk_k_new", ctypes.c_void_p), ("chunk_v_new", ctypes.c_void_p),
                 ("chunk_slot_mapping", ctypes.c_void_p)]
+
+
+class RopeAppendArgs(ctypes.Structure):
+    """pkv_rope_append_args (field order and types as in pagedkv.h)."""
+    _fields_ = [("q_out", ctypes.c_void_p), ("q", ctypes.c_void_p),
+                ("k_new", ctypes.c_void_p), ("v_new", ctypes.c_void_p),
+                ("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("slot_mapping", ctypes.c_void_p), ("num_tokens", ctypes.c_int64),
+                ("num_blocks", ctypes.c_int64), ("q_out_stride", ctypes.c_int64),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("num_q_heads", ctypes.c_int),
+                ("num_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("block_size", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("cos_sin", ctypes.c_void_p), ("num_positions", ctypes.c_int64),
+                ("positions", ctypes.c_void_p), ("num_axes", ctypes.c_int),
+                ("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("pair_axis", ctypes.c_void_p)]
 
 
 class PagedKVError(RuntimeError):
@@ -91,6 +111,10 @@ def open_library(path: str):
     lib.pkv_paged_decode_attention_fp8.argtypes = [p, p, p, p, p, p, p, p, i, i, i, i64, i, i,
                                                    i, i, f, p, sz, p]
     lib.pkv_paged_decode_attention_fp8.restype = ctypes.c_int
+    for name in ("pkv_kv_append_rope", "pkv_kv_append_fp8_block"):
+        fn = getattr(lib, name)
+        fn.argtypes = [ctypes.POINTER(RopeAppendArgs), p]
+        fn.restype = ctypes.c_int
     lib.pkv_latent_append.argtypes = [p, p, p, i64, i64, i, i, p]
     lib.pkv_latent_append.restype = ctypes.c_int
     lib.pkv_mla_workspace_bytes.argtypes = [i, i, i, i]
@@ -285,6 +309,136 @@ def paged_decode_attention_fp8(out, q, k_cache, v_cache, k_scale, v_scale, block
         _ptr(block_table), _ptr(seq_lens), b, int(block_table.shape[1]), int(max_seq_len), nb, hq,
         hkv, d, bs, float(scale), _ptr(workspace), ws_bytes, _stream(stream))
     _check("pkv_paged_decode_attention_fp8", st)
+
+
+# ------------------------------------------------ rotating and block-scaled appends
+def _need(fn: str, ok, what: str) -> None:
+    if not ok:
+        raise PagedKVError(fn, 1, what)
+
+
+def _placed(fn: str, dev, **tensors) -> None:
+    """Every tensor on dev, dev the current CUDA device (the stream's)."""
+    _need(fn, dev.type == "cuda" and dev.index == torch.cuda.current_device(),
+          f"tensors on {dev}, not on the current CUDA device")
+    for name, t in tensors.items():
+        _need(fn, t.device == dev, f"{name} on {t.device}, the pools on {dev}")
+
+
+def _token_stride(fn: str, name: str, t, heads: int, d: int, tokens: int, dtype) -> int:
+    """Stride between the tokens of t [tokens, heads, d], its heads contiguous
+    (0 where no second token tells)."""
+    _need(fn, t.dtype == dtype, f"{name} is {t.dtype}, not {dtype}")
+    _need(fn, t.shape == (tokens, heads, d), f"{name} is {tuple(t.shape)}, not {(tokens, heads, d)}")
+    st = t.stride()
+    _need(fn, (st[2] == 1 or d == 1) and (st[1] == d or heads == 1),
+          f"the heads of one token of {name} are not contiguous")
+    return st[0] if tokens > 1 else 0
+
+
+class Rope:
+    """How an append rotates: cos_sin float32 [num_positions, rot_dim] on the
+    device (the cosines of a position's pairs, then their sines), pairs
+    (i, i + rot_dim/2) or, interleaved, (2i, 2i + 1), and each pair's position
+    axis (rot_dim/2 small integers; None: one axis)."""
+
+    def __init__(self, cos_sin, interleaved: bool = False, pair_axis=None):
+        fn = "Rope"
+        _need(fn, cos_sin.dim() == 2 and cos_sin.dtype == torch.float32 and cos_sin.is_contiguous(),
+              "cos_sin is not a contiguous float32 [num_positions, rot_dim]")
+        self.cos_sin = cos_sin
+        self.num_positions, self.rot_dim = cos_sin.shape
+        self.interleaved = bool(interleaved)
+        self.num_axes, self._pair_axis = 1, None
+        if pair_axis is not None:
+            axes = [int(x) for x in pair_axis]
+            _need(fn, len(axes) == self.rot_dim // 2, f"pair_axis has {len(axes)} entries for "
+                  f"{self.rot_dim // 2} pairs")
+            _need(fn, axes and 0 <= min(axes) and max(axes) < 4, "pair_axis entries outside [0, 4)")
+            self.num_axes = max(axes) + 1
+            self._pair_axis = (ctypes.c_uint8 * len(axes))(*axes)
+        self._pair_ptr = None if self._pair_axis is None else ctypes.addressof(self._pair_axis)
+
+
+def _rope_append(fn, q_out, q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, slot_mapping,
+                 positions, rope, in_dtype, stream):
+    nb, hkv, bs, d = k_cache.shape
+    t = slot_mapping.shape[0]
+    _need(fn, k_cache.is_contiguous() and v_cache.is_contiguous() and v_cache.shape == k_cache.shape
+          and v_cache.dtype == k_cache.dtype, "the pools are not two contiguous tensors of one shape and type")
+    _need(fn, slot_mapping.dtype == torch.int64 and slot_mapping.dim() == 1
+          and slot_mapping.is_contiguous(), "slot_mapping is not a contiguous int64 [tokens]")
+    _placed(fn, k_cache.device, v_cache=v_cache, k_new=k_new, v_new=v_new, slot_mapping=slot_mapping)
+    ks = _token_stride(fn, "k_new", k_new, hkv, d, t, in_dtype)
+    vs = _token_stride(fn, "v_new", v_new, hkv, d, t, in_dtype)
+    _need(fn, (q is None) == (q_out is None), "q and q_out go together")
+    hq = qs = qos = 0
+    qp = qop = None
+    if q is not None:
+        hq = q.shape[1]
+        _placed(fn, k_cache.device, q=q, q_out=q_out)
+        qs = _token_stride(fn, "q", q, hq, d, t, in_dtype)
+        qos = _token_stride(fn, "q_out", q_out, hq, d, t, in_dtype)
+        qp, qop = q.data_ptr(), q_out.data_ptr()
+    table = pos = pair = None
+    num_positions = rot = axes = inter = 0
+    if rope is not None:
+        axes = rope.num_axes
+        _need(fn, positions is not None and positions.dtype == torch.int32 and positions.is_contiguous()
+              and positions.shape in ((axes, t), (t,) if axes == 1 else None),
+              f"positions is not a contiguous int32 [{axes}, {t}]")
+        _placed(fn, k_cache.device, positions=positions, cos_sin=rope.cos_sin)
+        table, pos, pair = rope.cos_sin.data_ptr(), positions.data_ptr(), rope._pair_ptr
+        num_positions, rot, inter = rope.num_positions, rope.rot_dim, int(rope.interleaved)
+    a = RopeAppendArgs(qop, qp, k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(),
+                       v_cache.data_ptr(), None if k_scale is None else k_scale.data_ptr(),
+                       None if v_scale is None else v_scale.data_ptr(), slot_mapping.data_ptr(), t,
+                       nb, qos, qs, ks, vs, hq, hkv, d, bs,
+                       PKV_BF16 if in_dtype == torch.bfloat16 else PKV_F32, table, num_positions,
+                       pos, axes, rot, inter, pair)
+    _check(fn, getattr(load(), fn)(ctypes.byref(a), _stream(stream)))
+
+
+def kv_append_rope(q_out, q, k_new, v_new, k_cache, v_cache, slot_mapping, positions, rope,
+                   stream=None) -> None:
+    """kv_append with the position rotation: q [T, Hq, D] rotated into q_out
+    (which may be q; both None: no queries), k_new [T, Hkv, D] rotated and
+    v_new copied into the bf16 or fp32 pools [NB, Hkv, bs, D] at slot_mapping.
+    positions int32 [axes, T] (or [T]); rope a ``Rope``.  Tokens may be
+    strided (the columns of one projection); their heads are contiguous."""
+    fn = "pkv_kv_append_rope"
+    _need(fn, rope is not None, "no rope")
+    dtype = k_cache.dtype
+    _dtype_code(k_cache)
+    _validate(fn, "check_slots", slot_mapping, k_cache.shape[0], k_cache.shape[2])
+    _validate(fn, "check_positions", positions, slot_mapping, rope.num_positions)
+    _rope_append(fn, q_out, q, k_new, v_new, k_cache, v_cache, None, None, slot_mapping, positions,
+                 rope, dtype, stream)
+
+
+def kv_append_fp8_block(k_new, v_new, k_cache, v_cache, k_scale, v_scale, slot_mapping, stream=None,
+                        q_out=None, q=None, positions=None, rope=None) -> None:
+    """bf16 k_new, v_new [T, Hkv, D] -> E4M3 codes in the uint8 pools
+    [NB, Hkv, bs, D] with one power-of-two scale per block and head in the
+    uint8 k_scale, v_scale [NB, Hkv] (byte b: 2^(b - 127)).  The new rows of
+    a block are consecutive entries of slot_mapping.  With rope (and
+    positions) the keys, and q into q_out, are rotated on the way."""
+    fn = "pkv_kv_append_fp8_block"
+    _need(fn, k_cache.dtype == torch.uint8, f"the pools are {k_cache.dtype}, not torch.uint8")
+    _block_scales(fn, k_cache, k_scale, v_scale)
+    _need(fn, rope is not None or q is None, "queries need a rope")
+    _validate(fn, "check_runs", slot_mapping, k_cache.shape[0], k_cache.shape[2])
+    if rope is not None:
+        _validate(fn, "check_positions", positions, slot_mapping, rope.num_positions)
+    _rope_append(fn, q_out, q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, slot_mapping,
+                 positions, rope, torch.bfloat16, stream)
+
+
+def _block_scales(fn, k_cache, k_scale, v_scale) -> None:
+    for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
+        _need(fn, s.dtype == torch.uint8 and s.shape == k_cache.shape[:2] and s.is_contiguous()
+              and s.device == k_cache.device,
+              f"{name} is not a contiguous uint8 {list(k_cache.shape[:2])} beside the pools")
 
 
 def latent_append(c_new, c_cache, slot_mapping, stream=None) -> None:

@@ -8,6 +8,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <initializer_list>
 #include <mutex>
 
 #include "host_cache.h"
@@ -173,6 +174,122 @@ pkv_status pkv_kv_append(const void* k_new, const void* v_new, void* k_cache, vo
   pkv::AppendArgs a{k_new, v_new, k_cache, v_cache, slot_mapping, num_tokens, num_blocks,
                     num_kv_heads, row_bytes, err};
   return pkv::launch_kv_append(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PKV_OK
+             : PKV_ECUDA;
+}
+
+}  // extern "C"
+
+namespace {
+
+// One token stride of a rotating append: 0 is the contiguous layout.
+bool token_stride(int64_t given, int64_t heads, int head_dim, int elem, int64_t* out) {
+  const int64_t least = heads * head_dim;
+  *out = given == 0 ? least : given;
+  return *out >= least && (*out * elem) % 16 == 0;
+}
+
+// Validates a rotating append and fills its launch arguments (num_tokens > 0).
+pkv_status rope_append_prepare(const pkv_rope_append_args& x, pkv::RopeAppendArgs* out) {
+  const int elem = elem_bytes(x.dtype);
+  if (!x.k_new || !x.v_new || !x.k_cache || !x.v_cache || !x.slot_mapping) return PKV_EINVAL;
+  if (!x.q != !x.q_out) return PKV_EINVAL;
+  if (x.q && x.num_q_heads < 1) return PKV_EINVAL;
+  for (const void* p : {(const void*)x.q_out, x.q, x.k_new, x.v_new, (const void*)x.k_cache,
+                        (const void*)x.v_cache, (const void*)x.cos_sin})
+    if (!aligned16(p)) return PKV_EINVAL;
+  if (reinterpret_cast<uintptr_t>(x.slot_mapping) & 7u) return PKV_EINVAL;
+  pkv::RopeAppendArgs a{};
+  const int hq = x.q ? x.num_q_heads : 0;
+  if (!token_stride(x.k_stride, x.num_kv_heads, x.head_dim, elem, &a.k_stride) ||
+      !token_stride(x.v_stride, x.num_kv_heads, x.head_dim, elem, &a.v_stride) ||
+      (x.q && (!token_stride(x.q_stride, hq, x.head_dim, elem, &a.q_stride) ||
+               !token_stride(x.q_out_stride, hq, x.head_dim, elem, &a.q_out_stride))))
+    return PKV_EINVAL;
+  if (x.q == x.q_out && a.q_stride != a.q_out_stride) return PKV_EINVAL;
+  if (x.cos_sin) {
+    if (!x.positions || (reinterpret_cast<uintptr_t>(x.positions) & 3u) || x.num_positions < 1)
+      return PKV_EINVAL;
+    if (x.num_axes < 1 || x.num_axes > PKV_MAX_ROPE_AXES || (x.num_axes > 1 && !x.pair_axis))
+      return PKV_EINVAL;
+    if (x.rot_dim < 2 || x.rot_dim % 2 != 0 || x.rot_dim > x.head_dim) return PKV_EINVAL;
+    if (x.rot_dim > PKV_MAX_ROT_DIM) return PKV_EUNSUPPORTED;
+    a.rope.cos_sin = x.cos_sin;
+    a.rope.num_positions = x.num_positions;
+    a.rope.positions = x.positions;
+    a.rope.num_axes = x.num_axes;
+    a.rope.rot_dim = x.rot_dim;
+    a.rope.interleaved = x.interleaved != 0;
+    for (int i = 0; x.pair_axis && i < x.rot_dim / 2; ++i) {
+      if (x.pair_axis[i] >= x.num_axes) return PKV_EINVAL;
+      a.rope.pair_axis[i] = x.pair_axis[i];
+    }
+  }
+  a.q_out = x.q_out;
+  a.q = x.q;
+  a.k_new = x.k_new;
+  a.v_new = x.v_new;
+  a.k_cache = x.k_cache;
+  a.v_cache = x.v_cache;
+  a.k_scale = x.k_scale;
+  a.v_scale = x.v_scale;
+  a.slot_mapping = x.slot_mapping;
+  a.num_tokens = x.num_tokens;
+  a.num_blocks = x.num_blocks;
+  a.num_q_heads = hq;
+  a.num_kv_heads = x.num_kv_heads;
+  a.head_dim = x.head_dim;
+  int sms = 0;
+  const pkv_status st = device_state(&a.err, &sms);
+  *out = a;
+  return st;
+}
+
+// Sizes every rotating append checks before its pointers.
+pkv_status rope_append_sizes(const pkv_rope_append_args& x) {
+  if (!dtype_ok(x.dtype)) return PKV_EDTYPE;
+  if (x.num_tokens < 0 || x.num_blocks < 1 || x.num_kv_heads < 1 || x.head_dim < 1 ||
+      x.block_size < 1)
+    return PKV_EINVAL;
+  if (x.block_size != pkv::kBlockSize) return PKV_EUNSUPPORTED;
+  if (x.num_tokens > INT_MAX) return PKV_ERANGE;
+  return PKV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+pkv_status pkv_kv_append_rope(const pkv_rope_append_args* x, pkv_stream_t stream) {
+  if (!x) return PKV_EINVAL;
+  pkv_status st = rope_append_sizes(*x);
+  if (st != PKV_OK) return st;
+  if ((x->head_dim * elem_bytes(x->dtype)) % 16 != 0 || x->head_dim > PKV_MAX_APPEND_HEAD_DIM)
+    return PKV_EUNSUPPORTED;
+  if (x->num_tokens == 0) return PKV_OK;
+  if (!x->cos_sin) return PKV_EINVAL;
+  pkv::RopeAppendArgs a;
+  st = rope_append_prepare(*x, &a);
+  if (st != PKV_OK) return st;
+  return pkv::launch_kv_append_rope(a, x->dtype == PKV_BF16,
+                                    reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PKV_OK
+             : PKV_ECUDA;
+}
+
+pkv_status pkv_kv_append_fp8_block(const pkv_rope_append_args* x, pkv_stream_t stream) {
+  if (!x) return PKV_EINVAL;
+  pkv_status st = rope_append_sizes(*x);
+  if (st != PKV_OK) return st;
+  if (x->dtype != PKV_BF16) return PKV_EUNSUPPORTED;
+  if (x->num_tokens == 0) return PKV_OK;
+  if (!x->k_scale || !x->v_scale || (x->q && !x->cos_sin)) return PKV_EINVAL;
+  if (x->head_dim % 16 != 0 || x->head_dim > 128) return PKV_EUNSUPPORTED;
+  pkv::RopeAppendArgs a;
+  st = rope_append_prepare(*x, &a);
+  if (st != PKV_OK) return st;
+  if (!pkv::append_fp8_block_supported(a)) return PKV_EUNSUPPORTED;
+  return pkv::launch_kv_append_fp8_block(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? PKV_OK
              : PKV_ECUDA;
 }

@@ -21,6 +21,8 @@ enum DevErr : int {
   DEVERR_SEQLEN_RANGE = 3,  // a sequence length < 1 or beyond its bound
   DEVERR_TIMEOUT = 4,       // an mbarrier wait ran out of time
   DEVERR_SMEM_LAYOUT = 5,   // dynamic shared memory not 1 KiB aligned (kernel skipped)
+  DEVERR_POSITION_RANGE = 6,  // a rotating append: position outside the table
+  DEVERR_SLOT_ORDER = 7,    // block-scaled append: a block's new rows not in order
 };
 
 // Wait limits: 2^31 SM cycles (about 1 s at GB300 clocks), checked every 64

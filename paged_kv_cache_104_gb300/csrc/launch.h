@@ -42,6 +42,45 @@ struct AppendFp8Args {
 };
 cudaError_t launch_kv_append_fp8(const AppendFp8Args& a, cudaStream_t stream);
 
+// The rotation of an append: tables, positions and which axis turns a pair.
+constexpr int kMaxRotPairs = 128;
+struct RopeArgs {
+  const float* cos_sin;       // [num_positions][rot_dim]: cosines, then sines
+  int64_t num_positions;
+  const int32_t* positions;   // [num_axes][num_tokens]
+  int num_axes;
+  int rot_dim;                // 0: no rotation
+  int interleaved;            // pairs (2i, 2i + 1) instead of (i, i + rot_dim / 2)
+  int whole_axes;             // set by the launcher: pairs in one 16-byte chunk share an axis
+  uint8_t pair_axis[kMaxRotPairs];
+};
+struct RopeAppendArgs {
+  void* q_out;                // [T][Hq][D] at q_out_stride, with q
+  const void* q;              // null: no queries (num_q_heads 0)
+  const void* k_new;
+  const void* v_new;
+  void* k_cache;
+  void* v_cache;
+  uint8_t* k_scale;           // block-scaled cache: [NB][Hkv] exponents + 127
+  uint8_t* v_scale;
+  const int64_t* slot_mapping;
+  int64_t num_tokens;
+  int64_t num_blocks;
+  int64_t q_out_stride;       // elements between tokens
+  int64_t q_stride;
+  int64_t k_stride;
+  int64_t v_stride;
+  int num_q_heads;
+  int num_kv_heads;
+  int head_dim;
+  int* err;
+  RopeArgs rope;
+};
+cudaError_t launch_kv_append_rope(const RopeAppendArgs& a, bool is_bf16, cudaStream_t stream);
+// bf16 rows -> E4M3 codes of x / 2^e, one exponent e per block and head
+bool append_fp8_block_supported(const RopeAppendArgs& a);
+cudaError_t launch_kv_append_fp8_block(const RopeAppendArgs& a, cudaStream_t stream);
+
 struct DecodeArgs {
   void* out;
   const void* q;

@@ -36,6 +36,30 @@ def check_slots(slot_mapping, num_blocks: int, block_size: int) -> None:
         raise ValidationError(f"slot {int(vals[counts > 1][0])} appears more than once")
 
 
+def check_runs(slot_mapping, num_blocks: int, block_size: int) -> None:
+    """Slots of a block-scaled append: as check_slots, and the new rows of one
+    block consecutive entries with consecutive slots."""
+    check_slots(slot_mapping, num_blocks, block_size)
+    seen, prev = set(), None
+    for t, s in enumerate(_host(slot_mapping).tolist()):
+        if s >= 0 and not (prev == s - 1 and s % block_size):
+            if s // block_size in seen:
+                raise ValidationError(f"slot_mapping[{t}] = {s} returns to block {s // block_size}: a "
+                                      "block's new rows must be consecutive entries and slots")
+            seen.add(s // block_size)
+        prev = s
+
+
+def check_positions(positions, slot_mapping, num_positions: int) -> None:
+    """Every position of a token that is not padding inside the table."""
+    p = _host(positions).to(torch.int64).reshape(-1, slot_mapping.shape[0])
+    bad = ((p < 0) | (p >= num_positions)) & (_host(slot_mapping) >= 0)[None]
+    if bool(bad.any()):
+        ax, t = (int(x) for x in bad.nonzero()[0])
+        raise ValidationError(f"position {int(p[ax, t])} of token {t} (axis {ax}) outside "
+                              f"[0, {num_positions})")
+
+
 def check_decode(block_table, seq_lens, max_seq_len: int, num_blocks: int, block_size: int,
                  appends: bool = False) -> None:
     """Every length in [1, min(max_seq_len, blocks per row x block_size)];
