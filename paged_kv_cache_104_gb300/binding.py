@@ -36,6 +36,7 @@ EXPORTS = ("pkv_kv_append", "pkv_decode_workspace_bytes", "pkv_paged_decode_atte
            "pkv_prefix_cache_destroy", "pkv_prefix_cache_size", "pkv_prefix_cache_insert",
            "pkv_prefix_cache_evict", "pkv_prefix_cache_match", "pkv_prefix_plan",
            "pkv_l2_flush", "pkv_set_span_buffer")
+MAX_ROPE_AXES = 4                 # PKV_MAX_ROPE_AXES
 NOALLOC_SCRATCH_BYTES = 32 << 20  # PKV_NOALLOC_SCRATCH_BYTES
 
 
@@ -156,6 +157,8 @@ def open_library(path: str):
 def load():
     """Load the shared library (built by ``paged_kv_cache_104_gb300.build``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -311,29 +314,51 @@ def paged_decode_attention_fp8(out, q, k_cache, v_cache, k_scale, v_scale, block
     _check("pkv_paged_decode_attention_fp8", st)
 
 
-# ------------------------------------------------ rotating and block-scaled appends
-def _need(fn: str, ok, what: str) -> None:
-    if not ok:
-        raise PagedKVError(fn, 1, what)
+# ------------------------------------------------ rotating and block-scaled calls
+# These wrappers check types, shapes, layouts and devices.  A check formats
+# its message only when it fails: with eagerly built messages a call spent 20
+# of its 30 us in them (one token's append; the library's part is 3.3 us).
+def _refuse(fn: str, what: str):
+    raise PagedKVError(fn, 1, what)
 
 
-def _placed(fn: str, dev, **tensors) -> None:
-    """Every tensor on dev, dev the current CUDA device (the stream's)."""
-    _need(fn, dev.type == "cuda" and dev.index == torch.cuda.current_device(),
-          f"tensors on {dev}, not on the current CUDA device")
-    for name, t in tensors.items():
-        _need(fn, t.device == dev, f"{name} on {t.device}, the pools on {dev}")
+def _refuse_tensor(fn: str, name: str, t, dtype, shape, index: int):
+    _refuse(fn, f"{name} is {t.dtype} {list(t.shape)}{'' if t.is_contiguous() else ', not contiguous,'} on "
+                f"{t.device}; expected a contiguous {dtype} {list(shape)} on cuda:{index}")
 
 
-def _token_stride(fn: str, name: str, t, heads: int, d: int, tokens: int, dtype) -> int:
-    """Stride between the tokens of t [tokens, heads, d], its heads contiguous
-    (0 where no second token tells)."""
-    _need(fn, t.dtype == dtype, f"{name} is {t.dtype}, not {dtype}")
-    _need(fn, t.shape == (tokens, heads, d), f"{name} is {tuple(t.shape)}, not {(tokens, heads, d)}")
-    st = t.stride()
-    _need(fn, (st[2] == 1 or d == 1) and (st[1] == d or heads == 1),
-          f"the heads of one token of {name} are not contiguous")
-    return st[0] if tokens > 1 else 0
+def _device_of(fn: str, t) -> int:
+    """Index of t's device, which must be the current CUDA device (the
+    library launches there)."""
+    index = t.get_device()
+    if index < 0 or index != torch.cuda.current_device():
+        _refuse(fn, f"tensors on {t.device}, not on the current CUDA device")
+    return index
+
+
+def _whole(fn: str, name: str, t, dtype, shape, index: int) -> int:
+    """Pointer of a contiguous tensor of this type and shape on this device."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        _refuse_tensor(fn, name, t, dtype, shape, index)
+    return t.data_ptr()
+
+
+def _token_stride(fn: str, name: str, t, dtype, shape, index: int) -> int:
+    """Stride between the tokens of t [tokens, heads, d], whose heads are
+    contiguous (0: the contiguous layout)."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index:
+        if t.is_contiguous():
+            return 0
+        st = t.stride()
+        if (st[2] == 1 or shape[2] == 1) and (st[1] == shape[2] or shape[1] == 1) and st[0] > 0:
+            return st[0]
+    _refuse_tensor(fn, name, t, dtype, shape, index)
+
+
+def _stream_on(stream, index: int) -> int:
+    """Handle of the stream, by default the device's current one (without the
+    2.8 us that building a torch Stream takes)."""
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
 class Rope:
@@ -343,60 +368,59 @@ class Rope:
     axis (rot_dim/2 small integers; None: one axis)."""
 
     def __init__(self, cos_sin, interleaved: bool = False, pair_axis=None):
-        fn = "Rope"
-        _need(fn, cos_sin.dim() == 2 and cos_sin.dtype == torch.float32 and cos_sin.is_contiguous(),
-              "cos_sin is not a contiguous float32 [num_positions, rot_dim]")
+        if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32 or not cos_sin.is_contiguous():
+            _refuse("Rope", "cos_sin is not a contiguous float32 [num_positions, rot_dim]")
         self.cos_sin = cos_sin
         self.num_positions, self.rot_dim = cos_sin.shape
         self.interleaved = bool(interleaved)
-        self.num_axes, self._pair_axis = 1, None
+        self.num_axes, self._pair_axis, self._pair_ptr = 1, None, None
         if pair_axis is not None:
             axes = [int(x) for x in pair_axis]
-            _need(fn, len(axes) == self.rot_dim // 2, f"pair_axis has {len(axes)} entries for "
-                  f"{self.rot_dim // 2} pairs")
-            _need(fn, axes and 0 <= min(axes) and max(axes) < 4, "pair_axis entries outside [0, 4)")
+            if len(axes) != self.rot_dim // 2:
+                _refuse("Rope", f"pair_axis has {len(axes)} entries for {self.rot_dim // 2} pairs")
+            if not axes or min(axes) < 0 or max(axes) >= MAX_ROPE_AXES:
+                _refuse("Rope", f"pair_axis entries outside [0, {MAX_ROPE_AXES})")
             self.num_axes = max(axes) + 1
             self._pair_axis = (ctypes.c_uint8 * len(axes))(*axes)
-        self._pair_ptr = None if self._pair_axis is None else ctypes.addressof(self._pair_axis)
+            self._pair_ptr = ctypes.addressof(self._pair_axis)
 
 
-def _rope_append(fn, q_out, q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, slot_mapping,
-                 positions, rope, in_dtype, stream):
-    nb, hkv, bs, d = k_cache.shape
-    t = slot_mapping.shape[0]
-    _need(fn, k_cache.is_contiguous() and v_cache.is_contiguous() and v_cache.shape == k_cache.shape
-          and v_cache.dtype == k_cache.dtype, "the pools are not two contiguous tensors of one shape and type")
-    _need(fn, slot_mapping.dtype == torch.int64 and slot_mapping.dim() == 1
-          and slot_mapping.is_contiguous(), "slot_mapping is not a contiguous int64 [tokens]")
-    _placed(fn, k_cache.device, v_cache=v_cache, k_new=k_new, v_new=v_new, slot_mapping=slot_mapping)
-    ks = _token_stride(fn, "k_new", k_new, hkv, d, t, in_dtype)
-    vs = _token_stride(fn, "v_new", v_new, hkv, d, t, in_dtype)
-    _need(fn, (q is None) == (q_out is None), "q and q_out go together")
+def _rope_append(fn, call, q_out, q, k_new, v_new, k_cache, v_cache, scale_ptrs, slot_mapping,
+                 positions, rope, dtype, dtype_code, index, stream):
+    shape = k_cache.shape
+    nb, hkv, bs, d = shape
+    kp = _whole(fn, "k_cache", k_cache, k_cache.dtype, shape, index)
+    vp = _whole(fn, "v_cache", v_cache, k_cache.dtype, shape, index)
+    t = slot_mapping.shape[0] if slot_mapping.dim() else -1
+    sp = _whole(fn, "slot_mapping", slot_mapping, torch.int64, (t,), index)
+    heads = (t, hkv, d)
+    ks = _token_stride(fn, "k_new", k_new, dtype, heads, index)
+    vs = _token_stride(fn, "v_new", v_new, dtype, heads, index)
     hq = qs = qos = 0
     qp = qop = None
-    if q is not None:
+    if q is not None or q_out is not None:
+        if q is None or q_out is None or q.dim() != 3:
+            _refuse(fn, "q and q_out go together, [tokens, heads, head_dim]")
         hq = q.shape[1]
-        _placed(fn, k_cache.device, q=q, q_out=q_out)
-        qs = _token_stride(fn, "q", q, hq, d, t, in_dtype)
-        qos = _token_stride(fn, "q_out", q_out, hq, d, t, in_dtype)
+        qs = _token_stride(fn, "q", q, dtype, (t, hq, d), index)
+        qos = _token_stride(fn, "q_out", q_out, dtype, (t, hq, d), index)
         qp, qop = q.data_ptr(), q_out.data_ptr()
     table = pos = pair = None
     num_positions = rot = axes = inter = 0
     if rope is not None:
-        axes = rope.num_axes
-        _need(fn, positions is not None and positions.dtype == torch.int32 and positions.is_contiguous()
-              and positions.shape in ((axes, t), (t,) if axes == 1 else None),
-              f"positions is not a contiguous int32 [{axes}, {t}]")
-        _placed(fn, k_cache.device, positions=positions, cos_sin=rope.cos_sin)
-        table, pos, pair = rope.cos_sin.data_ptr(), positions.data_ptr(), rope._pair_ptr
-        num_positions, rot, inter = rope.num_positions, rope.rot_dim, int(rope.interleaved)
-    a = RopeAppendArgs(qop, qp, k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(),
-                       v_cache.data_ptr(), None if k_scale is None else k_scale.data_ptr(),
-                       None if v_scale is None else v_scale.data_ptr(), slot_mapping.data_ptr(), t,
-                       nb, qos, qs, ks, vs, hq, hkv, d, bs,
-                       PKV_BF16 if in_dtype == torch.bfloat16 else PKV_F32, table, num_positions,
-                       pos, axes, rot, inter, pair)
-    _check(fn, getattr(load(), fn)(ctypes.byref(a), _stream(stream)))
+        axes, rot, num_positions = rope.num_axes, rope.rot_dim, rope.num_positions
+        if positions is None:
+            _refuse(fn, "a rope needs positions")
+        one = (t,) if axes == 1 and positions.dim() == 1 else (axes, t)
+        pos = _whole(fn, "positions", positions, torch.int32, one, index)
+        table = _whole(fn, "cos_sin", rope.cos_sin, torch.float32, (num_positions, rot), index)
+        pair, inter = rope._pair_ptr, rope.interleaved
+    a = RopeAppendArgs(qop, qp, k_new.data_ptr(), v_new.data_ptr(), kp, vp, scale_ptrs[0],
+                       scale_ptrs[1], sp, t, nb, qos, qs, ks, vs, hq, hkv, d, bs, dtype_code, table,
+                       num_positions, pos, axes, rot, inter, pair)
+    status = call(ctypes.byref(a), _stream_on(stream, index))
+    if status:
+        _check(fn, status)
 
 
 def kv_append_rope(q_out, q, k_new, v_new, k_cache, v_cache, slot_mapping, positions, rope,
@@ -407,13 +431,16 @@ def kv_append_rope(q_out, q, k_new, v_new, k_cache, v_cache, slot_mapping, posit
     positions int32 [axes, T] (or [T]); rope a ``Rope``.  Tokens may be
     strided (the columns of one projection); their heads are contiguous."""
     fn = "pkv_kv_append_rope"
-    _need(fn, rope is not None, "no rope")
+    if rope is None:
+        _refuse(fn, "no rope")
     dtype = k_cache.dtype
-    _dtype_code(k_cache)
-    _validate(fn, "check_slots", slot_mapping, k_cache.shape[0], k_cache.shape[2])
-    _validate(fn, "check_positions", positions, slot_mapping, rope.num_positions)
-    _rope_append(fn, q_out, q, k_new, v_new, k_cache, v_cache, None, None, slot_mapping, positions,
-                 rope, dtype, stream)
+    code = _dtype_code(k_cache)
+    if _debug:
+        _validate(fn, "check_slots", slot_mapping, k_cache.shape[0], k_cache.shape[2])
+        _validate(fn, "check_positions", positions, slot_mapping, rope.num_positions)
+    _rope_append(fn, load().pkv_kv_append_rope, q_out, q, k_new, v_new, k_cache, v_cache,
+                 (None, None), slot_mapping, positions, rope, dtype, code, _device_of(fn, k_cache),
+                 stream)
 
 
 def kv_append_fp8_block(k_new, v_new, k_cache, v_cache, k_scale, v_scale, slot_mapping, stream=None,
@@ -424,21 +451,24 @@ def kv_append_fp8_block(k_new, v_new, k_cache, v_cache, k_scale, v_scale, slot_m
     a block are consecutive entries of slot_mapping.  With rope (and
     positions) the keys, and q into q_out, are rotated on the way."""
     fn = "pkv_kv_append_fp8_block"
-    _need(fn, k_cache.dtype == torch.uint8, f"the pools are {k_cache.dtype}, not torch.uint8")
-    _block_scales(fn, k_cache, k_scale, v_scale)
-    _need(fn, rope is not None or q is None, "queries need a rope")
-    _validate(fn, "check_runs", slot_mapping, k_cache.shape[0], k_cache.shape[2])
-    if rope is not None:
-        _validate(fn, "check_positions", positions, slot_mapping, rope.num_positions)
-    _rope_append(fn, q_out, q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, slot_mapping,
-                 positions, rope, torch.bfloat16, stream)
+    if k_cache.dtype is not torch.uint8:
+        _refuse(fn, f"the pools are {k_cache.dtype}, not torch.uint8")
+    if rope is None and q is not None:
+        _refuse(fn, "queries need a rope")
+    if _debug:
+        _validate(fn, "check_runs", slot_mapping, k_cache.shape[0], k_cache.shape[2])
+        if rope is not None:
+            _validate(fn, "check_positions", positions, slot_mapping, rope.num_positions)
+    index = _device_of(fn, k_cache)
+    _rope_append(fn, load().pkv_kv_append_fp8_block, q_out, q, k_new, v_new, k_cache, v_cache,
+                 _block_scales(fn, k_cache, k_scale, v_scale, index), slot_mapping, positions, rope,
+                 torch.bfloat16, PKV_BF16, index, stream)
 
 
-def _block_scales(fn, k_cache, k_scale, v_scale) -> None:
-    for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
-        _need(fn, s.dtype == torch.uint8 and s.shape == k_cache.shape[:2] and s.is_contiguous()
-              and s.device == k_cache.device,
-              f"{name} is not a contiguous uint8 {list(k_cache.shape[:2])} beside the pools")
+def _block_scales(fn, k_cache, k_scale, v_scale, index: int):
+    shape = k_cache.shape[:2]
+    return (_whole(fn, "k_scale", k_scale, torch.uint8, shape, index),
+            _whole(fn, "v_scale", v_scale, torch.uint8, shape, index))
 
 
 def latent_append(c_new, c_cache, slot_mapping, stream=None) -> None:

@@ -112,30 +112,61 @@ def _tensors(t=4, dtype=torch.bfloat16, pool=torch.bfloat16):
     return q, k, v, kc, vc, R.scattered_slots(t, 4, 1), pos
 
 
-def test_binding_refuses_before_the_library(monkeypatch):
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+def test_binding_refuses_before_the_library():
     q, k, v, kc, vc, slots, pos = _tensors()
     rope = B.Rope(R.table(64, 128))
-    with pytest.raises(B.PagedKVError, match="current CUDA device"):
-        B.kv_append_rope(q, q, k, v, kc, vc, slots, pos, rope)
     with pytest.raises(B.PagedKVError, match="no rope"):
         B.kv_append_rope(q, q, k, v, kc, vc, slots, pos, None)
-    with pytest.raises(B.PagedKVError, match="slot_mapping"):
-        B.kv_append_rope(q, q, k, v, kc, vc, slots.int(), pos, rope)
-    with pytest.raises(B.PagedKVError, match="pools"):
-        B.kv_append_rope(q, q, k, v, kc, vc.float(), slots, pos, rope)
     with pytest.raises(TypeError):
         B.kv_append_rope(q, q, k, v, kc.half(), vc.half(), slots, pos, rope)
     sc = torch.zeros(4, 2, dtype=torch.uint8)
     with pytest.raises(B.PagedKVError, match="the pools are torch.bfloat16"):
         B.kv_append_fp8_block(k, v, kc, vc, sc, sc, slots)
     k8 = kc.to(torch.uint8)
-    with pytest.raises(B.PagedKVError, match="v_scale"):
-        B.kv_append_fp8_block(k, v, k8, k8, sc, sc.float(), slots)
-    with pytest.raises(B.PagedKVError, match="k_scale"):
-        B.kv_append_fp8_block(k, v, k8, k8, sc[:3], sc, slots)
     with pytest.raises(B.PagedKVError, match="queries need a rope"):
         B.kv_append_fp8_block(k, v, k8, k8, sc, sc, slots, q=q, q_out=q)
+
+
+def test_binding_refuses_tensors_off_the_device(monkeypatch):
+    q, k, v, kc, vc, slots, pos = _tensors()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    with pytest.raises(B.PagedKVError, match="current CUDA device"):
+        B.kv_append_rope(q, q, k, v, kc, vc, slots, pos, B.Rope(R.table(64, 128)))
+
+
+ROPE_BAD = {
+    "v_cache": lambda a: a["vc"].float(), "vc": lambda a: a["vc"][:3], "slots": lambda a: a["slots"].int(),
+    "slots2": lambda a: a["slots"][:, None], "k": lambda a: a["k"].float(), "k2": lambda a: a["k"][:3],
+    "v": lambda a: a["v"].transpose(1, 2), "v2": lambda a: a["v"].expand(4, 2, 128)[:, :, ::2],
+    "q": lambda a: a["q"][:, :, :64], "q2": lambda a: None, "qo": lambda a: a["qo"][:3], "qo2": lambda a: None,
+    "pos": lambda a: a["pos"].long(), "pos2": lambda a: a["pos"][:, :3], "pos3": lambda a: None,
+    "pos4": lambda a: a["pos"].expand(2, 4), "kc": lambda a: a["kc"].transpose(0, 1),
+}
+
+
+@pytest.mark.parametrize("which", sorted(ROPE_BAD))
+def test_binding_names_the_tensor(which, monkeypatch):
+    """Shape, type and layout refusals, with the tensors' device left aside."""
+    monkeypatch.setattr(B, "_device_of", lambda fn, t: -1)   # CPU tensors answer get_device() with -1
+    q, k, v, kc, vc, slots, pos = _tensors()
+    a = dict(qo=q.clone(), q=q, k=k, v=v, kc=kc, vc=vc, slots=slots, pos=pos)
+    key = {"v_cache": "vc"}.get(which, which.rstrip("234"))
+    a[key] = ROPE_BAD[which](a)
+    name = {"kc": "k_cache", "vc": "v_cache", "slots": "slot_mapping", "k": "k_new", "v": "v_new", "q": "q",
+            "qo": "q_out|q is", "pos": "positions"}[key]
+    with pytest.raises(B.PagedKVError, match=name):
+        B.kv_append_rope(a["qo"], a["q"], a["k"], a["v"], a["kc"], a["vc"], a["slots"], a["pos"],
+                         B.Rope(R.table(64, 128)))
+
+
+@pytest.mark.parametrize("ks,vs,name", [(lambda s: s[:3], lambda s: s, "k_scale"), (lambda s: s, lambda s: s.float(), "v_scale"),
+                                        (lambda s: s, lambda s: s.T.contiguous().T, "v_scale")])
+def test_binding_names_the_scale(ks, vs, name, monkeypatch):
+    monkeypatch.setattr(B, "_device_of", lambda fn, t: -1)
+    _, k, v, kc, _, slots, _ = _tensors()
+    k8, sc = kc.to(torch.uint8), torch.zeros(4, 2, dtype=torch.uint8)
+    with pytest.raises(B.PagedKVError, match=name):
+        B.kv_append_fp8_block(k, v, k8, k8.clone(), ks(sc), vs(sc), slots)
 
 
 @pytest.mark.parametrize("make", [
