@@ -410,6 +410,25 @@ pkv_status pkv_paged_decode_attention_fp8(void *out, const void *q, const void *
  * the rest of its run. */
 pkv_status pkv_kv_append_fp8_block(const pkv_rope_append_args *args, pkv_stream_t stream);
 
+/* Bytes of device workspace pkv_paged_decode_attention_fp8_block needs (0:
+ * none).  fp32 partials, as pkv_decode_workspace_bytes, but a small batch is
+ * cut into splits of 256, 128 or 64 tokens instead of 512.  Host-only. */
+size_t pkv_decode_fp8_block_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads,
+                                            int head_dim, int max_seq_len);
+
+/* Decode attention over the block-scaled pools: pkv_paged_decode_attention
+ * with q and out in bf16, head_dim 128, groups of 1, 2, 4, 8 or 16 query heads
+ * to a KV head, and a workspace of
+ * pkv_decode_fp8_block_workspace_bytes(...).  A length of 0 marks a padded
+ * row of the batch: its out row is left as it was and no error is recorded.
+ * A NaN code in a stored row makes its sequence's results NaN. */
+pkv_status pkv_paged_decode_attention_fp8_block(
+    void *out, const void *q, const void *k_cache, const void *v_cache, const uint8_t *k_scale,
+    const uint8_t *v_scale, const int32_t *block_table, const int32_t *seq_lens, int num_seqs,
+    int max_blocks_per_seq, int max_seq_len, int64_t num_blocks, int num_q_heads, int num_kv_heads,
+    int head_dim, int block_size, float scale, void *workspace, size_t workspace_bytes,
+    pkv_stream_t stream);
+
 /* ---------------------------------------------------------------------------
  * Latent (MLA-style) cache.  "The KV cache and prefix caching", section "What
  * prefill stores and decode reads", names multi-head latent attention: the

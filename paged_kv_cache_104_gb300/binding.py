@@ -30,6 +30,7 @@ EXPORTS = ("pkv_kv_append", "pkv_decode_workspace_bytes", "pkv_paged_decode_atte
            "pkv_get_device_error", "pkv_status_str", "pkv_abi_version",
            "pkv_kv_append_fp8", "pkv_paged_decode_attention_fp8",
            "pkv_kv_append_rope", "pkv_kv_append_fp8_block",
+           "pkv_decode_fp8_block_workspace_bytes", "pkv_paged_decode_attention_fp8_block",
            "pkv_latent_append", "pkv_mla_workspace_bytes", "pkv_mla_decode_attention",
            "pkv_mla_decode_attention_append",
            "pkv_fnv1a64", "pkv_prefix_hash_blocks", "pkv_prefix_cache_create",
@@ -116,6 +117,11 @@ def open_library(path: str):
         fn = getattr(lib, name)
         fn.argtypes = [ctypes.POINTER(RopeAppendArgs), p]
         fn.restype = ctypes.c_int
+    lib.pkv_decode_fp8_block_workspace_bytes.argtypes = [i, i, i, i, i]
+    lib.pkv_decode_fp8_block_workspace_bytes.restype = sz
+    lib.pkv_paged_decode_attention_fp8_block.argtypes = [p, p, p, p, p, p, p, p, i, i, i, i64, i, i,
+                                                         i, i, f, p, sz, p]
+    lib.pkv_paged_decode_attention_fp8_block.restype = ctypes.c_int
     lib.pkv_latent_append.argtypes = [p, p, p, i64, i64, i, i, p]
     lib.pkv_latent_append.restype = ctypes.c_int
     lib.pkv_mla_workspace_bytes.argtypes = [i, i, i, i]
@@ -469,6 +475,56 @@ def _block_scales(fn, k_cache, k_scale, v_scale, index: int):
     shape = k_cache.shape[:2]
     return (_whole(fn, "k_scale", k_scale, torch.uint8, shape, index),
             _whole(fn, "v_scale", v_scale, torch.uint8, shape, index))
+
+
+def decode_fp8_block_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int,
+                                     head_dim: int, max_seq_len: int) -> int:
+    return int(load().pkv_decode_fp8_block_workspace_bytes(num_seqs, num_q_heads, num_kv_heads,
+                                                           head_dim, max_seq_len))
+
+
+def decode_workspace_fp8_block(num_seqs, num_q_heads, num_kv_heads, head_dim, max_seq_len,
+                               device="cuda"):
+    """Allocate (through torch) the workspace paged_decode_attention_fp8_block needs."""
+    n = decode_fp8_block_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, max_seq_len)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def paged_decode_attention_fp8_block(out, q, k_cache, v_cache, k_scale, v_scale, block_table,
+                                     seq_lens, max_seq_len: int, scale: float, workspace=None,
+                                     stream=None) -> None:
+    """Decode over block-scaled uint8 E4M3 pools [NB, Hkv, bs, 128] with scale
+    bytes [NB, Hkv]; q/out bf16 [B, Hq, 128]; block_table [B, max_blocks] and
+    seq_lens [B] int32 (0: a padded row, left alone); max_seq_len >=
+    max(seq_lens); workspace from ``decode_workspace_fp8_block``."""
+    fn = "pkv_paged_decode_attention_fp8_block"
+    if k_cache.dtype is not torch.uint8:
+        _refuse(fn, f"the pools are {k_cache.dtype}, not torch.uint8")
+    index = _device_of(fn, k_cache)
+    shape = k_cache.shape
+    nb, hkv, bs, d = shape
+    if q.dim() != 3 or block_table.dim() != 2:
+        _refuse(fn, "q is not [sequences, heads, head_dim] or block_table not [sequences, blocks]")
+    b, hq, _ = q.shape
+    blocks = block_table.shape[1]
+    kp = _whole(fn, "k_cache", k_cache, torch.uint8, shape, index)
+    vp = _whole(fn, "v_cache", v_cache, torch.uint8, shape, index)
+    ksp, vsp = _block_scales(fn, k_cache, k_scale, v_scale, index)
+    qp = _whole(fn, "q", q, torch.bfloat16, (b, hq, d), index)
+    op = _whole(fn, "out", out, torch.bfloat16, (b, hq, d), index)
+    bp = _whole(fn, "block_table", block_table, torch.int32, (b, blocks), index)
+    lp = _whole(fn, "seq_lens", seq_lens, torch.int32, (b,), index)
+    if _debug:
+        _validate(fn, "check_decode", block_table, seq_lens, max_seq_len, nb, bs, empty_ok=True)
+    wp, ws_bytes = None, 0
+    if workspace is not None:
+        ws_bytes = workspace.numel() * workspace.element_size()
+        wp = _whole(fn, "workspace", workspace, workspace.dtype, workspace.shape, index)
+    status = load().pkv_paged_decode_attention_fp8_block(
+        op, qp, kp, vp, ksp, vsp, bp, lp, b, blocks, max_seq_len, nb, hq, hkv, d, bs, scale, wp,
+        ws_bytes, _stream_on(stream, index))
+    if status:
+        _check(fn, status)
 
 
 def latent_append(c_new, c_cache, slot_mapping, stream=None) -> None:

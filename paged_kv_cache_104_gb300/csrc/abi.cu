@@ -62,20 +62,27 @@ pkv_status device_state(int** err, int* num_sms) {
   return PKV_OK;
 }
 
-int max_splits_for(int max_seq_len) {
-  return (max_seq_len + pkv::kSplitTokens - 1) / pkv::kSplitTokens;
+int max_splits_for(int max_seq_len, int split_tokens = pkv::kSplitTokens) {
+  return (max_seq_len + split_tokens - 1) / split_tokens;
 }
 
 // Partial slots per (sequence, query head) row: a sequence of n tokens gives
 // at most ceil(n / kSplitTokens) partials in 512-token splits, and at most
 // one more in the bf16 decode's balanced walk (each CTA's share of at least
 // 512 tokens may start inside a sequence).  One slot: no partials at all.
-int partial_slots_for(int max_seq_len) {
-  const int s = max_splits_for(max_seq_len);
+int partial_slots_for(int max_seq_len, int split_tokens = pkv::kSplitTokens) {
+  const int s = max_splits_for(max_seq_len, split_tokens);
   return s <= 1 ? 1 : s + 1;
 }
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+size_t partials_bytes(int num_seqs, int num_q_heads, int head_dim, int slots) {
+  if (slots <= 1) return 0;
+  const size_t rows = (size_t)num_seqs * num_q_heads * slots;
+  return align256(rows * head_dim * sizeof(float)) + align256(rows * 2 * sizeof(float)) +
+         align256((size_t)num_seqs * num_q_heads * sizeof(int));
+}
 
 // The decode workspace, in order: fp32 partial rows [rows][head_dim], their
 // (m, l) pairs [rows][2], and the partial count per (sequence, head) [count],
@@ -296,11 +303,7 @@ pkv_status pkv_kv_append_fp8_block(const pkv_rope_append_args* x, pkv_stream_t s
 
 size_t pkv_decode_workspace_bytes(int num_seqs, int num_q_heads, int head_dim, int max_seq_len) {
   if (num_seqs < 1 || num_q_heads < 1 || head_dim < 1 || max_seq_len < 1) return 0;
-  const int s = partial_slots_for(max_seq_len);
-  if (s <= 1) return 0;
-  const size_t rows = (size_t)num_seqs * num_q_heads * s;
-  return align256(rows * head_dim * sizeof(float)) + align256(rows * 2 * sizeof(float)) +
-         align256((size_t)num_seqs * num_q_heads * sizeof(int));
+  return partials_bytes(num_seqs, num_q_heads, head_dim, partial_slots_for(max_seq_len));
 }
 
 }  // extern "C"
@@ -524,15 +527,20 @@ pkv_status pkv_kv_append_fp8(const void* k_new, const void* v_new, void* k_cache
              : PKV_ECUDA;
 }
 
-pkv_status pkv_paged_decode_attention_fp8(void* out, const void* q, const void* k_cache,
-                                          const void* v_cache, const float* k_scale,
-                                          const float* v_scale, const int32_t* block_table,
-                                          const int32_t* seq_lens, int num_seqs,
-                                          int max_blocks_per_seq, int max_seq_len,
-                                          int64_t num_blocks, int num_q_heads, int num_kv_heads,
-                                          int head_dim, int block_size, float scale,
-                                          void* workspace, size_t workspace_bytes,
-                                          pkv_stream_t stream) {
+}  // extern "C"
+
+namespace {
+
+// Validates a decode call over an fp8 cache (either kind of scale) and fills
+// its launch arguments but for the scales (scales_ok: given and aligned);
+// num_seqs 0 in them: nothing to do.
+pkv_status fp8_decode_prepare(pkv::DecodeArgs* out_args, int* sms, bool scales_ok,
+                              int split_tokens, void* out, const void* q, const void* k_cache, const void* v_cache,
+                              const int32_t* block_table, const int32_t* seq_lens, int num_seqs,
+                              int max_blocks_per_seq, int max_seq_len, int64_t num_blocks,
+                              int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                              float scale, void* workspace, size_t workspace_bytes) {
+  *out_args = pkv::DecodeArgs{};
   if (num_q_heads < 1 || num_kv_heads < 1 || num_q_heads % num_kv_heads != 0 || head_dim < 1 ||
       block_size < 1)
     return PKV_EINVAL;
@@ -545,23 +553,21 @@ pkv_status pkv_paged_decode_attention_fp8(void* out, const void* q, const void* 
   if (num_seqs > PKV_MAX_SEQS) return PKV_ERANGE;
   if ((int64_t)max_seq_len > (int64_t)max_blocks_per_seq * block_size) return PKV_EINVAL;
   if (!isfinite(scale)) return PKV_EINVAL;
-  if (!out || !q || !k_cache || !v_cache || !block_table || !seq_lens || !k_scale || !v_scale)
+  if (!out || !q || !k_cache || !v_cache || !block_table || !seq_lens || !scales_ok)
     return PKV_EINVAL;
   if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) ||
       (reinterpret_cast<uintptr_t>(block_table) & 3u) ||
-      (reinterpret_cast<uintptr_t>(seq_lens) & 3u) ||
-      (reinterpret_cast<uintptr_t>(k_scale) & 3u) || (reinterpret_cast<uintptr_t>(v_scale) & 3u))
+      (reinterpret_cast<uintptr_t>(seq_lens) & 3u))
     return PKV_EINVAL;
-  const size_t need = pkv_decode_workspace_bytes(num_seqs, num_q_heads, head_dim, max_seq_len);
+  const int s = partial_slots_for(max_seq_len, split_tokens);
+  const size_t need = partials_bytes(num_seqs, num_q_heads, head_dim, s);
   if (workspace_bytes < need) return PKV_ERANGE;
-  if ((int64_t)num_seqs * num_kv_heads * max_splits_for(max_seq_len) >= (int64_t)INT_MAX)
+  if ((int64_t)num_seqs * num_kv_heads * max_splits_for(max_seq_len, split_tokens) >= (int64_t)INT_MAX)
     return PKV_ERANGE;  // the kernels' unit list is indexed by int
   if (need > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u))) return PKV_EINVAL;
   int* err = nullptr;
-  int sms = 0;
-  pkv_status st = device_state(&err, &sms);
+  const pkv_status st = device_state(&err, sms);
   if (st != PKV_OK) return st;
-  const int s = partial_slots_for(max_seq_len);
   const Partials part = carve_partials(workspace, (size_t)num_seqs * num_q_heads * s, head_dim);
   pkv::DecodeArgs a{};
   a.out = out;
@@ -579,7 +585,7 @@ pkv_status pkv_paged_decode_attention_fp8(void* out, const void* q, const void* 
   a.max_blocks_per_seq = max_blocks_per_seq;
   a.max_seq_len = max_seq_len;
   a.max_splits = s;
-  a.split_tokens = pkv::kSplitTokens;
+  a.split_tokens = split_tokens;
   a.num_blocks = num_blocks;
   a.num_q_heads = num_q_heads;
   a.num_kv_heads = num_kv_heads;
@@ -587,9 +593,70 @@ pkv_status pkv_paged_decode_attention_fp8(void* out, const void* q, const void* 
   a.scale = scale;
   a.chunk_prior = -1;
   a.is_bf16 = 1;
+  *out_args = a;
+  return PKV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+pkv_status pkv_paged_decode_attention_fp8(void* out, const void* q, const void* k_cache,
+                                          const void* v_cache, const float* k_scale,
+                                          const float* v_scale, const int32_t* block_table,
+                                          const int32_t* seq_lens, int num_seqs,
+                                          int max_blocks_per_seq, int max_seq_len,
+                                          int64_t num_blocks, int num_q_heads, int num_kv_heads,
+                                          int head_dim, int block_size, float scale,
+                                          void* workspace, size_t workspace_bytes,
+                                          pkv_stream_t stream) {
+  pkv::DecodeArgs a;
+  const bool scales_ok = k_scale && v_scale && !(reinterpret_cast<uintptr_t>(k_scale) & 3u) &&
+                         !(reinterpret_cast<uintptr_t>(v_scale) & 3u);
+  int sms = 0;
+  const pkv_status st = fp8_decode_prepare(
+      &a, &sms, scales_ok, pkv::kSplitTokens, out, q, k_cache, v_cache, block_table, seq_lens, num_seqs,
+      max_blocks_per_seq, max_seq_len, num_blocks, num_q_heads, num_kv_heads, head_dim, block_size,
+      scale, workspace, workspace_bytes);
+  if (st != PKV_OK || a.num_seqs == 0) return st;
   a.k_scale = k_scale;
   a.v_scale = v_scale;
   return pkv::launch_paged_decode_fp8(a, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PKV_OK
+             : PKV_ECUDA;
+}
+
+size_t pkv_decode_fp8_block_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads,
+                                            int head_dim, int max_seq_len) {
+  if (num_seqs < 1 || num_q_heads < 1 || num_kv_heads < 1 || head_dim < 1 || max_seq_len < 1 ||
+      max_seq_len > INT_MAX - pkv::kSplitTokens)
+    return 0;
+  const int split = pkv::fp8_block_split_tokens(num_seqs, num_kv_heads, max_seq_len);
+  return partials_bytes(num_seqs, num_q_heads, head_dim, partial_slots_for(max_seq_len, split));
+}
+
+pkv_status pkv_paged_decode_attention_fp8_block(
+    void* out, const void* q, const void* k_cache, const void* v_cache, const uint8_t* k_scale,
+    const uint8_t* v_scale, const int32_t* block_table, const int32_t* seq_lens, int num_seqs,
+    int max_blocks_per_seq, int max_seq_len, int64_t num_blocks, int num_q_heads, int num_kv_heads,
+    int head_dim, int block_size, float scale, void* workspace, size_t workspace_bytes,
+    pkv_stream_t stream) {
+  if (max_seq_len > INT_MAX - pkv::kSplitTokens) return PKV_ERANGE;   // rounded up to whole splits
+  pkv::DecodeArgs a;
+  int sms = 0;
+  const int split = num_seqs > 0 && num_kv_heads > 0 && max_seq_len > 0
+                        ? pkv::fp8_block_split_tokens(num_seqs, num_kv_heads, max_seq_len)
+                        : pkv::kSplitTokens;
+  const pkv_status st = fp8_decode_prepare(
+      &a, &sms, k_scale && v_scale, split, out, q, k_cache, v_cache, block_table, seq_lens, num_seqs,
+      max_blocks_per_seq, max_seq_len, num_blocks, num_q_heads, num_kv_heads, head_dim, block_size,
+      scale, workspace, workspace_bytes);
+  if (st != PKV_OK || a.num_seqs == 0) return st;
+  a.k_bscale = k_scale;
+  a.v_bscale = v_scale;
+  a.skip_empty = 1;
+  return pkv::launch_paged_decode_fp8_block(a, sms, reinterpret_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess
              ? PKV_OK
              : PKV_ECUDA;
 }

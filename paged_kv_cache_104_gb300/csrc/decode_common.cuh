@@ -52,7 +52,7 @@ __device__ __forceinline__ void plan_units(const DecodeArgs& a, int* cu, int sta
         int units = 0;
         if (b < a.num_seqs) {
           if (n[k] < 1 || n[k] > limit) {
-            record_error(a.err, DEVERR_SEQLEN_RANGE);
+            if (n[k] != 0 || !a.skip_empty) record_error(a.err, DEVERR_SEQLEN_RANGE);
           } else {
             const int per = stage_tok > 0 ? stage_tok : a.split_tokens;
             units = a.num_kv_heads * ((n[k] + per - 1) / per + (stage_tok > 0 ? pad : 0));

@@ -1,0 +1,110 @@
+// Decode attention over the block-scaled fp8 cache: the kernel of
+// decode_fp8_kernel.cuh with the scales of every block and head, and the
+// merge of its fp32 partials.
+#include "decode_fp8_kernel.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kMergeWarps = 8;
+
+// Merge of one (sequence, query head) row's partials by a whole CTA, for the
+// few rows of a small batch, which is cut into many short pieces (one
+// sequence of 32,001 tokens: up to 228 a row): o = sum 2^(m_s - M) O_s / sum
+// 2^(m_s - M) l_s.  Warp w takes the partials w, w + 8, ..., a lane four
+// columns; four rows are in flight per warp.  The programmatic dependent of
+// the main kernel.
+__global__ void __launch_bounds__(kMergeWarps * 32)
+merge_row_kernel(const DecodeArgs a) {
+  __shared__ float4 part[kMergeWarps][32];
+  __shared__ float2 ml[kMergeWarps];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = blockIdx.x;
+  const int b = row / a.num_q_heads;
+  const int n = a.seq_lens[b];
+  if (n < 1 || n > min(a.max_seq_len, a.max_blocks_per_seq * kBlockSize)) return;
+  const int h = row - b * a.num_q_heads;
+  const int ns = a.balanced ? a.ws_np[b * a.num_kv_heads + h / (a.num_q_heads / a.num_kv_heads)]
+                            : (n + a.split_tokens - 1) / a.split_tokens;
+  if (ns <= 1) return;              // written directly by the main kernel
+  const int64_t base = (int64_t)row * a.max_splits;
+  const float2* rml = reinterpret_cast<const float2*>(a.ws_ml) + base;
+  const float4* acc = reinterpret_cast<const float4*>(a.ws_acc) + base * (kHD / 4) + lane;
+  // this warp's own reference, so its rows can be read before the others' are known
+  float m = -INFINITY;
+  for (int s = warp + kMergeWarps * lane; s < ns; s += kMergeWarps * 32) m = fmaxf(m, rml[s].x);
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll8, m, o));
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+  for (int s0 = warp; s0 < ns; s0 += 4 * kMergeWarps) {
+    float4 v[4];
+    float2 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int s = s0 + i * kMergeWarps;
+      x[i] = s < ns ? rml[s] : make_float2(-INFINITY, 0.f);
+      v[i] = s < ns ? acc[(int64_t)s * (kHD / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (s0 + i * kMergeWarps >= ns) break;
+      const float w = ex2(x[i].x - m);
+      l = fmaf(w, x[i].y, l);
+      sum.x = fmaf(w, v[i].x, sum.x);
+      sum.y = fmaf(w, v[i].y, sum.y);
+      sum.z = fmaf(w, v[i].z, sum.z);
+      sum.w = fmaf(w, v[i].w, sum.w);
+    }
+  }
+  part[warp][lane] = sum;
+  if (lane == 0) ml[warp] = make_float2(m, l);
+  __syncthreads();
+  if (threadIdx.x >= kHD) return;
+  const int live = min(ns, kMergeWarps);   // the other warps had no partial
+  float M = -INFINITY;
+  for (int w = 0; w < live; ++w) M = fmaxf(M, ml[w].x);
+  float L = 0.f, O = 0.f;
+  for (int w = 0; w < live; ++w) {
+    const float f = ex2(ml[w].x - M);
+    L = fmaf(f, ml[w].y, L);
+    O = fmaf(f, reinterpret_cast<const float*>(part[w])[threadIdx.x], O);
+  }
+  static_cast<__nv_bfloat16*>(a.out)[(int64_t)row * kHD + threadIdx.x] = __float2bfloat16_rn(O / L);
+}
+
+}  // namespace
+
+int fp8_block_split_tokens(int num_seqs, int num_kv_heads, int max_seq_len) {
+  const int64_t streams = num_kv_heads % kBPS == 0 ? num_kv_heads / kBPS : num_kv_heads;
+  const int64_t tokens = (int64_t)num_seqs * streams * max_seq_len;
+  int s = kSplitTokens;
+  while (s > kStageTok && tokens < 4ll * s * (3 * 152)) s /= 2;
+  return s;
+}
+
+cudaError_t launch_paged_decode_fp8_block(const DecodeArgs& a, int num_sms, cudaStream_t stream) {
+  if (a.chunk_prior >= 0 || a.split_tokens % kStageTok != 0 || !a.k_bscale || !a.v_bscale)
+    return cudaErrorInvalidValue;
+  cudaError_t e = launch_fp8<true>(a, num_sms, stream);
+  if (e != cudaSuccess || a.max_splits <= 1) return e;
+  DecodeArgs m = a;
+  m.partials_f16 = 0;
+  m.balanced = fp8_balanced(a);
+  // a warp a row fills the GPU once there are some thousand rows
+  if ((int64_t)a.num_seqs * a.num_q_heads > 8 * 152) return launch_decode_reduce_bf16_128(m, stream);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.num_seqs * a.num_q_heads);
+  cfg.blockDim = dim3(kMergeWarps * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, merge_row_kernel, m);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace pkv

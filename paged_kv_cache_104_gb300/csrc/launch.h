@@ -112,6 +112,10 @@ struct DecodeArgs {
   // fp8 cache only: per-KV-head dequantisation scales [Hkv]
   const float* k_scale;
   const float* v_scale;
+  // block-scaled fp8 cache only: scale bytes [NB][Hkv]
+  const uint8_t* k_bscale;
+  const uint8_t* v_bscale;
+  int skip_empty;           // 1: a length of 0 is padding, not an error
   // 1: the main kernel stores split partials with an L2 evict-last hint and
   // the merge drops each partial line from L2 once read (no write-back);
   // 0: plain stores.  Set by the bf16 decode launcher, except for per-head
@@ -150,6 +154,11 @@ cudaError_t launch_paged_decode_mma(const DecodeArgs& a, int num_sms, cudaStream
 // fp8 (E4M3) cache, bf16 q/out, head_dim 128, group in {1,2,4,8,16}; uses
 // DecodeArgs with k_scale / v_scale set.
 cudaError_t launch_paged_decode_fp8(const DecodeArgs& a, int num_sms, cudaStream_t stream);
+// The same over the block-scaled cache (k_bscale / v_bscale set); any
+// split_tokens that is a multiple of 64.
+cudaError_t launch_paged_decode_fp8_block(const DecodeArgs& a, int num_sms, cudaStream_t stream);
+// Tokens of a split (and least share of a balanced walk) of that decode.
+int fp8_block_split_tokens(int num_seqs, int num_kv_heads, int max_seq_len);
 // Attention over a latent (MLA-style) cache and the output projection: one
 // pool of rank-128 latents, 32 query heads, q already absorbed into a.q;
 // a.k_cache is the latent pool, a.out receives z for sequences covered in one

@@ -61,8 +61,9 @@ def check_positions(positions, slot_mapping, num_positions: int) -> None:
 
 
 def check_decode(block_table, seq_lens, max_seq_len: int, num_blocks: int, block_size: int,
-                 appends: bool = False) -> None:
-    """Every length in [1, min(max_seq_len, blocks per row x block_size)];
+                 appends: bool = False, empty_ok: bool = False) -> None:
+    """Every length in [1, min(max_seq_len, blocks per row x block_size)]
+    (empty_ok: or 0, a padded row);
     every block id a sequence uses inside the pool.  appends: the call also
     writes each sequence's new token at position seq_lens[b] - 1, so those
     rows must be distinct."""
@@ -70,6 +71,8 @@ def check_decode(block_table, seq_lens, max_seq_len: int, num_blocks: int, block
     lens = _host(seq_lens).to(torch.int64)
     limit = min(int(max_seq_len), bt.shape[1] * block_size)
     for b, n in enumerate(lens.tolist()):
+        if n == 0 and empty_ok:
+            continue
         if n < 1 or n > limit:
             raise ValidationError(f"seq_lens[{b}] = {n} outside [1, {limit}]")
         used = bt[b, :(n + block_size - 1) // block_size]
