@@ -421,13 +421,25 @@ size_t pkv_decode_fp8_block_workspace_bytes(int num_seqs, int num_q_heads, int n
  * to a KV head, and a workspace of
  * pkv_decode_fp8_block_workspace_bytes(...).  A length of 0 marks a padded
  * row of the batch: its out row is left as it was and no error is recorded.
- * A NaN code in a stored row makes its sequence's results NaN. */
+ * A NaN code in a key makes its KV head's results NaN, one in a value its
+ * element of them. */
 pkv_status pkv_paged_decode_attention_fp8_block(
     void *out, const void *q, const void *k_cache, const void *v_cache, const uint8_t *k_scale,
     const uint8_t *v_scale, const int32_t *block_table, const int32_t *seq_lens, int num_seqs,
     int max_blocks_per_seq, int max_seq_len, int64_t num_blocks, int num_q_heads, int num_kv_heads,
     int head_dim, int block_size, float scale, void *workspace, size_t workspace_bytes,
     pkv_stream_t stream);
+
+/* pkv_chunked_prefill_attention over the block-scaled pools: the chunk's keys
+ * and values already appended, q and out in bf16, head_dim 128, groups of 1,
+ * 2, 4, 8 or 16.  The result is that of the bf16 call on pools that hold the
+ * same values, bit for bit: a code times its scale is a bf16 number.  A NaN
+ * code in a key or a value makes the rows that see it NaN, and no others. */
+pkv_status pkv_chunked_prefill_attention_fp8_block(
+    void *out, const void *q, const void *k_cache, const void *v_cache, const uint8_t *k_scale,
+    const uint8_t *v_scale, const int32_t *block_table_row, int max_blocks, int prior_len,
+    int chunk_len, int64_t num_blocks, int num_q_heads, int num_kv_heads, int head_dim,
+    int block_size, float scale, pkv_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * Latent (MLA-style) cache.  "The KV cache and prefix caching", section "What

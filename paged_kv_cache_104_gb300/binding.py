@@ -31,6 +31,7 @@ EXPORTS = ("pkv_kv_append", "pkv_decode_workspace_bytes", "pkv_paged_decode_atte
            "pkv_kv_append_fp8", "pkv_paged_decode_attention_fp8",
            "pkv_kv_append_rope", "pkv_kv_append_fp8_block",
            "pkv_decode_fp8_block_workspace_bytes", "pkv_paged_decode_attention_fp8_block",
+           "pkv_chunked_prefill_attention_fp8_block",
            "pkv_latent_append", "pkv_mla_workspace_bytes", "pkv_mla_decode_attention",
            "pkv_mla_decode_attention_append",
            "pkv_fnv1a64", "pkv_prefix_hash_blocks", "pkv_prefix_cache_create",
@@ -122,6 +123,9 @@ def open_library(path: str):
     lib.pkv_paged_decode_attention_fp8_block.argtypes = [p, p, p, p, p, p, p, p, i, i, i, i64, i, i,
                                                          i, i, f, p, sz, p]
     lib.pkv_paged_decode_attention_fp8_block.restype = ctypes.c_int
+    lib.pkv_chunked_prefill_attention_fp8_block.argtypes = [p, p, p, p, p, p, p, i, i, i, i64, i, i,
+                                                            i, i, f, p]
+    lib.pkv_chunked_prefill_attention_fp8_block.restype = ctypes.c_int
     lib.pkv_latent_append.argtypes = [p, p, p, i64, i64, i, i, p]
     lib.pkv_latent_append.restype = ctypes.c_int
     lib.pkv_mla_workspace_bytes.argtypes = [i, i, i, i]
@@ -523,6 +527,37 @@ def paged_decode_attention_fp8_block(out, q, k_cache, v_cache, k_scale, v_scale,
     status = load().pkv_paged_decode_attention_fp8_block(
         op, qp, kp, vp, ksp, vsp, bp, lp, b, blocks, max_seq_len, nb, hq, hkv, d, bs, scale, wp,
         ws_bytes, _stream_on(stream, index))
+    if status:
+        _check(fn, status)
+
+
+def chunked_prefill_attention_fp8_block(out, q, k_cache, v_cache, k_scale, v_scale,
+                                        block_table_row, prior_len: int, scale: float,
+                                        stream=None) -> None:
+    """chunked_prefill_attention over block-scaled uint8 E4M3 pools
+    [NB, Hkv, bs, 128] with scale bytes [NB, Hkv]; out, q bf16 [C, Hq, 128];
+    the chunk's keys and values are already appended."""
+    fn = "pkv_chunked_prefill_attention_fp8_block"
+    if k_cache.dtype is not torch.uint8:
+        _refuse(fn, f"the pools are {k_cache.dtype}, not torch.uint8")
+    index = _device_of(fn, k_cache)
+    shape = k_cache.shape
+    nb, hkv, bs, d = shape
+    if q.dim() != 3 or block_table_row.dim() != 1:
+        _refuse(fn, "q is not [chunk, heads, head_dim] or block_table_row not [blocks]")
+    c, hq, _ = q.shape
+    blocks = block_table_row.shape[0]
+    kp = _whole(fn, "k_cache", k_cache, torch.uint8, shape, index)
+    vp = _whole(fn, "v_cache", v_cache, torch.uint8, shape, index)
+    ksp, vsp = _block_scales(fn, k_cache, k_scale, v_scale, index)
+    qp = _whole(fn, "q", q, torch.bfloat16, (c, hq, d), index)
+    op = _whole(fn, "out", out, torch.bfloat16, (c, hq, d), index)
+    bp = _whole(fn, "block_table_row", block_table_row, torch.int32, (blocks,), index)
+    if _debug:
+        _validate(fn, "check_prefill", block_table_row, prior_len, c, nb, bs)
+    status = load().pkv_chunked_prefill_attention_fp8_block(
+        op, qp, kp, vp, ksp, vsp, bp, blocks, prior_len, c, nb, hq, hkv, d, bs, scale,
+        _stream_on(stream, index))
     if status:
         _check(fn, status)
 

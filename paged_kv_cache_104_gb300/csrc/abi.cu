@@ -812,6 +812,30 @@ pkv_status pkv_chunked_prefill_attention(void* out, const void* q, const void* k
                         reinterpret_cast<cudaStream_t>(stream));
 }
 
+pkv_status pkv_chunked_prefill_attention_fp8_block(
+    void* out, const void* q, const void* k_cache, const void* v_cache, const uint8_t* k_scale,
+    const uint8_t* v_scale, const int32_t* block_table_row, int max_blocks, int prior_len,
+    int chunk_len, int64_t num_blocks, int num_q_heads, int num_kv_heads, int head_dim,
+    int block_size, float scale, pkv_stream_t stream) {
+  pkv_status st = prefill_check(out, q, k_cache, v_cache, block_table_row, max_blocks, prior_len,
+                                chunk_len, num_blocks, num_q_heads, num_kv_heads, head_dim,
+                                block_size, scale, PKV_BF16);
+  if (st != PKV_OK || chunk_len == 0) return st;
+  if (!k_scale || !v_scale) return PKV_EINVAL;
+  if ((int64_t)prior_len + chunk_len > INT_MAX - 4096) return PKV_ERANGE;   // rounded up to tiles
+  int* err = nullptr;
+  int sms = 0;
+  st = device_state(&err, &sms);
+  if (st != PKV_OK) return st;
+  pkv::PrefillArgs a{out, q, k_cache, v_cache, block_table_row, max_blocks, prior_len, chunk_len,
+                     num_blocks, num_q_heads, num_kv_heads, scale, err};
+  a.k_bscale = k_scale;
+  a.v_bscale = v_scale;
+  return pkv::launch_prefill_pair(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PKV_OK
+             : PKV_ECUDA;
+}
+
 pkv_status pkv_decode_prefill_attention(const pkv_decode_prefill_args* x, pkv_stream_t stream) {
   if (!x) return PKV_EINVAL;
   // validate both halves before anything is launched

@@ -211,6 +211,9 @@ struct PrefillArgs {
   int* err;
   // optional span record, as DecodeArgs::span (the tcgen05 prefill)
   unsigned long long* span = nullptr;
+  // block-scaled fp8 pools: scale bytes [NB][Hkv] (null: bf16 pools)
+  const uint8_t* k_bscale = nullptr;
+  const uint8_t* v_bscale = nullptr;
 };
 // tcgen05 path (bf16, head_dim 128, block_size 16): two streams of 128 query
 // rows per CTA sharing each K/V tile -- two query heads of one KV head when

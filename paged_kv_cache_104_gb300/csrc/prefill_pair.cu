@@ -67,9 +67,20 @@
 // rest by the V producer).
 // Every mbarrier wait is bounded; on time-out the kernel records an error,
 // stops issuing work, lets its copies land, frees its TMEM and returns.
+//
+// The block-scaled fp8 cache (F8) changes the producers only.  Its codes times
+// their block's power of two are bf16 numbers, so four converter warps (12-13
+// K, 14-15 V) write the tiles the MMAs read exactly as the bf16 pools' would
+// be, and the result equals the bf16 kernel's on the dequantised pools bit
+// for bit.  A thread's 16-byte pieces of fp8 rows come through a staging
+// buffer of its own by cp.async, half a tile ahead of their conversion: moved
+// into place they are bf16 numbers 2^-120 times the code (an E4M3 exponent
+// read as a bf16 one), and one packed multiply by 2^120 times the scale makes
+// them the values, subnormals included.
 #include <cuda.h>
 
 #include <algorithm>
+#include <climits>
 #include <map>
 #include <mutex>
 #include <queue>
@@ -100,14 +111,25 @@ constexpr int OFF_BAR = OFF_V + NSV * KV_TILE;
 constexpr int SMEM_BYTES = OFF_BAR + 256;
 constexpr int kSoftThreads = 256;
 constexpr int kProdThreads = 64;
-constexpr int W_MMA = 10, W_VPROD = 11;     // K producers: warps 8-9
-constexpr int kThreadsPair = kSoftThreads + kProdThreads + 64;   // + MMA issuer + V producer
-// registers per thread after the split (setmaxnreg), against the launch budget
-constexpr int kRegsSoft = 200, kRegsRest = 96;
-constexpr int kRegsLaunch = (65536 / kThreadsPair) & ~7;   // 168
-static_assert(kRegsSoft * kSoftThreads + kRegsRest * (kThreadsPair - kSoftThreads) <=
-                  kRegsLaunch * kThreadsPair,
-              "the register split must fit in what the CTA was launched with");
+constexpr int W_VPROD = 11;                 // bf16 pools: K producers are warps 8-9
+constexpr int kStage8Tile = BN * HD;        // F8: one fp8 tile, 16 KiB
+constexpr int OFF_STAGE = OFF_BAR + 256;    // F8: the K and the V staging tile
+template <bool F8>
+struct PairCfg {
+  static constexpr int kWMma = F8 ? 8 : 10;
+  // bf16: K producers, MMA issuer, V producer; F8: a warpgroup with the MMA
+  // issuer (its other warps idle) and one of converters
+  static constexpr int kThreads = kSoftThreads + (F8 ? 256 : kProdThreads + 64);
+  static constexpr int kSmem = F8 ? OFF_STAGE + 2 * kStage8Tile : SMEM_BYTES;
+  static constexpr int kVArrivals = F8 ? kProdThreads : 32;
+  // registers per thread after the split (setmaxnreg), against the launch budget
+  static constexpr int kRegsSoft = 200, kRegsRest = F8 ? 56 : 96;
+  static constexpr int kRegsLaunch = (65536 / kThreads) & ~7;   // 168; F8 128
+  static_assert(kRegsSoft * kSoftThreads + kRegsRest * (kThreads - kSoftThreads) <=
+                    kRegsLaunch * kThreads,
+                "the register split must fit in what the CTA was launched with");
+  static_assert(kSmem <= 227 * 1024, "one CTA per SM");
+};
 constexpr uint32_t kTmemColsPair = 512;
 constexpr uint32_t COL_S = 0;                 // S_h at 128*h (P_h in its first 64 columns)
 constexpr uint32_t COL_O = 2 * BN;            // O_h at 256 + 128*h
@@ -126,7 +148,7 @@ enum {
   PB_OD = PB_PF + 4,          // [head]
   PB_COUNT = PB_OD + 2
 };
-static_assert(PB_COUNT * 8 + 8 <= 256, "barrier area");
+static_assert(PB_COUNT * 8 + 12 <= 256, "barrier area");
 
 constexpr int kMaxItems = 512;      // persistent mode: work items in the parameter list
 constexpr int kMaxCtas = 160;
@@ -164,15 +186,70 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// Two E4M3 codes (bytes b0, b1 or b2, b3 of w) as a bf16 pair 2^-120 times
+// their values: s eeee mmm becomes s 0000eeee mmm0000.  The permute puts the
+// lower code's sign where the shift brings it to that half's top.
+template <int SEL>
+__device__ __forceinline__ uint32_t e4m3x2_as_bf16x2(uint32_t w) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(w), "r"(0u), "n"(SEL));
+  return (uint32_t)((int32_t)d >> 4) & 0x87f087f0u;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// A power of two 2^(field - 127) as a bf16 pair.
+__device__ __forceinline__ uint32_t bf16x2_pow2(uint32_t field) { return field * 0x00800080u; }
 
-__global__ void __launch_bounds__(kThreadsPair, 1)
+// 16 codes of a block with scale byte b to their 16 bf16 values; returns
+// whether one is a NaN code (which comes out as 480 times the scale).
+__device__ __forceinline__ bool widen16(const uint4& c, uint32_t b, uint4& lo, uint4& hi) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  uint32_t o[8], nan = 0;
+  const uint32_t f = bf16x2_pow2(min(b + 120u, 254u));   // 2^120 times the scale
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    o[2 * i] = mul_bf16x2(e4m3x2_as_bf16x2<0x1804>(w[i]), f);
+    o[2 * i + 1] = mul_bf16x2(e4m3x2_as_bf16x2<0x3A24>(w[i]), f);
+    nan |= (w[i] & 0x7f7f7f7fu) + 0x01010101u;           // a NaN code carries into its top bit
+  }
+  if (b > 134u) {                                        // what is left of a scale above 2^7
+    const uint32_t f2 = bf16x2_pow2(b - 7u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = mul_bf16x2(o[i], f2);
+  }
+  lo = make_uint4(o[0], o[1], o[2], o[3]);
+  hi = make_uint4(o[4], o[5], o[6], o[7]);
+  return (nan & 0x80808080u) != 0;
+}
+
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts16(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+
+// F8: the pools are block-scaled fp8 (PrefillArgs k_bscale, v_bscale).
+template <bool F8>
+__global__ void __launch_bounds__(PairCfg<F8>::kThreads, 1)
 prefill_pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ CUtensorMap tm_q) {
+  using C = PairCfg<F8>;
+  constexpr int W_MMA = C::kWMma;
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t sbase = smem_u32(smem);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + PB_COUNT);
   int* abort_i = reinterpret_cast<int*>(tmem_slot + 1);
   volatile int* abort_flag = abort_i;
+  int* nan_key = abort_i + 1;   // F8: the first key whose value row holds a NaN
   auto bar = [&](int i) { return smem_u32(bars + i); };
   const PrefillArgs& a = p.a;
   if (sbase & 1023u) {  // swizzled operand tiles need a 1 KiB-aligned base
@@ -226,7 +303,7 @@ prefill_pair_kernel(const __grid_constant__ PairParams p, const __grid_constant_
       mbar_init(bar(PB_KE + s), 4);              // one arrival per head-B softmax warp
     }
     for (int s = 0; s < NSV; ++s) {
-      mbar_init(bar(PB_VF + s), 32);
+      mbar_init(bar(PB_VF + s), C::kVArrivals);
       mbar_init(bar(PB_VE + s), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -236,6 +313,7 @@ prefill_pair_kernel(const __grid_constant__ PairParams p, const __grid_constant_
       mbar_init(bar(PB_OD + i), 1);
     }
     *abort_i = 0;
+    *nan_key = INT_MAX;
     fence_mbar_init();
   }
   if (warp == W_MMA) {
@@ -254,11 +332,120 @@ prefill_pair_kernel(const __grid_constant__ PairParams p, const __grid_constant_
 
   if (warp >= 8) {
     // Warpgroup 2 (producers and MMA issuer) hands registers to
-    // the two softmax warpgroups (kRegsRest / kRegsSoft).  With the 168 of
+    // the two softmax warpgroups (C::kRegsRest / C::kRegsSoft).  With the 168 of
     // the launch the softmax spilled; with 200 its whole S row, the running
     // sums and the packed P fit.
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-    if (warp != W_MMA) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsRest));
+    if (F8 && warp >= 12) {
+      // ------------------------------------------------------------- K/V converters
+      const Item w = item_at(it_begin);
+      const bool is_v = warp >= 14;
+      const uint8_t* pool = static_cast<const uint8_t*>(is_v ? a.v_cache : a.k_cache);
+      const uint8_t* bscale = is_v ? a.v_bscale : a.k_bscale;
+      const uint32_t ring = sbase + (is_v ? OFF_V : OFF_K);
+      const int nst = is_v ? NSV : NSK;
+      const int full_bar = is_v ? PB_VF : PB_KF, empty_bar = is_v ? PB_VE : PB_KE;
+      const int nblk_seq = (p.total_len + kBlockSize - 1) / kBlockSize;
+      // a window's 32 block ids, one per lane, and their scale bytes; blocks
+      // behind the sequence stand as block 0 with scale 1 (their rows are zeros)
+      auto load_ids = [&](int win) {
+        const int idx = win * 32 + lane;
+        int blk = 0;
+        if (idx < nblk_seq) {
+          blk = __ldg(a.block_table_row + idx);
+          if (blk < 0 || (int64_t)blk >= a.num_blocks) {
+            record_error(a.err, DEVERR_BLOCK_RANGE);
+            blk = 0;
+          }
+        }
+        return blk;
+      };
+      auto load_scales = [&](int win, int blk) {
+        return win * 32 + lane < nblk_seq
+                   ? (uint32_t)__ldg(bscale + (int64_t)blk * a.num_kv_heads + w.g) : 127u;
+      };
+      constexpr int kBlkPerTile = BN / kBlockSize;    // 8
+      constexpr int kTilesPerWin = 32 / kBlkPerTile;  // 4
+      // 64 threads a pool: thread (rs, cc) takes the 16 codes of chunk cc in
+      // rows rs and rs + 8 of every block.  They are 32 bytes of a swizzled
+      // bf16 row; the threads of its two 64-column halves store their two
+      // 16-byte chunks in opposite order, so no banks conflict.
+      const int pt = tid & (kProdThreads - 1);
+      const int rs = pt >> 3, cc = pt & 7, half = cc >> 2;
+      const uint32_t stage = sbase + OFF_STAGE + (is_v ? kStage8Tile : 0) + pt * 16;
+      const uint32_t thr_dst = half * KHALF + rs * 128;
+      const uint32_t ch = 2 * (cc & 3);
+      const uint32_t sw_first = ((ch + half) ^ rs) << 4, sw_second = ((ch + 1 - half) ^ rs) << 4;
+      // request the two pieces of block bi of tile j
+      auto request = [&](int ids, int j, int bi) {
+        const int blk = __shfl_sync(0xffffffffu, ids, (j % kTilesPerWin) * kBlkPerTile + bi);
+        const uint8_t* src = pool + ((int64_t)blk * a.num_kv_heads + w.g) * (kBlockSize * HD) +
+                             rs * HD + cc * 16;
+        const int tok = j * BN + bi * kBlockSize + rs;
+        cp_async16(stage + (2 * bi) * (kProdThreads * 16), src, tok < p.total_len ? 16u : 0u);
+        cp_async16(stage + (2 * bi + 1) * (kProdThreads * 16), src + 8 * HD,
+                   tok + 8 < p.total_len ? 16u : 0u);
+      };
+      int ids = load_ids(0);                          // of the window requests are made in
+      uint32_t sc = load_scales(0, ids), sc_before = sc;
+      int ids_next = load_ids(1);
+      for (int bi = 0; bi < kBlkPerTile; ++bi) {
+        request(ids, 0, bi);
+        if (bi % (kBlkPerTile / 2) == kBlkPerTile / 2 - 1) cp_async_commit();
+      }
+      bool go = true;
+      for (int j = 0; j < w.n_tiles; ++j) {
+        const bool more = j + 1 < w.n_tiles;
+        const bool turn = (j + 1) % kTilesPerWin == 0;
+        if (turn && more) {                           // tile j + 1 begins a window
+          const int win = (j + 1) / kTilesPerWin;
+          sc_before = sc;
+          ids = ids_next;
+          sc = load_scales(win, ids);
+          ids_next = load_ids(win + 1);
+        }
+        if (j >= nst) go = wait_or_abort(bar(empty_bar + j % nst), ((j / nst) - 1) & 1, abort_flag, a.err);
+        go = __all_sync(0xffffffffu, go && !*abort_flag);
+        if (!go) break;                               // leave the loop as a warp
+        const uint32_t dst = ring + (j % nst) * KV_TILE + thr_dst;
+        const uint32_t sc_tile = turn && more ? sc_before : sc;
+#pragma unroll 1
+        for (int hb = 0; hb < 2; ++hb) {
+          cp_async_wait<1>();                         // this half's pieces; the other half may fly
+#pragma unroll 2
+          for (int b2 = 0; b2 < kBlkPerTile / 2; ++b2) {
+            const int bi = hb * (kBlkPerTile / 2) + b2;
+            const uint32_t b = __shfl_sync(0xffffffffu, sc_tile, (j % kTilesPerWin) * kBlkPerTile + bi);
+            const uint32_t s0 = stage + (2 * bi) * (kProdThreads * 16);
+            const uint4 c0 = lds16(s0), c1 = lds16(s0 + kProdThreads * 16);
+            const uint32_t d0 = dst + bi * kBlockSize * 128, d1 = d0 + 8 * 128;
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              uint4 lo, hi;
+              if (widen16(r ? c1 : c0, b, lo, hi)) {
+                // A NaN key makes its scores NaN where they are not masked.  A
+                // NaN value would reach masked rows too (0 * NaN): its key is
+                // noted instead, for the rows that see it.
+                if (is_v)
+                  atomicMin(nan_key, j * BN + bi * kBlockSize + 8 * r + rs);
+                else
+                  lo = hi = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+              }
+              const uint32_t d = r ? d1 : d0;
+              sts16(d + sw_first, half ? hi : lo);
+              sts16(d + sw_second, half ? lo : hi);
+            }
+            if (more) request(ids, j + 1, bi);        // both pieces are in registers: refill them
+          }
+          cp_async_commit();
+        }
+        fence_proxy_async_smem();                     // make the tile visible to the tensor core
+        mbar_arrive(bar(full_bar + j % nst));
+      }
+      cp_async_wait<0>();
+    } else if (F8 && warp != W_MMA) {
+      // the issuer's warpgroup, only there for the register split
+    } else if (warp != W_MMA) {
       // ------------------------------------------------------------- K/V producers
       // warps 8-9 gather K, warp 11 gathers V, each pool on its own ring
       const bool is_v = warp == W_VPROD;
@@ -458,7 +645,7 @@ prefill_pair_kernel(const __grid_constant__ PairParams p, const __grid_constant_
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoft));
     // ------------------------------------------------------------- softmax (head hh)
     const int hh = warp >> 2;               // 0: warps 0-3, 1: warps 4-7
     const int r = tid & 127;                // query row in the tile, TMEM lane
@@ -555,7 +742,8 @@ prefill_pair_kernel(const __grid_constant__ PairParams p, const __grid_constant_
     wait_or_abort(bar(PB_OD + hh), (it - it_begin) & 1, abort_flag, a.err);
     __syncwarp();
     tc_fence_after();
-    const float inv = 1.f / l_run;
+    // F8: a key with a NaN value makes the rows that see it NaN
+    const float inv = F8 && row_pos >= *nan_key ? __int_as_float(0x7fffffff) : 1.f / l_run;
     const bool row_ok = (q0 + r) < a.chunk_len;
     __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.out) +
                           ((int64_t)(q0 + r) * a.num_q_heads + head) * HD;
@@ -684,8 +872,13 @@ cudaError_t launch_prefill_pair(const PrefillArgs& a, cudaStream_t stream, int p
   if (p.q_tiles == 0) return cudaSuccess;
   CUtensorMap tm_q;
   if (!encode_rows_map_bf16(&tm_q, a.q, a.chunk_len, a.num_q_heads)) return cudaErrorInvalidValue;
-  cudaError_t e = allow_dynamic_smem(prefill_pair_kernel, SMEM_BYTES);
+  const bool f8 = a.k_bscale != nullptr;
+  using C8 = PairCfg<true>;
+  using C16 = PairCfg<false>;
+  cudaError_t e = f8 ? allow_dynamic_smem(prefill_pair_kernel<true>, C8::kSmem)
+                     : allow_dynamic_smem(prefill_pair_kernel<false>, C16::kSmem);
   if (e != cudaSuccess) return e;
+  if (f8 && persistent_ctas > 0) return cudaErrorInvalidValue;   // the converters run one item
   p.rows_mode = rows_mode_for(a) ? 1 : 0;
   const int n_x = p.rows_mode ? a.num_q_heads : a.num_q_heads / 2;
   const int n_t = p.rows_mode ? (p.q_tiles + 1) / 2 : p.q_tiles;
@@ -724,11 +917,14 @@ cudaError_t launch_prefill_pair(const PrefillArgs& a, cudaStream_t stream, int p
     }
     p.start[P] = (uint16_t)k;
     p.n_list = n_items;
-    prefill_pair_kernel<<<P, kThreadsPair, SMEM_BYTES, stream>>>(p, tm_q);
+    prefill_pair_kernel<false><<<P, C16::kThreads, C16::kSmem, stream>>>(p, tm_q);
     return cudaGetLastError();
   }
   dim3 grid(n_x, n_t);
-  prefill_pair_kernel<<<grid, kThreadsPair, SMEM_BYTES, stream>>>(p, tm_q);
+  if (f8)
+    prefill_pair_kernel<true><<<grid, C8::kThreads, C8::kSmem, stream>>>(p, tm_q);
+  else
+    prefill_pair_kernel<false><<<grid, C16::kThreads, C16::kSmem, stream>>>(p, tm_q);
   return cudaGetLastError();
 }
 

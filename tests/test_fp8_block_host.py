@@ -83,3 +83,49 @@ def test_debug_mode_allows_padded_rows_only_here(monkeypatch):
             B.paged_decode_attention_fp8_block(*a.values(), 64, 0.1)
     finally:
         B.set_debug(False)
+
+
+def _prefill(**kw):
+    P = 0x1000
+    a = dict(out=P, q=P, k=P, v=P, ks=0x1001, vs=0x1003, bt=P, mb=64, prior=100, C=50, nb=32, hq=16, hkv=4, d=128,
+             bs=16, scale=0.1)
+    a.update(kw)
+    return B.load().pkv_chunked_prefill_attention_fp8_block(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(hq=0), 1), (dict(hq=18), 1), (dict(hkv=0), 1), (dict(bs=32), 5), (dict(d=64), 5), (dict(hq=12), 5),
+    (dict(mb=0), 1), (dict(prior=-1), 1), (dict(C=-1), 1), (dict(nb=0), 1), (dict(C=1000), 1),
+    (dict(scale=float("nan")), 1), (dict(out=0), 1), (dict(q=0), 1), (dict(k=0), 1), (dict(v=0), 1), (dict(ks=0), 1),
+    (dict(vs=0), 1), (dict(bt=0), 1), (dict(k=0x1008), 1), (dict(bt=0x1001), 1), (dict(C=0, out=0, q=0), 0),
+    (dict(prior=2 ** 31 - 60, mb=2 ** 28), 3)])
+def test_prefill_refuses(kw, status):
+    assert _prefill(**kw) == status
+
+
+@pytest.mark.parametrize("key,change,name", [
+    ("k", lambda t: t.float(), "pools"), ("v", lambda t: t[:4], "v_cache"), ("ks", lambda t: t.int(), "k_scale"),
+    ("vs", lambda t: t[:4], "v_scale"), ("q", lambda t: t.float(), "q is"), ("q", lambda t: t[:, 0], "q is not"),
+    ("out", lambda t: t[:1], "out"), ("bt", lambda t: t.long(), "block_table_row"), ("bt", lambda t: t[None], "q is not"),
+    ("bt", lambda t: t[::2], "block_table_row")])
+def test_prefill_binding_names_the_tensor(key, change, name, monkeypatch):
+    monkeypatch.setattr(B, "_device_of", lambda fn, t: -1)
+    a = _tensors()
+    a["bt"] = torch.zeros(8, dtype=torch.int32)
+    del a["sl"]
+    a[key] = change(a[key])
+    with pytest.raises(B.PagedKVError, match=name):
+        B.chunked_prefill_attention_fp8_block(*a.values(), 0, 0.1)
+
+
+def test_prefill_debug_mode_names_the_block(monkeypatch):
+    monkeypatch.setattr(B, "_device_of", lambda fn, t: -1)
+    a = _tensors()
+    a["bt"] = torch.tensor([0, 8], dtype=torch.int32)
+    del a["sl"]
+    B.set_debug(True)
+    try:
+        with pytest.raises(B.PagedKVError, match="block 8"):
+            B.chunked_prefill_attention_fp8_block(*a.values(), 20, 0.1)
+    finally:
+        B.set_debug(False)
