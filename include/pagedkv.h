@@ -432,9 +432,9 @@ pkv_status pkv_paged_decode_attention_fp8_block(
 
 /* pkv_chunked_prefill_attention over the block-scaled pools: the chunk's keys
  * and values already appended, q and out in bf16, head_dim 128, groups of 1,
- * 2, 4, 8 or 16.  The result is that of the bf16 call on pools that hold the
- * same values, bit for bit: a code times its scale is a bf16 number.  A NaN
- * code in a key or a value makes the rows that see it NaN, and no others. */
+ * 2, 4, 8 or 16; scale > 0.  A NaN code in a key makes the rows that see it
+ * NaN, one in a value at least its element of them; other rows it leaves
+ * alone. */
 pkv_status pkv_chunked_prefill_attention_fp8_block(
     void *out, const void *q, const void *k_cache, const void *v_cache, const uint8_t *k_scale,
     const uint8_t *v_scale, const int32_t *block_table_row, int max_blocks, int prior_len,

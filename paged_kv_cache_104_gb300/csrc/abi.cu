@@ -821,7 +821,7 @@ pkv_status pkv_chunked_prefill_attention_fp8_block(
                                 chunk_len, num_blocks, num_q_heads, num_kv_heads, head_dim,
                                 block_size, scale, PKV_BF16);
   if (st != PKV_OK || chunk_len == 0) return st;
-  if (!k_scale || !v_scale) return PKV_EINVAL;
+  if (!k_scale || !v_scale || !(scale > 0.f)) return PKV_EINVAL;
   if ((int64_t)prior_len + chunk_len > INT_MAX - 4096) return PKV_ERANGE;   // rounded up to tiles
   int* err = nullptr;
   int sms = 0;

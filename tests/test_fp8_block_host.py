@@ -96,8 +96,8 @@ def _prefill(**kw):
 @pytest.mark.parametrize("kw,status", [
     (dict(hq=0), 1), (dict(hq=18), 1), (dict(hkv=0), 1), (dict(bs=32), 5), (dict(d=64), 5), (dict(hq=12), 5),
     (dict(mb=0), 1), (dict(prior=-1), 1), (dict(C=-1), 1), (dict(nb=0), 1), (dict(C=1000), 1),
-    (dict(scale=float("nan")), 1), (dict(out=0), 1), (dict(q=0), 1), (dict(k=0), 1), (dict(v=0), 1), (dict(ks=0), 1),
-    (dict(vs=0), 1), (dict(bt=0), 1), (dict(k=0x1008), 1), (dict(bt=0x1001), 1), (dict(C=0, out=0, q=0), 0),
+    (dict(scale=float("nan")), 1), (dict(scale=0.0), 1), (dict(scale=-0.1), 1),
+    (dict(out=0), 1), (dict(q=0), 1), (dict(k=0), 1), (dict(v=0), 1), (dict(ks=0), 1), (dict(vs=0), 1), (dict(bt=0), 1), (dict(k=0x1008), 1), (dict(bt=0x1001), 1), (dict(C=0, out=0, q=0), 0),
     (dict(prior=2 ** 31 - 60, mb=2 ** 28), 3)])
 def test_prefill_refuses(kw, status):
     assert _prefill(**kw) == status
