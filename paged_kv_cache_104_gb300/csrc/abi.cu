@@ -831,7 +831,7 @@ pkv_status pkv_chunked_prefill_attention_fp8_block(
                      num_blocks, num_q_heads, num_kv_heads, scale, err};
   a.k_bscale = k_scale;
   a.v_bscale = v_scale;
-  return pkv::launch_prefill_pair(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+  return pkv::launch_prefill_fp8_block(a, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? PKV_OK
              : PKV_ECUDA;
 }

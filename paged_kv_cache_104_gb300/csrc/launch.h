@@ -211,7 +211,7 @@ struct PrefillArgs {
   int* err;
   // optional span record, as DecodeArgs::span (the tcgen05 prefill)
   unsigned long long* span = nullptr;
-  // block-scaled fp8 pools: scale bytes [NB][Hkv] (null: bf16 pools)
+  // block-scaled fp8 pools only: scale bytes [NB][Hkv]
   const uint8_t* k_bscale = nullptr;
   const uint8_t* v_bscale = nullptr;
 };
@@ -224,5 +224,7 @@ struct PrefillArgs {
 // next with that attribute runs on the remaining SMs); 0: one CTA per item.
 bool prefill_pair_persistent_ok(const PrefillArgs& a, int ctas);
 cudaError_t launch_prefill_pair(const PrefillArgs& a, cudaStream_t stream, int persistent_ctas = 0);
+// The same over the block-scaled fp8 pools (k_bscale, v_bscale set).
+cudaError_t launch_prefill_fp8_block(const PrefillArgs& a, int num_sms, cudaStream_t stream);
 
 }  // namespace pkv

@@ -1,0 +1,816 @@
+// Chunked-prefill attention over the block-scaled fp8 cache, on tcgen05
+// (sm_103a).
+//
+// What it computes: chunk row i of one sequence, at absolute position prior +
+// i, attends keys 0 .. prior + i, K and V read as decode(code) * 2^e with an
+// exponent per block of 16 tokens and KV head.  As in the bf16 prefill a CTA
+// carries two streams of 128 query rows that share every K/V tile of 128 keys
+// (two query heads of one KV head over the same rows, or one head over two
+// query tiles when the GQA group is odd); S_h and O_h (128 columns each) of the
+// two streams fill TMEM, P_h lies in the columns of its S_h, and the streams
+// take turns on the tensor core.
+//
+// How the 8-bit cache is fed to it.
+//  * Q K^T needs no conversion: K's codes are operands of kind::f8f6f4 as they
+//    lie, gathered by TMA (one 16-row x 128-byte box per block).  A query row,
+//    scaled by a power of two to a largest element in [128, 256), is split
+//    into two E4M3 numbers, hi = E4M3(q) and lo = E4M3(q - hi): a bf16 has 8
+//    significant bits and the pair holds 4 + 4, exactly so within 2^-9 of the
+//    row's maximum and to 2^-10 absolute below.  S = hi K^T + lo K^T runs at
+//    the time of one 16-bit product.
+//  * P V: P is f16, V's codes are widened to f16 (exact) by four converter
+//    warps, from staging tiles that 1-D bulk copies fill (a block and head is
+//    2 KiB in one piece) into the 128B-swizzled tiles the MMAs read.
+//  * The scales act in the softmax, where they are uniform over 16 columns:
+//    key j of a block with scales 2^ek, 2^ev has the score t_j 2^ek and the
+//    output weight p_j = 2^(s_j + ev - M), M the running maximum of s_j + ev
+//    (raised lazily); O += p_j code_j, and the softmax sum is l += p_j 2^(E -
+//    ev), E the first tile's largest ev; the result is O 2^E / l.  One
+//    exponential serves both sums, at one FMA per block more than without
+//    scales.  A block whose ev is more than 40 off E could lose its weight in
+//    l to the fp32 range of p (an all-zero V block has the smallest ev there
+//    is): from the first tile with such a block on, l is summed from
+//    exponentials of its own.
+//  * A NaN value code would reach rows that do not see its key (0 * NaN).  In
+//    the tiles with masked entries it is zeroed, its key noted, and the rows
+//    that see the key come out as NaN.
+// Roles (512 threads):
+//   warps 0-3 / 4-7   softmax of stream A / B: thread r owns query row r
+//   warp 8            TMEM allocator and MMA issuer
+//   warp 9            producer: block ids, K boxes, V copies, scales
+//   warps 10-11       none (they complete the issuer's warpgroup)
+//   warps 12-15       V converters
+// Both pools' tiles are three stages deep in their fp8 form (K's ring is read
+// by the MMAs, V's by the converters), so 96 KiB are in flight or in use.
+// Measured on the way (2,048 tokens over 4,096, 32/8 heads): both pools
+// converted to bf16 by cp.async producers 280 us, to f16 185 us (with the
+// loads left out 141 us: bound by their latency at 32 KiB in flight).
+//
+// Splitting the keys.  Where the work items are fewer than the SMs, a cluster
+// of 2, 4 or 8 CTAs shares an item's key tiles.  At the end every CTA reads the
+// others' (M, l) rows through distributed shared memory, scales its O to the
+// common maximum, and sends each CTA its share of the columns, which adds them
+// up and writes them.
+// Every mbarrier wait is bounded; on time-out the kernel records an error,
+// stops issuing work, lets its copies land, frees its TMEM and returns.
+#include <cuda.h>
+
+#include <algorithm>
+#include <climits>
+
+#include "common.cuh"
+#include "host_cache.h"
+#include "launch.h"
+#include "tc_common.cuh"
+#include "tmap.h"
+
+namespace pkv {
+namespace {
+
+constexpr int BM = 128, BN = 128, HD = 128;
+constexpr int kTile8 = BN * HD;              // an fp8 tile, 16 KiB
+constexpr int kTile16 = 2 * kTile8;          // an f16 tile, two 64-column halves
+constexpr int kHalf16 = kTile8;
+constexpr int kBlk8 = kBlockSize * HD;       // one block and head, 2 KiB
+constexpr int kBlkPerTile = BN / kBlockSize;
+constexpr int NSK = 3, NSV = 2, NST = 3;     // K ring, V (f16) ring, V staging ring
+constexpr int OFF_Q = 0;                     // [stream][bf16 halves, then hi and lo]
+constexpr int OFF_K = 2 * kTile16;
+constexpr int OFF_V = OFF_K + NSK * kTile8;
+constexpr int OFF_ST = OFF_V + NSV * kTile16;
+constexpr int OFF_SCALES = OFF_ST + NST * kTile8;
+// the scales of a tile's 8 blocks, as the softmax uses them
+struct TileScales {
+  float k[kBlkPerTile];    // scale * log2e * 2^ek
+  float v[kBlkPerTile];    // ev
+  float l[kBlkPerTile];    // 2^(E - ev)
+  int wide;                // a block's ev is far from E
+  int e;                   // E
+  int pad[6];
+};
+// deeper than the K ring: a K stage is free again when its products are done,
+// its scales when its softmax is
+constexpr int kScaleSlots = NSK + 1;
+constexpr int kWideSpread = 40;
+constexpr int OFF_BAR = OFF_SCALES + kScaleSlots * (int)sizeof(TileScales);
+constexpr int OFF_ROWS = OFF_BAR + 256;      // split keys: [stream][row] (reference of l, l)
+constexpr int SMEM_BYTES = OFF_ROWS + 2 * BM * 8;
+constexpr int kSoftThreads = 256;
+constexpr int kThreads = 512;
+constexpr int W_MMA = 8, W_PROD = 9, W_CONV = 12;
+// registers per thread after the split (setmaxnreg), against the launch budget
+constexpr int kRegsSoft = 200, kRegsRest = 56;
+constexpr int kRegsLaunch = (65536 / kThreads) & ~7;   // 128
+static_assert(kRegsSoft * kSoftThreads + kRegsRest * (kThreads - kSoftThreads) <=
+                  kRegsLaunch * kThreads,
+              "the register split must fit in what the CTA was launched with");
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t COL_S = 0, COL_O = 2 * BN;
+constexpr float kLazy = 8.0f;
+static_assert(SMEM_BYTES <= 227 * 1024, "one CTA per SM");
+static_assert(2 * BM * HD * 4 <= OFF_SCALES, "the merge's columns lie in the tiles' place");
+
+enum {
+  B_Q = 0,
+  B_QC,                   // the queries are split
+  B_KF,                   // [NSK]
+  B_KE = B_KF + NSK,
+  B_STF = B_KE + NSK,     // [NST]
+  B_STE = B_STF + NST,
+  B_VF = B_STE + NST,     // [NSV]
+  B_VE = B_VF + NSV,
+  B_SF = B_VE + NSV,      // [stream]
+  B_PF = B_SF + 2,        // [stream][half]
+  B_OD = B_PF + 4,        // [stream]
+  B_COUNT = B_OD + 2
+};
+static_assert(B_COUNT * 8 + 12 <= 256, "barrier area");
+
+struct Params {
+  PrefillArgs a;
+  int total_len;
+  int q_tiles;
+  int rows_mode;          // 1: a CTA's streams are two query tiles of one head
+  int splits;             // CTAs (a cluster) that share an item's key tiles
+};
+
+// the value 2^(b - 127) of a scale byte, 0 included
+__device__ __forceinline__ float scale_value(uint32_t b) {
+  return b == 0 ? __uint_as_float(0x00400000u) : __uint_as_float(b << 23);
+}
+
+// w with its NaN codes replaced by +0; *found is set when there are any
+__device__ __forceinline__ uint32_t drop_nan(uint32_t w, bool* found) {
+  const uint32_t top = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;   // 0x7f carries
+  if (top == 0) return w;
+  *found = true;
+  return w & ~((top >> 7) * 0xffu);
+}
+
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts16(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ void tma_box8(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                         int row) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(row)
+      : "memory");
+}
+// as mma_ss_e, 8-bit operands
+__device__ __forceinline__ void mma8_ss_e(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
+}
+// instruction descriptor, fp32 accumulate, both operands format 0: E4M3 in
+// kind::f8f6f4, f16 in kind::f16
+__host__ __device__ constexpr uint32_t idesc0(bool b_mn_major, int m, int n) {
+  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
+         ((uint32_t)(m >> 4) << 24);
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
+               "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// address of addr in CTA `rank` of the cluster
+__device__ __forceinline__ uint32_t peer(uint32_t addr, int rank) {
+  uint32_t d;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(addr), "r"(rank));
+  return d;
+}
+__device__ __forceinline__ float2 ld_peer2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];"
+               : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_peer(uint32_t addr, float x, float y, float z, float w) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "f"(x), "f"(y), "f"(z),
+               "f"(w)
+               : "memory");
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tm_q,
+                         const __grid_constant__ CUtensorMap tm_k) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const uint32_t sbase = smem_u32(smem);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + B_COUNT);
+  int* abort_i = reinterpret_cast<int*>(tmem_slot + 1);
+  volatile int* abort_flag = abort_i;
+  int* nan_key = abort_i + 1;   // the first key whose value row holds a NaN
+  auto bar = [&](int i) { return smem_u32(bars + i); };
+  const PrefillArgs& a = p.a;
+  // swizzled operand tiles need a 1 KiB-aligned base (the same in every CTA)
+  if (sbase & 1023u) {
+    if (threadIdx.x == 0) record_error(a.err, DEVERR_SMEM_LAYOUT);
+    return;
+  }
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // the item: stream hh covers head[hh], query rows qrow[hh] .. + 127; both
+  // read KV head g; this CTA takes key tiles t0 .. t1 - 1
+  const int tq = (int)gridDim.y - 1 - (int)blockIdx.y;   // heaviest query tiles first
+  const int rank = (int)blockIdx.z;                       // in the cluster
+  const int head0 = p.rows_mode ? (int)blockIdx.x : 2 * (int)blockIdx.x;
+  const int head1 = p.rows_mode ? head0 : head0 + 1;
+  const int qrow0 = p.rows_mode ? 2 * tq * BM : tq * BM;
+  const int qrow1 = p.rows_mode ? qrow0 + BM : qrow0;
+  const int g = head0 / (a.num_q_heads / a.num_kv_heads);
+  const int all_tiles = (a.prior_len + min(a.chunk_len, qrow1 + BM) - 1) / BN + 1;
+  const int t0 = (int)((int64_t)all_tiles * rank / p.splits);
+  const int n_tiles = (int)((int64_t)all_tiles * (rank + 1) / p.splits) - t0;
+
+  if (tid == 0) {
+    mbar_init(bar(B_Q), 1);
+    mbar_init(bar(B_QC), kSoftThreads);
+    for (int s = 0; s < NSK; ++s) {
+      mbar_init(bar(B_KF + s), 1);
+      mbar_init(bar(B_KE + s), 4);               // one arrival per stream-B softmax warp
+    }
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(bar(B_STF + s), 1);
+      mbar_init(bar(B_STE + s), 4);              // one arrival per converter warp
+    }
+    for (int s = 0; s < NSV; ++s) {
+      mbar_init(bar(B_VF + s), 4);
+      mbar_init(bar(B_VE + s), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(B_SF + i), 1);
+      mbar_init(bar(B_PF + 2 * i), 4);           // one arrival per softmax warp
+      mbar_init(bar(B_PF + 2 * i + 1), 4);
+      mbar_init(bar(B_OD + i), 1);
+    }
+    *abort_i = 0;
+    *nan_key = INT_MAX;
+    fence_mbar_init();
+  }
+  if (warp == W_MMA) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_slot)),
+                 "r"(kTmemCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    if (warp == W_PROD) {
+      // ------------------------------------------------------------- producer
+      if (lane == 0 && n_tiles > 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
+      }
+      const uint8_t* vpool = static_cast<const uint8_t*>(a.v_cache);
+      const int nblk_seq = (p.total_len + kBlockSize - 1) / kBlockSize;
+      // a window of 32 blocks (4 tiles), one per lane: ids, and the scale
+      // bytes, K's in bits 0-7 and V's in 8-15 (-1 behind the sequence's end)
+      auto load_ids = [&](int win) {
+        const int idx = win * 32 + lane;
+        int blk = 0;
+        if (idx < nblk_seq) {
+          blk = __ldg(a.block_table_row + idx);
+          if (blk < 0 || (int64_t)blk >= a.num_blocks) {
+            record_error(a.err, DEVERR_BLOCK_RANGE);
+            blk = 0;
+          }
+        }
+        return blk;
+      };
+      auto load_scales = [&](int win, int blk) {
+        if (win * 32 + lane >= nblk_seq) return -1;
+        const int64_t i = (int64_t)blk * a.num_kv_heads + g;
+        return (int)__ldg(a.k_bscale + i) | (int)__ldg(a.v_bscale + i) << 8;
+      };
+      int ids = load_ids(t0 / 4);
+      int sc = load_scales(t0 / 4, ids);
+      int ids_next = load_ids(t0 / 4 + 1);
+      int sc_next = load_scales(t0 / 4 + 1, ids_next);
+      int e_ref = 0;
+      bool go = true;
+      int k_sent = 0, v_sent = 0;
+      for (int jj = 0; jj < n_tiles; ++jj) {
+        const int j = t0 + jj;
+        if (jj > 0 && j % 4 == 0) {
+          ids = ids_next;
+          sc = sc_next;
+          ids_next = load_ids(j / 4 + 1);
+          sc_next = load_scales(j / 4 + 1, ids_next);
+        }
+        const int blk = __shfl_sync(0xffffffffu, ids, (j % 4) * kBlkPerTile + (lane & 7));
+        const int both = __shfl_sync(0xffffffffu, sc, (j % 4) * kBlkPerTile + (lane & 7));
+        const int nb = min(kBlkPerTile, nblk_seq - j * kBlkPerTile);
+        const int64_t tile = (int64_t)blk * a.num_kv_heads + g;
+        // K, and the tile's scales, which its stage's barrier publishes
+        if (jj >= NSK) go = wait_or_abort(bar(B_KE + jj % NSK), (jj / NSK - 1) & 1, abort_flag, a.err);
+        go = __all_sync(0xffffffffu, go && !*abort_flag);
+        if (!go) break;                          // leave the loop as a warp
+        int ev = both < 0 ? INT_MIN : (both >> 8) - 127;
+        if (jj == 0) e_ref = __reduce_max_sync(0xffffffffu, ev);
+        if (both < 0) ev = e_ref;                // no key of this block counts
+        const int off = e_ref - ev;
+        const bool wide = __any_sync(0xffffffffu, abs(off) > kWideSpread);
+        TileScales* ts = reinterpret_cast<TileScales*>(smem + OFF_SCALES) + jj % kScaleSlots;
+        if (lane < kBlkPerTile) {
+          ts->k[lane] = a.scale * 1.4426950408889634f * scale_value(both < 0 ? 127u : both & 0xffu);
+          ts->v[lane] = (float)ev;
+          ts->l[lane] = __uint_as_float((uint32_t)(127 + max(-100, min(100, off))) << 23);
+          if (lane == 0) {
+            ts->wide = wide;
+            ts->e = e_ref;
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(bar(B_KF + jj % NSK), nb * kBlk8);
+        __syncwarp();
+        if (lane < nb)
+          tma_box8(sbase + OFF_K + (jj % NSK) * kTile8 + lane * kBlk8, &tm_k, bar(B_KF + jj % NSK),
+                   (int)(tile * kBlockSize));
+        ++k_sent;
+        // V's codes
+        if (jj >= NST) go = wait_or_abort(bar(B_STE + jj % NST), (jj / NST - 1) & 1, abort_flag, a.err);
+        go = __all_sync(0xffffffffu, go && !*abort_flag);
+        if (!go) break;
+        if (lane == 0) mbar_arrive_expect_tx(bar(B_STF + jj % NST), nb * kBlk8);
+        __syncwarp();
+        if (lane < nb)
+          bulk_g2s_hint(sbase + OFF_ST + (jj % NST) * kTile8 + lane * kBlk8, vpool + tile * kBlk8,
+                        kBlk8, bar(B_STF + jj % NST), policy_evict_normal());
+        ++v_sent;
+      }
+      if (!go && lane == 0) {                    // let the copies in flight land
+        for (int jj = max(0, k_sent - NSK); jj < k_sent; ++jj)
+          mbar_wait(bar(B_KF + jj % NSK), (jj / NSK) & 1, nullptr);
+        for (int jj = max(0, v_sent - NST); jj < v_sent; ++jj)
+          mbar_wait(bar(B_STF + jj % NST), (jj / NST) & 1, nullptr);
+      }
+      __syncwarp();
+    } else if (warp >= W_CONV) {
+      // ------------------------------------------------------------- V converters
+      // thread (rs, cc) takes the 16 codes of chunk cc in row rs of every
+      // block.  They are 32 bytes of a swizzled f16 row; the threads of its two
+      // 64-column halves store their two 16-byte chunks in opposite order, so
+      // no banks conflict.
+      const int pt = tid - W_CONV * 32;
+      const int rs = pt >> 3, cc = pt & 7, half = cc >> 2;
+      const uint32_t ch = 2 * (cc & 3);
+      const uint32_t thr_dst = half * kHalf16 + rs * 128;
+      const uint32_t sw_first = ((ch + half) ^ (rs & 7)) << 4;
+      const uint32_t sw_second = ((ch + 1 - half) ^ (rs & 7)) << 4;
+      const int masked_from = (a.prior_len + qrow0 + 1) / BN;   // tiles with a masked entry
+      bool go = true;
+      for (int jj = 0; jj < n_tiles; ++jj) {
+        const int j = t0 + jj;
+        go = wait_or_abort(bar(B_STF + jj % NST), (jj / NST) & 1, abort_flag, a.err);
+        if (go && jj >= NSV) go = wait_or_abort(bar(B_VE + jj % NSV), (jj / NSV - 1) & 1, abort_flag, a.err);
+        go = __all_sync(0xffffffffu, go && !*abort_flag);
+        if (!go) break;                          // leave the loop as a warp
+        const uint32_t src = sbase + OFF_ST + (jj % NST) * kTile8 + pt * 16;
+        const uint32_t dst = sbase + OFF_V + (jj % NSV) * kTile16 + thr_dst;
+        const bool masked = j >= masked_from;
+#pragma unroll 2
+        for (int b4 = 0; b4 < kBlkPerTile; b4 += 4) {
+          uint4 x[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = lds16(src + (b4 + i) * kBlk8);
+          if (masked) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int key = j * BN + (b4 + i) * kBlockSize + rs;
+              bool found = false;
+              if (key >= p.total_len) {          // behind the sequence: not its data
+                x[i] = make_uint4(0u, 0u, 0u, 0u);
+              } else {
+                x[i].x = drop_nan(x[i].x, &found);
+                x[i].y = drop_nan(x[i].y, &found);
+                x[i].z = drop_nan(x[i].z, &found);
+                x[i].w = drop_nan(x[i].w, &found);
+              }
+              if (found) atomicMin(nan_key, key);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t w[4] = {half ? x[i].z : x[i].x, half ? x[i].w : x[i].y,
+                                   half ? x[i].x : x[i].z, half ? x[i].y : x[i].w};
+            uint32_t o[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              o[2 * k] = e4m3x2_to_f16x2((uint16_t)(w[k] & 0xffffu));
+              o[2 * k + 1] = e4m3x2_to_f16x2((uint16_t)(w[k] >> 16));
+            }
+            const uint32_t d = dst + (b4 + i) * (kBlockSize * 128);
+            sts16(d + sw_first, make_uint4(o[0], o[1], o[2], o[3]));
+            sts16(d + sw_second, make_uint4(o[4], o[5], o[6], o[7]));
+          }
+        }
+        fence_proxy_async_smem();                // make the tile visible to the tensor core
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(B_STE + jj % NST));
+          mbar_arrive(bar(B_VF + jj % NSV));
+        }
+      }
+    } else if (warp == W_MMA && n_tiles > 0) {
+      // ------------------------------------------------------------- MMA issuer
+      if (lane == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_q)) : "memory");
+        mbar_arrive_expect_tx(bar(B_Q), 2 * kTile16);
+        for (int hh = 0; hh < 2; ++hh) {
+          const uint32_t dst = sbase + OFF_Q + hh * kTile16;
+          tma_load_3d(dst, &tm_q, bar(B_Q), 0, hh ? head1 : head0, hh ? qrow1 : qrow0);
+          tma_load_3d(dst + kHalf16, &tm_q, bar(B_Q), 64, hh ? head1 : head0, hh ? qrow1 : qrow0);
+        }
+      }
+      __syncwarp();
+      constexpr uint32_t idesc_qk = idesc0(false, BM, BN);
+      constexpr uint32_t idesc_pv = idesc0(true, BM, HD);
+      // S_h = (hi + lo)_h K^T of ring position jj into the columns of S_h
+      auto issue_qk = [&](int hh, int jj) {
+        const uint32_t kb = sbase + OFF_K + (jj % NSK) * kTile8;
+        const uint32_t qa = sbase + OFF_Q + hh * kTile16;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint64_t ad = make_sw128_desc(qa + (k >> 2) * kTile8 + (k & 3) * 32, 16, 1024);
+          const uint64_t bd = make_sw128_desc(kb + (k & 3) * 32, 16, 1024);
+          mma8_ss_e(tmem + COL_S + hh * BN, ad, bd, idesc_qk, k > 0 ? 1u : 0u);
+        }
+        commit_e(bar(B_SF + hh));
+      };
+      // O_h += P_h V for 64 of the tile's keys, P_h from TMEM (16 keys = 8 columns a step)
+      auto issue_pv = [&](int hh, int jj, int half) {
+        const uint32_t vb = sbase + OFF_V + (jj % NSV) * kTile16;
+#pragma unroll
+        for (int k = half * 4; k < half * 4 + 4; ++k) {
+          const uint64_t bd = make_sw128_desc(vb + k * 16 * 128, kHalf16, 1024);
+          mma_ts_e(tmem + COL_O + hh * HD, tmem + COL_S + hh * BN + k * 8, bd, idesc_pv,
+                   (jj > 0 || k > 0) ? 1u : 0u);
+        }
+        if (half == 1 && jj == n_tiles - 1) commit_e(bar(B_OD + hh));
+      };
+      // The streams alternate: while one's softmax runs, the other's products
+      // do.  Q K_{j+1}^T rewrites S_h, which holds P_h, right behind P_h V_j:
+      // products issued by one thread execute in issue order.
+      auto wait_k = [&](int jj) {
+        return __all_sync(0xffffffffu, wait_fast(bar(B_KF + jj % NSK), (jj / NSK) & 1, abort_flag, a.err));
+      };
+      bool ok = __all_sync(0xffffffffu, wait_or_abort(bar(B_QC), 0, abort_flag, a.err)) && wait_k(0);
+      if (ok) {
+        tc_fence_after();
+        issue_qk(0, 0);
+        issue_qk(1, 0);
+        for (int jj = 0; jj < n_tiles && ok; ++jj) {
+          const bool more = jj + 1 < n_tiles;
+          for (int hh = 0; hh < 2 && ok; ++hh) {
+            ok = __all_sync(0xffffffffu, wait_fast(bar(B_PF + 2 * hh), jj & 1, abort_flag, a.err));
+            if (!ok) break;
+            tc_fence_after();
+            if (hh == 0) ok = __all_sync(0xffffffffu, wait_fast(bar(B_VF + jj % NSV), (jj / NSV) & 1, abort_flag, a.err));
+            if (!ok) break;
+            issue_pv(hh, jj, 0);
+            ok = __all_sync(0xffffffffu, wait_fast(bar(B_PF + 2 * hh + 1), jj & 1, abort_flag, a.err));
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(hh, jj, 1);
+            if (hh == 1) commit_e(bar(B_VE + jj % NSV));   // V no longer needed
+            if (more) {
+              if (hh == 0) ok = wait_k(jj + 1);
+              if (!ok) break;
+              issue_qk(hh, jj + 1);
+            }
+          }
+        }
+      }
+      if (!ok) mbar_wait(bar(B_Q), 0, nullptr);  // after an abort, let the Q load land
+    }
+    __syncwarp();
+    if (p.splits > 1) {                          // the merge's two barriers
+      cluster_sync();
+      cluster_sync();
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+    // ------------------------------------------------------------- softmax (stream hh)
+    const int hh = warp >> 2;               // 0: warps 0-3, 1: warps 4-7
+    const int r = tid & 127;                // query row in the tile, TMEM lane
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t col_s = COL_S + hh * BN, col_o = COL_O + hh * HD;
+    const int q0 = hh ? qrow1 : qrow0, head = hh ? head1 : head0;
+    const int row_pos = a.prior_len + q0 + r;
+    float q_up = 1.f;                       // what brings products back to the query's size
+    if (n_tiles > 0 && wait_or_abort(bar(B_Q), 0, abort_flag, a.err)) {
+      // this row's query, bf16 in two halves, becomes its hi and lo rows
+      const uint32_t qrow = sbase + OFF_Q + hh * kTile16 + r * 128;
+      uint4 x[16];
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        x[i] = lds16(qrow + (i >> 3) * kHalf16 + (((i & 7) ^ (r & 7)) << 4));
+        top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                                     __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
+      }
+      // 2^(7 - exponent of the row's largest element), of zeros and of
+      // infinities or NaN 1
+      top = max(top & 0xffffu, top >> 16) >> 7;
+      const int ex = top == 255 ? 7 : max(-119, min((int)top - 127, 126));
+      const float down = __uint_as_float((uint32_t)(127 + 7 - ex) << 23);
+      q_up = __uint_as_float((uint32_t)(127 + ex - 7) << 23);
+      // an infinite or NaN element makes the row's scores NaN
+      const uint32_t bad = top == 255 ? 0x7f7f7f7fu : 0u;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {         // 16 elements: one chunk of hi and one of lo
+        const uint32_t w[8] = {x[2 * i].x, x[2 * i].y, x[2 * i].z, x[2 * i].w,
+                               x[2 * i + 1].x, x[2 * i + 1].y, x[2 * i + 1].z, x[2 * i + 1].w};
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t h4 = 0, l4 = 0;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float u0 = bf16lo(w[2 * k + e]) * down, u1 = bf16hi(w[2 * k + e]) * down;
+            const uint16_t h = f32x2_to_e4m3x2(u0, u1);
+            const uint32_t back = e4m3x2_to_f16x2(h);
+            const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&back));
+            h4 |= (uint32_t)h << (16 * e);
+            l4 |= (uint32_t)f32x2_to_e4m3x2(u0 - hf.x, u1 - hf.y) << (16 * e);
+          }
+          hi[k] = h4 | bad;
+          lo[k] = l4;
+        }
+        const uint32_t at = qrow + ((i ^ (r & 7)) << 4);
+        sts16(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+        sts16(at + kTile8, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(bar(B_QC));
+    }
+    float m_run = -INFINITY, l_run = 0.f;   // M, in log2 units, and l
+    bool wide = false;                      // once true, l is summed against
+    float ms_run = -INFINITY;               // a running maximum of its own
+    for (int jj = 0; jj < n_tiles; ++jj) {
+      wait_fast(bar(B_SF + hh), jj & 1, abort_flag, a.err);
+      __syncwarp();
+      tc_fence_after();
+      // the S_B commit follows both streams' Q K^T: this K stage can be refilled
+      if (hh == 1 && lane == 0) mbar_arrive(bar(B_KE + jj % NSK));
+      const int k0 = (t0 + jj) * BN;
+      const bool diag = k0 + BN - 1 > a.prior_len + q0;   // causal mask needed
+      // the whole S row into registers: four loads in flight, one wait
+      float t[BN / 32][32];
+#pragma unroll
+      for (int c = 0; c < BN / 32; ++c) tmem_ld32(lane_base + col_s + c * 32, t[c]);
+      tmem_wait_ld();
+#pragma unroll
+      for (int c = 0; c < BN / 32; ++c) reg_fence(t[c]);
+      if (diag) {
+#pragma unroll
+        for (int c = 0; c < BN / 32; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (k0 + c * 32 + i > row_pos) t[c][i] = -INFINITY;
+      }
+      const TileScales* ts =
+          reinterpret_cast<const TileScales*>(smem + OFF_SCALES) + jj % kScaleSlots;
+      // block b's factor from products to scores; never 0, so that a masked
+      // score stays -inf
+      auto kq = [&](int b) { return fmaxf(ts->k[b] * q_up, 1e-38f); };
+      float mx = -INFINITY, ms = -INFINITY;
+#pragma unroll
+      for (int b = 0; b < kBlkPerTile; ++b) {
+        const float* x = &t[b / 2][(b & 1) * 16];
+        float m0 = fmax3(x[0], x[1], x[2]), m1 = fmax3(x[3], x[4], x[5]);
+        m0 = fmax3(m0, x[6], x[7]);
+        m1 = fmax3(m1, x[8], x[9]);
+        m0 = fmax3(m0, x[10], x[11]);
+        m1 = fmax3(m1, x[12], x[13]);
+        m0 = fmax3(m0, x[14], x[15]);
+        const float s0 = fmaxf(m0, m1) * kq(b);
+        ms = fmaxf(ms, s0);
+        mx = fmaxf(mx, s0 + ts->v[b]);
+      }
+      if (ts->wide || wide) {
+        // from here on l = sum 2^(s - ms); before, it was sum 2^(s + E - M)
+        if (!wide && jj > 0) ms_run = m_run - (float)ts->e;
+        wide = true;
+        const float m2 = fmaxf(ms_run, ms);
+        l_run *= ms_run == m2 ? 1.f : fast_exp2(ms_run - m2);
+        ms_run = m2;
+        float sum = 0.f;
+        const float m0 = m2 == -INFINITY ? 0.f : m2;   // no key yet: every weight is 0
+#pragma unroll
+        for (int b = 0; b < kBlkPerTile; ++b) {
+          const float k = kq(b);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) sum += fast_exp2(fmaf(t[b / 2][(b & 1) * 16 + i], k, -m0));
+        }
+        l_run += sum;
+      }
+      float m_new = m_run;
+      if (mx > m_run + kLazy || m_run == -INFINITY) m_new = mx;
+      const float alpha = (m_new == m_run) ? 1.f : fast_exp2(m_run - m_new);
+      if (jj >= 1 && __any_sync(0xffffffffu, alpha != 1.f)) {
+        // O holds P V of the tiles before; the S_h commit of this tile was
+        // issued behind their last product, so that product is complete and
+        // O can be rescaled in place
+        __syncwarp();
+#pragma unroll 1
+        for (int c = 0; c < HD / 32; ++c) {
+          float o[32];
+          tmem_ld32(lane_base + col_o + c * 32, o);
+          tmem_wait_ld();
+          reg_fence(o);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] *= alpha;
+          tmem_st32(lane_base + col_o + c * 32, o);
+        }
+        tmem_wait_st();
+      }
+      // p = 2^(s + ev - M), written as f16 pairs over the first 64 columns of
+      // S; a row that has seen no key (its keys are in another CTA) has p = 0
+      const float m_ref = m_new == -INFINITY ? 0.f : m_new;
+      float l_new = wide ? l_run : l_run * alpha;
+#pragma unroll
+      for (int c = 0; c < BN / 32; ++c) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int b = 2 * c + h;
+          const float k = kq(b), n = ts->v[b] - m_ref;
+          const float2 k2 = make_float2(k, k), n2 = make_float2(n, n);
+          float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            const float2 x = ffma2(make_float2(t[c][16 * h + i], t[c][16 * h + i + 1]), k2, n2);
+            const float2 pp = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+            sum2[(i >> 1) & 1] = fadd2(sum2[(i >> 1) & 1], pp);
+            const __half2 ph = __floats2half2_rn(pp.x, pp.y);
+            pk[8 * h + i / 2] = *reinterpret_cast<const uint32_t*>(&ph);
+          }
+          const float2 s01 = fadd2(sum2[0], sum2[1]);
+          if (!wide) l_new = fmaf(s01.x + s01.y, ts->l[b], l_new);
+        }
+        tmem_st16(lane_base + col_s + c * 16, pk);
+        if (c & 1) {                        // a half of P is in TMEM
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B_PF + 2 * hh + (c >> 1)));
+        }
+      }
+      l_run = l_new;
+      m_run = m_new;
+    }
+    if (n_tiles > 0) {
+      wait_or_abort(bar(B_OD + hh), 0, abort_flag, a.err);
+      __syncwarp();
+      tc_fence_after();
+      if (row_pos >= *nan_key) l_run = __int_as_float(0x7fffffff);   // the row sees a NaN value
+    }
+    const bool row_ok = (q0 + r) < a.chunk_len;
+    __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.out) +
+                          ((int64_t)(q0 + r) * a.num_q_heads + head) * HD;
+    const int e = n_tiles > 0 ? (reinterpret_cast<const TileScales*>(smem + OFF_SCALES))->e : 0;
+    // l stands for l 2^ref, O for O 2^M = O 2^ref unit.  The results take 1 / l
+    // and then the unit, which may leave the normal range when V's scales do.
+    const float ref = wide ? ms_run : m_run - (float)e;
+    const float unit = wide ? fast_exp2(m_run - ms_run) : scale_value((uint32_t)(e + 127));
+    if (p.splits == 1) {
+      const float inv = 1.f / l_run;
+#pragma unroll 1
+      for (int c = 0; c < HD / 32; ++c) {
+        float o[32];
+        tmem_ld32(lane_base + col_o + c * 32, o);
+        tmem_wait_ld();
+        reg_fence(o);
+        if (row_ok) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = o[i] * inv * unit;
+#pragma unroll
+          for (int i = 0; i < 32; i += 8)
+            *reinterpret_cast<uint4*>(orow + c * 32 + i) =
+                make_uint4(pack_bf16(o[i], o[i + 1]), pack_bf16(o[i + 2], o[i + 3]),
+                           pack_bf16(o[i + 4], o[i + 5]), pack_bf16(o[i + 6], o[i + 7]));
+        }
+      }
+    } else {
+      const uint32_t row_at = sbase + OFF_ROWS + (hh * BM + r) * 8;
+      asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(row_at), "f"(ref), "f"(l_run) : "memory");
+      cluster_sync();                       // every CTA's stats are there, its tiles are done with
+      float top = -INFINITY, sum = 0.f;
+      for (int k = 0; k < p.splits; ++k) top = fmaxf(top, ld_peer2(peer(row_at, k)).x);
+      for (int k = 0; k < p.splits; ++k) {
+        const float2 x = ld_peer2(peer(row_at, k));
+        sum = fmaf(fast_exp2(x.x - top), x.y, sum);
+      }
+      const float f = n_tiles > 0 ? fast_exp2(ref - top) / sum : 0.f;
+      // CTA k adds up columns k W .. k W + W - 1: four columns of 128 rows are
+      // 2 KiB in a piece, rows side by side
+      const int W = HD / p.splits;
+#pragma unroll 1
+      for (int c = 0; c < HD / 32; ++c) {
+        float o[32];
+        if (n_tiles > 0) {
+          tmem_ld32(lane_base + col_o + c * 32, o);
+          tmem_wait_ld();
+          reg_fence(o);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+          const int col = c * 32 + i, owner = col / W;
+          const int piece = (rank * 2 + hh) * (W / 4) + (col - owner * W) / 4;
+          st_peer(peer(sbase + piece * (BM * 16) + r * 16, owner), o[i] * f * unit,
+                  o[i + 1] * f * unit, o[i + 2] * f * unit, o[i + 3] * f * unit);
+        }
+      }
+      cluster_sync();
+      for (int c4 = 0; c4 < W / 4; c4 += 2) {
+        float o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = 0.f;
+        for (int k = 0; k < p.splits; ++k) {
+          const uint32_t at = sbase + ((k * 2 + hh) * (W / 4) + c4) * (BM * 16) + r * 16;
+          const uint4 x = lds16(at), y = lds16(at + BM * 16);
+          o[0] += __uint_as_float(x.x);
+          o[1] += __uint_as_float(x.y);
+          o[2] += __uint_as_float(x.z);
+          o[3] += __uint_as_float(x.w);
+          o[4] += __uint_as_float(y.x);
+          o[5] += __uint_as_float(y.y);
+          o[6] += __uint_as_float(y.z);
+          o[7] += __uint_as_float(y.w);
+        }
+        if (row_ok)
+          *reinterpret_cast<uint4*>(orow + rank * W + c4 * 4) =
+              make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]),
+                         pack_bf16(o[6], o[7]));
+      }
+    }
+  }
+  __syncthreads();
+  if (warp == W_MMA) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(kTmemCols));
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_prefill_fp8_block(const PrefillArgs& a, int num_sms, cudaStream_t stream) {
+  Params p;
+  p.a = a;
+  p.total_len = a.prior_len + a.chunk_len;
+  p.q_tiles = (a.chunk_len + BM - 1) / BM;
+  if (p.q_tiles == 0) return cudaSuccess;
+  // two query tiles of one head to a CTA when the group is odd
+  p.rows_mode = (a.num_q_heads / a.num_kv_heads) % 2;
+  CUtensorMap tm_q, tm_k;
+  if (!encode_rows_map_bf16(&tm_q, a.q, a.chunk_len, a.num_q_heads) ||
+      !encode_pool_map_u8(&tm_k, a.k_cache, a.num_blocks * a.num_kv_heads * kBlockSize))
+    return cudaErrorInvalidValue;
+  cudaError_t e = allow_dynamic_smem(prefill_fp8_block_kernel, SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  const int n_x = p.rows_mode ? a.num_q_heads : a.num_q_heads / 2;
+  const int n_t = p.rows_mode ? (p.q_tiles + 1) / 2 : p.q_tiles;
+  const int most_tiles = (p.total_len - 1) / BN + 1;
+  // CTAs to an item, while they find SMs and key tiles
+  p.splits = 1;
+  while (p.splits < 8 && (int64_t)n_x * n_t * p.splits * 2 <= num_sms && p.splits * 2 <= most_tiles)
+    p.splits *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(n_x, n_t, p.splits);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = p.splits;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, prefill_fp8_block_kernel, p, tm_q, tm_k);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace pkv

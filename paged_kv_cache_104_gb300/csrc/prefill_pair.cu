@@ -67,35 +67,9 @@
 // rest by the V producer).
 // Every mbarrier wait is bounded; on time-out the kernel records an error,
 // stops issuing work, lets its copies land, frees its TMEM and returns.
-//
-// The block-scaled fp8 cache (F8).
-//  * Four converter warps (12-13 K, 14-15 V) take the producers' place.  A
-//    thread's 16-byte pieces of fp8 rows come through a staging buffer of its
-//    own by cp.async, half a tile ahead of their conversion, and go to the
-//    tiles as f16: every E4M3 code is an f16 number, so the tiles hold the
-//    raw codes exactly, and all operands are f16.
-//  * The scales act in the softmax, where they are uniform over 16 columns:
-//    key j of a block with scales 2^ek, 2^ev has the score t_j 2^ek and the
-//    output weight p_j = 2^(s_j + ev - M), M the running maximum of s_j + ev:
-//    O += p_j code_j, and the softmax sum is l += p_j 2^(E - ev), E the first
-//    tile's largest ev; the result is O 2^E / l.  One exponential serves both
-//    sums, at one FMA per block more than without scales.  A block whose ev is
-//    more than 40 off E could lose its weight in l to the fp32 range of p (an
-//    all-zero V block has the smallest ev there is): from the first tile with
-//    such a block on, l is summed from exponentials of its own.
-//  * (Converting to bf16 with the scale multiplied in, so that the rest of the
-//    kernel stays as it is, took 55 instructions per 16 codes instead of 18
-//    and made the converters the bound: 280 us against 130 us for the bf16
-//    pools on a 2,048-token chunk over 4,096.)
-//  * Queries become f16 in shared memory once, each row brought to [1, 2) by a
-//    power of two that goes back into its scores.
-//  * A NaN value code would reach rows that do not see its key (0 * NaN).  In
-//    the tiles with masked entries it is zeroed, its key noted, and the rows
-//    that see the key come out as NaN.
 #include <cuda.h>
 
 #include <algorithm>
-#include <climits>
 #include <map>
 #include <mutex>
 #include <queue>
@@ -126,39 +100,14 @@ constexpr int OFF_BAR = OFF_V + NSV * KV_TILE;
 constexpr int SMEM_BYTES = OFF_BAR + 256;
 constexpr int kSoftThreads = 256;
 constexpr int kProdThreads = 64;
-constexpr int W_VPROD = 11;                 // bf16 pools: K producers are warps 8-9
-constexpr int kStage8Tile = BN * HD;        // F8: one fp8 tile, 16 KiB
-constexpr int OFF_STAGE = OFF_BAR + 256;    // F8: the K and the V staging tile
-// F8: the scales of a tile's 8 blocks, as the softmax uses them.  The ring is
-// deeper than the K ring: a K stage is free again when its products are done,
-// its scales when its softmax is.
-struct TileScales {
-  float k[8];    // scale * log2e * 2^ek
-  float v[8];    // ev
-  float l[8];    // 2^(E - ev)
-  int wide;      // a block's ev is far from E
-  int e;         // E
-  int pad[6];
-};
-constexpr int kScaleSlots = 4;
-constexpr int OFF_SCALES = OFF_STAGE + 2 * kStage8Tile;
-constexpr int kWideSpread = 40;
-template <bool F8>
-struct PairCfg {
-  static constexpr int kWMma = F8 ? 8 : 10;
-  // bf16: K producers, MMA issuer, V producer; F8: a warpgroup with the MMA
-  // issuer (its other warps idle) and one of converters
-  static constexpr int kThreads = kSoftThreads + (F8 ? 256 : kProdThreads + 64);
-  static constexpr int kSmem = F8 ? OFF_SCALES + kScaleSlots * (int)sizeof(TileScales) : SMEM_BYTES;
-  static constexpr int kVArrivals = F8 ? kProdThreads : 32;
-  // registers per thread after the split (setmaxnreg), against the launch budget
-  static constexpr int kRegsSoft = 200, kRegsRest = F8 ? 56 : 96;
-  static constexpr int kRegsLaunch = (65536 / kThreads) & ~7;   // 168; F8 128
-  static_assert(kRegsSoft * kSoftThreads + kRegsRest * (kThreads - kSoftThreads) <=
-                    kRegsLaunch * kThreads,
-                "the register split must fit in what the CTA was launched with");
-  static_assert(kSmem <= 227 * 1024, "one CTA per SM");
-};
+constexpr int W_MMA = 10, W_VPROD = 11;     // K producers: warps 8-9
+constexpr int kThreadsPair = kSoftThreads + kProdThreads + 64;   // + MMA issuer + V producer
+// registers per thread after the split (setmaxnreg), against the launch budget
+constexpr int kRegsSoft = 200, kRegsRest = 96;
+constexpr int kRegsLaunch = (65536 / kThreadsPair) & ~7;   // 168
+static_assert(kRegsSoft * kSoftThreads + kRegsRest * (kThreadsPair - kSoftThreads) <=
+                  kRegsLaunch * kThreadsPair,
+              "the register split must fit in what the CTA was launched with");
 constexpr uint32_t kTmemColsPair = 512;
 constexpr uint32_t COL_S = 0;                 // S_h at 128*h (P_h in its first 64 columns)
 constexpr uint32_t COL_O = 2 * BN;            // O_h at 256 + 128*h
@@ -175,10 +124,9 @@ enum {
   PB_SF = PB_VE + NSV,        // [head]
   PB_PF = PB_SF + 2,          // [head][half]
   PB_OD = PB_PF + 4,          // [head]
-  PB_QC = PB_OD + 2,          // F8: the queries are f16
-  PB_COUNT = PB_QC + 1
+  PB_COUNT = PB_OD + 2
 };
-static_assert(PB_COUNT * 8 + 12 <= 256, "barrier area");
+static_assert(PB_COUNT * 8 + 8 <= 256, "barrier area");
 
 constexpr int kMaxItems = 512;      // persistent mode: work items in the parameter list
 constexpr int kMaxCtas = 160;
@@ -216,49 +164,15 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// 4 E4M3 codes as f16 pairs.
-__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  lo = e4m3x2_to_f16x2((uint16_t)(w & 0xffffu));
-  hi = e4m3x2_to_f16x2((uint16_t)(w >> 16));
-}
 
-// w with its NaN codes replaced by +0; *found is set when there are any.
-__device__ __forceinline__ uint32_t drop_nan(uint32_t w, bool* found) {
-  const uint32_t top = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;   // 0x7f carries
-  if (top == 0) return w;
-  *found = true;
-  return w & ~((top >> 7) * 0xffu);
-}
-
-// The value 2^(b - 127) of a scale byte, 0 included.
-__device__ __forceinline__ float scale_value(uint32_t b) {
-  return b == 0 ? __uint_as_float(0x00400000u) : __uint_as_float(b << 23);
-}
-
-__device__ __forceinline__ uint2 lds8(uint32_t addr) {
-  uint2 v;
-  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ void sts16(uint32_t addr, const uint4& v) {
-  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
-               "r"(v.w)
-               : "memory");
-}
-
-// F8: the pools are block-scaled fp8 (PrefillArgs k_bscale, v_bscale).
-template <bool F8>
-__global__ void __launch_bounds__(PairCfg<F8>::kThreads, 1)
+__global__ void __launch_bounds__(kThreadsPair, 1)
 prefill_pair_kernel(const __grid_constant__ PairParams p, const __grid_constant__ CUtensorMap tm_q) {
-  using C = PairCfg<F8>;
-  constexpr int W_MMA = C::kWMma;
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t sbase = smem_u32(smem);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + PB_COUNT);
   int* abort_i = reinterpret_cast<int*>(tmem_slot + 1);
   volatile int* abort_flag = abort_i;
-  int* nan_key = abort_i + 1;   // F8: the first key whose value row holds a NaN
   auto bar = [&](int i) { return smem_u32(bars + i); };
   const PrefillArgs& a = p.a;
   if (sbase & 1023u) {  // swizzled operand tiles need a 1 KiB-aligned base
@@ -312,7 +226,7 @@ prefill_pair_kernel(const __grid_constant__ PairParams p, const __grid_constant_
       mbar_init(bar(PB_KE + s), 4);              // one arrival per head-B softmax warp
     }
     for (int s = 0; s < NSV; ++s) {
-      mbar_init(bar(PB_VF + s), C::kVArrivals);
+      mbar_init(bar(PB_VF + s), 32);
       mbar_init(bar(PB_VE + s), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -321,9 +235,7 @@ prefill_pair_kernel(const __grid_constant__ PairParams p, const __grid_constant_
       mbar_init(bar(PB_PF + 2 * i + 1), 4);
       mbar_init(bar(PB_OD + i), 1);
     }
-    mbar_init(bar(PB_QC), kSoftThreads);
     *abort_i = 0;
-    *nan_key = INT_MAX;
     fence_mbar_init();
   }
   if (warp == W_MMA) {
@@ -342,156 +254,11 @@ prefill_pair_kernel(const __grid_constant__ PairParams p, const __grid_constant_
 
   if (warp >= 8) {
     // Warpgroup 2 (producers and MMA issuer) hands registers to
-    // the two softmax warpgroups (C::kRegsRest / C::kRegsSoft).  With the 168 of
+    // the two softmax warpgroups (kRegsRest / kRegsSoft).  With the 168 of
     // the launch the softmax spilled; with 200 its whole S row, the running
     // sums and the packed P fit.
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsRest));
-    if (F8 && warp >= 12) {
-      // ------------------------------------------------------------- K/V converters
-      const Item w = item_at(it_begin);
-      const bool is_v = warp >= 14;
-      const uint8_t* pool = static_cast<const uint8_t*>(is_v ? a.v_cache : a.k_cache);
-      const uint32_t ring = sbase + (is_v ? OFF_V : OFF_K);
-      const int nst = is_v ? NSV : NSK;
-      const int full_bar = is_v ? PB_VF : PB_KF, empty_bar = is_v ? PB_VE : PB_KE;
-      const int nblk_seq = (p.total_len + kBlockSize - 1) / kBlockSize;
-      // a window's 32 block ids, one per lane, and (warp 12) their scale bytes,
-      // K's in bits 0-7 and V's in 8-15; -1 behind the sequence's end
-      auto load_ids = [&](int win) {
-        const int idx = win * 32 + lane;
-        int blk = 0;
-        if (idx < nblk_seq) {
-          blk = __ldg(a.block_table_row + idx);
-          if (blk < 0 || (int64_t)blk >= a.num_blocks) {
-            record_error(a.err, DEVERR_BLOCK_RANGE);
-            blk = 0;
-          }
-        }
-        return blk;
-      };
-      const bool scales = warp == 12;
-      auto load_scales = [&](int win, int blk) {
-        if (!scales || win * 32 + lane >= nblk_seq) return -1;
-        const int64_t i = (int64_t)blk * a.num_kv_heads + w.g;
-        return (int)__ldg(a.k_bscale + i) | (int)__ldg(a.v_bscale + i) << 8;
-      };
-      int e_ref = 0;
-      // the scales of tile j: lane i < 8 writes block i's
-      auto publish = [&](int sc, int j) {
-        const int both = __shfl_sync(0xffffffffu, sc, (j % 4) * 8 + (lane & 7));
-        int ev = both < 0 ? INT_MIN : (both >> 8) - 127;
-        if (j == 0) e_ref = __reduce_max_sync(0xffffffffu, ev);
-        if (both < 0) ev = e_ref;                     // no key of this block counts
-        const int off = e_ref - ev;
-        const bool wide = __any_sync(0xffffffffu, abs(off) > kWideSpread);
-        TileScales* ts = reinterpret_cast<TileScales*>(smem + OFF_SCALES) + (j % kScaleSlots);
-        if (lane < 8) {
-          ts->k[lane] = a.scale * 1.4426950408889634f * scale_value(both < 0 ? 127u : both & 0xffu);
-          ts->v[lane] = (float)ev;
-          ts->l[lane] = __uint_as_float((uint32_t)(127 + max(-100, min(100, off))) << 23);
-          if (lane == 0) {
-            ts->wide = wide;
-            ts->e = e_ref;
-          }
-        }
-      };
-      constexpr int kBlkPerTile = BN / kBlockSize;    // 8
-      constexpr int kTilesPerWin = 32 / kBlkPerTile;  // 4
-      // 64 threads a pool: thread (rs, cc) takes the 16 codes of chunk cc in
-      // rows rs and rs + 8 of every block.  They are 32 bytes of a swizzled
-      // f16 row; the threads of its two 64-column halves store their two
-      // 16-byte chunks in opposite order, so no banks conflict.
-      const int pt = tid & (kProdThreads - 1);
-      const int rs = pt >> 3, cc = pt & 7, half = cc >> 2;
-      const uint32_t stage = sbase + OFF_STAGE + (is_v ? kStage8Tile : 0) + pt * 16;
-      const uint32_t thr_dst = half * KHALF + rs * 128;
-      const uint32_t ch = 2 * (cc & 3);
-      const uint32_t sw_first = ((ch + half) ^ rs) << 4, sw_second = ((ch + 1 - half) ^ rs) << 4;
-      const int first = half * 8, second = 8 - first;   // their codes in the staged piece
-      // V tiles with a masked entry: their NaN codes are dropped
-      const int masked_from = (a.prior_len + w.qrow[0] + 1) / BN;
-      // request the two pieces of block bi of tile j
-      auto request = [&](int ids, int j, int bi) {
-        const int blk = __shfl_sync(0xffffffffu, ids, (j % kTilesPerWin) * kBlkPerTile + bi);
-        const uint8_t* src = pool + ((int64_t)blk * a.num_kv_heads + w.g) * (kBlockSize * HD) +
-                             rs * HD + cc * 16;
-        const int tok = j * BN + bi * kBlockSize + rs;
-        cp_async16(stage + (2 * bi) * (kProdThreads * 16), src, tok < p.total_len ? 16u : 0u);
-        cp_async16(stage + (2 * bi + 1) * (kProdThreads * 16), src + 8 * HD,
-                   tok + 8 < p.total_len ? 16u : 0u);
-      };
-      int ids = load_ids(0);                          // of the window requests are made in
-      int sc = load_scales(0, ids), sc_before = sc;
-      int ids_next = load_ids(1);
-      for (int bi = 0; bi < kBlkPerTile; ++bi) {
-        request(ids, 0, bi);
-        if (bi % (kBlkPerTile / 2) == kBlkPerTile / 2 - 1) cp_async_commit();
-      }
-      bool go = true;
-      for (int j = 0; j < w.n_tiles; ++j) {
-        const bool more = j + 1 < w.n_tiles;
-        const bool turn = (j + 1) % kTilesPerWin == 0;
-        if (turn && more) {                           // tile j + 1 begins a window
-          const int win = (j + 1) / kTilesPerWin;
-          sc_before = sc;
-          ids = ids_next;
-          sc = load_scales(win, ids);
-          ids_next = load_ids(win + 1);
-        }
-        if (j >= nst) go = wait_or_abort(bar(empty_bar + j % nst), ((j / nst) - 1) & 1, abort_flag, a.err);
-        go = __all_sync(0xffffffffu, go && !*abort_flag);
-        if (!go) break;                               // leave the loop as a warp
-        const uint32_t dst = ring + (j % nst) * KV_TILE + thr_dst;
-        if (scales) publish(turn && more ? sc_before : sc, j);
-        const bool drop = is_v && j >= masked_from;
-#pragma unroll 1
-        for (int hb = 0; hb < 2; ++hb) {
-          cp_async_wait<1>();                         // this half's pieces; the other half may fly
-#pragma unroll 2
-          for (int b2 = 0; b2 < kBlkPerTile / 2; ++b2) {
-            const int bi = hb * (kBlkPerTile / 2) + b2;
-            const uint32_t s0 = stage + (2 * bi) * (kProdThreads * 16);
-            const uint32_t d0 = dst + bi * kBlockSize * 128;
-            uint2 x[2][2];
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              x[r][0] = lds8(s0 + r * (kProdThreads * 16) + first);
-              x[r][1] = lds8(s0 + r * (kProdThreads * 16) + second);
-            }
-            if (drop) {
-#pragma unroll
-              for (int r = 0; r < 2; ++r) {
-                bool found = false;
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                  x[r][k].x = drop_nan(x[r][k].x, &found);
-                  x[r][k].y = drop_nan(x[r][k].y, &found);
-                }
-                if (found) atomicMin(nan_key, j * BN + bi * kBlockSize + 8 * r + rs);
-              }
-            }
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              uint4 v[2];
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                widen4(x[r][k].x, v[k].x, v[k].y);
-                widen4(x[r][k].y, v[k].z, v[k].w);
-              }
-              sts16(d0 + r * (8 * 128) + sw_first, v[0]);
-              sts16(d0 + r * (8 * 128) + sw_second, v[1]);
-            }
-            if (more) request(ids, j + 1, bi);        // both pieces are in registers: refill them
-          }
-          cp_async_commit();
-        }
-        fence_proxy_async_smem();                     // make the tile visible to the tensor core
-        mbar_arrive(bar(full_bar + j % nst));
-      }
-      cp_async_wait<0>();
-    } else if (F8 && warp != W_MMA) {
-      // the issuer's warpgroup, only there for the register split
-    } else if (warp != W_MMA) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    if (warp != W_MMA) {
       // ------------------------------------------------------------- K/V producers
       // warps 8-9 gather K, warp 11 gathers V, each pool on its own ring
       const bool is_v = warp == W_VPROD;
@@ -610,8 +377,8 @@ prefill_pair_kernel(const __grid_constant__ PairParams p, const __grid_constant_
           }
         }
         __syncwarp();
-        constexpr uint32_t idesc_qk = make_idesc(false, BM, BN, !F8);
-        constexpr uint32_t idesc_pv = make_idesc(true, BM, HD, !F8);
+        constexpr uint32_t idesc_qk = make_idesc(false, BM, BN);
+        constexpr uint32_t idesc_pv = make_idesc(true, BM, HD);
         // S_h = Q_h K^T of ring position jg into the TMEM columns of S_h
         auto issue_qk = [&](int hh, int jg) {
           const uint32_t kb = sbase + OFF_K + (jg % NSK) * KV_TILE;
@@ -656,10 +423,9 @@ prefill_pair_kernel(const __grid_constant__ PairParams p, const __grid_constant_
           const Item w = item_at(it);
           const int ii = it - it_begin;
           // this item's Q
-          ok = __all_sync(0xffffffffu, wait_or_abort(bar(F8 ? PB_QC : PB_Q), ii & 1, abort_flag, a.err));
+          ok = __all_sync(0xffffffffu, wait_or_abort(bar(PB_Q), ii & 1, abort_flag, a.err));
           if (!ok) break;
           q0_landed = true;
-          if (F8) tc_fence_after();
           ok = __all_sync(0xffffffffu, wait_fast(bar(PB_KF + jg % NSK), (jg / NSK) & 1, abort_flag, a.err));
           if (!ok) break;
           tc_fence_after();
@@ -692,55 +458,19 @@ prefill_pair_kernel(const __grid_constant__ PairParams p, const __grid_constant_
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoft));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
     // ------------------------------------------------------------- softmax (head hh)
     const int hh = warp >> 2;               // 0: warps 0-3, 1: warps 4-7
     const int r = tid & 127;                // query row in the tile, TMEM lane
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t col_s = COL_S + hh * BN, col_o = COL_O + hh * HD;
     const float sl2 = a.scale * 1.4426950408889634f;
-    float q_up = 1.f;                       // F8: the power of two taken out of the row's query
-    if constexpr (F8) {
-      if (wait_or_abort(bar(PB_Q), 0, abort_flag, a.err)) {
-        // this row's query to f16 in place
-        const uint32_t qrow = sbase + OFF_Q + hh * Q_BYTES + r * 128;
-        uint32_t top = 0;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const uint32_t at = qrow + (i >> 3) * QHALF + (((i & 7) ^ (r & 7)) << 4);
-          const uint2 x = lds8(at), y = lds8(at + 8);
-          top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
-                                       __vmaxu2(y.x & 0x7fff7fffu, y.y & 0x7fff7fffu)));
-        }
-        top = max(top & 0xffffu, top >> 16) >> 7;
-        // zeros, subnormals, infinities and NaN are taken as they are
-        const int ex = top == 0 || top == 255 ? 0 : (int)min(top, 253u) - 127;
-        const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
-        q_up = __uint_as_float((uint32_t)(127 + ex) << 23);
-        auto two = [&](uint32_t u) {
-          const __half2 h = __floats2half2_rn(bf16lo(u) * down, bf16hi(u) * down);
-          return *reinterpret_cast<const uint32_t*>(&h);
-        };
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const uint32_t at = qrow + (i >> 3) * QHALF + (((i & 7) ^ (r & 7)) << 4);
-          const uint2 x = lds8(at), y = lds8(at + 8);
-          sts16(at, make_uint4(two(x.x), two(x.y), two(y.x), two(y.y)));
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(bar(PB_QC));
-      }
-    }
     int jg = 0;                             // tile position over all items
     for (int it = it_begin; it < it_end; ++it) {
     const Item w = item_at(it);
     const int q0 = w.qrow[hh], head = w.head[hh];
     const int row_pos = a.prior_len + q0 + r;
     float m_run = -INFINITY, l_run = 0.f;   // running max in scaled log2 units
-    // F8: m_run is M, the maximum of score plus ev; once wide, l is summed
-    // against a running maximum of its own
-    bool wide = false;
-    float ms_run = -INFINITY;
     for (int j = 0; j < w.n_tiles; ++j, ++jg) {
       wait_fast(bar(PB_SF + hh), jg & 1, abort_flag, a.err);
       __syncwarp();
@@ -763,57 +493,17 @@ prefill_pair_kernel(const __grid_constant__ PairParams p, const __grid_constant_
           for (int i = 0; i < 32; ++i)
             if (k0 + c * 32 + i > row_pos) t[c][i] = -INFINITY;
       }
-      float mx;
-      const TileScales* ts = nullptr;
-      // block b's factor from products to scores; never 0, so that a masked
-      // score stays -inf
-      auto kq = [&](int b) { return fmaxf(ts->k[b] * q_up, 1e-38f); };
-      if constexpr (F8) {
-        ts = reinterpret_cast<const TileScales*>(smem + OFF_SCALES) + (jg % kScaleSlots);
-        mx = -INFINITY;
-        float ms = -INFINITY;
+      float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int b = 0; b < BN / 16; ++b) {
-          const float* x = &t[b / 2][(b & 1) * 16];
-          float m0 = fmax3(x[0], x[1], x[2]), m1 = fmax3(x[3], x[4], x[5]);
-          m0 = fmax3(m0, x[6], x[7]);
-          m1 = fmax3(m1, x[8], x[9]);
-          m0 = fmax3(m0, x[10], x[11]);
-          m1 = fmax3(m1, x[12], x[13]);
-          m0 = fmax3(m0, x[14], x[15]);
-          const float s0 = fmaxf(m0, m1) * kq(b);
-          ms = fmaxf(ms, s0);
-          mx = fmaxf(mx, s0 + ts->v[b]);
+      for (int c = 0; c < BN / 32; ++c)
+#pragma unroll
+        for (int i = 0; i < 32; i += 8) {
+          mx4[0] = fmax3(mx4[0], t[c][i], t[c][i + 4]);
+          mx4[1] = fmax3(mx4[1], t[c][i + 1], t[c][i + 5]);
+          mx4[2] = fmax3(mx4[2], t[c][i + 2], t[c][i + 6]);
+          mx4[3] = fmax3(mx4[3], t[c][i + 3], t[c][i + 7]);
         }
-        if (ts->wide || wide) {
-          // from here on l = sum 2^(s - ms); before, it was sum 2^(s + E - M)
-          if (!wide && jg > 0) ms_run = m_run - (float)ts->e;
-          wide = true;
-          const float m2 = fmaxf(ms_run, ms);
-          l_run *= ms_run == m2 ? 1.f : fast_exp2(ms_run - m2);
-          ms_run = m2;
-          float sum = 0.f;
-#pragma unroll
-          for (int b = 0; b < BN / 16; ++b) {
-            const float k = kq(b);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) sum += fast_exp2(fmaf(t[b / 2][(b & 1) * 16 + i], k, -m2));
-          }
-          l_run += sum;
-        }
-      } else {
-        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-  #pragma unroll
-        for (int c = 0; c < BN / 32; ++c)
-  #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            mx4[0] = fmax3(mx4[0], t[c][i], t[c][i + 4]);
-            mx4[1] = fmax3(mx4[1], t[c][i + 1], t[c][i + 5]);
-            mx4[2] = fmax3(mx4[2], t[c][i + 2], t[c][i + 6]);
-            mx4[3] = fmax3(mx4[3], t[c][i + 3], t[c][i + 7]);
-          }
-        mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl2;
-      }
+      const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl2;
       float m_new = m_run;
       if (mx > m_run + kLazyP || m_run == -INFINITY) m_new = mx;
       const float alpha = (m_new == m_run) ? 1.f : fast_exp2(m_run - m_new);
@@ -834,77 +524,38 @@ prefill_pair_kernel(const __grid_constant__ PairParams p, const __grid_constant_
         }
         tmem_wait_st();
       }
-      if constexpr (F8) {
-        // p = 2^(s + ev - M), written as f16 pairs over the first 64 columns of S
-        float l_new = wide ? l_run : l_run * alpha;
+      // p = 2^(s*scale*log2e - m), written as bf16 pairs over the first 64
+      // columns of S
+      float2 sum2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                        make_float2(0.f, 0.f)};
+      const float2 sl2x2 = make_float2(sl2, sl2), negm = make_float2(-m_new, -m_new);
 #pragma unroll
-        for (int c = 0; c < BN / 32; ++c) {
-          uint32_t pk[16];
+      for (int c = 0; c < BN / 32; ++c) {
+        uint32_t pk[16];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int b = 2 * c + h;
-            const float k = kq(b), n = ts->v[b] - m_new;
-            const float2 k2 = make_float2(k, k), n2 = make_float2(n, n);
-            float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              const float2 x = ffma2(make_float2(t[c][16 * h + i], t[c][16 * h + i + 1]), k2, n2);
-              const float2 pp = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-              sum2[(i >> 1) & 1] = fadd2(sum2[(i >> 1) & 1], pp);
-              const __half2 ph = __floats2half2_rn(pp.x, pp.y);
-              pk[8 * h + i / 2] = *reinterpret_cast<const uint32_t*>(&ph);
-            }
-            const float2 s01 = fadd2(sum2[0], sum2[1]);
-            if (!wide) l_new = fmaf(s01.x + s01.y, ts->l[b], l_new);
-          }
-          tmem_st16(lane_base + col_s + c * 16, pk);
-          if (c & 1) {                        // a half of P is in TMEM
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(PB_PF + 2 * hh + (c >> 1)));
-          }
+        for (int i = 0; i < 32; i += 2) {
+          const float2 x = ffma2(make_float2(t[c][i], t[c][i + 1]), sl2x2, negm);
+          const float2 pp = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+          sum2[(i >> 1) & 3] = fadd2(sum2[(i >> 1) & 3], pp);
+          pk[i / 2] = pack_bf16(pp.x, pp.y);
         }
-        l_run = l_new;
-      } else {
-        // p = 2^(s*scale*log2e - m), written as bf16 pairs over the first 64
-        // columns of S
-        float2 sum2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
-                          make_float2(0.f, 0.f)};
-        const float2 sl2x2 = make_float2(sl2, sl2), negm = make_float2(-m_new, -m_new);
-#pragma unroll
-        for (int c = 0; c < BN / 32; ++c) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float2 x = ffma2(make_float2(t[c][i], t[c][i + 1]), sl2x2, negm);
-            const float2 pp = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-            sum2[(i >> 1) & 3] = fadd2(sum2[(i >> 1) & 3], pp);
-            pk[i / 2] = pack_bf16(pp.x, pp.y);
-          }
-          tmem_st16(lane_base + col_s + c * 16, pk);
-          if (c & 1) {                        // a half of P is in TMEM
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(PB_PF + 2 * hh + (c >> 1)));
-          }
+        tmem_st16(lane_base + col_s + c * 16, pk);
+        if (c & 1) {                        // a half of P is in TMEM
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(PB_PF + 2 * hh + (c >> 1)));
         }
-        const float2 s01 = fadd2(sum2[0], sum2[1]), s23 = fadd2(sum2[2], sum2[3]);
-        const float sum0 = s01.x + s23.x, sum1 = s01.y + s23.y;
-        l_run = l_run * alpha + (sum0 + sum1);
       }
+      const float2 s01 = fadd2(sum2[0], sum2[1]), s23 = fadd2(sum2[2], sum2[3]);
+      const float sum0 = s01.x + s23.x, sum1 = s01.y + s23.y;
+      l_run = l_run * alpha + (sum0 + sum1);
       m_run = m_new;
     }
     wait_or_abort(bar(PB_OD + hh), (it - it_begin) & 1, abort_flag, a.err);
     __syncwarp();
     tc_fence_after();
-    float inv = 1.f / l_run;
-    if constexpr (F8) {
-      const int e = (reinterpret_cast<const TileScales*>(smem + OFF_SCALES))->e;   // E, of any tile
-      inv *= wide ? fast_exp2(m_run - ms_run) : scale_value((uint32_t)(e + 127));
-      if (row_pos >= *nan_key) inv = __int_as_float(0x7fffffff);   // the row sees a NaN value
-    }
+    const float inv = 1.f / l_run;
     const bool row_ok = (q0 + r) < a.chunk_len;
     __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.out) +
                           ((int64_t)(q0 + r) * a.num_q_heads + head) * HD;
@@ -1033,13 +684,8 @@ cudaError_t launch_prefill_pair(const PrefillArgs& a, cudaStream_t stream, int p
   if (p.q_tiles == 0) return cudaSuccess;
   CUtensorMap tm_q;
   if (!encode_rows_map_bf16(&tm_q, a.q, a.chunk_len, a.num_q_heads)) return cudaErrorInvalidValue;
-  const bool f8 = a.k_bscale != nullptr;
-  using C8 = PairCfg<true>;
-  using C16 = PairCfg<false>;
-  cudaError_t e = f8 ? allow_dynamic_smem(prefill_pair_kernel<true>, C8::kSmem)
-                     : allow_dynamic_smem(prefill_pair_kernel<false>, C16::kSmem);
+  cudaError_t e = allow_dynamic_smem(prefill_pair_kernel, SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  if (f8 && persistent_ctas > 0) return cudaErrorInvalidValue;   // the converters run one item
   p.rows_mode = rows_mode_for(a) ? 1 : 0;
   const int n_x = p.rows_mode ? a.num_q_heads : a.num_q_heads / 2;
   const int n_t = p.rows_mode ? (p.q_tiles + 1) / 2 : p.q_tiles;
@@ -1078,14 +724,11 @@ cudaError_t launch_prefill_pair(const PrefillArgs& a, cudaStream_t stream, int p
     }
     p.start[P] = (uint16_t)k;
     p.n_list = n_items;
-    prefill_pair_kernel<false><<<P, C16::kThreads, C16::kSmem, stream>>>(p, tm_q);
+    prefill_pair_kernel<<<P, kThreadsPair, SMEM_BYTES, stream>>>(p, tm_q);
     return cudaGetLastError();
   }
   dim3 grid(n_x, n_t);
-  if (f8)
-    prefill_pair_kernel<true><<<grid, C8::kThreads, C8::kSmem, stream>>>(p, tm_q);
-  else
-    prefill_pair_kernel<false><<<grid, C16::kThreads, C16::kSmem, stream>>>(p, tm_q);
+  prefill_pair_kernel<<<grid, kThreadsPair, SMEM_BYTES, stream>>>(p, tm_q);
   return cudaGetLastError();
 }
 

@@ -19,10 +19,10 @@ __device__ __forceinline__ uint64_t make_sw128_desc(uint32_t addr, uint32_t lbo,
   return d;
 }
 
-// kind::f16 instruction descriptor: fp32 accumulate, A and B both bf16 or both
-// f16 (A K-major), B K-major or MN-major, shape M x N
-__host__ __device__ constexpr uint32_t make_idesc(bool b_mn_major, int m, int n, bool bf16 = true) {
-  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | ((b_mn_major ? 1u : 0u) << 16) |
+// kind::f16 instruction descriptor: fp32 accumulate, bf16 A and B (A K-major),
+// B K-major or MN-major, shape M x N
+__host__ __device__ constexpr uint32_t make_idesc(bool b_mn_major, int m, int n) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn_major ? 1u : 0u) << 16) |
          ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
