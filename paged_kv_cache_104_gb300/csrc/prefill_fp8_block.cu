@@ -34,12 +34,18 @@
 //  * A NaN value code would reach rows that do not see its key (0 * NaN).  In
 //    the tiles with masked entries it is zeroed, its key noted, and the rows
 //    that see the key come out as NaN.
-// Roles (512 threads):
-//   warps 0-3 / 4-7   softmax of stream A / B: thread r owns query row r
-//   warp 8            TMEM allocator and MMA issuer
-//   warp 9            producer: block ids, K boxes, V copies, scales
-//   warps 10-11       none (they complete the issuer's warpgroup)
-//   warps 12-15       V converters
+// Roles (768 threads):
+//   warps 0-3, 4-7    softmax of stream A: thread r of each warpgroup owns 64
+//   warps 8-11, 12-15 columns of query row r; the two exchange their maxima
+//                     through shared memory; of stream B
+//   warp 16           TMEM allocator and MMA issuer
+//   warp 17           producer: block ids, K boxes, V copies, scales
+//   warps 18-19       none (they complete the issuer's warpgroup)
+//   warps 20-23       V converters
+// (One warpgroup a stream, a whole row to a thread, took 171 us: a stream's
+// chain softmax - P V - Q K^T bounds a tile, and a warp's 700 softmax
+// instructions took 2,100-2,400 cycles of its 4,000, a quarter of it waiting
+// for instructions of the long unrolled loop.)
 // Both pools' tiles are three stages deep in their fp8 form (K's ring is read
 // by the MMAs, V's by the converters), so 96 KiB are in flight or in use.
 // Measured on the way (2,048 tokens over 4,096, 32/8 heads): both pools
@@ -74,7 +80,7 @@ constexpr int kHalf16 = kTile8;
 constexpr int kBlk8 = kBlockSize * HD;       // one block and head, 2 KiB
 constexpr int kBlkPerTile = BN / kBlockSize;
 constexpr int NSK = 3, NSV = 2, NST = 3;     // K ring, V (f16) ring, V staging ring
-constexpr int OFF_Q = 0;                     // [stream][bf16 halves, then hi and lo]
+constexpr int OFF_Q = 0;                     // [stream][hi, lo]; the bf16 rows land in the V ring
 constexpr int OFF_K = 2 * kTile16;
 constexpr int OFF_V = OFF_K + NSK * kTile8;
 constexpr int OFF_ST = OFF_V + NSV * kTile16;
@@ -93,20 +99,25 @@ struct TileScales {
 constexpr int kScaleSlots = NSK + 1;
 constexpr int kWideSpread = 40;
 constexpr int OFF_BAR = OFF_SCALES + kScaleSlots * (int)sizeof(TileScales);
-constexpr int OFF_ROWS = OFF_BAR + 256;      // split keys: [stream][row] (reference of l, l)
+// [stream][half][row] floats the halves exchange; split keys: [stream][row]
+// (reference of l, l)
+constexpr int OFF_ROWS = OFF_BAR + 256;
 constexpr int SMEM_BYTES = OFF_ROWS + 2 * BM * 8;
-constexpr int kSoftThreads = 256;
-constexpr int kThreads = 512;
-constexpr int W_MMA = 8, W_PROD = 9, W_CONV = 12;
+constexpr int kSoftThreads = 512;
+constexpr int kThreads = 768;
+constexpr int W_MMA = 16, W_PROD = 17, W_CONV = 20;
+constexpr int kCols = BN / 2;                // a softmax thread's columns
 // registers per thread after the split (setmaxnreg), against the launch budget
-constexpr int kRegsSoft = 200, kRegsRest = 56;
-constexpr int kRegsLaunch = (65536 / kThreads) & ~7;   // 128
+constexpr int kRegsSoft = 96, kRegsRest = 48;
+constexpr int kRegsLaunch = (65536 / kThreads) & ~7;   // 80
 static_assert(kRegsSoft * kSoftThreads + kRegsRest * (kThreads - kSoftThreads) <=
                   kRegsLaunch * kThreads,
               "the register split must fit in what the CTA was launched with");
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t COL_S = 0, COL_O = 2 * BN;
 constexpr float kLazy = 8.0f;
+static_assert(2 * 2 * BM * 4 == 2 * BM * 8, "one area for both uses of the rows' slots");
+static_assert(NSV * kTile16 == 2 * BM * HD * 2, "the bf16 queries fit the V ring");
 static_assert(SMEM_BYTES <= 227 * 1024, "one CTA per SM");
 static_assert(2 * BM * HD * 4 <= OFF_SCALES, "the merge's columns lie in the tiles' place");
 
@@ -120,8 +131,8 @@ enum {
   B_VF = B_STE + NST,     // [NSV]
   B_VE = B_VF + NSV,
   B_SF = B_VE + NSV,      // [stream]
-  B_PF = B_SF + 2,        // [stream][half]
-  B_OD = B_PF + 4,        // [stream]
+  B_PF = B_SF + 2,        // [stream]
+  B_OD = B_PF + 2,        // [stream]
   B_COUNT = B_OD + 2
 };
 static_assert(B_COUNT * 8 + 12 <= 256, "barrier area");
@@ -145,6 +156,20 @@ __device__ __forceinline__ uint32_t drop_nan(uint32_t w, bool* found) {
   if (top == 0) return w;
   *found = true;
   return w & ~((top >> 7) * 0xffu);
+}
+
+// 16 columns of 32 bits of this thread's lane
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 __device__ __forceinline__ uint4 lds16(uint32_t addr) {
@@ -172,6 +197,12 @@ __device__ __forceinline__ void mma8_ss_e(uint32_t d_tmem, uint64_t a_desc, uint
       "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
+}
+// f16 pair to E4M3 codes, to nearest even, saturating
+__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t u) {
+  uint16_t d;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(d) : "r"(u));
+  return d;
 }
 // instruction descriptor, fp32 accumulate, both operands format 0: E4M3 in
 // kind::f8f6f4, f16 in kind::f16
@@ -240,7 +271,7 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
     mbar_init(bar(B_QC), kSoftThreads);
     for (int s = 0; s < NSK; ++s) {
       mbar_init(bar(B_KF + s), 1);
-      mbar_init(bar(B_KE + s), 4);               // one arrival per stream-B softmax warp
+      mbar_init(bar(B_KE + s), 4);               // one arrival per warp of stream B's first half
     }
     for (int s = 0; s < NST; ++s) {
       mbar_init(bar(B_STF + s), 1);
@@ -252,8 +283,7 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(B_SF + i), 1);
-      mbar_init(bar(B_PF + 2 * i), 4);           // one arrival per softmax warp
-      mbar_init(bar(B_PF + 2 * i + 1), 4);
+      mbar_init(bar(B_PF + i), 8);               // one arrival per softmax warp
       mbar_init(bar(B_OD + i), 1);
     }
     *abort_i = 0;
@@ -271,7 +301,7 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp >= 8) {
+  if (warp >= kSoftThreads / 32) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
     if (warp == W_PROD) {
       // ------------------------------------------------------------- producer
@@ -301,18 +331,16 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
       };
       int ids = load_ids(t0 / 4);
       int sc = load_scales(t0 / 4, ids);
-      int ids_next = load_ids(t0 / 4 + 1);
-      int sc_next = load_scales(t0 / 4 + 1, ids_next);
+      int ids_next = 0, sc_next = -1;            // requested behind the first tile
       int e_ref = 0;
       bool go = true;
       int k_sent = 0, v_sent = 0;
       for (int jj = 0; jj < n_tiles; ++jj) {
         const int j = t0 + jj;
-        if (jj > 0 && j % 4 == 0) {
+        const bool turn = jj > 0 && j % 4 == 0;
+        if (turn) {
           ids = ids_next;
           sc = sc_next;
-          ids_next = load_ids(j / 4 + 1);
-          sc_next = load_scales(j / 4 + 1, ids_next);
         }
         const int blk = __shfl_sync(0xffffffffu, ids, (j % 4) * kBlkPerTile + (lane & 7));
         const int both = __shfl_sync(0xffffffffu, sc, (j % 4) * kBlkPerTile + (lane & 7));
@@ -354,6 +382,10 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
           bulk_g2s_hint(sbase + OFF_ST + (jj % NST) * kTile8 + lane * kBlk8, vpool + tile * kBlk8,
                         kBlk8, bar(B_STF + jj % NST), policy_evict_normal());
         ++v_sent;
+        if (jj == 0 || turn) {
+          ids_next = load_ids(j / 4 + 1);
+          sc_next = load_scales(j / 4 + 1, ids_next);
+        }
       }
       if (!go && lane == 0) {                    // let the copies in flight land
         for (int jj = max(0, k_sent - NSK); jj < k_sent; ++jj)
@@ -378,7 +410,9 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
       bool go = true;
       for (int jj = 0; jj < n_tiles; ++jj) {
         const int j = t0 + jj;
-        go = wait_or_abort(bar(B_STF + jj % NST), (jj / NST) & 1, abort_flag, a.err);
+        // the V ring first holds the queries
+        go = jj > 0 || wait_or_abort(bar(B_QC), 0, abort_flag, a.err);
+        if (go) go = wait_or_abort(bar(B_STF + jj % NST), (jj / NST) & 1, abort_flag, a.err);
         if (go && jj >= NSV) go = wait_or_abort(bar(B_VE + jj % NSV), (jj / NSV - 1) & 1, abort_flag, a.err);
         go = __all_sync(0xffffffffu, go && !*abort_flag);
         if (!go) break;                          // leave the loop as a warp
@@ -434,7 +468,7 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_q)) : "memory");
         mbar_arrive_expect_tx(bar(B_Q), 2 * kTile16);
         for (int hh = 0; hh < 2; ++hh) {
-          const uint32_t dst = sbase + OFF_Q + hh * kTile16;
+          const uint32_t dst = sbase + OFF_V + hh * kTile16;
           tma_load_3d(dst, &tm_q, bar(B_Q), 0, hh ? head1 : head0, hh ? qrow1 : qrow0);
           tma_load_3d(dst + kHalf16, &tm_q, bar(B_Q), 64, hh ? head1 : head0, hh ? qrow1 : qrow0);
         }
@@ -454,16 +488,16 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
         }
         commit_e(bar(B_SF + hh));
       };
-      // O_h += P_h V for 64 of the tile's keys, P_h from TMEM (16 keys = 8 columns a step)
-      auto issue_pv = [&](int hh, int jj, int half) {
+      // O_h += P_h V, P_h from TMEM (16 keys = 8 columns a step)
+      auto issue_pv = [&](int hh, int jj) {
         const uint32_t vb = sbase + OFF_V + (jj % NSV) * kTile16;
 #pragma unroll
-        for (int k = half * 4; k < half * 4 + 4; ++k) {
+        for (int k = 0; k < BN / 16; ++k) {
           const uint64_t bd = make_sw128_desc(vb + k * 16 * 128, kHalf16, 1024);
           mma_ts_e(tmem + COL_O + hh * HD, tmem + COL_S + hh * BN + k * 8, bd, idesc_pv,
                    (jj > 0 || k > 0) ? 1u : 0u);
         }
-        if (half == 1 && jj == n_tiles - 1) commit_e(bar(B_OD + hh));
+        if (jj == n_tiles - 1) commit_e(bar(B_OD + hh));
       };
       // The streams alternate: while one's softmax runs, the other's products
       // do.  Q K_{j+1}^T rewrites S_h, which holds P_h, right behind P_h V_j:
@@ -479,16 +513,12 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
         for (int jj = 0; jj < n_tiles && ok; ++jj) {
           const bool more = jj + 1 < n_tiles;
           for (int hh = 0; hh < 2 && ok; ++hh) {
-            ok = __all_sync(0xffffffffu, wait_fast(bar(B_PF + 2 * hh), jj & 1, abort_flag, a.err));
+            ok = __all_sync(0xffffffffu, wait_fast(bar(B_PF + hh), jj & 1, abort_flag, a.err));
             if (!ok) break;
             tc_fence_after();
             if (hh == 0) ok = __all_sync(0xffffffffu, wait_fast(bar(B_VF + jj % NSV), (jj / NSV) & 1, abort_flag, a.err));
             if (!ok) break;
-            issue_pv(hh, jj, 0);
-            ok = __all_sync(0xffffffffu, wait_fast(bar(B_PF + 2 * hh + 1), jj & 1, abort_flag, a.err));
-            if (!ok) break;
-            tc_fence_after();
-            issue_pv(hh, jj, 1);
+            issue_pv(hh, jj);
             if (hh == 1) commit_e(bar(B_VE + jj % NSV));   // V no longer needed
             if (more) {
               if (hh == 0) ok = wait_k(jj + 1);
@@ -507,24 +537,30 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
-    // ------------------------------------------------------------- softmax (stream hh)
-    const int hh = warp >> 2;               // 0: warps 0-3, 1: warps 4-7
+    // -------------------------------------- softmax (stream hh, column half ch)
+    const int hh = warp >> 3, ch = (warp >> 2) & 1;
     const int r = tid & 127;                // query row in the tile, TMEM lane
+    const int pair = 1 + hh * 4 + (warp & 3);   // named barrier of the two warps of these rows
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t col_s = COL_S + hh * BN, col_o = COL_O + hh * HD;
+    const uint32_t col_s = COL_S + hh * BN, col_o = COL_O + hh * HD + ch * kCols;
     const int q0 = hh ? qrow1 : qrow0, head = hh ? head1 : head0;
     const int row_pos = a.prior_len + q0 + r;
+    volatile float* mine = reinterpret_cast<volatile float*>(smem + OFF_ROWS) + (2 * hh + ch) * BM + r;
+    volatile float* others = mine + (ch ? -BM : BM);
     float q_up = 1.f;                       // what brings products back to the query's size
     if (n_tiles > 0 && wait_or_abort(bar(B_Q), 0, abort_flag, a.err)) {
-      // this row's query, bf16 in two halves, becomes its hi and lo rows
-      const uint32_t qrow = sbase + OFF_Q + hh * kTile16 + r * 128;
-      uint4 x[16];
+      // this row's query becomes its hi and lo rows, half of each here
+      const uint32_t src = sbase + OFF_V + hh * kTile16 + r * 128;
+      const uint32_t dst = sbase + OFF_Q + hh * kTile16 + r * 128;
+      auto piece = [&](int i) {             // elements 8 i .. 8 i + 7
+        return lds16(src + (i >> 3) * kHalf16 + (((i & 7) ^ (r & 7)) << 4));
+      };
       uint32_t top = 0;
-#pragma unroll
+#pragma unroll 8
       for (int i = 0; i < 16; ++i) {
-        x[i] = lds16(qrow + (i >> 3) * kHalf16 + (((i & 7) ^ (r & 7)) << 4));
-        top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
-                                     __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
+        const uint4 x = piece(i);
+        top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                     __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
       }
       // 2^(7 - exponent of the row's largest element), of zeros and of
       // infinities or NaN 1
@@ -534,34 +570,36 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
       q_up = __uint_as_float((uint32_t)(127 + ex - 7) << 23);
       // an infinite or NaN element makes the row's scores NaN
       const uint32_t bad = top == 255 ? 0x7f7f7f7fu : 0u;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {         // 16 elements: one chunk of hi and one of lo
-        const uint32_t w[8] = {x[2 * i].x, x[2 * i].y, x[2 * i].z, x[2 * i].w,
-                               x[2 * i + 1].x, x[2 * i + 1].y, x[2 * i + 1].z, x[2 * i + 1].w};
+#pragma unroll 2
+      for (int i = 4 * ch; i < 4 * ch + 4; ++i) {   // 16 elements: a chunk of hi and one of lo
+        const uint4 x = piece(2 * i), y = piece(2 * i + 1);
+        const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          uint32_t h4 = 0, l4 = 0;
+          uint32_t h2[2], l2[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float u0 = bf16lo(w[2 * k + e]) * down, u1 = bf16hi(w[2 * k + e]) * down;
-            const uint16_t h = f32x2_to_e4m3x2(u0, u1);
-            const uint32_t back = e4m3x2_to_f16x2(h);
-            const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&back));
-            h4 |= (uint32_t)h << (16 * e);
-            l4 |= (uint32_t)f32x2_to_e4m3x2(u0 - hf.x, u1 - hf.y) << (16 * e);
+            // f16 holds the scaled element exactly, or to 2^-25
+            const __half2 u = __floats2half2_rn(bf16lo(w[2 * k + e]) * down,
+                                                bf16hi(w[2 * k + e]) * down);
+            h2[e] = f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&u));
+            const uint32_t back = e4m3x2_to_f16x2((uint16_t)h2[e]);
+            const __half2 d = __hsub2(u, *reinterpret_cast<const __half2*>(&back));
+            l2[e] = f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&d));
           }
-          hi[k] = h4 | bad;
-          lo[k] = l4;
+          hi[k] = (h2[0] | h2[1] << 16) | bad;
+          lo[k] = l2[0] | l2[1] << 16;
         }
-        const uint32_t at = qrow + ((i ^ (r & 7)) << 4);
+        const uint32_t at = dst + ((i ^ (r & 7)) << 4);
         sts16(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
         sts16(at + kTile8, make_uint4(lo[0], lo[1], lo[2], lo[3]));
       }
       fence_proxy_async_smem();
       mbar_arrive(bar(B_QC));
     }
-    float m_run = -INFINITY, l_run = 0.f;   // M, in log2 units, and l
+    // M of the whole row in log2 units, l of this half's columns
+    float m_run = -INFINITY, l_run = 0.f;
     bool wide = false;                      // once true, l is summed against
     float ms_run = -INFINITY;               // a running maximum of its own
     for (int jj = 0; jj < n_tiles; ++jj) {
@@ -569,31 +607,34 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
       __syncwarp();
       tc_fence_after();
       // the S_B commit follows both streams' Q K^T: this K stage can be refilled
-      if (hh == 1 && lane == 0) mbar_arrive(bar(B_KE + jj % NSK));
-      const int k0 = (t0 + jj) * BN;
-      const bool diag = k0 + BN - 1 > a.prior_len + q0;   // causal mask needed
-      // the whole S row into registers: four loads in flight, one wait
-      float t[BN / 32][32];
-#pragma unroll
-      for (int c = 0; c < BN / 32; ++c) tmem_ld32(lane_base + col_s + c * 32, t[c]);
+      if (hh == 1 && ch == 0 && lane == 0) mbar_arrive(bar(B_KE + jj % NSK));
+      const int k0 = (t0 + jj) * BN + ch * kCols;
+      // this half of the S row into registers: two loads in flight, one wait
+      float t[2][32];
+      tmem_ld32(lane_base + col_s + ch * kCols, t[0]);
+      tmem_ld32(lane_base + col_s + ch * kCols + 32, t[1]);
       tmem_wait_ld();
+      reg_fence(t[0]);
+      reg_fence(t[1]);
+      if (k0 + kCols - 1 > a.prior_len + q0) {            // causal mask needed
 #pragma unroll
-      for (int c = 0; c < BN / 32; ++c) reg_fence(t[c]);
-      if (diag) {
-#pragma unroll
-        for (int c = 0; c < BN / 32; ++c)
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
           for (int i = 0; i < 32; ++i)
             if (k0 + c * 32 + i > row_pos) t[c][i] = -INFINITY;
       }
       const TileScales* ts =
           reinterpret_cast<const TileScales*>(smem + OFF_SCALES) + jj % kScaleSlots;
-      // block b's factor from products to scores; never 0, so that a masked
+      // blocks' factors from products to scores; never 0, so that a masked
       // score stays -inf
-      auto kq = [&](int b) { return fmaxf(ts->k[b] * q_up, 1e-38f); };
-      float mx = -INFINITY, ms = -INFINITY;
+      const float4 k4 = *reinterpret_cast<const float4*>(ts->k + 4 * ch);
+      const float4 v4 = *reinterpret_cast<const float4*>(ts->v + 4 * ch);
+      const float kq[4] = {fmaxf(k4.x * q_up, 1e-38f), fmaxf(k4.y * q_up, 1e-38f),
+                           fmaxf(k4.z * q_up, 1e-38f), fmaxf(k4.w * q_up, 1e-38f)};
+      const float ev[4] = {v4.x, v4.y, v4.z, v4.w};
+      float mx = -INFINITY;
 #pragma unroll
-      for (int b = 0; b < kBlkPerTile; ++b) {
+      for (int b = 0; b < 4; ++b) {
         const float* x = &t[b / 2][(b & 1) * 16];
         float m0 = fmax3(x[0], x[1], x[2]), m1 = fmax3(x[3], x[4], x[5]);
         m0 = fmax3(m0, x[6], x[7]);
@@ -601,59 +642,72 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
         m0 = fmax3(m0, x[10], x[11]);
         m1 = fmax3(m1, x[12], x[13]);
         m0 = fmax3(m0, x[14], x[15]);
-        const float s0 = fmaxf(m0, m1) * kq(b);
-        ms = fmaxf(ms, s0);
-        mx = fmaxf(mx, s0 + ts->v[b]);
+        mx = fmaxf(mx, fmaf(fmaxf(m0, m1), kq[b], ev[b]));
       }
       if (ts->wide || wide) {
-        // from here on l = sum 2^(s - ms); before, it was sum 2^(s + E - M)
+        // from here on l = sum 2^(s - ms); before, it was sum 2^(s + E - M).
+        // Rare, so it reads S again block by block and keeps the code short.
         if (!wide && jj > 0) ms_run = m_run - (float)ts->e;
         wide = true;
-        const float m2 = fmaxf(ms_run, ms);
-        l_run *= ms_run == m2 ? 1.f : fast_exp2(ms_run - m2);
-        ms_run = m2;
-        float sum = 0.f;
-        const float m0 = m2 == -INFINITY ? 0.f : m2;   // no key yet: every weight is 0
+#pragma unroll 1
+        for (int b = 0; b < 4; ++b) {
+          float x[16];
+          tmem_ld16(lane_base + col_s + ch * kCols + b * 16, x);
+          tmem_wait_ld();
+          reg_fence(x);
+          const float k = fmaxf(ts->k[4 * ch + b] * q_up, 1e-38f);
+          float m2 = ms_run;
 #pragma unroll
-        for (int b = 0; b < kBlkPerTile; ++b) {
-          const float k = kq(b);
+          for (int i = 0; i < 16; ++i) {
+            x[i] = k0 + b * 16 + i > row_pos ? -INFINITY : x[i] * k;
+            m2 = fmaxf(m2, x[i]);
+          }
+          const float m0 = m2 == -INFINITY ? 0.f : m2;   // no key yet: every weight is 0
+          l_run *= ms_run == m2 ? 1.f : fast_exp2(ms_run - m2);
+          ms_run = m2;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) sum += fast_exp2(fmaf(t[b / 2][(b & 1) * 16 + i], k, -m0));
+          for (int i = 0; i < 16; ++i) l_run += fast_exp2(x[i] - m0);
         }
-        l_run += sum;
       }
+      // The row's maximum from both halves.  The barrier also orders the P
+      // stores below, which lie over S columns of the other half, behind that
+      // half's loads.  (The slots are free again before the next tile: its S
+      // follows P V of this one, which waits for both halves' P.)
+      *mine = mx;
+      named_bar_sync(pair, 64);
+      mx = fmaxf(mx, *others);
       float m_new = m_run;
       if (mx > m_run + kLazy || m_run == -INFINITY) m_new = mx;
       const float alpha = (m_new == m_run) ? 1.f : fast_exp2(m_run - m_new);
       if (jj >= 1 && __any_sync(0xffffffffu, alpha != 1.f)) {
         // O holds P V of the tiles before; the S_h commit of this tile was
         // issued behind their last product, so that product is complete and
-        // O can be rescaled in place
+        // O can be rescaled in place, this half's columns here
         __syncwarp();
 #pragma unroll 1
-        for (int c = 0; c < HD / 32; ++c) {
-          float o[32];
-          tmem_ld32(lane_base + col_o + c * 32, o);
+        for (int c = 0; c < kCols / 16; ++c) {
+          float o[16];
+          tmem_ld16(lane_base + col_o + c * 16, o);
           tmem_wait_ld();
           reg_fence(o);
+          uint32_t u[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] *= alpha;
-          tmem_st32(lane_base + col_o + c * 32, o);
+          for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(o[i] * alpha);
+          tmem_st16(lane_base + col_o + c * 16, u);
         }
-        tmem_wait_st();
       }
       // p = 2^(s + ev - M), written as f16 pairs over the first 64 columns of
       // S; a row that has seen no key (its keys are in another CTA) has p = 0
       const float m_ref = m_new == -INFINITY ? 0.f : m_new;
       float l_new = wide ? l_run : l_run * alpha;
 #pragma unroll
-      for (int c = 0; c < BN / 32; ++c) {
+      for (int c = 0; c < 2; ++c) {
         uint32_t pk[16];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int b = 2 * c + h;
-          const float k = kq(b), n = ts->v[b] - m_ref;
-          const float2 k2 = make_float2(k, k), n2 = make_float2(n, n);
+          const float n = ev[b] - m_ref;
+          const float2 k2 = make_float2(kq[b], kq[b]), n2 = make_float2(n, n);
           float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
@@ -664,16 +718,14 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
             pk[8 * h + i / 2] = *reinterpret_cast<const uint32_t*>(&ph);
           }
           const float2 s01 = fadd2(sum2[0], sum2[1]);
-          if (!wide) l_new = fmaf(s01.x + s01.y, ts->l[b], l_new);
+          if (!wide) l_new = fmaf(s01.x + s01.y, ts->l[4 * ch + b], l_new);
         }
-        tmem_st16(lane_base + col_s + c * 16, pk);
-        if (c & 1) {                        // a half of P is in TMEM
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(B_PF + 2 * hh + (c >> 1)));
-        }
+        tmem_st16(lane_base + col_s + (2 * ch + c) * 16, pk);
       }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_PF + hh));
       l_run = l_new;
       m_run = m_new;
     }
@@ -681,88 +733,125 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
       wait_or_abort(bar(B_OD + hh), 0, abort_flag, a.err);
       __syncwarp();
       tc_fence_after();
-      if (row_pos >= *nan_key) l_run = __int_as_float(0x7fffffff);   // the row sees a NaN value
     }
+    // l stands for l 2^ref, O for O 2^M = O 2^(M - ref): the halves' sums
+    // against their larger reference (the same unless wide)
+    const int e = n_tiles > 0 ? (reinterpret_cast<const TileScales*>(smem + OFF_SCALES))->e : 0;
+    float ref = wide ? ms_run : m_run - (float)e;
+    {
+      *mine = ref;
+      named_bar_sync(pair, 64);
+      const float ref2 = *others;
+      named_bar_sync(pair, 64);
+      *mine = l_run;
+      named_bar_sync(pair, 64);
+      const float l2 = *others;
+      named_bar_sync(pair, 64);             // the rows' slots may be reused
+      if (ref != ref2) {
+        const float m = fmaxf(ref, ref2);
+        l_run = l_run * fast_exp2(ref - m) + l2 * fast_exp2(ref2 - m);
+        ref = m;
+      } else {
+        l_run += l2;
+      }
+    }
+    // The results take 1 / l and then the unit, which may leave the normal
+    // range when V's scales do.
+    const float unit = wide ? fast_exp2(m_run - ref) : scale_value((uint32_t)(e + 127));
+    if (n_tiles > 0 && row_pos >= *nan_key)
+      l_run = __int_as_float(0x7fffffff);   // the row sees a NaN value
     const bool row_ok = (q0 + r) < a.chunk_len;
     __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.out) +
                           ((int64_t)(q0 + r) * a.num_q_heads + head) * HD;
-    const int e = n_tiles > 0 ? (reinterpret_cast<const TileScales*>(smem + OFF_SCALES))->e : 0;
-    // l stands for l 2^ref, O for O 2^M = O 2^ref unit.  The results take 1 / l
-    // and then the unit, which may leave the normal range when V's scales do.
-    const float ref = wide ? ms_run : m_run - (float)e;
-    const float unit = wide ? fast_exp2(m_run - ms_run) : scale_value((uint32_t)(e + 127));
     if (p.splits == 1) {
       const float inv = 1.f / l_run;
 #pragma unroll 1
-      for (int c = 0; c < HD / 32; ++c) {
-        float o[32];
-        tmem_ld32(lane_base + col_o + c * 32, o);
+      for (int c = 0; c < kCols; c += 16) {
+        float o[16];
+        tmem_ld16(lane_base + col_o + c, o);
         tmem_wait_ld();
         reg_fence(o);
         if (row_ok) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = o[i] * inv * unit;
+          for (int i = 0; i < 16; ++i) o[i] = o[i] * inv * unit;
 #pragma unroll
-          for (int i = 0; i < 32; i += 8)
-            *reinterpret_cast<uint4*>(orow + c * 32 + i) =
+          for (int i = 0; i < 16; i += 8)
+            *reinterpret_cast<uint4*>(orow + ch * kCols + c + i) =
                 make_uint4(pack_bf16(o[i], o[i + 1]), pack_bf16(o[i + 2], o[i + 3]),
                            pack_bf16(o[i + 4], o[i + 5]), pack_bf16(o[i + 6], o[i + 7]));
         }
       }
     } else {
       const uint32_t row_at = sbase + OFF_ROWS + (hh * BM + r) * 8;
-      asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(row_at), "f"(ref), "f"(l_run) : "memory");
+      named_bar_sync(9, kSoftThreads);      // the stats lie over other rows' slots
+      if (ch == 0)
+        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(row_at), "f"(ref), "f"(l_run) : "memory");
       cluster_sync();                       // every CTA's stats are there, its tiles are done with
-      float top = -INFINITY, sum = 0.f;
-      for (int k = 0; k < p.splits; ++k) top = fmaxf(top, ld_peer2(peer(row_at, k)).x);
-      for (int k = 0; k < p.splits; ++k) {
-        const float2 x = ld_peer2(peer(row_at, k));
-        sum = fmaf(fast_exp2(x.x - top), x.y, sum);
-      }
-      const float f = n_tiles > 0 ? fast_exp2(ref - top) / sum : 0.f;
-      // CTA k adds up columns k W .. k W + W - 1: four columns of 128 rows are
-      // 2 KiB in a piece, rows side by side
-      const int W = HD / p.splits;
-#pragma unroll 1
-      for (int c = 0; c < HD / 32; ++c) {
-        float o[32];
-        if (n_tiles > 0) {
-          tmem_ld32(lane_base + col_o + c * 32, o);
-          tmem_wait_ld();
-          reg_fence(o);
-        } else {
+      // CTA k adds up columns k W .. k W + W - 1 (W = 2^w): four columns of
+      // 128 rows are 2 KiB in a piece, rows side by side
+      const int w = 31 - __clz(HD / p.splits);
+      if (row_ok) {
+        float2 stat[8];
+        float top = -INFINITY, sum = 0.f;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = 0.f;
+        for (int k = 0; k < 8; ++k) {
+          stat[k] = k < p.splits ? ld_peer2(peer(row_at, k)) : make_float2(-INFINITY, 0.f);
+          top = fmaxf(top, stat[k].x);
         }
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          const int col = c * 32 + i, owner = col / W;
-          const int piece = (rank * 2 + hh) * (W / 4) + (col - owner * W) / 4;
-          st_peer(peer(sbase + piece * (BM * 16) + r * 16, owner), o[i] * f * unit,
-                  o[i + 1] * f * unit, o[i + 2] * f * unit, o[i + 3] * f * unit);
+        for (int k = 0; k < 8; ++k)
+          if (k < p.splits) sum = fmaf(fast_exp2(stat[k].x - top), stat[k].y, sum);
+        // rows that no CTA gave a weight to (their scores are all -inf) are NaN
+        const float f = n_tiles > 0 ? fast_exp2(ref - top) / sum : 0.f;
+        l_run = f;
+      }
+#pragma unroll 1
+      for (int c = 0; c < kCols; c += 16) {
+        float o[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] = 0.f;
+        if (n_tiles > 0) {
+          tmem_ld16(lane_base + col_o + c, o);
+          tmem_wait_ld();
+          reg_fence(o);
+        }
+        // W is at least 16: the 16 columns have one owner
+        const int col = ch * kCols + c, owner = col >> w;
+        const int piece = ((rank * 2 + hh) << (w - 2)) + ((col & ((1 << w) - 1)) >> 2);
+        const uint32_t at = peer(sbase + piece * (BM * 16) + r * 16, owner);
+        if (row_ok) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = o[i] * l_run * unit;
+#pragma unroll
+          for (int i = 0; i < 16; i += 4)
+            st_peer(at + i / 4 * (BM * 16), o[i], o[i + 1], o[i + 2], o[i + 3]);
         }
       }
       cluster_sync();
-      for (int c4 = 0; c4 < W / 4; c4 += 2) {
-        float o[8];
+      // this CTA's columns, half of them here
+      const int own = 1 << (w - 3);         // pieces of four columns a half
+      if (row_ok) {
+        for (int c4 = ch * own; c4 < ch * own + own; c4 += 2) {
+          float o[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = 0.f;
-        for (int k = 0; k < p.splits; ++k) {
-          const uint32_t at = sbase + ((k * 2 + hh) * (W / 4) + c4) * (BM * 16) + r * 16;
-          const uint4 x = lds16(at), y = lds16(at + BM * 16);
-          o[0] += __uint_as_float(x.x);
-          o[1] += __uint_as_float(x.y);
-          o[2] += __uint_as_float(x.z);
-          o[3] += __uint_as_float(x.w);
-          o[4] += __uint_as_float(y.x);
-          o[5] += __uint_as_float(y.y);
-          o[6] += __uint_as_float(y.z);
-          o[7] += __uint_as_float(y.w);
-        }
-        if (row_ok)
-          *reinterpret_cast<uint4*>(orow + rank * W + c4 * 4) =
+          for (int i = 0; i < 8; ++i) o[i] = 0.f;
+#pragma unroll 4
+          for (int k = 0; k < p.splits; ++k) {
+            const uint32_t at = sbase + (((k * 2 + hh) << (w - 2)) + c4) * (BM * 16) + r * 16;
+            const uint4 x = lds16(at), y = lds16(at + BM * 16);
+            o[0] += __uint_as_float(x.x);
+            o[1] += __uint_as_float(x.y);
+            o[2] += __uint_as_float(x.z);
+            o[3] += __uint_as_float(x.w);
+            o[4] += __uint_as_float(y.x);
+            o[5] += __uint_as_float(y.y);
+            o[6] += __uint_as_float(y.z);
+            o[7] += __uint_as_float(y.w);
+          }
+          *reinterpret_cast<uint4*>(orow + (rank << w) + c4 * 4) =
               make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]),
                          pack_bf16(o[6], o[7]));
+        }
       }
     }
   }
