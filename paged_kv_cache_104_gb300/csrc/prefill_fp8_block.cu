@@ -34,18 +34,12 @@
 //  * A NaN value code would reach rows that do not see its key (0 * NaN).  In
 //    the tiles with masked entries it is zeroed, its key noted, and the rows
 //    that see the key come out as NaN.
-// Roles (768 threads):
-//   warps 0-3, 4-7    softmax of stream A: thread r of each warpgroup owns 64
-//   warps 8-11, 12-15 columns of query row r; the two exchange their maxima
-//                     through shared memory; of stream B
-//   warp 16           TMEM allocator and MMA issuer
-//   warp 17           producer: block ids, K boxes, V copies, scales
-//   warps 18-19       none (they complete the issuer's warpgroup)
-//   warps 20-23       V converters
-// (One warpgroup a stream, a whole row to a thread, took 171 us: a stream's
-// chain softmax - P V - Q K^T bounds a tile, and a warp's 700 softmax
-// instructions took 2,100-2,400 cycles of its 4,000, a quarter of it waiting
-// for instructions of the long unrolled loop.)
+// Roles (512 threads):
+//   warps 0-3 / 4-7   softmax of stream A / B: thread r owns query row r
+//   warp 8            TMEM allocator and MMA issuer
+//   warp 9 / 10       producers: K's boxes and the scales / V's copies
+//   warp 11           none (it completes the issuer's warpgroup)
+//   warps 12-15       V converters
 // Both pools' tiles are three stages deep in their fp8 form (K's ring is read
 // by the MMAs, V's by the converters), so 96 KiB are in flight or in use.
 // Measured on the way (2,048 tokens over 4,096, 32/8 heads): both pools
@@ -94,21 +88,21 @@ struct TileScales {
   int e;                   // E
   int pad[6];
 };
-// deeper than the K ring: a K stage is free again when its products are done,
-// its scales when its softmax is
-constexpr int kScaleSlots = NSK + 1;
+// Deeper than the K ring: a K stage is free again when its products are done,
+// but the softmax reads l after it has handed over P, so tile j's scales are
+// done with when both streams have handed over P of tile j + 1, which S of tile
+// j + 2, and so K's stage of that tile becoming free, follows.
+constexpr int kScaleSlots = NSK + 2;
 constexpr int kWideSpread = 40;
 constexpr int OFF_BAR = OFF_SCALES + kScaleSlots * (int)sizeof(TileScales);
-// [stream][half][row] floats the halves exchange; split keys: [stream][row]
-// (reference of l, l)
+// split keys: [stream][row] (reference of l, l)
 constexpr int OFF_ROWS = OFF_BAR + 256;
 constexpr int SMEM_BYTES = OFF_ROWS + 2 * BM * 8;
-constexpr int kSoftThreads = 512;
-constexpr int kThreads = 768;
-constexpr int W_MMA = 16, W_PROD = 17, W_CONV = 20;
-constexpr int kCols = BN / 2;                // a softmax thread's columns
+constexpr int kSoftThreads = 256;
+constexpr int kThreads = 512;
+constexpr int W_MMA = 8, W_KPROD = 9, W_VPROD = 10, W_CONV = 12;
 // registers per thread after the split (setmaxnreg), against the launch budget
-constexpr int kRegsSoft = 96, kRegsRest = 48;
+constexpr int kRegsSoft = 200, kRegsRest = 56;
 constexpr int kRegsLaunch = (65536 / kThreads) & ~7;   // 80
 static_assert(kRegsSoft * kSoftThreads + kRegsRest * (kThreads - kSoftThreads) <=
                   kRegsLaunch * kThreads,
@@ -116,7 +110,7 @@ static_assert(kRegsSoft * kSoftThreads + kRegsRest * (kThreads - kSoftThreads) <
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t COL_S = 0, COL_O = 2 * BN;
 constexpr float kLazy = 8.0f;
-static_assert(2 * 2 * BM * 4 == 2 * BM * 8, "one area for both uses of the rows' slots");
+
 static_assert(NSV * kTile16 == 2 * BM * HD * 2, "the bf16 queries fit the V ring");
 static_assert(SMEM_BYTES <= 227 * 1024, "one CTA per SM");
 static_assert(2 * BM * HD * 4 <= OFF_SCALES, "the merge's columns lie in the tiles' place");
@@ -131,11 +125,25 @@ enum {
   B_VF = B_STE + NST,     // [NSV]
   B_VE = B_VF + NSV,
   B_SF = B_VE + NSV,      // [stream]
-  B_PF = B_SF + 2,        // [stream]
-  B_OD = B_PF + 2,        // [stream]
+  B_PF = B_SF + 2,        // [stream][half]
+  B_OD = B_PF + 4,        // [stream]
   B_COUNT = B_OD + 2
 };
 static_assert(B_COUNT * 8 + 12 <= 256, "barrier area");
+
+// Position in a ring of N stages: the slot, and the parity of its current use
+// (a division by 3 in every tile costs the issuer more than the products do)
+template <int N>
+struct Ring {
+  int slot = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) {
+      slot = 0;
+      parity ^= 1;
+    }
+  }
+};
 
 struct Params {
   PrefillArgs a;
@@ -156,6 +164,24 @@ __device__ __forceinline__ uint32_t drop_nan(uint32_t w, bool* found) {
   if (top == 0) return w;
   *found = true;
   return w & ~((top >> 7) * 0xffu);
+}
+
+// A wait for the roles that run ahead (producer, converters): it sleeps
+// between polls and leaves the issue slots to the softmax.  Bounded and
+// abort-aware as the others.
+__device__ __forceinline__ bool wait_idle(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                          int* err) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  for (unsigned int it = 0; it < kWaitLimitIters; ++it) {
+    if (*abort_flag) return false;
+    __nanosleep(100);
+    if (mbar_try_wait(bar, parity)) return true;
+    if (clock64() - t0 > kWaitLimitCycles) break;
+  }
+  record_error(err, DEVERR_TIMEOUT);
+  *abort_flag = 1;
+  return false;
 }
 
 // 16 columns of 32 bits of this thread's lane
@@ -266,12 +292,12 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
   const int t0 = (int)((int64_t)all_tiles * rank / p.splits);
   const int n_tiles = (int)((int64_t)all_tiles * (rank + 1) / p.splits) - t0;
 
-  if (tid == 0) {
+  if (warp == W_KPROD && lane == 0) {
     mbar_init(bar(B_Q), 1);
     mbar_init(bar(B_QC), kSoftThreads);
     for (int s = 0; s < NSK; ++s) {
       mbar_init(bar(B_KF + s), 1);
-      mbar_init(bar(B_KE + s), 4);               // one arrival per warp of stream B's first half
+      mbar_init(bar(B_KE + s), 4);               // one arrival per stream-B softmax warp
     }
     for (int s = 0; s < NST; ++s) {
       mbar_init(bar(B_STF + s), 1);
@@ -283,12 +309,23 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(B_SF + i), 1);
-      mbar_init(bar(B_PF + i), 8);               // one arrival per softmax warp
+      mbar_init(bar(B_PF + 2 * i), 4);           // one arrival per softmax warp
+      mbar_init(bar(B_PF + 2 * i + 1), 4);
       mbar_init(bar(B_OD + i), 1);
     }
     *abort_i = 0;
     *nan_key = INT_MAX;
     fence_mbar_init();
+    // the queries at once: what comes first needs nothing else
+    if (n_tiles > 0) {
+      mbar_arrive_expect_tx(bar(B_Q), 2 * kTile16);
+      for (int hh = 0; hh < 2; ++hh) {
+        const uint32_t dst = sbase + OFF_V + hh * kTile16;
+        tma_load_3d(dst, &tm_q, bar(B_Q), 0, hh ? head1 : head0, hh ? qrow1 : qrow0);
+        tma_load_3d(dst + kHalf16, &tm_q, bar(B_Q), 64, hh ? head1 : head0, hh ? qrow1 : qrow0);
+      }
+    }
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
   }
   if (warp == W_MMA) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -303,15 +340,13 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
 
   if (warp >= kSoftThreads / 32) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-    if (warp == W_PROD) {
-      // ------------------------------------------------------------- producer
-      if (lane == 0 && n_tiles > 0) {
-        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
-      }
+    if (warp == W_KPROD || warp == W_VPROD) {
+      // ------------------------------------------------------------- producers
+      const bool is_v = warp == W_VPROD;
       const uint8_t* vpool = static_cast<const uint8_t*>(a.v_cache);
       const int nblk_seq = (p.total_len + kBlockSize - 1) / kBlockSize;
-      // a window of 32 blocks (4 tiles), one per lane: ids, and the scale
-      // bytes, K's in bits 0-7 and V's in 8-15 (-1 behind the sequence's end)
+      // a window of 32 blocks (4 tiles), one per lane: ids, and with K the
+      // scale bytes, K's in bits 0-7 and V's in 8-15 (-1 behind the end)
       auto load_ids = [&](int win) {
         const int idx = win * 32 + lane;
         int blk = 0;
@@ -325,17 +360,20 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
         return blk;
       };
       auto load_scales = [&](int win, int blk) {
-        if (win * 32 + lane >= nblk_seq) return -1;
+        if (is_v || win * 32 + lane >= nblk_seq) return -1;
         const int64_t i = (int64_t)blk * a.num_kv_heads + g;
         return (int)__ldg(a.k_bscale + i) | (int)__ldg(a.v_bscale + i) << 8;
       };
-      int ids = load_ids(t0 / 4);
+      int ids = n_tiles > 0 ? load_ids(t0 / 4) : 0;
       int sc = load_scales(t0 / 4, ids);
       int ids_next = 0, sc_next = -1;            // requested behind the first tile
-      int e_ref = 0;
+      int e_ref = 0, sent = 0;
       bool go = true;
-      int k_sent = 0, v_sent = 0;
-      for (int jj = 0; jj < n_tiles; ++jj) {
+      static_assert(NSK == NST, "both producers' rings turn alike");
+      Ring<NSK> ring;
+      Ring<kScaleSlots> sr;
+      const int full0 = is_v ? B_STF : B_KF, empty0 = is_v ? B_STE : B_KE;
+      for (int jj = 0; jj < n_tiles; ++jj, ring.next(), sr.next()) {
         const int j = t0 + jj;
         const bool turn = jj > 0 && j % 4 == 0;
         if (turn) {
@@ -343,55 +381,52 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
           sc = sc_next;
         }
         const int blk = __shfl_sync(0xffffffffu, ids, (j % 4) * kBlkPerTile + (lane & 7));
-        const int both = __shfl_sync(0xffffffffu, sc, (j % 4) * kBlkPerTile + (lane & 7));
         const int nb = min(kBlkPerTile, nblk_seq - j * kBlkPerTile);
         const int64_t tile = (int64_t)blk * a.num_kv_heads + g;
-        // K, and the tile's scales, which its stage's barrier publishes
-        if (jj >= NSK) go = wait_or_abort(bar(B_KE + jj % NSK), (jj / NSK - 1) & 1, abort_flag, a.err);
+        if (jj >= NSK) go = wait_idle(bar(empty0 + ring.slot), ring.parity ^ 1, abort_flag, a.err);
         go = __all_sync(0xffffffffu, go && !*abort_flag);
         if (!go) break;                          // leave the loop as a warp
-        int ev = both < 0 ? INT_MIN : (both >> 8) - 127;
-        if (jj == 0) e_ref = __reduce_max_sync(0xffffffffu, ev);
-        if (both < 0) ev = e_ref;                // no key of this block counts
-        const int off = e_ref - ev;
-        const bool wide = __any_sync(0xffffffffu, abs(off) > kWideSpread);
-        TileScales* ts = reinterpret_cast<TileScales*>(smem + OFF_SCALES) + jj % kScaleSlots;
-        if (lane < kBlkPerTile) {
-          ts->k[lane] = a.scale * 1.4426950408889634f * scale_value(both < 0 ? 127u : both & 0xffu);
-          ts->v[lane] = (float)ev;
-          ts->l[lane] = __uint_as_float((uint32_t)(127 + max(-100, min(100, off))) << 23);
-          if (lane == 0) {
-            ts->wide = wide;
-            ts->e = e_ref;
+        const uint32_t full = bar(full0 + ring.slot);
+        if (is_v) {
+          if (lane == 0) mbar_arrive_expect_tx(full, nb * kBlk8);
+          __syncwarp();
+          if (lane < nb)
+            bulk_g2s_hint(sbase + OFF_ST + ring.slot * kTile8 + lane * kBlk8, vpool + tile * kBlk8,
+                          kBlk8, full, policy_evict_normal());
+        } else {
+          // the tile's scales, which its stage's barrier publishes
+          const int both = __shfl_sync(0xffffffffu, sc, (j % 4) * kBlkPerTile + (lane & 7));
+          int ev = both < 0 ? INT_MIN : (both >> 8) - 127;
+          if (jj == 0) e_ref = __reduce_max_sync(0xffffffffu, ev);
+          if (both < 0) ev = e_ref;              // no key of this block counts
+          const int off = e_ref - ev;
+          const bool wide = __any_sync(0xffffffffu, abs(off) > kWideSpread);
+          TileScales* ts = reinterpret_cast<TileScales*>(smem + OFF_SCALES) + sr.slot;
+          if (lane < kBlkPerTile) {
+            ts->k[lane] = a.scale * 1.4426950408889634f * scale_value(both < 0 ? 127u : both & 0xffu);
+            ts->v[lane] = (float)ev;
+            ts->l[lane] = __uint_as_float((uint32_t)(127 + max(-100, min(100, off))) << 23);
+            if (lane == 0) {
+              ts->wide = wide;
+              ts->e = e_ref;
+            }
           }
+          __syncwarp();
+          if (lane == 0) mbar_arrive_expect_tx(full, nb * kBlk8);
+          __syncwarp();
+          if (lane < nb)
+            tma_box8(sbase + OFF_K + ring.slot * kTile8 + lane * kBlk8, &tm_k, full,
+                     (int)(tile * kBlockSize));
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(bar(B_KF + jj % NSK), nb * kBlk8);
-        __syncwarp();
-        if (lane < nb)
-          tma_box8(sbase + OFF_K + (jj % NSK) * kTile8 + lane * kBlk8, &tm_k, bar(B_KF + jj % NSK),
-                   (int)(tile * kBlockSize));
-        ++k_sent;
-        // V's codes
-        if (jj >= NST) go = wait_or_abort(bar(B_STE + jj % NST), (jj / NST - 1) & 1, abort_flag, a.err);
-        go = __all_sync(0xffffffffu, go && !*abort_flag);
-        if (!go) break;
-        if (lane == 0) mbar_arrive_expect_tx(bar(B_STF + jj % NST), nb * kBlk8);
-        __syncwarp();
-        if (lane < nb)
-          bulk_g2s_hint(sbase + OFF_ST + (jj % NST) * kTile8 + lane * kBlk8, vpool + tile * kBlk8,
-                        kBlk8, bar(B_STF + jj % NST), policy_evict_normal());
-        ++v_sent;
+        ++sent;
         if (jj == 0 || turn) {
           ids_next = load_ids(j / 4 + 1);
           sc_next = load_scales(j / 4 + 1, ids_next);
         }
       }
       if (!go && lane == 0) {                    // let the copies in flight land
-        for (int jj = max(0, k_sent - NSK); jj < k_sent; ++jj)
-          mbar_wait(bar(B_KF + jj % NSK), (jj / NSK) & 1, nullptr);
-        for (int jj = max(0, v_sent - NST); jj < v_sent; ++jj)
-          mbar_wait(bar(B_STF + jj % NST), (jj / NST) & 1, nullptr);
+        for (int jj = max(0, sent - NSK); jj < sent; ++jj)
+          mbar_wait(bar(full0 + jj % NSK), (jj / NSK) & 1, nullptr);
       }
       __syncwarp();
     } else if (warp >= W_CONV) {
@@ -408,38 +443,40 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
       const uint32_t sw_second = ((ch + 1 - half) ^ (rs & 7)) << 4;
       const int masked_from = (a.prior_len + qrow0 + 1) / BN;   // tiles with a masked entry
       bool go = true;
-      for (int jj = 0; jj < n_tiles; ++jj) {
+      Ring<NST> tr;
+      Ring<NSV> vr;
+      for (int jj = 0; jj < n_tiles; ++jj, tr.next(), vr.next()) {
         const int j = t0 + jj;
         // the V ring first holds the queries
-        go = jj > 0 || wait_or_abort(bar(B_QC), 0, abort_flag, a.err);
-        if (go) go = wait_or_abort(bar(B_STF + jj % NST), (jj / NST) & 1, abort_flag, a.err);
-        if (go && jj >= NSV) go = wait_or_abort(bar(B_VE + jj % NSV), (jj / NSV - 1) & 1, abort_flag, a.err);
+        go = jj > 0 || wait_fast(bar(B_QC), 0, abort_flag, a.err);
+        if (go) go = wait_idle(bar(B_STF + tr.slot), tr.parity, abort_flag, a.err);
+        if (go && jj >= NSV) go = wait_idle(bar(B_VE + vr.slot), vr.parity ^ 1, abort_flag, a.err);
         go = __all_sync(0xffffffffu, go && !*abort_flag);
         if (!go) break;                          // leave the loop as a warp
-        const uint32_t src = sbase + OFF_ST + (jj % NST) * kTile8 + pt * 16;
-        const uint32_t dst = sbase + OFF_V + (jj % NSV) * kTile16 + thr_dst;
-        const bool masked = j >= masked_from;
-#pragma unroll 2
+        const uint32_t src = sbase + OFF_ST + tr.slot * kTile8 + pt * 16;
+        const uint32_t dst = sbase + OFF_V + vr.slot * kTile16 + thr_dst;
+        if (j >= masked_from) {
+          // NaN codes and rows behind the sequence become zeros where they are
+          // staged: rare, so its code stays short
+#pragma unroll 1
+          for (int b = 0; b < kBlkPerTile; ++b) {
+            const int key = j * BN + b * kBlockSize + rs;
+            uint4 x = lds16(src + b * kBlk8);
+            bool found = false;
+            x.x = drop_nan(x.x, &found);
+            x.y = drop_nan(x.y, &found);
+            x.z = drop_nan(x.z, &found);
+            x.w = drop_nan(x.w, &found);
+            if (key >= p.total_len) x = make_uint4(0u, 0u, 0u, 0u);
+            else if (found) atomicMin(nan_key, key);
+            sts16(src + b * kBlk8, x);
+          }
+        }
+#pragma unroll 1
         for (int b4 = 0; b4 < kBlkPerTile; b4 += 4) {
           uint4 x[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) x[i] = lds16(src + (b4 + i) * kBlk8);
-          if (masked) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int key = j * BN + (b4 + i) * kBlockSize + rs;
-              bool found = false;
-              if (key >= p.total_len) {          // behind the sequence: not its data
-                x[i] = make_uint4(0u, 0u, 0u, 0u);
-              } else {
-                x[i].x = drop_nan(x[i].x, &found);
-                x[i].y = drop_nan(x[i].y, &found);
-                x[i].z = drop_nan(x[i].z, &found);
-                x[i].w = drop_nan(x[i].w, &found);
-              }
-              if (found) atomicMin(nan_key, key);
-            }
-          }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const uint32_t w[4] = {half ? x[i].z : x[i].x, half ? x[i].w : x[i].y,
@@ -458,27 +495,17 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
         fence_proxy_async_smem();                // make the tile visible to the tensor core
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(bar(B_STE + jj % NST));
-          mbar_arrive(bar(B_VF + jj % NSV));
+          mbar_arrive(bar(B_STE + tr.slot));
+          mbar_arrive(bar(B_VF + vr.slot));
         }
       }
     } else if (warp == W_MMA && n_tiles > 0) {
       // ------------------------------------------------------------- MMA issuer
-      if (lane == 0) {
-        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_q)) : "memory");
-        mbar_arrive_expect_tx(bar(B_Q), 2 * kTile16);
-        for (int hh = 0; hh < 2; ++hh) {
-          const uint32_t dst = sbase + OFF_V + hh * kTile16;
-          tma_load_3d(dst, &tm_q, bar(B_Q), 0, hh ? head1 : head0, hh ? qrow1 : qrow0);
-          tma_load_3d(dst + kHalf16, &tm_q, bar(B_Q), 64, hh ? head1 : head0, hh ? qrow1 : qrow0);
-        }
-      }
-      __syncwarp();
       constexpr uint32_t idesc_qk = idesc0(false, BM, BN);
       constexpr uint32_t idesc_pv = idesc0(true, BM, HD);
-      // S_h = (hi + lo)_h K^T of ring position jj into the columns of S_h
-      auto issue_qk = [&](int hh, int jj) {
-        const uint32_t kb = sbase + OFF_K + (jj % NSK) * kTile8;
+      // S_h = (hi + lo)_h K^T of K's stage into the columns of S_h
+      auto issue_qk = [&](int hh, int stage) {
+        const uint32_t kb = sbase + OFF_K + stage * kTile8;
         const uint32_t qa = sbase + OFF_Q + hh * kTile16;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -488,42 +515,50 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
         }
         commit_e(bar(B_SF + hh));
       };
-      // O_h += P_h V, P_h from TMEM (16 keys = 8 columns a step)
-      auto issue_pv = [&](int hh, int jj) {
-        const uint32_t vb = sbase + OFF_V + (jj % NSV) * kTile16;
+      // O_h += P_h V for 64 of the tile's keys, P_h from TMEM (16 keys = 8 columns a step)
+      auto issue_pv = [&](int hh, int stage, bool first, int half) {
+        const uint32_t vb = sbase + OFF_V + stage * kTile16;
 #pragma unroll
-        for (int k = 0; k < BN / 16; ++k) {
+        for (int k = half * 4; k < half * 4 + 4; ++k) {
           const uint64_t bd = make_sw128_desc(vb + k * 16 * 128, kHalf16, 1024);
           mma_ts_e(tmem + COL_O + hh * HD, tmem + COL_S + hh * BN + k * 8, bd, idesc_pv,
-                   (jj > 0 || k > 0) ? 1u : 0u);
+                   (!first || k > 0) ? 1u : 0u);
         }
-        if (jj == n_tiles - 1) commit_e(bar(B_OD + hh));
       };
       // The streams alternate: while one's softmax runs, the other's products
       // do.  Q K_{j+1}^T rewrites S_h, which holds P_h, right behind P_h V_j:
       // products issued by one thread execute in issue order.
-      auto wait_k = [&](int jj) {
-        return __all_sync(0xffffffffu, wait_fast(bar(B_KF + jj % NSK), (jj / NSK) & 1, abort_flag, a.err));
+      auto wait_ok = [&](int b, uint32_t parity) {
+        return __all_sync(0xffffffffu, wait_fast(bar(b), parity, abort_flag, a.err));
       };
-      bool ok = __all_sync(0xffffffffu, wait_or_abort(bar(B_QC), 0, abort_flag, a.err)) && wait_k(0);
+      Ring<NSK> kr;
+      Ring<NSV> vr;
+      bool ok = wait_ok(B_QC, 0) && wait_ok(B_KF, 0);
       if (ok) {
         tc_fence_after();
         issue_qk(0, 0);
         issue_qk(1, 0);
-        for (int jj = 0; jj < n_tiles && ok; ++jj) {
+        for (int jj = 0; jj < n_tiles && ok; ++jj, vr.next()) {
           const bool more = jj + 1 < n_tiles;
+          kr.next();                             // of tile jj + 1
           for (int hh = 0; hh < 2 && ok; ++hh) {
-            ok = __all_sync(0xffffffffu, wait_fast(bar(B_PF + hh), jj & 1, abort_flag, a.err));
+            ok = wait_ok(B_PF + 2 * hh, jj & 1);
             if (!ok) break;
             tc_fence_after();
-            if (hh == 0) ok = __all_sync(0xffffffffu, wait_fast(bar(B_VF + jj % NSV), (jj / NSV) & 1, abort_flag, a.err));
+            if (hh == 0) ok = wait_ok(B_VF + vr.slot, vr.parity);
             if (!ok) break;
-            issue_pv(hh, jj);
-            if (hh == 1) commit_e(bar(B_VE + jj % NSV));   // V no longer needed
+            issue_pv(hh, vr.slot, jj == 0, 0);
+            ok = wait_ok(B_PF + 2 * hh + 1, jj & 1);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(hh, vr.slot, jj == 0, 1);
+            if (hh == 1) commit_e(bar(B_VE + vr.slot));   // V no longer needed
             if (more) {
-              if (hh == 0) ok = wait_k(jj + 1);
+              if (hh == 0) ok = wait_ok(B_KF + kr.slot, kr.parity);
               if (!ok) break;
-              issue_qk(hh, jj + 1);
+              issue_qk(hh, kr.slot);
+            } else {
+              commit_e(bar(B_OD + hh));
             }
           }
         }
@@ -537,19 +572,16 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
-    // -------------------------------------- softmax (stream hh, column half ch)
-    const int hh = warp >> 3, ch = (warp >> 2) & 1;
+    // ------------------------------------------------------------- softmax (stream hh)
+    const int hh = warp >> 2;
     const int r = tid & 127;                // query row in the tile, TMEM lane
-    const int pair = 1 + hh * 4 + (warp & 3);   // named barrier of the two warps of these rows
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t col_s = COL_S + hh * BN, col_o = COL_O + hh * HD + ch * kCols;
+    const uint32_t col_s = COL_S + hh * BN, col_o = COL_O + hh * HD;
     const int q0 = hh ? qrow1 : qrow0, head = hh ? head1 : head0;
     const int row_pos = a.prior_len + q0 + r;
-    volatile float* mine = reinterpret_cast<volatile float*>(smem + OFF_ROWS) + (2 * hh + ch) * BM + r;
-    volatile float* others = mine + (ch ? -BM : BM);
     float q_up = 1.f;                       // what brings products back to the query's size
-    if (n_tiles > 0 && wait_or_abort(bar(B_Q), 0, abort_flag, a.err)) {
-      // this row's query becomes its hi and lo rows, half of each here
+    if (n_tiles > 0 && wait_fast(bar(B_Q), 0, abort_flag, a.err)) {
+      // this row's query becomes its hi and lo rows
       const uint32_t src = sbase + OFF_V + hh * kTile16 + r * 128;
       const uint32_t dst = sbase + OFF_Q + hh * kTile16 + r * 128;
       auto piece = [&](int i) {             // elements 8 i .. 8 i + 7
@@ -570,8 +602,8 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
       q_up = __uint_as_float((uint32_t)(127 + ex - 7) << 23);
       // an infinite or NaN element makes the row's scores NaN
       const uint32_t bad = top == 255 ? 0x7f7f7f7fu : 0u;
-#pragma unroll 2
-      for (int i = 4 * ch; i < 4 * ch + 4; ++i) {   // 16 elements: a chunk of hi and one of lo
+#pragma unroll 4
+      for (int i = 0; i < 8; ++i) {         // 16 elements: a chunk of hi and one of lo
         const uint4 x = piece(2 * i), y = piece(2 * i + 1);
         const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
         uint32_t hi[4], lo[4];
@@ -598,43 +630,59 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
       fence_proxy_async_smem();
       mbar_arrive(bar(B_QC));
     }
-    // M of the whole row in log2 units, l of this half's columns
+    // M, in log2 units, and l
     float m_run = -INFINITY, l_run = 0.f;
     bool wide = false;                      // once true, l is summed against
     float ms_run = -INFINITY;               // a running maximum of its own
-    for (int jj = 0; jj < n_tiles; ++jj) {
+    Ring<NSK> kr;
+    Ring<kScaleSlots> sr;
+    for (int jj = 0; jj < n_tiles; ++jj, kr.next(), sr.next()) {
       wait_fast(bar(B_SF + hh), jj & 1, abort_flag, a.err);
       __syncwarp();
       tc_fence_after();
       // the S_B commit follows both streams' Q K^T: this K stage can be refilled
-      if (hh == 1 && ch == 0 && lane == 0) mbar_arrive(bar(B_KE + jj % NSK));
-      const int k0 = (t0 + jj) * BN + ch * kCols;
-      // this half of the S row into registers: two loads in flight, one wait
-      float t[2][32];
-      tmem_ld32(lane_base + col_s + ch * kCols, t[0]);
-      tmem_ld32(lane_base + col_s + ch * kCols + 32, t[1]);
-      tmem_wait_ld();
-      reg_fence(t[0]);
-      reg_fence(t[1]);
-      if (k0 + kCols - 1 > a.prior_len + q0) {            // causal mask needed
+      if (hh == 1 && lane == 0) mbar_arrive(bar(B_KE + kr.slot));
+      const int k0 = (t0 + jj) * BN;
+      if (k0 + BN - 1 > a.prior_len + q0) {
+        // the causal mask, written over S: rare, so its code stays short
+#pragma unroll 1
+        for (int c = 0; c < BN; c += 16) {
+          float x[16];
+          tmem_ld16(lane_base + col_s + c, x);
+          tmem_wait_ld();
+          reg_fence(x);
+          uint32_t u[16];
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (k0 + c * 32 + i > row_pos) t[c][i] = -INFINITY;
+          for (int i = 0; i < 16; ++i)
+            u[i] = k0 + c + i > row_pos ? 0xff800000u : __float_as_uint(x[i]);
+          tmem_st16(lane_base + col_s + c, u);
+        }
+        tmem_wait_st();
       }
       const TileScales* ts =
-          reinterpret_cast<const TileScales*>(smem + OFF_SCALES) + jj % kScaleSlots;
+          reinterpret_cast<const TileScales*>(smem + OFF_SCALES) + sr.slot;
+      // the whole S row into registers: four loads in flight, one wait
+      float t[BN / 32][32];
+#pragma unroll
+      for (int c = 0; c < BN / 32; ++c) tmem_ld32(lane_base + col_s + c * 32, t[c]);
       // blocks' factors from products to scores; never 0, so that a masked
       // score stays -inf
-      const float4 k4 = *reinterpret_cast<const float4*>(ts->k + 4 * ch);
-      const float4 v4 = *reinterpret_cast<const float4*>(ts->v + 4 * ch);
-      const float kq[4] = {fmaxf(k4.x * q_up, 1e-38f), fmaxf(k4.y * q_up, 1e-38f),
-                           fmaxf(k4.z * q_up, 1e-38f), fmaxf(k4.w * q_up, 1e-38f)};
-      const float ev[4] = {v4.x, v4.y, v4.z, v4.w};
+      float kq[kBlkPerTile], ev[kBlkPerTile];
+#pragma unroll
+      for (int b = 0; b < kBlkPerTile; b += 4) {
+        const float4 k = *reinterpret_cast<const float4*>(ts->k + b);
+        const float4 v = *reinterpret_cast<const float4*>(ts->v + b);
+        kq[b] = fmaxf(k.x * q_up, 1e-38f), kq[b + 1] = fmaxf(k.y * q_up, 1e-38f);
+        kq[b + 2] = fmaxf(k.z * q_up, 1e-38f), kq[b + 3] = fmaxf(k.w * q_up, 1e-38f);
+        ev[b] = v.x, ev[b + 1] = v.y, ev[b + 2] = v.z, ev[b + 3] = v.w;
+      }
+      const bool tile_wide = ts->wide;
+      tmem_wait_ld();
+#pragma unroll
+      for (int c = 0; c < BN / 32; ++c) reg_fence(t[c]);
       float mx = -INFINITY;
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
+      for (int b = 0; b < kBlkPerTile; ++b) {
         const float* x = &t[b / 2][(b & 1) * 16];
         float m0 = fmax3(x[0], x[1], x[2]), m1 = fmax3(x[3], x[4], x[5]);
         m0 = fmax3(m0, x[6], x[7]);
@@ -644,22 +692,22 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
         m0 = fmax3(m0, x[14], x[15]);
         mx = fmaxf(mx, fmaf(fmaxf(m0, m1), kq[b], ev[b]));
       }
-      if (ts->wide || wide) {
+      if (tile_wide || wide) {
         // from here on l = sum 2^(s - ms); before, it was sum 2^(s + E - M).
         // Rare, so it reads S again block by block and keeps the code short.
         if (!wide && jj > 0) ms_run = m_run - (float)ts->e;
         wide = true;
 #pragma unroll 1
-        for (int b = 0; b < 4; ++b) {
+        for (int b = 0; b < kBlkPerTile; ++b) {
           float x[16];
-          tmem_ld16(lane_base + col_s + ch * kCols + b * 16, x);
+          tmem_ld16(lane_base + col_s + b * 16, x);
           tmem_wait_ld();
           reg_fence(x);
-          const float k = fmaxf(ts->k[4 * ch + b] * q_up, 1e-38f);
+          const float k = fmaxf(ts->k[b] * q_up, 1e-38f);
           float m2 = ms_run;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            x[i] = k0 + b * 16 + i > row_pos ? -INFINITY : x[i] * k;
+            x[i] *= k;
             m2 = fmaxf(m2, x[i]);
           }
           const float m0 = m2 == -INFINITY ? 0.f : m2;   // no key yet: every weight is 0
@@ -669,23 +717,16 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
           for (int i = 0; i < 16; ++i) l_run += fast_exp2(x[i] - m0);
         }
       }
-      // The row's maximum from both halves.  The barrier also orders the P
-      // stores below, which lie over S columns of the other half, behind that
-      // half's loads.  (The slots are free again before the next tile: its S
-      // follows P V of this one, which waits for both halves' P.)
-      *mine = mx;
-      named_bar_sync(pair, 64);
-      mx = fmaxf(mx, *others);
       float m_new = m_run;
       if (mx > m_run + kLazy || m_run == -INFINITY) m_new = mx;
       const float alpha = (m_new == m_run) ? 1.f : fast_exp2(m_run - m_new);
       if (jj >= 1 && __any_sync(0xffffffffu, alpha != 1.f)) {
         // O holds P V of the tiles before; the S_h commit of this tile was
         // issued behind their last product, so that product is complete and
-        // O can be rescaled in place, this half's columns here
+        // O can be rescaled in place
         __syncwarp();
 #pragma unroll 1
-        for (int c = 0; c < kCols / 16; ++c) {
+        for (int c = 0; c < HD / 16; ++c) {
           float o[16];
           tmem_ld16(lane_base + col_o + c * 16, o);
           tmem_wait_ld();
@@ -699,65 +740,53 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
       // p = 2^(s + ev - M), written as f16 pairs over the first 64 columns of
       // S; a row that has seen no key (its keys are in another CTA) has p = 0
       const float m_ref = m_new == -INFINITY ? 0.f : m_new;
-      float l_new = wide ? l_run : l_run * alpha;
+      float2 sums[kBlkPerTile];              // of the blocks' weights, even and odd columns
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      for (int c = 0; c < BN / 32; ++c) {
         uint32_t pk[16];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int b = 2 * c + h;
           const float n = ev[b] - m_ref;
           const float2 k2 = make_float2(kq[b], kq[b]), n2 = make_float2(n, n);
-          float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          float2 part[2];
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
             const float2 x = ffma2(make_float2(t[c][16 * h + i], t[c][16 * h + i + 1]), k2, n2);
             const float2 pp = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-            sum2[(i >> 1) & 1] = fadd2(sum2[(i >> 1) & 1], pp);
+            part[(i >> 1) & 1] = i < 4 ? pp : fadd2(part[(i >> 1) & 1], pp);
             const __half2 ph = __floats2half2_rn(pp.x, pp.y);
             pk[8 * h + i / 2] = *reinterpret_cast<const uint32_t*>(&ph);
           }
-          const float2 s01 = fadd2(sum2[0], sum2[1]);
-          if (!wide) l_new = fmaf(s01.x + s01.y, ts->l[4 * ch + b], l_new);
+          sums[b] = fadd2(part[0], part[1]);
         }
-        tmem_st16(lane_base + col_s + (2 * ch + c) * 16, pk);
+        tmem_st16(lane_base + col_s + c * 16, pk);
+        if (c & 1) {                        // a half of P is in TMEM
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B_PF + 2 * hh + (c >> 1)));
+        }
       }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_PF + hh));
-      l_run = l_new;
+      // l, while the products run
+      if (!wide) {
+        l_run *= alpha;
+#pragma unroll
+        for (int b = 0; b < kBlkPerTile; ++b)
+          l_run = fmaf(sums[b].x + sums[b].y, ts->l[b], l_run);
+      }
       m_run = m_new;
     }
     if (n_tiles > 0) {
-      wait_or_abort(bar(B_OD + hh), 0, abort_flag, a.err);
+      wait_fast(bar(B_OD + hh), 0, abort_flag, a.err);
       __syncwarp();
       tc_fence_after();
     }
-    // l stands for l 2^ref, O for O 2^M = O 2^(M - ref): the halves' sums
-    // against their larger reference (the same unless wide)
+    // l stands for l 2^ref, O for O 2^M = O 2^ref unit.  The results take 1 / l
+    // and then the unit, which may leave the normal range when V's scales do.
     const int e = n_tiles > 0 ? (reinterpret_cast<const TileScales*>(smem + OFF_SCALES))->e : 0;
-    float ref = wide ? ms_run : m_run - (float)e;
-    {
-      *mine = ref;
-      named_bar_sync(pair, 64);
-      const float ref2 = *others;
-      named_bar_sync(pair, 64);
-      *mine = l_run;
-      named_bar_sync(pair, 64);
-      const float l2 = *others;
-      named_bar_sync(pair, 64);             // the rows' slots may be reused
-      if (ref != ref2) {
-        const float m = fmaxf(ref, ref2);
-        l_run = l_run * fast_exp2(ref - m) + l2 * fast_exp2(ref2 - m);
-        ref = m;
-      } else {
-        l_run += l2;
-      }
-    }
-    // The results take 1 / l and then the unit, which may leave the normal
-    // range when V's scales do.
-    const float unit = wide ? fast_exp2(m_run - ref) : scale_value((uint32_t)(e + 127));
+    const float ref = wide ? ms_run : m_run - (float)e;
+    const float unit = wide ? fast_exp2(m_run - ms_run) : scale_value((uint32_t)(e + 127));
     if (n_tiles > 0 && row_pos >= *nan_key)
       l_run = __int_as_float(0x7fffffff);   // the row sees a NaN value
     const bool row_ok = (q0 + r) < a.chunk_len;
@@ -766,26 +795,24 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
     if (p.splits == 1) {
       const float inv = 1.f / l_run;
 #pragma unroll 1
-      for (int c = 0; c < kCols; c += 16) {
-        float o[16];
-        tmem_ld16(lane_base + col_o + c, o);
+      for (int c = 0; c < HD; c += 32) {
+        float o[32];
+        tmem_ld32(lane_base + col_o + c, o);
         tmem_wait_ld();
         reg_fence(o);
         if (row_ok) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = o[i] * inv * unit;
+          for (int i = 0; i < 32; ++i) o[i] = o[i] * inv * unit;
 #pragma unroll
-          for (int i = 0; i < 16; i += 8)
-            *reinterpret_cast<uint4*>(orow + ch * kCols + c + i) =
+          for (int i = 0; i < 32; i += 8)
+            *reinterpret_cast<uint4*>(orow + c + i) =
                 make_uint4(pack_bf16(o[i], o[i + 1]), pack_bf16(o[i + 2], o[i + 3]),
                            pack_bf16(o[i + 4], o[i + 5]), pack_bf16(o[i + 6], o[i + 7]));
         }
       }
     } else {
       const uint32_t row_at = sbase + OFF_ROWS + (hh * BM + r) * 8;
-      named_bar_sync(9, kSoftThreads);      // the stats lie over other rows' slots
-      if (ch == 0)
-        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(row_at), "f"(ref), "f"(l_run) : "memory");
+      asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(row_at), "f"(ref), "f"(l_run) : "memory");
       cluster_sync();                       // every CTA's stats are there, its tiles are done with
       // CTA k adds up columns k W .. k W + W - 1 (W = 2^w): four columns of
       // 128 rows are 2 KiB in a piece, rows side by side
@@ -806,7 +833,7 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
         l_run = f;
       }
 #pragma unroll 1
-      for (int c = 0; c < kCols; c += 16) {
+      for (int c = 0; c < HD; c += 16) {
         float o[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[i] = 0.f;
@@ -816,8 +843,8 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
           reg_fence(o);
         }
         // W is at least 16: the 16 columns have one owner
-        const int col = ch * kCols + c, owner = col >> w;
-        const int piece = ((rank * 2 + hh) << (w - 2)) + ((col & ((1 << w) - 1)) >> 2);
+        const int owner = c >> w;
+        const int piece = ((rank * 2 + hh) << (w - 2)) + ((c & ((1 << w) - 1)) >> 2);
         const uint32_t at = peer(sbase + piece * (BM * 16) + r * 16, owner);
         if (row_ok) {
 #pragma unroll
@@ -828,10 +855,9 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
         }
       }
       cluster_sync();
-      // this CTA's columns, half of them here
-      const int own = 1 << (w - 3);         // pieces of four columns a half
+      // this CTA's columns
       if (row_ok) {
-        for (int c4 = ch * own; c4 < ch * own + own; c4 += 2) {
+        for (int c4 = 0; c4 < 1 << (w - 2); c4 += 2) {
           float o[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) o[i] = 0.f;
