@@ -36,10 +36,14 @@
 //    that see the key come out as NaN.
 // Roles (512 threads):
 //   warps 0-3 / 4-7   softmax of stream A / B: thread r owns query row r
-//   warp 8            TMEM allocator and MMA issuer
+//   warp 8            TMEM allocator and MMA issuer of both streams
 //   warp 9 / 10       producers: K's boxes and the scales / V's copies
 //   warp 11           none (it completes the issuer's warpgroup)
 //   warps 12-15       V converters
+// The issuer's own instructions count: with descriptors formed and a warp vote
+// taken at every wait it needed 1,500 cycles for a stream's 1,024 cycles of
+// products (161 us).  Two issuers, one a stream, let the streams fall into
+// step, both in their softmax or both at the tensor core (192 us).
 // Both pools' tiles are three stages deep in their fp8 form (K's ring is read
 // by the MMAs, V's by the converters), so 96 KiB are in flight or in use.
 // Measured on the way (2,048 tokens over 4,096, 32/8 heads): both pools
@@ -503,37 +507,44 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
       // ------------------------------------------------------------- MMA issuer
       constexpr uint32_t idesc_qk = idesc0(false, BM, BN);
       constexpr uint32_t idesc_pv = idesc0(true, BM, HD);
-      // S_h = (hi + lo)_h K^T of K's stage into the columns of S_h
+      // descriptors of the first step; a step's offset adds to the address
+      // field (16-byte units), which cannot carry out of it
+      const uint64_t q_desc = make_sw128_desc(sbase + OFF_Q, 16, 1024);
+      const uint64_t k_desc = make_sw128_desc(sbase + OFF_K, 16, 1024);
+      const uint64_t v_desc = make_sw128_desc(sbase + OFF_V, kHalf16, 1024);
+      // S_h = (hi + lo)_h K^T of K's stage
       auto issue_qk = [&](int hh, int stage) {
-        const uint32_t kb = sbase + OFF_K + stage * kTile8;
-        const uint32_t qa = sbase + OFF_Q + hh * kTile16;
+        const uint64_t qd = q_desc + hh * (kTile16 / 16);
+        const uint64_t kd = k_desc + stage * (kTile8 / 16);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint64_t ad = make_sw128_desc(qa + (k >> 2) * kTile8 + (k & 3) * 32, 16, 1024);
-          const uint64_t bd = make_sw128_desc(kb + (k & 3) * 32, 16, 1024);
-          mma8_ss_e(tmem + COL_S + hh * BN, ad, bd, idesc_qk, k > 0 ? 1u : 0u);
-        }
+        for (int k = 0; k < 8; ++k)
+          mma8_ss_e(tmem + COL_S + hh * BN, qd + ((k >> 2) * kTile8 + (k & 3) * 32) / 16,
+                    kd + (k & 3) * 32 / 16, idesc_qk, k > 0 ? 1u : 0u);
         commit_e(bar(B_SF + hh));
       };
       // O_h += P_h V for 64 of the tile's keys, P_h from TMEM (16 keys = 8 columns a step)
-      auto issue_pv = [&](int hh, int stage, bool first, int half) {
-        const uint32_t vb = sbase + OFF_V + stage * kTile16;
+      auto issue_pv = [&](int hh, int stage, uint32_t first, int half) {
+        const uint64_t vd = v_desc + stage * (kTile16 / 16);
 #pragma unroll
-        for (int k = half * 4; k < half * 4 + 4; ++k) {
-          const uint64_t bd = make_sw128_desc(vb + k * 16 * 128, kHalf16, 1024);
-          mma_ts_e(tmem + COL_O + hh * HD, tmem + COL_S + hh * BN + k * 8, bd, idesc_pv,
-                   (!first || k > 0) ? 1u : 0u);
-        }
+        for (int k = half * 4; k < half * 4 + 4; ++k)
+          mma_ts_e(tmem + COL_O + hh * HD, tmem + COL_S + hh * BN + k * 8, vd + k * 16 * 128 / 16,
+                   idesc_pv, k > 0 ? 1u : first);
       };
       // The streams alternate: while one's softmax runs, the other's products
       // do.  Q K_{j+1}^T rewrites S_h, which holds P_h, right behind P_h V_j:
-      // products issued by one thread execute in issue order.
-      auto wait_ok = [&](int b, uint32_t parity) {
-        return __all_sync(0xffffffffu, wait_fast(bar(b), parity, abort_flag, a.err));
+      // products issued by one thread execute in issue order.  A lane that
+      // gives up a wait keeps issuing (every address stays valid) until the
+      // vote at the tile's end.
+      bool ok = true;
+      auto wait_for = [&](int b, uint32_t parity) {
+        ok &= wait_fast(bar(b), parity, abort_flag, a.err);
+        __syncwarp();
       };
       Ring<NSK> kr;
       Ring<NSV> vr;
-      bool ok = wait_ok(B_QC, 0) && wait_ok(B_KF, 0);
+      wait_for(B_QC, 0);
+      wait_for(B_KF, 0);
+      ok = __all_sync(0xffffffffu, ok);
       if (ok) {
         tc_fence_after();
         issue_qk(0, 0);
@@ -541,26 +552,24 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
         for (int jj = 0; jj < n_tiles && ok; ++jj, vr.next()) {
           const bool more = jj + 1 < n_tiles;
           kr.next();                             // of tile jj + 1
-          for (int hh = 0; hh < 2 && ok; ++hh) {
-            ok = wait_ok(B_PF + 2 * hh, jj & 1);
-            if (!ok) break;
+          // ahead of the softmax, where this warp waits anyway
+          wait_for(B_VF + vr.slot, vr.parity);
+          if (more) wait_for(B_KF + kr.slot, kr.parity);
+#pragma unroll 1
+          for (int hh = 0; hh < 2; ++hh) {
+            wait_for(B_PF + 2 * hh, jj & 1);
             tc_fence_after();
-            if (hh == 0) ok = wait_ok(B_VF + vr.slot, vr.parity);
-            if (!ok) break;
-            issue_pv(hh, vr.slot, jj == 0, 0);
-            ok = wait_ok(B_PF + 2 * hh + 1, jj & 1);
-            if (!ok) break;
+            issue_pv(hh, vr.slot, jj > 0 ? 1u : 0u, 0);
+            wait_for(B_PF + 2 * hh + 1, jj & 1);
             tc_fence_after();
-            issue_pv(hh, vr.slot, jj == 0, 1);
-            if (hh == 1) commit_e(bar(B_VE + vr.slot));   // V no longer needed
-            if (more) {
-              if (hh == 0) ok = wait_ok(B_KF + kr.slot, kr.parity);
-              if (!ok) break;
+            issue_pv(hh, vr.slot, 1u, 1);
+            if (more)
               issue_qk(hh, kr.slot);
-            } else {
+            else
               commit_e(bar(B_OD + hh));
-            }
           }
+          commit_e(bar(B_VE + vr.slot));         // V no longer needed
+          ok = __all_sync(0xffffffffu, ok && !*abort_flag);
         }
       }
       if (!ok) mbar_wait(bar(B_Q), 0, nullptr);  // after an abort, let the Q load land
@@ -793,22 +802,36 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
     __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.out) +
                           ((int64_t)(q0 + r) * a.num_q_heads + head) * HD;
     if (p.splits == 1) {
+      // The rows leave through this stream's query tiles, which its products
+      // are done with: 16-byte chunks XORed by the row, then whole rows of
+      // the warp's 32, two to a store.  (Each thread storing its own row, 32
+      // lines to a store, took 5,400 cycles.)
       const float inv = 1.f / l_run;
+      const uint32_t tile = sbase + OFF_Q + hh * kTile16;
 #pragma unroll 1
       for (int c = 0; c < HD; c += 32) {
         float o[32];
         tmem_ld32(lane_base + col_o + c, o);
         tmem_wait_ld();
         reg_fence(o);
-        if (row_ok) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = o[i] * inv * unit;
+        for (int i = 0; i < 32; ++i) o[i] = o[i] * inv * unit;
 #pragma unroll
-          for (int i = 0; i < 32; i += 8)
-            *reinterpret_cast<uint4*>(orow + c + i) =
+        for (int i = 0; i < 32; i += 8)
+          sts16(tile + r * 256 + ((((c + i) / 8) ^ (r & 15)) << 4),
                 make_uint4(pack_bf16(o[i], o[i + 1]), pack_bf16(o[i + 2], o[i + 3]),
-                           pack_bf16(o[i + 4], o[i + 5]), pack_bf16(o[i + 6], o[i + 7]));
-        }
+                           pack_bf16(o[i + 4], o[i + 5]), pack_bf16(o[i + 6], o[i + 7])));
+      }
+      __syncwarp();
+      const int r0 = r - lane + (lane >> 4), chunk = lane & 15;
+      __nv_bfloat16* base = static_cast<__nv_bfloat16*>(a.out) +
+                            ((int64_t)q0 * a.num_q_heads + head) * HD + chunk * 8;
+#pragma unroll 4
+      for (int i = 0; i < 32; i += 2) {
+        const int row = r0 + i;
+        const uint4 v = lds16(tile + row * 256 + ((chunk ^ (row & 15)) << 4));
+        if (q0 + row < a.chunk_len)
+          *reinterpret_cast<uint4*>(base + (int64_t)row * a.num_q_heads * HD) = v;
       }
     } else {
       const uint32_t row_at = sbase + OFF_ROWS + (hh * BM + r) * 8;
