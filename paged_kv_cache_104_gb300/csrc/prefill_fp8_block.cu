@@ -220,13 +220,52 @@ __device__ __forceinline__ void tma_box8(uint32_t dst, const CUtensorMap* map, u
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(row)
       : "memory");
 }
-// as mma_ss_e, 8-bit operands
-__device__ __forceinline__ void mma8_ss_e(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+// S = (hi + lo) K^T in eight products of 32 dims, then the commit to `bar`: one
+// elected lane, one block (an election and descriptors formed for every
+// product made the issuer the bound).  A step adds 32 bytes to the operands'
+// addresses (2 in a descriptor's 16-byte units, which cannot carry out of the
+// address field), lo lies 16 KiB behind hi.
+__device__ __forceinline__ void issue_qk8(uint32_t d_tmem, uint64_t q_desc, uint64_t k_desc,
+                                          uint32_t idesc, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e, t, f;\n\t.reg .b64 a, b;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\tsetp.eq.u32 t, 0, 0;\n\tsetp.ne.u32 f, 0, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, f;\n\t"
+      "add.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+      "add.s64 a, %1, 4;\n\tadd.s64 b, %2, 4;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+      "add.s64 a, %1, 6;\n\tadd.s64 b, %2, 6;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+      "add.s64 a, %1, 1024;\n\tadd.s64 b, %2, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+      "add.s64 a, %1, 1026;\n\tadd.s64 b, %2, 2;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+      "add.s64 a, %1, 1028;\n\tadd.s64 b, %2, 4;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+      "add.s64 a, %1, 1030;\n\tadd.s64 b, %2, 6;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t}" ::"r"(
+          d_tmem),
+      "l"(q_desc), "l"(k_desc), "r"(idesc), "r"(bar)
+      : "memory");
+}
+// O (+)= P V over 64 keys in four products of 16: P from TMEM, 8 columns a
+// step, V's rows 2 KiB a step.
+__device__ __forceinline__ void issue_pv4(uint32_t d_tmem, uint32_t p_tmem, uint64_t v_desc,
                                           uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
+      "{\n\t.reg .pred e, t, f;\n\t.reg .b32 a;\n\t.reg .b64 b;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\tsetp.eq.u32 t, 0, 0;\n\tsetp.ne.u32 f, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, f;\n\t"
+      "add.u32 a, %1, 8;\n\tadd.s64 b, %2, 128;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "add.u32 a, %1, 16;\n\tadd.s64 b, %2, 256;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "add.u32 a, %1, 24;\n\tadd.s64 b, %2, 384;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t}" ::"r"(d_tmem),
+      "r"(p_tmem), "l"(v_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
 // f16 pair to E4M3 codes, to nearest even, saturating
 __device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t u) {
@@ -507,28 +546,16 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
       // ------------------------------------------------------------- MMA issuer
       constexpr uint32_t idesc_qk = idesc0(false, BM, BN);
       constexpr uint32_t idesc_pv = idesc0(true, BM, HD);
-      // descriptors of the first step; a step's offset adds to the address
-      // field (16-byte units), which cannot carry out of it
       const uint64_t q_desc = make_sw128_desc(sbase + OFF_Q, 16, 1024);
       const uint64_t k_desc = make_sw128_desc(sbase + OFF_K, 16, 1024);
       const uint64_t v_desc = make_sw128_desc(sbase + OFF_V, kHalf16, 1024);
-      // S_h = (hi + lo)_h K^T of K's stage
       auto issue_qk = [&](int hh, int stage) {
-        const uint64_t qd = q_desc + hh * (kTile16 / 16);
-        const uint64_t kd = k_desc + stage * (kTile8 / 16);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma8_ss_e(tmem + COL_S + hh * BN, qd + ((k >> 2) * kTile8 + (k & 3) * 32) / 16,
-                    kd + (k & 3) * 32 / 16, idesc_qk, k > 0 ? 1u : 0u);
-        commit_e(bar(B_SF + hh));
+        issue_qk8(tmem + COL_S + hh * BN, q_desc + hh * (kTile16 / 16),
+                  k_desc + stage * (kTile8 / 16), idesc_qk, bar(B_SF + hh));
       };
-      // O_h += P_h V for 64 of the tile's keys, P_h from TMEM (16 keys = 8 columns a step)
-      auto issue_pv = [&](int hh, int stage, uint32_t first, int half) {
-        const uint64_t vd = v_desc + stage * (kTile16 / 16);
-#pragma unroll
-        for (int k = half * 4; k < half * 4 + 4; ++k)
-          mma_ts_e(tmem + COL_O + hh * HD, tmem + COL_S + hh * BN + k * 8, vd + k * 16 * 128 / 16,
-                   idesc_pv, k > 0 ? 1u : first);
+      auto issue_pv = [&](int hh, int stage, uint32_t accumulate, int half) {
+        issue_pv4(tmem + COL_O + hh * HD, tmem + COL_S + hh * BN + half * 32,
+                  v_desc + stage * (kTile16 / 16) + half * (64 * 128 / 16), idesc_pv, accumulate);
       };
       // The streams alternate: while one's softmax runs, the other's products
       // do.  Q K_{j+1}^T rewrites S_h, which holds P_h, right behind P_h V_j:
