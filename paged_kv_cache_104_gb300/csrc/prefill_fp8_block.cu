@@ -38,8 +38,10 @@
 //   warps 0-3 / 4-7   softmax of stream A / B: thread r owns query row r
 //   warp 8            TMEM allocator and MMA issuer of both streams
 //   warp 9 / 10       producers: K's boxes and the scales / V's copies
-//   warp 11           none (it completes the issuer's warpgroup)
-//   warps 12-15       V converters
+//   warps 11, 13-15   V converters
+//   warp 12           none: it shares a scheduler with the issuer, whose two
+//                     softmax warps lagged the others by 400 cycles a tile
+//                     with a converter there (141.5 us against 139.6 us)
 // The issuer's own instructions count: with descriptors formed and a warp vote
 // taken at every wait it needed 1,500 cycles for a stream's 1,024 cycles of
 // products (161 us).  Two issuers, one a stream, let the streams fall into
@@ -104,7 +106,7 @@ constexpr int OFF_ROWS = OFF_BAR + 256;
 constexpr int SMEM_BYTES = OFF_ROWS + 2 * BM * 8;
 constexpr int kSoftThreads = 256;
 constexpr int kThreads = 512;
-constexpr int W_MMA = 8, W_KPROD = 9, W_VPROD = 10, W_CONV = 12;
+constexpr int W_MMA = 8, W_KPROD = 9, W_VPROD = 10, W_NONE = 12;
 // registers per thread after the split (setmaxnreg), against the launch budget
 constexpr int kRegsSoft = 200, kRegsRest = 56;
 constexpr int kRegsLaunch = (65536 / kThreads) & ~7;   // 80
@@ -472,13 +474,13 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
           mbar_wait(bar(full0 + jj % NSK), (jj / NSK) & 1, nullptr);
       }
       __syncwarp();
-    } else if (warp >= W_CONV) {
+    } else if (warp > W_VPROD && warp != W_NONE) {
       // ------------------------------------------------------------- V converters
       // thread (rs, cc) takes the 16 codes of chunk cc in row rs of every
       // block.  They are 32 bytes of a swizzled f16 row; the threads of its two
       // 64-column halves store their two 16-byte chunks in opposite order, so
       // no banks conflict.
-      const int pt = tid - W_CONV * 32;
+      const int pt = (warp < W_NONE ? 0 : warp - W_NONE) * 32 + lane;
       const int rs = pt >> 3, cc = pt & 7, half = cc >> 2;
       const uint32_t ch = 2 * (cc & 3);
       const uint32_t thr_dst = half * kHalf16 + rs * 128;
