@@ -246,10 +246,8 @@ pkv_status rope_append_prepare(const pkv_rope_append_args& x, pkv::RopeAppendArg
   a.num_q_heads = hq;
   a.num_kv_heads = x.num_kv_heads;
   a.head_dim = x.head_dim;
-  int sms = 0;
-  const pkv_status st = device_state(&a.err, &sms);
   *out = a;
-  return st;
+  return PKV_OK;
 }
 
 // Sizes every rotating append checks before its pointers.
@@ -278,6 +276,9 @@ pkv_status pkv_kv_append_rope(const pkv_rope_append_args* x, pkv_stream_t stream
   pkv::RopeAppendArgs a;
   st = rope_append_prepare(*x, &a);
   if (st != PKV_OK) return st;
+  int sms = 0;
+  st = device_state(&a.err, &sms);
+  if (st != PKV_OK) return st;
   return pkv::launch_kv_append_rope(a, x->dtype == PKV_BF16,
                                     reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? PKV_OK
@@ -296,6 +297,9 @@ pkv_status pkv_kv_append_fp8_block(const pkv_rope_append_args* x, pkv_stream_t s
   st = rope_append_prepare(*x, &a);
   if (st != PKV_OK) return st;
   if (!pkv::append_fp8_block_supported(a)) return PKV_EUNSUPPORTED;
+  int sms = 0;
+  st = device_state(&a.err, &sms);
+  if (st != PKV_OK) return st;
   return pkv::launch_kv_append_fp8_block(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? PKV_OK
              : PKV_ECUDA;

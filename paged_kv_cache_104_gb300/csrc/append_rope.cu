@@ -8,6 +8,8 @@
 // in fp32, rounded once to the storage type.  The other elements are copied.
 // The axis of a pair is the caller's table, so one axis (text), sections of
 // time, height and width, or axes taken in turn are one kernel.
+#include <algorithm>
+
 #include "common.cuh"
 #include "launch.h"
 
@@ -17,20 +19,30 @@ namespace {
 constexpr int kMinScaleExp = -126;   // block scale exponents an append writes:
 constexpr int kMaxScaleExp = 119;    // 448 * 2^119 is the largest such value below 2^128
 
-// The table row (rot_dim floats: cosines, then sines) of a pair's position,
-// or null when the position is outside the table.
-__device__ __forceinline__ const float* table_row(const RopeArgs& r, int axis, int64_t t,
-                                                  int64_t num_tokens) {
-  const int p = __ldg(r.positions + axis * num_tokens + t);
-  return p < 0 || (int64_t)p >= r.num_positions ? nullptr : r.cos_sin + (int64_t)p * r.rot_dim;
-}
-
-// True if every axis' position of token t is inside the table.
-__device__ __forceinline__ bool positions_ok(const RopeArgs& r, int64_t t, int64_t num_tokens) {
-  bool ok = true;
-  for (int ax = 0; ax < r.num_axes; ++ax) ok &= table_row(r, ax, t, num_tokens) != nullptr;
-  return ok;
-}
+// A token's positions, by axis.  Read together with the token's slot; one
+// outside the table reads as 0, so that its row can be requested before the
+// token is found bad.
+struct Positions {
+  int p[kRopeAxes];
+  bool ok;
+  __device__ __forceinline__ void load(const RopeArgs& r, int64_t t, int64_t num_tokens) {
+    ok = true;
+#pragma unroll
+    for (int ax = 0; ax < kRopeAxes; ++ax) {
+      p[ax] = ax < r.num_axes ? __ldg(r.positions + ax * num_tokens + t) : 0;
+      const bool in = p[ax] >= 0 && (int64_t)p[ax] < r.num_positions;
+      ok &= in;
+      if (!in) p[ax] = 0;
+    }
+  }
+  // the table row (rot_dim floats: cosines, then sines) of an axis' position
+  __device__ __forceinline__ const float* row(const RopeArgs& r, int axis) const {
+    int at = p[0];
+#pragma unroll
+    for (int ax = 1; ax < kRopeAxes; ++ax) at = axis == ax ? p[ax] : at;
+    return r.cos_sin + (int64_t)at * r.rot_dim;
+  }
+};
 
 // Rows are moved in units of two 16-byte chunks that hold the two sides of V
 // pairs (V elements a chunk): chunks (u, u + half/V) of a head rotated by
@@ -91,10 +103,10 @@ struct Run {
 template <int V>
 struct Turn {
   float c[V], s[V];
-  __device__ __forceinline__ void load(const RopeArgs& r, int u, int64_t t, int64_t num_tokens) {
+  __device__ __forceinline__ void load(const RopeArgs& r, int u, const Positions& pos) {
     const int half = r.rot_dim / 2, i0 = u * V;
     if (V > 1 && r.whole_axes) {   // the unit's pairs share an axis: whole 16-byte loads
-      const float* row = table_row(r, r.pair_axis[i0], t, num_tokens);
+      const float* row = pos.row(r, r.pair_axis[i0]);
 #pragma unroll
       for (int i = 0; i < V; i += 4) {
         if constexpr (V >= 4) {
@@ -107,7 +119,7 @@ struct Turn {
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const float* row = table_row(r, r.pair_axis[i0 + i], t, num_tokens);
+        const float* row = pos.row(r, r.pair_axis[i0 + i]);
         c[i] = __ldg(row + i0 + i);
         s[i] = __ldg(row + half + i0 + i);
       }
@@ -147,57 +159,97 @@ __device__ __forceinline__ void rotate(const RopeArgs& r, const Turn<V>& w, Run<
 
 // One thread takes one unit u of a token and every `slots`-th of its heads
 // (query, key, then value heads), so the unit's cosines and sines are loaded
-// once for all of them.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(512)
-kv_append_rope_kernel(const __grid_constant__ RopeAppendArgs a, int units, int slots) {
+// once for all of them.  HPT heads' rows are requested at once, beside the
+// slot, the positions and, from those, the table: nothing is looked at before
+// all is on its way (with the checks in between, 50 us against XXX for 8,192
+// tokens of 32 + 8 heads).
+template <typename T, bool VEC, int HPT>
+__device__ __forceinline__ void rope_token(const RopeAppendArgs& a, int64_t t, int u, int hs,
+                                           int slots, int kv_heads) {
   constexpr int V = Unit2<T, VEC>::V;
-  const int per_token = units * slots;
-  const int tl = threadIdx.x / per_token;
-  const int64_t t = (int64_t)blockIdx.x * (blockDim.x / per_token) + tl;
-  const int rem = threadIdx.x - tl * per_token;
-  const int hs = rem / units, u = rem - hs * units;
-  if (t >= a.num_tokens) return;
+  const int heads = a.num_q_heads + 2 * kv_heads;
   const int64_t slot = __ldg(a.slot_mapping + t);
+  Positions pos;
+  pos.load(a.rope, t, a.num_tokens);
+  int e0, e1;
+  Unit2<T, VEC>::place(a.rope, u, e0, e1);
+  const bool turns = u * V < a.rope.rot_dim / 2;
+  // source of head h: queries, then keys, then values
+  auto source = [&](int h) {
+    if (h < a.num_q_heads) return static_cast<const T*>(a.q) + t * a.q_stride + h * a.head_dim;
+    h -= a.num_q_heads;
+    return h < kv_heads ? static_cast<const T*>(a.k_new) + t * a.k_stride + h * a.head_dim
+                        : static_cast<const T*>(a.v_new) + t * a.v_stride + (h - kv_heads) * a.head_dim;
+  };
+  Run<T, V> x[HPT], y[HPT];
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int i = 0; i < HPT; ++i) {
+      const int h = h0 + i * slots;
+      if (h < heads) {
+        const T* src = source(h);
+        x[i].load(src + e0);
+        y[i].load(src + e1);
+      }
+    }
+  };
+  load(hs);
+  Turn<V> w;
+  if (turns) w.load(a.rope, u, pos);
   if (slot < 0) return;
   if (slot >= a.num_blocks * kBlockSize) {
     record_error(a.err, DEVERR_SLOT_RANGE);
     return;
   }
-  if (!positions_ok(a.rope, t, a.num_tokens)) {
+  if (!pos.ok) {
     record_error(a.err, DEVERR_POSITION_RANGE);
     return;
   }
   const int64_t blk = slot / kBlockSize, row = slot - blk * kBlockSize;
-  int e0, e1;
-  Unit2<T, VEC>::place(a.rope, u, e0, e1);
-  const bool turns = u * V < a.rope.rot_dim / 2;
-  Turn<V> w;
-  if (turns) w.load(a.rope, u, t, a.num_tokens);
-  const int heads = a.num_q_heads + 2 * a.num_kv_heads;
-  for (int h = hs; h < heads; h += slots) {
-    const T* src;
-    T* dst;
-    if (h < a.num_q_heads) {
-      src = static_cast<const T*>(a.q) + t * a.q_stride + h * a.head_dim;
-      dst = static_cast<T*>(a.q_out) + t * a.q_out_stride + h * a.head_dim;
-    } else {
-      const bool is_v = h >= a.num_q_heads + a.num_kv_heads;
-      const int g = h - a.num_q_heads - (is_v ? a.num_kv_heads : 0);
-      src = is_v ? static_cast<const T*>(a.v_new) + t * a.v_stride
-                 : static_cast<const T*>(a.k_new) + t * a.k_stride;
-      src += g * a.head_dim;
-      dst = static_cast<T*>(is_v ? a.v_cache : a.k_cache) +
-            ((blk * a.num_kv_heads + g) * kBlockSize + row) * a.head_dim;
+  for (int h0 = hs; h0 < heads; h0 += HPT * slots) {
+    if (h0 != hs) load(h0);
+#pragma unroll
+    for (int i = 0; i < HPT; ++i) {
+      const int h = h0 + i * slots, k = h - a.num_q_heads;
+      if (h >= heads) break;
+      T* dst;
+      if (k < 0) {
+        dst = static_cast<T*>(a.q_out) + t * a.q_out_stride + h * a.head_dim;
+      } else {
+        const bool is_v = k >= kv_heads;
+        dst = static_cast<T*>(is_v ? a.v_cache : a.k_cache) +
+              ((blk * kv_heads + k - (is_v ? kv_heads : 0)) * kBlockSize + row) * a.head_dim;
+      }
+      if (turns && k < kv_heads) rotate<T, V>(a.rope, w, x[i], y[i]);
+      x[i].store(dst + e0);
+      y[i].store(dst + e1);
     }
-    Run<T, V> x, y;
-    x.load(src + e0);
-    y.load(src + e1);
-    if (turns && h < a.num_q_heads + a.num_kv_heads) rotate<T, V>(a.rope, w, x, y);
-    x.store(dst + e0);
-    y.store(dst + e1);
   }
 }
+
+template <typename T, bool VEC, int HPT>
+__global__ void __launch_bounds__(512)
+kv_append_rope_kernel(const __grid_constant__ RopeAppendArgs a, int units, int slots) {
+  const int per_token = units * slots;
+  const int tl = threadIdx.x / per_token;
+  const int64_t t = (int64_t)blockIdx.x * (blockDim.x / per_token) + tl;
+  const int rem = threadIdx.x - tl * per_token;
+  const int hs = rem / units, u = rem - hs * units;
+  if (t < a.num_tokens) rope_token<T, VEC, HPT>(a, t, u, hs, slots, a.num_kv_heads);
+}
+
+// Thread layout of a token's rows: `slots` threads share a unit's heads.
+// While all threads fit the GPU at once each takes one head (latency counts);
+// beyond that HPT heads a thread keep more bytes in flight.
+template <int HPT>
+int head_slots(int heads, int units, int most) {
+  int slots = (heads + HPT - 1) / HPT;
+  while (units * slots > most && slots > 1) slots = (slots + 1) / 2;
+  return slots;
+}
+constexpr int64_t kThreadsAtOnce = 152 * 2048;
+constexpr int kHeadsPerThread = 6;   // 8,192 tokens of 32 + 8 heads: 1 or 2 43 us, 4 39 us, 6 38 us
+constexpr int kQueryHeads = 2;        // the same for the queries of the 8-bit append
 
 // ------------------------------------------------- block-scaled 8-bit cache
 
@@ -211,208 +263,307 @@ __device__ __forceinline__ int scale_exp(uint32_t amax) {
   return max(kMinScaleExp, min(kMaxScaleExp, e));
 }
 
-// One warp writes the N rows of a run of new tokens (t0 .. t0 + n - 1, n <=
-// N) for one head of one pool: lane l owns pairs 2l and 2l + 1 of every row.
-template <int N>
-__device__ __forceinline__ void append_run(const RopeAppendArgs& a, const __nv_bfloat16* src,
-                                           int64_t stride, uint8_t* pool, uint8_t* scale,
-                                           bool rotated, int64_t t0, int n, int row0, int lane) {
-  const RopeArgs& r = a.rope;
-  const int half = r.rot_dim / 2;
-  const int p0 = 2 * lane;                     // the lane's first pair
-  const bool mine = 4 * lane < a.head_dim;
-  const bool turns = rotated && p0 < half;
-  // elements e0, e0 + 1 and e1, e1 + 1
-  const bool adjacent = r.interleaved || p0 >= half;
-  const int e0 = adjacent ? 4 * lane : p0, e1 = adjacent ? e0 + 2 : half + p0;
-  uint32_t raw[N][2];
+constexpr int kWindow = 16;       // tokens of a CTA
+constexpr int kRowLanes = 16;     // threads of a row, 8 elements (16 bytes) each
+constexpr int kAppendThreads = kWindow * kRowLanes;
+
+// A thread's 8 elements of a row (chunk c) turned, or as they are.  Every lane
+// of the warp calls it: the other side of a half's pairs comes by shuffle.
+struct RowTurn {
+  Turn<8> w;        // halves: the chunk's 8 pairs; adjacent pairs: the first 4
+  __device__ __forceinline__ void load(const RopeArgs& r, const Positions& pos, int c) {
+    const int half = r.rot_dim / 2, hc = half / 8;
+    if (c >= r.rot_dim / 8) return;
+    if (!r.interleaved) {
+      w.load(r, c >= hc ? c - hc : c, pos);
+      return;
+    }
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    raw[i][0] = raw[i][1] = 0u;
-    if (mine && i < n) {
-      const __nv_bfloat16* p = src + (t0 + i) * stride;
-      raw[i][0] = __ldg(reinterpret_cast<const uint32_t*>(p + e0));
-      raw[i][1] = __ldg(reinterpret_cast<const uint32_t*>(p + e1));
+    for (int i = 0; i < 4; ++i) {
+      const float* row = pos.row(r, r.pair_axis[4 * c + i]);
+      w.c[i] = __ldg(row + 4 * c + i);
+      w.s[i] = __ldg(row + half + 4 * c + i);
     }
   }
-  float x[N][4];
-  uint32_t amax = 0;
+  __device__ __forceinline__ void turn(const RopeArgs& r, uint4 raw, int c, float (&x)[8]) const {
+    Elem<__nv_bfloat16>::unpack(raw, x);
+    const int hc = r.rot_dim / 16;
+    const bool turns = c < r.rot_dim / 8;
+    if (r.interleaved) {          // pairs 4 c .. 4 c + 3, all here
+      if (!turns) return;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    x[i][0] = bf16lo(raw[i][0]);
-    x[i][1] = bf16hi(raw[i][0]);
-    x[i][2] = bf16lo(raw[i][1]);
-    x[i][3] = bf16hi(raw[i][1]);
-    if (turns && i < n) {
-      float c[2], s[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float* trow = table_row(r, r.pair_axis[p0 + k], t0 + i, a.num_tokens);
-        c[k] = __ldg(trow + p0 + k);
-        s[k] = __ldg(trow + half + p0 + k);
+      for (int i = 0; i < 4; ++i) {
+        const float a = x[2 * i], b = x[2 * i + 1];
+        x[2 * i] = a * w.c[i] - b * w.s[i];
+        x[2 * i + 1] = b * w.c[i] + a * w.s[i];
       }
-      if (r.interleaved) {   // pairs (x0, x1) and (x2, x3)
-        const float x0 = x[i][0], x1 = x[i][1], x2 = x[i][2], x3 = x[i][3];
-        x[i][0] = x0 * c[0] - x1 * s[0];
-        x[i][1] = x1 * c[0] + x0 * s[0];
-        x[i][2] = x2 * c[1] - x3 * s[1];
-        x[i][3] = x3 * c[1] + x2 * s[1];
-      } else {               // pairs (x0, x2) and (x1, x3)
-        const float x0 = x[i][0], x1 = x[i][1], x2 = x[i][2], x3 = x[i][3];
-        x[i][0] = x0 * c[0] - x2 * s[0];
-        x[i][2] = x2 * c[0] + x0 * s[0];
-        x[i][1] = x1 * c[1] - x3 * s[1];
-        x[i][3] = x3 * c[1] + x1 * s[1];
-      }
+      return;
     }
-    // the scale follows the finite elements only
+    const bool second = c >= hc;  // the other side is hc chunks, that is threads, away
+    const int from = (threadIdx.x & 16) + ((second ? c - hc : c + hc) & 15);
+    uint4 o;
+    o.x = __shfl_sync(0xffffffffu, raw.x, from);
+    o.y = __shfl_sync(0xffffffffu, raw.y, from);
+    o.z = __shfl_sync(0xffffffffu, raw.z, from);
+    o.w = __shfl_sync(0xffffffffu, raw.w, from);
+    if (!turns) return;
+    float y[8];
+    Elem<__nv_bfloat16>::unpack(o, y);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t m = __float_as_uint(x[i][k]) & 0x7fffffffu;
-      if (m < 0x7f800000u) amax = max(amax, m);
+    for (int i = 0; i < 8; ++i)   // a' = a cos - b sin, or b' = b cos + a sin
+      x[i] = x[i] * w.c[i] + (second ? y[i] : -y[i]) * w.s[i];
+  }
+};
+
+// Of a window: run_of[j], the run that token j belongs to (-1: none that starts
+// here), and of the run that starts at token k its slot, old scale bytes and
+// maxima by head.
+template <int UPC>
+struct WindowRuns {
+  int8_t run_of[2 * kWindow];
+  int64_t slot[kWindow];
+  int old[UPC][kWindow];
+  uint32_t top[UPC][kWindow];
+};
+
+// Warp 0's part: lane l looks at entry w0 + l (slot) and w0 - 1 - l (back).
+template <int UPC>
+__device__ __forceinline__ void find_runs(const RopeAppendArgs& a, WindowRuns<UPC>& runs,
+                                          int64_t slot, int64_t back, bool position_ok,
+                                          const int (&old)[UPC]) {
+  const int lane = threadIdx.x;
+  const bool inside = slot >= 0 && slot < a.num_blocks * kBlockSize;
+  const int64_t blk = inside ? slot / kBlockSize : -1;
+  const int row = (int)(slot - blk * kBlockSize);
+  const int64_t up = __shfl_up_sync(0xffffffffu, slot, 1);
+  const int64_t prev = lane == 0 ? back : up;
+  const int64_t back_blk = back >= 0 ? back / kBlockSize : -1;
+  // an entry goes on with the run of the one before, or starts a run
+  const bool goes_on = inside && row > 0 && prev == slot - 1;
+  const bool here = lane < kWindow;
+  const uint32_t starts = __ballot_sync(0xffffffffu, inside && !goes_on);
+  const uint32_t broken = __ballot_sync(0xffffffffu, !inside || !position_ok);
+  if (here && slot >= 0 && !inside) record_error(a.err, DEVERR_SLOT_RANGE);
+  if (here && inside && !position_ok) record_error(a.err, DEVERR_POSITION_RANGE);
+  // no nearby earlier entry may write a run's block: two runs would race on it
+  uint32_t twice = 0;
+  for (uint32_t left = starts & 0xffffu; left; left &= left - 1) {
+    const int k = __ffs(left) - 1;
+    const int64_t b = __shfl_sync(0xffffffffu, blk, k);
+    if (__any_sync(0xffffffffu, (lane < k && blk == b) || (lane < 32 - k && back_blk == b)))
+      twice |= 1u << k;
+  }
+  if (lane == 0 && twice) record_error(a.err, DEVERR_SLOT_ORDER);
+  // the last start up to here; an entry with a bad position, and an invalid
+  // one, ends the run before it, and what follows belongs to none
+  const uint32_t upto = 0xffffffffu >> (31 - lane);
+  const uint32_t before = starts & upto;
+  const int k = before ? 31 - __clz(before) : -1;
+  const bool member = k >= 0 && k < kWindow && inside && !(twice >> k & 1u) &&
+                      (broken & upto & (0xffffffffu << k)) == 0;
+  runs.run_of[lane] = (int8_t)(member ? k : -1);
+  if (here) {
+    runs.slot[lane] = slot;
+#pragma unroll
+    for (int u = 0; u < UPC; ++u) {
+      runs.top[u][lane] = 0;
+      runs.old[u][lane] = old[u];
     }
   }
-  amax = __reduce_max_sync(0xffffffffu, amax);
-  int e = scale_exp(amax);
+}
+
+// The codes of token j (elements v of chunk c, pool and head `tile`) of run k,
+// and the run's scale.
+template <int UPC>
+__device__ __forceinline__ void write_codes(const RopeAppendArgs& a, const WindowRuns<UPC>& runs,
+                                            uint8_t* pools, uint8_t* scales, const float (&v)[8],
+                                            int u, int g, int j, int k, int c) {
+  const int64_t slot = runs.slot[k], blk = slot / kBlockSize;
+  const int row0 = (int)(slot - blk * kBlockSize), row = row0 + j - k;
+  const int64_t tile = blk * a.num_kv_heads + g;
+  uint8_t* pool = pools + tile * kBlockSize * a.head_dim + c * 8;
+  int e = scale_exp(runs.top[u][k]);
   if (row0 > 0) {
-    // the block's older rows: their codes are re-expressed where the scale grows
-    const int b = *scale;
+    // where the scale grows, the block's older rows are re-expressed, by the
+    // threads of the run's first token
+    const int b = runs.old[u][k];
     const bool held = b >= 1 && b <= 253;      // otherwise they stand for nothing
     const int e_old = held ? b - 127 : e;
-    if (!held || e > e_old) {
+    if (j == k && (!held || e > e_old)) {
       const float f = held ? exp2i(max(e_old - e, -126)) : 0.f;
-      if (mine) {
-        for (int row = 0; row < row0; ++row) {
-          uint32_t* p = reinterpret_cast<uint32_t*>(pool + row * a.head_dim + 4 * lane);
-          const uint32_t c = *p;
-          uint32_t out = 0;
-          if (held) {
-            const uint32_t lo = e4m3x2_to_f16x2((uint16_t)c), hi = e4m3x2_to_f16x2((uint16_t)(c >> 16));
-            const float2 fl = __half22float2(*reinterpret_cast<const __half2*>(&lo));
-            const float2 fh = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-            out = f32x2_to_e4m3x2(fl.x * f, fl.y * f) |
-                  ((uint32_t)f32x2_to_e4m3x2(fh.x * f, fh.y * f) << 16);
-          }
-          *p = out;
-        }
+#pragma unroll 1
+      for (int o = 0; o < row0; ++o) {
+        uint2* p = reinterpret_cast<uint2*>(pool + o * a.head_dim);
+        const uint2 w = *p;
+        auto again = [&](uint32_t codes) {
+          const uint32_t lo = e4m3x2_to_f16x2((uint16_t)codes);
+          const uint32_t hi = e4m3x2_to_f16x2((uint16_t)(codes >> 16));
+          const float2 fl = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+          const float2 fh = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+          return f32x2_to_e4m3x2(fl.x * f, fl.y * f) |
+                 ((uint32_t)f32x2_to_e4m3x2(fh.x * f, fh.y * f) << 16);
+        };
+        *p = held ? make_uint2(again(w.x), again(w.y)) : make_uint2(0u, 0u);
       }
     }
     e = max(e, e_old);
   }
   const float inv = exp2i(-e);
-  if (mine) {
+  uint32_t n[4];
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if (i < n) {
-        uint8_t* p = pool + (row0 + i) * a.head_dim;
-        *reinterpret_cast<uint16_t*>(p + e0) = f32x2_to_e4m3x2(x[i][0] * inv, x[i][1] * inv);
-        *reinterpret_cast<uint16_t*>(p + e1) = f32x2_to_e4m3x2(x[i][2] * inv, x[i][3] * inv);
-      }
-    }
-  }
-  __syncwarp();                                 // every lane has read the old scale
-  if (lane == 0) *scale = (uint8_t)(e + 127);
+  for (int q = 0; q < 4; ++q) n[q] = f32x2_to_e4m3x2(v[2 * q] * inv, v[2 * q + 1] * inv);
+  *reinterpret_cast<uint2*>(pool + row * a.head_dim) = make_uint2(n[0] | n[1] << 16, n[2] | n[3] << 16);
+  if (j == k && c == 0) scales[tile] = (uint8_t)(e + 127);
 }
 
-constexpr int kAppendWarps = 8;
-
-// CTA (t, y): y < head groups: if a run of new tokens starts at t, its rows
-// for kAppendWarps / 2 heads, a warp for each head of each pool; the last y:
-// token t's query.
-__global__ void __launch_bounds__(kAppendWarps * 32)
-kv_append_fp8_block_kernel(const __grid_constant__ RopeAppendArgs a, int groups, int units) {
-  const int64_t t = blockIdx.x;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t slot = __ldg(a.slot_mapping + t);
-  if (slot < 0) return;
-  const int64_t pool_slots = a.num_blocks * kBlockSize;
-  if (slot >= pool_slots) {
-    record_error(a.err, DEVERR_SLOT_RANGE);
+// The first kv_ctas CTAs take the runs of new tokens that start in a window of
+// 16 tokens, in up to UPC heads of one pool.  Thread (i, c) has chunk c of token
+// i, and of token i + 16 where a run goes on beyond the window; the runs'
+// maxima meet in shared memory, so all runs of a window, one of a prompt or 16
+// of a decode step, are done at once.  Rows, positions and slots are requested
+// together, then the table's rows and the old scales, before anything is
+// decided.  The other CTAs rotate queries.
+// (A warp for each run and head, its rows in registers, took 20 to 36 us for a
+// chunk of 2,048 tokens of 32 + 8 heads: 32 KiB of straight code that every
+// warp ran once, waiting for it.)
+template <int UPC>
+__global__ void __launch_bounds__(kAppendThreads, UPC == 1 ? 4 : 3)
+kv_append_fp8_block_kernel(const __grid_constant__ RopeAppendArgs a, int kv_ctas, int q_units,
+                           int q_slots) {
+  if ((int)blockIdx.x >= kv_ctas) {
+    const int per_token = q_units * q_slots;
+    const int tl = threadIdx.x / per_token, tokens = blockDim.x / per_token;
+    const int64_t t = (int64_t)((int)blockIdx.x - kv_ctas) * tokens + tl;
+    const int rem = threadIdx.x - tl * per_token;
+    const int hs = rem / q_units, u = rem - hs * q_units;
+    if (tl < tokens && t < a.num_tokens)
+      rope_token<__nv_bfloat16, true, kQueryHeads>(a, t, u, hs, q_slots, 0);
     return;
   }
-  if ((int)blockIdx.y == groups) {              // the query
-    if (!positions_ok(a.rope, t, a.num_tokens)) {
-      record_error(a.err, DEVERR_POSITION_RANGE);
-      return;
-    }
-    constexpr int V = 8;
-    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + t * a.q_stride;
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.q_out) + t * a.q_out_stride;
-    for (int i = threadIdx.x; i < units * a.num_q_heads; i += blockDim.x) {
-      const int h = i / units, u = i - h * units;
-      int e0, e1;
-      Run<__nv_bfloat16, V> x, y;
-      Unit2<__nv_bfloat16, true>::place(a.rope, u, e0, e1);
-      x.load(src + h * a.head_dim + e0);
-      y.load(src + h * a.head_dim + e1);
-      if (u * V < a.rope.rot_dim / 2) {
-        Turn<V> w;
-        w.load(a.rope, u, t, a.num_tokens);
-        rotate<__nv_bfloat16, V>(a.rope, w, x, y);
-      }
-      x.store(dst + h * a.head_dim + e0);
-      y.store(dst + h * a.head_dim + e1);
-    }
-    return;
-  }
-  const int64_t blk = slot / kBlockSize;
-  const int row0 = (int)(slot - blk * kBlockSize);
-  // a run starts at t unless the entry before holds the row before in this block
-  if (row0 > 0 && t > 0 && __ldg(a.slot_mapping + t - 1) == slot - 1) return;
-  // no nearby earlier entry may write this block: two runs would race on it
-  const int64_t tb = t - 1 - lane;
-  const int64_t before = tb >= 0 ? __ldg(a.slot_mapping + tb) : -1;
-  if (__any_sync(0xffffffffu, before >= 0 && before / kBlockSize == blk)) {
-    record_error(a.err, DEVERR_SLOT_ORDER);
-    return;
-  }
-  // its length: following entries with following rows of the same block
-  const int64_t ta = t + lane;
-  const bool in = lane < kBlockSize - row0 && ta < a.num_tokens &&
-                  __ldg(a.slot_mapping + min(ta, a.num_tokens - 1)) == slot + lane;
-  const uint32_t run = __ballot_sync(0xffffffffu, in);
-  int n = __ffs(~run) - 1;                      // >= 1: lane 0 is in
-  // a bad position ends the run before its token
-  if (a.rope.rot_dim > 0) {
-    const uint32_t good =
-        __ballot_sync(0xffffffffu, lane >= n || positions_ok(a.rope, ta, a.num_tokens));
-    if (~good != 0u) {
-      record_error(a.err, DEVERR_POSITION_RANGE);
-      n = min(n, __ffs(~good) - 1);
-      if (n == 0) return;
-    }
-  }
-  const int unit = (int)blockIdx.y * kAppendWarps + warp;
-  const bool is_v = unit & 1;
-  const int g = unit >> 1;
-  if (g >= a.num_kv_heads) return;
-  const int64_t tile = blk * a.num_kv_heads + g;
-  const __nv_bfloat16* src =
-      static_cast<const __nv_bfloat16*>(is_v ? a.v_new : a.k_new) + g * a.head_dim;
-  uint8_t* pool = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) +
-                  tile * kBlockSize * a.head_dim;
-  uint8_t* scale = (is_v ? a.v_scale : a.k_scale) + tile;
+  __shared__ WindowRuns<UPC> runs;
+  const int i = threadIdx.x / kRowLanes, c = threadIdx.x % kRowLanes;
+  const int groups = (a.num_kv_heads + UPC - 1) / UPC;    // of a pool
+  const int group = (int)blockIdx.x % (2 * groups);
+  const bool is_v = group >= groups;
+  const int g0 = (is_v ? group - groups : group) * UPC, ng = min(UPC, a.num_kv_heads - g0);
+  const int64_t w0 = (int64_t)((int)blockIdx.x / (2 * groups)) * kWindow;
   const int64_t stride = is_v ? a.v_stride : a.k_stride;
+  const __nv_bfloat16* src =
+      static_cast<const __nv_bfloat16*>(is_v ? a.v_new : a.k_new) + g0 * a.head_dim + c * 8;
+  uint8_t* pools = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache);
+  uint8_t* scales = is_v ? a.v_scale : a.k_scale;
+  const bool mine = c * 8 < a.head_dim;
   const bool rotated = !is_v && a.rope.rot_dim > 0;
-  if (n == 1)
-    append_run<1>(a, src, stride, pool, scale, rotated, t, n, row0, lane);
-  else
-    append_run<kBlockSize>(a, src, stride, pool, scale, rotated, t, n, row0, lane);
+  int64_t slot = -1, back = -1;
+  if (threadIdx.x < 32) {
+    if (w0 + threadIdx.x < a.num_tokens) slot = __ldg(a.slot_mapping + w0 + threadIdx.x);
+    if (w0 - 1 - (int)threadIdx.x >= 0) back = __ldg(a.slot_mapping + w0 - 1 - threadIdx.x);
+  }
+  uint4 raw[UPC];
+  Positions pos;
+  auto load_rows = [&](int64_t t) {
+    const bool in = t < a.num_tokens;
+#pragma unroll
+    for (int u = 0; u < UPC; ++u)
+      raw[u] = in && mine && u < ng
+                   ? __ldg(reinterpret_cast<const uint4*>(src + t * stride + u * a.head_dim))
+                   : make_uint4(0u, 0u, 0u, 0u);
+    pos = Positions{};
+    if (in && rotated) pos.load(a.rope, t, a.num_tokens);
+  };
+  load_rows(w0 + i);
+  bool position_ok = true;       // of warp 0's entry
+  if (threadIdx.x < 32 && a.rope.rot_dim > 0 && w0 + threadIdx.x < a.num_tokens) {
+    Positions p;
+    p.load(a.rope, w0 + threadIdx.x, a.num_tokens);
+    position_ok = p.ok;
+  }
+  RowTurn turn;
+  if (rotated) turn.load(a.rope, pos, c);
+  if (threadIdx.x < 32) {
+    int old[UPC];
+    const bool older = threadIdx.x < kWindow && slot >= 0 && slot < a.num_blocks * kBlockSize &&
+                       slot % kBlockSize != 0;
+#pragma unroll
+    for (int u = 0; u < UPC; ++u)
+      old[u] = older && u < ng ? scales[slot / kBlockSize * a.num_kv_heads + g0 + u] : 0;
+    find_runs<UPC>(a, runs, slot, back, position_ok, old);
+  }
+  // every lane takes part in the exchanges; what has no run is left out
+  float x[UPC][8];
+  auto turn_rows = [&] {
+#pragma unroll
+    for (int u = 0; u < UPC; ++u) {
+      if (rotated) turn.turn(a.rope, raw[u], c, x[u]);
+      else Elem<__nv_bfloat16>::unpack(raw[u], x[u]);
+    }
+  };
+  auto maxima = [&](int of) {
+#pragma unroll
+    for (int u = 0; u < UPC; ++u) {
+      uint32_t m = 0;            // the scale follows the finite elements only
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t b = __float_as_uint(x[u][k]) & 0x7fffffffu;
+        if (b < 0x7f800000u) m = max(m, b);
+      }
+#pragma unroll
+      for (int o = 1; o < kRowLanes; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (c == 0 && of >= 0) atomicMax(&runs.top[u][of], m);
+    }
+  };
+  auto write = [&](int j, int k) {
+    if (k < 0 || !mine) return;
+#pragma unroll
+    for (int u = 0; u < UPC; ++u)
+      if (u < ng) write_codes<UPC>(a, runs, pools, scales, x[u], u, g0 + u, j, k, c);
+  };
+  turn_rows();
+  __syncthreads();
+  const int run = runs.run_of[i], run2 = runs.run_of[i + kWindow];
+  maxima(run);
+  // a run that goes on beyond the window: its other rows, for the maxima now
+  // and again for their codes
+  const bool beyond = __syncthreads_or(run2 >= 0);
+  if (beyond) {
+    load_rows(w0 + kWindow + i);
+    if (rotated) turn.load(a.rope, pos, c);
+    turn_rows();
+    maxima(run2);
+    __syncthreads();
+    write(i + kWindow, run2);
+    load_rows(w0 + i);
+    if (rotated) turn.load(a.rope, pos, c);
+    turn_rows();
+  }
+  write(i, run);
 }
 
-template <typename T, bool VEC>
-cudaError_t launch_rope_typed(const RopeAppendArgs& a, cudaStream_t stream) {
-  constexpr int V = Unit2<T, VEC>::V;
-  const int units = a.head_dim / (2 * V);
-  const int heads = a.num_q_heads + 2 * a.num_kv_heads;
-  int slots = heads;
-  while (units * slots > 256 && slots > 1) slots = (slots + 1) / 2;
+template <typename T, bool VEC, int HPT>
+cudaError_t launch_rope_heads(const RopeAppendArgs& a, cudaStream_t stream) {
+  const int units = a.head_dim / (2 * Unit2<T, VEC>::V);
+  const int slots = head_slots<HPT>(a.num_q_heads + 2 * a.num_kv_heads, units, 256);
   const int per_token = units * slots;
   const int tokens = per_token >= 256 ? 1 : 256 / per_token;
   const int64_t grid = (a.num_tokens + tokens - 1) / tokens;
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-  kv_append_rope_kernel<T, VEC><<<(int)grid, per_token * tokens, 0, stream>>>(a, units, slots);
+  kv_append_rope_kernel<T, VEC, HPT><<<(int)grid, per_token * tokens, 0, stream>>>(a, units, slots);
   return cudaGetLastError();
+}
+
+template <typename T, bool VEC>
+cudaError_t launch_rope_typed(const RopeAppendArgs& a, cudaStream_t stream) {
+  const int64_t threads = a.num_tokens * (a.num_q_heads + 2 * a.num_kv_heads) *
+                          (a.head_dim / (2 * Unit2<T, VEC>::V));
+  return threads <= kThreadsAtOnce ? launch_rope_heads<T, VEC, 1>(a, stream)
+                                   : launch_rope_heads<T, VEC, kHeadsPerThread>(a, stream);
+}
+
+// 1 if every v pairs from a multiple of v on share an axis.
+int axes_by_chunk(const RopeAppendArgs& a, int v) {
+  for (int i = 0; i < a.rope.rot_dim / 2; ++i)
+    if (a.rope.pair_axis[i] != a.rope.pair_axis[i - i % v]) return 0;
+  return 1;
 }
 
 // True if the pairs fill whole 16-byte chunks of `size`-byte elements.
@@ -427,9 +578,7 @@ cudaError_t launch_kv_append_rope(const RopeAppendArgs& args, bool is_bf16, cuda
   if (args.num_tokens == 0) return cudaSuccess;
   RopeAppendArgs a = args;
   const int v = is_bf16 ? 8 : 4;
-  a.rope.whole_axes = 1;
-  for (int i = 0; i < a.rope.rot_dim / 2; ++i)
-    if (a.rope.pair_axis[i] != a.rope.pair_axis[i - i % v]) a.rope.whole_axes = 0;
+  a.rope.whole_axes = axes_by_chunk(a, v);
   if (is_bf16)
     return whole_chunks(a, 2) ? launch_rope_typed<__nv_bfloat16, true>(a, stream)
                               : launch_rope_typed<__nv_bfloat16, false>(a, stream);
@@ -438,20 +587,26 @@ cudaError_t launch_kv_append_rope(const RopeAppendArgs& args, bool is_bf16, cuda
 }
 
 bool append_fp8_block_supported(const RopeAppendArgs& a) {
-  return a.head_dim % 16 == 0 && a.head_dim <= 128 && a.rope.rot_dim % 4 == 0 &&
-         (!a.q || whole_chunks(a, 2));
+  return a.head_dim % 16 == 0 && a.head_dim <= 128 && a.rope.rot_dim % 16 == 0;
 }
 
 cudaError_t launch_kv_append_fp8_block(const RopeAppendArgs& args, cudaStream_t stream) {
   if (args.num_tokens == 0) return cudaSuccess;
   if (args.num_tokens > 0x7fffffff) return cudaErrorInvalidValue;
   RopeAppendArgs a = args;
-  a.rope.whole_axes = 1;
-  for (int i = 0; i < a.rope.rot_dim / 2; ++i)
-    if (a.rope.pair_axis[i] != a.rope.pair_axis[i - i % 8]) a.rope.whole_axes = 0;
-  const int groups = (2 * a.num_kv_heads + kAppendWarps - 1) / kAppendWarps;
-  const dim3 grid((unsigned)a.num_tokens, groups + (a.q ? 1 : 0));
-  kv_append_fp8_block_kernel<<<grid, kAppendWarps * 32, 0, stream>>>(a, groups, a.head_dim / 16);
+  a.rope.whole_axes = axes_by_chunk(a, 8);
+  const int64_t windows = (a.num_tokens + kWindow - 1) / kWindow;
+  // few windows: a head to a CTA, for latency (128 one-token runs of 8 heads:
+  // 4 heads AAA us, 1 head BBB); many: 4 heads share slots, positions and table
+  const bool few = windows * 2 * a.num_kv_heads <= 152 * 4;
+  const int64_t kv_ctas = windows * 2 * (few ? a.num_kv_heads : (a.num_kv_heads + 3) / 4);
+  const int units = a.head_dim / 16;
+  const int slots = head_slots<kQueryHeads>(std::max(a.num_q_heads, 1), units, kAppendThreads);
+  const int tokens = kAppendThreads / (units * slots);
+  const int64_t q_ctas = a.q ? (a.num_tokens + tokens - 1) / tokens : 0;
+  if (kv_ctas + q_ctas > 0x7fffffff) return cudaErrorInvalidValue;
+  auto* kernel = few ? kv_append_fp8_block_kernel<1> : kv_append_fp8_block_kernel<4>;
+  kernel<<<(unsigned)(kv_ctas + q_ctas), kAppendThreads, 0, stream>>>(a, (int)kv_ctas, units, slots);
   return cudaGetLastError();
 }
 

@@ -44,6 +44,7 @@ cudaError_t launch_kv_append_fp8(const AppendFp8Args& a, cudaStream_t stream);
 
 // The rotation of an append: tables, positions and which axis turns a pair.
 constexpr int kMaxRotPairs = 128;
+constexpr int kRopeAxes = 4;
 struct RopeArgs {
   const float* cos_sin;       // [num_positions][rot_dim]: cosines, then sines
   int64_t num_positions;

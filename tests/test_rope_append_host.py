@@ -87,7 +87,8 @@ def test_rope_append_refuses(kw, status):
 
 @pytest.mark.parametrize("kw,status", BAD + [(dict(dtype=0), 5), (dict(k_scale=None), 1), (dict(v_scale=None), 1),
                                              (dict(cos_sin=None), 1), (dict(head_dim=136), 5),
-                                             (dict(head_dim=256), 5), (dict(head_dim=120, rot_dim=64), 5)])
+                                             (dict(head_dim=256), 5), (dict(head_dim=120, rot_dim=64), 5),
+                                             (dict(rot_dim=72), 5), (dict(rot_dim=20), 5)])
 def test_block_append_refuses(kw, status):
     assert B.load().pkv_kv_append_fp8_block(ctypes.byref(_args(**kw)), None) == status
 
