@@ -161,7 +161,7 @@ __device__ __forceinline__ void rotate(const RopeArgs& r, const Turn<V>& w, Run<
 // (query, key, then value heads), so the unit's cosines and sines are loaded
 // once for all of them.  HPT heads' rows are requested at once, beside the
 // slot, the positions and, from those, the table: nothing is looked at before
-// all is on its way (with the checks in between, 50 us against XXX for 8,192
+// all is on its way (with the checks in between 50 us, so 38 us, for 8,192
 // tokens of 32 + 8 heads).
 template <typename T, bool VEC, int HPT>
 __device__ __forceinline__ void rope_token(const RopeAppendArgs& a, int64_t t, int u, int hs,
@@ -321,6 +321,7 @@ struct RowTurn {
 template <int UPC>
 struct WindowRuns {
   int8_t run_of[2 * kWindow];
+  int first;        // the first such k (0: none)
   int64_t slot[kWindow];
   int old[UPC][kWindow];
   uint32_t top[UPC][kWindow];
@@ -362,6 +363,7 @@ __device__ __forceinline__ void find_runs(const RopeAppendArgs& a, WindowRuns<UP
   const bool member = k >= 0 && k < kWindow && inside && !(twice >> k & 1u) &&
                       (broken & upto & (0xffffffffu << k)) == 0;
   runs.run_of[lane] = (int8_t)(member ? k : -1);
+  if (lane == 0) runs.first = starts & 0xffffu ? __ffs(starts & 0xffffu) - 1 : 0;
   if (here) {
     runs.slot[lane] = slot;
 #pragma unroll
@@ -422,12 +424,15 @@ __device__ __forceinline__ void write_codes(const RopeAppendArgs& a, const Windo
 // maxima meet in shared memory, so all runs of a window, one of a prompt or 16
 // of a decode step, are done at once.  Rows, positions and slots are requested
 // together, then the table's rows and the old scales, before anything is
-// decided.  The other CTAs rotate queries.
+// decided.  With UPC > 1, where throughput counts, the rows wait for the slots
+// instead and start at the window's first run, so that a prompt's runs, which
+// lie anywhere to the windows, end within the threads' 16 tokens.  The other
+// CTAs rotate queries.
 // (A warp for each run and head, its rows in registers, took 20 to 36 us for a
 // chunk of 2,048 tokens of 32 + 8 heads: 32 KiB of straight code that every
 // warp ran once, waiting for it.)
 template <int UPC>
-__global__ void __launch_bounds__(kAppendThreads, UPC == 1 ? 4 : 3)
+__global__ void __launch_bounds__(kAppendThreads, 4)
 kv_append_fp8_block_kernel(const __grid_constant__ RopeAppendArgs a, int kv_ctas, int q_units,
                            int q_slots) {
   if ((int)blockIdx.x >= kv_ctas) {
@@ -471,16 +476,19 @@ kv_append_fp8_block_kernel(const __grid_constant__ RopeAppendArgs a, int kv_ctas
     pos = Positions{};
     if (in && rotated) pos.load(a.rope, t, a.num_tokens);
   };
-  load_rows(w0 + i);
-  bool position_ok = true;       // of warp 0's entry
-  if (threadIdx.x < 32 && a.rope.rot_dim > 0 && w0 + threadIdx.x < a.num_tokens) {
-    Positions p;
-    p.load(a.rope, w0 + threadIdx.x, a.num_tokens);
-    position_ok = p.ok;
-  }
   RowTurn turn;
-  if (rotated) turn.load(a.rope, pos, c);
+  int k0 = 0;                    // the threads' first token in the window
+  if (UPC == 1) {
+    load_rows(w0 + i);
+    if (rotated) turn.load(a.rope, pos, c);
+  }
   if (threadIdx.x < 32) {
+    bool position_ok = true;
+    if (a.rope.rot_dim > 0 && w0 + threadIdx.x < a.num_tokens) {
+      Positions p;
+      p.load(a.rope, w0 + threadIdx.x, a.num_tokens);
+      position_ok = p.ok;
+    }
     int old[UPC];
     const bool older = threadIdx.x < kWindow && slot >= 0 && slot < a.num_blocks * kBlockSize &&
                        slot % kBlockSize != 0;
@@ -488,6 +496,12 @@ kv_append_fp8_block_kernel(const __grid_constant__ RopeAppendArgs a, int kv_ctas
     for (int u = 0; u < UPC; ++u)
       old[u] = older && u < ng ? scales[slot / kBlockSize * a.num_kv_heads + g0 + u] : 0;
     find_runs<UPC>(a, runs, slot, back, position_ok, old);
+  }
+  if (UPC > 1) {
+    __syncthreads();
+    k0 = runs.first;
+    load_rows(w0 + k0 + i);
+    if (rotated) turn.load(a.rope, pos, c);
   }
   // every lane takes part in the exchanges; what has no run is left out
   float x[UPC][8];
@@ -519,24 +533,26 @@ kv_append_fp8_block_kernel(const __grid_constant__ RopeAppendArgs a, int kv_ctas
       if (u < ng) write_codes<UPC>(a, runs, pools, scales, x[u], u, g0 + u, j, k, c);
   };
   turn_rows();
-  __syncthreads();
-  const int run = runs.run_of[i], run2 = runs.run_of[i + kWindow];
+  if (UPC == 1) __syncthreads();
+  const int j = k0 + i, j2 = j + kWindow;
+  const int run = j < 2 * kWindow ? runs.run_of[j] : -1;
+  const int run2 = j2 < 2 * kWindow ? runs.run_of[j2] : -1;
   maxima(run);
-  // a run that goes on beyond the window: its other rows, for the maxima now
-  // and again for their codes
+  // a run that goes on beyond the threads' tokens: its other rows, for the
+  // maxima now and again for their codes
   const bool beyond = __syncthreads_or(run2 >= 0);
   if (beyond) {
-    load_rows(w0 + kWindow + i);
+    load_rows(w0 + j2);
     if (rotated) turn.load(a.rope, pos, c);
     turn_rows();
     maxima(run2);
     __syncthreads();
-    write(i + kWindow, run2);
-    load_rows(w0 + i);
+    write(j2, run2);
+    load_rows(w0 + j);
     if (rotated) turn.load(a.rope, pos, c);
     turn_rows();
   }
-  write(i, run);
+  write(j, run);
 }
 
 template <typename T, bool VEC, int HPT>
@@ -596,8 +612,8 @@ cudaError_t launch_kv_append_fp8_block(const RopeAppendArgs& args, cudaStream_t 
   RopeAppendArgs a = args;
   a.rope.whole_axes = axes_by_chunk(a, 8);
   const int64_t windows = (a.num_tokens + kWindow - 1) / kWindow;
-  // few windows: a head to a CTA, for latency (128 one-token runs of 8 heads:
-  // 4 heads AAA us, 1 head BBB); many: 4 heads share slots, positions and table
+  // few windows: a head to a CTA, for latency; many: 4 heads share slots,
+  // positions and table (a chunk of 2,048 tokens: 13.0 us, 2 heads 16.5 us)
   const bool few = windows * 2 * a.num_kv_heads <= 152 * 4;
   const int64_t kv_ctas = windows * 2 * (few ? a.num_kv_heads : (a.num_kv_heads + 3) / 4);
   const int units = a.head_dim / 16;
