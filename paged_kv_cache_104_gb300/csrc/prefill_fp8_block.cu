@@ -53,7 +53,7 @@
 // loads left out 141 us: bound by their latency at 32 KiB in flight).
 //
 // Splitting the keys.  Where the work items are fewer than the SMs, a cluster
-// of 2, 4 or 8 CTAs shares an item's key tiles.  At the end every CTA reads the
+// of 2 to 8 CTAs shares an item's key tiles.  At the end every CTA reads the
 // others' (M, l) rows through distributed shared memory, scales its O to the
 // common maximum, and sends each CTA its share of the columns, which adds them
 // up and writes them.
@@ -119,7 +119,8 @@ constexpr float kLazy = 8.0f;
 
 static_assert(NSV * kTile16 == 2 * BM * HD * 2, "the bf16 queries fit the V ring");
 static_assert(SMEM_BYTES <= 227 * 1024, "one CTA per SM");
-static_assert(2 * BM * HD * 4 <= OFF_SCALES, "the merge's columns lie in the tiles' place");
+// 7 CTAs of W = 32 columns are the most
+static_assert(7 * 2 * BM * 32 * 4 <= OFF_SCALES, "the merge's columns lie in the tiles' place");
 
 enum {
   B_Q = 0,
@@ -618,52 +619,61 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
     const int q0 = hh ? qrow1 : qrow0, head = hh ? head1 : head0;
     const int row_pos = a.prior_len + q0 + r;
     float q_up = 1.f;                       // what brings products back to the query's size
+    const bool queries = q0 + (r & ~31) < a.chunk_len;   // the warp has rows of the chunk
     if (n_tiles > 0 && wait_fast(bar(B_Q), 0, abort_flag, a.err)) {
-      // this row's query becomes its hi and lo rows
-      const uint32_t src = sbase + OFF_V + hh * kTile16 + r * 128;
-      const uint32_t dst = sbase + OFF_Q + hh * kTile16 + r * 128;
-      auto piece = [&](int i) {             // elements 8 i .. 8 i + 7
-        return lds16(src + (i >> 3) * kHalf16 + (((i & 7) ^ (r & 7)) << 4));
-      };
-      uint32_t top = 0;
+      if (queries) {
+        // this row's query becomes its hi and lo rows
+        const uint32_t src = sbase + OFF_V + hh * kTile16 + r * 128;
+        const uint32_t dst = sbase + OFF_Q + hh * kTile16 + r * 128;
+        auto piece = [&](int i) {             // elements 8 i .. 8 i + 7
+          return lds16(src + (i >> 3) * kHalf16 + (((i & 7) ^ (r & 7)) << 4));
+        };
+        uint32_t top = 0;
 #pragma unroll 8
-      for (int i = 0; i < 16; ++i) {
-        const uint4 x = piece(i);
-        top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
-                                     __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
-      }
-      // 2^(7 - exponent of the row's largest element), of zeros and of
-      // infinities or NaN 1
-      top = max(top & 0xffffu, top >> 16) >> 7;
-      const int ex = top == 255 ? 7 : max(-119, min((int)top - 127, 126));
-      const float down = __uint_as_float((uint32_t)(127 + 7 - ex) << 23);
-      q_up = __uint_as_float((uint32_t)(127 + ex - 7) << 23);
-      // an infinite or NaN element makes the row's scores NaN
-      const uint32_t bad = top == 255 ? 0x7f7f7f7fu : 0u;
-#pragma unroll 4
-      for (int i = 0; i < 8; ++i) {         // 16 elements: a chunk of hi and one of lo
-        const uint4 x = piece(2 * i), y = piece(2 * i + 1);
-        const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t h2[2], l2[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            // f16 holds the scaled element exactly, or to 2^-25
-            const __half2 u = __floats2half2_rn(bf16lo(w[2 * k + e]) * down,
-                                                bf16hi(w[2 * k + e]) * down);
-            h2[e] = f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&u));
-            const uint32_t back = e4m3x2_to_f16x2((uint16_t)h2[e]);
-            const __half2 d = __hsub2(u, *reinterpret_cast<const __half2*>(&back));
-            l2[e] = f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&d));
-          }
-          hi[k] = (h2[0] | h2[1] << 16) | bad;
-          lo[k] = l2[0] | l2[1] << 16;
+        for (int i = 0; i < 16; ++i) {
+          const uint4 x = piece(i);
+          top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                       __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
         }
-        const uint32_t at = dst + ((i ^ (r & 7)) << 4);
-        sts16(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-        sts16(at + kTile8, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+        // 2^(7 - exponent of the row's largest element), of zeros and of
+        // infinities or NaN 1
+        top = max(top & 0xffffu, top >> 16) >> 7;
+        const int ex = top == 255 ? 7 : max(-119, min((int)top - 127, 126));
+        const float down = __uint_as_float((uint32_t)(127 + 7 - ex) << 23);
+        q_up = __uint_as_float((uint32_t)(127 + ex - 7) << 23);
+        // an infinite or NaN element makes the row's scores NaN
+        const uint32_t bad = top == 255 ? 0x7f7f7f7fu : 0u;
+#pragma unroll 4
+        for (int i = 0; i < 8; ++i) {         // 16 elements: a chunk of hi and one of lo
+          const uint4 x = piece(2 * i), y = piece(2 * i + 1);
+          const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t h2[2], l2[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              // f16 holds the scaled element exactly, or to 2^-25
+              const __half2 u = __floats2half2_rn(bf16lo(w[2 * k + e]) * down,
+                                                  bf16hi(w[2 * k + e]) * down);
+              h2[e] = f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&u));
+              const uint32_t back = e4m3x2_to_f16x2((uint16_t)h2[e]);
+              const __half2 d = __hsub2(u, *reinterpret_cast<const __half2*>(&back));
+              l2[e] = f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&d));
+            }
+            hi[k] = (h2[0] | h2[1] << 16) | bad;
+            lo[k] = l2[0] | l2[1] << 16;
+          }
+          const uint32_t at = dst + ((i ^ (r & 7)) << 4);
+          sts16(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+          sts16(at + kTile8, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+        }
+      } else {                              // zeros: no score, no rescaling
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+        for (int i = 0; i < 8; ++i) {
+          sts16(sbase + OFF_Q + hh * kTile16 + r * 128 + i * 16, zero);
+          sts16(sbase + OFF_Q + hh * kTile16 + kTile8 + r * 128 + i * 16, zero);
+        }
       }
       fence_proxy_async_smem();
       mbar_arrive(bar(B_QC));
@@ -681,22 +691,6 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
       // the S_B commit follows both streams' Q K^T: this K stage can be refilled
       if (hh == 1 && lane == 0) mbar_arrive(bar(B_KE + kr.slot));
       const int k0 = (t0 + jj) * BN;
-      if (k0 + BN - 1 > a.prior_len + q0) {
-        // the causal mask, written over S: rare, so its code stays short
-#pragma unroll 1
-        for (int c = 0; c < BN; c += 16) {
-          float x[16];
-          tmem_ld16(lane_base + col_s + c, x);
-          tmem_wait_ld();
-          reg_fence(x);
-          uint32_t u[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            u[i] = k0 + c + i > row_pos ? 0xff800000u : __float_as_uint(x[i]);
-          tmem_st16(lane_base + col_s + c, u);
-        }
-        tmem_wait_st();
-      }
       const TileScales* ts =
           reinterpret_cast<const TileScales*>(smem + OFF_SCALES) + sr.slot;
       // the whole S row into registers: four loads in flight, one wait
@@ -718,6 +712,16 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
       tmem_wait_ld();
 #pragma unroll
       for (int c = 0; c < BN / 32; ++c) reg_fence(t[c]);
+      if (k0 + BN - 1 > a.prior_len + q0) {   // causal mask needed: bit i stands for column i
+#pragma unroll
+        for (int c = 0; c < BN / 32; ++c) {
+          const int last = row_pos - k0 - c * 32;
+          const uint32_t seen = last < 0 ? 0u : 0xffffffffu >> (31 - min(last, 31));
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (!(seen >> i & 1u)) t[c][i] = -INFINITY;
+        }
+      }
       float mx = -INFINITY;
 #pragma unroll
       for (int b = 0; b < kBlkPerTile; ++b) {
@@ -745,7 +749,7 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
           float m2 = ms_run;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            x[i] *= k;
+            x[i] = k0 + b * 16 + i > row_pos ? -INFINITY : x[i] * k;
             m2 = fmaxf(m2, x[i]);
           }
           const float m0 = m2 == -INFINITY ? 0.f : m2;   // no key yet: every weight is 0
@@ -824,12 +828,12 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
     // and then the unit, which may leave the normal range when V's scales do.
     const int e = n_tiles > 0 ? (reinterpret_cast<const TileScales*>(smem + OFF_SCALES))->e : 0;
     const float ref = wide ? ms_run : m_run - (float)e;
-    const float unit = wide ? fast_exp2(m_run - ms_run) : scale_value((uint32_t)(e + 127));
+    const float unit = !wide ? scale_value((uint32_t)(e + 127))
+                       : m_run == -INFINITY ? 0.f   // no key of the row in this CTA
+                                            : fast_exp2(m_run - ms_run);
     if (n_tiles > 0 && row_pos >= *nan_key)
       l_run = __int_as_float(0x7fffffff);   // the row sees a NaN value
     const bool row_ok = (q0 + r) < a.chunk_len;
-    __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.out) +
-                          ((int64_t)(q0 + r) * a.num_q_heads + head) * HD;
     if (p.splits == 1) {
       // The rows leave through this stream's query tiles, which its products
       // are done with: 16-byte chunks XORed by the row, then whole rows of
@@ -866,9 +870,10 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
       const uint32_t row_at = sbase + OFF_ROWS + (hh * BM + r) * 8;
       asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(row_at), "f"(ref), "f"(l_run) : "memory");
       cluster_sync();                       // every CTA's stats are there, its tiles are done with
-      // CTA k adds up columns k W .. k W + W - 1 (W = 2^w): four columns of
-      // 128 rows are 2 KiB in a piece, rows side by side
-      const int w = 31 - __clz(HD / p.splits);
+      // CTA k adds up columns k W .. k W + W - 1, W = 2^w the columns over the
+      // largest power of two of CTAs: four columns of 128 rows are 2 KiB in a
+      // piece, rows side by side
+      const int w = 7 - (31 - __clz(p.splits));
       if (row_ok) {
         float2 stat[8];
         float top = -INFINITY, sum = 0.f;
@@ -907,29 +912,33 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
         }
       }
       cluster_sync();
-      // this CTA's columns
-      if (row_ok) {
-        for (int c4 = 0; c4 < 1 << (w - 2); c4 += 2) {
-          float o[8];
+      // this CTA's columns of the chunk's rows, eight to a thread
+      const int groups = rank << w < HD ? 1 << (w - 3) : 0;
+      const int rows0 = min(BM, a.chunk_len - qrow0), rows1 = max(0, min(BM, a.chunk_len - qrow1));
+      for (int i = tid; i < (rows0 + rows1) * groups; i += kSoftThreads) {
+        const int row = i / groups, c8 = i - row * groups;
+        const int h = row >= rows0 ? 1 : 0, rr = row - (h ? rows0 : 0);
+        float o[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = 0.f;
+        for (int j = 0; j < 8; ++j) o[j] = 0.f;
 #pragma unroll 4
-          for (int k = 0; k < p.splits; ++k) {
-            const uint32_t at = sbase + (((k * 2 + hh) << (w - 2)) + c4) * (BM * 16) + r * 16;
-            const uint4 x = lds16(at), y = lds16(at + BM * 16);
-            o[0] += __uint_as_float(x.x);
-            o[1] += __uint_as_float(x.y);
-            o[2] += __uint_as_float(x.z);
-            o[3] += __uint_as_float(x.w);
-            o[4] += __uint_as_float(y.x);
-            o[5] += __uint_as_float(y.y);
-            o[6] += __uint_as_float(y.z);
-            o[7] += __uint_as_float(y.w);
-          }
-          *reinterpret_cast<uint4*>(orow + (rank << w) + c4 * 4) =
-              make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]),
-                         pack_bf16(o[6], o[7]));
+        for (int k = 0; k < p.splits; ++k) {
+          const uint32_t at = sbase + (((k * 2 + h) << (w - 2)) + 2 * c8) * (BM * 16) + rr * 16;
+          const uint4 x = lds16(at), y = lds16(at + BM * 16);
+          o[0] += __uint_as_float(x.x);
+          o[1] += __uint_as_float(x.y);
+          o[2] += __uint_as_float(x.z);
+          o[3] += __uint_as_float(x.w);
+          o[4] += __uint_as_float(y.x);
+          o[5] += __uint_as_float(y.y);
+          o[6] += __uint_as_float(y.z);
+          o[7] += __uint_as_float(y.w);
         }
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) +
+                             ((int64_t)((h ? qrow1 : qrow0) + rr) * a.num_q_heads +
+                              (h ? head1 : head0)) * HD + (rank << w) + c8 * 8;
+        *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]),
+                                                    pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7]));
       }
     }
   }
@@ -960,10 +969,8 @@ cudaError_t launch_prefill_fp8_block(const PrefillArgs& a, int num_sms, cudaStre
   const int n_x = p.rows_mode ? a.num_q_heads : a.num_q_heads / 2;
   const int n_t = p.rows_mode ? (p.q_tiles + 1) / 2 : p.q_tiles;
   const int most_tiles = (p.total_len - 1) / BN + 1;
-  // CTAs to an item, while they find SMs and key tiles
-  p.splits = 1;
-  while (p.splits < 8 && (int64_t)n_x * n_t * p.splits * 2 <= num_sms && p.splits * 2 <= most_tiles)
-    p.splits *= 2;
+  // CTAs to an item: as many as find SMs and key tiles, up to the portable cluster
+  p.splits = (int)std::min<int64_t>(std::min(8, most_tiles), std::max<int64_t>(1, num_sms / ((int64_t)n_x * n_t)));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(n_x, n_t, p.splits);
   cfg.blockDim = dim3(kThreads);
