@@ -54,9 +54,9 @@
 //
 // Splitting the keys.  Where the work items are fewer than the SMs, a cluster
 // of 2 to 8 CTAs shares an item's key tiles.  At the end every CTA reads the
-// others' (M, l) rows through distributed shared memory, scales its O to the
-// common maximum, and sends each CTA its share of the columns, which adds them
-// up and writes them.
+// others' sums through distributed shared memory, scales its O to the common
+// one, and sends each CTA its share of the columns, which adds them up and
+// writes them.
 // Every mbarrier wait is bounded; on time-out the kernel records an error,
 // stops issuing work, lets its copies land, frees its TMEM and returns.
 #include <cuda.h>
@@ -119,8 +119,10 @@ constexpr float kLazy = 8.0f;
 
 static_assert(NSV * kTile16 == 2 * BM * HD * 2, "the bf16 queries fit the V ring");
 static_assert(SMEM_BYTES <= 227 * 1024, "one CTA per SM");
-// 7 CTAs of W = 32 columns are the most
-static_assert(7 * 2 * BM * 32 * 4 <= OFF_SCALES, "the merge's columns lie in the tiles' place");
+// the merge, in the tiles' place: the CTAs' columns (7 CTAs of 32 are the most)
+// and what their rows count for
+constexpr int OFF_UNITS = 7 * 2 * BM * 32 * 2;
+static_assert(OFF_UNITS + 8 * 2 * BM * 4 <= OFF_SCALES, "the merge lies in the tiles' place");
 
 enum {
   B_Q = 0,
@@ -300,9 +302,13 @@ __device__ __forceinline__ float2 ld_peer2(uint32_t addr) {
                : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
   return v;
 }
-__device__ __forceinline__ void st_peer(uint32_t addr, float x, float y, float z, float w) {
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "f"(x), "f"(y), "f"(z),
-               "f"(w)
+__device__ __forceinline__ void st_peer1(uint32_t addr, float x) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
+}
+__device__ __forceinline__ void st_peer4(uint32_t addr, uint32_t x, uint32_t y, uint32_t z,
+                                         uint32_t w) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(x), "r"(y), "r"(z),
+               "r"(w)
                : "memory");
 }
 
@@ -622,14 +628,15 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
     const bool queries = q0 + (r & ~31) < a.chunk_len;   // the warp has rows of the chunk
     if (n_tiles > 0 && wait_fast(bar(B_Q), 0, abort_flag, a.err)) {
       if (queries) {
-        // this row's query becomes its hi and lo rows
+        // This row's query becomes its hi and lo rows.  Short loops: the code runs
+        // once, and fetching it is what takes the time.
         const uint32_t src = sbase + OFF_V + hh * kTile16 + r * 128;
         const uint32_t dst = sbase + OFF_Q + hh * kTile16 + r * 128;
         auto piece = [&](int i) {             // elements 8 i .. 8 i + 7
           return lds16(src + (i >> 3) * kHalf16 + (((i & 7) ^ (r & 7)) << 4));
         };
         uint32_t top = 0;
-#pragma unroll 8
+#pragma unroll 4
         for (int i = 0; i < 16; ++i) {
           const uint4 x = piece(i);
           top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
@@ -643,7 +650,7 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
         q_up = __uint_as_float((uint32_t)(127 + ex - 7) << 23);
         // an infinite or NaN element makes the row's scores NaN
         const uint32_t bad = top == 255 ? 0x7f7f7f7fu : 0u;
-#pragma unroll 4
+#pragma unroll 1
         for (int i = 0; i < 8; ++i) {         // 16 elements: a chunk of hi and one of lo
           const uint4 x = piece(2 * i), y = piece(2 * i + 1);
           const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
@@ -871,23 +878,43 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
       asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(row_at), "f"(ref), "f"(l_run) : "memory");
       cluster_sync();                       // every CTA's stats are there, its tiles are done with
       // CTA k adds up columns k W .. k W + W - 1, W = 2^w the columns over the
-      // largest power of two of CTAs: four columns of 128 rows are 2 KiB in a
-      // piece, rows side by side
+      // largest power of two of CTAs.  What it gets from each CTA: O as f16, whose
+      // 11 bits are P's own, each row brought to below 2 by a power of two, eight
+      // columns of 128 rows in a piece of 2 KiB, rows side by side; and what the
+      // rows count for.  (In fp32 the 128 KiB a CTA sends, at some 25 bytes a
+      // cycle, were the longest part of a short call.)
       const int w = 7 - (31 - __clz(p.splits));
+      const int owners = HD >> w;
+      float most = 0.f;                     // the row's largest |O|
+      if (n_tiles > 0) {
+#pragma unroll 1
+        for (int c = 0; c < HD; c += 32) {
+          float o[32];
+          tmem_ld32(lane_base + col_o + c, o);
+          tmem_wait_ld();
+          reg_fence(o);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) most = fmaxf(most, fabsf(o[i]));
+        }
+      }
+      // 2^x, x the exponent of the largest (a row of zeros: any), and its inverse
+      const uint32_t ex = max(1u, min(253u, __float_as_uint(most) >> 23));
+      const float up = __uint_as_float(ex << 23), down = __uint_as_float((254u - ex) << 23);
       if (row_ok) {
-        float2 stat[8];
+        float2 stat[8];                     // all on their way before the first is used
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          stat[k] = k < p.splits ? ld_peer2(peer(row_at, k)) : make_float2(-INFINITY, 0.f);
         float top = -INFINITY, sum = 0.f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          stat[k] = k < p.splits ? ld_peer2(peer(row_at, k)) : make_float2(-INFINITY, 0.f);
-          top = fmaxf(top, stat[k].x);
-        }
+        for (int k = 0; k < 8; ++k) top = fmaxf(top, stat[k].x);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           if (k < p.splits) sum = fmaf(fast_exp2(stat[k].x - top), stat[k].y, sum);
-        // rows that no CTA gave a weight to (their scores are all -inf) are NaN
-        const float f = n_tiles > 0 ? fast_exp2(ref - top) / sum : 0.f;
-        l_run = f;
+        const float f = n_tiles > 0 ? fast_exp2(ref - top) / sum * unit * up : 0.f;
+#pragma unroll 1
+        for (int k = 0; k < owners; ++k)
+          st_peer1(peer(sbase + OFF_UNITS + ((rank * 2 + hh) * BM + r) * 4, k), f);
       }
 #pragma unroll 1
       for (int c = 0; c < HD; c += 16) {
@@ -900,45 +927,57 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
           reg_fence(o);
         }
         // W is at least 16: the 16 columns have one owner
-        const int owner = c >> w;
-        const int piece = ((rank * 2 + hh) << (w - 2)) + ((c & ((1 << w) - 1)) >> 2);
-        const uint32_t at = peer(sbase + piece * (BM * 16) + r * 16, owner);
+        const int piece = ((rank * 2 + hh) << (w - 3)) + ((c & ((1 << w) - 1)) >> 3);
+        const uint32_t at = peer(sbase + piece * (BM * 16) + r * 16, c >> w);
         if (row_ok) {
+          uint32_t h[8];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = o[i] * l_run * unit;
-#pragma unroll
-          for (int i = 0; i < 16; i += 4)
-            st_peer(at + i / 4 * (BM * 16), o[i], o[i + 1], o[i + 2], o[i + 3]);
+          for (int i = 0; i < 8; ++i) {
+            const __half2 x = __floats2half2_rn(o[2 * i] * down, o[2 * i + 1] * down);
+            h[i] = *reinterpret_cast<const uint32_t*>(&x);
+          }
+          st_peer4(at, h[0], h[1], h[2], h[3]);
+          st_peer4(at + BM * 16, h[4], h[5], h[6], h[7]);
         }
       }
       cluster_sync();
       // this CTA's columns of the chunk's rows, eight to a thread
-      const int groups = rank << w < HD ? 1 << (w - 3) : 0;
+      const int shift = w - 3, groups = rank < owners ? 1 << shift : 0;
       const int rows0 = min(BM, a.chunk_len - qrow0), rows1 = max(0, min(BM, a.chunk_len - qrow1));
+#pragma unroll 1
       for (int i = tid; i < (rows0 + rows1) * groups; i += kSoftThreads) {
-        const int row = i / groups, c8 = i - row * groups;
+        const int row = i >> shift, c8 = i & (groups - 1);
         const int h = row >= rows0 ? 1 : 0, rr = row - (h ? rows0 : 0);
-        float o[8];
+        uint4 x[8];
+        float u[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = 0.f;
-#pragma unroll 4
-        for (int k = 0; k < p.splits; ++k) {
-          const uint32_t at = sbase + (((k * 2 + h) << (w - 2)) + 2 * c8) * (BM * 16) + rr * 16;
-          const uint4 x = lds16(at), y = lds16(at + BM * 16);
-          o[0] += __uint_as_float(x.x);
-          o[1] += __uint_as_float(x.y);
-          o[2] += __uint_as_float(x.z);
-          o[3] += __uint_as_float(x.w);
-          o[4] += __uint_as_float(y.x);
-          o[5] += __uint_as_float(y.y);
-          o[6] += __uint_as_float(y.z);
-          o[7] += __uint_as_float(y.w);
+        for (int k = 0; k < 8; ++k) {
+          if (k < p.splits) {
+            x[k] = lds16(sbase + (((k * 2 + h) << shift) + c8) * (BM * 16) + rr * 16);
+            u[k] = *reinterpret_cast<const float*>(smem + OFF_UNITS + ((k * 2 + h) * BM + rr) * 4);
+          }
+        }
+        float acc[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (k < p.splits) {
+            const uint32_t v[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&v[j]));
+              acc[2 * j] = fmaf(y.x, u[k], acc[2 * j]);
+              acc[2 * j + 1] = fmaf(y.y, u[k], acc[2 * j + 1]);
+            }
+          }
         }
         __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) +
                              ((int64_t)((h ? qrow1 : qrow0) + rr) * a.num_q_heads +
                               (h ? head1 : head0)) * HD + (rank << w) + c8 * 8;
-        *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]),
-                                                    pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7]));
+        *reinterpret_cast<uint4*>(dst) =
+            make_uint4(pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3]),
+                       pack_bf16(acc[4], acc[5]), pack_bf16(acc[6], acc[7]));
       }
     }
   }

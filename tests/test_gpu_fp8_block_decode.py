@@ -81,6 +81,20 @@ def test_a_block_that_takes_the_weight_and_holds_small_values(hkv, byte):
     C.check_decode(pools, q, table, lens, SCALE, got)
 
 
+@pytest.mark.parametrize("hkv", [4, 1])
+@pytest.mark.parametrize("n", [200, 3000])
+def test_rare_keys_with_large_values(n, hkv):
+    """A quarter of the keys weighs 2^-33 of the others and holds values 2^33
+    as large: both count alike, in whichever piece they fall."""
+    pools, q, table = _case([n], hkv, 2, poison=False, k_spread=0, v_spread=0)
+    q = torch.ones_like(q)
+    far = table[0, : n // 64].long()
+    pools.codes[0][far] = 0xF0                               # -128 * 2^-6 = -2 in every element: score -22.6
+    pools.scale[0][far] = 121
+    pools.scale[1][far] += 33
+    C.check_decode(pools, q, table, [n], SCALE, C.decode(pools, q, table, [n], SCALE))
+
+
 def test_large_and_small_queries_and_scales():
     lens = [90, 700]
     for size, k_exp in ((2.0 ** 70, -80), (2.0 ** -70, 60), (2.0 ** 17, -20)):

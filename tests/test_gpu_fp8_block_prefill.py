@@ -102,6 +102,19 @@ def test_one_block_far_from_the_others(at, byte):
     _check(pools, q, row, prior, _run(pools, q, row, prior), rows=[0, 1, 15, 16, 100, 112, 113, 127])
 
 
+@pytest.mark.parametrize("prior,chunk,hkv", [(480, 32, 1), (900, 130, 8), (3000, 1, 2)])
+def test_rare_keys_with_large_values(prior, chunk, hkv):
+    """A quarter of the keys weighs 2^-33 of the others and holds values 2^33
+    as large: both count alike, in whichever CTA they fall."""
+    pools, q, row = _case(prior, chunk, hkv, 2, poison=False, k_spread=0, v_spread=0)
+    q = torch.ones_like(q)
+    far = row[: prior // 64].long()
+    pools.codes[0][far] = 0xF0                               # -128 * 2^-6 = -2 in every element: score -22.6
+    pools.scale[0][far] = 121
+    pools.scale[1][far] += 33
+    _check(pools, q, row, prior, _run(pools, q, row, prior))
+
+
 def test_zero_values_still_take_their_weight():
     pools, q, row = _case(300, 30, 2, 2, poison=False)
     for b in row[2:9].tolist():
