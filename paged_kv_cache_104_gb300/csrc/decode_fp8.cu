@@ -7,11 +7,10 @@ namespace pkv {
 cudaError_t launch_paged_decode_fp8(const DecodeArgs& a, int num_sms, cudaStream_t stream) {
   if (a.chunk_prior >= 0 || a.split_tokens % kStageTok != 0 || !a.k_scale || !a.v_scale)
     return cudaErrorInvalidValue;
-  const cudaError_t e = launch_fp8<false>(a, num_sms, stream);
-  if (e != cudaSuccess || a.max_splits <= 1) return e;
-  DecodeArgs m = a;   // as the kernel was launched
+  DecodeArgs m = a;   // as the kernel is launched
   m.partials_f16 = 1;
-  m.balanced = fp8_balanced(a);
+  const cudaError_t e = launch_fp8<false>(a, num_sms, stream, &m.balanced);
+  if (e != cudaSuccess || a.max_splits <= 1) return e;
   return launch_decode_reduce_bf16_128(m, stream);
 }
 

@@ -12,17 +12,18 @@ constexpr int kMergeWarps = 8;
 // few rows of a small batch, which is cut into many short pieces (one
 // sequence of 32,001 tokens: up to 228 a row): o = sum 2^(m_s - M) O_s / sum
 // 2^(m_s - M) l_s.  Warp w takes the partials w, w + 8, ..., a lane four
-// columns; four rows are in flight per warp.  The programmatic dependent of
-// the main kernel.
+// columns; four rows are in flight per warp, beside their (m, l), under a
+// running maximum.  The programmatic dependent of the main kernel; lengths are
+// the caller's and are read before it ends.
 __global__ void __launch_bounds__(kMergeWarps * 32)
 merge_row_kernel(const DecodeArgs a) {
   __shared__ float4 part[kMergeWarps][32];
   __shared__ float2 ml[kMergeWarps];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = blockIdx.x;
   const int b = row / a.num_q_heads;
   const int n = a.seq_lens[b];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (n < 1 || n > min(a.max_seq_len, a.max_blocks_per_seq * kBlockSize)) return;
   const int h = row - b * a.num_q_heads;
   const int ns = a.balanced ? a.ws_np[b * a.num_kv_heads + h / (a.num_q_heads / a.num_kv_heads)]
@@ -31,11 +32,7 @@ merge_row_kernel(const DecodeArgs a) {
   const int64_t base = (int64_t)row * a.max_splits;
   const float2* rml = reinterpret_cast<const float2*>(a.ws_ml) + base;
   const float4* acc = reinterpret_cast<const float4*>(a.ws_acc) + base * (kHD / 4) + lane;
-  // this warp's own reference, so its rows can be read before the others' are known
   float m = -INFINITY;
-  for (int s = warp + kMergeWarps * lane; s < ns; s += kMergeWarps * 32) m = fmaxf(m, rml[s].x);
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll8, m, o));
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
   float l = 0.f;
   for (int s0 = warp; s0 < ns; s0 += 4 * kMergeWarps) {
@@ -46,6 +43,16 @@ merge_row_kernel(const DecodeArgs a) {
       const int s = s0 + i * kMergeWarps;
       x[i] = s < ns ? rml[s] : make_float2(-INFINITY, 0.f);
       v[i] = s < ns ? acc[(int64_t)s * (kHD / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    const float top = fmaxf(fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(x[2].x, x[3].x)), m);
+    if (top != m) {
+      const float f = ex2(m - top);
+      l *= f;
+      sum.x *= f;
+      sum.y *= f;
+      sum.z *= f;
+      sum.w *= f;
+      m = top;
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -87,11 +94,10 @@ int fp8_block_split_tokens(int num_seqs, int num_kv_heads, int max_seq_len) {
 cudaError_t launch_paged_decode_fp8_block(const DecodeArgs& a, int num_sms, cudaStream_t stream) {
   if (a.chunk_prior >= 0 || a.split_tokens % kStageTok != 0 || !a.k_bscale || !a.v_bscale)
     return cudaErrorInvalidValue;
-  cudaError_t e = launch_fp8<true>(a, num_sms, stream);
-  if (e != cudaSuccess || a.max_splits <= 1) return e;
   DecodeArgs m = a;
   m.partials_f16 = 0;
-  m.balanced = fp8_balanced(a);
+  cudaError_t e = launch_fp8<true>(a, num_sms, stream, &m.balanced);
+  if (e != cudaSuccess || a.max_splits <= 1) return e;
   // a warp a row fills the GPU once there are some thousand rows
   if ((int64_t)a.num_seqs * a.num_q_heads > 8 * 152) return launch_decode_reduce_bf16_128(m, stream);
   cudaLaunchConfig_t cfg = {};

@@ -680,8 +680,10 @@ inline int fp8_balanced(const DecodeArgs& a) {
   return a.ws_np != nullptr && stage_plan_fits(aw, hs ? kBlockSize : kStageTok);
 }
 
+// *balanced: the walk that the merge has to assume (the kernel leaves the piece
+// counts whenever it is set).
 template <int G, bool HS, bool BS>
-cudaError_t launch_fp8_g(const DecodeArgs& args, int num_sms, cudaStream_t stream) {
+cudaError_t launch_fp8_g(const DecodeArgs& args, int num_sms, cudaStream_t stream, int* balanced) {
   using C = F8Cfg<G>;
   DecodeArgs a = args;
   DecodeArgs aw = a;
@@ -707,20 +709,38 @@ cudaError_t launch_fp8_g(const DecodeArgs& args, int num_sms, cudaStream_t strea
   const int per_sm = by_smem < 1 ? 1 : (by_smem > (G <= 8 ? 3 : 2) ? (G <= 8 ? 3 : 2) : by_smem);
   const int64_t upper = (int64_t)a.num_seqs * (BS ? aw.num_kv_heads : a.num_kv_heads) * a.max_splits;
   const int grid = (int)(upper < (int64_t)num_sms * per_sm ? upper : (int64_t)num_sms * per_sm);
+  if (BS) {
+    // a batch that cannot give every CTA its least share, however long its
+    // sequences, is planned in splits at once
+    constexpr int tok = HS ? kBlockSize : kStageTok;
+    const int64_t most = (int64_t)a.num_seqs * aw.num_kv_heads * ((a.max_seq_len + tok - 1) / tok);
+    if (most < (int64_t)(a.split_tokens / tok) * grid) a.balanced = 0;
+  }
+  *balanced = a.balanced;
   decode_fp8_kernel<G, HS, BS><<<grid, kThreads8, smem, stream>>>(a, tm_k, tm_v);
   return cudaGetLastError();
 }
 
 // One block of kBPS KV heads per stage when the heads form such groups.
 template <bool BS>
-cudaError_t launch_fp8(const DecodeArgs& a, int num_sms, cudaStream_t stream) {
+cudaError_t launch_fp8(const DecodeArgs& a, int num_sms, cudaStream_t stream, int* balanced) {
   const bool hs = a.num_kv_heads % kBPS == 0;
   switch (a.num_q_heads / a.num_kv_heads) {
-    case 1: return hs ? launch_fp8_g<1, true, BS>(a, num_sms, stream) : launch_fp8_g<1, false, BS>(a, num_sms, stream);
-    case 2: return hs ? launch_fp8_g<2, true, BS>(a, num_sms, stream) : launch_fp8_g<2, false, BS>(a, num_sms, stream);
-    case 4: return hs ? launch_fp8_g<4, true, BS>(a, num_sms, stream) : launch_fp8_g<4, false, BS>(a, num_sms, stream);
-    case 8: return hs ? launch_fp8_g<8, true, BS>(a, num_sms, stream) : launch_fp8_g<8, false, BS>(a, num_sms, stream);
-    case 16: return hs ? launch_fp8_g<16, true, BS>(a, num_sms, stream) : launch_fp8_g<16, false, BS>(a, num_sms, stream);
+    case 1:
+      return hs ? launch_fp8_g<1, true, BS>(a, num_sms, stream, balanced)
+                : launch_fp8_g<1, false, BS>(a, num_sms, stream, balanced);
+    case 2:
+      return hs ? launch_fp8_g<2, true, BS>(a, num_sms, stream, balanced)
+                : launch_fp8_g<2, false, BS>(a, num_sms, stream, balanced);
+    case 4:
+      return hs ? launch_fp8_g<4, true, BS>(a, num_sms, stream, balanced)
+                : launch_fp8_g<4, false, BS>(a, num_sms, stream, balanced);
+    case 8:
+      return hs ? launch_fp8_g<8, true, BS>(a, num_sms, stream, balanced)
+                : launch_fp8_g<8, false, BS>(a, num_sms, stream, balanced);
+    case 16:
+      return hs ? launch_fp8_g<16, true, BS>(a, num_sms, stream, balanced)
+                : launch_fp8_g<16, false, BS>(a, num_sms, stream, balanced);
     default: return cudaErrorInvalidValue;
   }
 }
