@@ -406,19 +406,23 @@ pkv_status pkv_paged_decode_attention_fp8(void *out, const void *q, const void *
  * Entries of a block that follow another run of the same block among the 32
  * entries before them are skipped and reported (PKV_DEVERR_SLOT_ORDER); such
  * runs further apart race.  A position outside the table skips its token and
- * the rest of its run. */
+ * the rest of its run.  A skipped entry whose own slot and position are in
+ * range still has its query rotated. */
 pkv_status pkv_kv_append_fp8_block(const pkv_rope_append_args *args, pkv_stream_t stream);
 
 /* Bytes of device workspace pkv_paged_decode_attention_fp8_block needs (0:
  * none).  fp32 partials, as pkv_decode_workspace_bytes, but a small batch is
- * cut into splits of 256, 128 or 64 tokens instead of 512.  Host-only. */
+ * cut into splits of 256, 128 or 64 tokens instead of 512.  With less than
+ * this many bytes the call takes the shortest splits that fit, down to
+ * pkv_decode_workspace_bytes(...), so the workspace of a larger batch serves
+ * every smaller one.  Host-only. */
 size_t pkv_decode_fp8_block_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads,
                                             int head_dim, int max_seq_len);
 
 /* Decode attention over the block-scaled pools: pkv_paged_decode_attention
  * with q and out in bf16, head_dim 128, groups of 1, 2, 4, 8 or 16 query heads
  * to a KV head, and a workspace of
- * pkv_decode_fp8_block_workspace_bytes(...).  A length of 0 marks a padded
+ * pkv_decode_fp8_block_workspace_bytes(...) (or less, see there).  A length of 0 marks a padded
  * row of the batch: its out row is left as it was and no error is recorded.
  * A NaN code in a key makes its KV head's results NaN, one in a value its
  * element of them. */

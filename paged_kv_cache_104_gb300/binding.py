@@ -395,7 +395,7 @@ class Rope:
             self._pair_ptr = ctypes.addressof(self._pair_axis)
 
 
-def _rope_append(fn, call, q_out, q, k_new, v_new, k_cache, v_cache, scale_ptrs, slot_mapping,
+def _rope_append(fn, call, slots_check, q_out, q, k_new, v_new, k_cache, v_cache, scale_ptrs, slot_mapping,
                  positions, rope, dtype, dtype_code, index, stream):
     shape = k_cache.shape
     nb, hkv, bs, d = shape
@@ -428,6 +428,10 @@ def _rope_append(fn, call, q_out, q, k_new, v_new, k_cache, v_cache, scale_ptrs,
     a = RopeAppendArgs(qop, qp, k_new.data_ptr(), v_new.data_ptr(), kp, vp, scale_ptrs[0],
                        scale_ptrs[1], sp, t, nb, qos, qs, ks, vs, hq, hkv, d, bs, dtype_code, table,
                        num_positions, pos, axes, rot, inter, pair)
+    if _debug:
+        _validate(fn, slots_check, slot_mapping, nb, bs)
+        if rope is not None:
+            _validate(fn, "check_positions", positions, slot_mapping, num_positions)
     status = call(ctypes.byref(a), _stream_on(stream, index))
     if status:
         _check(fn, status)
@@ -445,12 +449,9 @@ def kv_append_rope(q_out, q, k_new, v_new, k_cache, v_cache, slot_mapping, posit
         _refuse(fn, "no rope")
     dtype = k_cache.dtype
     code = _dtype_code(k_cache)
-    if _debug:
-        _validate(fn, "check_slots", slot_mapping, k_cache.shape[0], k_cache.shape[2])
-        _validate(fn, "check_positions", positions, slot_mapping, rope.num_positions)
-    _rope_append(fn, load().pkv_kv_append_rope, q_out, q, k_new, v_new, k_cache, v_cache,
-                 (None, None), slot_mapping, positions, rope, dtype, code, _device_of(fn, k_cache),
-                 stream)
+    _rope_append(fn, load().pkv_kv_append_rope, "check_slots", q_out, q, k_new, v_new, k_cache,
+                 v_cache, (None, None), slot_mapping, positions, rope, dtype, code,
+                 _device_of(fn, k_cache), stream)
 
 
 def kv_append_fp8_block(k_new, v_new, k_cache, v_cache, k_scale, v_scale, slot_mapping, stream=None,
@@ -465,14 +466,10 @@ def kv_append_fp8_block(k_new, v_new, k_cache, v_cache, k_scale, v_scale, slot_m
         _refuse(fn, f"the pools are {k_cache.dtype}, not torch.uint8")
     if rope is None and q is not None:
         _refuse(fn, "queries need a rope")
-    if _debug:
-        _validate(fn, "check_runs", slot_mapping, k_cache.shape[0], k_cache.shape[2])
-        if rope is not None:
-            _validate(fn, "check_positions", positions, slot_mapping, rope.num_positions)
     index = _device_of(fn, k_cache)
-    _rope_append(fn, load().pkv_kv_append_fp8_block, q_out, q, k_new, v_new, k_cache, v_cache,
-                 _block_scales(fn, k_cache, k_scale, v_scale, index), slot_mapping, positions, rope,
-                 torch.bfloat16, PKV_BF16, index, stream)
+    _rope_append(fn, load().pkv_kv_append_fp8_block, "check_runs", q_out, q, k_new, v_new, k_cache,
+                 v_cache, _block_scales(fn, k_cache, k_scale, v_scale, index), slot_mapping, positions,
+                 rope, torch.bfloat16, PKV_BF16, index, stream)
 
 
 def _block_scales(fn, k_cache, k_scale, v_scale, index: int):
@@ -500,7 +497,8 @@ def paged_decode_attention_fp8_block(out, q, k_cache, v_cache, k_scale, v_scale,
     """Decode over block-scaled uint8 E4M3 pools [NB, Hkv, bs, 128] with scale
     bytes [NB, Hkv]; q/out bf16 [B, Hq, 128]; block_table [B, max_blocks] and
     seq_lens [B] int32 (0: a padded row, left alone); max_seq_len >=
-    max(seq_lens); workspace from ``decode_workspace_fp8_block``."""
+    max(seq_lens); workspace from ``decode_workspace_fp8_block``, for this
+    batch or a larger one."""
     fn = "pkv_paged_decode_attention_fp8_block"
     if k_cache.dtype is not torch.uint8:
         _refuse(fn, f"the pools are {k_cache.dtype}, not torch.uint8")

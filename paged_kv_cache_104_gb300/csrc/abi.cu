@@ -67,9 +67,9 @@ int max_splits_for(int max_seq_len, int split_tokens = pkv::kSplitTokens) {
 }
 
 // Partial slots per (sequence, query head) row: a sequence of n tokens gives
-// at most ceil(n / kSplitTokens) partials in 512-token splits, and at most
-// one more in the bf16 decode's balanced walk (each CTA's share of at least
-// 512 tokens may start inside a sequence).  One slot: no partials at all.
+// at most ceil(n / split_tokens) partials in splits, and at most one more in
+// the balanced walk (each CTA's share of at least split_tokens tokens may
+// start inside a sequence).  One slot: no partials at all.
 int partial_slots_for(int max_seq_len, int split_tokens = pkv::kSplitTokens) {
   const int s = max_splits_for(max_seq_len, split_tokens);
   return s <= 1 ? 1 : s + 1;
@@ -539,8 +539,9 @@ namespace {
 // its launch arguments but for the scales (scales_ok: given and aligned);
 // num_seqs 0 in them: nothing to do.
 pkv_status fp8_decode_prepare(pkv::DecodeArgs* out_args, int* sms, bool scales_ok,
-                              int split_tokens, void* out, const void* q, const void* k_cache, const void* v_cache,
-                              const int32_t* block_table, const int32_t* seq_lens, int num_seqs,
+                              int split_tokens, void* out, const void* q, const void* k_cache,
+                              const void* v_cache, const int32_t* block_table,
+                              const int32_t* seq_lens, int num_seqs,
                               int max_blocks_per_seq, int max_seq_len, int64_t num_blocks,
                               int num_q_heads, int num_kv_heads, int head_dim, int block_size,
                               float scale, void* workspace, size_t workspace_bytes) {
@@ -648,9 +649,16 @@ pkv_status pkv_paged_decode_attention_fp8_block(
   if (max_seq_len > INT_MAX - pkv::kSplitTokens) return PKV_ERANGE;   // rounded up to whole splits
   pkv::DecodeArgs a;
   int sms = 0;
-  const int split = num_seqs > 0 && num_kv_heads > 0 && max_seq_len > 0
-                        ? pkv::fp8_block_split_tokens(num_seqs, num_kv_heads, max_seq_len)
-                        : pkv::kSplitTokens;
+  int split = pkv::kSplitTokens;
+  if (num_seqs > 0 && num_q_heads > 0 && num_kv_heads > 0 && head_dim > 0 && max_seq_len > 0) {
+    split = pkv::fp8_block_split_tokens(num_seqs, num_kv_heads, max_seq_len);
+    // a caller's workspace for a larger batch may be too small for the shorter
+    // splits of this one
+    while (split < pkv::kSplitTokens &&
+           partials_bytes(num_seqs, num_q_heads, head_dim, partial_slots_for(max_seq_len, split)) >
+               workspace_bytes)
+      split *= 2;
+  }
   const pkv_status st = fp8_decode_prepare(
       &a, &sms, k_scale && v_scale, split, out, q, k_cache, v_cache, block_table, seq_lens, num_seqs,
       max_blocks_per_seq, max_seq_len, num_blocks, num_q_heads, num_kv_heads, head_dim, block_size,

@@ -23,7 +23,7 @@ def _decode(**kw):
     (dict(nb=0), 1), (dict(B=8193), 3), (dict(msl=1025), 1), (dict(scale=float("inf")), 1),
     (dict(out=0), 1), (dict(q=0), 1), (dict(k=0), 1), (dict(v=0), 1), (dict(ks=0), 1), (dict(vs=0), 1),
     (dict(bt=0), 1), (dict(sl=0), 1), (dict(q=0x1008), 1), (dict(bt=0x1002), 1), (dict(sl=0x1001), 1),
-    (dict(wsb=100), 3), (dict(ws=0), 1), (dict(ws=0x1010), 1), (dict(msl=2 ** 31 - 1, mb=2 ** 28), 3),
+    (dict(wsb=100), 3), (dict(ws=0, wsb=0), 3), (dict(ws=0), 1), (dict(ws=0x1010), 1), (dict(msl=2 ** 31 - 1, mb=2 ** 28), 3),
     (dict(B=0), 0)])
 def test_decode_refuses(kw, status):
     assert _decode(**kw) == status

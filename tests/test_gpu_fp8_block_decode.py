@@ -180,6 +180,33 @@ def test_empty_batch_and_graphs_that_share_a_workspace():
     assert torch.equal(outs[0].cpu(), ref) and torch.equal(outs[1].cpu(), ref.flip(0))
 
 
+def test_workspace_of_a_larger_batch_serves_smaller_ones():
+    """A small batch has shorter splits and so more partials a row than a large
+    one; a workspace too small for them makes the splits longer."""
+    n = B.decode_fp8_block_workspace_bytes
+    lens = [4000, 33, 2100]
+    pools, q, table = _case(lens, 4, 4)
+    least = B.decode_workspace_bytes(3, 16, 128, 4000)
+    full = n(3, 16, 4, 128, 4000)
+    assert least < full
+    for size in (least, least + 512, (least + full) // 2 // 256 * 256, full):
+        ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+        C.check_decode(pools, q, table, lens, SCALE, C.decode(pools, q, table, lens, SCALE, workspace=ws))
+    with pytest.raises(B.PagedKVError, match="status 3"):
+        C.decode(pools, q, table, lens, SCALE, workspace=torch.empty(least - 256, dtype=torch.uint8, device="cuda"))
+
+
+def test_up_to_512_tokens_need_no_workspace():
+    lens = [500, 3]
+    pools, q, table = _case(lens, 4, 4)
+    out = torch.zeros(2, 16, 128, dtype=torch.bfloat16, device="cuda")
+    B.paged_decode_attention_fp8_block(out, q.cuda(), *pools.cuda(), table.cuda(),
+                                       torch.tensor(lens, dtype=torch.int32).cuda(), 500, SCALE)
+    torch.cuda.synchronize()
+    assert B.get_device_error() == 0
+    C.check_decode(pools, q, table, lens, SCALE, out.cpu())
+
+
 def test_other_stream():
     lens = [300, 20]
     pools, q, table = _case(lens, 4, 4)

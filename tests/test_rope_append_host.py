@@ -194,7 +194,8 @@ def test_run_and_position_checks():
         V.check_positions(torch.tensor([0, 0, 10], dtype=torch.int32), slots, 10)
 
 
-def test_debug_mode_names_the_entry():
+def test_debug_mode_names_the_entry(monkeypatch):
+    monkeypatch.setattr(B, "_device_of", lambda fn, t: -1)
     q, k, v, kc, vc, slots, pos = _tensors()
     rope = B.Rope(R.table(64, 128))
     sc = torch.zeros(4, 2, dtype=torch.uint8)
@@ -207,5 +208,9 @@ def test_debug_mode_names_the_entry():
             B.kv_append_rope(q, q, k, v, kc, vc, torch.tensor([0, 1, 2, 3]), pos + 64, rope)
         with pytest.raises(B.PagedKVError, match="returns to block"):
             B.kv_append_fp8_block(k, v, k8, k8, sc, sc, torch.tensor([0, 1, 3, 2]))
+        with pytest.raises(B.PagedKVError, match="needs positions"):
+            B.kv_append_rope(q, q, k, v, kc, vc, slots, None, rope)
+        with pytest.raises(B.PagedKVError, match="positions is"):
+            B.kv_append_rope(q, q, k, v, kc, vc, slots, pos[:, :3].contiguous(), rope)
     finally:
         B.set_debug(False)
