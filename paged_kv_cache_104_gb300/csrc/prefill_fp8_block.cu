@@ -52,8 +52,8 @@
 // converted to bf16 by cp.async producers 280 us, to f16 185 us (with the
 // loads left out 141 us: bound by their latency at 32 KiB in flight).
 //
-// Splitting the keys.  Where the work items are fewer than the SMs, a cluster
-// of 2 to 8 CTAs shares an item's key tiles.  At the end every CTA reads the
+// Splitting the keys.  Where the work items fill the SMs badly, a cluster of 2
+// to 8 CTAs shares an item's key tiles.  At the end every CTA reads the
 // others' sums through distributed shared memory, scales its O to the common
 // one, and sends each CTA its share of the columns, which adds them up and
 // writes them.
@@ -63,6 +63,8 @@
 
 #include <algorithm>
 #include <climits>
+#include <map>
+#include <mutex>
 
 #include "common.cuh"
 #include "host_cache.h"
@@ -109,7 +111,7 @@ constexpr int kThreads = 512;
 constexpr int W_MMA = 8, W_KPROD = 9, W_VPROD = 10, W_NONE = 12;
 // registers per thread after the split (setmaxnreg), against the launch budget
 constexpr int kRegsSoft = 200, kRegsRest = 56;
-constexpr int kRegsLaunch = (65536 / kThreads) & ~7;   // 80
+constexpr int kRegsLaunch = (65536 / kThreads) & ~7;   // 128
 static_assert(kRegsSoft * kSoftThreads + kRegsRest * (kThreads - kSoftThreads) <=
                   kRegsLaunch * kThreads,
               "the register split must fit in what the CTA was launched with");
@@ -989,6 +991,86 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
   }
 }
 
+constexpr int kMaxSplits = 8;     // the portable cluster
+
+// Clusters of s CTAs (1 .. kMaxSplits) that run at once, at [s].  Of 152 SMs
+// clusters of 8 reach 120 only: they lie within a GPC.  Asked once per context.
+struct ClusterSlots {
+  int at[kMaxSplits + 1] = {};
+};
+cudaError_t cluster_slots(int num_sms, ClusterSlots* out) {
+  static std::mutex mu;
+  static std::map<uint64_t, ClusterSlots> known;
+  const uint64_t ctx = current_context_id();
+  std::lock_guard<std::mutex> lock(mu);
+  auto it = known.find(ctx);
+  if (ctx != 0 && it != known.end()) {
+    *out = it->second;
+    return cudaSuccess;
+  }
+  out->at[1] = num_sms;
+  for (int s = 2; s <= kMaxSplits; ++s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1, 1, s);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = SMEM_BYTES;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e =
+        cudaOccupancyMaxActiveClusters(&out->at[s], prefill_fp8_block_kernel, &cfg);
+    if (e != cudaSuccess) return e;
+  }
+  if (ctx != 0) {
+    if (known.size() > 256) known.clear();   // stale contexts: start over
+    known[ctx] = *out;
+  }
+  return cudaSuccess;
+}
+
+// CTAs to an item: the number by which the longest share of the GPU ends first.
+// Items go to the slots heaviest first, back and forth; an item costs its
+// tiles (1.56 us measured) and 6.5 us, when it is split 9.6 us and 0.45 us a CTA.
+// (640 rows of 32 heads over 16,384 keys are 80 items: one CTA each leaves 72
+// SMs idle.)  Measured against the best of all splits in us: 128 rows over
+// 1,024 keys 15.2 (8 CTAs, as many as SMs would hold: 26.5), 768 over 16,000
+// 179.7 (one: 205), 1,024 rows of 4 heads over 4,096 24.1 (8: 37).
+int choose_splits(const Params& p, int n_x, int n_t, const ClusterSlots& slots) {
+  const int64_t n = (int64_t)n_x * n_t;
+  if (n > 4 * (int64_t)slots.at[1]) return 1;          // many items even out by themselves
+  const int rows = p.rows_mode ? 2 * BM : BM;
+  auto tiles = [&](int64_t item) {                      // heaviest first
+    const int64_t end = (n_t - item / n_x) * rows;      // behind the item's last row
+    return (int)((p.a.prior_len + std::min<int64_t>(p.a.chunk_len, end) - 1) / BN + 1);
+  };
+  int best = 1;
+  int64_t best_cost = INT64_MAX;
+  for (int s = 1; s <= std::min(kMaxSplits, tiles(0)); ++s) {
+    const int64_t k = slots.at[s];
+    if (k < 1) continue;
+    // the longest slot is a first or last one, or beside the last round's end
+    const int64_t rem = n % k, ends[] = {0, k - 1, rem - 1, rem, k - rem - 1, k - rem};
+    int64_t cost = 0;
+    for (int64_t i : ends) {
+      int64_t sum = 0;
+      for (int64_t round = 0; i >= 0 && i < k && round * k < n; ++round) {
+        const int64_t item = round * k + (round % 2 ? k - 1 - i : i);
+        if (item < n) sum += (tiles(item) + s - 1) / s * 156 + (s == 1 ? 650 : 960 + 45 * s);
+      }
+      cost = std::max(cost, sum);
+    }
+    if (cost < best_cost) {
+      best = s;
+      best_cost = cost;
+    }
+  }
+  return best;
+}
+
 }  // namespace
 
 cudaError_t launch_prefill_fp8_block(const PrefillArgs& a, int num_sms, cudaStream_t stream) {
@@ -1007,9 +1089,10 @@ cudaError_t launch_prefill_fp8_block(const PrefillArgs& a, int num_sms, cudaStre
   if (e != cudaSuccess) return e;
   const int n_x = p.rows_mode ? a.num_q_heads : a.num_q_heads / 2;
   const int n_t = p.rows_mode ? (p.q_tiles + 1) / 2 : p.q_tiles;
-  const int most_tiles = (p.total_len - 1) / BN + 1;
-  // CTAs to an item: as many as find SMs and key tiles, up to the portable cluster
-  p.splits = (int)std::min<int64_t>(std::min(8, most_tiles), std::max<int64_t>(1, num_sms / ((int64_t)n_x * n_t)));
+  ClusterSlots slots;
+  e = cluster_slots(num_sms, &slots);
+  if (e != cudaSuccess) return e;
+  p.splits = choose_splits(p, n_x, n_t, slots);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(n_x, n_t, p.splits);
   cfg.blockDim = dim3(kThreads);

@@ -202,3 +202,17 @@ def test_graph_and_other_stream():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out.cpu(), ref)
+
+
+@pytest.mark.parametrize("hkv,group,prior,chunk", [
+    (8, 4, 1000, 500),      # 64 items: clusters of 2
+    (4, 2, 1200, 1270),     # 40 items: 3
+    (1, 2, 960, 50),        # one item of 8 tiles: 4
+    (1, 2, 590, 40),        # of 5: 5
+    (1, 2, 730, 30),        # of 6: 6
+    (1, 2, 850, 40),        # of 7: 7
+    (1, 2, 3100, 60),       # of 25: 8
+    (1, 1, 3100, 200), (3, 1, 1500, 300), (16, 16, 300, 140)])
+def test_every_cluster_size(hkv, group, prior, chunk):
+    pools, q, row = _case(prior, chunk, hkv, group, seed=9)
+    _check(pools, q, row, prior, _run(pools, q, row, prior))
