@@ -389,8 +389,8 @@ pkv_status pkv_paged_decode_attention_fp8(void *out, const void *q, const void *
  * ------------------------------------------------------------------------- */
 
 /* Quantise and scatter new keys and values, optionally rotated (cos_sin not
- * NULL; keys turn in fp32 and are rounded once, to E4M3), and rotate the
- * queries.  bf16 input; head_dim a multiple of 16 up to 128, rot_dim a
+ * NULL; a key's code is that of its rotation in fp64: one rounding, to E4M3),
+ * and rotate the queries.  bf16 input; head_dim a multiple of 16 up to 128, rot_dim a
  * multiple of 16 (PKV_EUNSUPPORTED otherwise).
  *   Slots: the new rows of one block must be consecutive entries of
  * slot_mapping with consecutive slots (a run), as the tokens of a sequence in

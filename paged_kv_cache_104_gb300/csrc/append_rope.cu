@@ -5,7 +5,8 @@
 // rot_dim/2) or, interleaved, (2i, 2i + 1); pair i of token t turns by the
 // angle whose cosine and sin stand in the table row of positions[axis(i)][t]:
 //   a' = a cos - b sin,  b' = b cos + a sin
-// in fp32, rounded once to the storage type.  The other elements are copied.
+// in fp32, rounded once to the storage type (to E4M3 from the exact value).  The
+// other elements are copied.
 // The axis of a pair is the caller's table, so one axis (text), sections of
 // time, height and width, or axes taken in turn are one kernel.
 #include <algorithm>
@@ -267,6 +268,13 @@ constexpr int kWindow = 16;       // tokens of a CTA
 constexpr int kRowLanes = 16;     // threads of a row, 8 elements (16 bytes) each
 constexpr int kAppendThreads = kWindow * kRowLanes;
 
+// x cos + y sin to within 2 ulps of the result, whatever cancels: where the
+// sum loses 8 bits or more it is exact, and the product's own error is added.
+__device__ __forceinline__ float turned(float x, float y, float c, float s) {
+  const float p = y * s;
+  return fmaf(x, c, p) - fmaf(-y, s, p);   // subtracted: a zero keeps its sign
+}
+
 // A thread's 8 elements of a row (chunk c) turned, or as they are.  Every lane
 // of the warp calls it: the other side of a half's pairs comes by shuffle.
 struct RowTurn {
@@ -294,8 +302,8 @@ struct RowTurn {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float a = x[2 * i], b = x[2 * i + 1];
-        x[2 * i] = a * w.c[i] - b * w.s[i];
-        x[2 * i + 1] = b * w.c[i] + a * w.s[i];
+        x[2 * i] = turned(a, -b, w.c[i], w.s[i]);
+        x[2 * i + 1] = turned(b, a, w.c[i], w.s[i]);
       }
       return;
     }
@@ -311,9 +319,40 @@ struct RowTurn {
     Elem<__nv_bfloat16>::unpack(o, y);
 #pragma unroll
     for (int i = 0; i < 8; ++i)   // a' = a cos - b sin, or b' = b cos + a sin
-      x[i] = x[i] * w.c[i] + (second ? y[i] : -y[i]) * w.s[i];
+      x[i] = turned(x[i], second ? y[i] : -y[i], w.c[i], w.s[i]);
   }
 };
+
+// Keys turn in fp32, which can fall on the other side of the middle between
+// two codes than the exact value does.  So the elements within kNear ulps of a
+// middle (five in a million) are turned again in fp64, and a key's code is the
+// exact value's.  A middle has the 20 lowest of fp32's bits 0x80000, brought to
+// the top here; below 2^-6, where codes are 2^-9 apart, so it has with 2^-6
+// added.
+// (A chunk of 2,048 tokens takes 13.6 us, with the fp32 values' codes 13.0 us;
+// all in fp64, at 2 operations a clock and SM, would take 10 us more.)
+constexpr uint32_t kNear = 4;
+__device__ __forceinline__ uint32_t off_middle(float y) {
+  return __float_as_uint(y) * 4096u - ((0x80000u - kNear) << 12);
+}
+constexpr uint32_t kAtMiddle = (2 * kNear + 1) << 12;   // off_middle of near ones is less
+
+// The code of element el of token t's key row, turned in fp64, times inv.
+__device__ __noinline__ uint32_t exact_code(const RopeArgs& r, int64_t num_tokens,
+                                            const __nv_bfloat16* row, int64_t t, int el, float inv) {
+  const int half = r.rot_dim / 2;
+  const int i = r.interleaved ? el >> 1 : el % half;
+  const bool second = r.interleaved ? (el & 1) : el >= half;
+  const int other = r.interleaved ? el ^ 1 : (second ? el - half : el + half);
+  const float* turn =
+      r.cos_sin + (int64_t)r.positions[r.pair_axis[i] * num_tokens + t] * r.rot_dim + i;
+  const double x = (double)__bfloat162float(row[el]) * turn[0];
+  const double y = (double)__bfloat162float(row[other]) * turn[half];
+  const double z = (second ? x + y : x - y) * inv;
+  float f = __double2float_rz(z);
+  if ((double)f != z) f = __uint_as_float(__float_as_uint(f) | 1u);   // not a middle
+  return f32x2_to_e4m3x2(f, 0.f) & 0xffu;
+}
 
 // Of a window: run_of[j], the run that token j belongs to (-1: none that starts
 // here), and of the run that starts at token k its slot, old scale bytes and
@@ -325,6 +364,15 @@ struct WindowRuns {
   int64_t slot[kWindow];
   int old[UPC][kWindow];
   uint32_t top[UPC][kWindow];
+  // whether the rows before run k (of head u) stand for something
+  __device__ __forceinline__ bool held(int u, int k) const {
+    return old[u][k] >= 1 && old[u][k] <= 253;
+  }
+  // the run's scale exponent
+  __device__ __forceinline__ int exponent(int u, int k, int row0) const {
+    const int e = scale_exp(top[u][k]);
+    return row0 > 0 && held(u, k) ? max(e, old[u][k] - 127) : e;
+  }
 };
 
 // Warp 0's part: lane l looks at entry w0 + l (slot) and w0 - 1 - l (back).
@@ -375,23 +423,24 @@ __device__ __forceinline__ void find_runs(const RopeAppendArgs& a, WindowRuns<UP
 }
 
 // The codes of token j (elements v of chunk c, pool and head `tile`) of run k,
-// and the run's scale.
+// and the run's scale.  Returns the elements, one bit each, whose code
+// exact_code has to say (is_turned: v was turned).
 template <int UPC>
-__device__ __forceinline__ void write_codes(const RopeAppendArgs& a, const WindowRuns<UPC>& runs,
-                                            uint8_t* pools, uint8_t* scales, const float (&v)[8],
-                                            int u, int g, int j, int k, int c) {
+__device__ __forceinline__ uint32_t write_codes(const RopeAppendArgs& a,
+                                                const WindowRuns<UPC>& runs, uint8_t* pools,
+                                                uint8_t* scales, const float (&v)[8],
+                                                int u, int g, int j, int k, int c, bool is_turned) {
   const int64_t slot = runs.slot[k], blk = slot / kBlockSize;
   const int row0 = (int)(slot - blk * kBlockSize), row = row0 + j - k;
   const int64_t tile = blk * a.num_kv_heads + g;
   uint8_t* pool = pools + tile * kBlockSize * a.head_dim + c * 8;
-  int e = scale_exp(runs.top[u][k]);
-  if (row0 > 0) {
+  const int e = runs.exponent(u, k, row0);
+  if (row0 > 0 && j == k) {
     // where the scale grows, the block's older rows are re-expressed, by the
     // threads of the run's first token
-    const int b = runs.old[u][k];
-    const bool held = b >= 1 && b <= 253;      // otherwise they stand for nothing
-    const int e_old = held ? b - 127 : e;
-    if (j == k && (!held || e > e_old)) {
+    const bool held = runs.held(u, k);
+    const int e_old = held ? runs.old[u][k] - 127 : e;
+    if (!held || e > e_old) {
       const float f = held ? exp2i(max(e_old - e, -126)) : 0.f;
 #pragma unroll 1
       for (int o = 0; o < row0; ++o) {
@@ -408,14 +457,34 @@ __device__ __forceinline__ void write_codes(const RopeAppendArgs& a, const Windo
         *p = held ? make_uint2(again(w.x), again(w.y)) : make_uint2(0u, 0u);
       }
     }
-    e = max(e, e_old);
   }
   const float inv = exp2i(-e);
   uint32_t n[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) n[q] = f32x2_to_e4m3x2(v[2 * q] * inv, v[2 * q + 1] * inv);
-  *reinterpret_cast<uint2*>(pool + row * a.head_dim) = make_uint2(n[0] | n[1] << 16, n[2] | n[3] << 16);
+  const uint2 codes = make_uint2(n[0] | n[1] << 16, n[2] | n[3] << 16);
+  *reinterpret_cast<uint2*>(pool + row * a.head_dim) = codes;
   if (j == k && c == 0) scales[tile] = (uint8_t)(e + 127);
+  if (!is_turned) return 0;
+  constexpr float kSmall = 0.015625f;          // 2^-6
+  uint32_t nearest = ~0u, least = ~0u;         // (a zero counts as large: it is exact)
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    nearest = min(nearest, off_middle(v[q] * inv));
+    least = min(least, __float_as_uint(v[q] * inv) * 2u - 1u);
+  }
+  // (an infinite element, which turned() made a NaN, is one of them too)
+  const uint32_t nan = (((codes.x & 0x7f7f7f7fu) + 0x01010101u) |
+                        ((codes.y & 0x7f7f7f7fu) + 0x01010101u)) & 0x80808080u;
+  if (nearest >= kAtMiddle && least >= __float_as_uint(kSmall) * 2u && nan == 0) return 0;
+  uint32_t again = 0;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const float y = fabsf(v[q] * inv);
+    const bool near = off_middle(y < kSmall ? y + kSmall : y) < kAtMiddle;
+    again |= (near || y != y ? 1u : 0u) << q;
+  }
+  return again;
 }
 
 // The first kv_ctas CTAs take the runs of new tokens that start in a window of
@@ -528,9 +597,21 @@ kv_append_fp8_block_kernel(const __grid_constant__ RopeAppendArgs a, int kv_ctas
   };
   auto write = [&](int j, int k) {
     if (k < 0 || !mine) return;
+    uint32_t again = 0;
+    const bool turned_here = rotated && c * 8 < a.rope.rot_dim;
 #pragma unroll
     for (int u = 0; u < UPC; ++u)
-      if (u < ng) write_codes<UPC>(a, runs, pools, scales, x[u], u, g0 + u, j, k, c);
+      if (u < ng)
+        again |= write_codes<UPC>(a, runs, pools, scales, x[u], u, g0 + u, j, k, c, turned_here)
+                 << 8 * u;
+    for (; again; again &= again - 1) {
+      const int u = (__ffs(again) - 1) >> 3, el = c * 8 + ((__ffs(again) - 1) & 7);
+      const int64_t at = runs.slot[k], tile = at / kBlockSize * a.num_kv_heads + g0 + u;
+      const int row0 = (int)(at % kBlockSize);
+      pools[(tile * kBlockSize + row0 + j - k) * a.head_dim + el] = (uint8_t)exact_code(
+          a.rope, a.num_tokens, src - c * 8 + (w0 + j) * stride + u * a.head_dim, w0 + j, el,
+          exp2i(-runs.exponent(u, k, row0)));
+    }
   };
   turn_rows();
   if (UPC == 1) __syncthreads();
@@ -613,7 +694,8 @@ cudaError_t launch_kv_append_fp8_block(const RopeAppendArgs& args, cudaStream_t 
   a.rope.whole_axes = axes_by_chunk(a, 8);
   const int64_t windows = (a.num_tokens + kWindow - 1) / kWindow;
   // few windows: a head to a CTA, for latency; many: 4 heads share slots,
-  // positions and table (a chunk of 2,048 tokens: 13.0 us, 2 heads 16.5 us)
+  // positions and table (a chunk of 2,048 tokens: 13.6 us; before the exact
+  // codes 13.0 us, and with 2 heads to a CTA 16.5 us)
   const bool few = windows * 2 * a.num_kv_heads <= 152 * 4;
   const int64_t kv_ctas = windows * 2 * (few ? a.num_kv_heads : (a.num_kv_heads + 3) / 4);
   const int units = a.head_dim / 16;

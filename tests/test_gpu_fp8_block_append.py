@@ -1,10 +1,10 @@
 """kv_append_fp8_block on the GPU against the oracle's quantiser.
 
-Without a rotation everything is exact: codes and scale bytes equal the
-oracle's bit for bit.  With one the keys turn in fp32 (within 2^-23 (|a| + |b|)
-of the fp64 value, see the rotating append's tests) before their one rounding,
-to nearest E4M3: at most half a step, 2^-4 relative to the rounded value's
-binade or 2^-10 of the scale below the normal range."""
+Codes and scale bytes equal the oracle's bit for bit, with a rotation too: the
+keys' one rounding is that of the fp64 rotation.  (test_rotated asks for less:
+the fp32 rotation, within 2^-23 (|a| + |b|) of the fp64 one, and half a step of
+E4M3, 2^-4 relative to the rounded value's binade or 2^-10 of the scale below
+the normal range.)"""
 import numpy as np
 import pytest
 import torch
@@ -164,6 +164,68 @@ def test_rotated(d, rot, interleaved, axes, pieces):
     B.kv_append_rope(ref, q.cuda(), k.cuda(), v.cuda(), pool, pool.clone(), slots.cuda(), pos.cuda(),
                      B.Rope(cs.cuda(), interleaved, axis))
     assert torch.equal(qo, ref)
+
+
+def _rotated_exactly(k, cs, pos, interleaved, codes, scale, slots):
+    """The key pool against the oracle's codes of the fp64 rotation (NaN: of either sign)."""
+    c, s = _append(k, k, codes, scale, slots, positions=pos.cuda(), rope=B.Rope(cs.cuda(), interleaved))
+    assert B.get_device_error() == 0
+    oc, os_ = codes[0].numpy().copy(), scale[0].numpy().copy()
+    with np.errstate(invalid="ignore"):
+        FB.append_pool(O.rotate(k.double().numpy(), cs.numpy(), pos.numpy(), interleaved), oc, os_, slots.tolist())
+    got = c[0].numpy().copy()
+    for x in (got, oc):
+        x[(x & 0x7F) == 0x7F] = 0x7F
+    assert np.array_equal(s[0].numpy(), os_)
+    assert np.array_equal(got, oc)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("outlier", [1.0, 200.0])        # 200: most codes are subnormal
+def test_rotated_codes_are_those_of_the_exact_keys(interleaved, outlier):
+    """Of two million codes some lie where fp32 falls on the other side of a middle."""
+    t, hkv, d = 2040, 8, 128
+    _, k, _, pos = R.draw(t, 1, hkv, d, torch.bfloat16, 21)
+    k[:, :, 5] *= outlier
+    codes, scale = _pools(131, hkv, d, 21)
+    _rotated_exactly(k, R.table(997, d), pos, interleaved, codes, scale, R.run_slots([(7, t)], 131, 21))
+
+
+@pytest.mark.parametrize("tokens", [1, 40])              # a head to a CTA, and four
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rotated_values_beside_the_middle_of_two_codes(interleaved, tokens):
+    hkv, d = 72 if tokens == 40 else 2, 32
+    first, second = O.pair_columns(d, interleaved)
+    k = torch.zeros(tokens, hkv, d)
+    cs = torch.zeros(4, d)
+    cs[:, :d // 2], cs[:, d // 2:] = 1.0, 2.0 ** -20
+    # middles: of normal codes, beside the subnormal ones, of those, of 0 and the least
+    middle = [1.0625, 1.1875, 248.0, -1.9375, 2.0 ** -6 * 1.0625, 2.0 ** -7 + 2.0 ** -10, 3 * 2.0 ** -10, -5 * 2.0 ** -10,
+              2.0 ** -10, 15 * 2.0 ** -10, 13 * 2.0 ** -10]
+    for i, m in enumerate(middle):
+        k[:, :, first[i]] = m
+        k[:, :, second[i]] = 2.0 ** -18 * m * (1 if i % 2 else -1)    # m -+ 2^-38 m
+    k[:, :, first[13]] = 400.0                                        # the scale is 1
+    k[:, :, first[14]], k[:, :, second[14]] = 1.5, 1.5
+    k[:, :, second[15]] = 0.0
+    cs[1] = -cs[1]
+    cs[2, 14], cs[2, d // 2 + 14] = 1.0 + 2.0 ** -23, 1.0             # cancels to 1.5 * 2^-23
+    cs[3, 14], cs[3, d // 2 + 14] = 1.0 + 2.0 ** -8, 1.0 - 2.0 ** -24
+    k = k.bfloat16()
+    pos = (torch.arange(tokens) % 4).to(torch.int32)[None]
+    codes, scale = _pools(5, hkv, d, 22)
+    for at in range(4):
+        _rotated_exactly(k, cs, (pos + at) % 4, interleaved, codes, scale, R.run_slots([(0, tokens)], 5, 22))
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rotated_infinities_and_nan(interleaved):
+    t, hkv, d = 20, 2, 64
+    _, k, _, pos = R.draw(t, 1, hkv, d, torch.bfloat16, 23)
+    k[3, 0, 1], k[4, 1, 40], k[5, 0, 33], k[6, 0, 2] = float("inf"), -float("inf"), float("inf"), float("nan")
+    k[7, 1, 9], k[8, 0, 10] = 3e38, -3e38
+    codes, scale = _pools(3, hkv, d, 23)
+    _rotated_exactly(k, R.table(997, d), pos, interleaved, codes, scale, R.run_slots([(4, t)], 3, 23))
 
 
 def test_bad_position_skips_the_rest_of_its_run():
