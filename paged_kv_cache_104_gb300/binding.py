@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -79,6 +80,10 @@ class RopeAppendArgs(ctypes.Structure):
                 ("pair_axis", ctypes.c_void_p)]
 
 
+# The same by struct: packing takes 0.2 us, filling the ctypes structure 0.9 us
+_ROPE_APPEND = struct.Struct("@9P6q5iPqP3iP")
+
+
 class PagedKVError(RuntimeError):
     def __init__(self, fn: str, status: int, msg: str):
         super().__init__(f"{fn} failed: status {status} ({msg})")
@@ -118,6 +123,9 @@ def open_library(path: str):
         fn = getattr(lib, name)
         fn.argtypes = [ctypes.POINTER(RopeAppendArgs), p]
         fn.restype = ctypes.c_int
+        packed = lib[name]                # of its own prototype, for _ROPE_APPEND's bytes
+        packed.argtypes, packed.restype = [ctypes.c_char_p, p], ctypes.c_int
+        setattr(lib, name + "_packed", packed)
     lib.pkv_decode_fp8_block_workspace_bytes.argtypes = [i, i, i, i, i]
     lib.pkv_decode_fp8_block_workspace_bytes.restype = sz
     lib.pkv_paged_decode_attention_fp8_block.argtypes = [p, p, p, p, p, p, p, p, i, i, i, i64, i, i,
@@ -383,7 +391,7 @@ class Rope:
         self.cos_sin = cos_sin
         self.num_positions, self.rot_dim = cos_sin.shape
         self.interleaved = bool(interleaved)
-        self.num_axes, self._pair_axis, self._pair_ptr = 1, None, None
+        self.num_axes, self._pair_axis, self._pair_ptr = 1, None, 0
         if pair_axis is not None:
             axes = [int(x) for x in pair_axis]
             if len(axes) != self.rot_dim // 2:
@@ -407,7 +415,7 @@ def _rope_append(fn, call, slots_check, q_out, q, k_new, v_new, k_cache, v_cache
     ks = _token_stride(fn, "k_new", k_new, dtype, heads, index)
     vs = _token_stride(fn, "v_new", v_new, dtype, heads, index)
     hq = qs = qos = 0
-    qp = qop = None
+    qp = qop = 0
     if q is not None or q_out is not None:
         if q is None or q_out is None or q.dim() != 3:
             _refuse(fn, "q and q_out go together, [tokens, heads, head_dim]")
@@ -415,7 +423,7 @@ def _rope_append(fn, call, slots_check, q_out, q, k_new, v_new, k_cache, v_cache
         qs = _token_stride(fn, "q", q, dtype, (t, hq, d), index)
         qos = _token_stride(fn, "q_out", q_out, dtype, (t, hq, d), index)
         qp, qop = q.data_ptr(), q_out.data_ptr()
-    table = pos = pair = None
+    table = pos = pair = 0
     num_positions = rot = axes = inter = 0
     if rope is not None:
         axes, rot, num_positions = rope.num_axes, rope.rot_dim, rope.num_positions
@@ -425,14 +433,14 @@ def _rope_append(fn, call, slots_check, q_out, q, k_new, v_new, k_cache, v_cache
         pos = _whole(fn, "positions", positions, torch.int32, one, index)
         table = _whole(fn, "cos_sin", rope.cos_sin, torch.float32, (num_positions, rot), index)
         pair, inter = rope._pair_ptr, rope.interleaved
-    a = RopeAppendArgs(qop, qp, k_new.data_ptr(), v_new.data_ptr(), kp, vp, scale_ptrs[0],
-                       scale_ptrs[1], sp, t, nb, qos, qs, ks, vs, hq, hkv, d, bs, dtype_code, table,
-                       num_positions, pos, axes, rot, inter, pair)
+    a = _ROPE_APPEND.pack(qop, qp, k_new.data_ptr(), v_new.data_ptr(), kp, vp, scale_ptrs[0],
+                          scale_ptrs[1], sp, t, nb, qos, qs, ks, vs, hq, hkv, d, bs, dtype_code,
+                          table, num_positions, pos, axes, rot, inter, pair)
     if _debug:
         _validate(fn, slots_check, slot_mapping, nb, bs)
         if rope is not None:
             _validate(fn, "check_positions", positions, slot_mapping, num_positions)
-    status = call(ctypes.byref(a), _stream_on(stream, index))
+    status = call(a, _stream_on(stream, index))
     if status:
         _check(fn, status)
 
@@ -449,8 +457,8 @@ def kv_append_rope(q_out, q, k_new, v_new, k_cache, v_cache, slot_mapping, posit
         _refuse(fn, "no rope")
     dtype = k_cache.dtype
     code = _dtype_code(k_cache)
-    _rope_append(fn, load().pkv_kv_append_rope, "check_slots", q_out, q, k_new, v_new, k_cache,
-                 v_cache, (None, None), slot_mapping, positions, rope, dtype, code,
+    _rope_append(fn, load().pkv_kv_append_rope_packed, "check_slots", q_out, q, k_new, v_new, k_cache,
+                 v_cache, (0, 0), slot_mapping, positions, rope, dtype, code,
                  _device_of(fn, k_cache), stream)
 
 
@@ -467,7 +475,7 @@ def kv_append_fp8_block(k_new, v_new, k_cache, v_cache, k_scale, v_scale, slot_m
     if rope is None and q is not None:
         _refuse(fn, "queries need a rope")
     index = _device_of(fn, k_cache)
-    _rope_append(fn, load().pkv_kv_append_fp8_block, "check_runs", q_out, q, k_new, v_new, k_cache,
+    _rope_append(fn, load().pkv_kv_append_fp8_block_packed, "check_runs", q_out, q, k_new, v_new, k_cache,
                  v_cache, _block_scales(fn, k_cache, k_scale, v_scale, index), slot_mapping, positions,
                  rope, torch.bfloat16, PKV_BF16, index, stream)
 

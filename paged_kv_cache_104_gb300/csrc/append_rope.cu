@@ -325,7 +325,7 @@ struct RowTurn {
 
 // Keys turn in fp32, which can fall on the other side of the middle between
 // two codes than the exact value does.  So the elements within kNear ulps of a
-// middle (five in a million) are turned again in fp64, and a key's code is the
+// middle (nine in a million) are turned again in fp64, and a key's code is the
 // exact value's.  A middle has the 20 lowest of fp32's bits 0x80000, brought to
 // the top here; below 2^-6, where codes are 2^-9 apart, so it has with 2^-6
 // added.

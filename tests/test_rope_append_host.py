@@ -214,3 +214,8 @@ def test_debug_mode_names_the_entry(monkeypatch):
             B.kv_append_rope(q, q, k, v, kc, vc, slots, pos[:, :3].contiguous(), rope)
     finally:
         B.set_debug(False)
+
+
+def test_packed_arguments_are_the_structure():
+    values = list(range(1, 28))
+    assert bytes(B.RopeAppendArgs(*values)) == B._ROPE_APPEND.pack(*values)
