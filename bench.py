@@ -412,7 +412,7 @@ def run_fp8_decode(args, w, lay, inputs, dev, stream, dist, n):
             "kernel": "kv_append_fp8 + paged_decode_attention_fp8 (split-K main + reduce), one "
                       "layer", "bound": "hbm",
             "achieved": leg_gbs, "peak": hbm_peak, "unit": "GB/s", "frac": leg_gbs / hbm_peak,
-            "traffic": profiled_traffic("decode_fp8_kernel", "decode_fp8.cu"),
+            "traffic": profiled_traffic("decode_fp8_kernel", "decode_fp8_kernel.cuh"),
             "algorithmic_bytes_per_launch": dec_bytes + app_bytes,
             "timing": "one layer's append + decode call = the timed step over L (CUDA events "
                       "around the replays of a graph with no other work); "
