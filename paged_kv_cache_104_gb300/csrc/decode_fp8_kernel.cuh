@@ -38,12 +38,14 @@
 // Block scales (BS).  The tile of one consumer warp and stage is one block of
 // one head, so its two scales are uniform over the tile's products: the K
 // scale multiplies the scores, and with the V scale 2^ev the weight of key j
-// in the output is 2^(s_j + ev).  The weights of the output and of the
-// softmax sum then differ block by block, so each has its own running
-// reference: l = sum 2^(s_j - m) and O = sum 2^(s_j + ev_j - M) code_j, the
-// result O 2^(M - m) / l.  One common reference would let the f16 weights of
-// a block underflow whose V scale is small beside the others': an all-zero V
-// block must still count in l.  Cost: a second exponential for every score.
+// in the output is p_j = 2^(s_j + ev - M), M the running reference of s + ev.
+// O = sum p_j code_j, and the softmax sum is l = sum p_j 2^(E - ev), E the ev of
+// the warp's first block: a factor for each block, no second exponential.  The
+// result is O 2^E / l.  A block whose ev is more than kWide8 off E could lose
+// its weight in l to the fp32 range of p (an all-zero V block has the smallest
+// ev there is, and must still count): from the first such block on, l is summed
+// from exponentials of its own, against a reference m of its own, and the
+// result is O 2^(M - m) / l.
 // Each consumer warp reads its own blocks' scale bytes, one block per lane, a
 // window of 32 stages ahead.  Queries are brought to [1, 2) times a power of
 // two by head before they become f16, which then loses nothing to its range.
@@ -73,6 +75,7 @@ constexpr int kRing8 = kNST8 * kStage8;
 constexpr int kHD = 128;
 constexpr int kCombRow = kHD + 4;                // padded row of the merge buffer
 constexpr float kLazy8 = 8.0f;
+constexpr int kWide8 = 40;                       // BS: binades between V scales
 constexpr unsigned kAll8 = 0xffffffffu;
 
 static_assert(kSplitTokens % kStageTok == 0, "a split holds whole stages");
@@ -147,6 +150,14 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ uint4 lds128(const unsigned char* p) {
   return *reinterpret_cast<const uint4*>(p);
+}
+
+// A load that stays where it is written, ahead of what waits for other loads
+__device__ __forceinline__ uint4 ld_now(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
 }
 
 // The value 2^(b - 127) of a scale byte (0 reads as zero, 255 as infinity).
@@ -296,8 +307,10 @@ decode_fp8_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tm_k,
     const int32_t* u_ids = a.block_table + (int64_t)u.b * a.bt_stride + u_blk0;
     auto stage_block = [&](int st0) {
       const int i = HS ? st0 + lane : (st0 + lane) * kBPS + warp;
-      const int blk = i < u_nblk ? __ldg(u_ids + i) : 0;
-      return blk < 0 || (int64_t)blk >= a.num_blocks ? 0 : blk;   // the producer reports it
+      return i < u_nblk ? __ldg(u_ids + i) : 0;
+    };
+    auto in_pool = [&](int blk) {       // the producer reports one that is not
+      return blk < 0 || (int64_t)blk >= a.num_blocks ? 0 : blk;
     };
     auto stage_scales = [&](int blk) {
       const int64_t i = (int64_t)blk * a.num_kv_heads + head;
@@ -305,9 +318,22 @@ decode_fp8_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tm_k,
     };
     uint32_t sc_cur = 0, sc_next = 0;
     int blk_next = 0;
+    // the queries too, before the ids are waited for (ragged batch 257 -> 251 us);
+    // a lane without a head takes the last one's, and its results are not written
+    uint4 qv[BS ? NT : 1][4];
     if constexpr (BS) {
-      const int b0 = stage_block(0);
+      int b0 = stage_block(0);
       blk_next = stage_block(32);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int hh = min(8 * nt + g, G - 1);
+        const uint4* qrow = reinterpret_cast<const uint4*>(
+            q32 + ((int64_t)u.b * a.num_q_heads + hq0 + hh) * (kHD / 2) + 16 * t);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) qv[nt][i] = ld_now(qrow + i);
+      }
+      b0 = in_pool(b0);
+      blk_next = in_pool(blk_next);
       sc_cur = stage_scales(b0);
       sc_next = stage_scales(blk_next);
       blk_next = stage_block(64);
@@ -319,18 +345,12 @@ decode_fp8_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tm_k,
     for (int nt = 0; nt < NT; ++nt) {
       const int hh = 8 * nt + g;
       if constexpr (BS) {
-        uint4 v[4];
+        const uint4 (&v)[4] = qv[nt];
         uint32_t top = 0;   // the largest magnitude's bf16 bits among this lane's 32 elements
-        if (hh < G) {
-          const uint4* qrow = reinterpret_cast<const uint4*>(
-              q32 + ((int64_t)u.b * a.num_q_heads + hq0 + hh) * (kHD / 2) + 16 * t);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            v[i] = __ldg(qrow + i);
-            top = __vmaxu2(top, __vmaxu2(__vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu),
-                                         __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu)));
-          }
-        }
+        for (int i = 0; i < 4; ++i)
+          top = __vmaxu2(top, __vmaxu2(__vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu),
+                                       __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu)));
         top = max(top & 0xffffu, top >> 16);
         top = max(top, __shfl_xor_sync(kAll8, top, 1));
         top = max(top, __shfl_xor_sync(kAll8, top, 2));
@@ -380,7 +400,9 @@ decode_fp8_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
       for (int mt = 0; mt < 8; ++mt) o[nt][mt][0] = o[nt][mt][1] = o[nt][mt][2] = o[nt][mt][3] = 0.f;
     float m_run[NT][2], l_run[NT][2];
-    float mo_run[NT][2];   // BS: the output weights' reference M
+    float mo_run[NT][2];   // BS: the reference M of s + ev (m_run is formed at the end)
+    bool wide = false;     // BS: l is summed against m_run
+    int e_ref = 0;         // BS: E
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       if constexpr (BS) mo_run[nt][0] = mo_run[nt][1] = -INFINITY;
@@ -393,16 +415,20 @@ decode_fp8_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tm_k,
     for (int st = 0; st < nst; ++st, ++consumed) {
       const int buf = consumed % kNST8;
       const uint32_t phase = (consumed / kNST8) & 1;
-      float kscale = 1.f, ev = 0.f;   // BS: the tile's K scale, and log2 of its V scale
+      float kscale = 1.f, ev = 0.f;   // BS: the tile's K scale, log2 of its V scale
+      int off = 0;                    // and E - ev
       if constexpr (BS) {
         if (st > 0 && (st & 31) == 0) {
           sc_cur = sc_next;
-          sc_next = stage_scales(blk_next);
+          sc_next = stage_scales(in_pool(blk_next));
           blk_next = stage_block(st + 64);
         }
         const uint32_t sc = __shfl_sync(kAll8, sc_cur, st & 31);
         kscale = scale_of(sc & 0xffu);
-        ev = (float)((int)(sc >> 8) - 127);
+        const int e = (int)(sc >> 8) - 127;
+        if (st == 0) e_ref = e;       // a warp without a block here has none in the unit
+        ev = (float)e;
+        off = e_ref - e;
       }
       if (!*vabort) {
         if (!mbar_wait(full0 + 8 * buf, phase, a.err)) *vabort = 1;
@@ -461,18 +487,44 @@ decode_fp8_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tm_k,
       const bool k0ok = g < valid, k1ok = g + 8 < valid;
       float v[NT][4];
       bool grow = false;
+      if constexpr (BS) {
+        if (wide || abs(off) > kWide8) {   // the same in every lane; rare
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              // m waits in shared memory: registers are short
+              const int hh = 8 * nt + 2 * t + j;
+              float* wm = comb_ml + (warp * G + min(hh, G - 1)) * 2;
+              const float m_old = wide ? *wm : mo_run[nt][j] - (float)e_ref;
+              const float k = slq[nt][j] * kscale;
+              const float x0 = k0ok ? s[nt][j] * k : -INFINITY;
+              const float x1 = k1ok ? s[nt][j + 2] * k : -INFINITY;
+              float mx = fmaxf(fmaxf(x0, x1), m_old);
+              mx = fmaxf(mx, __shfl_xor_sync(kAll8, mx, 4));
+              mx = fmaxf(mx, __shfl_xor_sync(kAll8, mx, 8));
+              mx = fmaxf(mx, __shfl_xor_sync(kAll8, mx, 16));
+              if (mx != m_old) l_run[nt][j] *= ex2(m_old - mx);
+              l_run[nt][j] += ex2(x0 - mx) + ex2(x1 - mx);
+              __syncwarp();
+              if (g == 0 && hh < G) *wm = mx;
+            }
+          __syncwarp();
+          wide = true;
+        }
+      }
+      float (&ref)[NT][2] = BS ? mo_run : m_run;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          v[nt][i] = (i < 2 ? k0ok : k1ok) ? s[nt][i] * (BS ? slq[nt][i & 1] * kscale : sl2) : -INFINITY;
-          grow |= v[nt][i] > m_run[nt][i & 1] + kLazy8;
-          if constexpr (BS) grow |= v[nt][i] + ev > mo_run[nt][i & 1] + kLazy8;
+          const float x = BS ? fmaf(s[nt][i], slq[nt][i & 1] * kscale, ev) : s[nt][i] * sl2;
+          v[nt][i] = (i < 2 ? k0ok : k1ok) ? x : -INFINITY;
+          grow |= v[nt][i] > ref[nt][i & 1] + kLazy8;
         }
       if (__any_sync(kAll8, grow)) {
         bool rescale = false;
         float alpha[NT][2];
-        float beta[NT][2];   // the factors of l and of O
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -481,31 +533,25 @@ decode_fp8_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tm_k,
             mx = fmaxf(mx, __shfl_xor_sync(kAll8, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(kAll8, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(kAll8, mx, 16));
-            float m_new = m_run[nt][j];
+            float m_new = ref[nt][j];
             if (mx > m_new + kLazy8 || m_new == -INFINITY) m_new = mx;
-            alpha[nt][j] = (m_new == m_run[nt][j]) ? 1.f : ex2(m_run[nt][j] - m_new);
-            m_run[nt][j] = m_new;
-            if constexpr (BS) {
-              float mo_new = mo_run[nt][j];
-              if (mx + ev > mo_new + kLazy8 || mo_new == -INFINITY) mo_new = mx + ev;
-              beta[nt][j] = (mo_new == mo_run[nt][j]) ? 1.f : ex2(mo_run[nt][j] - mo_new);
-              mo_run[nt][j] = mo_new;
-            } else {
-              beta[nt][j] = alpha[nt][j];
-            }
-            rescale |= alpha[nt][j] != 1.f || beta[nt][j] != 1.f;
+            alpha[nt][j] = (m_new == ref[nt][j]) ? 1.f : ex2(ref[nt][j] - m_new);
+            ref[nt][j] = m_new;
+            rescale |= alpha[nt][j] != 1.f;
           }
         if (__any_sync(kAll8, rescale)) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            l_run[nt][0] *= alpha[nt][0];
-            l_run[nt][1] *= alpha[nt][1];
+            if (!BS || !wide) {
+              l_run[nt][0] *= alpha[nt][0];
+              l_run[nt][1] *= alpha[nt][1];
+            }
 #pragma unroll
             for (int mt = 0; mt < 8; ++mt) {
-              o[nt][mt][0] *= beta[nt][0];
-              o[nt][mt][1] *= beta[nt][1];
-              o[nt][mt][2] *= beta[nt][0];
-              o[nt][mt][3] *= beta[nt][1];
+              o[nt][mt][0] *= alpha[nt][0];
+              o[nt][mt][1] *= alpha[nt][1];
+              o[nt][mt][2] *= alpha[nt][0];
+              o[nt][mt][3] *= alpha[nt][1];
             }
           }
         }
@@ -513,20 +559,21 @@ decode_fp8_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tm_k,
       uint32_t pb0[NT], pb1[NT];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
+        const float p0 = ex2(v[nt][0] - ref[nt][0]), p1 = ex2(v[nt][1] - ref[nt][1]);
+        const float p2 = ex2(v[nt][2] - ref[nt][0]), p3 = ex2(v[nt][3] - ref[nt][1]);
+        const uint32_t x0 = pack2_f16(p0, p1), x1 = pack2_f16(p2, p3);
         if constexpr (BS) {
-          l_run[nt][0] += ex2(v[nt][0] - m_run[nt][0]) + ex2(v[nt][2] - m_run[nt][0]);
-          l_run[nt][1] += ex2(v[nt][1] - m_run[nt][1]) + ex2(v[nt][3] - m_run[nt][1]);
-          const float r0 = mo_run[nt][0] - ev, r1 = mo_run[nt][1] - ev;
-          pb0[nt] = movm_t(pack2_f16(ex2(v[nt][0] - r0), ex2(v[nt][1] - r1)));
-          pb1[nt] = movm_t(pack2_f16(ex2(v[nt][2] - r0), ex2(v[nt][3] - r1)));
-          continue;
+          if (!wide) {
+            const float f = __uint_as_float((uint32_t)(127 + off) << 23);
+            l_run[nt][0] = fmaf(p0 + p2, f, l_run[nt][0]);
+            l_run[nt][1] = fmaf(p1 + p3, f, l_run[nt][1]);
+          }
+        } else {
+          const __half2 h0 = *reinterpret_cast<const __half2*>(&x0);   // key g,     heads 2t, 2t+1
+          const __half2 h1 = *reinterpret_cast<const __half2*>(&x1);   // key g + 8, heads 2t, 2t+1
+          l_run[nt][0] += __low2float(h0) + __low2float(h1);
+          l_run[nt][1] += __high2float(h0) + __high2float(h1);
         }
-        const uint32_t x0 = pack2_f16(ex2(v[nt][0] - m_run[nt][0]), ex2(v[nt][1] - m_run[nt][1]));
-        const uint32_t x1 = pack2_f16(ex2(v[nt][2] - m_run[nt][0]), ex2(v[nt][3] - m_run[nt][1]));
-        const __half2 h0 = *reinterpret_cast<const __half2*>(&x0);   // key g,     heads 2t, 2t+1
-        const __half2 h1 = *reinterpret_cast<const __half2*>(&x1);   // key g + 8, heads 2t, 2t+1
-        l_run[nt][0] += __low2float(h0) + __low2float(h1);
-        l_run[nt][1] += __high2float(h0) + __high2float(h1);
         pb0[nt] = movm_t(x0);                          // head g: keys 2t, 2t+1
         pb1[nt] = movm_t(x1);                          // head g: keys 2t+8, 2t+9
       }
@@ -572,9 +619,14 @@ decode_fp8_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          unit[nt][j] = m_run[nt][j] == -INFINITY && l_run[nt][j] == 0.f
-                            ? 0.f : ex2(mo_run[nt][j] - m_run[nt][j]);
+        for (int j = 0; j < 2; ++j) {
+          m_run[nt][j] = wide ? comb_ml[(warp * G + min(8 * nt + 2 * t + j, G - 1)) * 2]
+                              : mo_run[nt][j] - (float)e_ref;
+          unit[nt][j] = m_run[nt][j] == -INFINITY && l_run[nt][j] == 0.f ? 0.f
+                        : wide ? ex2(mo_run[nt][j] - m_run[nt][j])
+                               : scale_of((uint32_t)(e_ref + 127));
+        }
+      __syncwarp();   // m is read before its place is written
     }
     if constexpr (HS) {
       // this warp saw every key of the unit for its own heads: O / l (V's

@@ -81,6 +81,31 @@ def test_a_block_that_takes_the_weight_and_holds_small_values(hkv, byte):
     C.check_decode(pools, q, table, lens, SCALE, got)
 
 
+@pytest.mark.parametrize("hkv,group", [(4, 4), (4, 16), (4, 1), (3, 8)])
+@pytest.mark.parametrize("spread", [20, 45, 60])
+def test_v_scales_far_apart(spread, hkv, group):
+    """Beyond a spread of 40 binades the softmax sum is taken on its own."""
+    lens = [700, 90, 33, 2000]
+    pools, q, table = _case(lens, hkv, group, seed=spread, v_spread=spread)
+    C.check_decode(pools, q, table, lens, SCALE, C.decode(pools, q, table, lens, SCALE))
+
+
+@pytest.mark.parametrize("hkv", [4, 3])
+@pytest.mark.parametrize("at", [0, 5, 31, 32, 36])
+@pytest.mark.parametrize("byte", [1, 60, 86, 87, 88, 200])
+def test_one_block_far_from_the_others(at, byte, hkv):
+    """A block that holds most of the weight and whose V scale is far below or
+    above the others' (40 binades from one of them on), first, later and last."""
+    lens = [590, 20]
+    pools, q, table = _case(lens, hkv, 2, poison=False)
+    q = torch.ones_like(q)
+    blk = int(table[0, at])
+    pools.codes[0][blk] = 0x70                               # 128 * 2^-7 = 1 in every element: score 11.3
+    pools.scale[0][blk] = 120
+    pools.scale[1][blk] = byte
+    C.check_decode(pools, q, table, lens, SCALE, C.decode(pools, q, table, lens, SCALE))
+
+
 @pytest.mark.parametrize("hkv", [4, 1])
 @pytest.mark.parametrize("n", [200, 3000])
 def test_rare_keys_with_large_values(n, hkv):
