@@ -1,4 +1,5 @@
-"""GB300-native paged KV-cache attention: kv_append, paged decode attention
+"""GB300-native paged KV-cache attention: kv_append (with or without position
+rotation; bf16, fp32, fp8 and block-scaled fp8 pools), paged decode attention
 and chunked prefill attention, as hand-written sm_103a CUDA kernels behind a
 C ABI (``include/pagedkv.h``).
 
