@@ -76,17 +76,22 @@ __device__ __forceinline__ float widen(float x) { return x; }
 template <>
 __device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-// V elements from / to memory (16-byte accesses when V > 1)
+// V elements from / to memory (16-byte accesses when V > 1).  STREAM: marked as
+// used once.
 template <typename T, int V>
 struct Run {
   uint4 raw;
+  template <bool STREAM>
   __device__ __forceinline__ void load(const T* p) {
-    // plain loads: queries may be rotated in place
-    if constexpr (V > 1) raw = *reinterpret_cast<const uint4*>(p);
+    // not through the read-only path: queries may be rotated in place
+    if constexpr (V > 1 && STREAM) raw = __ldcs(reinterpret_cast<const uint4*>(p));
+    else if constexpr (V > 1) raw = *reinterpret_cast<const uint4*>(p);
     else *reinterpret_cast<T*>(&raw) = *p;
   }
+  template <bool STREAM>
   __device__ __forceinline__ void store(T* p) const {
-    if constexpr (V > 1) *reinterpret_cast<uint4*>(p) = raw;
+    if constexpr (V > 1 && STREAM) __stcs(reinterpret_cast<uint4*>(p), raw);
+    else if constexpr (V > 1) *reinterpret_cast<uint4*>(p) = raw;
     else *p = *reinterpret_cast<const T*>(&raw);
   }
   __device__ __forceinline__ void get(float (&f)[V]) const {
@@ -163,8 +168,8 @@ __device__ __forceinline__ void rotate(const RopeArgs& r, const Turn<V>& w, Run<
 // once for all of them.  HPT heads' rows are requested at once, beside the
 // slot, the positions and, from those, the table: nothing is looked at before
 // all is on its way (with the checks in between 50 us, so 38 us, for 8,192
-// tokens of 32 + 8 heads).
-template <typename T, bool VEC, int HPT>
+// tokens of 32 + 8 heads; now 33.6 us).
+template <typename T, bool VEC, int HPT, bool STREAM>
 __device__ __forceinline__ void rope_token(const RopeAppendArgs& a, int64_t t, int u, int hs,
                                            int slots, int kv_heads) {
   constexpr int V = Unit2<T, VEC>::V;
@@ -189,8 +194,8 @@ __device__ __forceinline__ void rope_token(const RopeAppendArgs& a, int64_t t, i
       const int h = h0 + i * slots;
       if (h < heads) {
         const T* src = source(h);
-        x[i].load(src + e0);
-        y[i].load(src + e1);
+        x[i].template load<STREAM>(src + e0);
+        y[i].template load<STREAM>(src + e1);
       }
     }
   };
@@ -222,21 +227,21 @@ __device__ __forceinline__ void rope_token(const RopeAppendArgs& a, int64_t t, i
               ((blk * kv_heads + k - (is_v ? kv_heads : 0)) * kBlockSize + row) * a.head_dim;
       }
       if (turns && k < kv_heads) rotate<T, V>(a.rope, w, x[i], y[i]);
-      x[i].store(dst + e0);
-      y[i].store(dst + e1);
+      x[i].template store<STREAM>(dst + e0);
+      y[i].template store<STREAM>(dst + e1);
     }
   }
 }
 
-template <typename T, bool VEC, int HPT>
-__global__ void __launch_bounds__(512)
+template <typename T, bool VEC, int HPT, bool STREAM>
+__global__ void __launch_bounds__(256)
 kv_append_rope_kernel(const __grid_constant__ RopeAppendArgs a, int units, int slots) {
   const int per_token = units * slots;
   const int tl = threadIdx.x / per_token;
   const int64_t t = (int64_t)blockIdx.x * (blockDim.x / per_token) + tl;
   const int rem = threadIdx.x - tl * per_token;
   const int hs = rem / units, u = rem - hs * units;
-  if (t < a.num_tokens) rope_token<T, VEC, HPT>(a, t, u, hs, slots, a.num_kv_heads);
+  if (t < a.num_tokens) rope_token<T, VEC, HPT, STREAM>(a, t, u, hs, slots, a.num_kv_heads);
 }
 
 // Thread layout of a token's rows: `slots` threads share a unit's heads.
@@ -249,7 +254,11 @@ int head_slots(int heads, int units, int most) {
   return slots;
 }
 constexpr int64_t kThreadsAtOnce = 152 * 2048;
-constexpr int kHeadsPerThread = 6;   // 8,192 tokens of 32 + 8 heads: 1 or 2 43 us, 4 39 us, 6 38 us
+// From the L2's size on loads and stores are marked as used once: 8,192 tokens
+// of 32 + 8 heads (206 MB) 33.6 us against 36.1, with the four prefills that read
+// them 178.4 against 178.5 us; 4,096 tokens with theirs 91.4 against 90.6.
+constexpr int64_t kStreamBytes = 128ll << 20;
+constexpr int kHeadsPerThread = 6;   // 8,192 tokens of 32 + 8 heads (in CTAs of 256): 1 or 2 43 us, 4 39, 6 38
 constexpr int kQueryHeads = 2;        // the same for the queries of the 8-bit append
 
 // ------------------------------------------------- block-scaled 8-bit cache
@@ -511,7 +520,7 @@ kv_append_fp8_block_kernel(const __grid_constant__ RopeAppendArgs a, int kv_ctas
     const int rem = threadIdx.x - tl * per_token;
     const int hs = rem / q_units, u = rem - hs * q_units;
     if (tl < tokens && t < a.num_tokens)
-      rope_token<__nv_bfloat16, true, kQueryHeads>(a, t, u, hs, q_slots, 0);
+      rope_token<__nv_bfloat16, true, kQueryHeads, false>(a, t, u, hs, q_slots, 0);
     return;
   }
   __shared__ WindowRuns<UPC> runs;
@@ -636,15 +645,19 @@ kv_append_fp8_block_kernel(const __grid_constant__ RopeAppendArgs a, int kv_ctas
   write(j, run);
 }
 
-template <typename T, bool VEC, int HPT>
+template <typename T, bool VEC, int HPT, bool STREAM>
 cudaError_t launch_rope_heads(const RopeAppendArgs& a, cudaStream_t stream) {
   const int units = a.head_dim / (2 * Unit2<T, VEC>::V);
   const int slots = head_slots<HPT>(a.num_q_heads + 2 * a.num_kv_heads, units, 256);
   const int per_token = units * slots;
-  const int tokens = per_token >= 256 ? 1 : 256 / per_token;
+  // small CTAs give their registers back as soon as their rows are out: 8,192
+  // tokens of 32 + 8 heads 37.8 us with 256 threads, 36.3 with 128, 35.6 with 64
+  const int threads = HPT > 1 ? 64 : 256;
+  const int tokens = per_token >= threads ? 1 : threads / per_token;
   const int64_t grid = (a.num_tokens + tokens - 1) / tokens;
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-  kv_append_rope_kernel<T, VEC, HPT><<<(int)grid, per_token * tokens, 0, stream>>>(a, units, slots);
+  kv_append_rope_kernel<T, VEC, HPT, STREAM>
+      <<<(int)grid, per_token * tokens, 0, stream>>>(a, units, slots);
   return cudaGetLastError();
 }
 
@@ -652,8 +665,10 @@ template <typename T, bool VEC>
 cudaError_t launch_rope_typed(const RopeAppendArgs& a, cudaStream_t stream) {
   const int64_t threads = a.num_tokens * (a.num_q_heads + 2 * a.num_kv_heads) *
                           (a.head_dim / (2 * Unit2<T, VEC>::V));
-  return threads <= kThreadsAtOnce ? launch_rope_heads<T, VEC, 1>(a, stream)
-                                   : launch_rope_heads<T, VEC, kHeadsPerThread>(a, stream);
+  if (threads <= kThreadsAtOnce) return launch_rope_heads<T, VEC, 1, false>(a, stream);
+  const int64_t bytes = 2 * threads * 2 * Unit2<T, VEC>::V * (int)sizeof(T);   // read and written
+  return bytes <= kStreamBytes ? launch_rope_heads<T, VEC, kHeadsPerThread, false>(a, stream)
+                               : launch_rope_heads<T, VEC, kHeadsPerThread, true>(a, stream);
 }
 
 // 1 if every v pairs from a multiple of v on share an axis.

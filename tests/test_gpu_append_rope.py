@@ -172,3 +172,29 @@ def test_empty_and_other_stream_and_graph():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(qg, qr * 2)
+
+
+@pytest.mark.parametrize("t,hq,hkv,d,rot,dtype", [
+    (8300, 32, 8, 128, 128, torch.bfloat16), (4300, 32, 8, 128, 64, torch.float32), (2500, 32, 8, 96, 96, torch.bfloat16),
+    (9001, 30, 3, 128, 20, torch.bfloat16), (1100, 128, 1, 128, 128, torch.bfloat16)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_large_batches_equal_small_ones(t, hq, hkv, d, rot, dtype, in_place):
+    """Several heads to a thread, and loads and stores that stream: bit for bit
+    what pieces of 300 tokens give."""
+    rope = B.Rope(R.table(997, rot).cuda(), False, R.sections(rot, 3))
+    q, k, v, pos = (x.cuda() for x in R.draw(t, hq, hkv, d, dtype, 9, 3))
+    nb = t // 16 + 3
+    slots = R.scattered_slots(t, nb, 9).cuda()
+    got = []
+    for step in (t, 300):
+        kc, vc = (torch.full((nb, hkv, 16, d), FILL, dtype=dtype, device="cuda") for _ in "kv")
+        src = q.clone()
+        qo = src if in_place else torch.empty_like(q)
+        for i in range(0, t, step):
+            s = slice(i, i + step)
+            B.kv_append_rope(qo[s], src[s], k[s], v[s], kc, vc, slots[s], pos[:, s].contiguous(), rope)
+        torch.cuda.synchronize()
+        got.append((qo, kc, vc))
+    assert B.get_device_error() == 0
+    assert all(torch.equal(_bits(a), _bits(b)) for a, b in zip(*got))
+    assert not torch.equal(_bits(got[0][0]), _bits(q))
