@@ -1052,13 +1052,13 @@ int choose_splits(const Params& p, int n_x, int n_t, const ClusterSlots& slots) 
   for (int s = 1; s <= std::min(kMaxSplits, tiles(0)); ++s) {
     const int64_t k = slots.at[s];
     if (k < 1) continue;
-    // the longest slot is a first or last one, or beside the last round's end
+    // the longest slot is a first or last one, or beside the last lap's end
     const int64_t rem = n % k, ends[] = {0, k - 1, rem - 1, rem, k - rem - 1, k - rem};
     int64_t cost = 0;
     for (int64_t i : ends) {
       int64_t sum = 0;
-      for (int64_t round = 0; i >= 0 && i < k && round * k < n; ++round) {
-        const int64_t item = round * k + (round % 2 ? k - 1 - i : i);
+      for (int64_t lap = 0; i >= 0 && i < k && lap * k < n; ++lap) {
+        const int64_t item = lap * k + (lap % 2 ? k - 1 - i : i);
         if (item < n) sum += (tiles(item) + s - 1) / s * 156 + (s == 1 ? 650 : 960 + 45 * s);
       }
       cost = std::max(cost, sum);
