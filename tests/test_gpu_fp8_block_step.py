@@ -184,3 +184,47 @@ def test_step_captured_whole_and_replayed():
         torch.cuda.synchronize()
         assert torch.equal(out, want[at])
     assert all(torch.equal(a, b) for a, b in zip(st, ref)) and B.get_device_error() == 0
+
+
+def test_two_threads_on_streams_of_their_own():
+    """Append, prefill and decode of two sequences' pools at once, from two host
+    threads, give what each gives alone."""
+    import threading
+    cs = R.table(512, D).cuda()
+    n = 300
+    table, nb = C.tables([n], 6)
+    pos = torch.arange(n)
+    slots = (table[0, pos // 16].long() * 16 + pos % 16).cuda()
+    row, pos32 = table[0].cuda(), pos.to(torch.int32).cuda()
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    inputs = [[x.cuda() for x in _new(n, 60 + i)] for i in range(2)]
+
+    def work(i, out, stream, times):
+        q, k, v = inputs[i]
+        rope = B.Rope(cs, bool(i))
+        with torch.cuda.stream(stream):
+            codes = [torch.zeros(nb, HKV, 16, D, dtype=torch.uint8, device="cuda") for _ in "kv"]
+            scale = [torch.zeros(nb, HKV, dtype=torch.uint8, device="cuda") for _ in "kv"]
+            ws = B.decode_workspace_fp8_block(1, HQ, HKV, D, n)
+            qo, pre, dec = torch.empty_like(q), torch.empty_like(q), torch.empty_like(q[:1])
+            for _ in range(times):
+                B.kv_append_fp8_block(k, v, *codes, *scale, slots, q_out=qo, q=q, positions=pos32, rope=rope)
+                B.chunked_prefill_attention_fp8_block(pre, qo, *codes, *scale, row, 0, SCALE)
+                B.paged_decode_attention_fp8_block(dec, qo[-1:], *codes, *scale, row[None], lens, n, SCALE, ws)
+            out[i] = [qo, pre, dec, *codes, *scale]
+
+    alone, both = {}, {}
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for i in range(2):
+        work(i, alone, streams[i], 1)
+        torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(i, both, streams[i], 30)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert B.get_device_error() == 0
+    for i in range(2):
+        assert all(torch.equal(a, b) for a, b in zip(alone[i], both[i]))
