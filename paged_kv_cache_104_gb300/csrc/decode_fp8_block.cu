@@ -8,13 +8,64 @@ namespace {
 
 constexpr int kMergeWarps = 8;
 
-// Merge of one (sequence, query head) row's partials by a whole CTA, for the
-// few rows of a small batch, which is cut into many short pieces (one
-// sequence of 32,001 tokens: up to 228 a row): o = sum 2^(m_s - M) O_s / sum
-// 2^(m_s - M) l_s.  Warp w takes the partials w, w + 8, ..., a lane four
-// columns; four rows are in flight per warp, beside their (m, l), under a
-// running maximum.  The programmatic dependent of the main kernel; lengths are
-// the caller's and are read before it ends.
+// Merge of a (sequence, query head) row's partials: o = sum 2^(m_s - M) O_s /
+// sum 2^(m_s - M) l_s.  A warp folds the partials first, first + step, ... under
+// a running maximum, a lane four columns; four rows are in flight, beside their
+// (m, l).  The merges are programmatic dependents of the main kernel; lengths
+// are the caller's and are read before it ends.
+struct Folded {
+  float m, l;
+  float4 sum;
+};
+__device__ __forceinline__ Folded fold(const DecodeArgs& a, int row, int lane, int first, int step,
+                                       int ns) {
+  const int64_t base = (int64_t)row * a.max_splits;
+  const float2* rml = reinterpret_cast<const float2*>(a.ws_ml) + base;
+  const float4* acc = reinterpret_cast<const float4*>(a.ws_acc) + base * (kHD / 4) + lane;
+  Folded r = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  for (int s0 = first; s0 < ns; s0 += 4 * step) {
+    float4 v[4];
+    float2 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int s = s0 + i * step;
+      x[i] = s < ns ? rml[s] : make_float2(-INFINITY, 0.f);
+      v[i] = s < ns ? acc[(int64_t)s * (kHD / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    const float top = fmaxf(fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(x[2].x, x[3].x)), r.m);
+    if (top != r.m) {
+      const float f = ex2(r.m - top);
+      r.l *= f;
+      r.sum.x *= f;
+      r.sum.y *= f;
+      r.sum.z *= f;
+      r.sum.w *= f;
+      r.m = top;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (s0 + i * step >= ns) break;
+      const float w = ex2(x[i].x - r.m);
+      r.l = fmaf(w, x[i].y, r.l);
+      r.sum.x = fmaf(w, v[i].x, r.sum.x);
+      r.sum.y = fmaf(w, v[i].y, r.sum.y);
+      r.sum.z = fmaf(w, v[i].z, r.sum.z);
+      r.sum.w = fmaf(w, v[i].w, r.sum.w);
+    }
+  }
+  return r;
+}
+
+// Partials of a row of sequence b, whose length is n (0: it has none).
+__device__ __forceinline__ int partials(const DecodeArgs& a, int row, int b, int n) {
+  if (n < 1 || n > min(a.max_seq_len, a.max_blocks_per_seq * kBlockSize)) return 0;
+  const int h = row - b * a.num_q_heads;
+  return a.balanced ? a.ws_np[b * a.num_kv_heads + h / (a.num_q_heads / a.num_kv_heads)]
+                    : (n + a.split_tokens - 1) / a.split_tokens;
+}
+
+// A CTA to a row, for the few rows of a small batch, which is cut into many
+// short pieces (one sequence of 32,001 tokens: up to 228 a row).
 __global__ void __launch_bounds__(kMergeWarps * 32)
 merge_row_kernel(const DecodeArgs a) {
   __shared__ float4 part[kMergeWarps][32];
@@ -24,49 +75,11 @@ merge_row_kernel(const DecodeArgs a) {
   const int b = row / a.num_q_heads;
   const int n = a.seq_lens[b];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (n < 1 || n > min(a.max_seq_len, a.max_blocks_per_seq * kBlockSize)) return;
-  const int h = row - b * a.num_q_heads;
-  const int ns = a.balanced ? a.ws_np[b * a.num_kv_heads + h / (a.num_q_heads / a.num_kv_heads)]
-                            : (n + a.split_tokens - 1) / a.split_tokens;
-  if (ns <= 1) return;              // written directly by the main kernel
-  const int64_t base = (int64_t)row * a.max_splits;
-  const float2* rml = reinterpret_cast<const float2*>(a.ws_ml) + base;
-  const float4* acc = reinterpret_cast<const float4*>(a.ws_acc) + base * (kHD / 4) + lane;
-  float m = -INFINITY;
-  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
-  for (int s0 = warp; s0 < ns; s0 += 4 * kMergeWarps) {
-    float4 v[4];
-    float2 x[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int s = s0 + i * kMergeWarps;
-      x[i] = s < ns ? rml[s] : make_float2(-INFINITY, 0.f);
-      v[i] = s < ns ? acc[(int64_t)s * (kHD / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    const float top = fmaxf(fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(x[2].x, x[3].x)), m);
-    if (top != m) {
-      const float f = ex2(m - top);
-      l *= f;
-      sum.x *= f;
-      sum.y *= f;
-      sum.z *= f;
-      sum.w *= f;
-      m = top;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (s0 + i * kMergeWarps >= ns) break;
-      const float w = ex2(x[i].x - m);
-      l = fmaf(w, x[i].y, l);
-      sum.x = fmaf(w, v[i].x, sum.x);
-      sum.y = fmaf(w, v[i].y, sum.y);
-      sum.z = fmaf(w, v[i].z, sum.z);
-      sum.w = fmaf(w, v[i].w, sum.w);
-    }
-  }
-  part[warp][lane] = sum;
-  if (lane == 0) ml[warp] = make_float2(m, l);
+  const int ns = partials(a, row, b, n);
+  if (ns <= 1) return;              // none, or written directly by the main kernel
+  const Folded r = fold(a, row, lane, warp, kMergeWarps, ns);
+  part[warp][lane] = r.sum;
+  if (lane == 0) ml[warp] = make_float2(r.m, r.l);
   __syncthreads();
   if (threadIdx.x >= kHD) return;
   const int live = min(ns, kMergeWarps);   // the other warps had no partial
@@ -79,6 +92,25 @@ merge_row_kernel(const DecodeArgs a) {
     O = fmaf(f, reinterpret_cast<const float*>(part[w])[threadIdx.x], O);
   }
   static_cast<__nv_bfloat16*>(a.out)[(int64_t)row * kHD + threadIdx.x] = __float2bfloat16_rn(O / L);
+}
+
+// A warp to a row, for many rows of few partials.
+__global__ void __launch_bounds__(kMergeWarps * 32)
+merge_warp_kernel(const DecodeArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int row = blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+  if (row >= a.num_seqs * a.num_q_heads) return;
+  const int b = row / a.num_q_heads;
+  const int n = a.seq_lens[b];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int ns = partials(a, row, b, n);
+  if (ns <= 1) return;
+  const Folded r = fold(a, row, lane, 0, 1, ns);
+  const float rl = 1.f / r.l;
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(r.sum.x * rl, r.sum.y * rl);
+  const __nv_bfloat162 hi = __floats2bfloat162_rn(r.sum.z * rl, r.sum.w * rl);
+  reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + (int64_t)row * kHD)[lane] =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
 
 }  // namespace
@@ -99,9 +131,10 @@ cudaError_t launch_paged_decode_fp8_block(const DecodeArgs& a, int num_sms, cuda
   cudaError_t e = launch_fp8<true>(a, num_sms, stream, &m.balanced);
   if (e != cudaSuccess || a.max_splits <= 1) return e;
   // a warp a row fills the GPU once there are some thousand rows
-  if ((int64_t)a.num_seqs * a.num_q_heads > 8 * 152) return launch_decode_reduce_bf16_128(m, stream);
+  const int rows = a.num_seqs * a.num_q_heads;
+  const bool by_warp = rows > 8 * 152;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.num_seqs * a.num_q_heads);
+  cfg.gridDim = dim3(by_warp ? (rows + kMergeWarps - 1) / kMergeWarps : rows);
   cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -109,7 +142,7 @@ cudaError_t launch_paged_decode_fp8_block(const DecodeArgs& a, int num_sms, cuda
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, merge_row_kernel, m);
+  e = cudaLaunchKernelEx(&cfg, by_warp ? merge_warp_kernel : merge_row_kernel, m);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
