@@ -30,44 +30,44 @@ E_MIN, E_MAX = -126, 119  # block scale exponents
 def listed():
     return [
         # one sequence's new token: the launch-bound end of a decode step
-        {"name": "rope one token", "op": "rope", "tokens": 1, "q_heads": 32, "kv_heads": 8, "dim": 128,
+        {"name": "rope, one token", "op": "rope", "tokens": 1, "q_heads": 32, "kv_heads": 8, "dim": 128,
          "rot": 128, "interleaved": False, "axes": 1, "cycle": False, "fp32": False, "positions": 32768},
         # a decode step of 128 sequences
-        {"name": "rope 128 sequences", "op": "rope", "tokens": 128, "q_heads": 32, "kv_heads": 8, "dim": 128,
+        {"name": "rope, 128 sequences", "op": "rope", "tokens": 128, "q_heads": 32, "kv_heads": 8, "dim": 128,
          "rot": 128, "interleaved": False, "axes": 1, "cycle": False, "fp32": False, "positions": 131072},
         # four prompt chunks of 2,048 tokens with image patches: time, height and width
-        {"name": "rope 8192 tokens three axes", "op": "rope", "tokens": 8192, "q_heads": 32, "kv_heads": 8,
+        {"name": "rope, 8192 tokens, three axes", "op": "rope", "tokens": 8192, "q_heads": 32, "kv_heads": 8,
          "dim": 128, "rot": 128, "interleaved": False, "axes": 3, "cycle": False, "fp32": False,
          "positions": 32768},
         # an odd chunk into fp32 pools, half of each head rotated, adjacent pairs
-        {"name": "rope 777 tokens fp32 partial", "op": "rope", "tokens": 777, "q_heads": 16, "kv_heads": 2,
+        {"name": "rope, 777 tokens, fp32, partial", "op": "rope", "tokens": 777, "q_heads": 16, "kv_heads": 2,
          "dim": 128, "rot": 64, "interleaved": True, "axes": 1, "cycle": False, "fp32": True,
          "positions": 8192},
         # the new tokens of 128 running sequences: each continues a block
-        {"name": "append8 128 sequences", "op": "append8", "sequences": 128, "tokens": 1, "first_row": -1,
+        {"name": "append8, 128 sequences", "op": "append8", "sequences": 128, "tokens": 1, "first_row": -1,
          "q_heads": 32, "kv_heads": 8, "dim": 128, "rot": 128, "interleaved": False, "axes": 1,
          "cycle": False, "positions": 131072},
         # a prompt chunk of 2,048 tokens that starts in the middle of a block
-        {"name": "append8 chunk of 2048", "op": "append8", "sequences": 1, "tokens": 2048, "first_row": 5,
+        {"name": "append8, chunk of 2048", "op": "append8", "sequences": 1, "tokens": 2048, "first_row": 5,
          "q_heads": 32, "kv_heads": 8, "dim": 128, "rot": 128, "interleaved": False, "axes": 1,
          "cycle": False, "positions": 32768},
         # one short conversation: latency
-        {"name": "decode8 one sequence of 777", "op": "decode8", "sequences": 1, "shortest": 777,
+        {"name": "decode8, one sequence of 777", "op": "decode8", "sequences": 1, "shortest": 777,
          "longest": 777, "q_heads": 32, "kv_heads": 8},
         # the even batch of the llama8b_decode workload, after its append
-        {"name": "decode8 64 sequences of 2301", "op": "decode8", "sequences": 64, "shortest": 2301,
+        {"name": "decode8, 64 sequences of 2301", "op": "decode8", "sequences": 64, "shortest": 2301,
          "longest": 2301, "q_heads": 32, "kv_heads": 8},
         # long documents, eight query heads to a KV head
-        {"name": "decode8 8 sequences of 32001 group 8", "op": "decode8", "sequences": 8, "shortest": 32001,
+        {"name": "decode8, 8 sequences of 32001, group 8", "op": "decode8", "sequences": 8, "shortest": 32001,
          "longest": 32001, "q_heads": 64, "kv_heads": 8},
         # the ragged batch of the default workload: lengths from 128 to 32,768
-        {"name": "decode8 128 ragged sequences", "op": "decode8", "sequences": 128, "shortest": 128,
+        {"name": "decode8, 128 ragged sequences", "op": "decode8", "sequences": 128, "shortest": 128,
          "longest": 32768, "q_heads": 32, "kv_heads": 8},
         # the last piece of a short prompt, two KV heads
-        {"name": "prefill8 77 over 500", "op": "prefill8", "chunk": 77, "prior": 500, "q_heads": 8,
+        {"name": "prefill8, 77 over 500", "op": "prefill8", "chunk": 77, "prior": 500, "q_heads": 8,
          "kv_heads": 2},
         # the default workload's prompt chunk: 2,048 tokens over 4,096 cached ones
-        {"name": "prefill8 2048 over 4096", "op": "prefill8", "chunk": 2048, "prior": 4096, "q_heads": 32,
+        {"name": "prefill8, 2048 over 4096", "op": "prefill8", "chunk": 2048, "prior": 4096, "q_heads": 32,
          "kv_heads": 8},
     ]
 
@@ -262,8 +262,7 @@ def _plan(s):
     if "table" in s:
         s["rope"] = binding.Rope(s["table"], interleaved=case["interleaved"], pair_axis=s["pair_axis"])
     elif case["op"] == "decode8":
-        s["workspace"] = binding.decode_workspace_fp8_block(case["sequences"], case["q_heads"], case["kv_heads"], 128,
-                                                            s["longest"])
+        s["workspace"] = binding.decode_workspace(case["sequences"], case["q_heads"], 128, s["longest"])
 
 
 # ------------------------------------------------------------ the plain forms
