@@ -338,7 +338,8 @@ struct RowTurn {
 // exact value's.  A middle has the 20 lowest of fp32's bits 0x80000, brought to
 // the top here; below 2^-6, where codes are 2^-9 apart, so it has with 2^-6
 // added.
-// (A chunk of 2,048 tokens takes 13.6 us, with the fp32 values' codes 13.0 us;
+// (GPU time of a chunk of 2,048 tokens: 13.0 us with the codes and scales of the
+// fp32 values, 13.5 with the exact codes, 14.1 with the exact scales too;
 // all in fp64, at 2 operations a clock and SM, would take 10 us more.)
 constexpr uint32_t kNear = 4;
 __device__ __forceinline__ uint32_t off_middle(float y) {
@@ -346,9 +347,10 @@ __device__ __forceinline__ uint32_t off_middle(float y) {
 }
 constexpr uint32_t kAtMiddle = (2 * kNear + 1) << 12;   // off_middle of near ones is less
 
-// The code of element el of token t's key row, turned in fp64, times inv.
-__device__ __noinline__ uint32_t exact_code(const RopeArgs& r, int64_t num_tokens,
-                                            const __nv_bfloat16* row, int64_t t, int el, float inv) {
+// Element el of token t's key row turned in fp64: the products are exact, so
+// this is the exact rotation rounded once.
+__device__ __forceinline__ double exact_turn(const RopeArgs& r, int64_t num_tokens,
+                                             const __nv_bfloat16* row, int64_t t, int el) {
   const int half = r.rot_dim / 2;
   const int i = r.interleaved ? el >> 1 : el % half;
   const bool second = r.interleaved ? (el & 1) : el >= half;
@@ -357,10 +359,40 @@ __device__ __noinline__ uint32_t exact_code(const RopeArgs& r, int64_t num_token
       r.cos_sin + (int64_t)r.positions[r.pair_axis[i] * num_tokens + t] * r.rot_dim + i;
   const double x = (double)__bfloat162float(row[el]) * turn[0];
   const double y = (double)__bfloat162float(row[other]) * turn[half];
-  const double z = (second ? x + y : x - y) * inv;
+  return second ? x + y : x - y;
+}
+
+// The code of element el of token t's key row, turned in fp64, times inv.
+__device__ __noinline__ uint32_t exact_code(const RopeArgs& r, int64_t num_tokens,
+                                            const __nv_bfloat16* row, int64_t t, int el, float inv) {
+  const double z = exact_turn(r, num_tokens, row, t, el) * inv;
   float f = __double2float_rz(z);
   if ((double)f != z) f = __uint_as_float(__float_as_uint(f) | 1u);   // not a middle
   return f32x2_to_e4m3x2(f, 0.f) & 0xffu;
+}
+
+// A scale's border, 448 * 2^e, has the mantissa 0x600000.  A maximum in fp32
+// within kNear ulps of one can lie on its other side than the exact maximum.
+__device__ __forceinline__ bool near_border(uint32_t amax) {
+  return (amax << 9) - ((0x600000u - kNear) << 9) < (2 * kNear + 1) << 9;
+}
+
+// The largest finite magnitude among elements el0 .. el0 + 7 of token t's row,
+// turned in fp64 (is_turned) or as they are, as the bits of a float that lies on
+// the same side of every border (rounded up: a float at a border is met exactly).
+// A turned element beyond fp32 counts as its largest number.
+__device__ __noinline__ uint32_t exact_max(const RopeArgs& r, int64_t num_tokens,
+                                           const __nv_bfloat16* row, int64_t t, int el0,
+                                           bool is_turned) {
+  uint32_t m = 0;
+#pragma unroll 1
+  for (int el = el0; el < el0 + 8; ++el) {
+    const double z = fabs(is_turned ? exact_turn(r, num_tokens, row, t, el)
+                                    : (double)__bfloat162float(row[el]));
+    if (!isfinite(z)) continue;   // infinite or NaN: the scale follows the others
+    m = max(m, min(__float_as_uint(__double2float_ru(z)), 0x7f7fffffu));
+  }
+  return m;
 }
 
 // Of a window: run_of[j], the run that token j belongs to (-1: none that starts
@@ -590,24 +622,52 @@ kv_append_fp8_block_kernel(const __grid_constant__ RopeAppendArgs a, int kv_ctas
       else Elem<__nv_bfloat16>::unpack(raw[u], x[u]);
     }
   };
+  const bool turned_here = rotated && c * 8 < a.rope.rot_dim;
   auto maxima = [&](int of) {
 #pragma unroll
     for (int u = 0; u < UPC; ++u) {
-      uint32_t m = 0;            // the scale follows the finite elements only
+      uint32_t m = 0;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t b = __float_as_uint(x[u][k]) & 0x7fffffffu;
-        if (b < 0x7f800000u) m = max(m, b);
-      }
+      for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(x[u][k]) & 0x7fffffffu);
 #pragma unroll
       for (int o = 1; o < kRowLanes; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
       if (c == 0 && of >= 0) atomicMax(&runs.top[u][of], m);
     }
   };
+  // A run's maximum that is not the scale's yet: an element is infinite or NaN,
+  // or fp32 may have put the maximum on the other side of a border.
+  auto unsettled = [&](uint32_t top) {
+    return top >= 0x7f800000u || (rotated && near_border(top));
+  };
+  // Such maxima taken again in fp64 (one run in a million).
+  auto settle = [&](int j, int of, int j2, int of2) {
+    uint32_t todo = 0;
+#pragma unroll
+    for (int u = 0; u < UPC; ++u) {
+      if (of >= 0 && unsettled(runs.top[u][of])) todo |= 1u << u;
+      if (of2 >= 0 && unsettled(runs.top[u][of2])) todo |= 0x100u << u;
+    }
+    __syncthreads();
+    if (threadIdx.x < kWindow) {
+#pragma unroll
+      for (int u = 0; u < UPC; ++u)
+        if (unsettled(runs.top[u][threadIdx.x])) runs.top[u][threadIdx.x] = 0;
+    }
+    __syncthreads();
+    if (!mine) todo = 0;
+    todo &= ((1u << ng) - 1) * 0x101u;
+#pragma unroll 1
+    for (; todo; todo &= todo - 1) {
+      const int bit = __ffs(todo) - 1, u = bit & 7, at = bit < 8 ? j : j2;
+      atomicMax(&runs.top[u][bit < 8 ? of : of2],
+                exact_max(a.rope, a.num_tokens, src - c * 8 + (w0 + at) * stride + u * a.head_dim,
+                          w0 + at, c * 8, turned_here));
+    }
+    __syncthreads();
+  };
   auto write = [&](int j, int k) {
     if (k < 0 || !mine) return;
     uint32_t again = 0;
-    const bool turned_here = rotated && c * 8 < a.rope.rot_dim;
 #pragma unroll
     for (int u = 0; u < UPC; ++u)
       if (u < ng)
@@ -627,20 +687,30 @@ kv_append_fp8_block_kernel(const __grid_constant__ RopeAppendArgs a, int kv_ctas
   const int j = k0 + i, j2 = j + kWindow;
   const int run = j < 2 * kWindow ? runs.run_of[j] : -1;
   const int run2 = j2 < 2 * kWindow ? runs.run_of[j2] : -1;
+  auto rows_of = [&](int of) {
+    load_rows(w0 + of);
+    if (rotated) turn.load(a.rope, pos, c);
+    turn_rows();
+  };
   maxima(run);
   // a run that goes on beyond the threads' tokens: its other rows, for the
   // maxima now and again for their codes
   const bool beyond = __syncthreads_or(run2 >= 0);
   if (beyond) {
-    load_rows(w0 + j2);
-    if (rotated) turn.load(a.rope, pos, c);
-    turn_rows();
+    rows_of(j2);
     maxima(run2);
     __syncthreads();
+  }
+  bool some = false;
+#pragma unroll
+  for (int u = 0; u < UPC; ++u) some |= unsettled(runs.top[u][threadIdx.x % kWindow]);
+  if (__any_sync(0xffffffffu, some)) {     // the same in every warp
+    settle(j, run, j2, run2);
+    rows_of(beyond ? j2 : j);              // read again, so that no registers wait for this
+  }
+  if (beyond) {
     write(j2, run2);
-    load_rows(w0 + j);
-    if (rotated) turn.load(a.rope, pos, c);
-    turn_rows();
+    rows_of(j);
   }
   write(j, run);
 }
@@ -709,8 +779,8 @@ cudaError_t launch_kv_append_fp8_block(const RopeAppendArgs& args, cudaStream_t 
   a.rope.whole_axes = axes_by_chunk(a, 8);
   const int64_t windows = (a.num_tokens + kWindow - 1) / kWindow;
   // few windows: a head to a CTA, for latency; many: 4 heads share slots,
-  // positions and table (a chunk of 2,048 tokens: 13.6 us; before the exact
-  // codes 13.0 us, and with 2 heads to a CTA 16.5 us)
+  // positions and table (a chunk of 2,048 tokens: 13.0 us before the exact
+  // codes, and with 2 heads to a CTA 16.5 us)
   const bool few = windows * 2 * a.num_kv_heads <= 152 * 4;
   const int64_t kv_ctas = windows * 2 * (few ? a.num_kv_heads : (a.num_kv_heads + 3) / 4);
   const int units = a.head_dim / 16;
