@@ -52,6 +52,8 @@ def check_runs(slot_mapping, num_blocks: int, block_size: int) -> None:
 
 def check_positions(positions, slot_mapping, num_positions: int) -> None:
     """Every position of a token that is not padding inside the table."""
+    if slot_mapping.shape[0] == 0:
+        return
     p = _host(positions).to(torch.int64).reshape(-1, slot_mapping.shape[0])
     bad = ((p < 0) | (p >= num_positions)) & (_host(slot_mapping) >= 0)[None]
     if bool(bad.any()):
