@@ -8,10 +8,11 @@ namespace {
 
 constexpr int kMergeWarps = 8;
 
-// Merge of a (sequence, query head) row's partials: o = sum 2^(m_s - M) O_s /
-// sum 2^(m_s - M) l_s.  A warp folds the partials first, first + step, ... under
-// a running maximum, a lane four columns; N rows are in flight, beside their
-// (m, l).  The merges are programmatic dependents of the main kernel; lengths
+// Merge of a (sequence, query head) row's partials: o = sum w_s o_s / sum w_s,
+// w_s = 2^(m_s - M) l_s, each o_s a result by itself.  A warp folds the partials
+// first, first + step, ... under a running maximum, a lane four columns, and
+// keeps the average of those it has met, which is within the values' range
+// whatever that is; N rows are in flight, beside their (m, l).  The merges are programmatic dependents of the main kernel; lengths
 // are the caller's and are read before it ends.
 struct Folded {
   float m, l;
@@ -36,24 +37,28 @@ __device__ __forceinline__ Folded fold(const DecodeArgs& a, int row, int lane, i
     float top = r.m;
 #pragma unroll
     for (int i = 0; i < N; ++i) top = fmaxf(top, x[i].x);
-    if (top != r.m) {
-      const float f = ex2(r.m - top);
-      r.l *= f;
-      r.sum.x *= f;
-      r.sum.y *= f;
-      r.sum.z *= f;
-      r.sum.w *= f;
-      r.m = top;
+    const float before = r.l * ex2(r.m - top);   // 0 at the first
+    float w[N], l = before;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      w[i] = ex2(x[i].x - top) * x[i].y;
+      l += w[i];
     }
+    const float inv = 1.f / l, f = before * inv;
+    r.m = top;
+    r.l = l;
+    r.sum.x *= f;
+    r.sum.y *= f;
+    r.sum.z *= f;
+    r.sum.w *= f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       if (s0 + i * step >= ns) break;
-      const float w = ex2(x[i].x - r.m);
-      r.l = fmaf(w, x[i].y, r.l);
-      r.sum.x = fmaf(w, v[i].x, r.sum.x);
-      r.sum.y = fmaf(w, v[i].y, r.sum.y);
-      r.sum.z = fmaf(w, v[i].z, r.sum.z);
-      r.sum.w = fmaf(w, v[i].w, r.sum.w);
+      const float share = w[i] * inv;
+      r.sum.x = fmaf(share, v[i].x, r.sum.x);
+      r.sum.y = fmaf(share, v[i].y, r.sum.y);
+      r.sum.z = fmaf(share, v[i].z, r.sum.z);
+      r.sum.w = fmaf(share, v[i].w, r.sum.w);
     }
   }
   return r;
@@ -89,12 +94,10 @@ merge_row_kernel(const DecodeArgs a) {
   float M = -INFINITY;
   for (int w = 0; w < live; ++w) M = fmaxf(M, ml[w].x);
   float L = 0.f, O = 0.f;
-  for (int w = 0; w < live; ++w) {
-    const float f = ex2(ml[w].x - M);
-    L = fmaf(f, ml[w].y, L);
-    O = fmaf(f, reinterpret_cast<const float*>(part[w])[threadIdx.x], O);
-  }
-  static_cast<__nv_bfloat16*>(a.out)[(int64_t)row * kHD + threadIdx.x] = __float2bfloat16_rn(O / L);
+  for (int w = 0; w < live; ++w) L = fmaf(ex2(ml[w].x - M), ml[w].y, L);
+  for (int w = 0; w < live; ++w)
+    O = fmaf(ex2(ml[w].x - M) * ml[w].y / L, reinterpret_cast<const float*>(part[w])[threadIdx.x], O);
+  static_cast<__nv_bfloat16*>(a.out)[(int64_t)row * kHD + threadIdx.x] = __float2bfloat16_rn(O);
 }
 
 // A warp to a row, for many rows of few partials (64 sequences of 2,301 tokens,
@@ -111,9 +114,8 @@ merge_warp_kernel(const DecodeArgs a) {
   const int ns = partials(a, row, b, n);
   if (ns <= 1) return;
   const Folded r = fold<8>(a, row, lane, 0, 1, ns);
-  const float rl = 1.f / r.l;
-  const __nv_bfloat162 lo = __floats2bfloat162_rn(r.sum.x * rl, r.sum.y * rl);
-  const __nv_bfloat162 hi = __floats2bfloat162_rn(r.sum.z * rl, r.sum.w * rl);
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(r.sum.x, r.sum.y);
+  const __nv_bfloat162 hi = __floats2bfloat162_rn(r.sum.z, r.sum.w);
   reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + (int64_t)row * kHD)[lane] =
       make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }

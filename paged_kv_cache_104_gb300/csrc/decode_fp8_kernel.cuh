@@ -160,8 +160,10 @@ __device__ __forceinline__ uint4 ld_now(const uint4* p) {
   return v;
 }
 
-// The value 2^(b - 127) of a scale byte (0 reads as zero, 255 as infinity).
-__device__ __forceinline__ float scale_of(uint32_t b) { return __uint_as_float(b << 23); }
+// The value 2^(b - 127) of a scale byte b <= 254, a subnormal number for 0.
+__device__ __forceinline__ float scale_of(uint32_t b) {
+  return __uint_as_float(b == 0 ? 0x00400000u : b << 23);
+}
 
 // G: query heads per KV head.  HS (grouped stages): a stage is one block of a
 // group of kBPS KV heads, warp w following head w with that head's scales;
@@ -613,8 +615,11 @@ decode_fp8_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tm_k,
         l_run[nt][j] += __shfl_xor_sync(kAll8, l_run[nt][j], 16);
       }
     const bool direct = (u.ns == 1);
-    // BS: O in the units of l (zero for a warp that met no block)
-    float unit[NT][2];
+    // BS: what O / l lacks to be a result, 2^E or 2^(M - m), in two factors: their
+    // product may leave fp32's normal range where the result does not.  l is
+    // divided by first: O 2^E can overflow where O 2^E / l, an average of cached
+    // values, cannot.  (A warp that met no block gives 0.)
+    float unit[NT][2][2], inv_l[NT][2];
     if constexpr (BS) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -622,9 +627,14 @@ decode_fp8_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tm_k,
         for (int j = 0; j < 2; ++j) {
           m_run[nt][j] = wide ? comb_ml[(warp * G + min(8 * nt + 2 * t + j, G - 1)) * 2]
                               : mo_run[nt][j] - (float)e_ref;
-          unit[nt][j] = m_run[nt][j] == -INFINITY && l_run[nt][j] == 0.f ? 0.f
-                        : wide ? ex2(mo_run[nt][j] - m_run[nt][j])
-                               : scale_of((uint32_t)(e_ref + 127));
+          inv_l[nt][j] = m_run[nt][j] == -INFINITY && l_run[nt][j] == 0.f ? 0.f : 1.f / l_run[nt][j];
+          if (wide) {
+            unit[nt][j][0] = unit[nt][j][1] = ex2(0.5f * (mo_run[nt][j] - m_run[nt][j]));
+          } else {
+            const int half = e_ref >> 1;
+            unit[nt][j][0] = scale_of((uint32_t)(half + 127));
+            unit[nt][j][1] = scale_of((uint32_t)(e_ref - half + 127));
+          }
         }
       __syncwarp();   // m is read before its place is written
     }
@@ -639,18 +649,20 @@ decode_fp8_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tm_k,
         for (int j = 0; j < 2; ++j) {
           const int hh = 8 * nt + 2 * t + j;
           if (hh < G) {
-            // BS: partials are fp32 and keep the weight l, as their sizes follow V's scales
-            const float rl = BS ? (direct ? unit[nt][j] / l_run[nt][j] : unit[nt][j])
-                                : vscale / l_run[nt][j];
+            const float rl = BS ? inv_l[nt][j] : vscale / l_run[nt][j];
             const int64_t row = (int64_t)u.b * a.num_q_heads + hq0 + hh;
             const int64_t pidx = row * a.max_splits + u.s;
 #pragma unroll
             for (int mt = 0; mt < 8; ++mt) {
               const int d = 16 * g + 2 * mt;
-              const float x0 = o[nt][mt][j] * rl, x1 = o[nt][mt][j + 2] * rl;
+              float x0 = o[nt][mt][j] * rl, x1 = o[nt][mt][j + 2] * rl;
+              if constexpr (BS) {
+                x0 = x0 * unit[nt][j][0] * unit[nt][j][1];
+                x1 = x1 * unit[nt][j][0] * unit[nt][j][1];
+              }
               if (direct)
                 *reinterpret_cast<__nv_bfloat162*>(outp + row * kHD + d) = __floats2bfloat162_rn(x0, x1);
-              else if constexpr (BS)
+              else if constexpr (BS)   // fp32: partials' sizes follow V's scales
                 *reinterpret_cast<float2*>(a.ws_acc + pidx * kHD + d) = make_float2(x0, x1);
               else
                 *reinterpret_cast<__half2*>(ws_half + pidx * kHD + d) = __floats2half2_rn(x0, x1);
@@ -678,7 +690,8 @@ decode_fp8_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
             for (int mt = 0; mt < 8; ++mt)   // pair slot mt stored at mt ^ g: no bank conflicts
               *reinterpret_cast<float2*>(crow + 2 * (mt ^ g)) =
-                  BS ? make_float2(o[nt][mt][j] * unit[nt][j], o[nt][mt][j + 2] * unit[nt][j])
+                  BS ? make_float2(o[nt][mt][j] * inv_l[nt][j] * unit[nt][j][0] * unit[nt][j][1],
+                                   o[nt][mt][j + 2] * inv_l[nt][j] * unit[nt][j][0] * unit[nt][j][1])
                      : make_float2(o[nt][mt][j], o[nt][mt][j + 2]);
           }
         }
@@ -696,7 +709,12 @@ decode_fp8_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tm_k,
           wk[k] = (mk == -INFINITY) ? 0.f : ex2(mk - M);
           L = fmaf(wk[k], comb_ml[(k * G + h) * 2 + 1], L);
         }
-        const float rl = vscale / L;
+        // BS: the warps' results, weighted by their shares of L
+        const float rl = BS ? 1.f : vscale / L;
+        if constexpr (BS) {
+#pragma unroll
+          for (int k = 0; k < kCW; ++k) wk[k] *= comb_ml[(k * G + h) * 2 + 1] / L;
+        }
         const int64_t row = (int64_t)u.b * a.num_q_heads + hq0 + h;
         const int64_t pidx = row * a.max_splits + u.s;
 #pragma unroll
