@@ -47,8 +47,9 @@
 // from exponentials of its own, against a reference m of its own, and the
 // result is O 2^(M - m) / l.
 // Each consumer warp reads its own blocks' scale bytes, one block per lane, a
-// window of 32 stages ahead.  Queries are brought to [1, 2) times a power of
-// two by head before they become f16, which then loses nothing to its range.
+// window of 32 stages ahead.  Before the queries become f16 a power of two brings
+// each head's largest element to [2^14, 2^15): elements down to 2^-31 of it keep
+// all their bits, smaller ones are off by at most 2^-39 of it.
 #pragma once
 
 #include <cuda.h>
@@ -356,12 +357,11 @@ decode_fp8_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tm_k,
         top = max(top & 0xffffu, top >> 16);
         top = max(top, __shfl_xor_sync(kAll8, top, 1));
         top = max(top, __shfl_xor_sync(kAll8, top, 2));
-        // 2^x with x the exponent of the head's largest element; a head of
-        // zeros, subnormals, infinities or NaN is taken as it is
-        const uint32_t ex = top >> 7;
-        const int x = ex == 0 || ex == 255 ? 0 : min((int)ex, 253) - 127;
-        const float down = __uint_as_float((uint32_t)(127 - x) << 23);
-        const float up = __uint_as_float((uint32_t)(127 + x) << 23);
+        // ex: the exponent of the head's largest element, biased (of infinities
+        // and NaN the largest there is, of zeros and the least numbers 2^-112)
+        const uint32_t ex = min(max(top >> 7, 15u), 254u);
+        const float down = __uint_as_float((268u - ex) << 23);   // 2^(14 - (ex - 127))
+        const float up = __uint_as_float((ex - 14u) << 23);
         if (hh < G) {
           auto two = [&](uint32_t w) { return pack2_f16(bf16lo(w) * down, bf16hi(w) * down); };
 #pragma unroll
