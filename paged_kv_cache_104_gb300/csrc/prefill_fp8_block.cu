@@ -121,10 +121,8 @@ constexpr float kLazy = 8.0f;
 
 static_assert(NSV * kTile16 == 2 * BM * HD * 2, "the bf16 queries fit the V ring");
 static_assert(SMEM_BYTES <= 227 * 1024, "one CTA per SM");
-// the merge, in the tiles' place: the CTAs' columns (7 CTAs of 32 are the most)
-// and what their rows count for
-constexpr int OFF_UNITS = 7 * 2 * BM * 32 * 2;
-static_assert(OFF_UNITS + 8 * 2 * BM * 4 <= OFF_SCALES, "the merge lies in the tiles' place");
+// the merge's fp32 columns: 7 CTAs of 32 are the most
+static_assert(7 * 2 * BM * 32 * 4 <= OFF_SCALES, "the merge lies in the tiles' place");
 
 enum {
   B_Q = 0,
@@ -304,13 +302,9 @@ __device__ __forceinline__ float2 ld_peer2(uint32_t addr) {
                : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
   return v;
 }
-__device__ __forceinline__ void st_peer1(uint32_t addr, float x) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
-}
-__device__ __forceinline__ void st_peer4(uint32_t addr, uint32_t x, uint32_t y, uint32_t z,
-                                         uint32_t w) {
-  asm volatile("st.shared::cluster.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(x), "r"(y), "r"(z),
-               "r"(w)
+__device__ __forceinline__ void st_peer4(uint32_t addr, float x, float y, float z, float w) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "f"(x), "f"(y), "f"(z),
+               "f"(w)
                : "memory");
 }
 
@@ -880,28 +874,14 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
       asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(row_at), "f"(ref), "f"(l_run) : "memory");
       cluster_sync();                       // every CTA's stats are there, its tiles are done with
       // CTA k adds up columns k W .. k W + W - 1, W = 2^w the columns over the
-      // largest power of two of CTAs.  What it gets from each CTA: O as f16, whose
-      // 11 bits are P's own, each row brought to below 2 by a power of two, eight
-      // columns of 128 rows in a piece of 2 KiB, rows side by side; and what the
-      // rows count for.  (In fp32 the 128 KiB a CTA sends, at some 25 bytes a
-      // cycle, were the longest part of a short call.)
+      // largest power of two of CTAs.  It gets each CTA's part of the results in
+      // fp32, four columns of 128 rows in a piece of 2 KiB, rows side by side.
+      // (These 128 KiB a CTA, at some 25 bytes a cycle, are the longest part of a
+      // short call: 77 rows over 500 keys take 13.2 us; 12.0 us with f16 parts,
+      // whose rounding would stand beside that of P.)
       const int w = 7 - (31 - __clz(p.splits));
       const int owners = HD >> w;
-      float most = 0.f;                     // the row's largest |O|
-      if (n_tiles > 0) {
-#pragma unroll 1
-        for (int c = 0; c < HD; c += 32) {
-          float o[32];
-          tmem_ld32(lane_base + col_o + c, o);
-          tmem_wait_ld();
-          reg_fence(o);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) most = fmaxf(most, fabsf(o[i]));
-        }
-      }
-      // 2^x, x the exponent of the largest (a row of zeros: any), and its inverse
-      const uint32_t ex = max(1u, min(253u, __float_as_uint(most) >> 23));
-      const float up = __uint_as_float(ex << 23), down = __uint_as_float((254u - ex) << 23);
+      float f = 0.f;                        // a row's share over l
       if (row_ok) {
         float2 stat[8];                     // all on their way before the first is used
 #pragma unroll
@@ -913,10 +893,7 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           if (k < p.splits) sum = fmaf(fast_exp2(stat[k].x - top), stat[k].y, sum);
-        const float f = n_tiles > 0 ? fast_exp2(ref - top) / sum * unit * up : 0.f;
-#pragma unroll 1
-        for (int k = 0; k < owners; ++k)
-          st_peer1(peer(sbase + OFF_UNITS + ((rank * 2 + hh) * BM + r) * 4, k), f);
+        if (n_tiles > 0) f = fast_exp2(ref - top) / sum;
       }
 #pragma unroll 1
       for (int c = 0; c < HD; c += 16) {
@@ -929,17 +906,15 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
           reg_fence(o);
         }
         // W is at least 16: the 16 columns have one owner
-        const int piece = ((rank * 2 + hh) << (w - 3)) + ((c & ((1 << w) - 1)) >> 3);
+        const int piece = ((rank * 2 + hh) << (w - 2)) + ((c & ((1 << w) - 1)) >> 2);
         const uint32_t at = peer(sbase + piece * (BM * 16) + r * 16, c >> w);
         if (row_ok) {
-          uint32_t h[8];
+          // f first: the unit may leave the normal range when V's scales do
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const __half2 x = __floats2half2_rn(o[2 * i] * down, o[2 * i + 1] * down);
-            h[i] = *reinterpret_cast<const uint32_t*>(&x);
-          }
-          st_peer4(at, h[0], h[1], h[2], h[3]);
-          st_peer4(at + BM * 16, h[4], h[5], h[6], h[7]);
+          for (int i = 0; i < 16; ++i) o[i] = o[i] * f * unit;
+#pragma unroll
+          for (int i = 0; i < 16; i += 4)
+            st_peer4(at + i / 4 * (BM * 16), o[i], o[i + 1], o[i + 2], o[i + 3]);
         }
       }
       cluster_sync();
@@ -950,28 +925,22 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
       for (int i = tid; i < (rows0 + rows1) * groups; i += kSoftThreads) {
         const int row = i >> shift, c8 = i & (groups - 1);
         const int h = row >= rows0 ? 1 : 0, rr = row - (h ? rows0 : 0);
-        uint4 x[8];
-        float u[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          if (k < p.splits) {
-            x[k] = lds16(sbase + (((k * 2 + h) << shift) + c8) * (BM * 16) + rr * 16);
-            u[k] = *reinterpret_cast<const float*>(smem + OFF_UNITS + ((k * 2 + h) * BM + rr) * 4);
-          }
-        }
         float acc[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[j] = 0.f;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           if (k < p.splits) {
-            const uint32_t v[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&v[j]));
-              acc[2 * j] = fmaf(y.x, u[k], acc[2 * j]);
-              acc[2 * j + 1] = fmaf(y.y, u[k], acc[2 * j + 1]);
-            }
+            const uint32_t at = sbase + (((k * 2 + h) << (w - 2)) + 2 * c8) * (BM * 16) + rr * 16;
+            const uint4 x = lds16(at), y = lds16(at + BM * 16);
+            acc[0] += __uint_as_float(x.x);
+            acc[1] += __uint_as_float(x.y);
+            acc[2] += __uint_as_float(x.z);
+            acc[3] += __uint_as_float(x.w);
+            acc[4] += __uint_as_float(y.x);
+            acc[5] += __uint_as_float(y.y);
+            acc[6] += __uint_as_float(y.z);
+            acc[7] += __uint_as_float(y.w);
           }
         }
         __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) +

@@ -118,3 +118,23 @@ def test_decode_small_results_beside_a_large_scale(bigger, hkv):
     got = C.decode(pools, torch.ones_like(q), table, [500], SCALE)
     assert bool(got.any())
     C.check_decode(pools, torch.ones_like(q), table, [500], SCALE, got)
+
+
+@pytest.mark.parametrize("hkv,prior,chunk", [(2, 500, 77), (1, 3100, 60), (8, 1000, 500), (1, 850, 40)])
+def test_prefill_small_elements_beside_large_ones(hkv, prior, chunk):
+    """Queries of zero give every key the same weight, a power of two, so P is
+    exact and a result is the mean of the codes rounded to bf16: elements of 448
+    and ones of 2^-13 in one row, whichever CTAs of a cluster they come from."""
+    pools, q, row = P._case(prior, chunk, hkv, 2, poison=False, k_spread=0, v_spread=0)
+    codes = torch.zeros(16, 128, dtype=torch.uint8)
+    codes[:, :64] = 0x7E
+    codes[torch.arange(128) % 16, torch.arange(128)] = 1     # 2^-9 in every 16th key
+    codes[:, :64] = 0x7E
+    pools.codes[1][:] = codes
+    pools.scale[1][:] = 127
+    got = P._run(pools, torch.zeros_like(q), row, prior).double()
+    seen = prior + torch.arange(chunk)[:, None] + 1          # keys of each row; those of its 16th: d, d + 16, ...
+    mean = ((seen - 1 - torch.arange(128) % 16) // 16 + 1) * 2.0 ** -9 / seen
+    mean[:, :64] = 448.0
+    # half a step of bf16, and 2^-20 for the fp32 sums of a few thousand exact terms
+    assert bool(((got - mean[:, None]).abs() <= (2.0 ** -8 + 2.0 ** -20) * mean[:, None]).all())
