@@ -827,13 +827,15 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
       __syncwarp();
       tc_fence_after();
     }
-    // l stands for l 2^ref, O for O 2^M = O 2^ref unit.  The results take 1 / l
-    // and then the unit, which may leave the normal range when V's scales do.
+    // l stands for l 2^ref, O for O 2^M = O 2^ref unit unit2.  The results take
+    // 1 / l and then the unit, which may leave the normal range when V's scales
+    // do (in two factors where it is an exponential, which flushes there).
     const int e = n_tiles > 0 ? (reinterpret_cast<const TileScales*>(smem + OFF_SCALES))->e : 0;
     const float ref = wide ? ms_run : m_run - (float)e;
     const float unit = !wide ? scale_value((uint32_t)(e + 127))
                        : m_run == -INFINITY ? 0.f   // no key of the row in this CTA
-                                            : fast_exp2(m_run - ms_run);
+                                            : fast_exp2(0.5f * (m_run - ms_run));
+    const float unit2 = wide ? unit : 1.f;
     if (n_tiles > 0 && row_pos >= *nan_key)
       l_run = __int_as_float(0x7fffffff);   // the row sees a NaN value
     const bool row_ok = (q0 + r) < a.chunk_len;
@@ -851,7 +853,7 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
         tmem_wait_ld();
         reg_fence(o);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = o[i] * inv * unit;
+        for (int i = 0; i < 32; ++i) o[i] = o[i] * inv * unit * unit2;
 #pragma unroll
         for (int i = 0; i < 32; i += 8)
           sts16(tile + r * 256 + ((((c + i) / 8) ^ (r & 15)) << 4),
@@ -911,7 +913,7 @@ prefill_fp8_block_kernel(const __grid_constant__ Params p, const __grid_constant
         if (row_ok) {
           // f first: the unit may leave the normal range when V's scales do
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = o[i] * f * unit;
+          for (int i = 0; i < 16; ++i) o[i] = o[i] * f * unit * unit2;
 #pragma unroll
           for (int i = 0; i < 16; i += 4)
             st_peer4(at + i / 4 * (BM * 16), o[i], o[i + 1], o[i + 2], o[i + 3]);

@@ -138,3 +138,12 @@ def test_prefill_small_elements_beside_large_ones(hkv, prior, chunk):
     mean[:, :64] = 448.0
     # half a step of bf16, and 2^-20 for the fp32 sums of a few thousand exact terms
     assert bool(((got - mean[:, None]).abs() <= (2.0 ** -8 + 2.0 ** -20) * mean[:, None]).all())
+
+
+@pytest.mark.parametrize("prior,chunk", [(0, 600), (420, 80)])
+@pytest.mark.parametrize("bigger", [9, 17, 25])              # before, in and behind the tile of the far block
+def test_prefill_small_results_beside_a_large_scale(bigger, prior, chunk):
+    pools, q, row = P._case(prior, chunk, 2, 2, poison=False, k_spread=0)
+    _far_block_that_counts_for_nothing(pools, row, bigger, 20)
+    got = P._run(pools, torch.ones_like(q), row, prior)
+    P._check(pools, torch.ones_like(q), row, prior, got, rows=[0, 1, chunk // 2, chunk - 1])
