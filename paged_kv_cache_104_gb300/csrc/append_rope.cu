@@ -339,7 +339,7 @@ struct RowTurn {
 // the top here; below 2^-6, where codes are 2^-9 apart, so it has with 2^-6
 // added.
 // (GPU time of a chunk of 2,048 tokens: 13.0 us with the codes and scales of the
-// fp32 values, 13.5 with the exact codes, 14.1 with the exact scales too;
+// fp32 values, 13.5 with the exact codes, 14.0 with the exact scales too;
 // all in fp64, at 2 operations a clock and SM, would take 10 us more.)
 constexpr uint32_t kNear = 4;
 __device__ __forceinline__ uint32_t off_middle(float y) {
@@ -528,6 +528,43 @@ __device__ __forceinline__ uint32_t write_codes(const RopeAppendArgs& a,
   return again;
 }
 
+// A run's maximum that is not the scale's yet: an element is infinite or NaN, or
+// fp32 may have put the maximum on the other side of a border.
+__device__ __forceinline__ bool unsettled(uint32_t top, bool rotated) {
+  return top >= 0x7f800000u || (rotated && near_border(top));
+}
+
+// Such maxima taken again in fp64 (one run in a million), in the first `heads`
+// heads: the caller's elements el0 .. el0 + 7 of tokens w0 + j, of run `of`, and
+// w0 + j2, of run of2.  (Out of line: as a part of the kernel it took a chunk of
+// 2,048 tokens from 14.0 to 14.3 us.)
+template <int UPC>
+__device__ __noinline__ void settle(const RopeAppendArgs& a, WindowRuns<UPC>& runs,
+                                    const __nv_bfloat16* src, int64_t stride, int64_t w0, int heads,
+                                    bool rotated, bool turned_here, int el0, int j, int of, int j2,
+                                    int of2) {
+  uint32_t todo = 0;
+  for (int u = 0; u < UPC; ++u) {
+    if (of >= 0 && unsettled(runs.top[u][of], rotated)) todo |= 1u << u;
+    if (of2 >= 0 && unsettled(runs.top[u][of2], rotated)) todo |= 0x100u << u;
+  }
+  __syncthreads();
+  if (threadIdx.x < kWindow) {
+    for (int u = 0; u < UPC; ++u)
+      if (unsettled(runs.top[u][threadIdx.x], rotated)) runs.top[u][threadIdx.x] = 0;
+  }
+  __syncthreads();
+  todo &= ((1u << heads) - 1) * 0x101u;
+#pragma unroll 1
+  for (; todo; todo &= todo - 1) {
+    const int bit = __ffs(todo) - 1, u = bit & 7;
+    const int64_t t = w0 + (bit < 8 ? j : j2);
+    atomicMax(&runs.top[u][bit < 8 ? of : of2],
+              exact_max(a.rope, a.num_tokens, src + t * stride + u * a.head_dim, t, el0, turned_here));
+  }
+  __syncthreads();
+}
+
 // The first kv_ctas CTAs take the runs of new tokens that start in a window of
 // 16 tokens, in up to UPC heads of one pool.  Thread (i, c) has chunk c of token
 // i, and of token i + 16 where a run goes on beyond the window; the runs'
@@ -634,37 +671,6 @@ kv_append_fp8_block_kernel(const __grid_constant__ RopeAppendArgs a, int kv_ctas
       if (c == 0 && of >= 0) atomicMax(&runs.top[u][of], m);
     }
   };
-  // A run's maximum that is not the scale's yet: an element is infinite or NaN,
-  // or fp32 may have put the maximum on the other side of a border.
-  auto unsettled = [&](uint32_t top) {
-    return top >= 0x7f800000u || (rotated && near_border(top));
-  };
-  // Such maxima taken again in fp64 (one run in a million).
-  auto settle = [&](int j, int of, int j2, int of2) {
-    uint32_t todo = 0;
-#pragma unroll
-    for (int u = 0; u < UPC; ++u) {
-      if (of >= 0 && unsettled(runs.top[u][of])) todo |= 1u << u;
-      if (of2 >= 0 && unsettled(runs.top[u][of2])) todo |= 0x100u << u;
-    }
-    __syncthreads();
-    if (threadIdx.x < kWindow) {
-#pragma unroll
-      for (int u = 0; u < UPC; ++u)
-        if (unsettled(runs.top[u][threadIdx.x])) runs.top[u][threadIdx.x] = 0;
-    }
-    __syncthreads();
-    if (!mine) todo = 0;
-    todo &= ((1u << ng) - 1) * 0x101u;
-#pragma unroll 1
-    for (; todo; todo &= todo - 1) {
-      const int bit = __ffs(todo) - 1, u = bit & 7, at = bit < 8 ? j : j2;
-      atomicMax(&runs.top[u][bit < 8 ? of : of2],
-                exact_max(a.rope, a.num_tokens, src - c * 8 + (w0 + at) * stride + u * a.head_dim,
-                          w0 + at, c * 8, turned_here));
-    }
-    __syncthreads();
-  };
   auto write = [&](int j, int k) {
     if (k < 0 || !mine) return;
     uint32_t again = 0;
@@ -703,9 +709,10 @@ kv_append_fp8_block_kernel(const __grid_constant__ RopeAppendArgs a, int kv_ctas
   }
   bool some = false;
 #pragma unroll
-  for (int u = 0; u < UPC; ++u) some |= unsettled(runs.top[u][threadIdx.x % kWindow]);
+  for (int u = 0; u < UPC; ++u) some |= unsettled(runs.top[u][threadIdx.x % kWindow], rotated);
   if (__any_sync(0xffffffffu, some)) {     // the same in every warp
-    settle(j, run, j2, run2);
+    settle<UPC>(a, runs, src - c * 8, stride, w0, mine ? ng : 0, rotated, turned_here, c * 8, j, run,
+                j2, run2);
     rows_of(beyond ? j2 : j);              // read again, so that no registers wait for this
   }
   if (beyond) {
