@@ -95,8 +95,9 @@ merge_row_kernel(const DecodeArgs a) {
   for (int w = 0; w < live; ++w) M = fmaxf(M, ml[w].x);
   float L = 0.f, O = 0.f;
   for (int w = 0; w < live; ++w) L = fmaf(ex2(ml[w].x - M), ml[w].y, L);
+  const float inv = 1.f / L;
   for (int w = 0; w < live; ++w)
-    O = fmaf(ex2(ml[w].x - M) * ml[w].y / L, reinterpret_cast<const float*>(part[w])[threadIdx.x], O);
+    O = fmaf(ex2(ml[w].x - M) * ml[w].y * inv, reinterpret_cast<const float*>(part[w])[threadIdx.x], O);
   static_cast<__nv_bfloat16*>(a.out)[(int64_t)row * kHD + threadIdx.x] = __float2bfloat16_rn(O);
 }
 

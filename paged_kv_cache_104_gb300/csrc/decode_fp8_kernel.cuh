@@ -615,11 +615,12 @@ decode_fp8_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tm_k,
         l_run[nt][j] += __shfl_xor_sync(kAll8, l_run[nt][j], 16);
       }
     const bool direct = (u.ns == 1);
-    // BS: what O / l lacks to be a result, 2^E or 2^(M - m), in two factors: their
-    // product may leave fp32's normal range where the result does not.  l is
-    // divided by first: O 2^E can overflow where O 2^E / l, an average of cached
-    // values, cannot.  (A warp that met no block gives 0.)
-    float unit[NT][2][2], inv_l[NT][2];
+    // BS: O / l lacks 2^E, or 2^(M - m), to be a result.  It comes in two factors, as
+    // it may leave fp32's normal range where the result does not: the first with
+    // 1 / l (still a normal number), then the other.  O 2^E by itself
+    // can overflow where O 2^E / l, an average of cached values, cannot.  (A warp
+    // that met no block gives 0.)
+    float part[NT][2], rest[NT][2];
     if constexpr (BS) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -627,14 +628,15 @@ decode_fp8_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tm_k,
         for (int j = 0; j < 2; ++j) {
           m_run[nt][j] = wide ? comb_ml[(warp * G + min(8 * nt + 2 * t + j, G - 1)) * 2]
                               : mo_run[nt][j] - (float)e_ref;
-          inv_l[nt][j] = m_run[nt][j] == -INFINITY && l_run[nt][j] == 0.f ? 0.f : 1.f / l_run[nt][j];
           if (wide) {
-            unit[nt][j][0] = unit[nt][j][1] = ex2(0.5f * (mo_run[nt][j] - m_run[nt][j]));
+            part[nt][j] = rest[nt][j] = ex2(0.5f * (mo_run[nt][j] - m_run[nt][j]));
           } else {
             const int half = e_ref >> 1;
-            unit[nt][j][0] = scale_of((uint32_t)(half + 127));
-            unit[nt][j][1] = scale_of((uint32_t)(e_ref - half + 127));
+            part[nt][j] = scale_of((uint32_t)(half + 127));
+            rest[nt][j] = scale_of((uint32_t)(e_ref - half + 127));
           }
+          part[nt][j] = m_run[nt][j] == -INFINITY && l_run[nt][j] == 0.f
+                            ? 0.f : part[nt][j] / l_run[nt][j];
         }
       __syncwarp();   // m is read before its place is written
     }
@@ -649,7 +651,7 @@ decode_fp8_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tm_k,
         for (int j = 0; j < 2; ++j) {
           const int hh = 8 * nt + 2 * t + j;
           if (hh < G) {
-            const float rl = BS ? inv_l[nt][j] : vscale / l_run[nt][j];
+            const float rl = BS ? part[nt][j] : vscale / l_run[nt][j];
             const int64_t row = (int64_t)u.b * a.num_q_heads + hq0 + hh;
             const int64_t pidx = row * a.max_splits + u.s;
 #pragma unroll
@@ -657,8 +659,8 @@ decode_fp8_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tm_k,
               const int d = 16 * g + 2 * mt;
               float x0 = o[nt][mt][j] * rl, x1 = o[nt][mt][j + 2] * rl;
               if constexpr (BS) {
-                x0 = x0 * unit[nt][j][0] * unit[nt][j][1];
-                x1 = x1 * unit[nt][j][0] * unit[nt][j][1];
+                x0 *= rest[nt][j];
+                x1 *= rest[nt][j];
               }
               if (direct)
                 *reinterpret_cast<__nv_bfloat162*>(outp + row * kHD + d) = __floats2bfloat162_rn(x0, x1);
@@ -690,8 +692,8 @@ decode_fp8_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
             for (int mt = 0; mt < 8; ++mt)   // pair slot mt stored at mt ^ g: no bank conflicts
               *reinterpret_cast<float2*>(crow + 2 * (mt ^ g)) =
-                  BS ? make_float2(o[nt][mt][j] * inv_l[nt][j] * unit[nt][j][0] * unit[nt][j][1],
-                                   o[nt][mt][j + 2] * inv_l[nt][j] * unit[nt][j][0] * unit[nt][j][1])
+                  BS ? make_float2(o[nt][mt][j] * part[nt][j] * rest[nt][j],
+                                   o[nt][mt][j + 2] * part[nt][j] * rest[nt][j])
                      : make_float2(o[nt][mt][j], o[nt][mt][j + 2]);
           }
         }
@@ -709,11 +711,11 @@ decode_fp8_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tm_k,
           wk[k] = (mk == -INFINITY) ? 0.f : ex2(mk - M);
           L = fmaf(wk[k], comb_ml[(k * G + h) * 2 + 1], L);
         }
-        // BS: the warps' results, weighted by their shares of L
         const float rl = BS ? 1.f : vscale / L;
-        if constexpr (BS) {
+        if constexpr (BS) {   // the warps' results, weighted by their shares of L
+          const float inv = 1.f / L;
 #pragma unroll
-          for (int k = 0; k < kCW; ++k) wk[k] *= comb_ml[(k * G + h) * 2 + 1] / L;
+          for (int k = 0; k < kCW; ++k) wk[k] *= comb_ml[(k * G + h) * 2 + 1] * inv;
         }
         const int64_t row = (int64_t)u.b * a.num_q_heads + hq0 + h;
         const int64_t pidx = row * a.max_splits + u.s;
