@@ -494,7 +494,8 @@ def decode_fp8_block_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_hea
 
 def decode_workspace_fp8_block(num_seqs, num_q_heads, num_kv_heads, head_dim, max_seq_len,
                                device="cuda"):
-    """Allocate (through torch) the workspace paged_decode_attention_fp8_block needs."""
+    """Allocate (through torch) the workspace paged_decode_attention_fp8_block needs
+    (one of ``decode_workspace`` will do, but makes small batches up to three times slower)."""
     n = decode_fp8_block_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, max_seq_len)
     return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
 
@@ -505,8 +506,8 @@ def paged_decode_attention_fp8_block(out, q, k_cache, v_cache, k_scale, v_scale,
     """Decode over block-scaled uint8 E4M3 pools [NB, Hkv, bs, 128] with scale
     bytes [NB, Hkv]; q/out bf16 [B, Hq, 128]; block_table [B, max_blocks] and
     seq_lens [B] int32 (0: a padded row, left alone); max_seq_len >=
-    max(seq_lens); workspace from ``decode_workspace_fp8_block``, for this
-    batch or a larger one."""
+    max(seq_lens), and at least 1; workspace from ``decode_workspace_fp8_block``,
+    for this batch or a larger one."""
     fn = "pkv_paged_decode_attention_fp8_block"
     if k_cache.dtype is not torch.uint8:
         _refuse(fn, f"the pools are {k_cache.dtype}, not torch.uint8")

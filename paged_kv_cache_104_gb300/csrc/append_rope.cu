@@ -9,6 +9,7 @@
 // other elements are copied.
 // The axis of a pair is the caller's table, so one axis (text), sections of
 // time, height and width, or axes taken in turn are one kernel.
+// Times in this file are GPU time, taken in CUDA graphs.
 #include <algorithm>
 
 #include "common.cuh"

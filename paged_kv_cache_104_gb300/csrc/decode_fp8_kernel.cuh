@@ -49,7 +49,9 @@
 // Each consumer warp reads its own blocks' scale bytes, one block per lane, a
 // window of 32 stages ahead.  Before the queries become f16 a power of two brings
 // each head's largest element to [2^14, 2^15): elements down to 2^-31 of it keep
-// all their bits, smaller ones are off by at most 2^-39 of it.
+// all their bits, smaller ones are off by at most 2^-39 of it.  p is f16 for the
+// second product: its 11 bits are three more than the result has, and below 2^-14
+// of a head's largest it is off by 2^-25 of that; l sums p in fp32.
 #pragma once
 
 #include <cuda.h>

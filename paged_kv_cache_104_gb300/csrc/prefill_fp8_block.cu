@@ -20,7 +20,9 @@
 //    the time of one 16-bit product.
 //  * P V: P is f16, V's codes are widened to f16 (exact) by four converter
 //    warps, from staging tiles that 1-D bulk copies fill (a block and head is
-//    2 KiB in one piece) into the 128B-swizzled tiles the MMAs read.
+//    2 KiB in one piece) into the 128B-swizzled tiles the MMAs read.  P's 11 bits
+//    are three more than the result has: a weight is off by 2^-11 at most, below
+//    2^-14 of the row's largest by 2^-25 of that; l sums the weights in fp32.
 //  * The scales act in the softmax, where they are uniform over 16 columns:
 //    key j of a block with scales 2^ek, 2^ev has the score t_j 2^ek and the
 //    output weight p_j = 2^(s_j + ev - M), M the running maximum of s_j + ev
@@ -1005,11 +1007,13 @@ cudaError_t cluster_slots(int num_sms, ClusterSlots* out) {
 
 // CTAs to an item: the number by which the longest share of the GPU ends first.
 // Items go to the slots heaviest first, back and forth; an item costs its
-// tiles (1.56 us measured) and 6.5 us, when it is split 9.6 us and 0.45 us a CTA.
+// tiles (1.56 us measured) and 6.5 us, when it is split 9.6 us and 0.45 us a CTA
+// (short chunks; where 128 rows meet, their fp32 sums take up to 2 us more).
 // (640 rows of 32 heads over 16,384 keys are 80 items: one CTA each leaves 72
-// SMs idle.)  Measured against the best of all splits in us: 128 rows over
-// 1,024 keys 15.2 (8 CTAs, as many as SMs would hold: 26.5), 768 over 16,000
-// 179.7 (one: 205), 1,024 rows of 4 heads over 4,096 24.1 (8: 37).
+// SMs idle.)  The choice is the best of all splits, in us: 128 rows over 1,024
+// keys 15.9 (8 CTAs, as many as SMs would hold: 26.8), 640 over 16,384 169 (one:
+// 209), 768 over 16,768 196 (one: 215), 1,024 rows of 4 heads over 5,120 27.9 (8:
+// 39.8), 200 of 8 heads over 32,200 63 (one: 389).
 int choose_splits(const Params& p, int n_x, int n_t, const ClusterSlots& slots) {
   const int64_t n = (int64_t)n_x * n_t;
   if (n > 4 * (int64_t)slots.at[1]) return 1;          // many items even out by themselves
