@@ -302,7 +302,7 @@ decode_fp8_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tm_k,
     if (a.balanced && u.s == 0 && (HS ? lane == 0 : tid == 0))
       a.ws_np[u.b * a.num_kv_heads + head] = u.ns;
     const float sl2 =
-        a.scale * 1.4426950408889634f * (BS ? 1.f : __ldg(a.k_scale + (BS ? 0 : head)));
+        (BS ? a.scale : a.scale * __ldg(a.k_scale + (BS ? 0 : head))) * 1.4426950408889634f;
     const float vscale = BS ? 1.f : __ldg(a.v_scale + (BS ? 0 : head));
     // BS: the scale bytes (K in bits 0-7, V in 8-15) of the blocks this warp
     // meets in 32 stages, lane i holding stage i's; the next window's are
