@@ -78,6 +78,8 @@ typedef enum { PKV_F32 = 0, PKV_BF16 = 1 } pkv_dtype;
 #define PKV_DEVERR_SMEM_LAYOUT 5  /* shared memory not laid out as a kernel needs (call skipped) */
 #define PKV_DEVERR_POSITION_RANGE 6 /* rotating append: position outside the table (token skipped) */
 #define PKV_DEVERR_SLOT_ORDER 7   /* block-scaled append: a block's new rows not in order (entry skipped) */
+#define PKV_DEVERR_DRAFT_RANGE 8  /* draft_offsets: a count or row outside its bounds (sequence skipped) */
+#define PKV_DEVERR_KEPT_RANGE 9   /* kv_compact: a kept row (entry skipped) or count (sequence skipped) outside its bounds */
 
 /* Largest num_seqs accepted by paged_decode_attention. */
 #define PKV_MAX_SEQS 8192
@@ -506,6 +508,149 @@ pkv_status pkv_mla_decode_attention_append(void *out, const void *q, const void 
                                            int64_t num_blocks, int num_q_heads, int head_dim,
                                            int rank, int block_size, float scale, void *workspace,
                                            size_t workspace_bytes, pkv_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Drafted tokens and eviction: what a serving loop does with the same pools
+ * between two decode steps.  Drafted tokens are appended (pkv_kv_append, or a
+ * rotating append), attend in one call, and the accepted ones move up; a
+ * sequence that has grown too long keeps the tokens that got most attention.
+ * ------------------------------------------------------------------------- */
+#define PKV_MAX_DRAFT 64              /* drafted tokens per sequence */
+#define PKV_MAX_COMPACT_ROW_BYTES 1024
+
+/*
+ * Sequence b has n_b = draft_offsets[b + 1] - draft_offsets[b] drafted tokens,
+ * 0 <= n_b <= max_draft: rows draft_offsets[b] .. of q, and the last n_b of
+ * its seq_lens[b] stored tokens (their keys and values are in the pools).
+ * Row i of a sequence sees every token before the drafted ones, and drafted
+ * token j if bit j of its tree_mask word is set (bits at n_b and above are
+ * ignored); without a tree_mask the drafted tokens are a chain, and row i
+ * sees drafted tokens 0 .. i.  A row need not see itself.
+ */
+typedef struct pkv_tree_args {
+  void *out;                   /* attention: [num_rows][num_q_heads][head_dim], device, written */
+  float *lse;                  /* [num_rows][num_q_heads]; attention: written, or NULL; */
+                               /* add_weights: read */
+  const void *q;               /* as out, read */
+  const void *k_cache;         /* pools [num_blocks][num_kv_heads][block_size][head_dim], read */
+  const void *v_cache;         /* attention only */
+  const int32_t *block_table;  /* [num_seqs][max_blocks_per_seq] */
+  const int32_t *seq_lens;     /* [num_seqs]; 1 .. max_seq_len where n_b > 0, else not read into */
+                               /* anything */
+  const int32_t *draft_offsets; /* [num_seqs + 1], not decreasing, within 0 .. num_rows */
+  const int64_t *tree_mask;    /* [num_rows] or NULL */
+  float *weights;              /* add_weights only: [num_seqs][num_kv_heads][weights_len], */
+                               /* device, read and written */
+  void *workspace;             /* attention only: pkv_tree_workspace_bytes, 256-byte aligned; */
+                               /* holds nothing between calls and needs no clearing */
+  size_t workspace_bytes;
+  int64_t weights_len;         /* >= max_seq_len */
+  int64_t num_blocks;
+  int num_seqs;                /* 0: nothing is done */
+  int num_rows;                /* rows of q (0: nothing is done); those outside every sequence's */
+                               /* range are left alone in out and lse */
+  int max_blocks_per_seq;
+  int max_seq_len;             /* bound on every seq_lens[b] */
+  int max_draft;               /* bound on every n_b, 1 .. PKV_MAX_DRAFT */
+  int num_q_heads;             /* as for pkv_paged_decode_attention: bf16 with head_dim 128 and */
+  int num_kv_heads;            /* groups of 1, 2, 4, 8 or 16; fp32 with head_dim 16 or 128 and */
+  int head_dim;                /* groups of 1, 2, 4 or 8 */
+  int block_size;
+  pkv_dtype dtype;             /* of q, out and the pools */
+  float scale;                 /* positive */
+} pkv_tree_args;
+
+/*
+ * Bytes of device workspace paged_tree_attention needs: it depends on the
+ * rows of a sequence only, not on the batch.  0 on sizes no call takes.
+ * Host-only, no GPU use.
+ */
+size_t pkv_tree_workspace_bytes(int num_q_heads, int num_kv_heads, int head_dim, int max_draft,
+                                int max_seq_len);
+
+/*
+ * paged_tree_attention -- attention of drafted tokens over their sequence's
+ * cache and over one another.  For row i of sequence b and query head h, over
+ * the keys n it sees,
+ *   s_n = scale q_ih . k_n,  lse_ih = ln sum_n e^s_n,
+ *   out_ih = sum_n e^(s_n - lse_ih) v_n
+ * in fp32, out rounded once to dtype.  A row that sees nothing gets out = 0
+ * and lse = -inf.  Values of keys that a row does not see never reach it.
+ * Accuracy as paged_decode_attention.
+ */
+pkv_status pkv_paged_tree_attention(const pkv_tree_args *args, pkv_stream_t stream);
+
+/*
+ * kv_add_weights -- the attention each stored token got, added up:
+ *   weights[b][g][n] += sum over the rows i of sequence b that see token n,
+ *                       and the query heads h of KV head g, of e^(s_n - lse_ih)
+ * with s_n and the rows as above and lse as paged_tree_attention gave it.  A
+ * row whose lse is -inf adds nothing.  Sums are fp32, added in a fixed order:
+ * the same inputs give the same bits.  Entries at seq_lens[b] and beyond, and
+ * those of sequences without rows, are left alone.  Start from zeros.
+ */
+pkv_status pkv_kv_add_weights(const pkv_tree_args *args, pkv_stream_t stream);
+
+/*
+ * kv_select -- which tokens of each sequence stay.  Of sequence b's
+ * n = seq_lens[b] tokens, KV head g keeps kept_lens[b] = min(n, budget): the
+ * first `sinks`, the last `recent`, and of the others those with the largest
+ * weights[b][g][t]; of equal weights the earlier token, a NaN after every
+ * number.  Their positions go to kept[b][g][0 .. kept_lens[b]), ascending;
+ * entries behind those are left alone.
+ *   kept       int32 [num_seqs][num_kv_heads][budget], device, written
+ *   kept_lens  int32 [num_seqs], device, written
+ *   weights    fp32 [num_seqs][num_kv_heads][weights_len], device, read
+ *   seq_lens   int32 [num_seqs], 0 .. max_seq_len; one outside is reported in
+ *              the device error word, and its kept_lens is 0
+ *   sinks + recent <= budget, weights_len >= max_seq_len
+ */
+pkv_status pkv_kv_select(int32_t *kept, int32_t *kept_lens, const float *weights,
+                         int64_t weights_len, const int32_t *seq_lens, int num_seqs,
+                         int num_kv_heads, int max_seq_len, int budget, int sinks, int recent,
+                         pkv_stream_t stream);
+
+typedef struct pkv_compact_args {
+  void *k_cache;               /* pools [num_blocks][num_kv_heads][block_size][row_bytes], device, */
+  void *v_cache;               /* read and written */
+  float *weights;              /* [num_seqs][num_kv_heads][weights_len], device, read and written, */
+                               /* or NULL */
+  const int32_t *block_table;  /* [num_seqs][max_blocks_per_seq] */
+  const int32_t *seq_lens;     /* [num_seqs]: tokens stored before the call */
+  const int32_t *kept;         /* [num_seqs][kept_heads][kept_len]: positions in the sequence */
+  const int32_t *kept_lens;    /* [num_seqs], 0 .. kept_len */
+  const int32_t *first;        /* [num_seqs], or NULL: 0 */
+  int64_t weights_len;         /* >= every seq_lens[b] */
+  int64_t num_blocks;
+  int num_seqs;                /* 0: nothing is done */
+  int max_blocks_per_seq;
+  int num_kv_heads;
+  int kept_heads;              /* num_kv_heads, or 1: the same rows in every head */
+  int kept_len;
+  int row_bytes;               /* of one token's key (or value) in one head: a multiple of 16, at */
+                               /* most PKV_MAX_COMPACT_ROW_BYTES */
+  int block_size;
+} pkv_compact_args;
+
+/*
+ * kv_compact -- rows that stay move up, in place.  For each sequence b, KV
+ * head g and i < kept_lens[b], the key, value and weight at position
+ * first[b] + i become those that position kept[b][g][i] had before the call;
+ * the weights from there to seq_lens[b] become 0.  The sequence then has
+ * first[b] + kept_lens[b] tokens.
+ *   After kv_select: first NULL, kept as it gave it, all heads' rows.
+ *   After a tree was verified: first the length without the drafted tokens,
+ *   kept the accepted ones' positions, the same in every head (kept_heads 1).
+ * kept[b][g][i] >= first[b] + i (true of every ascending list that starts at
+ * or behind first) and < seq_lens[b]; an entry outside is reported in the
+ * device error word and skipped, as is one whose block id is outside the
+ * pool.  A position may occur twice.  The blocks of one sequence must not
+ * be another's (those of a shared prefix neither read nor written excepted).
+ * Rows are copied byte by byte: bf16, fp32 and E4M3 codes with one scale per
+ * head alike.  A pool of kv_append_fp8_block has a scale per block and cannot
+ * be compacted.
+ */
+pkv_status pkv_kv_compact(const pkv_compact_args *args, pkv_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * Prefix caching (host-only): chained block hashes and a hash -> block index.

@@ -24,7 +24,8 @@ PKV_F32, PKV_BF16 = 0, 1
 DEVERR = {0: "none", 1: "slot out of range", 2: "block id out of range",
           3: "sequence length out of range", 4: "internal wait timed out",
           5: "shared-memory layout check failed", 6: "position out of range",
-          7: "new rows of a block out of order"}
+          7: "new rows of a block out of order", 8: "drafted tokens out of range",
+          9: "kept row out of range"}
 EXPORTS = ("pkv_kv_append", "pkv_decode_workspace_bytes", "pkv_paged_decode_attention",
            "pkv_paged_decode_attention_append", "pkv_paged_decode_attention_noalloc", "pkv_chunked_prefill_attention",
            "pkv_decode_prefill_attention",
@@ -33,6 +34,8 @@ EXPORTS = ("pkv_kv_append", "pkv_decode_workspace_bytes", "pkv_paged_decode_atte
            "pkv_kv_append_rope", "pkv_kv_append_fp8_block",
            "pkv_decode_fp8_block_workspace_bytes", "pkv_paged_decode_attention_fp8_block",
            "pkv_chunked_prefill_attention_fp8_block",
+           "pkv_tree_workspace_bytes", "pkv_paged_tree_attention", "pkv_kv_add_weights", "pkv_kv_select",
+           "pkv_kv_compact",
            "pkv_latent_append", "pkv_mla_workspace_bytes", "pkv_mla_decode_attention",
            "pkv_mla_decode_attention_append",
            "pkv_fnv1a64", "pkv_prefix_hash_blocks", "pkv_prefix_cache_create",
@@ -40,6 +43,7 @@ EXPORTS = ("pkv_kv_append", "pkv_decode_workspace_bytes", "pkv_paged_decode_atte
            "pkv_prefix_cache_evict", "pkv_prefix_cache_match", "pkv_prefix_plan",
            "pkv_l2_flush", "pkv_set_span_buffer")
 MAX_ROPE_AXES = 4                 # PKV_MAX_ROPE_AXES
+MAX_DRAFT = 64                    # PKV_MAX_DRAFT
 NOALLOC_SCRATCH_BYTES = 32 << 20  # PKV_NOALLOC_SCRATCH_BYTES
 
 
@@ -84,6 +88,30 @@ class RopeAppendArgs(ctypes.Structure):
 _ROPE_APPEND = struct.Struct("@9P6q5iPqP3iP")
 
 
+class TreeArgs(ctypes.Structure):
+    """pkv_tree_args (field order and types as in pagedkv.h)."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("out", "lse", "q", "k_cache", "v_cache", "block_table", "seq_lens",
+                                                "draft_offsets", "tree_mask", "weights", "workspace")] +
+                [("workspace_bytes", ctypes.c_size_t), ("weights_len", ctypes.c_int64),
+                 ("num_blocks", ctypes.c_int64)] +
+                [(n, ctypes.c_int) for n in ("num_seqs", "num_rows", "max_blocks_per_seq", "max_seq_len", "max_draft",
+                                             "num_q_heads", "num_kv_heads", "head_dim", "block_size", "dtype")] +
+                [("scale", ctypes.c_float)])
+
+
+class CompactArgs(ctypes.Structure):
+    """pkv_compact_args (field order and types as in pagedkv.h)."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k_cache", "v_cache", "weights", "block_table", "seq_lens", "kept",
+                                                "kept_lens", "first")] +
+                [("weights_len", ctypes.c_int64), ("num_blocks", ctypes.c_int64)] +
+                [(n, ctypes.c_int) for n in ("num_seqs", "max_blocks_per_seq", "num_kv_heads", "kept_heads",
+                                             "kept_len", "row_bytes", "block_size")])
+
+
+_TREE = struct.Struct("@11PN2q10if")
+_COMPACT = struct.Struct("@8P2q7i")
+
+
 class PagedKVError(RuntimeError):
     def __init__(self, fn: str, status: int, msg: str):
         super().__init__(f"{fn} failed: status {status} ({msg})")
@@ -119,13 +147,19 @@ def open_library(path: str):
     lib.pkv_paged_decode_attention_fp8.argtypes = [p, p, p, p, p, p, p, p, i, i, i, i64, i, i,
                                                    i, i, f, p, sz, p]
     lib.pkv_paged_decode_attention_fp8.restype = ctypes.c_int
-    for name in ("pkv_kv_append_rope", "pkv_kv_append_fp8_block"):
+    for name, args in (("pkv_kv_append_rope", RopeAppendArgs), ("pkv_kv_append_fp8_block", RopeAppendArgs),
+                       ("pkv_paged_tree_attention", TreeArgs), ("pkv_kv_add_weights", TreeArgs),
+                       ("pkv_kv_compact", CompactArgs)):
         fn = getattr(lib, name)
-        fn.argtypes = [ctypes.POINTER(RopeAppendArgs), p]
+        fn.argtypes = [ctypes.POINTER(args), p]
         fn.restype = ctypes.c_int
-        packed = lib[name]                # of its own prototype, for _ROPE_APPEND's bytes
+        packed = lib[name]                # of its own prototype, for the struct module's bytes
         packed.argtypes, packed.restype = [ctypes.c_char_p, p], ctypes.c_int
         setattr(lib, name + "_packed", packed)
+    lib.pkv_tree_workspace_bytes.argtypes = [i, i, i, i, i]
+    lib.pkv_tree_workspace_bytes.restype = sz
+    lib.pkv_kv_select.argtypes = [p, p, p, i64, p, i, i, i, i, i, i, p]
+    lib.pkv_kv_select.restype = ctypes.c_int
     lib.pkv_decode_fp8_block_workspace_bytes.argtypes = [i, i, i, i, i]
     lib.pkv_decode_fp8_block_workspace_bytes.restype = sz
     lib.pkv_paged_decode_attention_fp8_block.argtypes = [p, p, p, p, p, p, p, p, i, i, i, i64, i, i,
@@ -565,6 +599,147 @@ def chunked_prefill_attention_fp8_block(out, q, k_cache, v_cache, k_scale, v_sca
     status = load().pkv_chunked_prefill_attention_fp8_block(
         op, qp, kp, vp, ksp, vsp, bp, blocks, prior_len, c, nb, hq, hkv, d, bs, scale,
         _stream_on(stream, index))
+    if status:
+        _check(fn, status)
+
+
+# ------------------------------------------------- drafted tokens and eviction
+def tree_workspace_bytes(num_q_heads: int, num_kv_heads: int, head_dim: int, max_draft: int,
+                         max_seq_len: int) -> int:
+    return int(load().pkv_tree_workspace_bytes(num_q_heads, num_kv_heads, head_dim, max_draft, max_seq_len))
+
+
+def tree_workspace(num_q_heads, num_kv_heads, head_dim, max_draft, max_seq_len, device="cuda"):
+    """Allocate (through torch) the workspace paged_tree_attention needs, for
+    any batch of these sizes or smaller ones."""
+    n = tree_workspace_bytes(num_q_heads, num_kv_heads, head_dim, max_draft, max_seq_len)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def _tree_call(fn, call, out, lse, q, k_cache, v_cache, block_table, seq_lens, draft_offsets, tree_mask, weights,
+               max_seq_len, max_draft, scale, workspace, index, stream):
+    shape = k_cache.shape
+    nb, hkv, bs, d = shape
+    if q.dim() != 3 or block_table.dim() != 2:
+        _refuse(fn, "q is not [rows, heads, head_dim] or block_table not [sequences, blocks]")
+    dtype = k_cache.dtype
+    n, hq, _ = q.shape
+    b, blocks = block_table.shape
+    kp = _whole(fn, "k_cache", k_cache, dtype, shape, index)
+    qp = _whole(fn, "q", q, dtype, (n, hq, d), index)
+    bp = _whole(fn, "block_table", block_table, torch.int32, (b, blocks), index)
+    lp = _whole(fn, "seq_lens", seq_lens, torch.int32, (b,), index)
+    dp = _whole(fn, "draft_offsets", draft_offsets, torch.int32, (b + 1,), index)
+    mp = ep = vp = op = wp = ws_bytes = wl = 0
+    if tree_mask is not None:
+        mp = _whole(fn, "tree_mask", tree_mask, torch.int64, (n,), index)
+    if lse is not None:
+        ep = _whole(fn, "lse", lse, torch.float32, (n, hq), index)
+    if weights is None:
+        vp = _whole(fn, "v_cache", v_cache, dtype, shape, index)
+        op = _whole(fn, "out", out, dtype, (n, hq, d), index)
+    else:
+        wl = weights.shape[2] if weights.dim() == 3 else -1
+        wt = _whole(fn, "weights", weights, torch.float32, (b, hkv, wl), index)
+    if workspace is not None:
+        ws_bytes = workspace.numel() * workspace.element_size()
+        wp = _whole(fn, "workspace", workspace, workspace.dtype, workspace.shape, index)
+    if _debug:
+        _validate(fn, "check_tree", block_table, seq_lens, draft_offsets, n, max_seq_len, max_draft, nb, bs)
+    a = _TREE.pack(op, ep, qp, kp, vp, bp, lp, dp, mp, 0 if weights is None else wt, wp, ws_bytes, wl, nb, b, n,
+                   blocks, max_seq_len, max_draft, hq, hkv, d, bs, _dtype_code(k_cache), scale)
+    status = call(a, _stream_on(stream, index))
+    if status:
+        _check(fn, status)
+
+
+def paged_tree_attention(out, q, k_cache, v_cache, block_table, seq_lens, draft_offsets, tree_mask,
+                         max_seq_len: int, max_draft: int, scale: float, workspace=None, lse=None,
+                         stream=None) -> None:
+    """Attention of drafted tokens: out, q [N, Hq, D] (bf16 or fp32, as the
+    pools [NB, Hkv, bs, D]); sequence b's are rows draft_offsets[b] ..
+    draft_offsets[b + 1] - 1 (int32 [B + 1]), at most max_draft <= MAX_DRAFT,
+    and the last of its seq_lens[b] stored tokens (int32 [B]); block_table
+    int32 [B, max_blocks].  Each sees the tokens before the drafted ones, and
+    drafted token j if bit j of its tree_mask entry is set (int64 [N]; None: a
+    chain, itself and the ones before).  lse fp32 [N, Hq] (optional) gets the
+    logarithm of each row's softmax sum.  workspace from ``tree_workspace``."""
+    fn = "pkv_paged_tree_attention"
+    _tree_call(fn, load().pkv_paged_tree_attention_packed, out, lse, q, k_cache, v_cache, block_table, seq_lens,
+               draft_offsets, tree_mask, None, max_seq_len, max_draft, scale, workspace,
+               _device_of(fn, k_cache), stream)
+
+
+def kv_add_weights(weights, q, k_cache, block_table, seq_lens, draft_offsets, tree_mask, lse, max_seq_len: int,
+                   max_draft: int, scale: float, stream=None) -> None:
+    """Adds to weights (fp32 [B, Hkv, M], M >= max_seq_len; start from zeros)
+    what the softmax of the rows of q gave each stored token, summed over the
+    rows and the query heads of each KV head.  The arguments are those of
+    ``paged_tree_attention``, with the lse it wrote."""
+    fn = "pkv_kv_add_weights"
+    if weights is None or lse is None:
+        _refuse(fn, "no weights or no lse")
+    _tree_call(fn, load().pkv_kv_add_weights_packed, None, lse, q, k_cache, None, block_table, seq_lens,
+               draft_offsets, tree_mask, weights, max_seq_len, max_draft, scale, None,
+               _device_of(fn, k_cache), stream)
+
+
+def kv_select(kept, kept_lens, weights, seq_lens, max_seq_len: int, sinks: int, recent: int, stream=None) -> None:
+    """Which tokens stay: kept int32 [B, Hkv, budget] gets the positions, in
+    ascending order, of each sequence's first ``sinks`` tokens, its last
+    ``recent`` ones, and of the rest those with the largest weights (fp32
+    [B, Hkv, M]); kept_lens int32 [B] gets min(seq_lens, budget)."""
+    fn = "pkv_kv_select"
+    index = _device_of(fn, weights)
+    if weights.dim() != 3 or kept.dim() != 3:
+        _refuse(fn, "weights is not [sequences, KV heads, tokens] or kept not [sequences, KV heads, budget]")
+    b, hkv, m = weights.shape
+    budget = kept.shape[2]
+    wp = _whole(fn, "weights", weights, torch.float32, (b, hkv, m), index)
+    kp = _whole(fn, "kept", kept, torch.int32, (b, hkv, budget), index)
+    np_ = _whole(fn, "kept_lens", kept_lens, torch.int32, (b,), index)
+    lp = _whole(fn, "seq_lens", seq_lens, torch.int32, (b,), index)
+    if _debug:
+        _validate(fn, "check_lengths", seq_lens, max_seq_len)
+    status = load().pkv_kv_select(kp, np_, wp, m, lp, b, hkv, max_seq_len, budget, sinks, recent,
+                                  _stream_on(stream, index))
+    if status:
+        _check(fn, status)
+
+
+def kv_compact(k_cache, v_cache, block_table, seq_lens, kept, kept_lens, first=None, weights=None,
+               stream=None) -> None:
+    """Rows that stay move up in place: position first[b] + i (first int32
+    [B]; None: 0) of the pools [NB, Hkv, bs, D] (bf16, fp32, or uint8 codes
+    with one scale per head) and of weights (fp32 [B, Hkv, M], optional)
+    becomes what position kept[b, h, i] was, i < kept_lens[b]; the weights
+    behind, up to seq_lens[b], become 0.  kept int32 [B, Hkv, n], or [B, 1, n]:
+    the same rows in every head; kept[b, h, i] >= first[b] + i."""
+    fn = "pkv_kv_compact"
+    index = _device_of(fn, k_cache)
+    shape, dtype = k_cache.shape, k_cache.dtype
+    if dtype not in (torch.bfloat16, torch.float32, torch.uint8):
+        raise TypeError(f"unsupported dtype {dtype}")
+    nb, hkv, bs, d = shape
+    if block_table.dim() != 2 or kept.dim() != 3:
+        _refuse(fn, "block_table is not [sequences, blocks] or kept not [sequences, heads, rows]")
+    b, blocks = block_table.shape
+    heads, n = kept.shape[1:]
+    kp = _whole(fn, "k_cache", k_cache, dtype, shape, index)
+    vp = _whole(fn, "v_cache", v_cache, dtype, shape, index)
+    bp = _whole(fn, "block_table", block_table, torch.int32, (b, blocks), index)
+    lp = _whole(fn, "seq_lens", seq_lens, torch.int32, (b,), index)
+    tp = _whole(fn, "kept", kept, torch.int32, (b, heads, n), index)
+    np_ = _whole(fn, "kept_lens", kept_lens, torch.int32, (b,), index)
+    fp = 0 if first is None else _whole(fn, "first", first, torch.int32, (b,), index)
+    wp = m = 0
+    if weights is not None:
+        m = weights.shape[2] if weights.dim() == 3 else -1
+        wp = _whole(fn, "weights", weights, torch.float32, (b, hkv, m), index)
+    if _debug:
+        _validate(fn, "check_compact", block_table, seq_lens, kept, kept_lens, first, m if wp else None, nb, bs)
+    a = _COMPACT.pack(kp, vp, wp, bp, lp, tp, np_, fp, m, nb, b, blocks, hkv, heads, n, d * k_cache.element_size(), bs)
+    status = load().pkv_kv_compact_packed(a, _stream_on(stream, index))
     if status:
         _check(fn, status)
 

@@ -848,6 +848,169 @@ pkv_status pkv_chunked_prefill_attention_fp8_block(
              : PKV_ECUDA;
 }
 
+}  // extern "C"
+
+namespace {
+
+bool misaligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
+
+// Rows of one piece of work of the tensor-core tree attention, and CTAs that
+// may leave partials (two pieces each).
+constexpr int kTreePieceRows = 256;
+constexpr int kTreeMaxCtas = 160;
+
+// Validates a call of drafted tokens and fills its launch arguments.  *todo
+// false: valid, and nothing to launch.
+pkv_status tree_prepare(const pkv_tree_args* x, bool attention, pkv::TreeArgs* out, int* sms, bool* todo) {
+  *todo = false;
+  if (!x) return PKV_EINVAL;
+  pkv_status st = check_heads(x->num_q_heads, x->num_kv_heads, x->head_dim, x->block_size, x->dtype);
+  if (st != PKV_OK) return st;
+  if (x->num_seqs < 0 || x->num_rows < 0 || x->max_blocks_per_seq < 1 || x->max_seq_len < 1 || x->num_blocks < 1 ||
+      x->max_draft < 1)
+    return PKV_EINVAL;
+  if (x->max_draft > PKV_MAX_DRAFT) return PKV_EUNSUPPORTED;
+  if (x->num_seqs == 0 || x->num_rows == 0) return PKV_OK;
+  if (x->num_seqs > PKV_MAX_SEQS) return PKV_ERANGE;
+  if ((int64_t)x->max_seq_len > (int64_t)x->max_blocks_per_seq * x->block_size) return PKV_EINVAL;
+  if (!isfinite(x->scale) || !(x->scale > 0.f)) return PKV_EINVAL;
+  if (!x->q || !x->k_cache || !x->block_table || !x->seq_lens || !x->draft_offsets) return PKV_EINVAL;
+  if (!aligned16(x->q) || !aligned16(x->k_cache) || misaligned(x->block_table, 4) || misaligned(x->seq_lens, 4) ||
+      misaligned(x->draft_offsets, 4) || misaligned(x->tree_mask, 8) || misaligned(x->lse, 4))
+    return PKV_EINVAL;
+  if (attention) {
+    if (!x->out || !x->v_cache || !aligned16(x->out) || !aligned16(x->v_cache)) return PKV_EINVAL;
+    const size_t need = pkv_tree_workspace_bytes(x->num_q_heads, x->num_kv_heads, x->head_dim, x->max_draft,
+                                                 x->max_seq_len);
+    if (x->workspace_bytes < need) return PKV_ERANGE;
+    if (need > 0 && (!x->workspace || misaligned(x->workspace, 256))) return PKV_EINVAL;
+  } else {
+    if (!x->weights || !x->lse || misaligned(x->weights, 4)) return PKV_EINVAL;
+    if (x->weights_len < x->max_seq_len) return PKV_EINVAL;
+  }
+  // tiles of all sequences, heads and rows are counted in an int
+  const int64_t tiles = (x->max_seq_len + 31) / 32;
+  const int64_t chunks = ((int64_t)x->max_draft * (x->num_q_heads / x->num_kv_heads) + 31) / 32;
+  if ((int64_t)x->num_seqs * x->num_kv_heads * (tiles * chunks + 8) >= (int64_t)INT_MAX) return PKV_ERANGE;
+  int* err = nullptr;
+  st = device_state(&err, sms);
+  if (st != PKV_OK) return st;
+  pkv::TreeArgs a{};
+  a.out = x->out;
+  a.lse = x->lse;
+  a.weights = x->weights;
+  a.weights_len = x->weights_len;
+  a.q = x->q;
+  a.k_cache = x->k_cache;
+  a.v_cache = x->v_cache;
+  a.block_table = x->block_table;
+  a.seq_lens = x->seq_lens;
+  a.draft_offsets = x->draft_offsets;
+  a.tree_mask = x->tree_mask;
+  a.num_seqs = x->num_seqs;
+  a.num_rows = x->num_rows;
+  a.max_blocks_per_seq = x->max_blocks_per_seq;
+  a.max_seq_len = x->max_seq_len;
+  a.max_draft = x->max_draft;
+  a.num_blocks = x->num_blocks;
+  a.num_q_heads = x->num_q_heads;
+  a.num_kv_heads = x->num_kv_heads;
+  a.head_dim = x->head_dim;
+  a.scale = x->scale;
+  a.workspace = x->workspace;
+  a.err = err;
+  *out = a;
+  *todo = true;
+  return PKV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t pkv_tree_workspace_bytes(int num_q_heads, int num_kv_heads, int head_dim, int max_draft, int max_seq_len) {
+  if (num_q_heads < 1 || num_kv_heads < 1 || num_q_heads % num_kv_heads != 0 || head_dim < 1 || max_draft < 1 ||
+      max_seq_len < 1)
+    return 0;
+  const int64_t rows = (int64_t)max_draft * (num_q_heads / num_kv_heads);
+  const size_t piece = (size_t)std::min<int64_t>(rows, kTreePieceRows) * (head_dim + 2) * sizeof(float);
+  return 2 * (size_t)kTreeMaxCtas * align256(piece);
+}
+
+pkv_status pkv_paged_tree_attention(const pkv_tree_args* x, pkv_stream_t stream) {
+  pkv::TreeArgs a;
+  int sms = 0;
+  bool todo = false;
+  const pkv_status st = tree_prepare(x, true, &a, &sms, &todo);
+  if (st != PKV_OK || !todo) return st;
+  const cudaError_t e =
+      pkv::launch_tree_attention_cc(a, x->dtype == PKV_BF16, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PKV_OK : PKV_ECUDA;
+}
+
+pkv_status pkv_kv_add_weights(const pkv_tree_args* x, pkv_stream_t stream) {
+  pkv::TreeArgs a;
+  int sms = 0;
+  bool todo = false;
+  const pkv_status st = tree_prepare(x, false, &a, &sms, &todo);
+  if (st != PKV_OK || !todo) return st;
+  const cudaError_t e =
+      pkv::launch_kv_add_weights_cc(a, x->dtype == PKV_BF16, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PKV_OK : PKV_ECUDA;
+}
+
+pkv_status pkv_kv_select(int32_t* kept, int32_t* kept_lens, const float* weights, int64_t weights_len,
+                         const int32_t* seq_lens, int num_seqs, int num_kv_heads, int max_seq_len, int budget,
+                         int sinks, int recent, pkv_stream_t stream) {
+  if (num_seqs < 0 || num_kv_heads < 1 || max_seq_len < 1 || budget < 1 || sinks < 0 || recent < 0)
+    return PKV_EINVAL;
+  if (sinks > budget || recent > budget - sinks || weights_len < max_seq_len) return PKV_EINVAL;
+  if (num_seqs == 0) return PKV_OK;
+  if (num_seqs > PKV_MAX_SEQS || (int64_t)num_seqs * num_kv_heads > INT_MAX / 16 ||
+      max_seq_len > INT_MAX - 65536)
+    return PKV_ERANGE;
+  if (!kept || !kept_lens || !weights || !seq_lens) return PKV_EINVAL;
+  if (misaligned(kept, 4) || misaligned(kept_lens, 4) || misaligned(weights, 4) || misaligned(seq_lens, 4))
+    return PKV_EINVAL;
+  int* err = nullptr;
+  int sms = 0;
+  const pkv_status st = device_state(&err, &sms);
+  if (st != PKV_OK) return st;
+  pkv::SelectArgs a{kept, kept_lens, weights, weights_len, seq_lens, num_seqs, num_kv_heads, max_seq_len,
+                    budget, sinks, recent, err};
+  return pkv::launch_kv_select(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? PKV_OK : PKV_ECUDA;
+}
+
+pkv_status pkv_kv_compact(const pkv_compact_args* x, pkv_stream_t stream) {
+  if (!x) return PKV_EINVAL;
+  if (x->num_seqs < 0 || x->max_blocks_per_seq < 1 || x->num_blocks < 1 || x->num_kv_heads < 1 ||
+      x->kept_len < 0 || x->row_bytes < 1 || x->block_size < 1)
+    return PKV_EINVAL;
+  if (x->kept_heads != 1 && x->kept_heads != x->num_kv_heads) return PKV_EINVAL;
+  if (x->block_size != pkv::kBlockSize || x->row_bytes % 16 != 0 || x->row_bytes > PKV_MAX_COMPACT_ROW_BYTES)
+    return PKV_EUNSUPPORTED;
+  if (x->num_seqs == 0) return PKV_OK;
+  if (x->num_seqs > PKV_MAX_SEQS || (int64_t)x->num_seqs * x->num_kv_heads > INT_MAX / 64 ||
+      (int64_t)x->max_blocks_per_seq * x->block_size > INT_MAX - 65536)
+    return PKV_ERANGE;
+  if (!x->k_cache || !x->v_cache || !x->block_table || !x->seq_lens || !x->kept_lens || (x->kept_len > 0 && !x->kept))
+    return PKV_EINVAL;
+  if (x->k_cache == x->v_cache || (x->weights && x->weights_len < 1)) return PKV_EINVAL;
+  if (!aligned16(x->k_cache) || !aligned16(x->v_cache) || misaligned(x->block_table, 4) ||
+      misaligned(x->seq_lens, 4) || misaligned(x->kept, 4) || misaligned(x->kept_lens, 4) ||
+      misaligned(x->first, 4) || misaligned(x->weights, 4))
+    return PKV_EINVAL;
+  int* err = nullptr;
+  int sms = 0;
+  const pkv_status st = device_state(&err, &sms);
+  if (st != PKV_OK) return st;
+  pkv::CompactArgs a{x->k_cache, x->v_cache, x->weights, x->weights_len, x->block_table, x->seq_lens,
+                     x->kept, x->kept_lens, x->first, x->num_seqs, x->max_blocks_per_seq, x->num_kv_heads,
+                     x->kept_heads, x->kept_len, x->row_bytes, x->num_blocks, err};
+  return pkv::launch_kv_compact(a, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? PKV_OK
+                                                                                              : PKV_ECUDA;
+}
+
 pkv_status pkv_decode_prefill_attention(const pkv_decode_prefill_args* x, pkv_stream_t stream) {
   if (!x) return PKV_EINVAL;
   // validate both halves before anything is launched

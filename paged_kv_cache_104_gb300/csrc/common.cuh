@@ -23,6 +23,8 @@ enum DevErr : int {
   DEVERR_SMEM_LAYOUT = 5,   // dynamic shared memory not 1 KiB aligned (kernel skipped)
   DEVERR_POSITION_RANGE = 6,  // a rotating append: position outside the table
   DEVERR_SLOT_ORDER = 7,    // block-scaled append: a block's new rows not in order
+  DEVERR_DRAFT_RANGE = 8,   // draft_offsets: a count outside its bounds
+  DEVERR_KEPT_RANGE = 9,    // kv_compact: a kept row or count outside its bounds
 };
 
 // Wait limits: 2^31 SM cycles (about 1 s at GB300 clocks), checked every 64

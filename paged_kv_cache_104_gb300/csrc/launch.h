@@ -228,4 +228,76 @@ cudaError_t launch_prefill_pair(const PrefillArgs& a, cudaStream_t stream, int p
 // The same over the block-scaled fp8 pools (k_bscale, v_bscale set).
 cudaError_t launch_prefill_fp8_block(const PrefillArgs& a, int num_sms, cudaStream_t stream);
 
+// Drafted tokens over the paged cache: sequence b's drafted tokens are rows
+// draft_offsets[b] .. draft_offsets[b + 1] - 1 of q, and the last tokens of
+// its seq_lens[b] stored ones.
+constexpr int kMaxDraft = 64;        // drafted tokens per sequence: the bits of a mask word
+struct TreeArgs {
+  void* out;                  // attention: [num_rows][Hq][D]
+  float* lse;                 // attention: written, or null; weights: read
+  float* weights;             // weights only: [B][Hkv][weights_len], added to
+  int64_t weights_len;
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;        // attention only
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* draft_offsets;   // [B + 1]
+  const int64_t* tree_mask;       // [num_rows], or null: a chain
+  int num_seqs;
+  int num_rows;
+  int max_blocks_per_seq;
+  int max_seq_len;
+  int max_draft;
+  int64_t num_blocks;
+  int num_q_heads;
+  int num_kv_heads;
+  int head_dim;
+  float scale;
+  void* workspace;
+  int* err;
+};
+// fp32, head_dim 16 or 128 (CUDA cores)
+cudaError_t launch_tree_attention_cc(const TreeArgs& a, bool is_bf16, cudaStream_t stream);
+cudaError_t launch_kv_add_weights_cc(const TreeArgs& a, bool is_bf16, cudaStream_t stream);
+
+// Selection of the tokens that stay, per (sequence, KV head).
+struct SelectArgs {
+  int32_t* kept;              // [B][Hkv][budget]
+  int32_t* kept_lens;         // [B]
+  const float* weights;       // [B][Hkv][weights_len]
+  int64_t weights_len;
+  const int32_t* seq_lens;
+  int num_seqs;
+  int num_kv_heads;
+  int max_seq_len;
+  int budget;
+  int sinks;
+  int recent;
+  int* err;
+};
+cudaError_t launch_kv_select(const SelectArgs& a, cudaStream_t stream);
+
+// Rows that stay moved up in place.
+struct CompactArgs {
+  void* k_cache;
+  void* v_cache;
+  float* weights;             // [B][Hkv][weights_len] or null
+  int64_t weights_len;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* kept;        // [B][kept_heads][kept_len]
+  const int32_t* kept_lens;   // [B]
+  const int32_t* first;       // [B] or null: 0
+  int num_seqs;
+  int max_blocks_per_seq;
+  int num_kv_heads;
+  int kept_heads;             // num_kv_heads, or 1: the same rows in every head
+  int kept_len;
+  int row_bytes;
+  int64_t num_blocks;
+  int* err;
+};
+cudaError_t launch_kv_compact(const CompactArgs& a, int num_sms, cudaStream_t stream);
+
 }  // namespace pkv

@@ -102,3 +102,58 @@ def check_prefill(block_table_row, prior_len: int, chunk_len: int, num_blocks: i
     if bad.numel():
         raise ValidationError(f"prefill block table holds block {int(bad[0])} outside "
                               f"[0, {num_blocks})")
+
+
+def check_lengths(seq_lens, max_seq_len: int) -> None:
+    """Every length in [0, max_seq_len]."""
+    for b, n in enumerate(_host(seq_lens).tolist()):
+        if n < 0 or n > max_seq_len:
+            raise ValidationError(f"seq_lens[{b}] = {n} outside [0, {max_seq_len}]")
+
+
+def check_tree(block_table, seq_lens, draft_offsets, num_rows: int, max_seq_len: int, max_draft: int,
+               num_blocks: int, block_size: int) -> None:
+    """Draft offsets not decreasing, inside the rows, at most max_draft apart;
+    where a sequence has drafted tokens, its length and block ids in range."""
+    off, lens = _host(draft_offsets).tolist(), _host(seq_lens).tolist()
+    bt = _host(block_table).to(torch.int64)
+    limit = min(int(max_seq_len), bt.shape[1] * block_size)
+    for b, n in enumerate(lens):
+        if off[b] < 0 or off[b + 1] < off[b] or off[b + 1] > num_rows or off[b + 1] - off[b] > max_draft:
+            raise ValidationError(f"draft_offsets[{b}:{b + 2}] = {off[b:b + 2]}: not rows 0 .. {num_rows}, at "
+                                  f"most {max_draft} of them")
+        drafted = off[b + 1] - off[b]
+        if not drafted:
+            continue
+        if n < drafted or n > limit:
+            raise ValidationError(f"seq_lens[{b}] = {n} outside [{drafted}, {limit}]")
+        used = bt[b, :(n + block_size - 1) // block_size]
+        bad = used[(used < 0) | (used >= num_blocks)]
+        if bad.numel():
+            raise ValidationError(f"block_table[{b}] holds block {int(bad[0])} outside [0, {num_blocks})")
+
+
+def check_compact(block_table, seq_lens, kept, kept_lens, first, weights_len, num_blocks: int,
+                  block_size: int) -> None:
+    """Counts and kept rows in their bounds, and the block ids that the rows
+    from first[b] on use (the rows before are not touched)."""
+    bt, rows = _host(block_table).to(torch.int64), _host(kept).to(torch.int64)
+    lens, counts = _host(seq_lens).tolist(), _host(kept_lens).tolist()
+    starts = [0] * len(lens) if first is None else _host(first).tolist()
+    limit = bt.shape[1] * block_size if weights_len is None else min(bt.shape[1] * block_size, weights_len)
+    for b, (n, m, at) in enumerate(zip(lens, counts, starts)):
+        if n < 0 or n > limit:
+            raise ValidationError(f"seq_lens[{b}] = {n} outside [0, {limit}]")
+        if m < 0 or m > rows.shape[2] or at < 0 or at + m > n:
+            raise ValidationError(f"first[{b}] = {at} and kept_lens[{b}] = {m}: not within {rows.shape[2]} rows of "
+                                  f"a sequence of {n}")
+        r = rows[b, :, :m]
+        bad = (r < at + torch.arange(m)) | (r >= n)
+        if bool(bad.any()):
+            h, i = (int(x) for x in bad.nonzero()[0])
+            raise ValidationError(f"kept[{b}][{h}][{i}] = {int(r[h, i])} outside [{at + i}, {n})")
+        if m:
+            used = bt[b, at // block_size:(int(r.max()) // block_size) + 1]
+            wrong = used[(used < 0) | (used >= num_blocks)]
+            if wrong.numel():
+                raise ValidationError(f"block_table[{b}] holds block {int(wrong[0])} outside [0, {num_blocks})")
