@@ -854,11 +854,6 @@ namespace {
 
 bool misaligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
 
-// Rows of one piece of work of the tensor-core tree attention, and CTAs that
-// may leave partials (two pieces each).
-constexpr int kTreePieceRows = 256;
-constexpr int kTreeMaxCtas = 160;
-
 // Validates a call of drafted tokens and fills its launch arguments.  *todo
 // false: valid, and nothing to launch.
 pkv_status tree_prepare(const pkv_tree_args* x, bool attention, pkv::TreeArgs* out, int* sms, bool* todo) {
@@ -880,8 +875,9 @@ pkv_status tree_prepare(const pkv_tree_args* x, bool attention, pkv::TreeArgs* o
     return PKV_EINVAL;
   if (attention) {
     if (!x->out || !x->v_cache || !aligned16(x->out) || !aligned16(x->v_cache)) return PKV_EINVAL;
-    const size_t need = pkv_tree_workspace_bytes(x->num_q_heads, x->num_kv_heads, x->head_dim, x->max_draft,
-                                                 x->max_seq_len);
+    const size_t need = x->dtype != PKV_BF16 ? 0   // the fp32 kernel joins its splits in shared memory
+                                             : pkv_tree_workspace_bytes(x->num_q_heads, x->num_kv_heads, x->head_dim,
+                                                                        x->max_draft, x->max_seq_len);
     if (x->workspace_bytes < need) return PKV_ERANGE;
     if (need > 0 && (!x->workspace || misaligned(x->workspace, 256))) return PKV_EINVAL;
   } else {
@@ -932,9 +928,8 @@ size_t pkv_tree_workspace_bytes(int num_q_heads, int num_kv_heads, int head_dim,
   if (num_q_heads < 1 || num_kv_heads < 1 || num_q_heads % num_kv_heads != 0 || head_dim < 1 || max_draft < 1 ||
       max_seq_len < 1)
     return 0;
-  const int64_t rows = (int64_t)max_draft * (num_q_heads / num_kv_heads);
-  const size_t piece = (size_t)std::min<int64_t>(rows, kTreePieceRows) * (head_dim + 2) * sizeof(float);
-  return 2 * (size_t)kTreeMaxCtas * align256(piece);
+  if (head_dim != 128) return 0;
+  return pkv::tree_workspace_bytes(num_q_heads / num_kv_heads, max_draft);
 }
 
 pkv_status pkv_paged_tree_attention(const pkv_tree_args* x, pkv_stream_t stream) {
@@ -943,8 +938,9 @@ pkv_status pkv_paged_tree_attention(const pkv_tree_args* x, pkv_stream_t stream)
   bool todo = false;
   const pkv_status st = tree_prepare(x, true, &a, &sms, &todo);
   if (st != PKV_OK || !todo) return st;
-  const cudaError_t e =
-      pkv::launch_tree_attention_cc(a, x->dtype == PKV_BF16, reinterpret_cast<cudaStream_t>(stream));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = x->dtype == PKV_BF16 ? pkv::launch_tree_attention_mma(a, sms, s)
+                                             : pkv::launch_tree_attention_cc(a, false, s);
   return e == cudaSuccess ? PKV_OK : PKV_ECUDA;
 }
 

@@ -31,7 +31,7 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-enum MapKind { kPoolBf16 = 0, kPoolU8 = 1, kRowsBf16 = 2, kPoolBlocksBf16 = 3, kRows32Bf16 = 4 };
+enum MapKind { kPoolBf16 = 0, kPoolU8 = 1, kRowsBf16 = 2, kPoolBlocksBf16 = 3, kRows32Bf16 = 4, kGroupRowsBf16 = 5 };
 using Key = std::tuple<int, const void*, int64_t, int>;
 
 std::mutex g_map_mu;
@@ -124,6 +124,20 @@ bool encode_rows32_map_bf16(CUtensorMap* map, const void* base, int64_t rows) {
     cuuint32_t box[2] = {64, 32};
     cuuint32_t estr[2] = {1, 1};
     return f(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  });
+}
+
+bool encode_group_rows_map_bf16(CUtensorMap* map, const void* base, int64_t n, int heads, int group) {
+  EncodeTiledFn f = encode_fn();
+  if (!f || n <= 0 || heads <= 0 || group <= 0 || 128 % group != 0) return false;
+  return cached(map, kGroupRowsBf16, base, n, heads * 256 + group, [&](CUtensorMap* m) {
+    cuuint64_t dims[3] = {128, (cuuint64_t)heads, (cuuint64_t)n};
+    cuuint64_t strides[2] = {128 * 2, (cuuint64_t)heads * 128 * 2};
+    cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)(128 / group)};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return f(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   });

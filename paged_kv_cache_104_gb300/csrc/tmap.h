@@ -32,4 +32,9 @@ bool encode_latent_block_map(CUtensorMap* map, const void* base, int64_t num_blo
 // columns, 128-byte swizzle.
 bool encode_rows32_map_bf16(CUtensorMap* map, const void* base, int64_t rows);
 
+// q [n][heads][128] bf16 with the heads of one KV head together: box = 64
+// columns x group heads x 128 / group tokens (128 rows, token first), 128-byte
+// swizzle; group divides 128.
+bool encode_group_rows_map_bf16(CUtensorMap* map, const void* base, int64_t n, int heads, int group);
+
 }  // namespace pkv

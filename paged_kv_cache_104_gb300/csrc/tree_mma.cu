@@ -1,0 +1,722 @@
+// Attention of drafted tokens over the paged bf16 cache, on tcgen05 (sm_103a).
+//
+// What it computes: for row (drafted token i, query head h of KV head g) of a
+// sequence, over the keys the row sees (the whole context, and the drafted
+// tokens of its mask), out = sum_n softmax(scale q . k_n) v_n and the logarithm
+// of the softmax sum.
+//
+// What bounds it: every stored key and value is read once for all rows of its
+// sequence, 512 B for 512 R multiply-adds (R rows of a KV head), so up to about
+// R = 256 rows (64 drafted tokens of a group of 4) HBM is the bound.
+//
+// Work.  A stream is one (sequence, KV head, 256 rows), cut into tiles of 128
+// keys; the tiles of the whole batch are shared out equally to one persistent
+// CTA per SM (tree_common.cuh).  A CTA's part of a stream is an item; a stream
+// that falls to several CTAs leaves fp32 partials (unnormalised O, max, sum),
+// at most two per CTA, that a second kernel joins.
+//
+// Two softmax warpgroups ("sides") work in turn on S and O accumulators of
+// their own, so the tensor core and the loads run on while one exponentiates:
+//   more than 128 rows: side s takes rows 128 s .. of every tile;
+//   up to 128 rows:     side s takes every other tile, and the two join at the
+//                       item's end through TMEM (thread r of either side can
+//                       read row r of both accumulators).
+// Either way the products alternate between the sides ("steps").
+//
+// Roles (384 threads):
+//   warps 0-3 / 4-7  softmax of side 0 / 1: thread r owns row r (TMEM lane r);
+//                    warps whose rows do not exist only pass barriers on
+//   warp 8           K/V producer: one 4 KiB TMA copy per cache block (K and V
+//                    tiles through one ring of five 32 KiB slots)
+//   warp 9           tcgen05 issuer: S = Q K^T from shared memory, O += P V with
+//                    P (bf16) in TMEM over its S.  P is rounded to bf16 as the
+//                    cache's values are; the sum l takes the unrounded ones.
+//   warp 10          checks the drafted tokens' values: a row of V that holds an
+//                    infinity or NaN would reach, as 0 x inf, rows that do not
+//                    see it.  Such rows are cleared in shared memory and added
+//                    by the softmax threads to the rows that see them; rows of
+//                    the last block past the sequence's end are cleared too.
+//   warp 11          works out the plan, hands the items to the others through
+//                    a ring of four, and loads their queries
+// Every mbarrier wait is bounded; on time-out the kernel records an error,
+// stops issuing work, lets its copies land, frees its TMEM and returns.
+#include <climits>
+
+#include <cuda.h>
+
+#include "common.cuh"
+#include "host_cache.h"
+#include "launch.h"
+#include "tc_common.cuh"
+#include "tmap.h"
+#include "tree_common.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int BM = 128, BN = kTreeTile, HD = 128;
+constexpr int QHALF = BM * 128;               // 64 columns of 128 query rows, 16 KiB
+constexpr int Q_BYTES = 2 * QHALF;
+constexpr int TILE = BN * HD * 2;             // a K or V tile, 32 KiB: [8 rows][half][8 x 128 B]
+constexpr int GROUP8 = 2048;                  // 8 rows of a tile
+constexpr int NS = 5;                         // ring slots
+constexpr int NI = 4;                         // items in flight
+constexpr int NCK = 4;                        // V tiles on their way to the checker
+constexpr int OFF_Q = 0;                      // two 32 KiB buffers
+constexpr int OFF_KV = 2 * Q_BYTES;
+constexpr int OFF_ML = OFF_KV + NS * TILE;    // [side][row] (max, sum) exchange
+constexpr int OFF_ITEM = OFF_ML + 2 * BM * 8;
+constexpr int OFF_BAD = OFF_ITEM + NI * 64;   // drafted tokens whose V was cleared, per item slot
+constexpr int OFF_BAR = OFF_BAD + NI * 8;
+constexpr int kSoft = 256, kThreadsT = 384;
+constexpr int W_KV = 8, W_MMA = 9, W_FIX = 10, W_PLAN = 11;
+constexpr int kRegsSoft = 200, kRegsRest = 96;
+static_assert(kRegsSoft * kSoft + kRegsRest * (kThreadsT - kSoft) <= ((65536 / kThreadsT) & ~7) * kThreadsT,
+              "the register split must fit in what the CTA was launched with");
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t COL_S = 0, COL_O = 2 * BN;  // per side: S (P over its first 64 columns), O
+constexpr float kLazy = 8.0f;                  // the maximum is raised when it grows by more than 2^8
+
+enum {
+  TB_QF = 0,               // [2] queries loaded
+  TB_QE = TB_QF + 2,       // [2] queries no longer read
+  TB_F = TB_QE + 2,        // [NS] tile loaded
+  TB_E = TB_F + NS,        // [NS] tile no longer read
+  TB_IF = TB_E + NS,       // [NI] item there
+  TB_IE = TB_IF + NI,      // [NI] item no longer read
+  TB_CK = TB_IE + NI,      // [NCK] V tile to be checked loaded (its TB_F follows the check)
+  TB_SF = TB_CK + NCK,     // [side] S complete
+  TB_PF = TB_SF + 2,       // [side][half] P written
+  TB_OD = TB_PF + 4,       // [side] O complete, where the sides have rows of their own
+  TB_OJ = TB_OD + 2,       // both O complete, where they share their rows
+  TB_ML,                   // both sides' (max, sum) written
+  TB_JD,                   // both sides' O read by both
+  TB_COUNT
+};
+constexpr int SMEM_BYTES = OFF_BAR + TB_COUNT * 8 + 16;
+static_assert(SMEM_BYTES <= 227 * 1024, "one CTA per SM");
+static_assert(sizeof(TreeItem) <= 64, "an item's slot");
+
+// What CTA c left of a stream that starts in it and goes on in others.
+struct MergeDesc {
+  int pieces;      // 0: nothing to join
+  int b, g, row0, rows, q_tok;
+  int pad[2];
+};
+
+struct TreeMmaParams {
+  TreeArgs a;
+  int q_bufs;                // 2: no stream has more than 128 rows
+  MergeDesc* desc;           // [CTA]
+  char* partials;            // [CTA][2] of piece_bytes: O [rows][128], then (max, sum) [rows]
+  int64_t piece_bytes;
+  int piece_rows;
+};
+
+// Ring positions of an item's tiles, in the order the products need them.
+struct Order {
+  bool both;   // both sides take every tile
+  int n;
+  __device__ int steps() const { return both ? 2 * n : n; }
+  __device__ int tile(int s) const { return both ? s >> 1 : s; }
+  __device__ int k(int j) const { return both ? 2 * j : (j == 0 ? 0 : 2 * j - 1); }
+  __device__ int v(int j) const { return both ? 2 * j + 1 : (j < n - 1 ? 2 * j + 2 : 2 * n - 1); }
+  __device__ int side_steps(int side) const { return both ? n : (n + 1 - side) >> 1; }
+};
+
+__global__ void __launch_bounds__(kThreadsT, 1)
+tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__ CUtensorMap tm_q,
+                const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const uint32_t sbase = smem_u32(smem);
+  const TreeArgs& a = p.a;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + TB_COUNT);
+  int* abort_i = reinterpret_cast<int*>(tmem_slot + 1);
+  volatile int* abort_flag = abort_i;
+  unsigned long long* bad_v = reinterpret_cast<unsigned long long*>(smem + OFF_BAD);
+  auto bar = [&](int i) { return smem_u32(bars + i); };
+  if (sbase & 1023u) {   // swizzled operand tiles need a 1 KiB-aligned base
+    if (threadIdx.x == 0) {
+      record_error(a.err, DEVERR_SMEM_LAYOUT);
+      p.desc[blockIdx.x].pieces = 0;
+    }
+    return;
+  }
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int group = a.num_q_heads / a.num_kv_heads;
+
+  if (tid == 0) {
+    for (int i = 0; i < TB_COUNT; ++i) {
+      int count = 1;
+      if (i >= TB_IE && i < TB_CK) count = 3 + kSoft / 32;   // issuer, producer, checker, softmax warps
+      if (i >= TB_PF && i < TB_OD) count = 4;
+      if (i >= TB_ML) count = kSoft / 32;
+      mbar_init(bar(i), count);
+    }
+    *abort_i = 0;
+    fence_mbar_init();
+  }
+  if (warp == W_MMA) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(kTmemCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // The k-th item, for a warp that consumes items (false: none, or aborted).
+  auto item_at = [&](int k, TreeItem& it) {
+    bool ok = wait_or_abort(bar(TB_IF + k % NI), (k / NI) & 1, abort_flag, a.err);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) return false;
+    it = *reinterpret_cast<const TreeItem*>(smem + OFF_ITEM + (k % NI) * 64);
+    return it.n > 0;
+  };
+  auto item_done = [&](int k) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(TB_IE + k % NI));
+  };
+  // a whole warp waits and agrees
+  auto warp_wait = [&](int b, uint32_t parity) {
+    return (bool)__all_sync(0xffffffffu, wait_fast(bar(b), parity, abort_flag, a.err));
+  };
+  auto order_of = [&](const TreeItem& it) { return Order{it.rows > BM, it.n}; };
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    if (warp == W_PLAN) {
+      // ---------------------------------------------------------------- plan and queries
+      TreePlan<true> plan(a);
+      MergeDesc d{};
+      int made = 0, loaded = 0;        // items handed out; queries asked for
+      bool last = false;
+      TreeItem it;
+      const long long t0 = clock64();
+      long long since = t0;
+      while (!last || loaded < made - 1) {
+        bool moved = false;
+        if (!last && (made < NI || __all_sync(0xffffffffu, mbar_try_wait(bar(TB_IE + made % NI), ((made / NI) - 1) & 1)))) {
+          it = plan.next();
+          last = it.n == 0;
+          if (it.pieces > 0) d = MergeDesc{it.pieces, it.b, it.g, it.row0, it.rows, it.q_tok, {0, 0}};
+          if (lane == 0) *reinterpret_cast<TreeItem*>(smem + OFF_ITEM + (made % NI) * 64) = it;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(TB_IF + made % NI));
+          ++made;
+          moved = true;
+        }
+        if (loaded < made - (last ? 1 : 0)) {
+          const int qb = loaded % p.q_bufs;
+          if (loaded < p.q_bufs ||
+              __all_sync(0xffffffffu, mbar_try_wait(bar(TB_QE + qb), ((loaded / p.q_bufs) - 1) & 1))) {
+            // an item's slot is written again only once its queries were used
+            const TreeItem x = *reinterpret_cast<const TreeItem*>(smem + OFF_ITEM + (loaded % NI) * 64);
+            if (lane == 0) {
+              const int sides = x.rows > BM ? 2 : 1;
+              mbar_arrive_expect_tx(bar(TB_QF + qb), sides * Q_BYTES);
+              for (int s = 0; s < sides; ++s)
+                for (int h = 0; h < 2; ++h)
+                  tma_load_3d(sbase + OFF_Q + (qb + s) * Q_BYTES + h * QHALF, &tm_q, bar(TB_QF + qb), 64 * h,
+                              x.g * group, x.q_tok + (x.row0 + s * BM) / group);
+            }
+            __syncwarp();
+            ++loaded;
+            moved = true;
+          }
+        }
+        const long long now = clock64();
+        if (moved) since = now;
+        if (*abort_flag || now - since > kWaitLimitCycles) {
+          if (!*abort_flag) record_error(a.err, DEVERR_TIMEOUT);
+          *abort_flag = 1;
+          break;
+        }
+      }
+      __syncwarp();
+      if (*abort_flag)   // let the queries' copies still in flight land
+        for (int k = max(0, loaded - p.q_bufs); k < loaded; ++k)
+          mbar_wait(bar(TB_QF + k % p.q_bufs), (k / p.q_bufs) & 1, nullptr);
+      if (lane == 0) p.desc[blockIdx.x] = d;
+    } else if (warp == W_KV) {
+      // ---------------------------------------------------------------- K/V producer
+      if (lane == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
+      }
+      int pos = 0, checks = 0;        // ring position; V tiles sent to the checker
+      uint32_t history = 0;           // which of the last positions went to the checker
+      TreeItem it;
+      bool ok = true;
+      for (int k = 0; ok && item_at(k, it); ++k) {
+        const int32_t* row = a.block_table + (int64_t)it.b * a.max_blocks_per_seq;
+        const int blocks = (it.len + kBlockSize - 1) / kBlockSize;
+        // block ids of four tiles, one per lane
+        auto ids_of = [&](int window) {
+          const int idx = window * 32 + lane;
+          int blk = 0;
+          if (idx < blocks && idx < (it.t0 + it.n) * 8) {
+            blk = __ldg(row + idx);
+            if (blk < 0 || (int64_t)blk >= a.num_blocks) {
+              record_error(a.err, DEVERR_BLOCK_RANGE);
+              blk = 0;
+            }
+          }
+          return blk;
+        };
+        int window = it.t0 >> 2;
+        int ids = ids_of(window), next_ids = ids_of(window + 1);
+        auto load = [&](bool is_v, int j) {
+          const int t = it.t0 + j, slot = pos % NS;
+          if (pos >= NS) ok = warp_wait(TB_E + slot, ((pos / NS) - 1) & 1);
+          if (!ok) return;
+          if (is_v && (t >> 2) > window) {   // V follows K: nobody needs the older window
+            ids = next_ids;
+            next_ids = ids_of(++window + 1);
+          }
+          const int mine = __shfl_sync(0xffffffffu, (t >> 2) > window ? next_ids : ids, (t & 3) * 8 + (lane & 7));
+          const int nb = min(8, blocks - 8 * t);
+          const bool check = is_v && (t + 1) * BN > it.ctx;
+          const uint32_t full = bar(check ? TB_CK + checks % NCK : TB_F + slot);
+          if (lane == 0) mbar_arrive_expect_tx(full, nb * 2 * GROUP8);
+          __syncwarp();
+          if (lane < nb)
+            tma_load_4d(sbase + OFF_KV + slot * TILE + lane * 2 * GROUP8, is_v ? &tm_v : &tm_k, full, 0, 0, 0,
+                        2 * (mine * a.num_kv_heads + it.g));
+          history = history << 1 | (check ? 1u : 0u);
+          checks += check;
+          ++pos;
+        };
+        const bool both = it.rows > BM;
+        load(false, 0);
+        if (!both && it.n > 1 && ok) load(false, 1);
+        for (int j = 0; j < it.n && ok; ++j) {
+          load(true, j);
+          const int kj = both ? j + 1 : j + 2;
+          if (kj < it.n && ok) load(false, kj);
+        }
+        item_done(k);
+      }
+      if (*abort_flag) {   // let the copies already issued land
+        for (int i = max(0, pos - NS); i < pos; ++i)
+          if (!(history >> (pos - 1 - i) & 1)) mbar_wait(bar(TB_F + i % NS), (i / NS) & 1, nullptr);
+        for (int i = max(0, checks - NCK); i < checks; ++i) mbar_wait(bar(TB_CK + i % NCK), (i / NCK) & 1, nullptr);
+      }
+    } else if (warp == W_MMA) {
+      // ---------------------------------------------------------------- issuer
+      constexpr uint32_t idesc_qk = make_idesc(false, BM, BN);
+      constexpr uint32_t idesc_pv = make_idesc(true, BM, HD);
+      int base = 0;
+      uint32_t count[2] = {0, 0};     // steps of each side so far
+      TreeItem it;
+      bool ok = true;
+      for (int k = 0; ok && item_at(k, it); ++k) {
+        const Order ord = order_of(it);
+        const int steps = ord.steps(), qb = k % p.q_bufs;
+        ok = warp_wait(TB_QF + qb, (k / p.q_bufs) & 1);
+        auto issue_qk = [&](int s) {
+          const int side = s & 1, at = base + ord.k(ord.tile(s));
+          ok = warp_wait(TB_F + at % NS, (at / NS) & 1);
+          if (!ok) return;
+          tc_fence_after();
+          const uint32_t kb = sbase + OFF_KV + (at % NS) * TILE;
+          const uint32_t qa = sbase + OFF_Q + (qb + (ord.both ? side : 0)) * Q_BYTES;
+#pragma unroll
+          for (int i = 0; i < HD / 16; ++i) {
+            const uint64_t ad = make_sw128_desc(qa + (i >> 2) * QHALF + (i & 3) * 32, 16, 1024);
+            const uint64_t bd = make_sw128_desc(kb + (i >> 2) * 1024 + (i & 3) * 32, 16, GROUP8);
+            mma_ss_e(tmem + COL_S + side * BN, ad, bd, idesc_qk, i > 0 ? 1u : 0u);
+          }
+          commit_e(bar(TB_SF + side));
+          if (!ord.both || side == 1) commit_e(bar(TB_E + at % NS));
+          if (s == steps - 1) commit_e(bar(TB_QE + qb));
+        };
+        if (ok) issue_qk(0);
+        if (ok && steps > 1) issue_qk(1);
+        for (int s = 0; s < steps && ok; ++s) {
+          const int side = s & 1, j = ord.tile(s), t = it.t0 + j, at = base + ord.v(j);
+          const int ks = (min(BN, it.len - t * BN) + 15) / 16;   // 16-key products of the tile
+          const uint32_t vb = sbase + OFF_KV + (at % NS) * TILE;
+          const bool first = s == side;                          // the side's first step of the item
+          if (!ord.both || side == 0) ok = warp_wait(TB_F + at % NS, (at / NS) & 1);
+          for (int half = 0; half < 2 && ok; ++half) {
+            ok = warp_wait(TB_PF + 2 * side + half, count[side] & 1);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int i = 4 * half; i < 4 * half + 4; ++i)
+              if (i < ks)
+                mma_ts_e(tmem + COL_O + side * HD, tmem + COL_S + side * BN + i * 8,
+                         make_sw128_desc(vb + i * 2 * GROUP8, 1024, GROUP8), idesc_pv, (!first || i > 0) ? 1u : 0u);
+          }
+          if (!ok) break;
+          if (!ord.both || side == 1) commit_e(bar(TB_E + at % NS));
+          if (ord.both && s + 2 >= steps) commit_e(bar(TB_OD + side));
+          if (!ord.both && s == steps - 1) commit_e(bar(TB_OJ));
+          ++count[side];
+          if (s + 2 < steps) issue_qk(s + 2);
+        }
+        base += 2 * it.n;
+        item_done(k);
+      }
+    } else if (warp == W_FIX) {
+      // ---------------------------------------------------------------- checker of the drafted tokens' values
+      int base = 0, checks = 0;
+      TreeItem it;
+      bool ok = true;
+      for (int k = 0; ok && item_at(k, it); ++k) {
+        const Order ord = order_of(it);
+        unsigned long long bad = 0;
+        for (int t = max(it.t0, it.ctx / BN); t < it.t0 + it.n; ++t) {
+          const int at = base + ord.v(t - it.t0);
+          // (a barrier of its own: this warp does not follow every turn of the ring)
+          ok = warp_wait(TB_CK + checks % NCK, (checks / NCK) & 1);
+          ++checks;
+          if (!ok) break;
+          unsigned char* tile = smem + OFF_KV + (at % NS) * TILE;
+          const int r0 = max(it.ctx - t * BN, 0), r1 = min(it.len - t * BN, BN);
+          // two rows at a time, 16 bytes per lane (chunk lane & 15: which half
+          // and where in it does not matter to a check or a clear)
+          auto chunk = [&](int r) {
+            return reinterpret_cast<uint4*>(tile + (r >> 3) * GROUP8 + ((lane >> 3) & 1) * 1024 + (r & 7) * 128 +
+                                            (lane & 7) * 16);
+          };
+          for (int r = r0; r < r1; r += 2) {
+            const int mine = r + (lane >> 4);
+            bool odd = false;
+            if (mine < r1) {
+              const uint4 x = *chunk(mine);
+              const uint32_t words[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i)   // all exponent bits of either half set
+                odd |= (words[i] & 0x7f80u) == 0x7f80u || (words[i] & 0x7f800000u) == 0x7f800000u;
+            }
+            const uint32_t votes = __ballot_sync(0xffffffffu, odd);
+            const bool clear = lane < 16 ? (votes & 0xffffu) != 0 : (votes >> 16) != 0;
+            if (clear && mine < r1) *chunk(mine) = make_uint4(0, 0, 0, 0);
+            const int d = t * BN + r - it.ctx;
+            if (votes & 0xffffu) bad |= 1ull << d;
+            if (votes >> 16) bad |= 2ull << d;
+          }
+          // rows of the last block behind the sequence
+          for (int r = r1 + (lane >> 4); r < ((r1 + 15) & ~15); r += 2) *chunk(r) = make_uint4(0, 0, 0, 0);
+          if (lane == 0) bad_v[k % NI] = bad;
+          fence_proxy_async_smem();       // the clears become visible to the tensor core
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(TB_F + at % NS));
+        }
+        base += 2 * it.n;
+        item_done(k);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+    // ---------------------------------------------------------------- softmax
+    const int side = warp >> 2, r = tid & 127;
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t col_s = COL_S + side * BN, col_o = COL_O + side * HD;
+    const float sl2 = a.scale * 1.4426950408889634f;
+    float2* ml = reinterpret_cast<float2*>(smem + OFF_ML);
+    uint32_t count = 0, own = 0, joints = 0;   // steps, items of the two kinds so far
+    TreeItem it;
+    for (int k = 0; item_at(k, it); ++k) {
+      const Order ord = order_of(it);
+      const int row = r + (ord.both ? side * BM : 0);      // of the stream
+      const bool live = row < it.rows;
+      const bool warp_live = (warp & 3) * 32 + (ord.both ? side * BM : 0) < it.rows;
+      uint64_t bits = 0;
+      if (live) {
+        TreeSeq s;
+        s.len = it.len;
+        s.drafted = it.len - it.ctx;
+        s.row0 = it.q_tok;
+        bits = tree_bits(a, s, (it.row0 + row) / group);
+      }
+      float m_run = -INFINITY, l_run = 0.f;                // maximum in scaled log2 units
+      const int steps = ord.side_steps(side);
+      for (int i = 0; i < steps; ++i, ++count) {
+        wait_fast(bar(TB_SF + side), count & 1, abort_flag, a.err);
+        __syncwarp();
+        tc_fence_after();
+        if (!warp_live) {                                  // rows that do not exist
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar(TB_PF + 2 * side));
+            mbar_arrive(bar(TB_PF + 2 * side + 1));
+          }
+          continue;
+        }
+        const int t = it.t0 + (ord.both ? i : 2 * i + side), k0 = t * BN;
+        float x[BN / 32][32];
+#pragma unroll
+        for (int c = 0; c < BN / 32; ++c) tmem_ld32(lane_base + col_s + c * 32, x[c]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < BN / 32; ++c) reg_fence(x[c]);
+        if (k0 + BN > it.ctx) {
+          // which of the tile's 128 keys this row sees: drafted token d is key ctx + d
+#pragma unroll
+          for (int c = 0; c < BN / 32; ++c) {
+            const int d = k0 + 32 * c - it.ctx;            // drafted token of the chunk's first key
+            uint32_t see;
+            if (d >= 64) see = 0;
+            else if (d >= 0) see = (uint32_t)(bits >> d);
+            else if (d > -32) see = (uint32_t)(bits << -d) | ((1u << -d) - 1);
+            else see = 0xffffffffu;
+#pragma unroll
+            for (int q = 0; q < 32; ++q)
+              if (!((see >> q) & 1)) x[c][q] = -INFINITY;
+          }
+        }
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < BN / 32; ++c)
+#pragma unroll
+          for (int q = 0; q < 32; q += 8) {
+            mx4[0] = fmax3(mx4[0], x[c][q], x[c][q + 4]);
+            mx4[1] = fmax3(mx4[1], x[c][q + 1], x[c][q + 5]);
+            mx4[2] = fmax3(mx4[2], x[c][q + 2], x[c][q + 6]);
+            mx4[3] = fmax3(mx4[3], x[c][q + 3], x[c][q + 7]);
+          }
+        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl2;
+        float m_new = m_run;
+        if (mx > m_run + kLazy || m_run == -INFINITY) m_new = mx;
+        const float base = m_new == -INFINITY ? 0.f : m_new;   // nothing seen so far: all weights 0
+        const float alpha = (m_new == m_run) ? 1.f : fast_exp2(m_run - base);
+        if (i >= 1 && __any_sync(0xffffffffu, alpha != 1.f)) {
+          // this step's S was issued behind the last product into O, so that
+          // product is complete and O can be rescaled in place
+          __syncwarp();
+#pragma unroll 1
+          for (int c = 0; c < HD / 32; ++c) {
+            float o[32];
+            tmem_ld32(lane_base + col_o + c * 32, o);
+            tmem_wait_ld();
+            reg_fence(o);
+#pragma unroll
+            for (int q = 0; q < 32; ++q) o[q] *= alpha;
+            tmem_st32(lane_base + col_o + c * 32, o);
+          }
+          tmem_wait_st();
+        }
+        float2 sum2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                          make_float2(0.f, 0.f)};
+        const float2 sl2x2 = make_float2(sl2, sl2), negm = make_float2(-base, -base);
+#pragma unroll
+        for (int c = 0; c < BN / 32; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int q = 0; q < 32; q += 2) {
+            const float2 y = ffma2(make_float2(x[c][q], x[c][q + 1]), sl2x2, negm);
+            const float2 pp = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+            sum2[(q >> 1) & 3] = fadd2(sum2[(q >> 1) & 3], pp);
+            pk[q / 2] = pack_bf16(pp.x, pp.y);
+          }
+          tmem_st16(lane_base + col_s + c * 16, pk);
+          if (c & 1) {                                     // a half of P is in TMEM
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(TB_PF + 2 * side + (c >> 1)));
+          }
+        }
+        const float2 s01 = fadd2(sum2[0], sum2[1]), s23 = fadd2(sum2[2], sum2[3]);
+        l_run = l_run * alpha + ((s01.x + s23.x) + (s01.y + s23.y));
+        m_run = m_new;
+      }
+      // ---- the item's result.  Where the sides shared the rows' keys, each
+      // thread joins both for half of its row's columns.
+      const bool joint = !ord.both, two = ord.side_steps(1) > 0;
+      wait_or_abort(bar(joint ? TB_OJ : TB_OD + side), (joint ? joints : own) & 1, abort_flag, a.err);
+      __syncwarp();
+      tc_fence_after();
+      float w0 = 1.f, w1 = 1.f, m = m_run, l = l_run;
+      if (joint) {
+        ml[side * BM + r] = make_float2(m_run, l_run);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(TB_ML));
+        wait_or_abort(bar(TB_ML), joints & 1, abort_flag, a.err);
+        __syncwarp();
+        const float2 s0 = ml[r], s1 = ml[BM + r];
+        m = fmaxf(s0.x, s1.x);
+        const float base = m == -INFINITY ? 0.f : m;
+        w0 = fast_exp2(s0.x - base);
+        w1 = fast_exp2(s1.x - base);
+        l = w0 * s0.y + w1 * s1.y;
+      }
+      if (warp_live) {
+        const bool none = l == 0.f;                        // the row sees none of these keys
+        const float base = m == -INFINITY ? 0.f : m;
+        const int col0 = joint ? side * 64 : 0, cols = joint ? 64 : HD;
+        const unsigned long long extra =
+            (it.t0 + it.n) * BN > it.ctx ? bad_v[k % NI] & bits : 0;   // values the products left out
+        const int64_t out_row = (int64_t)(it.q_tok + (it.row0 + row) / group) * a.num_q_heads + it.g * group +
+                                (it.row0 + row) % group;
+        char* piece = p.partials + ((int64_t)blockIdx.x * 2 + it.slot) * p.piece_bytes;
+        const float inv = 1.f / l;
+#pragma unroll 1
+        for (int c = col0; c < col0 + cols; c += 32) {
+          __syncwarp();                                    // the TMEM loads are the whole warp's
+          float o[32];
+          tmem_ld32(lane_base + (joint ? COL_O : col_o) + c, o);
+          if (joint && two) {
+            float o2[32];
+            tmem_ld32(lane_base + COL_O + HD + c, o2);
+            tmem_wait_ld();
+            reg_fence(o);
+            reg_fence(o2);
+#pragma unroll
+            for (int q = 0; q < 32; ++q) o[q] = w0 * o[q] + w1 * o2[q];
+          } else {
+            tmem_wait_ld();
+            reg_fence(o);   // side 0 alone: w0 = 1
+          }
+          if (!live) continue;
+          for (unsigned long long left = extra; left; left &= left - 1) {
+            const int d = __ffsll((long long)left) - 1, pos = it.ctx + d;
+            int blk = __ldg(a.block_table + (int64_t)it.b * a.max_blocks_per_seq + pos / kBlockSize);
+            if (blk < 0 || (int64_t)blk >= a.num_blocks) blk = 0;
+            const int64_t at = (((int64_t)blk * a.num_kv_heads + it.g) * kBlockSize + pos % kBlockSize) * HD;
+            const __nv_bfloat16* kr = static_cast<const __nv_bfloat16*>(a.k_cache) + at;
+            const __nv_bfloat16* vr = static_cast<const __nv_bfloat16*>(a.v_cache) + at;
+            const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(a.q) + out_row * HD;
+            float s = 0.f;
+            for (int i = 0; i < HD; ++i) s = fmaf(__bfloat162float(qr[i]), __bfloat162float(kr[i]), s);
+            const float pw = fast_exp2(fmaf(s, sl2, -base));
+            for (int q = 0; q < 32; ++q) o[q] = fmaf(pw, __bfloat162float(vr[c + q]), o[q]);
+          }
+          if (it.slot < 0) {
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + out_row * HD + c;
+            const float f = none ? 0.f : inv;
+#pragma unroll
+            for (int q = 0; q < 32; q += 8)
+              *reinterpret_cast<uint4*>(out + q) =
+                  none ? make_uint4(0, 0, 0, 0)
+                       : make_uint4(pack_bf16(o[q] * f, o[q + 1] * f), pack_bf16(o[q + 2] * f, o[q + 3] * f),
+                                    pack_bf16(o[q + 4] * f, o[q + 5] * f), pack_bf16(o[q + 6] * f, o[q + 7] * f));
+          } else {
+            float* out = reinterpret_cast<float*>(piece) + row * HD + c;
+#pragma unroll
+            for (int q = 0; q < 32; q += 4)
+              *reinterpret_cast<float4*>(out + q) = make_float4(o[q], o[q + 1], o[q + 2], o[q + 3]);
+          }
+        }
+        if (live && (!joint || side == 0)) {
+          if (it.slot >= 0)
+            reinterpret_cast<float2*>(piece + (int64_t)p.piece_rows * HD * 4)[row] = make_float2(m, l);
+          else if (a.lse)
+            a.lse[out_row] = none ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (joint) {   // on to the next item once nobody reads this one's accumulators
+        if (lane == 0) mbar_arrive(bar(TB_JD));
+        wait_or_abort(bar(TB_JD), joints & 1, abort_flag, a.err);
+        ++joints;
+      } else {
+        ++own;
+      }
+      item_done(k);
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (tid == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (warp == W_MMA) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+  }
+}
+
+// Joins the partials of the stream that starts in CTA blockIdx.x and goes on
+// in the next ones: a warp per row, four dims per lane,
+//   M = max m_i, out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
+__global__ void __launch_bounds__(256) tree_merge_kernel(const TreeMmaParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const TreeArgs& a = p.a;
+  const MergeDesc d = p.desc[blockIdx.x];
+  if (d.pieces == 0) return;
+  const int lane = threadIdx.x & 31, group = a.num_q_heads / a.num_kv_heads;
+  for (int row = blockIdx.y * 8 + (threadIdx.x >> 5); row < d.rows; row += gridDim.y * 8) {
+    // the stream's first piece is its CTA's second partial, the others the first of theirs
+    auto piece = [&](int i) { return p.partials + ((int64_t)(blockIdx.x + i) * 2 + (i == 0)) * p.piece_bytes; };
+    auto stat = [&](int i) { return reinterpret_cast<const float2*>(piece(i) + (int64_t)p.piece_rows * HD * 4)[row]; };
+    float m = -INFINITY;
+    for (int i = lane; i < d.pieces; i += 32) m = fmaxf(m, stat(i).x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float base = m == -INFINITY ? 0.f : m;
+    float l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = 0; i < d.pieces; ++i) {
+      const float2 s = stat(i);
+      const float4 o = reinterpret_cast<const float4*>(piece(i))[row * (HD / 4) + lane];
+      const float w = fast_exp2(s.x - base);
+      l = fmaf(w, s.y, l);
+      if (s.y != 0.f) {   // a piece of which the row sees nothing holds no O
+        acc.x = fmaf(w, o.x, acc.x);
+        acc.y = fmaf(w, o.y, acc.y);
+        acc.z = fmaf(w, o.z, acc.z);
+        acc.w = fmaf(w, o.w, acc.w);
+      }
+    }
+    const bool none = l == 0.f;
+    const float inv = 1.f / l;
+    const int64_t at =
+        (int64_t)(d.q_tok + (d.row0 + row) / group) * a.num_q_heads + d.g * group + (d.row0 + row) % group;
+    uint2* out = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at * HD) + lane;
+    *out = none ? make_uint2(0, 0)
+                : make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+    if (a.lse && lane == 0) a.lse[at] = none ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+  }
+}
+
+}  // namespace
+
+size_t tree_workspace_bytes(int group, int max_draft) {
+  const int64_t rows = (int64_t)max_draft * group;
+  const size_t piece = ((rows < kTreeRows ? rows : kTreeRows) * (HD + 2) * 4 + 255) & ~(size_t)255;
+  return 2 * (size_t)kTreeMaxCtas * piece + kTreeMaxCtas * sizeof(MergeDesc);
+}
+
+cudaError_t launch_tree_attention_mma(const TreeArgs& a, int num_sms, cudaStream_t stream) {
+  const int group = a.num_q_heads / a.num_kv_heads;
+  const int64_t rows = (int64_t)a.max_draft * group;
+  TreeMmaParams p;
+  p.a = a;
+  p.q_bufs = rows <= BM ? 2 : 1;
+  p.piece_rows = (int)(rows < kTreeRows ? rows : kTreeRows);
+  p.piece_bytes = ((int64_t)p.piece_rows * (HD + 2) * 4 + 255) & ~255ll;
+  p.desc = static_cast<MergeDesc*>(a.workspace);
+  p.partials = static_cast<char*>(a.workspace) + kTreeMaxCtas * sizeof(MergeDesc);
+  CUtensorMap tm_q, tm_k, tm_v;
+  const int64_t tiles = a.num_blocks * a.num_kv_heads;
+  if (!encode_group_rows_map_bf16(&tm_q, a.q, a.num_rows, a.num_q_heads, group) ||
+      !encode_latent_block_map(&tm_k, a.k_cache, tiles) || !encode_latent_block_map(&tm_v, a.v_cache, tiles))
+    return cudaErrorInvalidValue;
+  cudaError_t e = allow_dynamic_smem(tree_mma_kernel, SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  const int64_t row_tiles = (rows + kTreeRows - 1) / kTreeRows;
+  const int64_t stages = (int64_t)a.num_seqs * a.num_kv_heads * row_tiles * ((a.max_seq_len + BN - 1) / BN);
+  int grid = num_sms < kTreeMaxCtas ? num_sms : kTreeMaxCtas;
+  if (stages < grid) grid = (int)stages;
+  tree_mma_kernel<<<grid, kThreadsT, SMEM_BYTES, stream>>>(p, tm_q, tm_k, tm_v);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || a.max_seq_len <= BN) return e;   // one tile a stream: no partials
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, (p.piece_rows + 7) / 8);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_merge_kernel, p);
+}
+
+}  // namespace pkv

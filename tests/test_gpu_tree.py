@@ -1,5 +1,6 @@
 """paged_tree_attention against the fp64 oracle."""
 import math
+import random
 
 import pytest
 import torch
@@ -88,6 +89,26 @@ def test_ragged_batch_with_empty_sequences():
     x2 = Batch(lens, drafted, 8, 2, seed=6, spare_rows=5)
     out, _ = run(x)
     assert torch.equal(out, run(x2)[0])
+
+
+@pytest.mark.parametrize("hq,most", [(32, 16), (64, 64), (8, 64), (128, 5)])
+def test_many_items_per_cta(hq, most):
+    """More key tiles than SMs, sequences beyond the first 32: every CTA walks
+    several streams, whole and cut, of few rows and of many."""
+    pick = random.Random(hq)
+    lens = [pick.choice([pick.randint(64, 300), pick.randint(64, 1500)]) for _ in range(45)]
+    drafted = [pick.choice([0, 1, pick.randint(1, most), most]) for _ in lens]
+    x = Batch(lens, drafted, hq, 8, seed=hq, mask="random" if hq == 8 else "tree")
+    out = run(x)
+    check(x, *out)
+    again = run(x)
+    assert torch.equal(out[0], again[0]) and torch.equal(out[1], again[1])
+
+
+@pytest.mark.parametrize("hq,drafted", [(8, 3), (32, 20), (64, 64)])
+def test_long_sequences(hq, drafted):
+    x = Batch([20011, 5000], [drafted, 1], hq, 8, seed=hq)
+    check(x, *run(x))
 
 
 @pytest.mark.parametrize("dim,hq,hkv", [(16, 4, 2), (128, 8, 1), (128, 2, 2), (16, 8, 1)])
