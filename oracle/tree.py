@@ -24,8 +24,9 @@ def sees(mask_words, drafted: int, n: int, i: int):
     return s
 
 
-def _per_row(q, k_cache, table, seq_lens, offsets, mask, scale):
-    """For every sequence, KV head and row: (b, g, query heads, row of q, scores [G, n], seen [n])."""
+def _per_head(q, k_cache, table, seq_lens, offsets, mask, scale):
+    """For every sequence with drafted tokens and KV head: (b, h, rows of q,
+    query heads, scores [m, G, n], seen [m, 1, n])."""
     hkv = k_cache.shape[1]
     g = q.shape[1] // hkv
     for b in range(len(seq_lens)):
@@ -33,43 +34,41 @@ def _per_row(q, k_cache, table, seq_lens, offsets, mask, scale):
         if hi == lo:
             continue
         words = None if mask is None else mask[lo:hi]
+        seen = torch.tensor(np.stack([sees(words, hi - lo, n, i) for i in range(hi - lo)]))[:, None]
         for h in range(hkv):
-            k = rows_of(k_cache, table, b, h, n)
             heads = slice(h * g, (h + 1) * g)
-            for i in range(hi - lo):
-                yield b, h, heads, lo + i, q[lo + i, heads].double() @ k.T * scale, sees(words, hi - lo, n, i)
+            s = q[lo:hi, heads].double() @ rows_of(k_cache, table, b, h, n).T * scale
+            yield b, h, slice(lo, hi), heads, s, seen
 
 
 def tree_attention(q, k_cache, v_cache, table, seq_lens, offsets, mask, scale):
-    """out [N, Hq, D] and lse [N, Hq] in fp64; rows of no sequence are NaN."""
+    """out [N, Hq, D] and lse [N, Hq] in fp64; rows of no sequence are NaN.
+    The value of a key that a row does not see is not touched: 0 x inf never
+    arises."""
     out = torch.full(q.shape, float("nan"), dtype=torch.float64)
     lse = torch.full(q.shape[:2], float("nan"), dtype=torch.float64)
-    values = {}
-    for b, h, heads, row, s, seen in _per_row(q, k_cache, table, seq_lens, offsets, mask, scale):
-        if (b, h) not in values:
-            values = {(b, h): rows_of(v_cache, table, b, h, int(seq_lens[b]))}
-        at = np.flatnonzero(seen)
-        if not len(at):
-            out[row, heads], lse[row, heads] = 0, -float("inf")
-            continue
-        s = s[:, at]
-        top = s.amax(1, keepdim=True)
-        p = torch.exp(s - top)
-        total = p.sum(1, keepdim=True)
-        out[row, heads] = (p / total) @ values[b, h][at]
-        lse[row, heads] = (top + torch.log(total))[:, 0]
+    for b, h, rows, heads, s, seen in _per_head(q, k_cache, table, seq_lens, offsets, mask, scale):
+        s = torch.where(seen, s, -float("inf"))
+        top = s.amax(2, keepdim=True)
+        p = torch.exp(s - torch.where(torch.isinf(top) & (top < 0), 0.0, top))
+        total = p.sum(2, keepdim=True)
+        v = rows_of(v_cache, table, b, h, s.shape[2])
+        odd = ~torch.isfinite(v).all(1)                       # values that need the care
+        acc = p[:, :, ~odd] @ v[~odd]
+        for n in odd.nonzero()[:, 0].tolist():
+            acc = acc + torch.where(seen[:, :, n:n + 1], p[:, :, n:n + 1] * v[n], 0.0)
+        out[rows, heads] = torch.where(total == 0, 0.0, acc / total)
+        lse[rows, heads] = torch.where(total == 0, -float("inf"), top + torch.log(total))[..., 0]
     return out, lse
 
 
 def add_weights(weights, q, k_cache, table, seq_lens, offsets, mask, lse, scale):
     """weights (fp64, a copy) with the softmax weights of the rows added."""
     w = weights.double().clone()
-    for b, h, heads, row, s, seen in _per_row(q, k_cache, table, seq_lens, offsets, mask, scale):
-        at = np.flatnonzero(seen)
-        for j in range(s.shape[0]):
-            given = float(lse[row, heads][j])
-            if given != -float("inf"):
-                w[b, h, at] += torch.exp(s[j, at] - given)
+    for b, h, rows, heads, s, seen in _per_head(q, k_cache, table, seq_lens, offsets, mask, scale):
+        given = lse[rows, heads].double()[..., None]
+        p = torch.where(seen & (given != -float("inf")), torch.exp(s - given), 0.0)
+        w[b, h, :s.shape[2]] += p.sum((0, 1))
     return w
 
 

@@ -20,7 +20,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpagedkv.so")
 SOURCES = ["abi.cu", "append.cu", "append_rope.cu", "decode.cu", "decode_fp8.cu", "decode_fp8_block.cu", "decode_mla.cu", "decode_mma.cu",
            "gemm_heads.cu", "decode_noalloc.cu", "host_cache.cu", "kv_compact.cu", "kv_select.cu", "l2_flush.cu", "prefill_fp8_block.cu",
-           "prefill_pair.cu", "prefix_cache.cpp", "tmap.cu", "tree_cc.cu", "tree_mma.cu"]
+           "prefill_pair.cu", "prefix_cache.cpp", "tmap.cu", "tree_cc.cu", "tree_mma.cu",
+           "weights_mma.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

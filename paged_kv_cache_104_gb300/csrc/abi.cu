@@ -950,8 +950,9 @@ pkv_status pkv_kv_add_weights(const pkv_tree_args* x, pkv_stream_t stream) {
   bool todo = false;
   const pkv_status st = tree_prepare(x, false, &a, &sms, &todo);
   if (st != PKV_OK || !todo) return st;
-  const cudaError_t e =
-      pkv::launch_kv_add_weights_cc(a, x->dtype == PKV_BF16, reinterpret_cast<cudaStream_t>(stream));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = x->dtype == PKV_BF16 ? pkv::launch_kv_add_weights_mma(a, sms, s)
+                                             : pkv::launch_kv_add_weights_cc(a, false, s);
   return e == cudaSuccess ? PKV_OK : PKV_ECUDA;
 }
 

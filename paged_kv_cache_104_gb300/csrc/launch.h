@@ -262,6 +262,7 @@ cudaError_t launch_tree_attention_cc(const TreeArgs& a, bool is_bf16, cudaStream
 // bf16, head_dim 128 (tcgen05); workspace of tree_workspace_bytes
 size_t tree_workspace_bytes(int group, int max_draft);
 cudaError_t launch_tree_attention_mma(const TreeArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_kv_add_weights_mma(const TreeArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_kv_add_weights_cc(const TreeArgs& a, bool is_bf16, cudaStream_t stream);
 
 // Selection of the tokens that stay, per (sequence, KV head).

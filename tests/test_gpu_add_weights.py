@@ -1,5 +1,6 @@
 """kv_add_weights against the fp64 oracle."""
 import math
+import random
 
 import pytest
 import torch
@@ -66,6 +67,28 @@ def test_lengths(n, drafted):
 @pytest.mark.parametrize("hq", [1, 4, 8, 16])
 def test_drafted(drafted, hq):
     x = Batch([190 + drafted], [drafted], hq, 1, seed=drafted, mask="tree")
+    lse, w = given_lse(x), start(x)
+    check(x, w, run(x, w, lse), lse)
+
+
+@pytest.mark.parametrize("hq,most", [(32, 16), (64, 64), (8, 64), (128, 40)])
+def test_many_items_per_cta(hq, most):
+    """More key tiles than SMs, sequences beyond the first 32, up to 640 rows
+    of a KV head: every CTA walks several streams, some of them twice."""
+    pick = random.Random(hq)
+    lens = [pick.choice([pick.randint(64, 300), pick.randint(64, 1300)]) for _ in range(40)]
+    drafted = [pick.choice([0, 1, 1, pick.randint(1, most)]) for _ in lens]
+    drafted[7] = drafted[39] = most
+    x = Batch(lens, drafted, hq, 8, seed=hq, mask="random" if hq == 8 else "tree")
+    lse, w = given_lse(x), start(x)
+    after = run(x, w, lse)
+    check(x, w, after, lse)
+    assert torch.equal(after, run(x, w, lse))
+
+
+@pytest.mark.parametrize("hq,drafted", [(8, 1), (64, 20)])
+def test_long_sequences(hq, drafted):
+    x = Batch([20011, 5000], [drafted, 1], hq, 8, seed=hq)
     lse, w = given_lse(x), start(x)
     check(x, w, run(x, w, lse), lse)
 
