@@ -182,6 +182,53 @@ __device__ __forceinline__ void commit_e(uint32_t bar) {
       : "memory");
 }
 
+// D = A B^T over 128 dims in eight kind::f16 products of 16, both operands in
+// shared memory, one elected lane in one block (an election and descriptors
+// formed for every product made the issuer the bound: twice the tensor core's
+// time for a tile).  A step adds 32 bytes to the operands' addresses (2 in a
+// descriptor's 16-byte units); dims 64.. lie a_far and b_far such units on.
+__device__ __forceinline__ void mma_ss8_e(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint64_t a_far, uint64_t b_far) {
+  asm volatile(
+      "{\n\t.reg .pred e, t, f;\n\t.reg .b64 a, b, fa, fb;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\tsetp.eq.u32 t, 0, 0;\n\tsetp.ne.u32 f, 0, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n\t"
+      "add.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.s64 a, %1, 4;\n\tadd.s64 b, %2, 4;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.s64 a, %1, 6;\n\tadd.s64 b, %2, 6;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.s64 fa, %1, %4;\n\tadd.s64 fb, %2, %5;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], fa, fb, %3, t;\n\t"
+      "add.s64 a, fa, 2;\n\tadd.s64 b, fb, 2;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.s64 a, fa, 4;\n\tadd.s64 b, fb, 4;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.s64 a, fa, 6;\n\tadd.s64 b, fb, 6;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "l"(a_far), "l"(b_far)
+      : "memory");
+}
+// D (+)= A B in the first n (0 .. 4) of four kind::f16 products of 16, A from
+// TMEM (8 columns a product), B b_step 16-byte units on each time.
+__device__ __forceinline__ void mma_ts4_e(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                          uint64_t b_step, uint32_t accumulate, int n) {
+  asm volatile(
+      "{\n\t.reg .pred e, t, f, q;\n\t.reg .b32 a;\n\t.reg .b64 b;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\tsetp.eq.u32 t, 0, 0;\n\tsetp.ne.u32 f, %5, 0;\n\t"
+      "setp.gt.and.s32 q, %6, 0, e;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, f;\n\t"
+      "add.u32 a, %1, 8;\n\tadd.s64 b, %2, %4;\n\tsetp.gt.and.s32 q, %6, 1, e;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "add.u32 a, %1, 16;\n\tadd.s64 b, b, %4;\n\tsetp.gt.and.s32 q, %6, 2, e;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "add.u32 a, %1, 24;\n\tadd.s64 b, b, %4;\n\tsetp.gt.and.s32 q, %6, 3, e;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "l"(b_step), "r"(accumulate), "r"(n)
+      : "memory");
+}
+
 // three-input maximum (one instruction on sm_100 and later)
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
   float r;

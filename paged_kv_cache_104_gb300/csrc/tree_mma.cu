@@ -313,6 +313,11 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
       TreeItem it;
       bool ok = true;
       for (int k = 0; ok && item_at(k, it); ++k) {
+        // the same in every lane, and known to be: descriptors stay in uniform registers
+        it.n = __shfl_sync(0xffffffffu, it.n, 0);
+        it.t0 = __shfl_sync(0xffffffffu, it.t0, 0);
+        it.rows = __shfl_sync(0xffffffffu, it.rows, 0);
+        it.len = __shfl_sync(0xffffffffu, it.len, 0);
         const Order ord = order_of(it);
         const int steps = ord.steps(), qb = k % p.q_bufs;
         ok = warp_wait(TB_QF + qb, (k / p.q_bufs) & 1);
@@ -323,12 +328,8 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
           tc_fence_after();
           const uint32_t kb = sbase + OFF_KV + (at % NS) * TILE;
           const uint32_t qa = sbase + OFF_Q + (qb + (ord.both ? side : 0)) * Q_BYTES;
-#pragma unroll
-          for (int i = 0; i < HD / 16; ++i) {
-            const uint64_t ad = make_sw128_desc(qa + (i >> 2) * QHALF + (i & 3) * 32, 16, 1024);
-            const uint64_t bd = make_sw128_desc(kb + (i >> 2) * 1024 + (i & 3) * 32, 16, GROUP8);
-            mma_ss_e(tmem + COL_S + side * BN, ad, bd, idesc_qk, i > 0 ? 1u : 0u);
-          }
+          mma_ss8_e(tmem + COL_S + side * BN, make_sw128_desc(qa, 16, 1024), make_sw128_desc(kb, 16, GROUP8), idesc_qk,
+                    QHALF >> 4, 1024 >> 4);
           commit_e(bar(TB_SF + side));
           if (!ord.both || side == 1) commit_e(bar(TB_E + at % NS));
           if (s == steps - 1) commit_e(bar(TB_QE + qb));
@@ -345,11 +346,9 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
             ok = warp_wait(TB_PF + 2 * side + half, count[side] & 1);
             if (!ok) break;
             tc_fence_after();
-#pragma unroll
-            for (int i = 4 * half; i < 4 * half + 4; ++i)
-              if (i < ks)
-                mma_ts_e(tmem + COL_O + side * HD, tmem + COL_S + side * BN + i * 8,
-                         make_sw128_desc(vb + i * 2 * GROUP8, 1024, GROUP8), idesc_pv, (!first || i > 0) ? 1u : 0u);
+            mma_ts4_e(tmem + COL_O + side * HD, tmem + COL_S + side * BN + half * 32,
+                      make_sw128_desc(vb + half * 8 * GROUP8, 1024, GROUP8), idesc_pv, 2 * GROUP8 >> 4,
+                      (!first || half) ? 1u : 0u, ks - 4 * half);
           }
           if (!ok) break;
           if (!ord.both || side == 1) commit_e(bar(TB_E + at % NS));

@@ -252,6 +252,8 @@ weights_mma_kernel(const __grid_constant__ WeightParams p, const __grid_constant
     TreeItem it;
     bool ok = true;
     for (int k = 0; ok && pass_at(k, it); ++k) {
+      it.n = __shfl_sync(0xffffffffu, it.n, 0);         // known to be the same in every lane
+      it.rows = __shfl_sync(0xffffffffu, it.rows, 0);
       const int qb = k % p.q_bufs;
       const uint32_t idesc = make_idesc(false, BK, (it.rows + 15) & ~15);
       ok = warp_wait(WB_QF + qb, (k / p.q_bufs) & 1);
@@ -262,12 +264,8 @@ weights_mma_kernel(const __grid_constant__ WeightParams p, const __grid_constant
         if (!ok) break;
         tc_fence_after();
         const uint32_t kb = sbase + OFF_K + slot * TILE, qa = sbase + OFF_Q + qb * Q_BYTES;
-#pragma unroll
-        for (int i = 0; i < HD / 16; ++i) {
-          const uint64_t ad = make_sw128_desc(kb + (i >> 2) * 1024 + (i & 3) * 32, 16, GROUP8);
-          const uint64_t bd = make_sw128_desc(qa + (i >> 2) * q_half + (i & 3) * 32, 16, 1024);
-          mma_ss_e(tmem + side * kTreeRows, ad, bd, idesc, i > 0 ? 1u : 0u);
-        }
+        mma_ss8_e(tmem + side * kTreeRows, make_sw128_desc(kb, 16, GROUP8), make_sw128_desc(qa, 16, 1024), idesc,
+                  1024 >> 4, q_half >> 4);
         commit_e(bar(WB_SF + side));
         commit_e(bar(WB_E + slot));
         ++uses[side];
