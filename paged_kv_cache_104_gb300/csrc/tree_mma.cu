@@ -113,13 +113,12 @@ struct TreeMmaParams {
   int piece_rows;
 };
 
-// Ring positions of an item's tiles, in the order the products need them.
+// The order of an item's tiles in the ring, as the products need them: with
+// `both` K0 V0 K1 V1 .., else K0 K1 V0 K2 V1 K3 .. (side s's Q K^T of its next
+// tile is issued behind its P V of this one).
 struct Order {
   bool both;   // both sides take every tile
   int n;
-  __device__ int steps() const { return both ? 2 * n : n; }
-  __device__ int tile(int s) const { return both ? s >> 1 : s; }
-  __device__ int k(int j) const { return both ? 2 * j : (j == 0 ? 0 : 2 * j - 1); }
   __device__ int v(int j) const { return both ? 2 * j + 1 : (j < n - 1 ? 2 * j + 2 : 2 * n - 1); }
   __device__ int side_steps(int side) const { return both ? n : (n + 1 - side) >> 1; }
 };
@@ -308,56 +307,100 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
       // ---------------------------------------------------------------- issuer
       constexpr uint32_t idesc_qk = make_idesc(false, BM, BN);
       constexpr uint32_t idesc_pv = make_idesc(true, BM, HD);
-      int base = 0;
-      uint32_t count[2] = {0, 0};     // steps of each side so far
+      // What this warp does between two products can leave the tensor core
+      // idle: descriptors are formed once, ring positions counted up, and only
+      // S (per step) and O (per item) are committed; the softmax threads free
+      // the ring's slots, which those commits tell them are read.
+      const uint64_t k_desc = make_sw128_desc(sbase + OFF_KV, 16, GROUP8);
+      const uint64_t v_desc = make_sw128_desc(sbase + OFF_KV, 1024, GROUP8);
+      const uint64_t q_desc = make_sw128_desc(sbase + OFF_Q, 16, 1024);
+      int slot = 0;                   // ring position: slot and parity
+      uint32_t par = 0, p_par[2] = {0, 0};
       TreeItem it;
       bool ok = true;
-      for (int k = 0; ok && item_at(k, it); ++k) {
-        // the same in every lane, and known to be: descriptors stay in uniform registers
-        it.n = __shfl_sync(0xffffffffu, it.n, 0);
-        it.t0 = __shfl_sync(0xffffffffu, it.t0, 0);
-        it.rows = __shfl_sync(0xffffffffu, it.rows, 0);
-        it.len = __shfl_sync(0xffffffffu, it.len, 0);
-        const Order ord = order_of(it);
-        const int steps = ord.steps(), qb = k % p.q_bufs;
-        ok = warp_wait(TB_QF + qb, (k / p.q_bufs) & 1);
-        auto issue_qk = [&](int s) {
-          const int side = s & 1, at = base + ord.k(ord.tile(s));
-          ok = warp_wait(TB_F + at % NS, (at / NS) & 1);
+      auto tile_there = [&](int sl, uint32_t pr) {
+        ok = ok && warp_wait(TB_F + sl, pr);
+        tc_fence_after();
+      };
+      auto step = [&] {
+        if (++slot == NS) {
+          slot = 0;
+          par ^= 1;
+        }
+      };
+      auto qk = [&](int side, uint64_t q, int sl) {
+        if (!ok) return;
+        mma_ss8_e(tmem + COL_S + side * BN, q, k_desc + (uint32_t)(sl * (TILE >> 4)), idesc_qk, QHALF >> 4, 1024 >> 4);
+        commit_e(bar(TB_SF + side));
+      };
+      auto pv = [&](int side, int sl, bool first, int ks) {
+        for (int half = 0; half < 2; ++half) {
+          ok = ok && warp_wait(TB_PF + 2 * side + half, p_par[side]);
           if (!ok) return;
           tc_fence_after();
-          const uint32_t kb = sbase + OFF_KV + (at % NS) * TILE;
-          const uint32_t qa = sbase + OFF_Q + (qb + (ord.both ? side : 0)) * Q_BYTES;
-          mma_ss8_e(tmem + COL_S + side * BN, make_sw128_desc(qa, 16, 1024), make_sw128_desc(kb, 16, GROUP8), idesc_qk,
-                    QHALF >> 4, 1024 >> 4);
-          commit_e(bar(TB_SF + side));
-          if (!ord.both || side == 1) commit_e(bar(TB_E + at % NS));
-          if (s == steps - 1) commit_e(bar(TB_QE + qb));
-        };
-        if (ok) issue_qk(0);
-        if (ok && steps > 1) issue_qk(1);
-        for (int s = 0; s < steps && ok; ++s) {
-          const int side = s & 1, j = ord.tile(s), t = it.t0 + j, at = base + ord.v(j);
-          const int ks = (min(BN, it.len - t * BN) + 15) / 16;   // 16-key products of the tile
-          const uint32_t vb = sbase + OFF_KV + (at % NS) * TILE;
-          const bool first = s == side;                          // the side's first step of the item
-          if (!ord.both || side == 0) ok = warp_wait(TB_F + at % NS, (at / NS) & 1);
-          for (int half = 0; half < 2 && ok; ++half) {
-            ok = warp_wait(TB_PF + 2 * side + half, count[side] & 1);
-            if (!ok) break;
-            tc_fence_after();
-            mma_ts4_e(tmem + COL_O + side * HD, tmem + COL_S + side * BN + half * 32,
-                      make_sw128_desc(vb + half * 8 * GROUP8, 1024, GROUP8), idesc_pv, 2 * GROUP8 >> 4,
-                      (!first || half) ? 1u : 0u, ks - 4 * half);
-          }
-          if (!ok) break;
-          if (!ord.both || side == 1) commit_e(bar(TB_E + at % NS));
-          if (ord.both && s + 2 >= steps) commit_e(bar(TB_OD + side));
-          if (!ord.both && s == steps - 1) commit_e(bar(TB_OJ));
-          ++count[side];
-          if (s + 2 < steps) issue_qk(s + 2);
+          mma_ts4_e(tmem + COL_O + side * HD, tmem + COL_S + side * BN + half * 32,
+                    v_desc + (uint32_t)(sl * (TILE >> 4) + half * (8 * GROUP8 >> 4)), idesc_pv, 2 * GROUP8 >> 4,
+                    (!first || half) ? 1u : 0u, ks - 4 * half);
         }
-        base += 2 * it.n;
+        p_par[side] ^= 1;
+      };
+      for (int k = 0; ok && item_at(k, it); ++k) {
+        // the same in every lane, and known to be: descriptors stay in uniform registers
+        const int n = __shfl_sync(0xffffffffu, it.n, 0);
+        const bool both = __shfl_sync(0xffffffffu, it.rows, 0) > BM;
+        // 16-key products of the item's last tile; 8 in the others
+        const int last_ks = __shfl_sync(0xffffffffu, (min(BN, it.len - (it.t0 + it.n - 1) * BN) + 15) / 16, 0);
+        const int qb = k % p.q_bufs;
+        ok = warp_wait(TB_QF + qb, (k / p.q_bufs) & 1);
+        const uint64_t q0 = q_desc + (uint32_t)(qb * (Q_BYTES >> 4)), q1 = q0 + (both ? Q_BYTES >> 4 : 0);
+        tile_there(slot, par);
+        qk(0, q0, slot);
+        if (both) {
+          qk(1, q1, slot);
+          step();
+          for (int j = 0; j < n && ok; ++j) {
+            const bool more = j + 1 < n;
+            const int vs = slot, ks = more ? 8 : last_ks;
+            const uint32_t vp = par;
+            step();
+            if (j == n - 1 && ok) commit_e(bar(TB_QE + qb));   // every Q K^T of the item is behind this
+            tile_there(vs, vp);
+            pv(0, vs, j == 0, ks);
+            if (more) {
+              tile_there(slot, par);
+              qk(0, q0, slot);
+            } else if (ok) {
+              commit_e(bar(TB_OD));
+            }
+            pv(1, vs, j == 0, ks);
+            if (more) {
+              qk(1, q1, slot);
+              step();
+            } else if (ok) {
+              commit_e(bar(TB_OD + 1));
+            }
+          }
+        } else {
+          step();
+          if (n > 1) {
+            tile_there(slot, par);
+            qk(1, q1, slot);
+            step();
+          }
+          for (int s = 0; s < n && ok; ++s) {
+            const int side = s & 1;
+            if (s + 2 == max(n, 2) && ok) commit_e(bar(TB_QE + qb));
+            tile_there(slot, par);
+            pv(side, slot, s < 2, s == n - 1 ? last_ks : 8);
+            step();
+            if (s + 2 < n) {
+              tile_there(slot, par);
+              qk(side, q0, slot);
+              step();
+            }
+          }
+          if (ok) commit_e(bar(TB_OJ));
+        }
         item_done(k);
       }
     } else if (warp == W_FIX) {
@@ -419,6 +462,9 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
     const float sl2 = a.scale * 1.4426950408889634f;
     float2* ml = reinterpret_cast<float2*>(smem + OFF_ML);
     uint32_t count = 0, own = 0, joints = 0;   // steps, items of the two kinds so far
+    int base_slot = 0;                         // ring slot of the item's first tile
+    const bool leader = (tid & 127) == 0;
+    auto release = [&](int at) { mbar_arrive(bar(TB_E + at % NS)); };
     TreeItem it;
     for (int k = 0; item_at(k, it); ++k) {
       const Order ord = order_of(it);
@@ -437,6 +483,20 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
       const int steps = ord.side_steps(side);
       for (int i = 0; i < steps; ++i, ++count) {
         wait_fast(bar(TB_SF + side), count & 1, abort_flag, a.err);
+        // S complete: the step's K tile is read, and so is the V tile of the
+        // side's step before, whose product was issued ahead of it (where the
+        // sides share the tiles, side 1 is the later one)
+        if (leader && ord.both && side == 1) {
+          if (i > 0) release(base_slot + 2 * i - 1);
+          release(base_slot + 2 * i);
+        } else if (leader && !ord.both) {
+          if (i > 0) {
+            release(base_slot + 4 * i + 2 * side - 2);
+            release(base_slot + 4 * i + 2 * side - 1);
+          } else {
+            release(base_slot + side);
+          }
+        }
         __syncwarp();
         tc_fence_after();
         if (!warp_live) {                                  // rows that do not exist
@@ -529,6 +589,11 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
       // thread joins both for half of its row's columns.
       const bool joint = !ord.both, two = ord.side_steps(1) > 0;
       wait_or_abort(bar(joint ? TB_OJ : TB_OD + side), (joint ? joints : own) & 1, abort_flag, a.err);
+      if (leader && side == (joint ? 0 : 1)) {             // the item's last V tiles are read
+        if (joint && it.n > 1) release(base_slot + 2 * it.n - 2);
+        release(base_slot + 2 * it.n - 1);
+      }
+      base_slot = (base_slot + 2 * it.n) % NS;
       __syncwarp();
       tc_fence_after();
       float w0 = 1.f, w1 = 1.f, m = m_run, l = l_run;

@@ -247,8 +247,10 @@ weights_mma_kernel(const __grid_constant__ WeightParams p, const __grid_constant
       for (int i = max(0, pos - NS); i < pos; ++i) mbar_wait(bar(WB_F + i % NS), (i / NS) & 1, nullptr);
   } else if (warp == W_MMA) {
     // ------------------------------------------------------------------ issuer
-    int pos = 0;
-    uint32_t uses[2] = {0, 0};
+    const uint64_t k_desc = make_sw128_desc(sbase + OFF_K, 16, GROUP8);
+    const uint64_t q_desc = make_sw128_desc(sbase + OFF_Q, 16, 1024);
+    int slot = 0;                    // ring position: slot and parity
+    uint32_t par = 0, uses[2] = {0, 0};
     TreeItem it;
     bool ok = true;
     for (int k = 0; ok && pass_at(k, it); ++k) {
@@ -257,18 +259,20 @@ weights_mma_kernel(const __grid_constant__ WeightParams p, const __grid_constant
       const int qb = k % p.q_bufs;
       const uint32_t idesc = make_idesc(false, BK, (it.rows + 15) & ~15);
       ok = warp_wait(WB_QF + qb, (k / p.q_bufs) & 1);
-      for (int j = 0; j < it.n && ok; ++j, ++pos) {
-        const int side = j & 1, slot = pos % NS;
+      const uint64_t q = q_desc + (uint32_t)(qb * (Q_BYTES >> 4));
+      for (int j = 0; j < it.n && ok; ++j) {
+        const int side = j & 1;
         if (uses[side] > 0) ok = warp_wait(WB_SE + side, (uses[side] - 1) & 1);
-        if (ok) ok = warp_wait(WB_F + slot, (pos / NS) & 1);
+        if (ok) ok = warp_wait(WB_F + slot, par);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t kb = sbase + OFF_K + slot * TILE, qa = sbase + OFF_Q + qb * Q_BYTES;
-        mma_ss8_e(tmem + side * kTreeRows, make_sw128_desc(kb, 16, GROUP8), make_sw128_desc(qa, 16, 1024), idesc,
-                  1024 >> 4, q_half >> 4);
-        commit_e(bar(WB_SF + side));
-        commit_e(bar(WB_E + slot));
+        mma_ss8_e(tmem + side * kTreeRows, k_desc + (uint32_t)(slot * (TILE >> 4)), q, idesc, 1024 >> 4, q_half >> 4);
+        commit_e(bar(WB_SF + side));   // the summing warps free the tile's slot
         ++uses[side];
+        if (++slot == NS) {
+          slot = 0;
+          par ^= 1;
+        }
       }
       if (ok) commit_e(bar(WB_QE + qb));
       pass_done(k);
@@ -279,6 +283,7 @@ weights_mma_kernel(const __grid_constant__ WeightParams p, const __grid_constant
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + side * kTreeRows;
     const float sl2 = a.scale * 1.4426950408889634f;
     uint32_t count = 0;
+    int base = 0;                    // ring slot of the pass's first tile
     TreeItem it;
     for (int k = 0; pass_at(k, it); ++k) {
       const int qb = k % p.q_bufs;
@@ -294,6 +299,7 @@ weights_mma_kernel(const __grid_constant__ WeightParams p, const __grid_constant
         // does some row not see some key of this warp?
         const bool masked = __any_sync(0xffffffffu, d >= 0);
         wait_fast(bar(WB_SF + side), count & 1, abort_flag, a.err);
+        if (r == 0) mbar_arrive(bar(WB_E + (base + j) % NS));
         __syncwarp();
         tc_fence_after();
         float2 sum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -333,6 +339,7 @@ weights_mma_kernel(const __grid_constant__ WeightParams p, const __grid_constant
         const float2 s01 = fadd2(sum[0], sum[1]), s23 = fadd2(sum[2], sum[3]);
         if (there) line[key] = old + ((s01.x + s23.x) + (s01.y + s23.y));
       }
+      base = (base + it.n) % NS;
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(WB_QE + qb));
       pass_done(k);
