@@ -85,6 +85,16 @@ def test_accepted_paths(weights):
     check(lens, [16, 20, 3, 0, 0], first, hkv=4, heads=4, weights=weights)
 
 
+@pytest.mark.parametrize("dtype,dim,most", [(torch.bfloat16, 128, 16), (torch.bfloat16, 128, 17), (torch.uint8, 128, 32),
+                                            (torch.uint8, 16, 32), (torch.float32, 256, 4), (torch.uint8, 80, 5),
+                                            (torch.uint8, 128, 33)])
+def test_few_rows(dtype, dim, most):
+    """Around the bounds of the kernel for a few rows, heads together and apart."""
+    lens, counts = [90, most, 0, 33, 47], [most, most, 0, 1, most // 2]
+    check(lens, counts, [90 - 2 * most if most < 40 else 0, 0, 0, 31, 3], hkv=3, heads=1, dim=dim, dtype=dtype)
+    check(lens, counts, None, hkv=3, dim=dim, dtype=dtype)
+
+
 def test_many_sequences():
     pick = random.Random(3)
     lens = [pick.randrange(0, 400) for _ in range(150)]
