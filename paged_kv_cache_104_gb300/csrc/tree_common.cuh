@@ -13,12 +13,18 @@ struct TreeSeq {
   int row0;     // first row of q
 };
 
-// Sequence b's lengths; what is out of range is recorded (report) and skipped.
-__device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b, bool report) {
+// Sequence b's lengths as they are given (drafted: q's rows end there).
+__device__ __forceinline__ TreeSeq tree_seq_fetch(const TreeArgs& a, int b) {
   TreeSeq s;
   s.row0 = __ldg(a.draft_offsets + b);
-  const int end = __ldg(a.draft_offsets + b + 1);
+  s.drafted = __ldg(a.draft_offsets + b + 1);
   s.len = __ldg(a.seq_lens + b);
+  return s;
+}
+
+// ... with their checks: what is out of range is recorded (report) and skipped.
+__device__ __forceinline__ TreeSeq tree_seq_check(const TreeArgs& a, TreeSeq s, bool report) {
+  const int end = s.drafted;
   const bool rows_ok = s.row0 >= 0 && end >= s.row0 && end <= a.num_rows && end - s.row0 <= a.max_draft;
   s.drafted = rows_ok ? end - s.row0 : 0;
   if (!rows_ok) {
@@ -32,6 +38,9 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b, bool repor
     }
   }
   return s;
+}
+__device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b, bool report) {
+  return tree_seq_check(a, tree_seq_fetch(a, b), report);
 }
 
 // The drafted tokens that drafted token i of the sequence sees, as bits: its
@@ -47,17 +56,25 @@ __device__ __forceinline__ uint64_t tree_bits(const TreeArgs& a, const TreeSeq& 
 // ---- the balanced plan of the tensor-core kernels
 //
 // A stream is one (sequence, KV head), or with row tiles one (sequence, KV
-// head, 256 rows); a stage is one of its 128-key tiles.  The stages of the
-// batch, in order, are cut into one equal share per CTA; what a CTA gets of a
-// stream is an item.  One warp of every CTA works the plan out from the
-// lengths, 32 sequences at a time, so no shared memory grows with the batch.
-constexpr int kTreeTile = 128;      // keys of a stage
+// head, 256 rows), cut into tiles of 128 keys.  The tiles of the batch, in
+// order, are shared out to one persistent CTA per SM, and what a CTA gets of a
+// stream is an item.  Where a CTA gets many tiles, shares are of equal weight:
+// a tile of more than 128 rows takes 1.4 times one of fewer (3,500 cycles
+// against 2,500 of the attention), so 3 against 2 units, and a tile belongs
+// to the CTA in whose units it starts; a stream's last tile is followed by 2
+// units for its start and end.  (Equal numbers of tiles: 231 us for 32 ragged
+// sequences of 1 to 64 drafted tokens, against TREE_RAGGED.)  Where a CTA gets a
+// few tiles, every tile counts alike.  One warp of every CTA works the
+// plan out from the lengths, 32 sequences at a time, so no shared memory grows
+// with the batch.
+constexpr int kTreeTile = 128;      // keys of a tile
 constexpr int kTreeRows = 256;      // rows of a stream
 constexpr int kTreeMaxCtas = 160;
+constexpr int kTreeManyTiles = 8;   // a CTA, from where on tiles are weighted
 
 struct TreeItem {
-  int n;          // stages; 0: no more items
-  int t0;         // first key tile
+  int n;          // tiles; 0: no more items
+  int t0;         // first tile
   int b, g;
   int row0;       // first row (drafted token * group + query head) of the stream
   int rows;       // rows of the stream, 1 .. 256 (without row tiles: of the sequence)
@@ -72,81 +89,137 @@ struct TreePlan {
   const TreeArgs& a;
   const int lane, group;
   int windows, w = -1;                 // windows of 32 sequences, the loaded one
-  int total = 0, ctas = 0;             // stages; CTAs that share them
-  int pos = 0, end = 0;                // this CTA's next stage and end
-  int start = 0, sum = 0;              // the window's first stage, its stages
+  bool weighted = false;
+  int total = 0, ctas = 0;             // units; CTAs that share them
+  int pos = 0, end = 0;                // this CTA's next unit and end
+  int start = 0, sum = 0;              // the window's first unit, its units
   TreeSeq seq;                         // lane: its sequence
-  int tiles = 0, stages = 0, first = 0;
+  int tiles = 0, units = 0, first = 0;
 
-  __device__ TreePlan(const TreeArgs& args)
+  // Units of a tile of so many rows.
+  __device__ int weight(int rows, bool heavy) const {
+    if (!heavy || rows == 0) return rows > 0;
+    return (rows > 128 ? 3 : 2) * (ROW_TILES ? 1 : (rows + kTreeRows - 1) / kTreeRows);
+  }
+  // Units of a stream of nt tiles, and of all the streams of a KV head.
+  __device__ int stream_units(int nt, int rows, bool heavy) const {
+    return rows > 0 ? nt * weight(rows, heavy) + (heavy ? 2 : 0) : 0;
+  }
+  __device__ int head_units(int nt, int rows, bool heavy) const {
+    if (!ROW_TILES) return stream_units(nt, rows, heavy);
+    return rows / kTreeRows * stream_units(nt, kTreeRows, heavy) + stream_units(nt, rows % kTreeRows, heavy);
+  }
+  // x * y / z without the 64-bit division, which takes hundreds of cycles,
+  // where the product is small (it is for any realistic batch)
+  static __device__ int ratio(int x, int y, int z, int plus) {
+    const uint64_t num = (uint64_t)x * (uint32_t)y + plus;
+    return num >> 32 ? (int)(num / (uint32_t)z) : (int)((uint32_t)num / (uint32_t)z);
+  }
+
+  // For one warp (active), while the others still set the CTA up.
+  __device__ TreePlan(const TreeArgs& args, bool active)
       : a(args), lane(threadIdx.x & 31), group(args.num_q_heads / args.num_kv_heads),
         windows((args.num_seqs + 31) / 32) {
+    if (!active) return;
     const bool report = blockIdx.x == 0;
-    int mine = 0;
-    for (int i = 0; i < windows; ++i) {
-      load(i, report);
-      mine += stages;
+    int plain = 0, heavy = 0;
+    // four windows' lengths are asked for before the first is looked at, the
+    // first window last, as the walk often starts there
+    for (int i = (windows - 1) / 4; i >= 0; --i) {
+      TreeSeq s[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[j] = fetch(4 * i + j);
+#pragma unroll
+      for (int j = 3; j >= 0; --j) {
+        const int b = 32 * (4 * i + j) + lane;
+        seq = tree_seq_check(a, s[j], report && b < a.num_seqs);
+        tiles = seq.drafted > 0 ? (seq.len + kTreeTile - 1) / kTreeTile : 0;
+        plain += head_units(tiles, seq.drafted * group, false);
+        heavy += head_units(tiles, seq.drafted * group, true);
+      }
     }
-    total = __reduce_add_sync(0xffffffffu, mine);
+    w = 0;
+    total = __reduce_add_sync(0xffffffffu, plain * a.num_kv_heads);
+    if (total >= kTreeManyTiles * (int)gridDim.x) {
+      weighted = true;
+      total = __reduce_add_sync(0xffffffffu, heavy * a.num_kv_heads);
+    }
     ctas = min((int)gridDim.x, total);
     if ((int)blockIdx.x >= ctas) return;
-    pos = (int)((int64_t)blockIdx.x * total / ctas);
-    end = (int)((int64_t)(blockIdx.x + 1) * total / ctas);
+    pos = ratio(blockIdx.x, total, ctas, 0);
+    end = ratio(blockIdx.x + 1, total, ctas, 0);
     open(0);
   }
-  __device__ void load(int i, bool report = false) {
-    if (w == i) return;
-    w = i;
+  __device__ TreeSeq fetch(int i) const {
     const int b = 32 * i + lane;
-    seq.len = seq.drafted = seq.row0 = 0;
-    if (b < a.num_seqs) seq = tree_seq(a, b, report);
-    tiles = seq.drafted > 0 ? (seq.len + kTreeTile - 1) / kTreeTile : 0;
-    const int parts = ROW_TILES ? (seq.drafted * group + kTreeRows - 1) / kTreeRows : 1;
-    stages = tiles * parts * a.num_kv_heads;
+    TreeSeq s;
+    s.len = s.drafted = s.row0 = 0;
+    if (b < a.num_seqs) s = tree_seq_fetch(a, b);
+    return s;
   }
-  // window i, whose first stage is `start`
+  // window i, whose first unit is `start`
   __device__ void open(int i) {
-    load(i);
-    int x = stages;
+    if (w != i) {
+      w = i;
+      seq = tree_seq_check(a, fetch(i), false);
+      tiles = seq.drafted > 0 ? (seq.len + kTreeTile - 1) / kTreeTile : 0;
+    }
+    units = head_units(tiles, seq.drafted * group, weighted) * a.num_kv_heads;
+    int x = units;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
-    first = start + x - stages;
+    first = start + x - units;
     sum = __shfl_sync(0xffffffffu, x, 31);
   }
-  __device__ int cta_of(int stage) const { return (int)(((int64_t)(stage + 1) * ctas - 1) / total); }
+  __device__ int cta_of(int unit) const { return ratio(unit + 1, ctas, total, -1); }
   // The CTA's next item (n = 0: none).  Every lane gets it.
   __device__ TreeItem next() {
     TreeItem it;
     it.n = it.slot = it.pieces = 0;
-    if (pos >= end) return it;
-    while (pos >= start + sum) {
-      start += sum;
-      open(w + 1);
+    while (pos < end) {
+      while (pos >= start + sum) {
+        start += sum;
+        open(w + 1);
+      }
+      const int l = __ffs(__ballot_sync(0xffffffffu, first <= pos && pos < first + units)) - 1;
+      const int at = __shfl_sync(0xffffffffu, first, l), nt = __shfl_sync(0xffffffffu, tiles, l);
+      const int drafted = __shfl_sync(0xffffffffu, seq.drafted, l), rows = drafted * group;
+      const int per_head = head_units(nt, rows, weighted);
+      it.g = (pos - at) / per_head;
+      int s0 = at + it.g * per_head;                       // the stream's first unit
+      it.row0 = 0;
+      it.rows = rows;
+      if (ROW_TILES) {
+        const int full = stream_units(nt, kTreeRows, weighted), part = min((pos - s0) / full, rows / kTreeRows);
+        s0 += part * full;
+        it.row0 = part * kTreeRows;
+        it.rows = min(rows - it.row0, kTreeRows);
+      }
+      const int each = weight(it.rows, weighted), s1 = s0 + stream_units(nt, it.rows, weighted);
+      // tiles that start in this CTA's units
+      it.t0 = (pos - s0 + each - 1) / each;
+      it.n = min((min(s1, end) - s0 + each - 1) / each, nt) - it.t0;
+      pos = min(s1, end);
+      if (it.n <= 0) {
+        it.n = 0;
+        continue;
+      }
+      it.b = 32 * w + l;
+      it.q_tok = __shfl_sync(0xffffffffu, seq.row0, l);
+      it.len = __shfl_sync(0xffffffffu, seq.len, l);
+      it.ctx = it.len - drafted;
+      if (it.n == nt) {
+        it.slot = -1;
+      } else {
+        it.slot = it.t0 == 0 ? 1 : 0;
+        // a CTA has more units than any tile, so the pieces are in CTAs one after another
+        if (it.t0 == 0) it.pieces = cta_of(s0 + (nt - 1) * each) - (int)blockIdx.x + 1;
+      }
+      return it;
     }
-    const int l = __ffs(__ballot_sync(0xffffffffu, first <= pos && pos < first + stages)) - 1;
-    const int at = __shfl_sync(0xffffffffu, first, l), nt = __shfl_sync(0xffffffffu, tiles, l);
-    const int drafted = __shfl_sync(0xffffffffu, seq.drafted, l);
-    const int stream = (pos - at) / nt, s0 = at + stream * nt, s1 = s0 + nt;
-    const int parts = ROW_TILES ? (drafted * group + kTreeRows - 1) / kTreeRows : 1;
-    it.b = 32 * w + l;
-    it.g = stream / parts;
-    it.row0 = stream % parts * kTreeRows;
-    it.rows = ROW_TILES ? min(drafted * group - it.row0, kTreeRows) : drafted * group;
-    it.t0 = pos - s0;
-    it.n = min(s1, end) - pos;
-    it.q_tok = __shfl_sync(0xffffffffu, seq.row0, l);
-    it.len = __shfl_sync(0xffffffffu, seq.len, l);
-    it.ctx = it.len - drafted;
-    if (it.n == nt) {
-      it.slot = -1;
-    } else {
-      it.slot = it.t0 == 0 ? 1 : 0;
-      if (it.t0 == 0) it.pieces = cta_of(s1 - 1) - (int)blockIdx.x + 1;
-    }
-    pos += it.n;
     return it;
   }
 };

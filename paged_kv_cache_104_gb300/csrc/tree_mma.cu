@@ -111,6 +111,7 @@ struct TreeMmaParams {
   char* partials;            // [CTA][2] of piece_bytes: O [rows][128], then (max, sum) [rows]
   int64_t piece_bytes;
   int piece_rows;
+  bool wide;                 // out is 32-byte aligned
 };
 
 // The order of an item's tiles in the ring, as the products need them: with
@@ -122,6 +123,54 @@ struct Order {
   __device__ int v(int j) const { return both ? 2 * j + 1 : (j < n - 1 ? 2 * j + 2 : 2 * n - 1); }
   __device__ int side_steps(int side) const { return both ? n : (n + 1 - side) >> 1; }
 };
+
+__device__ __forceinline__ void store32(char* to, const uint32_t (&v)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(to)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4*>(to)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+
+// Adds p V to the row's O (TMEM column o_col) for the drafted tokens `left`
+// whose values were cleared, p = 2^(scaled score - base) from q and k in
+// global memory.  The whole warp, each lane its row; not the usual path.
+__device__ __noinline__ void add_cleared(const TreeArgs& a, const TreeItem& it, unsigned long long left, float base,
+                                         uint32_t o_col, int out_row) {
+  const unsigned long long any = __reduce_or_sync(0xffffffffu, (uint32_t)left) |
+                                 (unsigned long long)__reduce_or_sync(0xffffffffu, (uint32_t)(left >> 32)) << 32;
+  for (unsigned long long todo = any; todo; todo &= todo - 1) {
+    const int d = __ffsll((long long)todo) - 1, pos = it.ctx + d;
+    const bool mine = left >> d & 1;
+    int blk = __ldg(a.block_table + (int64_t)it.b * a.max_blocks_per_seq + pos / kBlockSize);
+    if (blk < 0 || (int64_t)blk >= a.num_blocks) blk = 0;
+    const int64_t at = (((int64_t)blk * a.num_kv_heads + it.g) * kBlockSize + pos % kBlockSize) * HD;
+    const __nv_bfloat16* kr = static_cast<const __nv_bfloat16*>(a.k_cache) + at;
+    const __nv_bfloat16* vr = static_cast<const __nv_bfloat16*>(a.v_cache) + at;
+    const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(a.q) + (int64_t)out_row * HD;
+    float s = 0.f;
+    if (mine)
+      for (int i = 0; i < HD; ++i) s = fmaf(__bfloat162float(qr[i]), __bfloat162float(kr[i]), s);
+    const float pw = fast_exp2(fmaf(s, a.scale * 1.4426950408889634f, -base));
+#pragma unroll 1
+    for (int c = 0; c < HD; c += 32) {
+      float o[32];
+      __syncwarp();
+      tmem_ld32(o_col + c, o);
+      tmem_wait_ld();
+      reg_fence(o);
+      if (mine)
+#pragma unroll
+        for (int q = 0; q < 32; ++q) o[q] = fmaf(pw, __bfloat162float(vr[c + q]), o[q]);
+      __syncwarp();
+      tmem_st32(o_col + c, o);
+      tmem_wait_st();
+    }
+  }
+}
 
 __global__ void __launch_bounds__(kThreadsT, 1)
 tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__ CUtensorMap tm_q,
@@ -143,7 +192,7 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
     return;
   }
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int group = a.num_q_heads / a.num_kv_heads;
+  const int group = a.num_q_heads / a.num_kv_heads, log_group = 31 - __clz(group);   // a power of two
 
   if (tid == 0) {
     for (int i = 0; i < TB_COUNT; ++i) {
@@ -161,6 +210,7 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
                  "r"(kTmemCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
+  TreePlan<true> plan(a, warp == W_PLAN);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -188,8 +238,7 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
     if (warp == W_PLAN) {
       // ---------------------------------------------------------------- plan and queries
-      TreePlan<true> plan(a);
-      MergeDesc d{};
+            MergeDesc d{};
       int made = 0, loaded = 0;        // items handed out; queries asked for
       bool last = false;
       TreeItem it;
@@ -219,7 +268,7 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
               for (int s = 0; s < sides; ++s)
                 for (int h = 0; h < 2; ++h)
                   tma_load_3d(sbase + OFF_Q + (qb + s) * Q_BYTES + h * QHALF, &tm_q, bar(TB_QF + qb), 64 * h,
-                              x.g * group, x.q_tok + (x.row0 + s * BM) / group);
+                              x.g * group, x.q_tok + ((x.row0 + s * BM) >> log_group));
             }
             __syncwarp();
             ++loaded;
@@ -477,7 +526,7 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
         s.len = it.len;
         s.drafted = it.len - it.ctx;
         s.row0 = it.q_tok;
-        bits = tree_bits(a, s, (it.row0 + row) / group);
+        bits = tree_bits(a, s, (it.row0 + row) >> log_group);
       }
       float m_run = -INFINITY, l_run = 0.f;                // maximum in scaled log2 units
       const int steps = ord.side_steps(side);
@@ -508,27 +557,37 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
           continue;
         }
         const int t = it.t0 + (ord.both ? i : 2 * i + side), k0 = t * BN;
+        if (k0 + BN > it.ctx) {
+          // Drafted tokens among the keys: those that the row does not see
+          // become -inf in TMEM, 32 keys at a time (in the registers of the
+          // loop below it would be 400 more instructions for every CTA to
+          // fetch).  Drafted token d is key ctx + d.
+#pragma unroll 1
+          for (int c = 0; c < BN / 32; ++c) {
+            const int d = k0 + 32 * c - it.ctx;            // drafted token of the first key
+            uint32_t see;
+            if (d >= 64) see = 0;
+            else if (d >= 0) see = (uint32_t)(bits >> d);
+            else if (d > -32) see = (uint32_t)(bits << -d) | ((1u << -d) - 1);
+            else see = 0xffffffffu;
+            if (__all_sync(0xffffffffu, see == 0xffffffffu || !live)) continue;
+            float x[32];
+            tmem_ld32(lane_base + col_s + c * 32, x);
+            tmem_wait_ld();
+            reg_fence(x);
+#pragma unroll
+            for (int q = 0; q < 32; ++q)
+              if (!((see >> q) & 1)) x[q] = -INFINITY;
+            tmem_st32(lane_base + col_s + c * 32, x);
+          }
+          tmem_wait_st();
+        }
         float x[BN / 32][32];
 #pragma unroll
         for (int c = 0; c < BN / 32; ++c) tmem_ld32(lane_base + col_s + c * 32, x[c]);
         tmem_wait_ld();
 #pragma unroll
         for (int c = 0; c < BN / 32; ++c) reg_fence(x[c]);
-        if (k0 + BN > it.ctx) {
-          // which of the tile's 128 keys this row sees: drafted token d is key ctx + d
-#pragma unroll
-          for (int c = 0; c < BN / 32; ++c) {
-            const int d = k0 + 32 * c - it.ctx;            // drafted token of the chunk's first key
-            uint32_t see;
-            if (d >= 64) see = 0;
-            else if (d >= 0) see = (uint32_t)(bits >> d);
-            else if (d > -32) see = (uint32_t)(bits << -d) | ((1u << -d) - 1);
-            else see = 0xffffffffu;
-#pragma unroll
-            for (int q = 0; q < 32; ++q)
-              if (!((see >> q) & 1)) x[c][q] = -INFINITY;
-          }
-        }
         float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int c = 0; c < BN / 32; ++c)
@@ -596,13 +655,28 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
       base_slot = (base_slot + 2 * it.n) % NS;
       __syncwarp();
       tc_fence_after();
+      const int out_row = (it.q_tok + ((it.row0 + row) >> log_group)) * a.num_q_heads + it.g * group +
+                          (row & (group - 1));             // rows of q, times heads
+      if ((it.t0 + it.n) * BN > it.ctx && warp_live) {
+        // drafted tokens whose values the products left out, of this side's tiles
+        unsigned long long left = live ? bad_v[k % NI] & bits : 0;
+        if (joint && left) {
+          const int edge = min(max(it.ctx / BN * BN + BN - it.ctx, 0), 64);   // drafted tokens of the first such tile
+          const unsigned long long early = edge >= 64 ? ~0ull : (1ull << edge) - 1;
+          left &= ((it.ctx / BN - it.t0) & 1) == side ? early : ~early;
+        }
+        if (__any_sync(0xffffffffu, left != 0))
+          add_cleared(a, it, left, m_run == -INFINITY ? 0.f : m_run, lane_base + col_o, out_row);
+      }
       float w0 = 1.f, w1 = 1.f, m = m_run, l = l_run;
       if (joint) {
         ml[side * BM + r] = make_float2(m_run, l_run);
+        tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(TB_ML));
         wait_or_abort(bar(TB_ML), joints & 1, abort_flag, a.err);
         __syncwarp();
+        tc_fence_after();
         const float2 s0 = ml[r], s1 = ml[BM + r];
         m = fmaxf(s0.x, s1.x);
         const float base = m == -INFINITY ? 0.f : m;
@@ -612,14 +686,11 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
       }
       if (warp_live) {
         const bool none = l == 0.f;                        // the row sees none of these keys
-        const float base = m == -INFINITY ? 0.f : m;
-        const int col0 = joint ? side * 64 : 0, cols = joint ? 64 : HD;
-        const unsigned long long extra =
-            (it.t0 + it.n) * BN > it.ctx ? bad_v[k % NI] & bits : 0;   // values the products left out
-        const int64_t out_row = (int64_t)(it.q_tok + (it.row0 + row) / group) * a.num_q_heads + it.g * group +
-                                (it.row0 + row) % group;
+        const bool whole = it.slot < 0;
         char* piece = p.partials + ((int64_t)blockIdx.x * 2 + it.slot) * p.piece_bytes;
-        const float inv = 1.f / l;
+        char* to = whole ? static_cast<char*>(a.out) + (int64_t)out_row * (HD * 2) : piece + row * (HD * 4);
+        const float inv = none ? 0.f : 1.f / l;
+        const int col0 = joint ? side * 64 : 0, cols = joint ? 64 : HD;
 #pragma unroll 1
         for (int c = col0; c < col0 + cols; c += 32) {
           __syncwarp();                                    // the TMEM loads are the whole warp's
@@ -638,37 +709,27 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
             reg_fence(o);   // side 0 alone: w0 = 1
           }
           if (!live) continue;
-          for (unsigned long long left = extra; left; left &= left - 1) {
-            const int d = __ffsll((long long)left) - 1, pos = it.ctx + d;
-            int blk = __ldg(a.block_table + (int64_t)it.b * a.max_blocks_per_seq + pos / kBlockSize);
-            if (blk < 0 || (int64_t)blk >= a.num_blocks) blk = 0;
-            const int64_t at = (((int64_t)blk * a.num_kv_heads + it.g) * kBlockSize + pos % kBlockSize) * HD;
-            const __nv_bfloat16* kr = static_cast<const __nv_bfloat16*>(a.k_cache) + at;
-            const __nv_bfloat16* vr = static_cast<const __nv_bfloat16*>(a.v_cache) + at;
-            const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(a.q) + out_row * HD;
-            float s = 0.f;
-            for (int i = 0; i < HD; ++i) s = fmaf(__bfloat162float(qr[i]), __bfloat162float(kr[i]), s);
-            const float pw = fast_exp2(fmaf(s, sl2, -base));
-            for (int q = 0; q < 32; ++q) o[q] = fmaf(pw, __bfloat162float(vr[c + q]), o[q]);
-          }
-          if (it.slot < 0) {
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + out_row * HD + c;
-            const float f = none ? 0.f : inv;
+          // 32 bytes a store (a sector; 16 took twice as long) where out is so aligned
+          if (whole) {
 #pragma unroll
-            for (int q = 0; q < 32; q += 8)
-              *reinterpret_cast<uint4*>(out + q) =
-                  none ? make_uint4(0, 0, 0, 0)
-                       : make_uint4(pack_bf16(o[q] * f, o[q + 1] * f), pack_bf16(o[q + 2] * f, o[q + 3] * f),
-                                    pack_bf16(o[q + 4] * f, o[q + 5] * f), pack_bf16(o[q + 6] * f, o[q + 7] * f));
+            for (int q = 0; q < 32; q += 16) {
+              uint32_t v[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v[i] = none ? 0u : pack_bf16(o[q + 2 * i] * inv, o[q + 2 * i + 1] * inv);
+              store32(to + (c + q) * 2, v, p.wide);
+            }
           } else {
-            float* out = reinterpret_cast<float*>(piece) + row * HD + c;
 #pragma unroll
-            for (int q = 0; q < 32; q += 4)
-              *reinterpret_cast<float4*>(out + q) = make_float4(o[q], o[q + 1], o[q + 2], o[q + 3]);
+            for (int q = 0; q < 32; q += 8) {
+              uint32_t v[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v[i] = __float_as_uint(o[q + i]);
+              store32(to + (c + q) * 4, v, true);
+            }
           }
         }
         if (live && (!joint || side == 0)) {
-          if (it.slot >= 0)
+          if (!whole)
             reinterpret_cast<float2*>(piece + (int64_t)p.piece_rows * HD * 4)[row] = make_float2(m, l);
           else if (a.lse)
             a.lse[out_row] = none ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
@@ -755,6 +816,7 @@ cudaError_t launch_tree_attention_mma(const TreeArgs& a, int num_sms, cudaStream
   p.q_bufs = rows <= BM ? 2 : 1;
   p.piece_rows = (int)(rows < kTreeRows ? rows : kTreeRows);
   p.piece_bytes = ((int64_t)p.piece_rows * (HD + 2) * 4 + 255) & ~255ll;
+  p.wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
   p.desc = static_cast<MergeDesc*>(a.workspace);
   p.partials = static_cast<char*>(a.workspace) + kTreeMaxCtas * sizeof(MergeDesc);
   CUtensorMap tm_q, tm_k, tm_v;

@@ -107,6 +107,7 @@ weights_mma_kernel(const __grid_constant__ WeightParams p, const __grid_constant
                  "r"(kTmemCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
+  TreePlan<false> plan(a, warp == W_PLAN);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -130,8 +131,7 @@ weights_mma_kernel(const __grid_constant__ WeightParams p, const __grid_constant
 
   if (warp == W_PLAN) {
     // ------------------------------------------------------------------ plan, queries
-    TreePlan<false> plan(a);
-    int made = 0, loaded = 0;        // passes handed out; queries asked for
+        int made = 0, loaded = 0;        // passes handed out; queries asked for
     bool last = false;
     TreeItem it;
     it.rows = 0;
