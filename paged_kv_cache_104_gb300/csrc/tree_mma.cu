@@ -294,6 +294,10 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
       }
+      // K and V that are read once leave the L2 first; those of a sequence
+      // whose rows are several streams are read again
+      const uint64_t once = policy_evict_first(), again = policy_evict_normal();
+      uint64_t policy = once;
       int pos = 0, checks = 0;        // ring position; V tiles sent to the checker
       uint32_t history = 0;           // which of the last positions went to the checker
       TreeItem it;
@@ -332,12 +336,13 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
           __syncwarp();
           if (lane < nb)
             tma_load_4d(sbase + OFF_KV + slot * TILE + lane * 2 * GROUP8, is_v ? &tm_v : &tm_k, full, 0, 0, 0,
-                        2 * (mine * a.num_kv_heads + it.g));
+                        2 * (mine * a.num_kv_heads + it.g), policy);
           history = history << 1 | (check ? 1u : 0u);
           checks += check;
           ++pos;
         };
         const bool both = it.rows > BM;
+        policy = (it.len - it.ctx) * group <= kTreeRows ? once : again;
         load(false, 0);
         if (!both && it.n > 1 && ok) load(false, 1);
         for (int j = 0; j < it.n && ok; ++j) {

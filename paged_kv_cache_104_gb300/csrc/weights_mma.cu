@@ -205,12 +205,15 @@ weights_mma_kernel(const __grid_constant__ WeightParams p, const __grid_constant
   } else if (warp == W_KEYS) {
     // ------------------------------------------------------------------ key producer
     if (lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
+    // keys that are read once leave the L2 first; those of several passes are read again
+    const uint64_t once = policy_evict_first(), again = policy_evict_normal();
     int pos = 0;                     // ring position
     TreeItem it;
     bool ok = true;
     for (int k = 0; ok && pass_at(k, it); ++k) {
       const int32_t* row = a.block_table + (int64_t)it.b * a.max_blocks_per_seq;
       const int blocks = (it.len + kBlockSize - 1) / kBlockSize;
+      const uint64_t policy = (it.len - it.ctx) * group <= kTreeRows ? once : again;
       auto ids_of = [&](int window) {   // block ids of four tiles, one per lane
         const int idx = window * 32 + lane;
         int blk = 0;
@@ -239,7 +242,7 @@ weights_mma_kernel(const __grid_constant__ WeightParams p, const __grid_constant
         __syncwarp();
         if (lane < nb)
           tma_load_4d(sbase + OFF_K + slot * TILE + lane * 2 * GROUP8, &tm_k, bar(WB_F + slot), 0, 0, 0,
-                      2 * (mine * a.num_kv_heads + it.g));
+                      2 * (mine * a.num_kv_heads + it.g), policy);
       }
       pass_done(k);
     }
