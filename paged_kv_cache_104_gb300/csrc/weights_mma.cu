@@ -306,35 +306,43 @@ weights_mma_kernel(const __grid_constant__ WeightParams p, const __grid_constant
         __syncwarp();
         tc_fence_after();
         float2 sum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        for (int c = 0; c < it.rows; c += 32) {
+        // 2^(s sl2 - lse) of two rows
+        auto weight2 = [&](float x, float y, float lse_x, float lse_y) {
+          const float2 z = ffma2(make_float2(x, y), make_float2(sl2, sl2), make_float2(-lse_x, -lse_y));
+          return make_float2(fast_exp2(z.x), fast_exp2(z.y));
+        };
+        const int plain = masked ? 0 : it.rows & ~31;   // rows whose sums need no care
+        for (int c = 0; c < plain; c += 32) {
           float x[32];
           tmem_ld32(lane_base + c, x);
           tmem_wait_ld();
           reg_fence(x);
-          const bool whole = c + 32 <= it.rows && !masked;
 #pragma unroll
           for (int q = 0; q < 32; q += 4) {
             const float4 e = *reinterpret_cast<const float4*>(lse + c + q);
-            const float2 y0 = ffma2(make_float2(x[q], x[q + 1]), make_float2(sl2, sl2), make_float2(-e.x, -e.y));
-            const float2 y1 = ffma2(make_float2(x[q + 2], x[q + 3]), make_float2(sl2, sl2), make_float2(-e.z, -e.w));
-            x[q] = fast_exp2(y0.x);
-            x[q + 1] = fast_exp2(y0.y);
-            x[q + 2] = fast_exp2(y1.x);
-            x[q + 3] = fast_exp2(y1.y);
+            sum[q >> 1 & 2] = fadd2(sum[q >> 1 & 2], weight2(x[q], x[q + 1], e.x, e.y));
+            sum[(q >> 1 & 2) + 1] = fadd2(sum[(q >> 1 & 2) + 1], weight2(x[q + 2], x[q + 3], e.z, e.w));
           }
-          if (!whole) {
+        }
+        // the rest eight rows at a time: those behind the last, and those that
+        // do not see this key, add nothing
+#pragma unroll 1
+        for (int c = plain; c < it.rows; c += 8) {
+          float x[8];
+          tmem_ld8(lane_base + c, x);
+          tmem_wait_ld();
+          reg_fence(x);
 #pragma unroll
-            for (int q = 0; q < 32; ++q) {
-              const int row = c + q;
-              bool see = row < it.rows;
-              if (see && d >= 0) see = d < kMaxDraft && ((words[row >> log_group] >> d) & 1);
-              if (!see) x[q] = 0.f;
+          for (int q = 0; q < 8; q += 2) {
+            const float2 e = *reinterpret_cast<const float2*>(lse + c + q);
+            float2 y = weight2(x[q], x[q + 1], e.x, e.y);
+            bool see0 = c + q < it.rows, see1 = c + q + 1 < it.rows;
+            if (masked && d >= 0) {
+              see0 = see0 && d < kMaxDraft && ((words[(c + q) >> log_group] >> d) & 1);
+              see1 = see1 && d < kMaxDraft && ((words[(c + q + 1) >> log_group] >> d) & 1);
             }
+            sum[q >> 1] = fadd2(sum[q >> 1], make_float2(see0 ? y.x : 0.f, see1 ? y.y : 0.f));
           }
-#pragma unroll
-          for (int q = 0; q < 32; q += 8)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sum[i] = fadd2(sum[i], make_float2(x[q + 2 * i], x[q + 2 * i + 1]));
         }
         tc_fence_before();
         __syncwarp();
