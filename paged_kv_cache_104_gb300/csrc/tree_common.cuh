@@ -90,7 +90,7 @@ struct TreePlan {
   const int lane, group;
   int windows, w = -1;                 // windows of 32 sequences, the loaded one
   bool weighted = false;
-  int total = 0, ctas = 0;             // units; CTAs that share them
+  int share = 0, longer = 0;           // units of a CTA; the first `longer` CTAs have one more
   int pos = 0, end = 0;                // this CTA's next unit and end
   int start = 0, sum = 0;              // the window's first unit, its units
   TreeSeq seq;                         // lane: its sequence
@@ -109,13 +109,6 @@ struct TreePlan {
     if (!ROW_TILES) return stream_units(nt, rows, heavy);
     return rows / kTreeRows * stream_units(nt, kTreeRows, heavy) + stream_units(nt, rows % kTreeRows, heavy);
   }
-  // x * y / z without the 64-bit division, which takes hundreds of cycles,
-  // where the product is small (it is for any realistic batch)
-  static __device__ int ratio(int x, int y, int z, int plus) {
-    const uint64_t num = (uint64_t)x * (uint32_t)y + plus;
-    return num >> 32 ? (int)(num / (uint32_t)z) : (int)((uint32_t)num / (uint32_t)z);
-  }
-
   // For one warp (active), while the others still set the CTA up.
   __device__ TreePlan(const TreeArgs& args, bool active)
       : a(args), lane(threadIdx.x & 31), group(args.num_q_heads / args.num_kv_heads),
@@ -139,15 +132,18 @@ struct TreePlan {
       }
     }
     w = 0;
-    total = __reduce_add_sync(0xffffffffu, plain * a.num_kv_heads);
+    int total = __reduce_add_sync(0xffffffffu, plain * a.num_kv_heads);
     if (total >= kTreeManyTiles * (int)gridDim.x) {
       weighted = true;
       total = __reduce_add_sync(0xffffffffu, heavy * a.num_kv_heads);
     }
-    ctas = min((int)gridDim.x, total);
-    if ((int)blockIdx.x >= ctas) return;
-    pos = ratio(blockIdx.x, total, ctas, 0);
-    end = ratio(blockIdx.x + 1, total, ctas, 0);
+    // (a kernel starts with none of its code in the SM: every few instructions
+    // before the first item cost a fetch, so there is one division here)
+    share = total / gridDim.x;
+    longer = total - share * gridDim.x;
+    pos = begin_of(blockIdx.x);
+    end = begin_of(blockIdx.x + 1);
+    if (pos == end) return;
     open(0);
   }
   __device__ TreeSeq fetch(int i) const {
@@ -174,7 +170,15 @@ struct TreePlan {
     first = start + x - units;
     sum = __shfl_sync(0xffffffffu, x, 31);
   }
-  __device__ int cta_of(int unit) const { return ratio(unit + 1, ctas, total, -1); }
+  __device__ int begin_of(int cta) const { return cta * share + min(cta, longer); }
+  __device__ int cta_of(int unit) const {
+    const int rest = unit - longer * (share + 1);
+    return rest < 0 ? unit / (share + 1) : longer + rest / share;
+  }
+  // Tiles that start in so many units of a stream.
+  __device__ int tiles_before(int n, int each) const {
+    return each == 1 ? n : each == 2 ? (n + 1) >> 1 : each == 3 ? (n + 2) / 3 : (n + each - 1) / each;
+  }
   // The CTA's next item (n = 0: none).  Every lane gets it.
   __device__ TreeItem next() {
     TreeItem it;
@@ -188,20 +192,23 @@ struct TreePlan {
       const int at = __shfl_sync(0xffffffffu, first, l), nt = __shfl_sync(0xffffffffu, tiles, l);
       const int drafted = __shfl_sync(0xffffffffu, seq.drafted, l), rows = drafted * group;
       const int per_head = head_units(nt, rows, weighted);
-      it.g = (pos - at) / per_head;
-      int s0 = at + it.g * per_head;                       // the stream's first unit
+      int s0 = at;                                         // the stream's first unit
+      for (it.g = 0; pos - s0 >= per_head; ++it.g) s0 += per_head;
       it.row0 = 0;
       it.rows = rows;
       if (ROW_TILES) {
-        const int full = stream_units(nt, kTreeRows, weighted), part = min((pos - s0) / full, rows / kTreeRows);
-        s0 += part * full;
-        it.row0 = part * kTreeRows;
-        it.rows = min(rows - it.row0, kTreeRows);
+        const int full = stream_units(nt, kTreeRows, weighted);
+        while (it.rows > kTreeRows && pos - s0 >= full) {
+          s0 += full;
+          it.row0 += kTreeRows;
+          it.rows -= kTreeRows;
+        }
+        it.rows = min(it.rows, kTreeRows);
       }
       const int each = weight(it.rows, weighted), s1 = s0 + stream_units(nt, it.rows, weighted);
       // tiles that start in this CTA's units
-      it.t0 = (pos - s0 + each - 1) / each;
-      it.n = min((min(s1, end) - s0 + each - 1) / each, nt) - it.t0;
+      it.t0 = tiles_before(pos - s0, each);
+      it.n = min(tiles_before(min(s1, end) - s0, each), nt) - it.t0;
       pos = min(s1, end);
       if (it.n <= 0) {
         it.n = 0;

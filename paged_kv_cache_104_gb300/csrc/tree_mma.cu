@@ -587,62 +587,96 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
           }
           tmem_wait_st();
         }
-        float x[BN / 32][32];
-#pragma unroll
-        for (int c = 0; c < BN / 32; ++c) tmem_ld32(lane_base + col_s + c * 32, x[c]);
-        tmem_wait_ld();
-#pragma unroll
-        for (int c = 0; c < BN / 32; ++c) reg_fence(x[c]);
         float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int c = 0; c < BN / 32; ++c)
+        auto max32 = [&](const float (&x)[32]) {
 #pragma unroll
           for (int q = 0; q < 32; q += 8) {
-            mx4[0] = fmax3(mx4[0], x[c][q], x[c][q + 4]);
-            mx4[1] = fmax3(mx4[1], x[c][q + 1], x[c][q + 5]);
-            mx4[2] = fmax3(mx4[2], x[c][q + 2], x[c][q + 6]);
-            mx4[3] = fmax3(mx4[3], x[c][q + 3], x[c][q + 7]);
+            mx4[0] = fmax3(mx4[0], x[q], x[q + 4]);
+            mx4[1] = fmax3(mx4[1], x[q + 1], x[q + 5]);
+            mx4[2] = fmax3(mx4[2], x[q + 2], x[q + 6]);
+            mx4[3] = fmax3(mx4[3], x[q + 3], x[q + 7]);
           }
-        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl2;
-        float m_new = m_run;
-        if (mx > m_run + kLazy || m_run == -INFINITY) m_new = mx;
-        const float base = m_new == -INFINITY ? 0.f : m_new;   // nothing seen so far: all weights 0
-        const float alpha = (m_new == m_run) ? 1.f : fast_exp2(m_run - base);
-        if (i >= 1 && __any_sync(0xffffffffu, alpha != 1.f)) {
-          // this step's S was issued behind the last product into O, so that
-          // product is complete and O can be rescaled in place
-          __syncwarp();
+        };
+        // the maximum so far, and O scaled to it
+        float m_new, base, alpha;
+        auto raise = [&] {
+          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl2;
+          m_new = m_run;
+          if (mx > m_run + kLazy || m_run == -INFINITY) m_new = mx;
+          base = m_new == -INFINITY ? 0.f : m_new;         // nothing seen so far: all weights 0
+          alpha = (m_new == m_run) ? 1.f : fast_exp2(m_run - base);
+          if (i >= 1 && __any_sync(0xffffffffu, alpha != 1.f)) {
+            // this step's S was issued behind the last product into O, so that
+            // product is complete and O can be rescaled in place
+            __syncwarp();
 #pragma unroll 1
-          for (int c = 0; c < HD / 32; ++c) {
-            float o[32];
-            tmem_ld32(lane_base + col_o + c * 32, o);
-            tmem_wait_ld();
-            reg_fence(o);
+            for (int c = 0; c < HD / 32; ++c) {
+              float o[32];
+              tmem_ld32(lane_base + col_o + c * 32, o);
+              tmem_wait_ld();
+              reg_fence(o);
 #pragma unroll
-            for (int q = 0; q < 32; ++q) o[q] *= alpha;
-            tmem_st32(lane_base + col_o + c * 32, o);
+              for (int q = 0; q < 32; ++q) o[q] *= alpha;
+              tmem_st32(lane_base + col_o + c * 32, o);
+            }
+            tmem_wait_st();
           }
-          tmem_wait_st();
-        }
+        };
         float2 sum2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                           make_float2(0.f, 0.f)};
-        const float2 sl2x2 = make_float2(sl2, sl2), negm = make_float2(-base, -base);
-#pragma unroll
-        for (int c = 0; c < BN / 32; ++c) {
+        // P of 32 keys into TMEM, half a tile at a time to the issuer
+        auto exp32 = [&](const float (&x)[32], int c) {
+          const float2 sl2x2 = make_float2(sl2, sl2), negm = make_float2(-base, -base);
           uint32_t pk[16];
 #pragma unroll
           for (int q = 0; q < 32; q += 2) {
-            const float2 y = ffma2(make_float2(x[c][q], x[c][q + 1]), sl2x2, negm);
+            const float2 y = ffma2(make_float2(x[q], x[q + 1]), sl2x2, negm);
             const float2 pp = make_float2(fast_exp2(y.x), fast_exp2(y.y));
             sum2[(q >> 1) & 3] = fadd2(sum2[(q >> 1) & 3], pp);
             pk[q / 2] = pack_bf16(pp.x, pp.y);
           }
           tmem_st16(lane_base + col_s + c * 16, pk);
-          if (c & 1) {                                     // a half of P is in TMEM
+          if (c & 1) {
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(TB_PF + 2 * side + (c >> 1)));
+          }
+        };
+        if (ord.both) {
+          // the whole row in registers, four loads in flight: the exponentials
+          // are the tensor core's equal here
+          float x[BN / 32][32];
+#pragma unroll
+          for (int c = 0; c < BN / 32; ++c) tmem_ld32(lane_base + col_s + c * 32, x[c]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < BN / 32; ++c) reg_fence(x[c]);
+#pragma unroll
+          for (int c = 0; c < BN / 32; ++c) max32(x[c]);
+          raise();
+#pragma unroll
+          for (int c = 0; c < BN / 32; ++c) exp32(x[c], c);
+        } else {
+          // a side has every other tile, and time: 32 keys at a time, twice
+          // from TMEM, which is a quarter of the code (it has to be fetched
+          // by every CTA as it starts).  P of keys 32 c .. lies over S of keys
+          // 16 c .., which are read by then.
+          float x[32];
+#pragma unroll 1
+          for (int c = 0; c < BN / 32; ++c) {
+            tmem_ld32(lane_base + col_s + c * 32, x);
+            tmem_wait_ld();
+            reg_fence(x);
+            max32(x);
+          }
+          raise();
+#pragma unroll 1
+          for (int c = 0; c < BN / 32; ++c) {
+            tmem_ld32(lane_base + col_s + c * 32, x);
+            tmem_wait_ld();
+            reg_fence(x);
+            exp32(x, c);
           }
         }
         const float2 s01 = fadd2(sum2[0], sum2[1]), s23 = fadd2(sum2[2], sum2[3]);
