@@ -884,10 +884,12 @@ pkv_status tree_prepare(const pkv_tree_args* x, bool attention, pkv::TreeArgs* o
     if (!x->weights || !x->lse || misaligned(x->weights, 4)) return PKV_EINVAL;
     if (x->weights_len < x->max_seq_len) return PKV_EINVAL;
   }
-  // tiles of all sequences, heads and rows are counted in an int
+  // tiles of all sequences, heads and rows (and what the plan adds for a
+  // stream's start and end) are counted in an int
   const int64_t tiles = (x->max_seq_len + 31) / 32;
   const int64_t chunks = ((int64_t)x->max_draft * (x->num_q_heads / x->num_kv_heads) + 31) / 32;
-  if ((int64_t)x->num_seqs * x->num_kv_heads * (tiles * chunks + 8) >= (int64_t)INT_MAX) return PKV_ERANGE;
+  if ((int64_t)x->num_seqs * x->num_kv_heads * (tiles * chunks + 2 * chunks + 16) >= (int64_t)INT_MAX)
+    return PKV_ERANGE;
   int* err = nullptr;
   st = device_state(&err, sms);
   if (st != PKV_OK) return st;

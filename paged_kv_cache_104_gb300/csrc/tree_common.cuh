@@ -61,9 +61,9 @@ __device__ __forceinline__ uint64_t tree_bits(const TreeArgs& a, const TreeSeq& 
 // stream is an item.  Where a CTA gets many tiles, shares are of equal weight:
 // a tile of more than 128 rows takes 1.4 times one of fewer (3,500 cycles
 // against 2,500 of the attention), so 3 against 2 units, and a tile belongs
-// to the CTA in whose units it starts; a stream's last tile is followed by 2
-// units for its start and end.  (Equal numbers of tiles: 231 us for 32 ragged
-// sequences of 1 to 64 drafted tokens, against TREE_RAGGED.)  Where a CTA gets a
+// to the CTA in whose units it starts; a stream's last tile is followed by 6 or
+// 10 units for its start and end (7,000 and 13,000 cycles).  (Equal numbers of tiles: 231 us for 32 ragged
+// sequences of 1 to 64 drafted tokens, against 170.)  Where a CTA gets a
 // few tiles, every tile counts alike.  One warp of every CTA works the
 // plan out from the lengths, 32 sequences at a time, so no shared memory grows
 // with the batch.
@@ -103,7 +103,9 @@ struct TreePlan {
   }
   // Units of a stream of nt tiles, and of all the streams of a KV head.
   __device__ int stream_units(int nt, int rows, bool heavy) const {
-    return rows > 0 ? nt * weight(rows, heavy) + (heavy ? 2 : 0) : 0;
+    if (rows <= 0) return 0;
+    const int each = weight(rows, heavy);
+    return nt * each + (heavy ? 4 * each - 2 : 0);
   }
   __device__ int head_units(int nt, int rows, bool heavy) const {
     if (!ROW_TILES) return stream_units(nt, rows, heavy);
