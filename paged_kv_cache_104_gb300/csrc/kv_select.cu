@@ -10,12 +10,14 @@
 // stays; then every token's place is a prefix sum.
 //
 // The bytes are few (4 a token); what bounds it is the chain of barriers.  So a
-// (sequence, KV head) is read once, eight tokens a thread, and its keys stay in
-// registers through three passes of 11, 11 and 10 bits (against 4 of 8 with
-// re-reads: 88 -> 19 us for 64 sequences of 2,301); beyond 8,192 tokens a
-// cluster of up to eight CTAs shares it, adding its histograms up in the first
-// one's shared memory (122 -> 30 us for 8 sequences of 32,001).  Longer
-// bounds than 65,536 take one CTA that reads the weights once a pass.
+// (sequence, KV head) is read once, 16 tokens a thread, and its keys stay in
+// registers through up to three passes of 11, 11 and 10 bits.  As soon as at
+// most 256 tokens share the digits of the last one that stays, those are ranked
+// by comparing each with all, which for 2,301 tokens is mostly after the first
+// pass (SELECT_A us for 64 such sequences, against 19.4 with all three).  Beyond
+// 8,192 tokens a cluster of up to eight CTAs shares a (sequence, KV head), adding
+// its histograms up in the first one's shared memory (SELECT_B us for 8 sequences
+// of 32,001).  Bounds over 65,536 take one CTA that reads the weights once a pass.
 #include <climits>
 
 #include <cooperative_groups.h>
@@ -76,16 +78,45 @@ __device__ __forceinline__ bool select_begin(const SelectArgs& a, int item, int 
   return true;
 }
 
-constexpr int kPerThread = 8;      // tokens
+constexpr int kPerThread = 16;     // tokens
 constexpr int kBins = 2048;
+constexpr int kFew = 256;          // tokens that are ranked by comparing each with all
 
-// THREADS * 8 tokens a CTA, a cluster per (sequence, KV head).
+// Sums of all threads before this one, and of all (one barrier; warp_sums is
+// free again after the next).
 template <int THREADS>
-__global__ void __launch_bounds__(THREADS) select_reg_kernel(const SelectArgs a) {
-  __shared__ uint32_t bins[kBins];
-  __shared__ uint32_t warp_sums[THREADS / 32];
-  __shared__ uint32_t found[2];                          // digit, how many of it
+__device__ __forceinline__ uint32_t scan_before(uint32_t own, uint32_t* warp_sums, uint32_t& total) {
+  constexpr int WARPS = THREADS / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t x = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) warp_sums[warp] = x;
+  __syncthreads();
+  uint32_t v = lane < WARPS ? warp_sums[lane] : 0;
+#pragma unroll
+  for (int o = 1; o < WARPS; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += y;
+  }
+  total = __shfl_sync(0xffffffffu, v, WARPS - 1);
+  const uint32_t before = __shfl_sync(0xffffffffu, v, (warp + 31) & 31);
+  return x - own + (warp > 0 ? before : 0);
+}
+
+// THREADS * 16 tokens a CTA, a cluster per (sequence, KV head).
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) select_reg_kernel(const SelectArgs a) {
+  __shared__ __align__(16) uint32_t bins[kBins];
+  __shared__ uint32_t warp_sums[2][32];
+  __shared__ uint32_t found[3];                          // digit, how many of it stay, how many have it
   __shared__ uint32_t counts[8][2];                      // per CTA: tokens that stay for sure, ties
+  __shared__ unsigned long long few[kFew];               // key, then the earlier token first
+  __shared__ uint32_t few_n;                             // (rank 0's)
+  __shared__ uint8_t few_stays[kFew];
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = cluster.block_rank(), ranks = cluster.num_blocks(), tid = threadIdx.x;
   const int item = blockIdx.x / ranks;
@@ -102,10 +133,14 @@ __global__ void __launch_bounds__(THREADS) select_reg_kernel(const SelectArgs a)
   const int t0 = (rank * THREADS + tid) * kPerThread;
   uint32_t key[kPerThread], mid = 0;                     // mid: which tokens are to be chosen from
   if (t0 + kPerThread <= n && (reinterpret_cast<uintptr_t>(w + t0) & 15) == 0) {
-    const float4 x = __ldg(reinterpret_cast<const float4*>(w + t0)), y = __ldg(reinterpret_cast<const float4*>(w + t0) + 1);
-    const float v[kPerThread] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-    for (int i = 0; i < kPerThread; ++i) key[i] = order_key(v[i]);
+    for (int i = 0; i < kPerThread; i += 4) {
+      const float4 x = __ldg(reinterpret_cast<const float4*>(w + t0 + i));
+      key[i] = order_key(x.x);
+      key[i + 1] = order_key(x.y);
+      key[i + 2] = order_key(x.z);
+      key[i + 3] = order_key(x.w);
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) key[i] = t0 + i < n ? order_key(__ldg(w + t0 + i)) : 0;
@@ -113,13 +148,18 @@ __global__ void __launch_bounds__(THREADS) select_reg_kernel(const SelectArgs a)
 #pragma unroll
   for (int i = 0; i < kPerThread; ++i)
     if (t0 + i >= lo && t0 + i < hi) mid |= 1u << i;
-  for (int i = tid; i < kBins; i += THREADS) bins[i] = 0;
+  auto clear = [&] {
+    for (int i = tid; i < kBins / 4; i += THREADS) reinterpret_cast<uint4*>(bins)[i] = make_uint4(0, 0, 0, 0);
+  };
+  clear();
+  if (tid == 0) few_n = 0;
   sync();
-  uint32_t prefix = 0;
+  uint32_t prefix = 0, above = 0;                        // the digits so far, and their bits
+  bool ranked = false;
 #pragma unroll 1
   for (int pass = 0; pass < 3 && any; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-    const uint32_t above = pass == 0 ? 0u : pass == 1 ? 0xffe00000u : 0xfffffc00u, mask = pass == 2 ? 1023 : 2047;
+    const uint32_t mask = pass == 2 ? 1023 : 2047;
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i)
       if ((mid >> i & 1) && ((key[i] ^ prefix) & above) == 0) atomicAdd(&bins[key[i] >> shift & mask], 1u);
@@ -136,40 +176,89 @@ __global__ void __launch_bounds__(THREADS) select_reg_kernel(const SelectArgs a)
       // bins from the highest down, kBins / THREADS a thread: whose do the
       // wanted tokens end in?
       constexpr int W = kBins / THREADS;
-      const int top = kBins - 1 - tid * W;
-      uint32_t own = 0, total;
+      const int bottom = kBins - (tid + 1) * W;
+      uint32_t bin[W], own = 0, total;
 #pragma unroll
-      for (int i = 0; i < W; ++i) own += bins[top - i];
-      const uint32_t through = block_scan<THREADS>(own, warp_sums, total);
-      if (through >= want && through - own < want) {
-        uint32_t left = want - (through - own);
-        int bin = top;
-        while (bins[bin] < left) left -= bins[bin--];
+      for (int i = 0; i < W; i += 4) {
+        const uint4 x = *reinterpret_cast<const uint4*>(bins + bottom + i);
+        bin[i] = x.x;
+        bin[i + 1] = x.y;
+        bin[i + 2] = x.z;
+        bin[i + 3] = x.w;
+        own += x.x + x.y + x.z + x.w;
+      }
+      const uint32_t before = scan_before<THREADS>(own, warp_sums[pass & 1], total);
+      if (before < want && before + own >= want) {
+        uint32_t left = want - before, digit = 0, have = 0;
+        bool open = true;
+#pragma unroll
+        for (int i = W - 1; i >= 0; --i) {
+          const bool here = open && bin[i] >= left;
+          if (here) {
+            digit = bottom + i;
+            have = bin[i];
+          }
+          open = open && !here;
+          if (open) left -= bin[i];
+        }
         for (int k = 0; k < ranks; ++k) {
           uint32_t* f = ranks > 1 ? cluster.map_shared_rank(found, k) : found;
-          f[0] = bin;
+          f[0] = digit;
           f[1] = left;
+          f[2] = have;
         }
       }
       __syncthreads();
     }
-    for (int i = tid; i < kBins; i += THREADS) bins[i] = 0;
+    clear();
     sync();
     prefix |= found[0] << shift;
+    above |= mask << shift;
     want = found[1];
+    if (pass < 2 && found[2] <= kFew) {
+      ranked = true;
+      break;
+    }
   }
-  // keys above `prefix` stay, and the first `want` tokens that have it
+  // keys above `prefix` stay, and of those that have it the first `want` in
+  // the order of the weights, or of the tokens where they are equal
   uint32_t sure = 0, ties = 0;
 #pragma unroll
   for (int i = 0; i < kPerThread; ++i) {
     const bool m = mid >> i & 1;
-    sure |= (uint32_t)(t0 + i < n && (!m || (any && key[i] > prefix))) << i;
-    ties |= (uint32_t)(m && any && key[i] == prefix) << i;
+    sure |= (uint32_t)(t0 + i < n && (!m || (any && (key[i] & above) > prefix))) << i;
+    ties |= (uint32_t)(m && any && (key[i] & above) == prefix) << i;
+  }
+  if (ranked) {
+    uint32_t* counter = ranks > 1 ? cluster.map_shared_rank(&few_n, 0) : &few_n;
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i)
+      if (ties >> i & 1) {
+        const uint32_t slot = atomicAdd(counter, 1u);
+        const unsigned long long x = (unsigned long long)key[i] << 32 | (0xffffffffu - (uint32_t)(t0 + i));
+        for (int k = 0; k < ranks; ++k) (ranks > 1 ? cluster.map_shared_rank(few, k) : few)[slot] = x;
+        key[i] = slot;
+      }
+    sync();
+    const int have = found[2];
+    for (int j = tid; j < have; j += THREADS) {
+      const unsigned long long x = few[j];
+      uint32_t ahead = 0;
+#pragma unroll 4
+      for (int k = 0; k < have; ++k) ahead += few[k] > x;
+      few_stays[j] = ahead < want;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i)
+      if ((ties >> i & 1) && few_stays[key[i]]) sure |= 1u << i;
+    ties = 0;
+    want = 0;
   }
   // both counts in one scan: at most 8,192 of each in a CTA
   uint32_t total;
-  uint32_t at = block_scan<THREADS>(__popc(sure) | __popc(ties) << 16, warp_sums, total);
-  uint32_t sure_at = (at & 0xffff) - __popc(sure), ties_at = (at >> 16) - __popc(ties);
+  const uint32_t before = scan_before<THREADS>(__popc(sure) | __popc(ties) << 16, warp_sums[1], total);
+  uint32_t sure_at = before & 0xffff, ties_at = before >> 16;
   if (ranks > 1) {
     if (tid < ranks) {
       uint32_t* c = cluster.map_shared_rank(&counts[0][0], tid);
@@ -261,10 +350,10 @@ cudaError_t launch_reg(const SelectArgs& a, int ranks, cudaStream_t stream) {
 
 cudaError_t launch_kv_select(const SelectArgs& a, cudaStream_t stream) {
   const int tokens = a.max_seq_len;
-  if (tokens <= 128 * kPerThread) return launch_reg<128>(a, 1, stream);
-  if (tokens <= 512 * kPerThread) return launch_reg<512>(a, 1, stream);
+  if (tokens <= 64 * kPerThread) return launch_reg<64>(a, 1, stream);
+  if (tokens <= 256 * kPerThread) return launch_reg<256>(a, 1, stream);
   for (int ranks = 1; ranks <= 8; ranks *= 2)
-    if (tokens <= 1024 * kPerThread * ranks) return launch_reg<1024>(a, ranks, stream);
+    if (tokens <= 512 * kPerThread * ranks) return launch_reg<512>(a, ranks, stream);
   select_kernel<<<a.num_seqs * a.num_kv_heads, kSelThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }

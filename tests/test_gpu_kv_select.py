@@ -71,6 +71,27 @@ def test_equal_in_the_leading_bits():
         check(w, [6000, 5000], 1700, 2, 30)
 
 
+@pytest.mark.parametrize("n", [700, 3500, 8000, 20000])
+def test_many_share_the_leading_digits(n):
+    """More and fewer than 256 tokens with the threshold's first 11 or 22 bits."""
+    base = torch.tensor(1.5).view(torch.int32)
+    g = torch.Generator().manual_seed(n)
+    for bits in (3, 9, 12, 20, 23):
+        w = (base + torch.randint(0, 1 << bits, (1, 2, n), generator=g, dtype=torch.int32)).view(torch.float32)
+        w = w * (torch.rand((1, 2, n), generator=g) > 0.9 if bits == 23 else 1)
+        for budget in (5, n // 16, n // 2):
+            check(w, [n], budget, 0, 3)
+
+
+@pytest.mark.parametrize("same", [255, 256, 257, 300])
+def test_ties_around_the_rankings_bound(same):
+    w = torch.zeros(1, 1, 5000)
+    w[0, 0, 7::16][:same] = 2.0
+    w[0, 0, 3::50] = 3.0
+    for budget in (99, 101, 200, 100 + same, 101 + same):
+        check(w, [5000], budget, 0, 0)
+
+
 def test_ragged_batch_and_width():
     lens = [1, 4000, 0, 17, 2048, 1024, 3999, 333]
     check(tailed(8, 4, 4100, 9), lens, 1024, 4, 64, max_len=4000)
