@@ -9,15 +9,17 @@
 // of their digits, from the highest, narrow the key of the last token that
 // stays; then every token's place is a prefix sum.
 //
-// The bytes are few (4 a token); what bounds it is the chain of barriers.  So a
-// (sequence, KV head) is read once, 16 tokens a thread, and its keys stay in
-// registers through up to three passes of 11, 11 and 10 bits.  As soon as at
-// most 256 tokens share the digits of the last one that stays, those are ranked
-// by comparing each with all, which for 2,301 tokens is mostly after the first
-// pass (SELECT_A us for 64 such sequences, against 19.4 with all three).  Beyond
-// 8,192 tokens a cluster of up to eight CTAs shares a (sequence, KV head), adding
-// its histograms up in the first one's shared memory (SELECT_B us for 8 sequences
-// of 32,001).  Bounds over 65,536 take one CTA that reads the weights once a pass.
+// The bytes are few (4 a token); what bounds it is the chain of barriers, and
+// the code itself, which every launch fetches anew.  So a (sequence, KV head) is
+// read once, 16 tokens a thread, and its keys stay in shared memory (in
+// registers every loop over them was unrolled: 17.3 us for 64 sequences of
+// 2,301, against 11.9) through up to three passes of 11, 11 and 10 bits.  As
+// soon as at most 256 tokens share the digits of the last one that stays, those
+// are ranked by comparing each with all, which for 2,301 tokens is mostly after
+// the first pass.  Beyond 8,192 tokens a cluster of up to eight CTAs shares a
+// (sequence, KV head), adding its histograms up in the first one's shared memory
+// (16.4 us for 8 sequences of 32,001).  Bounds over 65,536 take one CTA that
+// reads the weights once a pass.
 #include <climits>
 
 #include <cooperative_groups.h>
@@ -109,50 +111,44 @@ __device__ __forceinline__ uint32_t scan_before(uint32_t own, uint32_t* warp_sum
 
 // THREADS * 16 tokens a CTA, a cluster per (sequence, KV head).
 template <int THREADS>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS) select_reg_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(THREADS, 1536 / THREADS) select_smem_kernel(const SelectArgs a) {
+  constexpr int TOKENS = THREADS * kPerThread;
+  __shared__ uint32_t keys[TOKENS + TOKENS / kPerThread];   // token t at t + t / 16: free of bank conflicts
   __shared__ __align__(16) uint32_t bins[kBins];
+  __shared__ uint32_t stays[TOKENS / 32];                // ranked tokens that stay
   __shared__ uint32_t warp_sums[2][32];
   __shared__ uint32_t found[3];                          // digit, how many of it stay, how many have it
   __shared__ uint32_t counts[8][2];                      // per CTA: tokens that stay for sure, ties
-  __shared__ unsigned long long few[kFew];               // key, then the earlier token first
-  __shared__ uint32_t few_n;                             // (rank 0's)
-  __shared__ uint8_t few_stays[kFew];
+  __shared__ unsigned long long few[kFew], mine[kFew];   // key, then the earlier token first: all, this CTA's
+  __shared__ uint32_t few_n, mine_n, few_base;           // (few_n: the first CTA's)
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = cluster.block_rank(), ranks = cluster.num_blocks(), tid = threadIdx.x;
   const int item = blockIdx.x / ranks;
+  const float* w = a.weights + (int64_t)item * a.weights_len;
+  const int base = rank * TOKENS;
+  auto at = [](int t) { return t + t / kPerThread; };
+  // the weights up to the bound on the length, asked for with the length
+  const int here = min(TOKENS, a.max_seq_len - base);
+#pragma unroll 8
+  for (int t = tid; t < here; t += THREADS) keys[at(t)] = order_key(__ldg(w + base + t));
   int n;
   if (!select_begin(a, item, rank * THREADS + tid, ranks * THREADS, &n)) return;
   auto sync = [&] {
     if (ranks > 1) cluster.sync();
     else __syncthreads();
   };
-  const float* w = a.weights + (int64_t)item * a.weights_len;
-  const int lo = a.sinks, hi = n - a.recent;             // the tokens to choose from
-  uint32_t want = a.budget - a.sinks - a.recent;         // and how many; < hi - lo
+  // the tokens to choose from are lo .. hi - 1 (of this CTA: lo0 .. hi0 - 1),
+  // and `want` of them, which are fewer
+  const int lo = a.sinks, hi = n - a.recent;
+  const int lo0 = max(lo - base, 0), hi0 = min(hi - base, TOKENS);
+  uint32_t want = a.budget - a.sinks - a.recent;
   const bool any = want > 0;
-  const int t0 = (rank * THREADS + tid) * kPerThread;
-  uint32_t key[kPerThread], mid = 0;                     // mid: which tokens are to be chosen from
-  if (t0 + kPerThread <= n && (reinterpret_cast<uintptr_t>(w + t0) & 15) == 0) {
-#pragma unroll
-    for (int i = 0; i < kPerThread; i += 4) {
-      const float4 x = __ldg(reinterpret_cast<const float4*>(w + t0 + i));
-      key[i] = order_key(x.x);
-      key[i + 1] = order_key(x.y);
-      key[i + 2] = order_key(x.z);
-      key[i + 3] = order_key(x.w);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kPerThread; ++i) key[i] = t0 + i < n ? order_key(__ldg(w + t0 + i)) : 0;
-  }
-#pragma unroll
-  for (int i = 0; i < kPerThread; ++i)
-    if (t0 + i >= lo && t0 + i < hi) mid |= 1u << i;
   auto clear = [&] {
     for (int i = tid; i < kBins / 4; i += THREADS) reinterpret_cast<uint4*>(bins)[i] = make_uint4(0, 0, 0, 0);
   };
   clear();
-  if (tid == 0) few_n = 0;
+  for (int i = tid; i < TOKENS / 32; i += THREADS) stays[i] = 0;
+  if (tid == 0) few_n = mine_n = 0;
   sync();
   uint32_t prefix = 0, above = 0;                        // the digits so far, and their bits
   bool ranked = false;
@@ -160,9 +156,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) select_reg_kernel(con
   for (int pass = 0; pass < 3 && any; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
     const uint32_t mask = pass == 2 ? 1023 : 2047;
-#pragma unroll
-    for (int i = 0; i < kPerThread; ++i)
-      if ((mid >> i & 1) && ((key[i] ^ prefix) & above) == 0) atomicAdd(&bins[key[i] >> shift & mask], 1u);
+#pragma unroll 4
+    for (int t = lo0 + tid; t < hi0; t += THREADS) {
+      const uint32_t key = keys[at(t)];
+      if (((key ^ prefix) & above) == 0) atomicAdd(&bins[key >> shift & mask], 1u);
+    }
     __syncthreads();
     if (ranks > 1) {
       if (rank > 0) {
@@ -177,35 +175,22 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) select_reg_kernel(con
       // wanted tokens end in?
       constexpr int W = kBins / THREADS;
       const int bottom = kBins - (tid + 1) * W;
-      uint32_t bin[W], own = 0, total;
+      uint32_t own = 0, total;
 #pragma unroll
       for (int i = 0; i < W; i += 4) {
         const uint4 x = *reinterpret_cast<const uint4*>(bins + bottom + i);
-        bin[i] = x.x;
-        bin[i + 1] = x.y;
-        bin[i + 2] = x.z;
-        bin[i + 3] = x.w;
         own += x.x + x.y + x.z + x.w;
       }
       const uint32_t before = scan_before<THREADS>(own, warp_sums[pass & 1], total);
       if (before < want && before + own >= want) {
-        uint32_t left = want - before, digit = 0, have = 0;
-        bool open = true;
-#pragma unroll
-        for (int i = W - 1; i >= 0; --i) {
-          const bool here = open && bin[i] >= left;
-          if (here) {
-            digit = bottom + i;
-            have = bin[i];
-          }
-          open = open && !here;
-          if (open) left -= bin[i];
-        }
+        uint32_t left = want - before;
+        int bin = bottom + W - 1;
+        while (bins[bin] < left) left -= bins[bin--];
         for (int k = 0; k < ranks; ++k) {
-          uint32_t* f = ranks > 1 ? cluster.map_shared_rank(found, k) : found;
-          f[0] = digit;
+          uint32_t* f = cluster.map_shared_rank(found, k);
+          f[0] = bin;
           f[1] = left;
-          f[2] = have;
+          f[2] = bins[bin];
         }
       }
       __syncthreads();
@@ -220,40 +205,54 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) select_reg_kernel(con
       break;
     }
   }
-  // keys above `prefix` stay, and of those that have it the first `want` in
-  // the order of the weights, or of the tokens where they are equal
-  uint32_t sure = 0, ties = 0;
-#pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    const bool m = mid >> i & 1;
-    sure |= (uint32_t)(t0 + i < n && (!m || (any && (key[i] & above) > prefix))) << i;
-    ties |= (uint32_t)(m && any && (key[i] & above) == prefix) << i;
-  }
+  // Keys above `prefix` stay, and of those that have it the first `want` in
+  // the order of the weights (ranked), or of the tokens where they are equal.
   if (ranked) {
-    uint32_t* counter = ranks > 1 ? cluster.map_shared_rank(&few_n, 0) : &few_n;
-#pragma unroll
-    for (int i = 0; i < kPerThread; ++i)
-      if (ties >> i & 1) {
-        const uint32_t slot = atomicAdd(counter, 1u);
-        const unsigned long long x = (unsigned long long)key[i] << 32 | (0xffffffffu - (uint32_t)(t0 + i));
-        for (int k = 0; k < ranks; ++k) (ranks > 1 ? cluster.map_shared_rank(few, k) : few)[slot] = x;
-        key[i] = slot;
-      }
-    sync();
-    const int have = found[2];
-    for (int j = tid; j < have; j += THREADS) {
-      const unsigned long long x = few[j];
-      uint32_t ahead = 0;
 #pragma unroll 4
-      for (int k = 0; k < have; ++k) ahead += few[k] > x;
-      few_stays[j] = ahead < want;
+    for (int t = lo0 + tid; t < hi0; t += THREADS) {
+      const uint32_t key = keys[at(t)];
+      if ((key & above) == prefix)
+        mine[atomicAdd(&mine_n, 1u)] = (unsigned long long)key << 32 | (0xffffffffu - (uint32_t)(base + t));
     }
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kPerThread; ++i)
-      if ((ties >> i & 1) && few_stays[key[i]]) sure |= 1u << i;
-    ties = 0;
+    const unsigned long long* all = mine;
+    if (ranks > 1) {
+      if (tid == 0) few_base = atomicAdd(cluster.map_shared_rank(&few_n, 0), mine_n);
+      __syncthreads();
+      for (int i = tid; i < (int)mine_n * ranks; i += THREADS)
+        cluster.map_shared_rank(few, i % ranks)[few_base + i / ranks] = mine[i / ranks];
+      cluster.sync();
+      all = few;
+    }
+    // this CTA's, each with all, by 1 .. 8 neighbouring threads
+    const int have = found[2], own = mine_n;
+    int log_parts = 0;
+    while (log_parts < 3 && own << (log_parts + 1) <= THREADS) ++log_parts;
+    const int parts = 1 << log_parts;
+    for (int j = tid >> log_parts; j < ((own + 31) & ~31); j += THREADS >> log_parts) {
+      const unsigned long long x = j < own ? mine[j] : 0;
+      uint32_t ahead = 0;
+#pragma unroll 4
+      for (int k = tid & (parts - 1); k < have; k += parts) ahead += all[k] > x;
+      for (int o = 1; o < parts; o <<= 1) ahead += __shfl_xor_sync(0xffffffffu, ahead, o);
+      if (j < own && ahead < want && (tid & (parts - 1)) == 0) {
+        const int t = (int)(0xffffffffu - (uint32_t)x) - base;
+        atomicOr(&stays[t >> 5], 1u << (t & 31));
+      }
+    }
     want = 0;
+    __syncthreads();
+  }
+  // a thread's 16 tokens: which stay, and which are equal to the last that does
+  const int t0 = tid * kPerThread;
+  uint32_t sure = ranked ? stays[t0 >> 5] >> (t0 & 31) & 0xffff : 0, ties = 0;
+#pragma unroll 4
+  for (int i = 0; i < kPerThread; ++i) {
+    const int t = t0 + i;
+    const bool mid = t >= lo0 && t < hi0;
+    const uint32_t key = keys[at(t)] & above;
+    sure |= (uint32_t)(base + t < n && (!mid || (any && key > prefix))) << i;
+    ties |= (uint32_t)(!ranked && mid && any && key == prefix) << i;
   }
   // both counts in one scan: at most 8,192 of each in a CTA
   uint32_t total;
@@ -272,11 +271,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) select_reg_kernel(con
     }
   }
   int32_t* kept = a.kept + (int64_t)item * a.budget;
-#pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
+  for (uint32_t left = sure | ties; left; left &= left - 1) {
+    const int i = __ffs(left) - 1;
     const bool tie = ties >> i & 1;
-    if ((sure >> i & 1) || (tie && ties_at < want)) kept[sure_at + min(ties_at, want)] = t0 + i;
-    sure_at += sure >> i & 1;
+    if (!tie || ties_at < want) kept[sure_at + min(ties_at, want)] = base + t0 + i;
+    sure_at += !tie;
     ties_at += tie;
   }
 }
@@ -332,7 +331,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
 }
 
 template <int THREADS>
-cudaError_t launch_reg(const SelectArgs& a, int ranks, cudaStream_t stream) {
+cudaError_t launch_smem(const SelectArgs& a, int ranks, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.num_seqs * a.num_kv_heads * ranks));
   cfg.blockDim = dim3(THREADS);
@@ -343,17 +342,17 @@ cudaError_t launch_reg(const SelectArgs& a, int ranks, cudaStream_t stream) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, select_reg_kernel<THREADS>, a);
+  return cudaLaunchKernelEx(&cfg, select_smem_kernel<THREADS>, a);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_select(const SelectArgs& a, cudaStream_t stream) {
   const int tokens = a.max_seq_len;
-  if (tokens <= 64 * kPerThread) return launch_reg<64>(a, 1, stream);
-  if (tokens <= 256 * kPerThread) return launch_reg<256>(a, 1, stream);
+  if (tokens <= 64 * kPerThread) return launch_smem<64>(a, 1, stream);
+  if (tokens <= 256 * kPerThread) return launch_smem<256>(a, 1, stream);
   for (int ranks = 1; ranks <= 8; ranks *= 2)
-    if (tokens <= 512 * kPerThread * ranks) return launch_reg<512>(a, ranks, stream);
+    if (tokens <= 512 * kPerThread * ranks) return launch_smem<512>(a, ranks, stream);
   select_kernel<<<a.num_seqs * a.num_kv_heads, kSelThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
