@@ -942,7 +942,7 @@ pkv_status pkv_paged_tree_attention(const pkv_tree_args* x, pkv_stream_t stream)
   if (st != PKV_OK || !todo) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = x->dtype == PKV_BF16 ? pkv::launch_tree_attention_mma(a, sms, s)
-                                             : pkv::launch_tree_attention_cc(a, false, s);
+                                             : pkv::launch_tree_attention_cc(a, s);
   return e == cudaSuccess ? PKV_OK : PKV_ECUDA;
 }
 
@@ -954,7 +954,7 @@ pkv_status pkv_kv_add_weights(const pkv_tree_args* x, pkv_stream_t stream) {
   if (st != PKV_OK || !todo) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = x->dtype == PKV_BF16 ? pkv::launch_kv_add_weights_mma(a, sms, s)
-                                             : pkv::launch_kv_add_weights_cc(a, false, s);
+                                             : pkv::launch_kv_add_weights_cc(a, s);
   return e == cudaSuccess ? PKV_OK : PKV_ECUDA;
 }
 

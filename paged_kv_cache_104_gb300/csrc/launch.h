@@ -258,12 +258,12 @@ struct TreeArgs {
   int* err;
 };
 // fp32, head_dim 16 or 128 (CUDA cores)
-cudaError_t launch_tree_attention_cc(const TreeArgs& a, bool is_bf16, cudaStream_t stream);
-// bf16, head_dim 128 (tcgen05); workspace of tree_workspace_bytes
+cudaError_t launch_tree_attention_cc(const TreeArgs& a, cudaStream_t stream);
+cudaError_t launch_kv_add_weights_cc(const TreeArgs& a, cudaStream_t stream);
+// bf16, head_dim 128 (tcgen05); the attention's workspace of tree_workspace_bytes
 size_t tree_workspace_bytes(int group, int max_draft);
 cudaError_t launch_tree_attention_mma(const TreeArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_kv_add_weights_mma(const TreeArgs& a, int num_sms, cudaStream_t stream);
-cudaError_t launch_kv_add_weights_cc(const TreeArgs& a, bool is_bf16, cudaStream_t stream);
 
 // Selection of the tokens that stay, per (sequence, KV head).
 struct SelectArgs {
