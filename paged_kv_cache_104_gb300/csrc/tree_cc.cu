@@ -17,7 +17,7 @@
 // its own, so that a K or V value that it reads serves four: for the scores a
 // lane has four keys and a quarter of the dims (8 reads of 16 bytes for 64
 // multiply-adds; a row and four keys a thread took 5 for 16, and 52.8 us for
-// four sequences of 500 to 1,500 against 24.5), for P V four dims of the four
+// four sequences of 500 to 1,500 against 21.4), for P V four dims of the four
 // rows (2 reads for 16).  A warp without rows only helps to load.
 #include <climits>
 
@@ -93,7 +93,7 @@ __device__ __forceinline__ void scores(const float (*q)[D + 4], const float (*k)
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
-#pragma unroll 2
+#pragma unroll 4
   for (int d = d0; d < d0 + D / 4; d += 4) {
     float4 x[4], y[4];
 #pragma unroll
@@ -138,20 +138,40 @@ __global__ void __launch_bounds__(kThreadsCC) tree_cc_kernel(const TreeArgs a) {
   const int32_t* table = a.block_table + (int64_t)b * a.max_blocks_per_seq;
 
   constexpr int CH = D / 4, STEPS = (kKeys * CH + kThreadsCC - 1) / kThreadsCC;
+  constexpr int BLOCKS = kKeys / kBlockSize;
+  static_assert(BLOCKS == 2, "two cache blocks a tile");
   float4 kr[STEPS], vr[STEPS];
+  int blocks[BLOCKS];                    // of the tile to be fetched next
+  auto ask_blocks = [&](int tile) {
+#pragma unroll
+    for (int i = 0; i < BLOCKS; ++i) {
+      blocks[i] = 0;
+      if ((tile * BLOCKS + i) * kBlockSize < s.len) blocks[i] = __ldg(table + tile * BLOCKS + i);
+    }
+  };
   auto fetch = [&](int tile) {
 #pragma unroll
+    for (int i = 0; i < BLOCKS; ++i)
+      if (blocks[i] < 0 || (int64_t)blocks[i] >= a.num_blocks) {
+        record_error(a.err, DEVERR_BLOCK_RANGE);
+        blocks[i] = 0;
+      }
+#pragma unroll
     for (int i = 0; i < STEPS; ++i) {
-      const int at = tid + i * kThreadsCC, key = at / CH, t = tile * kKeys + key;
+      const int at = tid + i * kThreadsCC, key = at / CH;
       kr[i] = vr[i] = make_float4(0.f, 0.f, 0.f, 0.f);   // past the end: zeros, whatever the pool holds
-      if (at < kKeys * CH && t < s.len) {
-        const int64_t prow = pool_row(a, table, t, g) * D;
+      if (at < kKeys * CH && tile * kKeys + key < s.len) {
+        const int64_t prow =
+            (((int64_t)(key < kBlockSize ? blocks[0] : blocks[1]) * a.num_kv_heads + g) * kBlockSize +
+             key % kBlockSize) * D;
         kr[i] = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.k_cache) + prow) + at % CH);
         vr[i] = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.v_cache) + prow) + at % CH);
       }
     }
+    ask_blocks(tile + ranks);
   };
   const int tiles = (s.len + kKeys - 1) / kKeys;
+  ask_blocks(rank);
   if (rank < tiles) fetch(rank);
   load_q<D>(a, s, g, group, row0, rows, sm.q);
 
@@ -190,13 +210,14 @@ __global__ void __launch_bounds__(kThreadsCC) tree_cc_kernel(const TreeArgs a) {
     if (!live) continue;
     float sc[4][4];
     scores<D>(sm.q + 4 * warp, sm.k, lane, sc);
+    const bool all = (tile + 1) * kKeys <= ctx;   // every row sees every key
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float mx = -INFINITY;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int t = tile * kKeys + (lane & 7) + 8 * j;
-        sc[i][j] = t < s.len && seen(t, ctx, bits[i]) ? sc[i][j] * sl2 : -INFINITY;
+        sc[i][j] = all || (t < s.len && seen(t, ctx, bits[i])) ? sc[i][j] * sl2 : -INFINITY;
         mx = fmaxf(mx, sc[i][j]);
       }
 #pragma unroll
