@@ -59,14 +59,14 @@ __device__ __forceinline__ uint64_t tree_bits(const TreeArgs& a, const TreeSeq& 
 // head, 256 rows), cut into tiles of 128 keys.  The tiles of the batch, in
 // order, are shared out to one persistent CTA per SM, and what a CTA gets of a
 // stream is an item.  Where a CTA gets many tiles, shares are of equal weight:
-// a tile of more than 128 rows takes 1.4 times one of fewer (3,500 cycles
-// against 2,500 of the attention), so 3 against 2 units, and a tile belongs
-// to the CTA in whose units it starts; a stream's last tile is followed by 6 or
-// 10 units for its start and end (7,000 and 13,000 cycles).  (Equal numbers of tiles: 231 us for 32 ragged
-// sequences of 1 to 64 drafted tokens, against 170.)  Where a CTA gets a
-// few tiles, every tile counts alike.  One warp of every CTA works the
-// plan out from the lengths, 32 sequences at a time, so no shared memory grows
-// with the batch.
+// 3 units for a tile of more than 128 rows, 2 for one of fewer, a tile with the
+// CTA in whose units it starts; a stream's last tile is followed by 10 or 6
+// units for its start and end (13,000 and 7,000 cycles).  For 32 ragged
+// sequences of 1 to 64 drafted tokens that took 60 us off the 231 of equal
+// numbers of tiles (6 and 5 units, nearer to a tile's 3,300 and 2,700 cycles
+// alone: 1.5% slower).  Where a CTA gets a few tiles, every tile counts alike.
+// One warp of every CTA works the plan out from the lengths, 32 sequences at a
+// time, so no shared memory grows with the batch.
 constexpr int kTreeTile = 128;      // keys of a tile
 constexpr int kTreeRows = 256;      // rows of a stream
 constexpr int kTreeMaxCtas = 160;
