@@ -535,14 +535,14 @@ typedef struct pkv_tree_args {
   const void *k_cache;         /* pools [num_blocks][num_kv_heads][block_size][head_dim], read */
   const void *v_cache;         /* attention only */
   const int32_t *block_table;  /* [num_seqs][max_blocks_per_seq] */
-  const int32_t *seq_lens;     /* [num_seqs]; 1 .. max_seq_len where n_b > 0, else not read into */
-                               /* anything */
+  const int32_t *seq_lens;     /* [num_seqs]; n_b .. max_seq_len where n_b > 0, else not used */
   const int32_t *draft_offsets; /* [num_seqs + 1], not decreasing, within 0 .. num_rows */
   const int64_t *tree_mask;    /* [num_rows] or NULL */
   float *weights;              /* add_weights only: [num_seqs][num_kv_heads][weights_len], */
                                /* device, read and written */
-  void *workspace;             /* attention only: pkv_tree_workspace_bytes, 256-byte aligned; */
-                               /* holds nothing between calls and needs no clearing */
+  void *workspace;             /* attention in bf16 only: pkv_tree_workspace_bytes, 256-byte */
+                               /* aligned; holds nothing between calls and needs no clearing; */
+                               /* calls that overlap on the GPU need one each */
   size_t workspace_bytes;
   int64_t weights_len;         /* >= max_seq_len */
   int64_t num_blocks;

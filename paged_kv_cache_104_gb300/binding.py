@@ -663,7 +663,8 @@ def paged_tree_attention(out, q, k_cache, v_cache, block_table, seq_lens, draft_
     int32 [B, max_blocks].  Each sees the tokens before the drafted ones, and
     drafted token j if bit j of its tree_mask entry is set (int64 [N]; None: a
     chain, itself and the ones before).  lse fp32 [N, Hq] (optional) gets the
-    logarithm of each row's softmax sum.  workspace from ``tree_workspace``."""
+    logarithm of each row's softmax sum.  workspace from ``tree_workspace``
+    (bf16; calls that overlap on the GPU need one each)."""
     fn = "pkv_paged_tree_attention"
     _tree_call(fn, load().pkv_paged_tree_attention_packed, out, lse, q, k_cache, v_cache, block_table, seq_lens,
                draft_offsets, tree_mask, None, max_seq_len, max_draft, scale, workspace,

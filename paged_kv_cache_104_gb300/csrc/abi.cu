@@ -890,6 +890,7 @@ pkv_status tree_prepare(const pkv_tree_args* x, bool attention, pkv::TreeArgs* o
   const int64_t chunks = ((int64_t)x->max_draft * (x->num_q_heads / x->num_kv_heads) + 31) / 32;
   if ((int64_t)x->num_seqs * x->num_kv_heads * (tiles * chunks + 2 * chunks + 16) >= (int64_t)INT_MAX)
     return PKV_ERANGE;
+  if ((int64_t)x->num_rows * x->num_q_heads >= (int64_t)INT_MAX) return PKV_ERANGE;
   int* err = nullptr;
   st = device_state(&err, sms);
   if (st != PKV_OK) return st;

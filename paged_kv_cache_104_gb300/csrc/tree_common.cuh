@@ -187,6 +187,10 @@ struct TreePlan {
     it.n = it.slot = it.pieces = 0;
     while (pos < end) {
       while (pos >= start + sum) {
+        if (w + 1 >= windows) {        // lengths that changed meanwhile: end here
+          pos = end;
+          return it;
+        }
         start += sum;
         open(w + 1);
       }

@@ -238,12 +238,11 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
     if (warp == W_PLAN) {
       // ---------------------------------------------------------------- plan and queries
-            MergeDesc d{};
+      MergeDesc d{};
       int made = 0, loaded = 0;        // items handed out; queries asked for
       bool last = false;
       TreeItem it;
-      const long long t0 = clock64();
-      long long since = t0;
+      long long since = clock64();
       while (!last || loaded < made - 1) {
         bool moved = false;
         if (!last && (made < NI || __all_sync(0xffffffffu, mbar_try_wait(bar(TB_IE + made % NI), ((made / NI) - 1) & 1)))) {
@@ -277,7 +276,7 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
         }
         const long long now = clock64();
         if (moved) since = now;
-        if (*abort_flag || now - since > kWaitLimitCycles) {
+        if (__any_sync(0xffffffffu, *abort_flag || now - since > kWaitLimitCycles)) {
           if (!*abort_flag) record_error(a.err, DEVERR_TIMEOUT);
           *abort_flag = 1;
           break;

@@ -131,7 +131,7 @@ weights_mma_kernel(const __grid_constant__ WeightParams p, const __grid_constant
 
   if (warp == W_PLAN) {
     // ------------------------------------------------------------------ plan, queries
-        int made = 0, loaded = 0;        // passes handed out; queries asked for
+    int made = 0, loaded = 0;        // passes handed out; queries asked for
     bool last = false;
     TreeItem it;
     it.rows = 0;
@@ -192,7 +192,7 @@ weights_mma_kernel(const __grid_constant__ WeightParams p, const __grid_constant
       }
       const long long now = clock64();
       if (moved) since = now;
-      if (*abort_flag || now - since > kWaitLimitCycles) {
+      if (__any_sync(0xffffffffu, *abort_flag || now - since > kWaitLimitCycles)) {
         if (!*abort_flag) record_error(a.err, DEVERR_TIMEOUT);
         *abort_flag = 1;
         break;
