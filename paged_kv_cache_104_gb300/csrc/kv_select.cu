@@ -18,8 +18,10 @@
 // are ranked by comparing each with all, which for 2,301 tokens is mostly after
 // the first pass.  Beyond 8,192 tokens a cluster of up to eight CTAs shares a
 // (sequence, KV head), adding its histograms up in the first one's shared memory
-// (16.4 us for 8 sequences of 32,001).  Bounds over 65,536 take one CTA that
-// reads the weights once a pass.
+// (16.4 us for 8 sequences of 32,001).  Where the bound passes the shared memory
+// of eight, at 65,536 tokens, a cluster of eight reads its weights anew for every
+// pass: 62 us at 65,537 for 64 (sequence, KV head)s, against 33 at 65,536, and 81
+// at 131,072, where one CTA took 438.
 #include <climits>
 
 #include <cooperative_groups.h>
@@ -39,28 +41,6 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   if (x != x) return 0;
   const uint32_t u = __float_as_uint(x == 0.f ? 0.f : x);
   return u >> 31 ? ~u : u | 0x80000000u;
-}
-
-// Inclusive prefix sums over the CTA's threads, and the total.
-template <int THREADS>
-__device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* warp_sums, uint32_t& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  __syncthreads();
-  if (lane == 31) warp_sums[warp] = x;
-  __syncthreads();
-  uint32_t before = 0;
-  total = 0;
-#pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) {
-    if (w < warp) before += warp_sums[w];
-    total += warp_sums[w];
-  }
-  return before + x;
 }
 
 // The head of either kernel: the sequence's length, kept_lens, and the trivial
@@ -280,61 +260,124 @@ __global__ void __launch_bounds__(THREADS, 1536 / THREADS) select_smem_kernel(co
   }
 }
 
-// Any length: the weights are read once a pass, and once more.
+// Any length: a cluster per (sequence, KV head), whose CTAs read their share of
+// the weights once a pass, mostly from the L2, and twice more.
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a) {
-  __shared__ uint32_t bins[256];
-  __shared__ uint32_t warp_sums[kSelThreads / 32];
-  __shared__ uint32_t found[2];
-  const int tid = threadIdx.x;
+  __shared__ __align__(16) uint32_t bins[kBins];
+  __shared__ uint32_t warp_sums[2][32];
+  __shared__ uint32_t found[2];                          // digit, how many of it stay
+  __shared__ uint32_t counts[8][2];                      // per CTA: tokens that stay for sure, ties
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = cluster.block_rank(), ranks = cluster.num_blocks(), tid = threadIdx.x;
+  const int item = blockIdx.x / ranks;
+  const float* w = a.weights + (int64_t)item * a.weights_len;
   int n;
-  if (!select_begin(a, blockIdx.x, tid, kSelThreads, &n)) return;
-  int32_t* kept = a.kept + (int64_t)blockIdx.x * a.budget;
-  const float* w = a.weights + (int64_t)blockIdx.x * a.weights_len;
+  if (!select_begin(a, item, rank * kSelThreads + tid, ranks * kSelThreads, &n)) return;
+  const int span = (n + ranks - 1) / ranks, begin = min(rank * span, n), end = min(begin + span, n);
   const int lo = a.sinks, hi = n - a.recent;             // the tokens to choose from
-  uint32_t want = a.budget - a.sinks - a.recent;         // and how many; < hi - lo
-  uint32_t prefix = 0;
-  for (int shift = 24; want > 0 && shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256; i += kSelThreads) bins[i] = 0;
-    __syncthreads();
-    for (int t = lo + tid; t < hi; t += kSelThreads) {
-      const uint32_t key = order_key(w[t]);
-      if (shift == 24 || key >> (shift + 8) == prefix >> (shift + 8)) atomicAdd(&bins[key >> shift & 255], 1);
+  const int lo0 = max(lo, begin), hi0 = min(hi, end);
+  uint32_t want = a.budget - a.sinks - a.recent;         // and how many, which are fewer
+  const bool any = want > 0;
+  auto clear = [&] {
+    for (int i = tid; i < kBins; i += kSelThreads) bins[i] = 0;
+  };
+  clear();
+  cluster.sync();
+  uint32_t prefix = 0, above = 0;                        // the digits so far, and their bits
+#pragma unroll 1
+  for (int pass = 0; pass < 3 && any; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const uint32_t mask = pass == 2 ? 1023 : 2047;
+#pragma unroll 8
+    for (int t = lo0 + tid; t < hi0; t += kSelThreads) {
+      const uint32_t key = order_key(__ldg(w + t));
+      if (((key ^ prefix) & above) == 0) atomicAdd(&bins[key >> shift & mask], 1u);
     }
     __syncthreads();
-    if (tid == 0) {
-      uint32_t left = want;
-      int bin = 255;
-      while (bin > 0 && bins[bin] < left) left -= bins[bin--];
-      found[0] = bin;
-      found[1] = left;
+    if (rank > 0) {
+      uint32_t* sum = cluster.map_shared_rank(bins, 0);
+      for (int i = tid; i < kBins; i += kSelThreads)
+        if (bins[i]) atomicAdd(sum + i, bins[i]);
     }
-    __syncthreads();
+    cluster.sync();
+    if (rank == 0) {
+      uint32_t total;
+      const int top = kBins - 1 - 2 * tid;               // two bins a thread, from the highest down
+      const uint32_t x = bins[top], y = bins[top - 1];
+      const uint32_t before = scan_before<kSelThreads>(x + y, warp_sums[0], total);
+      if (before < want && before + x + y >= want) {
+        const bool second = before + x < want;
+        for (int k = 0; k < ranks; ++k) {
+          uint32_t* f = cluster.map_shared_rank(found, k);
+          f[0] = top - second;
+          f[1] = want - before - (second ? x : 0);
+        }
+      }
+      __syncthreads();
+    }
+    clear();
+    cluster.sync();
     prefix |= found[0] << shift;
+    above |= mask << shift;
     want = found[1];
-    __syncthreads();
   }
-  // keys above `prefix` stay, and the first `want` tokens that have it
-  const bool any = a.budget > a.sinks + a.recent;
-  uint32_t equal_before = 0, kept_before = 0, total;
-  for (int base = 0; base < n; base += kSelThreads) {
-    const int t = base + tid;
-    const bool mid = t >= lo && t < hi;
-    const uint32_t key = mid ? order_key(w[t]) : 0;
-    const bool equal = any && mid && key == prefix;
-    const uint32_t rank = equal_before + block_scan<kSelThreads>(equal, warp_sums, total);
-    equal_before += total;
-    const bool stays = t < n && (!mid || (any && key > prefix) || (equal && rank <= want));
-    const uint32_t at = kept_before + block_scan<kSelThreads>(stays, warp_sums, total);
-    kept_before += total;
-    if (stays) kept[at - 1] = t;
+  // Keys above `prefix` stay, and the first `want` tokens that have it.
+  auto look = [&](int t, uint32_t& sure, uint32_t& tie) {
+    const bool mid = any && t >= lo && t < hi;
+    const uint32_t key = mid ? order_key(__ldg(w + t)) : 0;
+    sure = t < lo || t >= hi || (mid && key > prefix);
+    tie = mid && key == prefix;
+  };
+  uint32_t sure_at = 0, ties_at = 0, total;
+#pragma unroll 8
+  for (int t = begin + tid; t < end; t += kSelThreads) {
+    uint32_t sure, tie;
+    look(t, sure, tie);
+    sure_at += sure;
+    ties_at += tie;
+  }
+  scan_before<kSelThreads>(sure_at, warp_sums[0], total);
+  if (tid < ranks) cluster.map_shared_rank(&counts[0][0], tid)[2 * rank] = total;
+  scan_before<kSelThreads>(ties_at, warp_sums[1], total);
+  if (tid < ranks) cluster.map_shared_rank(&counts[0][0], tid)[2 * rank + 1] = total;
+  cluster.sync();                                        // the last access to another's shared memory
+  sure_at = ties_at = 0;                                 // of the tokens before
+  for (int k = 0; k < rank; ++k) {
+    sure_at += counts[k][0];
+    ties_at += counts[k][1];
+  }
+  int32_t* kept = a.kept + (int64_t)item * a.budget;
+  int turn = 0;
+  for (int t0 = begin; t0 < end; t0 += 8 * kSelThreads, turn ^= 1) {
+    uint32_t sure = 0, ties = 0;                         // of this thread's eight tokens
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int t = t0 + 8 * tid + i;
+      uint32_t x = 0, y = 0;
+      if (t < end) look(t, x, y);
+      sure |= x << i;
+      ties |= y << i;
+    }
+    const uint32_t before =
+        scan_before<kSelThreads>(__popc(sure) | __popc(ties) << 16, warp_sums[turn], total);
+    uint32_t to = sure_at + (before & 0xffff), tie = ties_at + (before >> 16);
+    for (uint32_t left = sure | ties; left; left &= left - 1) {
+      const int i = __ffs(left) - 1;
+      const bool is_tie = ties >> i & 1;
+      if (!is_tie || tie < want) kept[to + min(tie, want)] = t0 + 8 * tid + i;
+      to += !is_tie;
+      tie += is_tie;
+    }
+    sure_at += total & 0xffff;
+    ties_at += total >> 16;
   }
 }
 
-template <int THREADS>
-cudaError_t launch_smem(const SelectArgs& a, int ranks, cudaStream_t stream) {
+cudaError_t launch_clusters(void (*kernel)(SelectArgs), int threads, const SelectArgs& a, int ranks,
+                            cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.num_seqs * a.num_kv_heads * ranks));
-  cfg.blockDim = dim3(THREADS);
+  cfg.blockDim = dim3(threads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -342,19 +385,18 @@ cudaError_t launch_smem(const SelectArgs& a, int ranks, cudaStream_t stream) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, select_smem_kernel<THREADS>, a);
+  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_select(const SelectArgs& a, cudaStream_t stream) {
   const int tokens = a.max_seq_len;
-  if (tokens <= 64 * kPerThread) return launch_smem<64>(a, 1, stream);
-  if (tokens <= 256 * kPerThread) return launch_smem<256>(a, 1, stream);
+  if (tokens <= 64 * kPerThread) return launch_clusters(select_smem_kernel<64>, 64, a, 1, stream);
+  if (tokens <= 256 * kPerThread) return launch_clusters(select_smem_kernel<256>, 256, a, 1, stream);
   for (int ranks = 1; ranks <= 8; ranks *= 2)
-    if (tokens <= 512 * kPerThread * ranks) return launch_smem<512>(a, ranks, stream);
-  select_kernel<<<a.num_seqs * a.num_kv_heads, kSelThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+    if (tokens <= 512 * kPerThread * ranks) return launch_clusters(select_smem_kernel<512>, 512, a, ranks, stream);
+  return launch_clusters(select_kernel, kSelThreads, a, 8, stream);
 }
 
 }  // namespace pkv

@@ -133,3 +133,31 @@ def test_captured_and_replayed():
     torch.cuda.synchronize()
     ref = T.select(w.cpu(), [3000, 700], 500, 4, 50)
     assert kept.cpu().tolist() == ref
+
+
+# a bound over 65,536 takes the kernel for any length, whatever the lengths are
+@pytest.mark.parametrize("budget,sinks,recent", [(1, 0, 0), (7, 3, 4), (64, 0, 30), (1000, 4, 100)])
+def test_any_length(budget, sinks, recent):
+    lens = [65537, 0, 1, 8, 9, 63, 64, 65, 1001, 8191, 8193, 66000]
+    check(tailed(len(lens), 2, 66001, 8), lens, budget, sinks, recent, max_len=66001)
+
+
+@pytest.mark.parametrize("values", [[0.0], [0.0, -0.0], [1.0, math.inf, -math.inf], [0.0, math.nan], [math.nan],
+                                    [1e-45, 0.0, -1e-45], [3.4e38, 3.3e38, math.inf]])
+def test_any_length_ties_and_odd_numbers(values):
+    g = torch.Generator().manual_seed(11)
+    w = torch.tensor(values)[torch.randint(0, len(values), (2, 2, 70003), generator=g)]
+    for budget in (1, 20000, 70002):
+        check(w, [70003, 20001], budget, 0, 0)
+
+
+def test_any_length_equal_in_the_leading_bits():
+    base = torch.tensor(1.5).view(torch.int32)
+    g = torch.Generator().manual_seed(12)
+    for span in (2, 200, 70000, 1 << 22):
+        w = (base + torch.randint(0, span, (2, 1, 131071), generator=g, dtype=torch.int32)).view(torch.float32)
+        check(w, [131071, 100000], 30001, 2, 30)
+
+
+def test_a_million_tokens():
+    check(tailed(1, 1, 1048577, 13), [1048577], 5000, 4, 64)
