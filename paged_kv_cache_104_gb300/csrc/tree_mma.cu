@@ -7,7 +7,12 @@
 //
 // What bounds it: every stored key and value is read once for all rows of its
 // sequence, 512 B for 512 R multiply-adds (R rows of a KV head), so up to about
-// R = 256 rows (64 drafted tokens of a group of 4) HBM is the bound.
+// R = 256 rows (64 drafted tokens of a group of 4) HBM is the bound.  Measured,
+// 32 query and 8 KV heads, with the merge: 64 sequences of 2,301 with 16 drafted
+// tokens 106 us (5.8 TB/s, 86% of a plain copy's rate), 8 of 32,001 with 64 drafted
+// 200 us (5.3 TB/s and 1,340 TFLOP/s: the tensor pipe is busy 65% of the time, the
+// rest is softmax between a side's two products, as tensor memory holds one S for
+// each side), one of 777 with 8 drafted 10.4 us (latency).
 //
 // Work.  A stream is one (sequence, KV head, 256 rows), cut into tiles of 128
 // keys; the tiles of the whole batch are shared out equally to one persistent
