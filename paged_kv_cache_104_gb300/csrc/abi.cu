@@ -866,7 +866,7 @@ pkv_status tree_prepare(const pkv_tree_args* x, bool attention, pkv::TreeArgs* o
     return PKV_EINVAL;
   if (x->max_draft > PKV_MAX_DRAFT) return PKV_EUNSUPPORTED;
   if (x->num_seqs == 0 || x->num_rows == 0) return PKV_OK;
-  if (x->num_seqs > PKV_MAX_SEQS) return PKV_ERANGE;
+  if (x->num_seqs > PKV_MAX_SEQS || x->max_seq_len > INT_MAX - 65536) return PKV_ERANGE;
   if ((int64_t)x->max_seq_len > (int64_t)x->max_blocks_per_seq * x->block_size) return PKV_EINVAL;
   if (!isfinite(x->scale) || !(x->scale > 0.f)) return PKV_EINVAL;
   if (!x->q || !x->k_cache || !x->block_table || !x->seq_lens || !x->draft_offsets) return PKV_EINVAL;

@@ -214,3 +214,104 @@ def test_debug_mode_lets_good_calls_pass():
     finally:
         B.set_debug(False)
     check(x, out, lse)
+
+
+def test_rows_before_the_first_sequence():
+    """draft_offsets that do not start at 0: q's rows before them are nobody's."""
+    x = Batch([200, 33, 90], [5, 0, 17], 8, 2, seed=11)
+    t = on(x)
+    want = attend(x, t)
+    pad = torch.zeros((3, 8, 128), dtype=BF16, device=D)
+    out, lse = torch.full((x.rows + 3, 8, 128), 7.0, dtype=BF16, device=D), torch.full((x.rows + 3, 8), 7.0, device=D)
+    B.paged_tree_attention(out, torch.cat([pad, t[0]]), *t[1:5], t[5] + 3, torch.cat([t[6][:3], t[6]]), x.max_len,
+                           x.max_draft, x.scale, B.tree_workspace(8, 2, 128, x.max_draft, x.max_len), lse)
+    assert B.get_device_error() == 0
+    assert bool((out[:3] == 7).all()) and bool((lse[:3] == 7).all())
+    assert torch.equal(out[3:], want[0]) and torch.equal(lse[3:], want[1])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_bounds_above_the_batch(dtype):
+    """max_seq_len and max_draft are bounds: larger ones change nothing but rounding."""
+    x = Batch([700, 2, 90], [5, 2, 1], 8, 2, dtype=dtype, seed=12)
+    x.table = torch.cat([x.table, torch.full((3, 500), -1, dtype=torch.int32)], 1)
+    x.max_len, x.max_draft = x.table.shape[1] * 16, 64
+    t = on(x)
+    out, lse = attend(x, t)
+    assert B.get_device_error() == 0
+    check(x, out, lse)
+    w = torch.zeros((3, 2, x.max_len), device=D)
+    B.kv_add_weights(w, t[0], t[1], *t[3:6], t[6], lse, x.max_len, 64, x.scale)
+    assert B.get_device_error() == 0
+    rows = torch.tensor([20.0, 8.0, 4.0])
+    assert float((w.cpu().sum(2) - rows[:, None]).abs().max()) < 1e-4
+    assert bool((w[1, :, 2:] == 0).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_a_replayed_graph_follows_what_its_tensors_hold(dtype):
+    """One capture; then other lengths, other numbers of drafted tokens, other
+    trees and blocks in the same tensors."""
+    first = Batch([900, 40, 64, 0], [12, 3, 64, 0], 8, 2, dtype=dtype, seed=13)
+    t = on(first)
+    ws = B.tree_workspace(8, 2, 128, 64, 900)
+    width = t[3].shape[1]
+    out, lse, w = torch.zeros_like(t[0]), torch.zeros((first.rows, 8), device=D), torch.zeros((4, 2, 900), device=D)
+
+    def both():
+        B.paged_tree_attention(out, *t, 900, 64, first.scale, ws, lse)
+        B.kv_add_weights(w, t[0], t[1], *t[3:6], t[6], lse, 900, 64, first.scale)
+
+    both()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        both()
+    for seed, lens, drafted in ((14, [33, 700, 1, 200], [2, 40, 1, 11]), (15, [0, 0, 0, 1], [0, 0, 0, 1]),
+                                (16, [64, 64, 64, 64], [0, 0, 64, 15])):
+        x = Batch(lens, drafted, 8, 2, dtype=dtype, seed=seed)
+        assert x.num_blocks <= first.num_blocks and x.rows <= first.rows
+        t[0][:x.rows] = x.q.to(D)
+        t[1][:x.num_blocks], t[2][:x.num_blocks] = torch.nan_to_num(x.k).to(D), torch.nan_to_num(x.v).to(D)
+        t[3].zero_()
+        t[3][:, :min(width, x.table.shape[1])] = x.table[:, :width].to(D)
+        t[4].copy_(x.lens)
+        t[5].copy_(x.offsets)
+        t[6][:x.rows] = x.mask.to(D)
+        w.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert B.get_device_error() == 0
+        check(x, out[:x.rows], lse[:x.rows])
+        rows = torch.tensor([4.0 * n for n in drafted])
+        assert float((w.cpu().sum(2) - rows[:, None]).abs().max()) < 1e-4
+
+
+def test_compaction_by_a_replayed_graph_whose_lists_change():
+    g = torch.Generator().manual_seed(17)
+    k, v = (torch.randn((80, 2, 16, 128), generator=g).bfloat16() for _ in "kv")
+    table = torch.randperm(80, generator=g).to(torch.int32).view(2, 40)
+    w = torch.rand((2, 2, 640), generator=g)
+    dk, dv, dw, dt = k.to(D), v.to(D), w.to(D), table.to(D)
+    lens = torch.tensor([640, 500], dtype=torch.int32, device=D)
+    kept, n = torch.zeros((2, 2, 200), dtype=torch.int32, device=D), torch.zeros(2, dtype=torch.int32, device=D)
+
+    def both():
+        B.kv_select(kept, n, dw, lens, 640, 4, 30)
+        B.kv_compact(dk, dv, dt, lens, kept, n, None, dw)
+
+    lens.zero_()
+    both()                                                 # nothing stored: nothing moves
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        both()
+    for now in ([640, 500], [201, 199], [0, 300]):
+        lens.copy_(torch.tensor(now, dtype=torch.int32))
+        k, v, w = dk.cpu(), dv.cpu(), dw.cpu()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert B.get_device_error() == 0
+        ref = T.select(w, now, 200, 4, 30)
+        assert n.tolist() == [min(x, 200) for x in now]
+        assert all(kept[b, h, :len(ref[b][h])].tolist() == ref[b][h] for b in range(2) for h in range(2))
+        exp = T.compact(k, v, w, table, now, kept.cpu(), n.tolist(), None)
+        assert all(torch.equal(a.cpu(), e) for a, e in zip((dk, dv, dw), exp))

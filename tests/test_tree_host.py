@@ -34,6 +34,7 @@ SHARED = [
     (dict(q=0x1008), 1), (dict(k_cache=0x1008), 1), (dict(block_table=0x1002), 1), (dict(seq_lens=0x1001), 1),
     (dict(draft_offsets=0x1002), 1), (dict(tree_mask=0x1004), 1), (dict(lse=0x1002), 1),
     (dict(num_seqs=8192, max_blocks_per_seq=1 << 20, max_seq_len=1 << 24, weights_len=1 << 24), 3),
+    (dict(num_seqs=1, max_blocks_per_seq=1 << 27, max_seq_len=2 ** 31 - 1, weights_len=1 << 31), 3),
     (dict(num_rows=2 ** 31 - 1), 3), (dict(num_seqs=0), 0), (dict(num_rows=0), 0)]
 
 
