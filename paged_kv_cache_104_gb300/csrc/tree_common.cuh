@@ -56,7 +56,8 @@ __device__ __forceinline__ uint64_t tree_bits(const TreeArgs& a, const TreeSeq& 
 // ---- the balanced plan of the tensor-core kernels
 //
 // A stream is one (sequence, KV head), or with row tiles one (sequence, KV
-// head, 256 rows), cut into tiles of 128 keys.  The tiles of the batch, in
+// head, 256 rows), or a pair of KV heads of up to 128 rows each, cut into tiles of
+// 128 keys.  The tiles of the batch, in
 // order, are shared out to one persistent CTA per SM, and what a CTA gets of a
 // stream is an item.  Where a CTA gets many tiles, shares are of equal weight:
 // 3 units for a tile of more than 128 rows, 2 for one of fewer, a tile with the
@@ -65,17 +66,26 @@ __device__ __forceinline__ uint64_t tree_bits(const TreeArgs& a, const TreeSeq& 
 // sequences of 1 to 64 drafted tokens that took 60 us off the 231 of equal
 // numbers of tiles (6 and 5 units, nearer to a tile's 3,300 and 2,700 cycles
 // alone: 1.5% slower).  Where a CTA gets a few tiles, every tile counts alike.
+// Pairs save starts and ends and cut the batch more coarsely, so sequences of up
+// to eight tiles go in pairs where there is work for all CTAs: 126 of 27 to 609
+// tokens 65.4 -> 55.3 us (57.0 with pairs up to four tiles only), 112 of 1 to 5
+// 33.3 -> 22.6; pairs of any length made 64 of 2,301 5% slower, 105.7 -> 111.2, and
+// these leave 32 ragged ones, few of them paired, at 154 instead of 150.
 // One warp of every CTA works the plan out from the lengths, 32 sequences at a
 // time, so no shared memory grows with the batch.
 constexpr int kTreeTile = 128;      // keys of a tile
 constexpr int kTreeRows = 256;      // rows of a stream
 constexpr int kTreeMaxCtas = 160;
 constexpr int kTreeManyTiles = 8;   // a CTA, from where on tiles are weighted
+constexpr int kTreePairTiles = 2;   // ... and from where on KV heads go in pairs
+constexpr int kTwinTiles = 8;       // ... of sequences of at most so many tiles
+constexpr int kTwinEnds = 8;        // units for the start and end of a pair (4 or 12: up to 3% slower)
 
 struct TreeItem {
   int n;          // tiles; 0: no more items
   int t0;         // first tile
-  int b, g;
+  int b, g;       // sequence, (first) KV head
+  int heads;      // 2: a pair of KV heads, of `rows` rows each
   int row0;       // first row (drafted token * group + query head) of the stream
   int rows;       // rows of the stream, 1 .. 256 (without row tiles: of the sequence)
   int q_tok;      // q's row of the sequence's first drafted token
@@ -84,12 +94,12 @@ struct TreeItem {
   int pieces;     // of the stream, where this is the first of several (else 0)
 };
 
-template <bool ROW_TILES>
+template <bool ROW_TILES, bool PAIRS = false>
 struct TreePlan {
   const TreeArgs& a;
   const int lane, group;
   int windows, w = -1;                 // windows of 32 sequences, the loaded one
-  bool weighted = false;
+  bool weighted = false, paired = false;
   int share = 0, longer = 0;           // units of a CTA; the first `longer` CTAs have one more
   int pos = 0, end = 0;                // this CTA's next unit and end
   int start = 0, sum = 0;              // the window's first unit, its units
@@ -111,13 +121,23 @@ struct TreePlan {
     if (!ROW_TILES) return stream_units(nt, rows, heavy);
     return rows / kTreeRows * stream_units(nt, kTreeRows, heavy) + stream_units(nt, rows % kTreeRows, heavy);
   }
+  // Two KV heads of a sequence of nt tiles are one stream?
+  __device__ bool twin(int nt, int rows, bool pairs) const {
+    return PAIRS && pairs && rows <= kTreeRows / 2 && nt <= kTwinTiles;
+  }
+  __device__ int twin_units(int nt, bool heavy) const { return heavy ? 4 * nt + kTwinEnds : nt; }
+  // ... and of all of a sequence's streams.
+  __device__ int seq_units(int nt, int rows, bool heavy, bool pairs) const {
+    if (twin(nt, rows, pairs)) return rows > 0 ? twin_units(nt, heavy) * (a.num_kv_heads >> 1) : 0;
+    return head_units(nt, rows, heavy) * a.num_kv_heads;
+  }
   // For one warp (active), while the others still set the CTA up.
   __device__ TreePlan(const TreeArgs& args, bool active)
       : a(args), lane(threadIdx.x & 31), group(args.num_q_heads / args.num_kv_heads),
         windows((args.num_seqs + 31) / 32) {
     if (!active) return;
     const bool report = blockIdx.x == 0;
-    int plain = 0, heavy = 0;
+    int plain = 0, twins = 0, heavy = 0;
     // four windows' lengths are asked for before the first is looked at, the
     // first window last, as the walk often starts there
     for (int i = (windows - 1) / 4; i >= 0; --i) {
@@ -129,16 +149,16 @@ struct TreePlan {
         const int b = 32 * (4 * i + j) + lane;
         seq = tree_seq_check(a, s[j], report && b < a.num_seqs);
         tiles = seq.drafted > 0 ? (seq.len + kTreeTile - 1) / kTreeTile : 0;
-        plain += head_units(tiles, seq.drafted * group, false);
-        heavy += head_units(tiles, seq.drafted * group, true);
+        plain += seq_units(tiles, seq.drafted * group, false, false);
+        if (PAIRS) twins += seq_units(tiles, seq.drafted * group, false, true);
+        heavy += seq_units(tiles, seq.drafted * group, true, PAIRS);
       }
     }
     w = 0;
-    int total = __reduce_add_sync(0xffffffffu, plain * a.num_kv_heads);
-    if (total >= kTreeManyTiles * (int)gridDim.x) {
-      weighted = true;
-      total = __reduce_add_sync(0xffffffffu, heavy * a.num_kv_heads);
-    }
+    int total = __reduce_add_sync(0xffffffffu, plain);
+    weighted = total >= kTreeManyTiles * (int)gridDim.x;
+    paired = PAIRS && total >= kTreePairTiles * (int)gridDim.x;
+    if (weighted || paired) total = __reduce_add_sync(0xffffffffu, weighted ? heavy : twins);
     // (a kernel starts with none of its code in the SM: every few instructions
     // before the first item cost a fetch, so there is one division here)
     share = total / gridDim.x;
@@ -162,7 +182,7 @@ struct TreePlan {
       seq = tree_seq_check(a, fetch(i), false);
       tiles = seq.drafted > 0 ? (seq.len + kTreeTile - 1) / kTreeTile : 0;
     }
-    units = head_units(tiles, seq.drafted * group, weighted) * a.num_kv_heads;
+    units = seq_units(tiles, seq.drafted * group, weighted, paired);
     int x = units;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -179,7 +199,7 @@ struct TreePlan {
   }
   // Tiles that start in so many units of a stream.
   __device__ int tiles_before(int n, int each) const {
-    return each == 1 ? n : each == 2 ? (n + 1) >> 1 : each == 3 ? (n + 2) / 3 : (n + each - 1) / each;
+    return each == 1 ? n : each == 2 ? (n + 1) >> 1 : each == 4 ? (n + 3) >> 2 : (n + each - 1) / each;
   }
   // The CTA's next item (n = 0: none).  Every lane gets it.
   __device__ TreeItem next() {
@@ -197,9 +217,11 @@ struct TreePlan {
       const int l = __ffs(__ballot_sync(0xffffffffu, first <= pos && pos < first + units)) - 1;
       const int at = __shfl_sync(0xffffffffu, first, l), nt = __shfl_sync(0xffffffffu, tiles, l);
       const int drafted = __shfl_sync(0xffffffffu, seq.drafted, l), rows = drafted * group;
-      const int per_head = head_units(nt, rows, weighted);
+      const bool two = twin(nt, rows, paired);
+      const int per_head = two ? twin_units(nt, weighted) : head_units(nt, rows, weighted);
       int s0 = at;                                         // the stream's first unit
-      for (it.g = 0; pos - s0 >= per_head; ++it.g) s0 += per_head;
+      it.heads = two ? 2 : 1;
+      for (it.g = 0; pos - s0 >= per_head; it.g += it.heads) s0 += per_head;
       it.row0 = 0;
       it.rows = rows;
       if (ROW_TILES) {
@@ -211,7 +233,8 @@ struct TreePlan {
         }
         it.rows = min(it.rows, kTreeRows);
       }
-      const int each = weight(it.rows, weighted), s1 = s0 + stream_units(nt, it.rows, weighted);
+      const int each = two ? (weighted ? 4 : 1) : weight(it.rows, weighted);
+      const int s1 = s0 + (two ? per_head : stream_units(nt, it.rows, weighted));
       // tiles that start in this CTA's units
       it.t0 = tiles_before(pos - s0, each);
       it.n = min(tiles_before(min(s1, end) - s0, each), nt) - it.t0;

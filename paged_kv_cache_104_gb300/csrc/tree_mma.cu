@@ -25,8 +25,10 @@
 //   more than 128 rows: side s takes rows 128 s .. of every tile;
 //   up to 128 rows:     side s takes every other tile, and the two join at the
 //                       item's end through TMEM (thread r of either side can
-//                       read row r of both accumulators).
-// Either way the products alternate between the sides ("steps").
+//                       read row r of both accumulators);
+//   two KV heads:       short sequences of up to 128 rows go in pairs of KV heads,
+//                       one to a side, whose items start and end once for both.
+// Each way the products alternate between the sides ("steps").
 //
 // Roles (384 threads):
 //   warps 0-3 / 4-7  softmax of side 0 / 1: thread r owns row r (TMEM lane r);
@@ -72,7 +74,7 @@ constexpr int OFF_KV = 2 * Q_BYTES;
 constexpr int OFF_ML = OFF_KV + NS * TILE;    // [side][row] (max, sum) exchange
 constexpr int OFF_ITEM = OFF_ML + 2 * BM * 8;
 constexpr int OFF_BAD = OFF_ITEM + NI * 64;   // drafted tokens whose V was cleared, per item slot
-constexpr int OFF_BAR = OFF_BAD + NI * 8;
+constexpr int OFF_BAR = OFF_BAD + NI * 16;
 constexpr int kSoft = 256, kThreadsT = 384;
 constexpr int W_KV = 8, W_MMA = 9, W_FIX = 10, W_PLAN = 11;
 constexpr int kRegsSoft = 200, kRegsRest = 96;
@@ -106,12 +108,13 @@ static_assert(sizeof(TreeItem) <= 64, "an item's slot");
 struct MergeDesc {
   int pieces;      // 0: nothing to join
   int b, g, row0, rows, q_tok;
-  int pad[2];
+  int heads;       // 2: rows of KV head g, then of g + 1
+  int pad;
 };
 
 struct TreeMmaParams {
   TreeArgs a;
-  int q_bufs;                // 2: no stream has more than 128 rows
+  int q_bufs;                // 2: no item has more than 128 rows, or two KV heads
   MergeDesc* desc;           // [CTA]
   char* partials;            // [CTA][2] of piece_bytes: O [rows][128], then (max, sum) [rows]
   int64_t piece_bytes;
@@ -121,10 +124,11 @@ struct TreeMmaParams {
 
 // The order of an item's tiles in the ring, as the products need them: with
 // `both` K0 V0 K1 V1 .., else K0 K1 V0 K2 V1 K3 .. (side s's Q K^T of its next
-// tile is issued behind its P V of this one).
+// tile is issued behind its P V of this one).  A pair's tiles are numbered
+// alternately: 2 j + s is tile j of side s's KV head.
 struct Order {
   bool both;   // both sides take every tile
-  int n;
+  int n;       // tiles of K (and of V)
   __device__ int v(int j) const { return both ? 2 * j + 1 : (j < n - 1 ? 2 * j + 2 : 2 * n - 1); }
   __device__ int side_steps(int side) const { return both ? n : (n + 1 - side) >> 1; }
 };
@@ -143,8 +147,8 @@ __device__ __forceinline__ void store32(char* to, const uint32_t (&v)[8], bool w
 // Adds p V to the row's O (TMEM column o_col) for the drafted tokens `left`
 // whose values were cleared, p = 2^(scaled score - base) from q and k in
 // global memory.  The whole warp, each lane its row; not the usual path.
-__device__ __noinline__ void add_cleared(const TreeArgs& a, const TreeItem& it, unsigned long long left, float base,
-                                         uint32_t o_col, int out_row) {
+__device__ __noinline__ void add_cleared(const TreeArgs& a, const TreeItem& it, int g, unsigned long long left,
+                                         float base, uint32_t o_col, int out_row) {
   const unsigned long long any = __reduce_or_sync(0xffffffffu, (uint32_t)left) |
                                  (unsigned long long)__reduce_or_sync(0xffffffffu, (uint32_t)(left >> 32)) << 32;
   for (unsigned long long todo = any; todo; todo &= todo - 1) {
@@ -152,7 +156,7 @@ __device__ __noinline__ void add_cleared(const TreeArgs& a, const TreeItem& it, 
     const bool mine = left >> d & 1;
     int blk = __ldg(a.block_table + (int64_t)it.b * a.max_blocks_per_seq + pos / kBlockSize);
     if (blk < 0 || (int64_t)blk >= a.num_blocks) blk = 0;
-    const int64_t at = (((int64_t)blk * a.num_kv_heads + it.g) * kBlockSize + pos % kBlockSize) * HD;
+    const int64_t at = (((int64_t)blk * a.num_kv_heads + g) * kBlockSize + pos % kBlockSize) * HD;
     const __nv_bfloat16* kr = static_cast<const __nv_bfloat16*>(a.k_cache) + at;
     const __nv_bfloat16* vr = static_cast<const __nv_bfloat16*>(a.v_cache) + at;
     const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(a.q) + (int64_t)out_row * HD;
@@ -177,6 +181,7 @@ __device__ __noinline__ void add_cleared(const TreeArgs& a, const TreeItem& it, 
   }
 }
 
+template <bool PAIRS>
 __global__ void __launch_bounds__(kThreadsT, 1)
 tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__ CUtensorMap tm_q,
                 const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
@@ -215,7 +220,7 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
                  "r"(kTmemCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  TreePlan<true> plan(a, warp == W_PLAN);
+  TreePlan<true, PAIRS> plan(a, warp == W_PLAN);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -237,7 +242,7 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
   auto warp_wait = [&](int b, uint32_t parity) {
     return (bool)__all_sync(0xffffffffu, wait_fast(bar(b), parity, abort_flag, a.err));
   };
-  auto order_of = [&](const TreeItem& it) { return Order{it.rows > BM, it.n}; };
+  auto order_of = [&](const TreeItem& it) { return Order{it.rows > BM, PAIRS ? it.n * it.heads : it.n}; };
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
@@ -253,7 +258,7 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
         if (!last && (made < NI || __all_sync(0xffffffffu, mbar_try_wait(bar(TB_IE + made % NI), ((made / NI) - 1) & 1)))) {
           it = plan.next();
           last = it.n == 0;
-          if (it.pieces > 0) d = MergeDesc{it.pieces, it.b, it.g, it.row0, it.rows, it.q_tok, {0, 0}};
+          if (it.pieces > 0) d = MergeDesc{it.pieces, it.b, it.g, it.row0, it.rows, it.q_tok, it.heads, 0};
           if (lane == 0) *reinterpret_cast<TreeItem*>(smem + OFF_ITEM + (made % NI) * 64) = it;
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(TB_IF + made % NI));
@@ -267,12 +272,14 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
             // an item's slot is written again only once its queries were used
             const TreeItem x = *reinterpret_cast<const TreeItem*>(smem + OFF_ITEM + (loaded % NI) * 64);
             if (lane == 0) {
-              const int sides = x.rows > BM ? 2 : 1;
+              const bool pair = PAIRS && x.heads == 2;
+              const int sides = pair || x.rows > BM ? 2 : 1;
               mbar_arrive_expect_tx(bar(TB_QF + qb), sides * Q_BYTES);
               for (int s = 0; s < sides; ++s)
                 for (int h = 0; h < 2; ++h)
                   tma_load_3d(sbase + OFF_Q + (qb + s) * Q_BYTES + h * QHALF, &tm_q, bar(TB_QF + qb), 64 * h,
-                              x.g * group, x.q_tok + ((x.row0 + s * BM) >> log_group));
+                              (x.g + (pair ? s : 0)) * group,
+                              x.q_tok + ((x.row0 + (pair ? 0 : s * BM)) >> log_group));
             }
             __syncwarp();
             ++loaded;
@@ -324,8 +331,10 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
         };
         int window = it.t0 >> 2;
         int ids = ids_of(window), next_ids = ids_of(window + 1);
+        const bool both = it.rows > BM;
+        const int pair = PAIRS ? it.heads - 1 : 0, tiles = it.n << pair;
         auto load = [&](bool is_v, int j) {
-          const int t = it.t0 + j, slot = pos % NS;
+          const int t = it.t0 + (j >> pair), slot = pos % NS;
           if (pos >= NS) ok = warp_wait(TB_E + slot, ((pos / NS) - 1) & 1);
           if (!ok) return;
           if (is_v && (t >> 2) > window) {   // V follows K: nobody needs the older window
@@ -340,19 +349,18 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
           __syncwarp();
           if (lane < nb)
             tma_load_4d(sbase + OFF_KV + slot * TILE + lane * 2 * GROUP8, is_v ? &tm_v : &tm_k, full, 0, 0, 0,
-                        2 * (mine * a.num_kv_heads + it.g), policy);
+                        2 * (mine * a.num_kv_heads + it.g + (j & pair)), policy);
           history = history << 1 | (check ? 1u : 0u);
           checks += check;
           ++pos;
         };
-        const bool both = it.rows > BM;
         policy = (it.len - it.ctx) * group <= kTreeRows ? once : again;
         load(false, 0);
-        if (!both && it.n > 1 && ok) load(false, 1);
-        for (int j = 0; j < it.n && ok; ++j) {
+        if (!both && tiles > 1 && ok) load(false, 1);
+        for (int j = 0; j < tiles && ok; ++j) {
           load(true, j);
           const int kj = both ? j + 1 : j + 2;
-          if (kj < it.n && ok) load(false, kj);
+          if (kj < tiles && ok) load(false, kj);
         }
         item_done(k);
       }
@@ -404,13 +412,13 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
       };
       for (int k = 0; ok && item_at(k, it); ++k) {
         // the same in every lane, and known to be: descriptors stay in uniform registers
-        const int n = __shfl_sync(0xffffffffu, it.n, 0);
+        const int heads = PAIRS ? __shfl_sync(0xffffffffu, it.heads, 0) : 1, n = __shfl_sync(0xffffffffu, it.n, 0) * heads;
         const bool both = __shfl_sync(0xffffffffu, it.rows, 0) > BM;
         // 16-key products of the item's last tile; 8 in the others
         const int last_ks = __shfl_sync(0xffffffffu, (min(BN, it.len - (it.t0 + it.n - 1) * BN) + 15) / 16, 0);
         const int qb = k % p.q_bufs;
         ok = warp_wait(TB_QF + qb, (k / p.q_bufs) & 1);
-        const uint64_t q0 = q_desc + (uint32_t)(qb * (Q_BYTES >> 4)), q1 = q0 + (both ? Q_BYTES >> 4 : 0);
+        const uint64_t q0 = q_desc + (uint32_t)(qb * (Q_BYTES >> 4)), q1 = q0 + (both || heads == 2 ? Q_BYTES >> 4 : 0);
         tile_there(slot, par);
         qk(0, q0, slot);
         if (both) {
@@ -449,15 +457,17 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
             const int side = s & 1;
             if (s + 2 == max(n, 2) && ok) commit_e(bar(TB_QE + qb));
             tile_there(slot, par);
-            pv(side, slot, s < 2, s == n - 1 ? last_ks : 8);
+            pv(side, slot, s < 2, s >= n - heads ? last_ks : 8);
             step();
             if (s + 2 < n) {
               tile_there(slot, par);
-              qk(side, q0, slot);
+              qk(side, side ? q1 : q0, slot);
               step();
+            } else if (heads == 2 && ok) {
+              commit_e(bar(TB_OD + side));
             }
           }
-          if (ok) commit_e(bar(TB_OJ));
+          if (heads == 1 && ok) commit_e(bar(TB_OJ));
         }
         item_done(k);
       }
@@ -468,9 +478,10 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
       bool ok = true;
       for (int k = 0; ok && item_at(k, it); ++k) {
         const Order ord = order_of(it);
-        unsigned long long bad = 0;
-        for (int t = max(it.t0, it.ctx / BN); t < it.t0 + it.n; ++t) {
-          const int at = base + ord.v(t - it.t0);
+        const int pair = PAIRS ? it.heads - 1 : 0;
+        unsigned long long bad[2] = {0, 0};
+        for (int j = (max(it.t0, it.ctx / BN) - it.t0) << pair; j < it.n << pair; ++j) {
+          const int t = it.t0 + (j >> pair), at = base + ord.v(j);
           // (a barrier of its own: this warp does not follow every turn of the ring)
           ok = warp_wait(TB_CK + checks % NCK, (checks / NCK) & 1);
           ++checks;
@@ -497,17 +508,18 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
             const bool clear = lane < 16 ? (votes & 0xffffu) != 0 : (votes >> 16) != 0;
             if (clear && mine < r1) *chunk(mine) = make_uint4(0, 0, 0, 0);
             const int d = t * BN + r - it.ctx;
-            if (votes & 0xffffu) bad |= 1ull << d;
-            if (votes >> 16) bad |= 2ull << d;
+            const unsigned long long found = (votes & 0xffffu ? 1ull << d : 0) | (votes >> 16 ? 2ull << d : 0);
+            if (j & pair) bad[1] |= found;
+            else bad[0] |= found;
           }
           // rows of the last block behind the sequence
           for (int r = r1 + (lane >> 4); r < ((r1 + 15) & ~15); r += 2) *chunk(r) = make_uint4(0, 0, 0, 0);
-          if (lane == 0) bad_v[k % NI] = bad;
+          if (lane == 0) bad_v[2 * (k % NI) + (j & pair)] = j & pair ? bad[1] : bad[0];
           fence_proxy_async_smem();       // the clears become visible to the tensor core
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(TB_F + at % NS));
         }
-        base += 2 * it.n;
+        base += 2 * ord.n;
         item_done(k);
       }
     }
@@ -527,6 +539,7 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
     for (int k = 0; item_at(k, it); ++k) {
       const Order ord = order_of(it);
       const int row = r + (ord.both ? side * BM : 0);      // of the stream
+      const bool pair = PAIRS && it.heads == 2;                     // this side's KV head is its own
       const bool live = row < it.rows;
       const bool warp_live = (warp & 3) * 32 + (ord.both ? side * BM : 0) < it.rows;
       uint64_t bits = 0;
@@ -565,7 +578,7 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
           }
           continue;
         }
-        const int t = it.t0 + (ord.both ? i : 2 * i + side), k0 = t * BN;
+        const int t = it.t0 + (ord.both || pair ? i : 2 * i + side), k0 = t * BN;
         if (k0 + BN > it.ctx) {
           // Drafted tokens among the keys: those that the row does not see
           // become -inf in TMEM, 32 keys at a time (in the registers of the
@@ -666,27 +679,29 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
       }
       // ---- the item's result.  Where the sides shared the rows' keys, each
       // thread joins both for half of its row's columns.
-      const bool joint = !ord.both, two = ord.side_steps(1) > 0;
+      const bool joint = !ord.both && !pair, two = ord.side_steps(1) > 0;
       wait_or_abort(bar(joint ? TB_OJ : TB_OD + side), (joint ? joints : own) & 1, abort_flag, a.err);
-      if (leader && side == (joint ? 0 : 1)) {             // the item's last V tiles are read
-        if (joint && it.n > 1) release(base_slot + 2 * it.n - 2);
-        release(base_slot + 2 * it.n - 1);
+      // the item's last V tiles are read
+      if (leader && (pair || side == (joint ? 0 : 1))) {
+        if (ord.n > 1 && (joint || (pair && side == 0))) release(base_slot + 2 * ord.n - 2);
+        if (!pair || side == 1) release(base_slot + 2 * ord.n - 1);
       }
-      base_slot = (base_slot + 2 * it.n) % NS;
+      base_slot = (base_slot + 2 * ord.n) % NS;
       __syncwarp();
       tc_fence_after();
-      const int out_row = (it.q_tok + ((it.row0 + row) >> log_group)) * a.num_q_heads + it.g * group +
+      const int g = it.g + (pair ? side : 0);
+      const int out_row = (it.q_tok + ((it.row0 + row) >> log_group)) * a.num_q_heads + g * group +
                           (row & (group - 1));             // rows of q, times heads
       if ((it.t0 + it.n) * BN > it.ctx && warp_live) {
         // drafted tokens whose values the products left out, of this side's tiles
-        unsigned long long left = live ? bad_v[k % NI] & bits : 0;
+        unsigned long long left = live ? bad_v[2 * (k % NI) + (pair ? side : 0)] & bits : 0;
         if (joint && left) {
           const int edge = min(max(it.ctx / BN * BN + BN - it.ctx, 0), 64);   // drafted tokens of the first such tile
           const unsigned long long early = edge >= 64 ? ~0ull : (1ull << edge) - 1;
           left &= ((it.ctx / BN - it.t0) & 1) == side ? early : ~early;
         }
         if (__any_sync(0xffffffffu, left != 0))
-          add_cleared(a, it, left, m_run == -INFINITY ? 0.f : m_run, lane_base + col_o, out_row);
+          add_cleared(a, it, g, left, m_run == -INFINITY ? 0.f : m_run, lane_base + col_o, out_row);
       }
       float w0 = 1.f, w1 = 1.f, m = m_run, l = l_run;
       if (joint) {
@@ -708,7 +723,8 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
         const bool none = l == 0.f;                        // the row sees none of these keys
         const bool whole = it.slot < 0;
         char* piece = p.partials + ((int64_t)blockIdx.x * 2 + it.slot) * p.piece_bytes;
-        char* to = whole ? static_cast<char*>(a.out) + (int64_t)out_row * (HD * 2) : piece + row * (HD * 4);
+        const int piece_row = row + (pair && side ? it.rows : 0);
+        char* to = whole ? static_cast<char*>(a.out) + (int64_t)out_row * (HD * 2) : piece + piece_row * (HD * 4);
         const float inv = none ? 0.f : 1.f / l;
         const int col0 = joint ? side * 64 : 0, cols = joint ? 64 : HD;
 #pragma unroll 1
@@ -750,7 +766,7 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
         }
         if (live && (!joint || side == 0)) {
           if (!whole)
-            reinterpret_cast<float2*>(piece + (int64_t)p.piece_rows * HD * 4)[row] = make_float2(m, l);
+            reinterpret_cast<float2*>(piece + (int64_t)p.piece_rows * HD * 4)[piece_row] = make_float2(m, l);
           else if (a.lse)
             a.lse[out_row] = none ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
         }
@@ -796,7 +812,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeMmaParams p) 
   // inside the workspace, if not this stream's
   if (FEW && row < p.piece_rows && blockIdx.x + lane < gridDim.x) mine = stat(lane);
   const MergeDesc d = p.desc[blockIdx.x];
-  if (row >= d.rows || d.pieces == 0) return;
+  if (d.pieces == 0 || row >= d.rows * d.heads) return;
   if (!FEW && lane < d.pieces) mine = stat(lane);
   if (lane >= d.pieces) mine = make_float2(-INFINITY, 0.f);
   auto value = [&](int i) { return reinterpret_cast<const float4*>(piece(i))[row * (HD / 4) + lane]; };
@@ -832,7 +848,9 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeMmaParams p) 
   const bool none = l == 0.f;
   const float inv = 1.f / l;
   const int group = a.num_q_heads / a.num_kv_heads;
-  const int64_t at = (int64_t)(d.q_tok + (d.row0 + row) / group) * a.num_q_heads + d.g * group + (d.row0 + row) % group;
+  const bool second = row >= d.rows;                       // the pair's other KV head
+  const int of = d.row0 + row - (second ? d.rows : 0);
+  const int64_t at = (int64_t)(d.q_tok + of / group) * a.num_q_heads + (d.g + second) * group + of % group;
   uint2* out = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at * HD) + lane;
   *out = none ? make_uint2(0, 0)
               : make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
@@ -841,9 +859,14 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeMmaParams p) 
 
 }  // namespace
 
+// Rows of a partial: up to 256, of one KV head or of a pair.
+static int64_t piece_rows(int64_t rows, bool pairs) {
+  const int64_t most = pairs ? 2 * rows : rows;
+  return most < kTreeRows ? most : kTreeRows;
+}
+
 size_t tree_workspace_bytes(int group, int max_draft) {
-  const int64_t rows = (int64_t)max_draft * group;
-  const size_t piece = ((rows < kTreeRows ? rows : kTreeRows) * (HD + 2) * 4 + 255) & ~(size_t)255;
+  const size_t piece = (piece_rows((int64_t)max_draft * group, true) * (HD + 2) * 4 + 255) & ~(size_t)255;
   return 2 * (size_t)kTreeMaxCtas * piece + kTreeMaxCtas * sizeof(MergeDesc);
 }
 
@@ -852,9 +875,6 @@ cudaError_t launch_tree_attention_mma(const TreeArgs& a, int num_sms, cudaStream
   const int64_t rows = (int64_t)a.max_draft * group;
   TreeMmaParams p;
   p.a = a;
-  p.q_bufs = rows <= BM ? 2 : 1;
-  p.piece_rows = (int)(rows < kTreeRows ? rows : kTreeRows);
-  p.piece_bytes = ((int64_t)p.piece_rows * (HD + 2) * 4 + 255) & ~255ll;
   p.wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
   p.desc = static_cast<MergeDesc*>(a.workspace);
   p.partials = static_cast<char*>(a.workspace) + kTreeMaxCtas * sizeof(MergeDesc);
@@ -863,14 +883,20 @@ cudaError_t launch_tree_attention_mma(const TreeArgs& a, int num_sms, cudaStream
   if (!encode_group_rows_map_bf16(&tm_q, a.q, a.num_rows, a.num_q_heads, group) ||
       !encode_latent_block_map(&tm_k, a.k_cache, tiles) || !encode_latent_block_map(&tm_v, a.v_cache, tiles))
     return cudaErrorInvalidValue;
-  cudaError_t e = allow_dynamic_smem(tree_mma_kernel, SMEM_BYTES);
-  if (e != cudaSuccess) return e;
   const int64_t row_tiles = (rows + kTreeRows - 1) / kTreeRows;
   const int64_t stages = (int64_t)a.num_seqs * a.num_kv_heads * row_tiles * ((a.max_seq_len + BN - 1) / BN);
   int grid = num_sms < kTreeMaxCtas ? num_sms : kTreeMaxCtas;
   const bool few = stages <= 4 * grid;
+  // a batch that may have enough tiles, and whose KV heads and rows go in pairs
+  const bool pairs = stages >= kTreePairTiles * grid && !(a.num_kv_heads & 1);
+  p.q_bufs = rows <= BM && !pairs ? 2 : 1;
+  p.piece_rows = (int)piece_rows(rows, pairs);
+  p.piece_bytes = ((int64_t)p.piece_rows * (HD + 2) * 4 + 255) & ~255ll;
   if (stages < grid) grid = (int)stages;
-  tree_mma_kernel<<<grid, kThreadsT, SMEM_BYTES, stream>>>(p, tm_q, tm_k, tm_v);
+  const auto kernel = pairs ? tree_mma_kernel<true> : tree_mma_kernel<false>;
+  cudaError_t e = allow_dynamic_smem(kernel, SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  kernel<<<grid, kThreadsT, SMEM_BYTES, stream>>>(p, tm_q, tm_k, tm_v);
   e = cudaGetLastError();
   if (e != cudaSuccess || a.max_seq_len <= BN) return e;   // one tile a stream: no partials
   cudaLaunchConfig_t cfg = {};

@@ -6,8 +6,8 @@
 // What bounds it: every stored key is read once, 256 B for 128 R multiply-adds
 // and R exponentials (R rows of a KV head): HBM up to about 170 rows, the
 // exponentials behind that.  Measured, 8 KV heads: 64 sequences of 2,301 with one
-// row of four heads 49-50 us, 8 of 32,001 with 32 such rows 87-88 us, 6.2 TB/s
-// either way (91-94% of a plain copy's rate); on CUDA cores 593 and 4,877 us.
+// row of four heads 49-50 us, 8 of 32,001 with 32 such rows 86 us, 6.2 to 6.3
+// TB/s (92-94% of a plain copy's rate); on CUDA cores 593 and 4,877 us.
 //
 // The products are formed with the keys as the M side, S^T = K Q^T (128 keys x
 // up to 256 rows), so that a thread holds all rows of one key: the sum over the

@@ -315,3 +315,31 @@ def test_compaction_by_a_replayed_graph_whose_lists_change():
         assert all(kept[b, h, :len(ref[b][h])].tolist() == ref[b][h] for b in range(2) for h in range(2))
         exp = T.compact(k, v, w, table, now, kept.cpu(), n.tolist(), None)
         assert all(torch.equal(a.cpu(), e) for a, e in zip((dk, dv, dw), exp))
+
+
+@pytest.mark.parametrize("hq,hkv,most", [(32, 8, 1000), (4, 4, 260), (32, 2, 700), (6, 6, 3000)])
+def test_many_short_sequences(hq, hkv, most):
+    """KV heads that go in pairs, whole and cut between CTAs, next to sequences
+    of more rows or tiles that do not; drafted values of one head that are
+    infinite or NaN reach only the rows of that head that see them."""
+    pick = random.Random(most)
+    lens = [pick.randint(1, most) for _ in range(160)]
+    drafted = [min(n, pick.choice([1, 2, 5, 8, pick.randint(0, 64)])) for n in lens]
+    x = Batch(lens, drafted, hq, hkv, seed=most)
+    for b in range(0, 160, 3):
+        if drafted[b] == 0:
+            continue
+        t, h = lens[b] - 1 - pick.randrange(drafted[b]), pick.randrange(hkv)
+        x.v[int(x.table[b, t // 16]), h, t % 16, pick.randrange(128)] = pick.choice([float("inf"), float("nan"), 1e30])
+    d = [a.to(D) for a in (x.q, x.k, x.v, x.table, x.lens, x.offsets, x.mask)]
+    out, lse = attend(x, d)
+    assert B.get_device_error() == 0
+    ref, ref_lse = T.tree_attention(*x.args())
+    tol, tol_lse = x.bounds(ref)
+    out, lse = out.cpu().double(), lse.cpu().double()
+    plain = torch.isfinite(ref) & (ref.abs() < 1e20)
+    assert bool(((out - ref).abs() <= tol)[plain].all())
+    assert bool((torch.isnan(out) == torch.isnan(ref)).all()) and bool((out[torch.isinf(ref)] == ref[torch.isinf(ref)]).all())
+    assert bool(((lse - ref_lse).abs() <= tol_lse).all())
+    again = attend(x, d)
+    assert torch.equal(again[0].cpu().double().nan_to_num(), out.nan_to_num())
