@@ -8,8 +8,8 @@
 // A row that sees nothing gets out = 0 and lse = -inf.
 //
 // A row of this kernel is (drafted token, query head of the group), token
-// first.  A CTA takes 32 rows of one (sequence, KV head) and walks key tiles
-// of 32 tokens; the cluster's CTAs (up to 8) take turns on the tiles and join
+// first.  A CTA takes 32 rows of one (sequence, KV head), or 16 or 8 where no
+// sequence has more, and walks key tiles of 32 tokens; the cluster's CTAs (up to 8) take turns on the tiles and join
 // their running (m, l, O) through distributed shared memory at the end, so a
 // short batch still fills the GPU and no workspace is needed.
 //
@@ -18,7 +18,11 @@
 // lane has four keys and a quarter of the dims (8 reads of 16 bytes for 64
 // multiply-adds; a row and four keys a thread took 5 for 16, and 52.8 us for
 // four sequences of 500 to 1,500 against 21.4), for P V four dims of the four
-// rows (2 reads for 16).  A warp without rows only helps to load.
+// rows (2 reads for 16).  A warp without rows only helps to load; with up to 16 or
+// 8 rows two or four warps split a tile's keys and join at the end (8 query heads
+// to 4 KV heads and 5 drafted tokens over 500 to 1,500 21.4 -> 20.0 us; 4 sequences
+// of 30,842 with 8 rows, 1 GB, 402 -> 354; 2 of 10,457 with 4 rows of 16 dims 58 ->
+// 31; 16 of 2,000 with 12 rows 67 -> 66).
 #include <climits>
 
 #include <cooperative_groups.h>
@@ -68,12 +72,12 @@ __device__ __forceinline__ int64_t pool_row(const TreeArgs& a, const int32_t* ta
   return ((int64_t)blk * a.num_kv_heads + g) * kBlockSize + t % kBlockSize;
 }
 
-// Rows row0 .. row0 + 31 of the queries (zeros behind the last).
-template <int D>
+// Rows row0 .. row0 + ROWS - 1 of the queries (zeros behind the last).
+template <int D, int ROWS = kRows>
 __device__ __forceinline__ void load_q(const TreeArgs& a, const TreeSeq& s, int g, int group, int row0, int rows,
                                        float (*q)[D + 4]) {
   constexpr int CH = D / 4;
-  for (int i = threadIdx.x; i < kRows * CH; i += kThreadsCC) {
+  for (int i = threadIdx.x; i < ROWS * CH; i += kThreadsCC) {
     const int r = i / CH, c = i % CH, row = row0 + r;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (row < rows) {
@@ -84,32 +88,32 @@ __device__ __forceinline__ void load_q(const TreeArgs& a, const TreeSeq& s, int 
   }
 }
 
-// Scores (not scaled) of a warp's four rows q with keys (lane & 7) + 8 j: a
-// lane sums a quarter of the dims, then four lanes add theirs.
-template <int D>
-__device__ __forceinline__ void scores(const float (*q)[D + 4], const float (*k)[D + 4], int lane, float (&s)[4][4]) {
+// Scores (not scaled) of a warp's four rows q with keys (lane & 7) + 8 j, j < J:
+// a lane sums a quarter of the dims, then four lanes add theirs.
+template <int D, int J>
+__device__ __forceinline__ void scores(const float (*q)[D + 4], const float (*k)[D + 4], int lane, float (&s)[4][J]) {
   const int key = lane & 7, d0 = (lane >> 3) * (D / 4);
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+    for (int j = 0; j < J; ++j) s[i][j] = 0.f;
 #pragma unroll 4
   for (int d = d0; d < d0 + D / 4; d += 4) {
-    float4 x[4], y[4];
+    float4 x[4], y[J];
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4*>(&q[i][d]);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4*>(&k[key + 8 * j][d]);
+    for (int j = 0; j < J; ++j) y[j] = *reinterpret_cast<const float4*>(&k[key + 8 * j][d]);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < J; ++j)
         s[i][j] = fmaf(x[i].x, y[j].x, fmaf(x[i].y, y[j].y, fmaf(x[i].z, y[j].z, fmaf(x[i].w, y[j].w, s[i][j]))));
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < J; ++j) {
       s[i][j] += __shfl_xor_sync(kAll, s[i][j], 8);
       s[i][j] += __shfl_xor_sync(kAll, s[i][j], 16);
     }
@@ -119,17 +123,20 @@ __device__ __forceinline__ bool seen(int t, int ctx, uint64_t bits) {
   return t < ctx || (t - ctx < 64 && ((bits >> (t - ctx)) & 1));
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreadsCC) tree_cc_kernel(const TreeArgs a) {
+// SPLIT: the keys of a tile are split between so many warps, of 32 / SPLIT rows.
+template <int D, int SPLIT>
+__global__ void __launch_bounds__(kThreadsCC, SPLIT > 1 ? 2 : 0) tree_cc_kernel(const TreeArgs a) {
+  constexpr int ROWS = kRows / SPLIT, QUADS = ROWS / 4, J = 4 / SPLIT;
+  static_assert(QUADS * SPLIT == kWarps, "a warp has four rows and 8 J keys");
   extern __shared__ __align__(16) unsigned char smem_raw[];
   TreeSmem<D>& sm = *reinterpret_cast<TreeSmem<D>*>(smem_raw);
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = cluster.block_rank(), ranks = cluster.num_blocks();
   const int group = a.num_q_heads / a.num_kv_heads;
-  const int chunks = (a.max_draft * group + kRows - 1) / kRows;
-  const int item = blockIdx.x / ranks;   // (sequence, KV head, 32 rows)
+  const int chunks = (a.max_draft * group + ROWS - 1) / ROWS;
+  const int item = blockIdx.x / ranks;   // (sequence, KV head, ROWS rows)
   const int b = item / chunks / a.num_kv_heads, g = item / chunks % a.num_kv_heads;
-  const int row0 = item % chunks * kRows;
+  const int row0 = item % chunks * ROWS;
   const TreeSeq s = tree_seq(a, b, rank == 0 && threadIdx.x == 0);
   const int rows = s.drafted * group;
   if (row0 >= rows) return;              // the same for the whole cluster
@@ -173,17 +180,18 @@ __global__ void __launch_bounds__(kThreadsCC) tree_cc_kernel(const TreeArgs a) {
   const int tiles = (s.len + kKeys - 1) / kKeys;
   ask_blocks(rank);
   if (rank < tiles) fetch(rank);
-  load_q<D>(a, s, g, group, row0, rows, sm.q);
+  load_q<D, ROWS>(a, s, g, group, row0, rows, sm.q);
 
-  // this warp's rows 4 warp + i, a lane's keys (lane & 7) + 8 j and dims 4 dg ..
+  // this warp's rows r0 + i and keys k0 .., a lane's keys k0 + (lane & 7) + 8 j and dims 4 dg ..
+  const int r0 = 4 * (SPLIT == 1 ? warp : warp % QUADS), part = SPLIT == 1 ? 0 : warp / QUADS, k0 = part * 8 * J;
   constexpr int DG = D / 4 < 32 ? D / 4 : 32, KS = 32 / DG;   // lanes over dims, and over keys
   static_assert(D == 4 * DG, "four dims a lane");
-  const bool live = row0 + 4 * warp < rows;
+  const bool live = row0 + r0 < rows;
   const int dg = lane % DG;
   uint64_t bits[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int row = row0 + 4 * warp + i;
+    const int row = row0 + r0 + i;
     bits[i] = row < rows ? tree_bits(a, s, row / group) : 0;
   }
   const float sl2 = a.scale * kLog2e;
@@ -208,15 +216,15 @@ __global__ void __launch_bounds__(kThreadsCC) tree_cc_kernel(const TreeArgs a) {
     __syncthreads();
     if (tile + ranks < tiles) fetch(tile + ranks);
     if (!live) continue;
-    float sc[4][4];
-    scores<D>(sm.q + 4 * warp, sm.k, lane, sc);
+    float sc[4][J];
+    scores<D, J>(sm.q + r0, sm.k + k0, lane, sc);
     const bool all = (tile + 1) * kKeys <= ctx;   // every row sees every key
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float mx = -INFINITY;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int t = tile * kKeys + (lane & 7) + 8 * j;
+      for (int j = 0; j < J; ++j) {
+        const int t = tile * kKeys + k0 + (lane & 7) + 8 * j;
         sc[i][j] = all || (t < s.len && seen(t, ctx, bits[i])) ? sc[i][j] * sl2 : -INFINITY;
         mx = fmaxf(mx, sc[i][j]);
       }
@@ -227,22 +235,28 @@ __global__ void __launch_bounds__(kThreadsCC) tree_cc_kernel(const TreeArgs a) {
       l[i] *= alpha;                          // this lane's share of the row's sum
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        sc[i][j] = ex2(sc[i][j] - base);
-        l[i] += sc[i][j];
+        if (j < J) {
+          sc[i][j % J] = ex2(sc[i][j % J] - base);
+          l[i] += sc[i][j % J];
+        }
         o[i][j] *= alpha;
       }
       m[i] = m_new;
     }
     // four lanes have the same weights: each writes one key's
     const int j = lane >> 3;
-    auto pick = [&](int i) { return j < 2 ? (j == 0 ? sc[i][0] : sc[i][1]) : (j == 2 ? sc[i][2] : sc[i][3]); };
+    auto pick = [&](int i) {
+      if constexpr (J == 1) return sc[i][0];
+      else if constexpr (J == 2) return j & 1 ? sc[i][1] : sc[i][0];
+      else return j < 2 ? (j == 0 ? sc[i][0] : sc[i][1]) : (j == 2 ? sc[i][2] : sc[i][3]);
+    };
     __syncwarp();
-    sm.p[warp][lane] = make_float4(pick(0), pick(1), pick(2), pick(3));   // key (lane & 7) + 8 j
+    if (j < J) sm.p[warp][lane] = make_float4(pick(0), pick(1), pick(2), pick(3));   // key (lane & 7) + 8 j
     __syncwarp();
 #pragma unroll 4
-    for (int n = lane / DG; n < kKeys; n += KS) {
+    for (int n = lane / DG; n < 8 * J; n += KS) {
       const float4 p = sm.p[warp][n];
-      const float4 v = *reinterpret_cast<const float4*>(&sm.v[n][4 * dg]);
+      const float4 v = *reinterpret_cast<const float4*>(&sm.v[k0 + n][4 * dg]);
       const float w[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -262,22 +276,29 @@ __global__ void __launch_bounds__(kThreadsCC) tree_cc_kernel(const TreeArgs a) {
     for (int d = DG; d < 32; d <<= 1)
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[i][j] += __shfl_xor_sync(kAll, o[i][j], d);
-    const int r = 4 * warp + i;
-    if (lane < DG) *reinterpret_cast<float4*>(&sm.o[r][4 * dg]) = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+    const int at = part * ROWS + r0 + i;
+    if (lane < DG) *reinterpret_cast<float4*>(&sm.o[at][4 * dg]) = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
     if (lane == 0) {
-      sm.m[r] = m[i];
-      sm.l[r] = l[i];
+      sm.m[at] = m[i];
+      sm.l[at] = l[i];
     }
   }
   cluster.sync();
   // the ranks share the rows, a warp per row: rank k joins rows k, k + ranks, ...
-  for (int r = rank + ranks * warp; r < kRows && row0 + r < rows; r += ranks * kWarps) {
-    const float mine = lane < ranks ? cluster.map_shared_rank(sm.m, lane)[r] : -INFINITY;
-    float total = lane < ranks ? cluster.map_shared_rank(sm.l, lane)[r] : 0.f;
-    float4 x[kMaxCluster];
+  // piece e of a row: part e % SPLIT of rank e / SPLIT
+  const int pieces = ranks * SPLIT;
+  static_assert(kMaxCluster * SPLIT <= 32, "a lane per piece");
+  for (int r = rank + ranks * warp; r < ROWS && row0 + r < rows; r += ranks * kWarps) {
+    auto value = [&](int e) {
+      return *reinterpret_cast<const float4*>(cluster.map_shared_rank(&sm.o[e % SPLIT * ROWS + r][4 * dg], e / SPLIT));
+    };
+    const int of = lane % SPLIT * ROWS + r;
+    const float mine = lane < pieces ? cluster.map_shared_rank(sm.m, lane / SPLIT)[of] : -INFINITY;
+    float total = lane < pieces ? cluster.map_shared_rank(sm.l, lane / SPLIT)[of] : 0.f;
+    float4 x[8];
 #pragma unroll
-    for (int k = 0; k < kMaxCluster; ++k)
-      if (k < ranks) x[k] = *reinterpret_cast<const float4*>(cluster.map_shared_rank(&sm.o[r][4 * dg], k));
+    for (int k = 0; k < 8; ++k)
+      if (k < pieces) x[k] = value(k);
     float top = mine;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
@@ -286,15 +307,21 @@ __global__ void __launch_bounds__(kThreadsCC) tree_cc_kernel(const TreeArgs a) {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(kAll, total, d);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int e = 0; e < (SPLIT == 1 ? 1 : pieces); e += 8) {
 #pragma unroll
-    for (int k = 0; k < kMaxCluster; ++k) {
-      const float wk = __shfl_sync(kAll, w, k);
-      if (k < ranks && wk != 0.f) {
-        acc.x = fmaf(wk, x[k].x, acc.x);
-        acc.y = fmaf(wk, x[k].y, acc.y);
-        acc.z = fmaf(wk, x[k].z, acc.z);
-        acc.w = fmaf(wk, x[k].w, acc.w);
+      for (int k = 0; k < 8; ++k) {
+        const float wk = __shfl_sync(kAll, w, (e + k) & 31);
+        if (e + k < pieces && wk != 0.f) {
+          acc.x = fmaf(wk, x[k].x, acc.x);
+          acc.y = fmaf(wk, x[k].y, acc.y);
+          acc.z = fmaf(wk, x[k].z, acc.z);
+          acc.w = fmaf(wk, x[k].w, acc.w);
+        }
       }
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (SPLIT > 1 && e + 8 + k < pieces) x[k] = value(e + 8 + k);
     }
     const bool none = total == 0.f;      // the row sees nothing (a NaN score makes total NaN)
     const float inv = none ? 0.f : 1.f / total;
@@ -322,7 +349,7 @@ struct WeightSmem {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreadsCC) weights_cc_kernel(const TreeArgs a) {
+__global__ void __launch_bounds__(kThreadsCC, 2) weights_cc_kernel(const TreeArgs a) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   WeightSmem<D>& sm = *reinterpret_cast<WeightSmem<D>*>(smem_raw);
   const int group = a.num_q_heads / a.num_kv_heads;
@@ -335,15 +362,26 @@ __global__ void __launch_bounds__(kThreadsCC) weights_cc_kernel(const TreeArgs a
   const int ctx = s.len - s.drafted;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int32_t* table = a.block_table + (int64_t)b * a.max_blocks_per_seq;
-  constexpr int CH = D / 4;
-#pragma unroll 4
-  for (int i = tid; i < kWKeys * CH; i += kThreadsCC) {
-    const int key = i / CH, t = key0 + key;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (t < s.len)
-      x = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.k_cache) + pool_row(a, table, t, g) * D) +
-                i % CH);
-    *reinterpret_cast<float4*>(&sm.k[key][i % CH * 4]) = x;
+  // block ids first, then eight keys' chunks on their way at a time
+  constexpr int CH = D / 4, STEPS = kWKeys * CH / kThreadsCC, AT_ONCE = STEPS < 8 ? STEPS : 8;
+  int64_t from[STEPS];
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) {
+    const int t = key0 + (tid + i * kThreadsCC) / CH;
+    from[i] = t < s.len ? pool_row(a, table, t, g) : -1;
+  }
+#pragma unroll
+  for (int i0 = 0; i0 < STEPS; i0 += AT_ONCE) {
+    float4 x[AT_ONCE];
+#pragma unroll
+    for (int i = 0; i < AT_ONCE; ++i) {
+      x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (from[i0 + i] >= 0)
+        x[i] = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.k_cache) + from[i0 + i] * D) + tid % CH);
+    }
+#pragma unroll
+    for (int i = 0; i < AT_ONCE; ++i)
+      *reinterpret_cast<float4*>(&sm.k[(tid + (i0 + i) * kThreadsCC) / CH][tid % CH * 4]) = x[i];
   }
   const float sl2 = a.scale * kLog2e;
   const int sub = kKeys * (warp & 3);    // this warp's keys
@@ -364,7 +402,7 @@ __global__ void __launch_bounds__(kThreadsCC) weights_cc_kernel(const TreeArgs a
     __syncthreads();
     for (int r = 4 * (warp >> 2); r < kRows && row0 + r < rows; r += 8) {
       float sc[4][4];
-      scores<D>(sm.q + r, sm.k + sub, lane, sc);
+      scores<D, 4>(sm.q + r, sm.k + sub, lane, sc);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int row = row0 + r + i;
@@ -385,15 +423,15 @@ __global__ void __launch_bounds__(kThreadsCC) weights_cc_kernel(const TreeArgs a
         sm.part[tid >> 5][tid & 31] + sm.part[(tid >> 5) + 4][tid & 31];
 }
 
-template <int D>
+template <int D, int SPLIT>
 cudaError_t launch_attention(const TreeArgs& a, cudaStream_t stream) {
   const int group = a.num_q_heads / a.num_kv_heads;
-  const int chunks = (a.max_draft * group + kRows - 1) / kRows;
+  const int chunks = (a.max_draft * group + kRows / SPLIT - 1) / (kRows / SPLIT);
   const int tiles = (a.max_seq_len + kKeys - 1) / kKeys;
   int ranks = 1;
   while (ranks < kMaxCluster && 2 * ranks <= tiles) ranks *= 2;
   const int smem = (int)sizeof(TreeSmem<D>);
-  cudaError_t e = allow_dynamic_smem(tree_cc_kernel<D>, smem);
+  cudaError_t e = allow_dynamic_smem(tree_cc_kernel<D, SPLIT>, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   const int64_t ctas = (int64_t)a.num_seqs * a.num_kv_heads * chunks * ranks;
@@ -408,7 +446,7 @@ cudaError_t launch_attention(const TreeArgs& a, cudaStream_t stream) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, tree_cc_kernel<D>, a);
+  e = cudaLaunchKernelEx(&cfg, tree_cc_kernel<D, SPLIT>, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -426,7 +464,12 @@ cudaError_t launch_weights(const TreeArgs& a, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_tree_attention_cc(const TreeArgs& a, cudaStream_t stream) {
-  return a.head_dim == 16 ? launch_attention<16>(a, stream) : launch_attention<128>(a, stream);
+  const int rows = a.max_draft * (a.num_q_heads / a.num_kv_heads);
+  if (a.head_dim == 16)
+    return rows <= 8 ? launch_attention<16, 4>(a, stream)
+                     : rows <= 16 ? launch_attention<16, 2>(a, stream) : launch_attention<16, 1>(a, stream);
+  return rows <= 8 ? launch_attention<128, 4>(a, stream)
+                   : rows <= 16 ? launch_attention<128, 2>(a, stream) : launch_attention<128, 1>(a, stream);
 }
 
 cudaError_t launch_kv_add_weights_cc(const TreeArgs& a, cudaStream_t stream) {

@@ -247,3 +247,14 @@ def test_device_errors():
         assert got == want, kw
         if want == 3:
             assert bool((out[:3] == 7).all()) and bool((out[3:] != 7).any())
+
+
+@pytest.mark.parametrize("dim", [16, 128])
+@pytest.mark.parametrize("hq,hkv,drafted", [(1, 1, 1), (2, 1, 4), (4, 2, 4), (8, 1, 1), (3, 3, 9), (8, 2, 4), (2, 1, 8),
+                                            (4, 1, 5), (8, 1, 64)])
+@pytest.mark.parametrize("mask", [None, "tree", "random"])
+def test_fp32_rows_and_parts(dim, hq, hkv, drafted, mask):
+    """Up to 8, 16 and more rows a KV head: keys split between four, two and no warps."""
+    x = Batch([700, drafted, drafted + 1, 33 + drafted, 0, 300], [drafted, drafted, max(1, drafted - 1), drafted, 0, 1],
+              hq, hkv, dim=dim, dtype=F32, mask=mask, seed=hq + drafted, spare_rows=2)
+    check(x, *run(x))
