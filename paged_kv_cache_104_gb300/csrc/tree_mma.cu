@@ -10,9 +10,9 @@
 // R = 256 rows (64 drafted tokens of a group of 4) HBM is the bound.  Measured,
 // 32 query and 8 KV heads, with the merge: 64 sequences of 2,301 with 16 drafted
 // tokens 106 us (5.8 TB/s, 86% of a plain copy's rate), 8 of 32,001 with 64 drafted
-// 200 us (5.3 TB/s and 1,340 TFLOP/s: the tensor pipe is busy 65% of the time, the
-// rest is softmax between a side's two products, as tensor memory holds one S for
-// each side), one of 777 with 8 drafted 10.4 us (latency).
+// 192-200 us (5.3-5.5 TB/s and 1,340-1,390 TFLOP/s: the tensor pipe is busy 64% of
+// the time, the rest is softmax between a side's two products, as tensor memory
+// holds one S for each side), one of 777 with 8 drafted 10.4 us (latency).
 //
 // Work.  A stream is one (sequence, KV head, 256 rows), cut into tiles of 128
 // keys; the tiles of the whole batch are shared out equally to one persistent
@@ -68,7 +68,7 @@ constexpr int TILE = BN * HD * 2;             // a K or V tile, 32 KiB: [8 rows]
 constexpr int GROUP8 = 2048;                  // 8 rows of a tile
 constexpr int NS = 5;                         // ring slots
 constexpr int NI = 4;                         // items in flight
-constexpr int NCK = 4;                        // V tiles on their way to the checker
+constexpr int NCK = 4;                        // V tiles on their way to the guard
 constexpr int OFF_Q = 0;                      // two 32 KiB buffers
 constexpr int OFF_KV = 2 * Q_BYTES;
 constexpr int OFF_ML = OFF_KV + NS * TILE;    // [side][row] (max, sum) exchange
@@ -207,7 +207,7 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
   if (tid == 0) {
     for (int i = 0; i < TB_COUNT; ++i) {
       int count = 1;
-      if (i >= TB_IE && i < TB_CK) count = 3 + kSoft / 32;   // issuer, producer, checker, softmax warps
+      if (i >= TB_IE && i < TB_CK) count = 3 + kSoft / 32;   // issuer, producer, guard, softmax warps
       if (i >= TB_PF && i < TB_OD) count = 4;
       if (i >= TB_ML) count = kSoft / 32;
       mbar_init(bar(i), count);
@@ -309,8 +309,8 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
       // whose rows are several streams are read again
       const uint64_t once = policy_evict_first(), again = policy_evict_normal();
       uint64_t policy = once;
-      int pos = 0, checks = 0;        // ring position; V tiles sent to the checker
-      uint32_t history = 0;           // which of the last positions went to the checker
+      int pos = 0, checks = 0;        // ring position; V tiles sent to the guard
+      uint32_t history = 0;           // which of the last positions went to the guard
       TreeItem it;
       bool ok = true;
       for (int k = 0; ok && item_at(k, it); ++k) {
@@ -472,7 +472,7 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
         item_done(k);
       }
     } else if (warp == W_FIX) {
-      // ---------------------------------------------------------------- checker of the drafted tokens' values
+      // ---------------------------------------------------------------- guard of the drafted tokens' values
       int base = 0, checks = 0;
       TreeItem it;
       bool ok = true;
