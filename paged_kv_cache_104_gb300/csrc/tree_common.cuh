@@ -98,6 +98,7 @@ template <bool ROW_TILES, bool PAIRS = false>
 struct TreePlan {
   const TreeArgs& a;
   const int lane, group;
+  const bool whole;                    // streams are not cut
   int windows, w = -1;                 // windows of 32 sequences, the loaded one
   bool weighted = false, paired = false;
   int share = 0, longer = 0;           // units of a CTA; the first `longer` CTAs have one more
@@ -132,8 +133,8 @@ struct TreePlan {
     return head_units(nt, rows, heavy) * a.num_kv_heads;
   }
   // For one warp (active), while the others still set the CTA up.
-  __device__ TreePlan(const TreeArgs& args, bool active)
-      : a(args), lane(threadIdx.x & 31), group(args.num_q_heads / args.num_kv_heads),
+  __device__ TreePlan(const TreeArgs& args, bool active, bool uncut = false)
+      : a(args), lane(threadIdx.x & 31), group(args.num_q_heads / args.num_kv_heads), whole(uncut),
         windows((args.num_seqs + 31) / 32) {
     if (!active) return;
     const bool report = blockIdx.x == 0;
@@ -235,10 +236,14 @@ struct TreePlan {
       }
       const int each = two ? (weighted ? 4 : 1) : weight(it.rows, weighted);
       const int s1 = s0 + (two ? per_head : stream_units(nt, it.rows, weighted));
+      if (whole && pos > s0) {                             // started in an earlier CTA
+        pos = s1;
+        continue;
+      }
       // tiles that start in this CTA's units
       it.t0 = tiles_before(pos - s0, each);
-      it.n = min(tiles_before(min(s1, end) - s0, each), nt) - it.t0;
-      pos = min(s1, end);
+      it.n = whole ? nt : min(tiles_before(min(s1, end) - s0, each), nt) - it.t0;
+      pos = whole ? s1 : min(s1, end);
       if (it.n <= 0) {
         it.n = 0;
         continue;

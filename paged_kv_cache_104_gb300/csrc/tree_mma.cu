@@ -120,6 +120,7 @@ struct TreeMmaParams {
   int64_t piece_bytes;
   int piece_rows;
   bool wide;                 // out is 32-byte aligned
+  bool whole;                // streams are not cut
 };
 
 // The order of an item's tiles in the ring, as the products need them: with
@@ -220,7 +221,7 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
                  "r"(kTmemCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  TreePlan<true, PAIRS> plan(a, warp == W_PLAN);
+  TreePlan<true, PAIRS> plan(a, warp == W_PLAN, p.whole);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -887,6 +888,12 @@ cudaError_t launch_tree_attention_mma(const TreeArgs& a, int num_sms, cudaStream
   const int64_t stages = (int64_t)a.num_seqs * a.num_kv_heads * row_tiles * ((a.max_seq_len + BN - 1) / BN);
   int grid = num_sms < kTreeMaxCtas ? num_sms : kTreeMaxCtas;
   const bool few = stages <= 4 * grid;
+  // Short sequences are not cut: nothing to write in parts, and no second kernel
+  // (4 sequences of up to 500 with 64 drafted tokens 23.4 -> 17.0 us, 50 of 131 to
+  // 393 with one KV head 15.5 -> 12.1, one of 200 10.1 -> 8.8), but where a few of
+  // three or four tiles and few rows leave CTAs without any (one of 500 with 8
+  // drafted tokens 10.3 -> 11.0); cut at eight tiles, 16 of 1,000 take 21.5, whole 24.4.
+  p.whole = a.max_seq_len <= 2 * BN || (a.max_seq_len <= 4 * BN && (stages >= grid || rows > BM));
   // a batch that may have enough tiles, and whose KV heads and rows go in pairs
   const bool pairs = stages >= kTreePairTiles * grid && !(a.num_kv_heads & 1);
   p.q_bufs = rows <= BM && !pairs ? 2 : 1;
@@ -898,7 +905,7 @@ cudaError_t launch_tree_attention_mma(const TreeArgs& a, int num_sms, cudaStream
   if (e != cudaSuccess) return e;
   kernel<<<grid, kThreadsT, SMEM_BYTES, stream>>>(p, tm_q, tm_k, tm_v);
   e = cudaGetLastError();
-  if (e != cudaSuccess || a.max_seq_len <= BN) return e;   // one tile a stream: no partials
+  if (e != cudaSuccess || p.whole) return e;               // no partials
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, (p.piece_rows + 7) / 8);
   cfg.blockDim = dim3(256);

@@ -258,3 +258,14 @@ def test_fp32_rows_and_parts(dim, hq, hkv, drafted, mask):
     x = Batch([700, drafted, drafted + 1, 33 + drafted, 0, 300], [drafted, drafted, max(1, drafted - 1), drafted, 0, 1],
               hq, hkv, dim=dim, dtype=F32, mask=mask, seed=hq + drafted, spare_rows=2)
     check(x, *run(x))
+
+
+@pytest.mark.parametrize("most", [1, 128, 129, 256, 257, 384, 385, 512, 513])
+@pytest.mark.parametrize("count,hq,hkv,drafted", [(1, 8, 2, 5), (3, 16, 1, 40), (70, 4, 4, 3), (60, 3, 3, 9), (40, 8, 1, 20)])
+def test_short_sequences_around_where_they_are_cut(most, count, hq, hkv, drafted):
+    """One to five tiles: whole streams or parts, one KV head or two to an item."""
+    pick = random.Random(most)
+    lens = [most] + [pick.randint(0, most) for _ in range(count - 1)]
+    x = Batch(lens, [min(n, pick.randint(0, drafted)) if i else min(n, drafted) for i, n in enumerate(lens)], hq, hkv,
+              seed=most + count, spare_rows=1)
+    check(x, *run(x))
