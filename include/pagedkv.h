@@ -561,8 +561,9 @@ typedef struct pkv_tree_args {
 } pkv_tree_args;
 
 /*
- * Bytes of device workspace paged_tree_attention needs: it depends on the
- * rows of a sequence only, not on the batch.  0 on sizes no call takes.
+ * Bytes of device workspace paged_tree_attention needs in bf16: it depends on
+ * the rows of a sequence only, not on the batch.  0 on sizes no bf16 call takes
+ * (heads, head_dim, max_draft or max_seq_len); fp32 calls need none.
  * Host-only, no GPU use.
  */
 size_t pkv_tree_workspace_bytes(int num_q_heads, int num_kv_heads, int head_dim, int max_draft,

@@ -852,6 +852,8 @@ pkv_status pkv_chunked_prefill_attention_fp8_block(
 
 namespace {
 
+constexpr int kMaxTreeLen = INT_MAX - 65536;   // positions a little behind the end are formed as ints
+
 bool misaligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
 
 // Validates a call of drafted tokens and fills its launch arguments.  *todo
@@ -866,7 +868,7 @@ pkv_status tree_prepare(const pkv_tree_args* x, bool attention, pkv::TreeArgs* o
     return PKV_EINVAL;
   if (x->max_draft > PKV_MAX_DRAFT) return PKV_EUNSUPPORTED;
   if (x->num_seqs == 0 || x->num_rows == 0) return PKV_OK;
-  if (x->num_seqs > PKV_MAX_SEQS || x->max_seq_len > INT_MAX - 65536) return PKV_ERANGE;
+  if (x->num_seqs > PKV_MAX_SEQS || x->max_seq_len > kMaxTreeLen) return PKV_ERANGE;
   if ((int64_t)x->max_seq_len > (int64_t)x->max_blocks_per_seq * x->block_size) return PKV_EINVAL;
   if (!isfinite(x->scale) || !(x->scale > 0.f)) return PKV_EINVAL;
   if (!x->q || !x->k_cache || !x->block_table || !x->seq_lens || !x->draft_offsets) return PKV_EINVAL;
@@ -928,10 +930,9 @@ pkv_status tree_prepare(const pkv_tree_args* x, bool attention, pkv::TreeArgs* o
 extern "C" {
 
 size_t pkv_tree_workspace_bytes(int num_q_heads, int num_kv_heads, int head_dim, int max_draft, int max_seq_len) {
-  if (num_q_heads < 1 || num_kv_heads < 1 || num_q_heads % num_kv_heads != 0 || head_dim < 1 || max_draft < 1 ||
-      max_seq_len < 1)
+  if (check_heads(num_q_heads, num_kv_heads, head_dim, pkv::kBlockSize, PKV_BF16) != PKV_OK || max_draft < 1 ||
+      max_draft > PKV_MAX_DRAFT || max_seq_len < 1 || max_seq_len > kMaxTreeLen)
     return 0;
-  if (head_dim != 128) return 0;
   return pkv::tree_workspace_bytes(num_q_heads / num_kv_heads, max_draft);
 }
 
