@@ -391,12 +391,8 @@ __global__ void __launch_bounds__(kThreadsCC, 2) weights_cc_kernel(const TreeArg
     load_q<D>(a, s, g, group, row0, rows, sm.q);
     if (tid < kRows) {
       const int row = row0 + tid;
-      // a row that sees nothing (lse = -inf) gives nothing: 2^(s - inf) = 0
-      float x = INFINITY;
-      if (row < rows) {
-        x = a.lse[(int64_t)(s.row0 + row / group) * a.num_q_heads + g * group + row % group];
-        x = x == -INFINITY ? INFINITY : x * kLog2e;
-      }
+      float x = -INFINITY;
+      if (row < rows) x = a.lse[(int64_t)(s.row0 + row / group) * a.num_q_heads + g * group + row % group] * kLog2e;
       sm.lse[tid] = x;
     }
     __syncthreads();
@@ -407,6 +403,7 @@ __global__ void __launch_bounds__(kThreadsCC, 2) weights_cc_kernel(const TreeArg
       for (int i = 0; i < 4; ++i) {
         const int row = row0 + r + i;
         if (row >= rows) break;
+        if (sm.lse[r + i] == -INFINITY) continue;   // adds nothing, be its scores NaN
         const uint64_t bits = tree_bits(a, s, row / group);
 #pragma unroll
         for (int j = 0; j < 4; ++j)

@@ -48,7 +48,8 @@ constexpr int OFF_Q = 0;
 constexpr int OFF_K = 2 * Q_BYTES;
 constexpr int OFF_LSE = OFF_K + NS * TILE;     // 256 floats: a pass's rows (or two of 128 rows)
 constexpr int OFF_MASK = OFF_LSE + kTreeRows * 4;    // [2][64] words
-constexpr int OFF_PASS = OFF_MASK + 2 * kMaxDraft * 8;
+constexpr int OFF_SKIP = OFF_MASK + 2 * kMaxDraft * 8;   // [2]: has the pass a row that adds nothing?
+constexpr int OFF_PASS = OFF_SKIP + 16;
 constexpr int OFF_BAR = OFF_PASS + NI * 64;
 constexpr int kSoft = 256, kThreadsW = 352;
 constexpr int W_KEYS = 8, W_MMA = 9, W_PLAN = 10;
@@ -91,6 +92,7 @@ weights_mma_kernel(const __grid_constant__ WeightParams p, const __grid_constant
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int group = a.num_q_heads / a.num_kv_heads;
   const int log_group = 31 - __clz(group);      // a power of two
+  int* skips = reinterpret_cast<int*>(smem + OFF_SKIP);
   const int q_half = (p.q_bufs == 2 ? 1 : 2) * (Q_BYTES / 2);   // bytes of 64 columns of a pass's queries
 
   if (tid == 0) {
@@ -166,13 +168,16 @@ weights_mma_kernel(const __grid_constant__ WeightParams p, const __grid_constant
           const int tok0 = x.row0 >> log_group, drafted = x.len - x.ctx;
           float* lse = reinterpret_cast<float*>(smem + OFF_LSE) + qb * 128;
           unsigned long long* words = reinterpret_cast<unsigned long long*>(smem + OFF_MASK) + qb * kMaxDraft;
+          bool skip = false;
           for (int r = lane; r < x.rows; r += 32) {
             const int row = x.row0 + r;
             const float v = a.lse[(int64_t)(x.q_tok + (row >> log_group)) * a.num_q_heads + x.g * group +
                                   (row & (group - 1))];
-            // a row that sees nothing gives nothing: 2^(s - inf) = 0
-            lse[r] = v == -INFINITY ? INFINITY : v * 1.4426950408889634f;
+            lse[r] = v * 1.4426950408889634f;
+            skip |= v == -INFINITY;
           }
+          skip = __any_sync(0xffffffffu, skip);
+          if (lane == 0) skips[qb] = skip;
           TreeSeq s;
           s.len = x.len;
           s.drafted = drafted;
@@ -296,6 +301,7 @@ weights_mma_kernel(const __grid_constant__ WeightParams p, const __grid_constant
       __syncwarp();
       const float* lse = reinterpret_cast<const float*>(smem + OFF_LSE) + qb * 128;
       const unsigned long long* words = reinterpret_cast<const unsigned long long*>(smem + OFF_MASK) + qb * kMaxDraft;
+      const bool skip = skips[qb] != 0;
       float* line = a.weights + ((int64_t)it.b * a.num_kv_heads + it.g) * a.weights_len;
       for (int j = side; j < it.n; j += 2, ++count) {
         const int key = (it.t0 + j) * BK + r, d = key - it.ctx;
@@ -313,7 +319,7 @@ weights_mma_kernel(const __grid_constant__ WeightParams p, const __grid_constant
           const float2 z = ffma2(make_float2(x, y), make_float2(sl2, sl2), make_float2(-lse_x, -lse_y));
           return make_float2(fast_exp2(z.x), fast_exp2(z.y));
         };
-        const int plain = masked ? 0 : it.rows & ~31;   // rows whose sums need no care
+        const int plain = masked || skip ? 0 : it.rows & ~31;   // rows whose sums need no care
         for (int c = 0; c < plain; c += 32) {
           float x[32];
           tmem_ld32(lane_base + c, x);
@@ -326,8 +332,9 @@ weights_mma_kernel(const __grid_constant__ WeightParams p, const __grid_constant
             sum[(q >> 1 & 2) + 1] = fadd2(sum[(q >> 1 & 2) + 1], weight2(x[q + 2], x[q + 3], e.z, e.w));
           }
         }
-        // the rest eight rows at a time: those behind the last, and those that
-        // do not see this key, add nothing.  A key of the context is seen by
+        // the rest eight rows at a time: those behind the last, those that do
+        // not see this key and those whose lse is -inf (their scores may be
+        // NaN) add nothing.  A key of the context is seen by
         // all, the pass's first token in bit 0.  (The words looked up row by row,
         // short sequences took two to three times as long: 64 of 1 to 300 with 16
         // drafted tokens 29 us, against 14.8.)
@@ -350,8 +357,8 @@ weights_mma_kernel(const __grid_constant__ WeightParams p, const __grid_constant
           for (int q = 0; q < 8; q += 2) {
             const float2 e = *reinterpret_cast<const float2*>(lse + c + q);
             const float2 y = weight2(x[q], x[q + 1], e.x, e.y);
-            const bool see0 = c + q < it.rows && (seers >> ((c + q) >> log_group) & 1);
-            const bool see1 = c + q + 1 < it.rows && (seers >> ((c + q + 1) >> log_group) & 1);
+            const bool see0 = c + q < it.rows && (seers >> ((c + q) >> log_group) & 1) && e.x != -INFINITY;
+            const bool see1 = c + q + 1 < it.rows && (seers >> ((c + q + 1) >> log_group) & 1) && e.y != -INFINITY;
             sum[q >> 1] = fadd2(sum[q >> 1], make_float2(see0 ? y.x : 0.f, see1 ? y.y : 0.f));
           }
         }
