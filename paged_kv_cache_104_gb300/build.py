@@ -69,11 +69,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return LIB
 
 
-# A test-only build of the library: the same objects but decode_mma.cu
-# compiled with PKV_TEST_WAIT_TIMEOUT, which shortens every wait limit of that
-# file to about 2 ms and makes the decode kernel's producer withhold its
+# A test-only build of the library: the same objects but the files below
+# compiled with PKV_TEST_WAIT_TIMEOUT, which shortens every wait limit of
+# theirs to about 2 ms and makes their key and value producers withhold the
 # copies, so a test can see a wait run out and the kernel return with
 # PKV_DEVERR_TIMEOUT.  Never loaded by the product.
+WAIT_TEST_SOURCES = ["decode_mma.cu", "tree_mma.cu", "weights_mma.cu"]
 WAIT_TEST_DIR = os.path.join(BUILD, "wait_test")
 WAIT_TEST_LIB = os.path.join(WAIT_TEST_DIR, "libpagedkv_wait_test.so")
 
@@ -81,15 +82,21 @@ WAIT_TEST_LIB = os.path.join(WAIT_TEST_DIR, "libpagedkv_wait_test.so")
 def build_wait_test() -> str:
     build()
     os.makedirs(WAIT_TEST_DIR, exist_ok=True)
-    src = os.path.join(CSRC, "decode_mma.cu")
-    obj = os.path.join(WAIT_TEST_DIR, "decode_mma.o")
-    dep_time = max([os.path.getmtime(p) for p in _deps()] + [os.path.getmtime(src)])
-    if not os.path.exists(obj) or os.path.getmtime(obj) < dep_time:
-        subprocess.run([nvcc(), *ARCH, "-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC",
-                        "-DPKV_TEST_WAIT_TIMEOUT", "-I", INCLUDE, "-I", CSRC, "-c", src, "-o", obj],
-                       check=True)
-    objs = [obj] + [os.path.join(BUILD, os.path.splitext(f)[0] + ".o") for f in SOURCES
-                    if f != "decode_mma.cu"]
+    dep_time = max(os.path.getmtime(p) for p in _deps())
+    procs, objs = [], []
+    for f in SOURCES:
+        src = os.path.join(CSRC, f)
+        obj = os.path.join(WAIT_TEST_DIR if f in WAIT_TEST_SOURCES else BUILD, os.path.splitext(f)[0] + ".o")
+        objs.append(obj)
+        if f not in WAIT_TEST_SOURCES or (os.path.exists(obj) and
+                                          os.path.getmtime(obj) >= max(dep_time, os.path.getmtime(src))):
+            continue
+        cmd = [nvcc(), *ARCH, "-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC",
+               "-DPKV_TEST_WAIT_TIMEOUT", "-I", INCLUDE, "-I", CSRC, "-c", src, "-o", obj]
+        procs.append((f, subprocess.Popen(cmd)))
+    failed = [f for f, p in procs if p.wait() != 0]
+    if failed:
+        raise RuntimeError(f"nvcc failed: {failed}")
     if not os.path.exists(WAIT_TEST_LIB) or os.path.getmtime(WAIT_TEST_LIB) < max(
             os.path.getmtime(o) for o in objs):
         tmp = WAIT_TEST_LIB + f".tmp{os.getpid()}"

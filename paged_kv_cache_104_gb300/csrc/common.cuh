@@ -32,10 +32,13 @@ enum DevErr : int {
 // most 2^28 polls in any case.
 #ifdef PKV_TEST_WAIT_TIMEOUT
 // Test build only (never the shipped library): waits give up after 2^22
-// cycles, about 2 ms, so a test can make one run out quickly.
+// cycles, about 2 ms, so a test can make one run out quickly, and the key and
+// value producers withhold every copy.
 constexpr long long kWaitLimitCycles = 1ll << 22;
+constexpr bool kWithholdCopies = true;
 #else
 constexpr long long kWaitLimitCycles = 1ll << 31;
+constexpr bool kWithholdCopies = false;
 #endif
 constexpr unsigned int kWaitLimitIters = 1u << 28;
 

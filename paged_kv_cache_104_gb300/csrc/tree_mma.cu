@@ -313,7 +313,7 @@ tree_mma_kernel(const __grid_constant__ TreeMmaParams p, const __grid_constant__
       int pos = 0, checks = 0;        // ring position; V tiles sent to the guard
       uint32_t history = 0;           // which of the last positions went to the guard
       TreeItem it;
-      bool ok = true;
+      bool ok = !kWithholdCopies;     // (a test's build: the others' waits run out, nothing is in flight)
       for (int k = 0; ok && item_at(k, it); ++k) {
         const int32_t* row = a.block_table + (int64_t)it.b * a.max_blocks_per_seq;
         const int blocks = (it.len + kBlockSize - 1) / kBlockSize;

@@ -216,7 +216,7 @@ weights_mma_kernel(const __grid_constant__ WeightParams p, const __grid_constant
     const uint64_t once = policy_evict_first(), again = policy_evict_normal();
     int pos = 0;                     // ring position
     TreeItem it;
-    bool ok = true;
+    bool ok = !kWithholdCopies;      // (a test's build: the others' waits run out, nothing is in flight)
     for (int k = 0; ok && pass_at(k, it); ++k) {
       const int32_t* row = a.block_table + (int64_t)it.b * a.max_blocks_per_seq;
       const int blocks = (it.len + kBlockSize - 1) / kBlockSize;
