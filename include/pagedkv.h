@@ -577,7 +577,12 @@ size_t pkv_tree_workspace_bytes(int num_q_heads, int num_kv_heads, int head_dim,
  *   out_ih = sum_n e^(s_n - lse_ih) v_n
  * in fp32, out rounded once to dtype.  A row that sees nothing gets out = 0
  * and lse = -inf.  Values of keys that a row does not see never reach it.
- * Accuracy as paged_decode_attention.
+ *   In bf16 each weight is rounded to bf16 (by at most 2^-8 of itself) before
+ * it multiplies its value; their sum and lse take it unrounded.  Out is off by
+ * that and by its own rounding, together 2.1e-3 to 2.4e-3 of its norm for
+ * normal values (its own rounding alone: 1.7e-3).  paged_decode_attention sums
+ * the rounded weights: a row that one key dominates is that key's value there,
+ * and may be the bf16 number next to it here.  In fp32 only out is rounded.
  */
 pkv_status pkv_paged_tree_attention(const pkv_tree_args *args, pkv_stream_t stream);
 

@@ -36,8 +36,13 @@
 //   warp 8           K/V producer: one 4 KiB TMA copy per cache block (K and V
 //                    tiles through one ring of five 32 KiB slots)
 //   warp 9           tcgen05 issuer: S = Q K^T from shared memory, O += P V with
-//                    P (bf16) in TMEM over its S.  P is rounded to bf16 as the
-//                    cache's values are; the sum l takes the unrounded ones.
+//                    P (bf16) in TMEM over its S.  P is rounded to bf16, the
+//                    values' type, as the product's operands have one type: up
+//                    to 2^-8 of each weight, 1.3e-3 to 1.6e-3 of the result's
+//                    norm for normal values, next to 1.7e-3 for its own
+//                    rounding (P as a sum of two bf16 would take the product
+//                    twice).  The sum l takes the unrounded weights, as lse
+//                    needs them; the rounded ones would be a second sum.
 //   warp 10          checks the drafted tokens' values: a row of V that holds an
 //                    infinity or NaN would reach, as 0 x inf, rows that do not
 //                    see it.  Such rows are cleared in shared memory and added
