@@ -514,6 +514,8 @@ pkv_status pkv_mla_decode_attention_append(void *out, const void *q, const void 
  * between two decode steps.  Drafted tokens are appended (pkv_kv_append, or a
  * rotating append), attend in one call, and the accepted ones move up; a
  * sequence that has grown too long keeps the tokens that got most attention.
+ *   The attention and the counts take bf16 and fp32 pools.  Of the E4M3 pools
+ * those with one scale per head can be compacted, by lists from elsewhere.
  * ------------------------------------------------------------------------- */
 #define PKV_MAX_DRAFT 64              /* drafted tokens per sequence */
 #define PKV_MAX_COMPACT_ROW_BYTES 1024
@@ -590,10 +592,13 @@ pkv_status pkv_paged_tree_attention(const pkv_tree_args *args, pkv_stream_t stre
  * kv_add_weights -- the attention each stored token got, added up:
  *   weights[b][g][n] += sum over the rows i of sequence b that see token n,
  *                       and the query heads h of KV head g, of e^(s_n - lse_ih)
- * with s_n and the rows as above and lse as paged_tree_attention gave it.  A
- * row whose lse is -inf adds nothing.  Sums are fp32, added in a fixed order:
- * the same inputs give the same bits.  Entries at seq_lens[b] and beyond, and
- * those of sequences without rows, are left alone.  Start from zeros.
+ * with s_n and the rows as above and lse as paged_tree_attention gave it (the
+ * decode and prefill calls give none: a decode step whose attention is counted
+ * uses paged_tree_attention with one drafted token a sequence instead, 98 us
+ * against the decode's 94 for 64 sequences of 2,301).  A row whose lse is -inf
+ * adds nothing, whatever q and the keys hold.  Sums are fp32, added in a fixed
+ * order: the same inputs give the same bits.  Entries at seq_lens[b] and beyond,
+ * and those of sequences without rows, are left alone.  Start from zeros.
  */
 pkv_status pkv_kv_add_weights(const pkv_tree_args *args, pkv_stream_t stream);
 

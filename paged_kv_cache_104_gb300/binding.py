@@ -676,7 +676,9 @@ def kv_add_weights(weights, q, k_cache, block_table, seq_lens, draft_offsets, tr
     """Adds to weights (fp32 [B, Hkv, M], M >= max_seq_len; start from zeros)
     what the softmax of the rows of q gave each stored token, summed over the
     rows and the query heads of each KV head.  The arguments are those of
-    ``paged_tree_attention``, with the lse it wrote."""
+    ``paged_tree_attention``, with the lse it wrote; decode and prefill give
+    none, so a decode step that is counted uses ``paged_tree_attention`` with one
+    drafted token a sequence.  bf16 and fp32 pools only."""
     fn = "pkv_kv_add_weights"
     if weights is None or lse is None:
         _refuse(fn, "no weights or no lse")
