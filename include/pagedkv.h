@@ -615,6 +615,10 @@ pkv_status pkv_kv_add_weights(const pkv_tree_args *args, pkv_stream_t stream);
  *   seq_lens   int32 [num_seqs], 0 .. max_seq_len; one outside is reported in
  *              the device error word, and its kept_lens is 0
  *   sinks + recent <= budget, weights_len >= max_seq_len
+ *   max_seq_len sizes the launch and is what is read, whatever the lengths: pass
+ * a tight one.  64 sequences of 500 in 8 KV heads, down to 256, take 9.4 us under
+ * a bound of 500 or 4,096, 15 under 8,192, 32 under 16,384, 127 under 65,536 and 202
+ * under 131,072.
  */
 pkv_status pkv_kv_select(int32_t *kept, int32_t *kept_lens, const float *weights,
                          int64_t weights_len, const int32_t *seq_lens, int num_seqs,

@@ -691,7 +691,8 @@ def kv_select(kept, kept_lens, weights, seq_lens, max_seq_len: int, sinks: int, 
     """Which tokens stay: kept int32 [B, Hkv, budget] gets the positions, in
     ascending order, of each sequence's first ``sinks`` tokens, its last
     ``recent`` ones, and of the rest those with the largest weights (fp32
-    [B, Hkv, M]); kept_lens int32 [B] gets min(seq_lens, budget)."""
+    [B, Hkv, M]); kept_lens int32 [B] gets min(seq_lens, budget).  The time goes
+    by max_seq_len, not by the lengths: pass a tight bound."""
     fn = "pkv_kv_select"
     index = _device_of(fn, weights)
     if weights.dim() != 3 or kept.dim() != 3:

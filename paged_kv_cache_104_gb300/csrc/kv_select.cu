@@ -9,19 +9,24 @@
 // of their digits, from the highest, narrow the key of the last token that
 // stays; then every token's place is a prefix sum.
 //
-// The bytes are few (4 a token); what bounds it is the chain of barriers, and
-// the code itself, which every launch fetches anew.  So a (sequence, KV head) is
-// read once, 16 tokens a thread, and its keys stay in shared memory (in
-// registers every loop over them was unrolled: 17.3 us for 64 sequences of
-// 2,301, against 11.9) through up to three passes of 11, 11 and 10 bits.  As
-// soon as at most 256 tokens share the digits of the last one that stays, those
-// are ranked by comparing each with all, which for 2,301 tokens is mostly after
+// The bytes are few (4 a token); what bounds it is the chain of barriers, and the
+// code itself, which every launch fetches anew.  Cycles of a cold launch (clock64 in
+// one CTA) for 64 sequences of 2,301: 4,900 until its weights are there, 1,600 for
+// the histogram, 1,000 for the digit, 2,300 to collect and 1,500 to rank the
+// candidates, 3,900 to place what stays: 16,500 in all.  For 8 of 32,001, seven
+// barriers of clusters of four: 5,500 for the weights, 5,800 until the last CTA has
+// its own, 5,200 and 5,800 for two passes, 4,100 for the candidates, 5,100 to place:
+// 33,000.  So a (sequence, KV head) is read once, 16 tokens a thread, and its keys
+// stay in shared memory (in registers every loop over them was unrolled: 17.3 us for
+// 64 sequences of 2,301, against 11.9) through up to three passes of 11, 11 and 10
+// bits.  As soon as at most 256 tokens share the digits of the last one that stays,
+// those are ranked by comparing each with all, which for 2,301 tokens is mostly after
 // the first pass.  Beyond 8,192 tokens a cluster of up to eight CTAs shares a
 // (sequence, KV head), adding its histograms up in the first one's shared memory
-// (16.4 us for 8 sequences of 32,001).  Where the bound passes the shared memory
-// of eight, at 65,536 tokens, a cluster of eight reads its weights anew for every
-// pass: 62 us at 65,537 for 64 (sequence, KV head)s, against 33 at 65,536, and 81
-// at 131,072, where one CTA took 438.
+// (16.4 us for 8 sequences of 32,001).  Where the bound passes the shared memory of
+// eight, at 65,536 tokens, a cluster of eight reads its weights anew for every pass:
+// 62 us at 65,537 for 64 (sequence, KV head)s, against 33 at 65,536, and 81 at
+// 131,072, where one CTA took 438.
 #include <climits>
 
 #include <cooperative_groups.h>
@@ -62,7 +67,11 @@ __device__ __forceinline__ bool select_begin(const SelectArgs& a, int item, int 
 
 constexpr int kPerThread = 16;     // tokens
 constexpr int kBins = 2048;
-constexpr int kFew = 256;          // tokens that are ranked by comparing each with all
+// Tokens that are ranked by comparing each with all.  With 64 or 128 instead the
+// listed cases take the same (11.5, 16.6 us), 64 sequences of 8,000 24.6 instead of
+// 25.8, of 4,000 14.3 instead of 16.1; twice as many do not fit the static
+// shared memory of 512 threads.
+constexpr int kFew = 256;
 
 // Sums of all threads before this one, and of all (one barrier; warp_sums is
 // free again after the next).
@@ -392,6 +401,11 @@ cudaError_t launch_clusters(void (*kernel)(SelectArgs), int threads, const Selec
 }  // namespace
 
 cudaError_t launch_kv_select(const SelectArgs& a, cudaStream_t stream) {
+  // The fewest threads that hold the bound's tokens, 16 each, 64, 256 or 512: a
+  // large batch then has more CTAs on an SM (256 sequences of 1,000 in 8 heads 17.2,
+  // 26.4 and 41.1 us with 64, 256 and 512 threads, 64 of 4,000 16.2 and 21.0 with 256
+  // and 512); one sequence alone would take more (1,000 tokens 9.2, 6.5, 6.2 us, 4,000
+  // 10.1 and 9.1).
   const int tokens = a.max_seq_len;
   if (tokens <= 64 * kPerThread) return launch_clusters(select_smem_kernel<64, true>, 64, a, 1, stream);
   if (tokens <= 256 * kPerThread) return launch_clusters(select_smem_kernel<256, true>, 256, a, 1, stream);
