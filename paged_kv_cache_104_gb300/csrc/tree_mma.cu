@@ -15,7 +15,7 @@
 // holds one S for each side), one of 777 with 8 drafted 10.4 us (latency).
 //
 // Work.  A stream is one (sequence, KV head, 256 rows), cut into tiles of 128
-// keys; the tiles of the whole batch are shared out equally to one persistent
+// keys; the tiles of the whole batch are shared out by weight to one persistent
 // CTA per SM (tree_common.cuh).  A CTA's part of a stream is an item; a stream
 // that falls to several CTAs leaves fp32 partials (unnormalised O, max, sum),
 // at most two per CTA, that a second kernel joins.
