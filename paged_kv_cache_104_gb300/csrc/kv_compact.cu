@@ -144,6 +144,13 @@ __global__ void __launch_bounds__(kCpThreads) compact_kernel(const CompactArgs a
   for (int k = 0; k < rounds; ++k) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");   // round k's rows are here
     __syncthreads();                                      // ... of every thread, and round k - 1 is written
+    // The cluster's barrier orders nothing by itself (relaxed: a release would
+    // wait for the stores of the round before).  It need not: what the others
+    // overwrite behind it this CTA has read, and those reads are complete, not
+    // only issued: the round's rows by cp.async.wait_group and the barrier
+    // above, its weights, asked for a batch ahead, as `sums` was written before
+    // an earlier such barrier.  No read of rows or weights that a round needs
+    // may be in flight here.
     if (ranks > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     if ((k & (batch - 1)) == 0) {                         // the batch before is done with
       const int q = (k >> log_batch) + 1;
