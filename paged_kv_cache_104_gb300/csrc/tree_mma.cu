@@ -894,10 +894,11 @@ cudaError_t launch_tree_attention_mma(const TreeArgs& a, int num_sms, cudaStream
   int grid = num_sms < kTreeMaxCtas ? num_sms : kTreeMaxCtas;
   const bool few = stages <= 4 * grid;
   // Short sequences are not cut: nothing to write in parts, and no second kernel
-  // (4 sequences of up to 500 with 64 drafted tokens 23.4 -> 17.0 us, 50 of 131 to
-  // 393 with one KV head 15.5 -> 12.1, one of 200 10.1 -> 8.8), but where a few of
-  // three or four tiles and few rows leave CTAs without any (one of 500 with 8
-  // drafted tokens 10.3 -> 11.0); cut at eight tiles, 16 of 1,000 take 21.5, whole 24.4.
+  // (4 sequences of 300 to 500 with 64 drafted tokens 23.4 -> 17.0 us, 50 of 131 to
+  // 393 with 9 drafted, 8 query heads and one KV head 14.9 -> 11.8, 80 of 300 to 500
+  // with 16 45.4 -> 36.6, one of 200 with 8 10.1 -> 8.6), but where a few of three or
+  // four tiles and few rows leave CTAs without any (one of 500 with 8 drafted tokens
+  // 10.2 cut, 10.8 whole); of eight tiles, 16 of 1,000 with 8 take 21.3 cut, 24.0 whole.
   p.whole = a.max_seq_len <= 2 * BN || (a.max_seq_len <= 4 * BN && (stages >= grid || rows > BM));
   // a batch that may have enough tiles, and whose KV heads and rows go in pairs
   const bool pairs = stages >= kTreePairTiles * grid && !(a.num_kv_heads & 1);
