@@ -67,9 +67,9 @@ __device__ __forceinline__ bool select_begin(const SelectArgs& a, int item, int 
 
 constexpr int kPerThread = 16;     // tokens
 constexpr int kBins = 2048;
-// Tokens that are ranked by comparing each with all.  With 64 or 128 instead the
-// listed cases take the same (11.5, 16.6 us), 64 sequences of 8,000 24.6 instead of
-// 25.8, of 4,000 14.3 instead of 16.1; twice as many do not fit the static
+// Tokens that are ranked by comparing each with all.  With 64 or 128 instead 64
+// sequences of 2,301 and 8 of 32,001 take the same (11.5, 16.6 us), 64 of 8,000 24.6, not
+// 25.8, 64 of 4,000 14.3, not 16.1; twice as many do not fit the static
 // shared memory of 512 threads.
 constexpr int kFew = 256;
 
